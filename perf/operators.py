@@ -381,7 +381,8 @@ def run(state):
     if op == "combine":
         return {"y": experts.combine(s["rows"], s["slots"], s["weights"])}
     if op == "combine gradient":
-        drows, dweights = experts.combine_backward(s["dy"], s["rows"], s["slots"], s["weights"])
+        drows, dweights = experts.combine_backward(s["dy"], s["rows"], s["slots"], s["weights"],
+                                                   s["offsets"])
         dlogits = experts.route_backward(dweights, s["weights"], s["experts"], s["logits"])
         return {"drows": drows, "dweights": dweights, "dlogits": dlogits}
     off = s["offsets"]
