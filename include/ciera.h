@@ -435,6 +435,198 @@ int ciera_set_wait_timeout_ns(uint64_t ns);
 /* Static description of a status code. */
 const char *ciera_strerror(int status);
 
+/* ------------------------------------------------------------------------
+ * Operators of the mixture-of-experts layer whose weights the path above
+ * rebuilds: the norm before the layer, the router's choice, the products
+ * grouped by expert that read the rebuilt bucket in place, and the
+ * combination of the experts' rows, each with its gradient.
+ *
+ * Conventions, beside those at the top of this file:
+ *   - Matrices are row-major with a row stride in elements (>= the row
+ *     length) and contiguous rows; bf16 values are uint16_t bit patterns,
+ *     e4m3 values uint8_t.  Sums, norms, softmax statistics and gradients'
+ *     partial sums are held in 32-bit floats; each output is rounded once.
+ *   - Rows, tokens or experts may be zero in number.  Any size, stride and
+ *     alignment of the element type is accepted.
+ *   - "Expert order": the (token, expert) pairs grouped by expert and, in a
+ *     group, by token.  Expert e owns the rows [offsets[e], offsets[e+1]) of
+ *     `rows` = tokens * topk rows; the pairs of tokens that chose fewer than
+ *     topk experts leave as many rows unused at the end.  Products and
+ *     gradients write zeros to unused rows.
+ *   - Offsets, slots and token indexes are read by the kernels.  An index
+ *     outside its buffer is taken for "none" (a zero row), an offset outside
+ *     [previous offset, rows] for the nearest end of that range; offsets[0]
+ *     is taken for 0.
+ *   - Calls that take a workspace want ciera_moe_workspace_bytes() bytes,
+ *     zero-filled once (ciera_moe_workspace_init), and use it as above:
+ *     one call at a time.  Its status is read with ciera_status().
+ *   - Results do not depend on the order in which thread blocks run.
+ */
+#define CIERA_BF16 0
+#define CIERA_E4M3 1
+#define CIERA_F32 2
+
+/* Bytes of workspace for calls of at most these sizes: tokens (rows of a
+ * norm's gradient, tokens of a route), experts, dim (columns of a norm's
+ * gradient).  0 for a negative argument. */
+int64_t ciera_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t dim);
+
+/* Zero-fill the status and control words of such a workspace on `stream`. */
+int ciera_moe_workspace_init(void *workspace_dev, void *stream);
+
+/* Root-mean-square norm of s = x + residual (s = x without a residual):
+ *   rstd = (mean_i s_i^2 + eps)^(-1/2),  y_i = s_i rstd weight_i
+ *   residual_dev  rows x dim bf16, or NULL
+ *   weight_dev    dim bf16
+ *   y_dev         rows x dim, contiguous: bf16 (y_type CIERA_BF16), or e4m3
+ *                 (CIERA_E4M3) with scale_dev: row t stands for
+ *                 e4m3 * scale[t], scale[t] = max(max_i |y_i|, 1e-30) / 448;
+ *                 NaN for a row that holds an infinity or a NaN
+ *   scale_dev     rows floats (CIERA_E4M3), else NULL
+ *   h_dev         rows x dim bf16, contiguous: s rounded, the next residual
+ *                 (may be residual_dev itself when its stride is dim), or NULL
+ *   rstd_dev      rows floats, kept for the gradient, or NULL
+ * s is rounded to bf16 only where it is stored; the norm is of the sum in 32
+ * bits.  Errors: CIERA_E_INVAL (a negative size, a short stride, NULL or
+ * misaligned pointers, eps < 0 or not finite, an unknown type), CIERA_E_CUDA. */
+int ciera_rmsnorm(const uint16_t *x_dev, int64_t x_stride, const uint16_t *residual_dev,
+                  int64_t residual_stride, const uint16_t *weight_dev, int64_t rows, int64_t dim,
+                  float eps, void *y_dev, int y_type, float *scale_dev, uint16_t *h_dev,
+                  float *rstd_dev, void *stream);
+
+/* Gradients of ciera_rmsnorm's bf16 output, with g_i = dy_i weight_i:
+ *   dx_i = rstd g_i - h_i rstd^3 mean_j(g_j h_j) + dh_i
+ *   dweight_i = sum over rows of dy_i h_i rstd
+ * dx is the gradient of x and of the residual alike.
+ *   h_dev, rstd_dev  as the norm stored them
+ *   dh_dev           rows x dim bf16: the gradient that reaches h through the
+ *                    next residual, or NULL
+ *   dweight_dev      dim floats, overwritten
+ * The workspace holds per-block partial sums.  Errors: as ciera_rmsnorm, and
+ * CIERA_E_INVAL for a workspace smaller than
+ * ciera_moe_workspace_bytes(rows, 0, dim). */
+int ciera_rmsnorm_backward(const uint16_t *dy_dev, int64_t dy_stride, const uint16_t *h_dev,
+                           int64_t h_stride, const float *rstd_dev, const uint16_t *weight_dev,
+                           const uint16_t *dh_dev, int64_t dh_stride, int64_t rows, int64_t dim,
+                           uint16_t *dx_dev, float *dweight_dev, void *workspace_dev,
+                           int64_t workspace_bytes, void *stream);
+
+/* Rows of bf16 to e4m3 with a scale each, as ciera_rmsnorm's e4m3 output:
+ * weights laid out once, and rows between two e4m3 products. */
+int ciera_quantize_rows(const uint16_t *x_dev, int64_t x_stride, int64_t rows, int64_t dim,
+                        uint8_t *y_dev, float *scale_dev, void *stream);
+
+#define CIERA_ROUTE_RENORMALIZE 1u  /* a token's weights divided by their sum */
+
+/* The router's choice: for each token the topk experts of the largest
+ * logits, ties to the lowest index (a NaN counts as the largest), weighted
+ * with the softmax over all experts' logits, and the expert order.  A logit
+ * of -inf is never chosen; a token without topk finite-or-larger logits, or
+ * whose token_mask is 0, has chosen[] = slots[] = -1 and weight 0 in what is
+ * left over.
+ *   logits_dev      tokens x experts, CIERA_F32 or CIERA_BF16
+ *   token_mask_dev  one byte per token, 0: routed nowhere; or NULL
+ *   weights_dev     tokens x topk floats, in order of falling logit
+ *   chosen_dev      tokens x topk expert indexes, likewise
+ *   slots_dev       tokens x topk: the pair's row in expert order
+ *   row_tokens_dev  tokens * topk: each row's token, -1 for unused rows
+ *   offsets_dev     experts + 1 row offsets
+ * Errors: CIERA_E_INVAL (topk outside [1, min(experts, 32)], experts outside
+ * [1, 1024], tokens * topk >= 2^31, short stride, NULL or misaligned pointers,
+ * unknown flags, a workspace smaller than
+ * ciera_moe_workspace_bytes(tokens, experts, 0)), CIERA_E_CUDA. */
+int ciera_route(const void *logits_dev, int logits_type, int64_t logits_stride,
+                const uint8_t *token_mask_dev, int64_t tokens, int64_t experts, int topk,
+                uint32_t flags, float *weights_dev, int32_t *chosen_dev, int32_t *slots_dev,
+                int32_t *row_tokens_dev, int32_t *offsets_dev, void *workspace_dev,
+                int64_t workspace_bytes, void *stream);
+
+/* Gradient of the logits from that of the weights, w the weights as
+ * ciera_route returned them and p the softmax over all experts:
+ *   dl_i = [i chosen as j] w_j dw_j - p_i sum_j w_j dw_j
+ * with w in the place of p when they were renormalised.  Zero for a token
+ * that chose no expert.
+ *   dlogits_dev  tokens x experts, contiguous, of the logits' type
+ * Errors: as ciera_route. */
+int ciera_route_backward(const float *dweights_dev, const float *weights_dev,
+                         const int32_t *chosen_dev, const void *logits_dev, int logits_type,
+                         int64_t logits_stride, int64_t tokens, int64_t experts, int topk,
+                         uint32_t flags, void *dlogits_dev, void *stream);
+
+/* Rows in expert order back to their tokens:
+ *   y_t = sum_j weights[t, j] row(slots[t, j]),  nothing for slots of -1
+ *   weights_dev  tokens x topk floats, or NULL: 1 (the gradient of a product
+ *                whose rows were gathered by token)
+ *   y_dev        tokens x dim bf16, contiguous
+ * Errors: CIERA_E_INVAL (topk outside [1, 32], ...), CIERA_E_CUDA. */
+int ciera_combine(const uint16_t *rows_dev, int64_t rows_stride, int64_t rows,
+                  const int32_t *slots_dev, const float *weights_dev, int64_t tokens, int topk,
+                  int64_t dim, uint16_t *y_dev, void *stream);
+
+/* Gradients of ciera_combine:
+ *   drow(slots[t, j]) = weights[t, j] dy_t,  dweights[t, j] = dy_t . row(slots[t, j])
+ * (0 for slots of -1).
+ *   offsets_dev  experts + 1 offsets: rows from the last one on get zeros
+ *   drows_dev    rows x dim bf16, contiguous
+ * Errors: as ciera_combine. */
+int ciera_combine_backward(const uint16_t *dy_dev, int64_t dy_stride, const uint16_t *rows_dev,
+                           int64_t rows_stride, int64_t rows, const int32_t *slots_dev,
+                           const float *weights_dev, const int32_t *offsets_dev, int64_t experts,
+                           int64_t tokens, int topk, int64_t dim, uint16_t *drows_dev,
+                           float *dweights_dev, void *stream);
+
+#define CIERA_GATED 1u       /* ciera_expert_mm: silu(gate) * up of 2n features */
+#define CIERA_ACCUMULATE 2u  /* ciera_expert_mm_dw: added to what dw_dev holds */
+
+/* Product grouped by expert: for each row r of expert e
+ *   y[r, i] = sum_j x[r, j] w_e[i, j],  i < n, j < k
+ * With CIERA_GATED w_e has 2n rows, gate then up, and
+ *   y[r, i] = silu(a_i) a_(n+i),  a = the 2n products, silu(a) = a / (1 + exp(-a))
+ *   x_dev        x_rows x k; row r is x's row r, or x's row row_tokens[r]
+ *   w_dev        expert e's weights at w_dev + e * w_expert_stride, its rows
+ *                w_stride apart: for instance a view of the rebuilt bucket
+ *   type         CIERA_BF16: x and w are bf16, x_scale and w_scale NULL;
+ *                CIERA_E4M3: both e4m3, standing for x * x_scale[x's row] and
+ *                w_e * w_scale[e, i] (experts x n, or x 2n, contiguous); the
+ *                scales go on after the 32-bit sum
+ *   y_dev        rows x n bf16, contiguous
+ *   pre_dev      rows x 2n bf16, contiguous: a, kept for the gradient; or NULL
+ * Errors: CIERA_E_INVAL (experts outside [0, 1024], rows or x_rows >= 2^31,
+ * sizes, strides, NULL or misaligned pointers, flags), CIERA_E_CUDA. */
+int ciera_expert_mm(const void *x_dev, int64_t x_stride, int64_t x_rows,
+                    const int32_t *row_tokens_dev, const void *w_dev, int64_t w_stride,
+                    int64_t w_expert_stride, const float *x_scale_dev, const float *w_scale_dev,
+                    const int32_t *offsets_dev, int64_t rows, int64_t experts, int64_t n,
+                    int64_t k, int type, uint32_t flags, uint16_t *y_dev, uint16_t *pre_dev,
+                    void *workspace_dev, void *stream);
+
+/* Gradient of the rows (bf16), w_e of n x k:
+ *   dx[r, j] = sum_i dy[r, i] w_e[i, j],  j < k
+ * With pre_dev (rows x 2k, what ciera_expert_mm with CIERA_GATED kept where
+ * it produced these k columns) the result goes on through the gated unit:
+ *   dx[r, j] = d u s (1 + g (1 - s)),  dx[r, k + j] = d g s,
+ *   d the sum above, g = pre[r, j], u = pre[r, k + j], s = 1 / (1 + exp(-g))
+ *   dx_dev  rows x k (or 2k) bf16, contiguous
+ * Errors: as ciera_expert_mm. */
+int ciera_expert_mm_dx(const uint16_t *dy_dev, int64_t dy_stride, const uint16_t *w_dev,
+                       int64_t w_stride, int64_t w_expert_stride, const int32_t *offsets_dev,
+                       int64_t rows, int64_t experts, int64_t n, int64_t k,
+                       const uint16_t *pre_dev, uint16_t *dx_dev, void *workspace_dev,
+                       void *stream);
+
+/* Gradient of the weights (bf16 operands):
+ *   dw_e[i, j] = sum over rows r of e of dy[r, i] x[r, j]
+ * x as in ciera_expert_mm.  An expert without rows gets zeros (with
+ * CIERA_ACCUMULATE, its dw_e stays).
+ *   dw_dev   bf16 or float (dw_type), strided like w: a view of a bucket
+ *   flags    CIERA_ACCUMULATE or 0
+ * Errors: as ciera_expert_mm. */
+int ciera_expert_mm_dw(const uint16_t *dy_dev, int64_t dy_stride, const uint16_t *x_dev,
+                       int64_t x_stride, int64_t x_rows, const int32_t *row_tokens_dev,
+                       const int32_t *offsets_dev, int64_t rows, int64_t experts, int64_t n,
+                       int64_t k, void *dw_dev, int64_t dw_stride, int64_t dw_expert_stride,
+                       int dw_type, uint32_t flags, void *workspace_dev, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -75,6 +75,7 @@ class _CostModel(ctypes.Structure):
 
 # Every symbol include/ciera.h declares, with (restype, argtypes).
 _vp, _i64, _i32, _u32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint32
+_f32 = ctypes.c_float
 SIGNATURES = {
     "ciera_plan": (_i32, [ctypes.POINTER(ctypes.c_int64), _i32, _i64, _i32,
                           ctypes.POINTER(_vp)]),
@@ -104,6 +105,26 @@ SIGNATURES = {
     "ciera_get_cost_model": (_i32, [ctypes.POINTER(_CostModel)]),
     "ciera_set_wait_timeout_ns": (_i32, [ctypes.c_uint64]),
     "ciera_strerror": (ctypes.c_char_p, [_i32]),
+    "ciera_moe_workspace_bytes": (_i64, [_i64, _i64, _i64]),
+    "ciera_moe_workspace_init": (_i32, [_vp, _vp]),
+    "ciera_rmsnorm": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _f32, _vp, _i32, _vp, _vp,
+                             _vp, _vp]),
+    "ciera_rmsnorm_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp,
+                                      _vp, _vp, _i64, _vp]),
+    "ciera_quantize_rows": (_i32, [_vp, _i64, _i64, _i64, _vp, _vp, _vp]),
+    "ciera_route": (_i32, [_vp, _i32, _i64, _vp, _i64, _i64, _i32, _u32, _vp, _vp, _vp, _vp, _vp,
+                           _vp, _i64, _vp]),
+    "ciera_route_backward": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _u32, _vp,
+                                    _vp]),
+    "ciera_combine": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i32, _i64, _vp, _vp]),
+    "ciera_combine_backward": (_i32, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i32,
+                                      _i64, _vp, _vp, _vp]),
+    "ciera_expert_mm": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64,
+                               _i64, _i64, _i32, _u32, _vp, _vp, _vp, _vp]),
+    "ciera_expert_mm_dx": (_i32, [_vp, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _i64, _vp,
+                                  _vp, _vp, _vp]),
+    "ciera_expert_mm_dw": (_i32, [_vp, _i64, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i64,
+                                  _vp, _i64, _i64, _i32, _u32, _vp, _vp]),
 }
 
 _lock = threading.Lock()

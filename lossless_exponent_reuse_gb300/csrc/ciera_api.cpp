@@ -16,6 +16,7 @@
 
 #include "ciera.h"
 #include "ciera_internal.h"
+#include "ciera_moe.h"
 #include "ciera_rans.h"
 
 using namespace ciera;
@@ -91,6 +92,8 @@ bool raw_can_hold_unchanged(int64_t len, int64_t B) {
 }
 
 }  // namespace
+
+uint64_t ciera::wait_timeout_ns() { return g_timeout_ns.load(std::memory_order_relaxed); }
 
 extern "C" {
 

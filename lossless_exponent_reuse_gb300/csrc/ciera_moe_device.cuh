@@ -1,0 +1,83 @@
+// ciera_moe_device.cuh -- device helpers shared by the kernels of the
+// mixture-of-experts operators: bf16 and e4m3 conversion, block sums.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "ciera_moe.h"
+
+namespace ciera {
+namespace {
+
+constexpr float kE4m3Max = 448.0f;
+constexpr float kTinyAmax = 1e-30f;  // an all-zero row's scale is not 0
+
+__device__ __forceinline__ float bf16_to_f32(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_lo(uint32_t v) { return __uint_as_float(v << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t v) { return __uint_as_float(v & 0xFFFF0000u); }
+
+__device__ __forceinline__ uint16_t f32_to_bf16(float v) {
+  return __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+
+// Two floats to bf16 in one word, `lo` in bits 0..15.
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+__device__ __forceinline__ uint8_t f32_to_e4m3(float v) {
+  return static_cast<uint8_t>(__nv_cvt_float_to_fp8(v, __NV_SATFINITE, __NV_E4M3));
+}
+
+__device__ __forceinline__ float e4m3_to_f32(uint8_t v) {
+  const __half_raw h = __nv_cvt_fp8_to_halfraw(v, __NV_E4M3);
+  return __half2float(__half(h));
+}
+
+// Scale of a row from the largest |value|'s bits: NaN for a row that holds an
+// infinity or a NaN (their bits are the largest).
+__device__ __forceinline__ float e4m3_scale(uint32_t amax_bits) {
+  if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
+  return fmaxf(__uint_as_float(amax_bits), kTinyAmax) / kE4m3Max;
+}
+
+__device__ __forceinline__ float warp_sum_f32(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+
+// Sum over the block, the same in every thread; `part` holds 32 floats, and a
+// barrier stands between two uses of it.
+__device__ __forceinline__ float block_sum(float v, float* part) {
+  v = warp_sum_f32(v);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) part[warp] = v;
+  __syncthreads();
+  const int warps = (blockDim.x + 31) >> 5;
+  v = lane < warps ? part[lane] : 0.0f;
+  return warp_sum_f32(v);
+}
+
+__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* part) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (lane == 0) part[warp] = v;
+  __syncthreads();
+  const int warps = (blockDim.x + 31) >> 5;
+  v = lane < warps ? part[lane] : 0u;
+  return __reduce_max_sync(0xffffffffu, v);
+}
+
+// Offset of group e, clamped to [lo, rows]; `lo` is the one before it.
+__device__ __forceinline__ int32_t clamp_offset(int32_t v, int32_t lo, int32_t rows) {
+  return v < lo ? lo : v > rows ? rows : v;
+}
+
+}  // namespace
+}  // namespace ciera
