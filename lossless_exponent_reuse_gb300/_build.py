@@ -12,7 +12,8 @@ OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libciera.so")
 LIB_CHECKED = os.path.join(OUT_DIR, "libciera_checked.so")
 SOURCES = ["ciera_kernels.cu", "ciera_rans.cu", "ciera_api.cpp", "ciera_noalloc.cu",
-           "ciera_moe_api.cpp", "ciera_rows.cu", "ciera_experts.cu"]
+           "ciera_moe_api.cpp", "ciera_rows.cu", "ciera_experts.cu",
+           "ciera_experts_tc.cu"]
 HEADERS = [os.path.join(ROOT, "include", "ciera.h"), os.path.join(CSRC, "ciera_internal.h"),
            os.path.join(CSRC, "ciera_device.cuh"), os.path.join(CSRC, "ciera_rans.h"),
            os.path.join(CSRC, "ciera_moe.h"), os.path.join(CSRC, "ciera_moe_device.cuh")]

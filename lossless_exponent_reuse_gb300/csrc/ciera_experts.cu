@@ -199,6 +199,8 @@ int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 }  // namespace
 
 int launch_expert(const ExpertParams& p, void* stream) {
+  int status = cudaSuccess;
+  if (launch_expert_tc(p, stream, &status)) return status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t cols = p.op == kExpertForward ? p.n : p.k;
   if (tiles_of(cols) > 65535) return cudaErrorInvalidConfiguration;

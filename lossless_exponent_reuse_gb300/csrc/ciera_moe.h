@@ -140,5 +140,7 @@ int launch_route_backward(const RouteBackwardParams& p, void* stream);
 int launch_combine(const CombineParams& p, void* stream);
 int launch_combine_backward(const CombineParams& p, void* stream);
 int launch_expert(const ExpertParams& p, void* stream);
+// The tensor-core form; false when it cannot take these sizes and strides.
+bool launch_expert_tc(const ExpertParams& p, void* stream, int* status);
 
 }  // namespace ciera
