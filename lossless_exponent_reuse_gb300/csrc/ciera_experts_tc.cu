@@ -11,10 +11,10 @@
 // would waste up to 127, and the lanes of a warp hold neighbouring features of
 // one row, which they store contiguously without a transposition.
 //
-// A persistent block of six warps per SM: warp 0 moves tiles of 128 bytes by
-// 64 or 128 rows into a ring of stages with TMA (128-byte swizzle; gathered
-// rows four per instruction), one lane of warp 1 issues tcgen05.mma into one
-// of two accumulators in TMEM, warps 2 to 5 store the other accumulator.
+// A persistent block per SM: warp 0 moves tiles of 128 bytes by 64 or 128 rows
+// into a ring of stages with TMA (128-byte swizzle), four warps copy gathered
+// rows to the same places, one lane of warp 1 issues tcgen05.mma into one
+// of two accumulators in TMEM, warps 2 to 9 store the other accumulator.
 // Tiles are dealt out round-robin over all groups; each block finds the
 // groups' tiles from the offsets by itself.
 #include <cuda.h>
@@ -25,7 +25,9 @@
 namespace ciera {
 namespace {
 
-constexpr int kTcThreads = 192;
+constexpr int kStoreWarps = 8;
+constexpr int kGatherWarps = 4;
+constexpr int kTcThreads = 64 + 32 * kStoreWarps + 32 * kGatherWarps;
 constexpr int kTileM = 128;             // features of one accumulator
 constexpr int kRowBytes = 128;          // bytes of the contraction per stage and row
 constexpr int kBoxRows = 64;            // rows of one B load
@@ -64,14 +66,15 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
       : "memory");
 }
 
-// Four rows of one box height each; a row outside the matrix arrives as zeros.
-__device__ __forceinline__ void tma_gather(uint32_t dst, const CUtensorMap* map, int32_t x,
-                                           int4 row, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(row.x), "r"(row.y), "r"(row.z), "r"(row.w), "r"(smem_addr(bar))
-      : "memory");
+// 16 bytes to shared memory, of which the first `bytes` come from `src`.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
 }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
@@ -100,21 +103,6 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
   asm volatile(
       "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
           smem_addr(bar))
-      : "memory");
-}
-
-__device__ __forceinline__ void tmem_ld32(uint32_t addr, float (&v)[32]) {
-  uint32_t* r = reinterpret_cast<uint32_t*>(v);
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
-        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
-        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
-      : "r"(addr)
       : "memory");
 }
 
@@ -277,21 +265,22 @@ __device__ __forceinline__ bool wait(const TcParams& p, Shared& sh, uint64_t* ba
   return true;
 }
 
+// x's row behind grouped row r; -1: none (zeros).
 __device__ __forceinline__ int32_t token_row(const ExpertParams& p, int32_t r, int32_t end) {
-  if (r >= end) return static_cast<int32_t>(p.x_rows);  // outside: zeros
+  if (r >= end) return -1;
   const int32_t t = p.row_tokens[r];
-  return t >= 0 && t < p.x_rows ? t : static_cast<int32_t>(p.x_rows);
+  return t >= 0 && t < p.x_rows ? t : -1;
 }
 
-__device__ __forceinline__ int4 token_rows(const ExpertParams& p, int32_t r, int32_t end) {
-  return make_int4(token_row(p, r, end), token_row(p, r + 1, end), token_row(p, r + 2, end),
-                   token_row(p, r + 3, end));
+// exp and the quotient to a few units in the last of 24 bits; the results are
+// rounded to 8.
+__device__ __forceinline__ float sigmoid(float a) {
+  return __fdividef(1.0f, 1.0f + __expf(-a));
 }
-
-__device__ __forceinline__ float silu(float a) { return a / (1.0f + expf(-a)); }
+__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
 
 // ------------------------------------------------------------------------
-// Warp 0: loads.
+// Warp 0: loads by TMA.  Gathered rows are left to the gathering warps.
 
 template <int kOp, bool kGated, bool kE4m3>
 __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CUtensorMap* map_b,
@@ -299,23 +288,16 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
   constexpr int kDepth = kE4m3 ? 128 : 64;  // contraction per stage
   constexpr bool kFused = kOp == kExpertForward && kGated;
   const int lane = threadIdx.x & 31;
-  const bool gather = p.e.row_tokens != nullptr;
+  const bool gather = kOp != kExpertDx && p.e.row_tokens != nullptr;
   int issued = 0;
   Walk<kOp> walk;
   OutTile t;
   bool alive = true;
   while (alive && walk.next(p, sh, t)) {
-    const int n = (t.rows + 15) & ~15;
-    const int boxes = (n + kBoxRows - 1) / kBoxRows;
-    const int32_t end = kOp == kExpertDw ? t.from + t.depth : t.row + t.rows;
-    int4 rows_lo{}, rows_hi{};  // forward: this lane's gathered rows
-    if (kOp == kExpertForward && gather && t.depth > 0) {
-      rows_lo = token_rows(p.e, t.row + 4 * lane, end);
-      rows_hi = token_rows(p.e, t.row + 4 * lane + 128, end);
-    }
-    int4 rows_next{};           // dw: of the next stage, fetched one ahead
-    const int quad = (lane & 15) * 4;
-    if (kOp == kExpertDw && gather && t.depth > 0) rows_next = token_rows(p.e, t.from + quad, end);
+    const int boxes = (t.rows + kBoxRows - 1) / kBoxRows;
+    const bool load_a = !(kOp == kExpertDw && gather), load_b = !(kOp == kExpertForward && gather);
+    const uint32_t bytes =
+        (load_a ? p.a_bytes : 0) + (load_b ? boxes * kBoxRows * kRowBytes : 0);
     for (int c = 0; c < t.depth; c += kDepth) {
       const int stage = issued % p.stages;
       const uint32_t parity = (issued / p.stages) & 1;
@@ -323,43 +305,26 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
       if (!alive) break;
       const uint32_t a = ring + stage * p.stage_bytes, b = a + p.a_bytes;
       uint64_t* bar = &sh.full[stage];
-      if (kOp == kExpertDw) {
-        const int4 rows = rows_next;
-        if (lane == 0) mbar_arrive_expect_tx(bar, p.a_bytes + boxes * kBoxRows * kRowBytes);
-        __syncwarp();
-        if (gather) {
-          if (c + kDepth < t.depth) rows_next = token_rows(p.e, t.from + c + kDepth + quad, end);
-          tma_gather(a + (lane >> 4) * 64 * kRowBytes + quad * kRowBytes, map_a,
-                     t.feature + (lane >> 4) * 64, rows, bar);
-        } else if (lane < 2) {
-          tma_2d(a + lane * 64 * kRowBytes, map_a, t.feature + lane * 64, t.from + c, bar);
-        }
-        if (lane >= 8 && lane < 8 + boxes) {
-          const int i = lane - 8;
-          tma_2d(b + i * 64 * kRowBytes, map_b, t.row + i * 64, t.from + c, bar);
-        }
-      } else {
-        const bool by_token = kOp == kExpertForward && gather;
-        if (lane == 0)
-          mbar_arrive_expect_tx(
-              bar, p.a_bytes + (by_token ? n : boxes * kBoxRows) * kRowBytes);
-        __syncwarp();
-        if (kOp == kExpertForward) {
-          if (lane == 0) tma_3d(a, map_a, c, t.feature, t.group, bar);
-          if (kFused && lane == 1)
-            tma_3d(a + kTileM * kRowBytes, map_a, c, static_cast<int>(p.e.n) + t.feature, t.group,
-                   bar);
-        } else if (lane < 2) {
-          tma_3d(a + lane * 64 * kRowBytes, map_a, t.feature + lane * 64, c, t.group, bar);
-        }
-        if (by_token) {
-          if (4 * lane < n) tma_gather(b + 4 * lane * kRowBytes, map_b, c, rows_lo, bar);
-          if (4 * lane + 128 < n)
-            tma_gather(b + (4 * lane + 128) * kRowBytes, map_b, c, rows_hi, bar);
-        } else if (lane >= 8 && lane < 8 + boxes) {
-          const int i = lane - 8;
+      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      __syncwarp();
+      if (kOp == kExpertForward) {
+        if (lane == 0) tma_3d(a, map_a, c, t.feature, t.group, bar);
+        if (kFused && lane == 1)
+          tma_3d(a + kTileM * kRowBytes, map_a, c, static_cast<int>(p.e.n) + t.feature, t.group,
+                 bar);
+      } else if (load_a && lane < 2) {
+        const uint32_t to = a + lane * 64 * kRowBytes;
+        if (kOp == kExpertDx)
+          tma_3d(to, map_a, t.feature + lane * 64, c, t.group, bar);
+        else
+          tma_2d(to, map_a, t.feature + lane * 64, t.from + c, bar);
+      }
+      if (load_b && lane >= 8 && lane < 8 + boxes) {
+        const int i = lane - 8;
+        if (kOp == kExpertDw)
+          tma_2d(b + i * kBoxRows * kRowBytes, map_b, t.row + i * kBoxRows, t.from + c, bar);
+        else
           tma_2d(b + i * kBoxRows * kRowBytes, map_b, c, t.row + i * kBoxRows, bar);
-        }
       }
       ++issued;
     }
@@ -368,6 +333,91 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
   if (!alive)
     for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
       mbar_wait_bounded(&sh.full[i % p.stages], (i / p.stages) & 1, p.e.timeout_ns);
+}
+
+// ------------------------------------------------------------------------
+// Warps 10 to 13: gathered rows, 16 bytes per thread and copy, written where
+// the 128-byte swizzle has them.  (TMA's own gather of four rows delivers 128
+// bytes about every 20 cycles, a sixth of what the products take: 1222 us for
+// the gated product of 64225 rows, 2048 to 2 x 1024.)  A stage is handed over
+// kBehind stages after its copies were issued, so that their latency overlaps.
+
+constexpr int kBehind = 2;
+
+template <int kOp, bool kE4m3>
+__device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
+  constexpr int kDepth = kE4m3 ? 128 : 64;
+  constexpr int kSize = kE4m3 ? 1 : 2;
+  const ExpertParams& e = p.e;
+  const int tid = threadIdx.x - (kTcThreads - 32 * kGatherWarps);
+  const int piece = tid & 7, row0 = tid >> 3;  // 16 rows of 8 pieces a sweep
+  const unsigned char* x = static_cast<const unsigned char*>(e.x);
+  const int64_t stride = e.x_stride * kSize;
+  int issued = 0;
+  const auto hand_over = [&](int i) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.full[i % p.stages]);
+  };
+  Walk<kOp> walk;
+  OutTile t;
+  bool alive = true;
+  while (alive && walk.next(p, sh, t)) {
+    if (t.depth == 0) continue;
+    constexpr int kRows = kOp == kExpertForward ? kMaxN / 16 : 4;  // rows per thread and stage
+    const int32_t end = kOp == kExpertDw ? t.from + t.depth : t.row + t.rows;
+    int32_t token[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      token[i] = token_row(e, (kOp == kExpertDw ? t.from : t.row) + row0 + 16 * i, end);
+    for (int c = 0; c < t.depth; c += kDepth) {
+      const int stage = issued % p.stages;
+      alive = wait(p, sh, &sh.empty[stage], ((issued / p.stages) & 1) ^ 1);
+      if (!alive) break;
+      const uint32_t to = ring + stage * p.stage_bytes + (kOp == kExpertForward ? p.a_bytes : 0);
+      if (kOp == kExpertForward) {
+        // bytes of the row from this piece on
+        const int64_t have = (static_cast<int64_t>(t.depth) - c) * kSize - piece * 16;
+        const int bytes = have <= 0 ? 0 : have < 16 ? static_cast<int>(have) : 16;
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+          const int row = row0 + 16 * i;
+          if (row >= ((t.rows + 15) & ~15)) break;
+          const bool some = token[i] >= 0 && bytes > 0;
+          copy16(to + row * kRowBytes + ((piece ^ (row & 7)) << 4),
+                 some ? x + token[i] * stride + static_cast<int64_t>(c) * kSize + piece * 16 : x,
+                 some ? bytes : 0);
+        }
+      } else {
+#pragma unroll
+        for (int column = 0; column < 2; ++column) {
+          const int64_t first = t.feature + column * 64 + piece * 8;
+          const int64_t have = (e.k - first) * 2;
+          const int bytes = have <= 0 ? 0 : have < 16 ? static_cast<int>(have) : 16;
+#pragma unroll
+          for (int i = 0; i < kRows; ++i) {
+            const int row = row0 + 16 * i;
+            const bool some = token[i] >= 0 && bytes > 0;
+            copy16(to + column * 64 * kRowBytes + row * kRowBytes + ((piece ^ (row & 7)) << 4),
+                   some ? x + token[i] * stride + first * 2 : x, some ? bytes : 0);
+          }
+        }
+        if (c + kDepth < t.depth)
+#pragma unroll
+          for (int i = 0; i < kRows; ++i)
+            token[i] = token_row(e, t.from + c + kDepth + row0 + 16 * i, end);
+      }
+      copy_commit();
+      ++issued;
+      if (issued > kBehind) {
+        copy_wait<kBehind>();
+        hand_over(issued - 1 - kBehind);
+      }
+    }
+  }
+  copy_wait<0>();
+  if (alive)
+    for (int i = issued > kBehind ? issued - kBehind : 0; i < issued; ++i) hand_over(i);
 }
 
 // ------------------------------------------------------------------------
@@ -438,23 +488,67 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned 
 }
 
 // ------------------------------------------------------------------------
-// Warps 2 to 5: outputs.  A thread holds one feature of 32 (or 16) rows; the
-// 32 lanes of a warp store 32 neighbouring features of a row.
+// Warps 2 to 9: outputs.  A thread holds one feature of 16 rows at a time;
+// the 32 lanes of a warp store 32 neighbouring features of a row.  Two warps
+// share a quarter of the features (a warp can read only the TMEM lanes of its
+// number modulo 4) and take alternate chunks of rows.
+//
+// Nothing in a chunk branches on a row: loads come from the last row where a
+// row lies behind the tile, so that sixteen independent rows hide each
+// other's latency, and only the stores are predicated.  (With a test per row
+// the exponentials, divisions and loads of a chunk ran one after another:
+// 2111 instead of 259 us for the
+// gradient through the gated unit of 64225 rows, 2048 to 1024.)
+
+constexpr int kChunk = 16;
+
+// 16 rows of one feature each to bf16, row j at out + j * stride.
+__device__ __forceinline__ void store_bf16(uint16_t* out, int64_t stride, const float* v, int left,
+                                           bool mine) {
+  if (left >= kChunk) {
+    if (mine)
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) out[j * stride] = f32_to_bf16(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kChunk; ++j)
+      if (mine && j < left) out[j * stride] = f32_to_bf16(v[j]);
+  }
+}
+
+// Scale of x's row behind grouped row r.
+__device__ __forceinline__ float row_scale(const ExpertParams& e, int64_t r) {
+  int64_t x = r;
+  if (e.row_tokens) {
+    x = e.row_tokens[r];
+    if (x < 0 || x >= e.x_rows) return 0.0f;
+  }
+  return e.x_scale[x];
+}
 
 template <int kOp, bool kGated, bool kE4m3>
 __device__ void store_tiles(const TcParams& p, Shared& sh) {
   constexpr bool kFused = kOp == kExpertForward && kGated;
   const ExpertParams& e = p.e;
-  const int lane = threadIdx.x & 31, quadrant = (threadIdx.x >> 5) & 3;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quadrant = warp & 3;
+  const int half = (warp - 2) >> 2;
   const int64_t features = kOp == kExpertForward ? e.n : e.k;
+  uint16_t* y = static_cast<uint16_t*>(e.y);
   int tiles = 0;
   Walk<kOp> walk;
   OutTile t;
   while (walk.next(p, sh, t)) {
     const int64_t f = t.feature + quadrant * 32 + lane;
     const bool mine = f < features;
+    const int64_t f_in = mine ? f : features - 1;  // for loads
     const int buffer = tiles & 1;
     const bool zero = t.depth == 0;
+    float scale = 1.0f, scale_up = 1.0f;
+    if (kE4m3 && !zero) {
+      const float* ws = e.w_scale + static_cast<int64_t>(t.group) * (kFused ? 2 : 1) * e.n;
+      scale = ws[f_in];
+      if (kFused) scale_up = ws[f_in + e.n];
+    }
     if (!zero) {
       if (!wait(p, sh, &sh.acc_full[buffer], (tiles >> 1) & 1)) return;
       tc_fence_after();
@@ -462,76 +556,86 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
     }
     const uint32_t acc =
         sh.tmem + buffer * kMaxN + (static_cast<uint32_t>(quadrant * 32) << 16);
-    float scale = 1.0f, scale_up = 1.0f;
-    if (kE4m3 && !zero && mine) {
-      const float* ws = e.w_scale + static_cast<int64_t>(t.group) * (kFused ? 2 : 1) * e.n;
-      scale = ws[f];
-      if (kFused) scale_up = ws[f + e.n];
-    }
-    constexpr int kChunk = kFused ? 16 : 32;
-    for (int c = 0; c < t.rows; c += kChunk) {
-      float v[kChunk * (kFused ? 2 : 1)];
+    for (int c = half * kChunk; c < t.rows; c += 2 * kChunk) {
+      const int left = t.rows - c;
+      const int64_t r = t.row + c;
+      float v[kChunk], up[kChunk];
+      uint16_t gate_in[kChunk], up_in[kChunk];
+      float row = 0.0f;  // e4m3: lane j holds row j's scale
+      if (kOp == kExpertDx && kGated && !zero) {
+        const uint16_t* pre = e.pre_in + r * 2 * e.k + f_in;
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) {
+          const int64_t at = min(j, left - 1) * 2 * e.k;
+          gate_in[j] = pre[at];
+          up_in[j] = pre[at + e.k];
+        }
+      }
+      if (kE4m3 && !zero && lane < min(left, kChunk)) row = row_scale(e, r + lane);
       if (zero) {
 #pragma unroll
-        for (int j = 0; j < kChunk * (kFused ? 2 : 1); ++j) v[j] = 0.0f;
+        for (int j = 0; j < kChunk; ++j) v[j] = up[j] = 0.0f;
       } else {
-        if constexpr (kFused) {
-          tmem_ld16(acc + c, v);
-          tmem_ld16(acc + kMaxN / 2 + c, v + 16);
-        } else {
-          tmem_ld32(acc + c, v);
-        }
+        tmem_ld16(acc + c, v);
+        if (kFused) tmem_ld16(acc + kMaxN / 2 + c, up);
         tmem_ld_wait();
       }
+      if (kE4m3 && !zero) {
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        if (c + j >= t.rows || !mine) break;
-        const int64_t r = t.row + c + j;
-        if (kOp == kExpertDw) {
-          const int64_t at = t.group * e.y_expert_stride + r * e.y_stride + f;
-          if (e.f32_out) {
-            float* out = static_cast<float*>(e.y) + at;
-            *out = e.accumulate ? *out + v[j] : v[j];
-          } else {
-            uint16_t* out = static_cast<uint16_t*>(e.y) + at;
-            *out = f32_to_bf16(e.accumulate ? bf16_to_f32(*out) + v[j] : v[j]);
-          }
-          continue;
+        for (int j = 0; j < kChunk; ++j) {
+          const float xs = __shfl_sync(0xffffffffu, row, j);
+          v[j] *= xs * scale;
+          if (kFused) up[j] *= xs * scale_up;
         }
-        uint16_t* y = static_cast<uint16_t*>(e.y);
-        if (kOp == kExpertForward) {
-          float a = v[j], up = kFused ? v[kChunk + j - (kFused ? 0 : kChunk)] : 0.0f;
-          if (kE4m3 && !zero) {
-            int64_t x = r;
-            if (e.row_tokens) {
-              x = e.row_tokens[r];
-              x = x >= 0 && x < e.x_rows ? x : -1;
-            }
-            const float xs = x >= 0 ? e.x_scale[x] : 0.0f;
-            a *= xs * scale;
-            if (kFused) up *= xs * scale_up;
+      }
+      if (kFused) {
+        if (e.pre_out) {
+          uint16_t* pre = e.pre_out + r * 2 * e.n + f;
+          store_bf16(pre, 2 * e.n, v, left, mine);
+          store_bf16(pre + e.n, 2 * e.n, up, left, mine);
+        }
+#pragma unroll
+        for (int j = 0; j < kChunk; ++j) v[j] = silu(v[j]) * up[j];
+      }
+      if (kOp == kExpertForward) {
+        store_bf16(y + r * e.n + f, e.n, v, left, mine);
+      } else if (kOp == kExpertDx && kGated) {
+        if (!zero) {
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) {
+            const float g = bf16_to_f32(gate_in[j]), u = bf16_to_f32(up_in[j]);
+            const float s = sigmoid(g);
+            up[j] = v[j] * g * s;
+            v[j] = v[j] * u * s * (1.0f + g * (1.0f - s));
           }
-          if (kFused) {
-            if (e.pre_out) {
-              e.pre_out[r * 2 * e.n + f] = f32_to_bf16(a);
-              e.pre_out[r * 2 * e.n + e.n + f] = f32_to_bf16(up);
-            }
-            a = silu(a) * up;
+        }
+        store_bf16(y + r * 2 * e.k + f, 2 * e.k, v, left, mine);
+        store_bf16(y + r * 2 * e.k + e.k + f, 2 * e.k, up, left, mine);
+      } else if (kOp == kExpertDx) {
+        store_bf16(y + r * e.k + f, e.k, v, left, mine);
+      } else {
+        const int64_t at = t.group * e.y_expert_stride + r * e.y_stride + f;
+        if (e.f32_out) {
+          float* out = static_cast<float*>(e.y) + at;
+          if (e.accumulate) {
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j)
+              up[j] = mine && j < left ? out[j * e.y_stride] : 0.0f;
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) v[j] += up[j];
           }
-          y[r * e.n + f] = f32_to_bf16(a);
-        } else if (kGated) {
-          float dg = 0.0f, du = 0.0f;
-          if (!zero) {
-            const float g = bf16_to_f32(e.pre_in[r * 2 * e.k + f]);
-            const float u = bf16_to_f32(e.pre_in[r * 2 * e.k + e.k + f]);
-            const float s = 1.0f / (1.0f + expf(-g));
-            dg = v[j] * u * s * (1.0f + g * (1.0f - s));
-            du = v[j] * g * s;
-          }
-          y[r * 2 * e.k + f] = f32_to_bf16(dg);
-          y[r * 2 * e.k + e.k + f] = f32_to_bf16(du);
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j)
+            if (mine && j < left) out[j * e.y_stride] = v[j];
         } else {
-          y[r * e.k + f] = f32_to_bf16(v[j]);
+          uint16_t* out = y + at;
+          if (e.accumulate) {
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) up_in[j] = mine && j < left ? out[j * e.y_stride] : 0;
+#pragma unroll
+            for (int j = 0; j < kChunk; ++j) v[j] += bf16_to_f32(up_in[j]);
+          }
+          store_bf16(out, e.y_stride, v, left, mine);
         }
       }
       __syncwarp();
@@ -554,14 +658,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t ring = (base + 1023) & ~1023u;
   unsigned char* ring_ptr = raw + (ring - base);
   const int warp = threadIdx.x >> 5;
+  const bool gather = kOp != kExpertDx && p.e.row_tokens != nullptr;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], gather ? 1 + kGatherWarps : 1);
       mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 1);
-      mbar_init(&sh.acc_empty[i], 128);
+      mbar_init(&sh.acc_empty[i], 32 * kStoreWarps);
     }
     sh.stop = 0;
     fence_barrier_init();
@@ -582,8 +687,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     load_tiles<kOp, kGated, kE4m3>(p, &map_a, &map_b, sh, ring);
   else if (warp == 1)
     multiply<kOp, kGated, kE4m3>(p, sh, ring, ring_ptr);
-  else
+  else if (warp < 2 + kStoreWarps)
     store_tiles<kOp, kGated, kE4m3>(p, sh);
+  else if (gather)
+    gather_tiles<kOp, kE4m3>(p, sh, ring);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -685,18 +792,17 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   p.n_tiles = static_cast<int32_t>(n_tiles);
 
   CUtensorMap a, b;
-  const int gathered = e.row_tokens ? 1 : 0;
   bool ok;
   if (e.op == kExpertForward)
     ok = make_map(&a, e.w, e.e4m3, e.k, fused ? 2 * e.n : e.n, e.w_stride, e.experts,
                   e.w_expert_stride, kTileM) &&
          make_map(&b, e.x, e.e4m3, e.k, e.x_rows, e.x_stride, 1, kNoPlanes,
-                  gathered ? 1 : kBoxRows);
+                  kBoxRows);
   else if (e.op == kExpertDx)
     ok = make_map(&a, e.w, false, e.k, e.n, e.w_stride, e.experts, e.w_expert_stride, 64) &&
          make_map(&b, e.x, false, e.n, e.x_rows, e.x_stride, 1, kNoPlanes, kBoxRows);
   else
-    ok = make_map(&a, e.x, false, e.k, e.x_rows, e.x_stride, 1, kNoPlanes, gathered ? 1 : 64) &&
+    ok = make_map(&a, e.x, false, e.k, e.x_rows, e.x_stride, 1, kNoPlanes, 64) &&
          make_map(&b, e.w, false, e.n, e.rows, e.w_stride, 1, kNoPlanes, 64);
   if (!ok) return false;
 
