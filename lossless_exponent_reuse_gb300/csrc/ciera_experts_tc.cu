@@ -71,11 +71,13 @@ __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes)
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int kLeft>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+// Arrives on `bar` (an arrival it counts on) when this thread's copies so far
+// have landed.
+__device__ __forceinline__ void copy_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
 }
+__device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
@@ -339,10 +341,8 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
 // Warps 10 to 13: gathered rows, 16 bytes per thread and copy, written where
 // the 128-byte swizzle has them.  (TMA's own gather of four rows delivers 128
 // bytes about every 20 cycles, a sixth of what the products take: 1222 us for
-// the gated product of 64225 rows, 2048 to 2 x 1024.)  A stage is handed over
-// kBehind stages after its copies were issued, so that their latency overlaps.
-
-constexpr int kBehind = 2;
+// the gated product of 64225 rows, 2048 to 2 x 1024.)  A stage's barrier counts
+// the threads whose copies have landed; nobody waits for them but the products.
 
 template <int kOp, bool kE4m3>
 __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
@@ -354,11 +354,6 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
   const unsigned char* x = static_cast<const unsigned char*>(e.x);
   const int64_t stride = e.x_stride * kSize;
   int issued = 0;
-  const auto hand_over = [&](int i) {
-    fence_proxy_async_smem();
-    __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive(&sh.full[i % p.stages]);
-  };
   Walk<kOp> walk;
   OutTile t;
   bool alive = true;
@@ -407,17 +402,11 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
           for (int i = 0; i < kRows; ++i)
             token[i] = token_row(e, t.from + c + kDepth + row0 + 16 * i, end);
       }
-      copy_commit();
+      copy_arrive(&sh.full[stage]);
       ++issued;
-      if (issued > kBehind) {
-        copy_wait<kBehind>();
-        hand_over(issued - 1 - kBehind);
-      }
     }
   }
-  copy_wait<0>();
-  if (alive)
-    for (int i = issued > kBehind ? issued - kBehind : 0; i < issued; ++i) hand_over(i);
+  copy_wait_all();
 }
 
 // ------------------------------------------------------------------------
@@ -430,6 +419,7 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned 
   constexpr bool kFused = kOp == kExpertForward && kGated;
   constexpr bool kARows = kOp != kExpertForward, kBRows = kOp == kExpertDw;
   const int lane = threadIdx.x & 31;
+  const bool gather = kOp != kExpertDx && p.e.row_tokens != nullptr;
   int used = 0, tiles = 0;
   Walk<kOp> walk;
   OutTile t;
@@ -462,6 +452,9 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned 
         fence_proxy_async_smem();
         __syncwarp();
       }
+      // gathered rows came by ordinary copies: order them before the
+      // tensor core's reads
+      if (gather) fence_proxy_async_smem();
       tc_fence_after();
       if (lane == 0) {
         for (int s = 0; s < steps; ++s) {
@@ -661,7 +654,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const bool gather = kOp != kExpertDx && p.e.row_tokens != nullptr;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&sh.full[i], gather ? 1 + kGatherWarps : 1);
+      mbar_init(&sh.full[i], gather ? 1 + 32 * kGatherWarps : 1);
       mbar_init(&sh.empty[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
