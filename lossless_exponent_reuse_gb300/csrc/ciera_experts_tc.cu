@@ -48,22 +48,40 @@ struct TcParams {
 // ------------------------------------------------------------------------
 // PTX
 
+// Loads to this block's shared memory; `bar` counts their bytes: a barrier of
+// this block, or (kPair 2) one of the pair's first block.
+template <int kPair>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
-                                       uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(smem_addr(bar))
-      : "memory");
+                                       uint32_t bar) {
+  if (kPair == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(bar)
+        : "memory");
 }
 
+template <int kPair>
 __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
-                                       int32_t z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-      "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
-      : "memory");
+                                       int32_t z, uint32_t bar) {
+  if (kPair == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
 }
 
 // 16 bytes to shared memory, of which the first `bytes` come from `src`.
@@ -83,29 +101,72 @@ __device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
   asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
-template <bool kE4m3>
+// kPair: blocks of one product (1, or 2 neighbours of a cluster, whose tensor
+// cores take the two halves of its features and share its rows).
+template <bool kE4m3, int kPair>
 __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                     uint32_t accumulate) {
-  if (kE4m3)
+#define CIERA_MMA(group, kind)                                                         \
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma." group kind \
+               " [%0], %1, %2, %3, p;\n\t}" ::"r"(d),                                  \
+               "l"(a), "l"(b), "r"(idesc), "r"(accumulate)                             \
+               : "memory")
+  if (kPair == 2) {
+    if (kE4m3)
+      CIERA_MMA("cta_group::2", ".kind::f8f6f4");
+    else
+      CIERA_MMA("cta_group::2", ".kind::f16");
+  } else {
+    if (kE4m3)
+      CIERA_MMA("cta_group::1", ".kind::f8f6f4");
+    else
+      CIERA_MMA("cta_group::1", ".kind::f16");
+  }
+#undef CIERA_MMA
+}
+
+// Arrives on `bar` (of both blocks of a pair) when every MMA issued so far by
+// this thread is done.
+template <int kPair>
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  if (kPair == 2)
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_addr(bar)),
+        "h"(static_cast<uint16_t>(3))
         : "memory");
   else
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+            smem_addr(bar))
         : "memory");
 }
 
-// Arrives on `bar` when every MMA issued so far by this thread is done.
-__device__ __forceinline__ void mma_commit(uint64_t* bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-          smem_addr(bar))
-      : "memory");
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+
+// Address of the barrier at the same place in the pair's first block.
+__device__ __forceinline__ uint32_t in_first(const uint64_t* bar) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_addr(bar)));
+  return a;
+}
+
+__device__ __forceinline__ void mbar_arrive_first(const uint64_t* bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(in_first(bar)) : "memory");
+}
+
+template <int kPair>
+__device__ __forceinline__ void sync_all() {
+  if (kPair == 2)
+    asm volatile(
+        "barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::
+            : "memory");
+  else
+    __syncthreads();
 }
 
 __device__ __forceinline__ void tmem_ld16(uint32_t addr, float* v) {
@@ -140,10 +201,11 @@ __device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t stride, uint
 
 // Instruction descriptor: 32-bit float sums, operand types, which operands
 // have the contraction along their rows, N and M.
-__device__ __forceinline__ uint32_t instruction(bool e4m3, bool a_rows, bool b_rows, int n) {
+__device__ __forceinline__ uint32_t instruction(bool e4m3, bool a_rows, bool b_rows, int m,
+                                                int n) {
   const uint32_t type = e4m3 ? 0u : 1u;
   return 1u << 4 | type << 7 | type << 10 | (a_rows ? 1u << 15 : 0u) | (b_rows ? 1u << 16 : 0u) |
-         static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(kTileM >> 4) << 24;
+         static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
 }
 
 // ------------------------------------------------------------------------
@@ -152,6 +214,7 @@ __device__ __forceinline__ uint32_t instruction(bool e4m3, bool a_rows, bool b_r
 struct Shared {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
+  uint64_t tail[kMaxStages];         // dw, second block of a pair: a group's last stage is full
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint32_t tmem;
@@ -160,21 +223,29 @@ struct Shared {
   int32_t tile[kMaxExperts + 2];     // tiles before each group
 };
 
-// Rows per tile of a group of m rows: as few tiles as tile_n allows, of even size.
-__device__ __forceinline__ int rows_per_tile(int m, int tile_n) {
-  const int tiles = (m + tile_n - 1) / tile_n;
-  return tiles <= 1 ? tile_n : ((m + tiles - 1) / tiles + 15) & ~15;
+// N of a tile's instructions: multiples of 16, of 32 for a pair.
+template <int kPair>
+__device__ __forceinline__ int padded(int rows) {
+  constexpr int kGrain = 16 * kPair;
+  return (rows + kGrain - 1) / kGrain * kGrain;
 }
 
-template <int kOp>
+// Rows per tile of a group of m rows: as few tiles as tile_n allows, of even size.
+template <int kPair>
+__device__ __forceinline__ int rows_per_tile(int m, int tile_n) {
+  const int tiles = (m + tile_n - 1) / tile_n;
+  return tiles <= 1 ? tile_n : padded<kPair>((m + tiles - 1) / tiles);
+}
+
+template <int kOp, int kPair>
 __device__ __forceinline__ int tiles_of_group(const TcParams& p, int m, bool unused) {
   if (kOp == kExpertDw) return unused ? 0 : p.m_tiles * p.n_tiles;
-  const int per = rows_per_tile(m, p.tile_n);
+  const int per = rows_per_tile<kPair>(m, p.tile_n);
   return (m + per - 1) / per * p.m_tiles;
 }
 
 // Fills start[] and tile[]; one warp.
-template <int kOp>
+template <int kOp, int kPair>
 __device__ void find_groups(const TcParams& p, Shared& sh) {
   const int lane = threadIdx.x & 31, E = p.e.experts;
   const int32_t rows = static_cast<int32_t>(p.e.rows);
@@ -191,7 +262,7 @@ __device__ void find_groups(const TcParams& p, Shared& sh) {
     end = max(end, highest);
     int32_t begin = __shfl_up_sync(0xffffffffu, end, 1);
     if (lane == 0) begin = highest;
-    const int32_t tiles = g <= E ? tiles_of_group<kOp>(p, end - begin, g == E) : 0;
+    const int32_t tiles = g <= E ? tiles_of_group<kOp, kPair>(p, end - begin, g == E) : 0;
     int32_t sum = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -213,18 +284,18 @@ __device__ void find_groups(const TcParams& p, Shared& sh) {
 
 struct OutTile {
   int group;
-  int feature;   // first feature
+  int feature;   // first feature of this block
   int row;       // first output row: of the grouped rows, or dw's n
   int rows;      // output rows
   int from;      // dw: first grouped row
   int depth;     // length of the contraction; 0: the tile is zeros
 };
 
-// Walks this block's tiles in order.
-template <int kOp>
+// Walks this block's (or pair's) tiles in order.
+template <int kOp, int kPair>
 struct Walk {
   int index, group = 0;
-  __device__ explicit Walk() : index(blockIdx.x) {}
+  __device__ explicit Walk() : index(blockIdx.x / kPair) {}
   __device__ bool next(const TcParams& p, const Shared& sh, OutTile& t) {
     const int E = p.e.experts;
     if (index >= sh.tile[E + 1]) return false;
@@ -232,7 +303,8 @@ struct Walk {
     const int local = index - sh.tile[group];
     const int m = sh.start[group + 1] - sh.start[group];
     t.group = group;
-    t.feature = local % p.m_tiles * kTileM;
+    t.feature = local % p.m_tiles * (kTileM * kPair) +
+                (kPair == 2 ? static_cast<int>(cluster_rank()) * kTileM : 0);
     const int at = local / p.m_tiles;
     if (kOp == kExpertDw) {
       t.row = at * p.tile_n;
@@ -240,13 +312,13 @@ struct Walk {
       t.from = sh.start[group];
       t.depth = m;
     } else {
-      const int per = rows_per_tile(m, p.tile_n);
+      const int per = rows_per_tile<kPair>(m, p.tile_n);
       t.row = sh.start[group] + at * per;
       t.rows = min(per, m - at * per);
       t.from = 0;
       t.depth = group == E ? 0 : static_cast<int>(kOp == kExpertForward ? p.e.k : p.e.n);
     }
-    index += gridDim.x;
+    index += gridDim.x / kPair;
     return true;
   }
 };
@@ -282,21 +354,28 @@ __device__ __forceinline__ float sigmoid(float a) {
 __device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
 
 // ------------------------------------------------------------------------
-// Warp 0: loads by TMA.  Gathered rows are left to the gathering warps.
+// Warp 0: loads by TMA.  Gathered rows are left to the gathering warps.  The
+// bytes of both blocks of a pair are counted by the first one's barriers,
+// where the products are issued.  Only a group's last stage of dw, which has
+// to be cleared behind the last row, is counted where it lands.
 
-template <int kOp, bool kGated, bool kE4m3>
+template <int kOp, bool kGated, bool kE4m3, int kPair>
 __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CUtensorMap* map_b,
                            Shared& sh, uint32_t ring) {
   constexpr int kDepth = kE4m3 ? 128 : 64;  // contraction per stage
   constexpr bool kFused = kOp == kExpertForward && kGated;
   const int lane = threadIdx.x & 31;
-  const bool gather = kOp != kExpertDx && p.e.row_tokens != nullptr;
+  const bool first = kPair == 1 || cluster_rank() == 0;
+  const bool gather = kPair == 1 && kOp != kExpertDx && p.e.row_tokens != nullptr;
   int issued = 0;
-  Walk<kOp> walk;
+  Walk<kOp, kPair> walk;
   OutTile t;
   bool alive = true;
   while (alive && walk.next(p, sh, t)) {
-    const int boxes = (t.rows + kBoxRows - 1) / kBoxRows;
+    // this block's share of the rows
+    const int share = padded<kPair>(t.rows) / kPair;
+    const int row = t.row + (first ? 0 : share);
+    const int boxes = (share + kBoxRows - 1) / kBoxRows;
     const bool load_a = !(kOp == kExpertDw && gather), load_b = !(kOp == kExpertForward && gather);
     const uint32_t bytes =
         (load_a ? p.a_bytes : 0) + (load_b ? boxes * kBoxRows * kRowBytes : 0);
@@ -306,35 +385,51 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
       alive = wait(p, sh, &sh.empty[stage], parity ^ 1);
       if (!alive) break;
       const uint32_t a = ring + stage * p.stage_bytes, b = a + p.a_bytes;
-      uint64_t* bar = &sh.full[stage];
-      if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+      uint32_t bar = smem_addr(&sh.full[stage]);
+      if (kPair == 2) {
+        const bool tail = kOp == kExpertDw && t.depth - c < kDepth;
+        bar = in_first(&sh.full[stage]);
+        if (first) {
+          if (lane == 0) mbar_arrive_expect_tx(&sh.full[stage], tail ? bytes : 2 * bytes);
+        } else if (tail) {
+          bar = smem_addr(&sh.tail[stage]);
+          if (lane == 0) mbar_arrive_expect_tx(&sh.tail[stage], bytes);
+        } else if (kOp == kExpertDw) {
+          if (lane == 0) mbar_arrive_first(&sh.full[stage]);
+        }
+      } else if (lane == 0) {
+        mbar_arrive_expect_tx(&sh.full[stage], bytes);
+      }
       __syncwarp();
       if (kOp == kExpertForward) {
-        if (lane == 0) tma_3d(a, map_a, c, t.feature, t.group, bar);
+        if (lane == 0) tma_3d<kPair>(a, map_a, c, t.feature, t.group, bar);
         if (kFused && lane == 1)
-          tma_3d(a + kTileM * kRowBytes, map_a, c, static_cast<int>(p.e.n) + t.feature, t.group,
-                 bar);
+          tma_3d<kPair>(a + kTileM * kRowBytes, map_a, c, static_cast<int>(p.e.n) + t.feature,
+                        t.group, bar);
       } else if (load_a && lane < 2) {
         const uint32_t to = a + lane * 64 * kRowBytes;
         if (kOp == kExpertDx)
-          tma_3d(to, map_a, t.feature + lane * 64, c, t.group, bar);
+          tma_3d<kPair>(to, map_a, t.feature + lane * 64, c, t.group, bar);
         else
-          tma_2d(to, map_a, t.feature + lane * 64, t.from + c, bar);
+          tma_2d<kPair>(to, map_a, t.feature + lane * 64, t.from + c, bar);
       }
       if (load_b && lane >= 8 && lane < 8 + boxes) {
         const int i = lane - 8;
         if (kOp == kExpertDw)
-          tma_2d(b + i * kBoxRows * kRowBytes, map_b, t.row + i * kBoxRows, t.from + c, bar);
+          tma_2d<kPair>(b + i * kBoxRows * kRowBytes, map_b, row + i * kBoxRows, t.from + c, bar);
         else
-          tma_2d(b + i * kBoxRows * kRowBytes, map_b, c, t.row + i * kBoxRows, bar);
+          tma_2d<kPair>(b + i * kBoxRows * kRowBytes, map_b, c, row + i * kBoxRows, bar);
       }
       ++issued;
     }
   }
-  // Copies still in flight write this block's shared memory: see them land.
-  if (!alive)
-    for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
-      mbar_wait_bounded(&sh.full[i % p.stages], (i / p.stages) & 1, p.e.timeout_ns);
+  // What is still under way writes this block's shared memory: see the products'
+  // last arrivals come in, or after a wait that ran out the copies land (the
+  // second block's are the first's to see).
+  for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
+    uint64_t* bar = alive ? &sh.empty[i % p.stages] : &sh.full[i % p.stages];
+    if (alive || first) mbar_wait_bounded(bar, (i / p.stages) & 1, p.e.timeout_ns);
+  }
 }
 
 // ------------------------------------------------------------------------
@@ -354,17 +449,20 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
   const unsigned char* x = static_cast<const unsigned char*>(e.x);
   const int64_t stride = e.x_stride * kSize;
   int issued = 0;
-  Walk<kOp> walk;
+  Walk<kOp, 1> walk;
   OutTile t;
   bool alive = true;
   while (alive && walk.next(p, sh, t)) {
     if (t.depth == 0) continue;
-    constexpr int kRows = kOp == kExpertForward ? kMaxN / 16 : 4;  // rows per thread and stage
+    const int share = padded<1>(t.rows);
+    const int first_row = kOp == kExpertDw ? t.from : t.row;
+    // rows per thread and stage
+    constexpr int kRows = kOp == kExpertForward ? kMaxN / 16 : 4;
     const int32_t end = kOp == kExpertDw ? t.from + t.depth : t.row + t.rows;
     int32_t token[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
-      token[i] = token_row(e, (kOp == kExpertDw ? t.from : t.row) + row0 + 16 * i, end);
+      token[i] = token_row(e, first_row + row0 + 16 * i, end);
     for (int c = 0; c < t.depth; c += kDepth) {
       const int stage = issued % p.stages;
       alive = wait(p, sh, &sh.empty[stage], ((issued / p.stages) & 1) ^ 1);
@@ -377,7 +475,7 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
           const int row = row0 + 16 * i;
-          if (row >= ((t.rows + 15) & ~15)) break;
+          if (row >= share) break;
           const bool some = token[i] >= 0 && bytes > 0;
           copy16(to + row * kRowBytes + ((piece ^ (row & 7)) << 4),
                  some ? x + token[i] * stride + static_cast<int64_t>(c) * kSize + piece * 16 : x,
@@ -412,16 +510,28 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
 // ------------------------------------------------------------------------
 // Warp 1: products.
 
-template <int kOp, bool kGated, bool kE4m3>
+// Zeroes what a stage holds behind the group's last row, up to the next whole
+// step: rows of the next group, or stale ones.  Both operands, since 0 times
+// an infinity there would be a NaN.
+__device__ __forceinline__ void clear_tail(unsigned char* stage, int columns, int have, int to) {
+  const int words = (to - have) * (kRowBytes / 16);
+  for (int i = threadIdx.x & 31; i < columns * words; i += 32) {
+    const int column = i / words, at = i % words;
+    *reinterpret_cast<uint4*>(stage + column * 64 * kRowBytes + have * kRowBytes + at * 16) =
+        make_uint4(0, 0, 0, 0);
+  }
+}
+
+template <int kOp, bool kGated, bool kE4m3, int kPair>
 __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned char* ring_ptr) {
   constexpr int kDepth = kE4m3 ? 128 : 64;
   constexpr int kStep = kE4m3 ? 32 : 16;   // contraction per instruction
   constexpr bool kFused = kOp == kExpertForward && kGated;
   constexpr bool kARows = kOp != kExpertForward, kBRows = kOp == kExpertDw;
   const int lane = threadIdx.x & 31;
-  const bool gather = kOp != kExpertDx && p.e.row_tokens != nullptr;
+  const bool gather = kPair == 1 && kOp != kExpertDx && p.e.row_tokens != nullptr;
   int used = 0, tiles = 0;
-  Walk<kOp> walk;
+  Walk<kOp, kPair> walk;
   OutTile t;
   while (walk.next(p, sh, t)) {
     if (t.depth == 0) continue;
@@ -429,32 +539,25 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned 
     if (!wait(p, sh, &sh.acc_empty[buffer], ((tiles >> 1) & 1) ^ 1)) return;
     tc_fence_after();
     const uint32_t d = sh.tmem + buffer * kMaxN;
-    const uint32_t idesc = instruction(kE4m3, kARows, kBRows, (t.rows + 15) & ~15);
+    const int n = padded<kPair>(t.rows);
+    const uint32_t idesc = instruction(kE4m3, kARows, kBRows, kTileM * kPair, n);
     for (int c = 0; c < t.depth; c += kDepth) {
       const int stage = used % p.stages;
       if (!wait(p, sh, &sh.full[stage], (used / p.stages) & 1)) return;
       const uint32_t a = ring + stage * p.stage_bytes, b = a + p.a_bytes;
       int steps = kDepth / kStep;
       if (kOp == kExpertDw && t.depth - c < kDepth) {
-        // The stage holds rows of the next group (or stale ones) behind the
-        // group's last: whole steps are skipped, the rest is zeroed in both
-        // operands, since 0 times an infinity there would be a NaN.
         const int have = t.depth - c;
         steps = (have + kStep - 1) / kStep;
-        const int columns = p.a_bytes / (64 * kRowBytes) + (t.rows + 63) / 64;
-        const int words = (steps * kStep - have) * (kRowBytes / 16);
-        unsigned char* base = ring_ptr + stage * p.stage_bytes;
-        for (int i = lane; i < columns * words; i += 32) {
-          const int column = i / words, at = i % words;
-          *reinterpret_cast<uint4*>(base + column * 64 * kRowBytes + have * kRowBytes + at * 16) =
-              make_uint4(0, 0, 0, 0);
-        }
+        clear_tail(ring_ptr + stage * p.stage_bytes,
+                   p.a_bytes / (64 * kRowBytes) + (n / kPair + 63) / 64, have, steps * kStep);
         fence_proxy_async_smem();
         __syncwarp();
+      } else if (gather) {
+        // gathered rows came by ordinary copies: order them before the
+        // tensor core's reads
+        fence_proxy_async_smem();
       }
-      // gathered rows came by ordinary copies: order them before the
-      // tensor core's reads
-      if (gather) fence_proxy_async_smem();
       tc_fence_after();
       if (lane == 0) {
         for (int s = 0; s < steps; ++s) {
@@ -463,20 +566,46 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned 
           const uint32_t step_b = kBRows ? s * kStep * kRowBytes : s * 32;
           const uint64_t da = operand(a + step_a, 8 * kRowBytes, kARows ? 64 * kRowBytes : 0);
           const uint64_t db = operand(b + step_b, 8 * kRowBytes, kBRows ? 64 * kRowBytes : 0);
-          mma<kE4m3>(d, da, db, idesc, c + s > 0);
+          mma<kE4m3, kPair>(d, da, db, idesc, c + s > 0);
           if (kFused) {
             const uint64_t du = operand(a + kTileM * kRowBytes + step_a, 8 * kRowBytes, 0);
-            mma<kE4m3>(d + kMaxN / 2, du, db, idesc, c + s > 0);
+            mma<kE4m3, kPair>(d + kMaxN / 2, du, db, idesc, c + s > 0);
           }
         }
-        mma_commit(&sh.empty[stage]);
+        mma_commit<kPair>(&sh.empty[stage]);
       }
       __syncwarp();
       ++used;
     }
-    if (lane == 0) mma_commit(&sh.acc_full[buffer]);
+    if (lane == 0) mma_commit<kPair>(&sh.acc_full[buffer]);
     __syncwarp();
     ++tiles;
+  }
+}
+
+// Warp 1 of a pair's second block: its part of a group's last stage of dw.  A
+// stage has a barrier of its own for this (several groups' last stages can be
+// under way), used again only when the products have read the stage.
+__device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_ptr) {
+  int used = 0;
+  uint32_t parity = 0;  // of each stage's barrier
+  Walk<kExpertDw, 2> walk;
+  OutTile t;
+  while (walk.next(p, sh, t)) {
+    if (t.depth == 0) continue;
+    used += (t.depth + 63) / 64;
+    const int have = t.depth % 64;
+    if (have == 0) continue;
+    const int stage = (used - 1) % p.stages;
+    if (!wait(p, sh, &sh.tail[stage], parity >> stage & 1)) return;
+    parity ^= 1u << stage;
+    clear_tail(ring_ptr + stage * p.stage_bytes,
+               p.a_bytes / (64 * kRowBytes) + (padded<2>(t.rows) / 2 + 63) / 64, have,
+               (have + 15) & ~15);
+    fence_proxy_async_smem();
+    asm volatile("fence.acq_rel.cluster;" ::: "memory");
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive_first(&sh.full[stage]);
   }
 }
 
@@ -519,7 +648,7 @@ __device__ __forceinline__ float row_scale(const ExpertParams& e, int64_t r) {
   return e.x_scale[x];
 }
 
-template <int kOp, bool kGated, bool kE4m3>
+template <int kOp, bool kGated, bool kE4m3, int kPair>
 __device__ void store_tiles(const TcParams& p, Shared& sh) {
   constexpr bool kFused = kOp == kExpertForward && kGated;
   const ExpertParams& e = p.e;
@@ -528,7 +657,7 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
   const int64_t features = kOp == kExpertForward ? e.n : e.k;
   uint16_t* y = static_cast<uint16_t*>(e.y);
   int tiles = 0;
-  Walk<kOp> walk;
+  Walk<kOp, kPair> walk;
   OutTile t;
   while (walk.next(p, sh, t)) {
     const int64_t f = t.feature + quadrant * 32 + lane;
@@ -635,12 +764,18 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
     }
     if (!zero) {
       tc_fence_before();
-      mbar_arrive(&sh.acc_empty[buffer]);
+      __syncwarp();
+      if (lane == 0) {
+        if (kPair == 2)
+          mbar_arrive_first(&sh.acc_empty[buffer]);
+        else
+          mbar_arrive(&sh.acc_empty[buffer]);
+      }
     }
   }
 }
 
-template <int kOp, bool kGated, bool kE4m3>
+template <int kOp, bool kGated, bool kE4m3, int kPair>
 __global__ void __launch_bounds__(kTcThreads, 1)
     k_expert_tc(const TcParams p, const __grid_constant__ CUtensorMap map_a,
                 const __grid_constant__ CUtensorMap map_b) {
@@ -651,46 +786,66 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t ring = (base + 1023) & ~1023u;
   unsigned char* ring_ptr = raw + (ring - base);
   const int warp = threadIdx.x >> 5;
-  const bool gather = kOp != kExpertDx && p.e.row_tokens != nullptr;
+  const bool gather = kPair == 1 && kOp != kExpertDx && p.e.row_tokens != nullptr;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(&sh.full[i], gather ? 1 + 32 * kGatherWarps : 1);
+      mbar_init(&sh.full[i], gather ? 1 + 32 * kGatherWarps
+                             : kPair == 2 && kOp == kExpertDw ? 2 : 1);
       mbar_init(&sh.empty[i], 1);
+      mbar_init(&sh.tail[i], 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 1);
-      mbar_init(&sh.acc_empty[i], 32 * kStoreWarps);
+      mbar_init(&sh.acc_empty[i], kStoreWarps * kPair);
     }
     sh.stop = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_addr(&sh.tmem)),
-                 "r"(2 * kMaxN)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    if (kPair == 2) {
+      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&sh.tmem)),
+                   "r"(2 * kMaxN)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    } else {
+      asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                       smem_addr(&sh.tmem)),
+                   "r"(2 * kMaxN)
+                   : "memory");
+      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
     tc_fence_before();
   } else if (warp == 2) {
-    find_groups<kOp>(p, sh);
+    find_groups<kOp, kPair>(p, sh);
   }
   __syncthreads();
+  sync_all<kPair>();
   tc_fence_after();
   if (warp == 0)
-    load_tiles<kOp, kGated, kE4m3>(p, &map_a, &map_b, sh, ring);
-  else if (warp == 1)
-    multiply<kOp, kGated, kE4m3>(p, sh, ring, ring_ptr);
-  else if (warp < 2 + kStoreWarps)
-    store_tiles<kOp, kGated, kE4m3>(p, sh);
-  else if (gather)
+    load_tiles<kOp, kGated, kE4m3, kPair>(p, &map_a, &map_b, sh, ring);
+  else if (warp == 1 && (kPair == 1 || cluster_rank() == 0))
+    multiply<kOp, kGated, kE4m3, kPair>(p, sh, ring, ring_ptr);
+  else if (warp == 1 && kOp == kExpertDw)
+    clear_tails(p, sh, ring_ptr);
+  else if (warp >= 2 && warp < 2 + kStoreWarps)
+    store_tiles<kOp, kGated, kE4m3, kPair>(p, sh);
+  else if (warp >= 2 + kStoreWarps && gather)
     gather_tiles<kOp, kE4m3>(p, sh, ring);
   tc_fence_before();
   __syncthreads();
+  sync_all<kPair>();
   tc_fence_after();
-  if (warp == 1)
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem),
-                 "r"(2 * kMaxN)
-                 : "memory");
+  if (warp == 1) {
+    if (kPair == 2)
+      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem),
+                   "r"(2 * kMaxN)
+                   : "memory");
+    else
+      asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem),
+                   "r"(2 * kMaxN)
+                   : "memory");
+  }
 }
 
 // ------------------------------------------------------------------------
@@ -735,16 +890,42 @@ bool make_map(CUtensorMap* map, const void* base, bool e4m3, int64_t columns, in
 }
 constexpr int64_t kNoPlanes = -1;
 
-template <int kOp, bool kGated, bool kE4m3>
+template <int kOp, bool kGated, bool kE4m3, int kPair>
 int launch_at(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid,
               cudaStream_t s) {
-  const int smem = p.stages * p.stage_bytes + 1024;
   static const cudaError_t ready =
-      cudaFuncSetAttribute(k_expert_tc<kOp, kGated, kE4m3>,
+      cudaFuncSetAttribute(k_expert_tc<kOp, kGated, kE4m3, kPair>,
                            cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemLimit - 12 * 1024);
   if (ready != cudaSuccess) return ready;
-  k_expert_tc<kOp, kGated, kE4m3><<<grid, kTcThreads, smem, s>>>(p, a, b);
-  return cudaGetLastError();
+  cudaLaunchConfig_t config{};
+  config.gridDim = dim3(static_cast<unsigned>(grid));
+  config.blockDim = dim3(kTcThreads);
+  config.dynamicSmemBytes = static_cast<size_t>(p.stages) * p.stage_bytes + 1024;
+  config.stream = s;
+  cudaLaunchAttribute pair{};
+  pair.id = cudaLaunchAttributeClusterDimension;
+  pair.val.clusterDim.x = 2;
+  pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
+  config.attrs = &pair;
+  config.numAttrs = kPair == 2 ? 1 : 0;
+  return cudaLaunchKernelEx(&config, k_expert_tc<kOp, kGated, kE4m3, kPair>, p, a, b);
+}
+
+template <int kPair>
+int launch_with(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid,
+                cudaStream_t s) {
+  const ExpertParams& e = p.e;
+  if (e.op == kExpertForward) {
+    if (e.e4m3)
+      return e.gated ? launch_at<kExpertForward, true, true, kPair>(p, a, b, grid, s)
+                     : launch_at<kExpertForward, false, true, kPair>(p, a, b, grid, s);
+    return e.gated ? launch_at<kExpertForward, true, false, kPair>(p, a, b, grid, s)
+                   : launch_at<kExpertForward, false, false, kPair>(p, a, b, grid, s);
+  }
+  if (e.op == kExpertDx)
+    return e.gated ? launch_at<kExpertDx, true, false, kPair>(p, a, b, grid, s)
+                   : launch_at<kExpertDx, false, false, kPair>(p, a, b, grid, s);
+  return launch_at<kExpertDw, false, false, kPair>(p, a, b, grid, s);
 }
 
 int sm_count() {
@@ -773,10 +954,11 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   const bool small = e.op != kExpertDw && e.rows <= 32 * static_cast<int64_t>(e.experts);
   p.tile_n = small ? 64 : fused ? kMaxN / 2 : kMaxN;
   p.a_bytes = (fused ? 2 : 1) * kTileM * kRowBytes;
-  p.stage_bytes = p.a_bytes + p.tile_n * kRowBytes;
+  const int pair = small || e.row_tokens ? 1 : 2;
+  p.stage_bytes = p.a_bytes + p.tile_n / pair * kRowBytes;
   p.stages = (kSmemLimit - 14 * 1024) / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const int64_t m_tiles = (features + kTileM - 1) / kTileM;
+  const int64_t m_tiles = (features + kTileM * pair - 1) / (kTileM * pair);
   const int64_t n_tiles = e.op == kExpertDw ? (e.n + p.tile_n - 1) / p.tile_n : 1;
   const int64_t row_tiles = e.op == kExpertDw ? n_tiles * e.experts
                                               : e.rows / 16 + e.experts + 1;  // at most
@@ -800,21 +982,9 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   if (!ok) return false;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const int64_t most = m_tiles * row_tiles;
-  const int grid = most < sm_count() ? static_cast<int>(most) : sm_count();
-  if (e.op == kExpertForward) {
-    if (e.e4m3)
-      *status = e.gated ? launch_at<kExpertForward, true, true>(p, a, b, grid, s)
-                        : launch_at<kExpertForward, false, true>(p, a, b, grid, s);
-    else
-      *status = e.gated ? launch_at<kExpertForward, true, false>(p, a, b, grid, s)
-                        : launch_at<kExpertForward, false, false>(p, a, b, grid, s);
-  } else if (e.op == kExpertDx) {
-    *status = e.gated ? launch_at<kExpertDx, true, false>(p, a, b, grid, s)
-                      : launch_at<kExpertDx, false, false>(p, a, b, grid, s);
-  } else {
-    *status = launch_at<kExpertDw, false, false>(p, a, b, grid, s);
-  }
+  const int64_t most = m_tiles * row_tiles, slots = sm_count() / pair;
+  const int grid = static_cast<int>(most < slots ? most : slots) * pair;
+  *status = pair == 2 ? launch_with<2>(p, a, b, grid, s) : launch_with<1>(p, a, b, grid, s);
   return true;
 }
 
