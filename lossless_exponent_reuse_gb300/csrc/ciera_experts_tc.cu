@@ -191,6 +191,15 @@ __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// One lane of a warp, the same for every call; the compiler then knows that
+// what it issues is issued once.
+__device__ __forceinline__ bool one_lane() {
+  uint32_t one;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}"
+               : "=r"(one));
+  return one != 0;
+}
+
 // Shared-memory operand: 128-byte swizzle; `stride` bytes between groups of
 // eight rows, `lead` between 128-byte columns (operands with the contraction
 // along the rows only).
@@ -282,6 +291,18 @@ __device__ void find_groups(const TcParams& p, Shared& sh) {
   }
 }
 
+// Place in the ring of stages and the parity of its barriers' phase.
+struct Place {
+  int stage = 0;
+  uint32_t parity = 0;
+  __device__ __forceinline__ void advance(int stages) {
+    if (++stage == stages) {
+      stage = 0;
+      parity ^= 1;
+    }
+  }
+};
+
 struct OutTile {
   int group;
   int feature;   // first feature of this block
@@ -364,9 +385,11 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
                            Shared& sh, uint32_t ring) {
   constexpr int kDepth = kE4m3 ? 128 : 64;  // contraction per stage
   constexpr bool kFused = kOp == kExpertForward && kGated;
-  const int lane = threadIdx.x & 31;
+  if (!one_lane()) return;
   const bool first = kPair == 1 || cluster_rank() == 0;
   const bool gather = kPair == 1 && kOp != kExpertDx && p.e.row_tokens != nullptr;
+  const bool load_a = !(kOp == kExpertDw && gather), load_b = !(kOp == kExpertForward && gather);
+  Place at;
   int issued = 0;
   Walk<kOp, kPair> walk;
   OutTile t;
@@ -376,50 +399,49 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
     const int share = padded<kPair>(t.rows) / kPair;
     const int row = t.row + (first ? 0 : share);
     const int boxes = (share + kBoxRows - 1) / kBoxRows;
-    const bool load_a = !(kOp == kExpertDw && gather), load_b = !(kOp == kExpertForward && gather);
     const uint32_t bytes =
         (load_a ? p.a_bytes : 0) + (load_b ? boxes * kBoxRows * kRowBytes : 0);
     for (int c = 0; c < t.depth; c += kDepth) {
-      const int stage = issued % p.stages;
-      const uint32_t parity = (issued / p.stages) & 1;
-      alive = wait(p, sh, &sh.empty[stage], parity ^ 1);
+      uint64_t* full = &sh.full[at.stage];
+      alive = wait(p, sh, &sh.empty[at.stage], at.parity ^ 1);
       if (!alive) break;
-      const uint32_t a = ring + stage * p.stage_bytes, b = a + p.a_bytes;
-      uint32_t bar = smem_addr(&sh.full[stage]);
+      const uint32_t a = ring + at.stage * p.stage_bytes, b = a + p.a_bytes;
+      uint32_t bar = smem_addr(full);
       if (kPair == 2) {
         const bool tail = kOp == kExpertDw && t.depth - c < kDepth;
-        bar = in_first(&sh.full[stage]);
+        bar = in_first(full);
         if (first) {
-          if (lane == 0) mbar_arrive_expect_tx(&sh.full[stage], tail ? bytes : 2 * bytes);
+          mbar_arrive_expect_tx(full, tail ? bytes : 2 * bytes);
         } else if (tail) {
-          bar = smem_addr(&sh.tail[stage]);
-          if (lane == 0) mbar_arrive_expect_tx(&sh.tail[stage], bytes);
+          bar = smem_addr(&sh.tail[at.stage]);
+          mbar_arrive_expect_tx(&sh.tail[at.stage], bytes);
         } else if (kOp == kExpertDw) {
-          if (lane == 0) mbar_arrive_first(&sh.full[stage]);
+          mbar_arrive_first(full);
         }
-      } else if (lane == 0) {
-        mbar_arrive_expect_tx(&sh.full[stage], bytes);
+      } else {
+        mbar_arrive_expect_tx(full, bytes);
       }
-      __syncwarp();
       if (kOp == kExpertForward) {
-        if (lane == 0) tma_3d<kPair>(a, map_a, c, t.feature, t.group, bar);
-        if (kFused && lane == 1)
+        tma_3d<kPair>(a, map_a, c, t.feature, t.group, bar);
+        if (kFused)
           tma_3d<kPair>(a + kTileM * kRowBytes, map_a, c, static_cast<int>(p.e.n) + t.feature,
                         t.group, bar);
-      } else if (load_a && lane < 2) {
-        const uint32_t to = a + lane * 64 * kRowBytes;
-        if (kOp == kExpertDx)
-          tma_3d<kPair>(to, map_a, t.feature + lane * 64, c, t.group, bar);
-        else
-          tma_2d<kPair>(to, map_a, t.feature + lane * 64, t.from + c, bar);
+      } else if (kOp == kExpertDx) {
+        tma_3d<kPair>(a, map_a, t.feature, c, t.group, bar);
+        tma_3d<kPair>(a + 64 * kRowBytes, map_a, t.feature + 64, c, t.group, bar);
+      } else if (load_a) {
+        tma_2d<kPair>(a, map_a, t.feature, t.from + c, bar);
+        tma_2d<kPair>(a + 64 * kRowBytes, map_a, t.feature + 64, t.from + c, bar);
       }
-      if (load_b && lane >= 8 && lane < 8 + boxes) {
-        const int i = lane - 8;
-        if (kOp == kExpertDw)
-          tma_2d<kPair>(b + i * kBoxRows * kRowBytes, map_b, row + i * kBoxRows, t.from + c, bar);
-        else
-          tma_2d<kPair>(b + i * kBoxRows * kRowBytes, map_b, c, row + i * kBoxRows, bar);
-      }
+      if (load_b)
+        for (int i = 0; i < boxes; ++i) {
+          const uint32_t to = b + i * kBoxRows * kRowBytes;
+          if (kOp == kExpertDw)
+            tma_2d<kPair>(to, map_b, row + i * kBoxRows, t.from + c, bar);
+          else
+            tma_2d<kPair>(to, map_b, c, row + i * kBoxRows, bar);
+        }
+      at.advance(p.stages);
       ++issued;
     }
   }
@@ -448,7 +470,7 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
   const int piece = tid & 7, row0 = tid >> 3;  // 16 rows of 8 pieces a sweep
   const unsigned char* x = static_cast<const unsigned char*>(e.x);
   const int64_t stride = e.x_stride * kSize;
-  int issued = 0;
+  Place at;
   Walk<kOp, 1> walk;
   OutTile t;
   bool alive = true;
@@ -464,8 +486,8 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
     for (int i = 0; i < kRows; ++i)
       token[i] = token_row(e, first_row + row0 + 16 * i, end);
     for (int c = 0; c < t.depth; c += kDepth) {
-      const int stage = issued % p.stages;
-      alive = wait(p, sh, &sh.empty[stage], ((issued / p.stages) & 1) ^ 1);
+      const int stage = at.stage;
+      alive = wait(p, sh, &sh.empty[stage], at.parity ^ 1);
       if (!alive) break;
       const uint32_t to = ring + stage * p.stage_bytes + (kOp == kExpertForward ? p.a_bytes : 0);
       if (kOp == kExpertForward) {
@@ -501,7 +523,7 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
             token[i] = token_row(e, t.from + c + kDepth + row0 + 16 * i, end);
       }
       copy_arrive(&sh.full[stage]);
-      ++issued;
+      at.advance(p.stages);
     }
   }
   copy_wait_all();
@@ -525,12 +547,21 @@ __device__ __forceinline__ void clear_tail(unsigned char* stage, int columns, in
 template <int kOp, bool kGated, bool kE4m3, int kPair>
 __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned char* ring_ptr) {
   constexpr int kDepth = kE4m3 ? 128 : 64;
-  constexpr int kStep = kE4m3 ? 32 : 16;   // contraction per instruction
+  constexpr int kSteps = 4;                // instructions a stage
+  constexpr int kStep = kDepth / kSteps;   // contraction per instruction
   constexpr bool kFused = kOp == kExpertForward && kGated;
   constexpr bool kARows = kOp != kExpertForward, kBRows = kOp == kExpertDw;
-  const int lane = threadIdx.x & 31;
+  // an operand's next step: 32 bytes along its rows, or 16 rows
+  constexpr int kStepA = (kARows ? kStep * kRowBytes : 32) >> 4;
+  constexpr int kStepB = (kBRows ? kStep * kRowBytes : 32) >> 4;
+  const bool one = one_lane();
+  if (kOp != kExpertDw && !one) return;    // dw: the whole warp clears tails
   const bool gather = kPair == 1 && kOp != kExpertDx && p.e.row_tokens != nullptr;
-  int used = 0, tiles = 0;
+  const uint64_t a0 = operand(ring, 8 * kRowBytes, kARows ? 64 * kRowBytes : 0);
+  const uint64_t b0 = operand(ring + p.a_bytes, 8 * kRowBytes, kBRows ? 64 * kRowBytes : 0);
+  const uint32_t tmem = sh.tmem;
+  Place at;
+  int tiles = 0;
   Walk<kOp, kPair> walk;
   OutTile t;
   while (walk.next(p, sh, t)) {
@@ -538,14 +569,14 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned 
     const int buffer = tiles & 1;
     if (!wait(p, sh, &sh.acc_empty[buffer], ((tiles >> 1) & 1) ^ 1)) return;
     tc_fence_after();
-    const uint32_t d = sh.tmem + buffer * kMaxN;
+    const uint32_t d = tmem + buffer * kMaxN;
     const int n = padded<kPair>(t.rows);
     const uint32_t idesc = instruction(kE4m3, kARows, kBRows, kTileM * kPair, n);
+    uint32_t accumulate = 0;
     for (int c = 0; c < t.depth; c += kDepth) {
-      const int stage = used % p.stages;
-      if (!wait(p, sh, &sh.full[stage], (used / p.stages) & 1)) return;
-      const uint32_t a = ring + stage * p.stage_bytes, b = a + p.a_bytes;
-      int steps = kDepth / kStep;
+      const int stage = at.stage;
+      if (!wait(p, sh, &sh.full[stage], at.parity)) return;
+      int steps = kSteps;
       if (kOp == kExpertDw && t.depth - c < kDepth) {
         const int have = t.depth - c;
         steps = (have + kStep - 1) / kStep;
@@ -559,26 +590,23 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned 
         fence_proxy_async_smem();
       }
       tc_fence_after();
-      if (lane == 0) {
-        for (int s = 0; s < steps; ++s) {
-          // along the row 32 bytes a step, along the rows 16 rows
-          const uint32_t step_a = kARows ? s * kStep * kRowBytes : s * 32;
-          const uint32_t step_b = kBRows ? s * kStep * kRowBytes : s * 32;
-          const uint64_t da = operand(a + step_a, 8 * kRowBytes, kARows ? 64 * kRowBytes : 0);
-          const uint64_t db = operand(b + step_b, 8 * kRowBytes, kBRows ? 64 * kRowBytes : 0);
-          mma<kE4m3, kPair>(d, da, db, idesc, c + s > 0);
-          if (kFused) {
-            const uint64_t du = operand(a + kTileM * kRowBytes + step_a, 8 * kRowBytes, 0);
-            mma<kE4m3, kPair>(d + kMaxN / 2, du, db, idesc, c + s > 0);
-          }
+      if (one) {
+        const uint32_t offset = static_cast<uint32_t>(stage * p.stage_bytes) >> 4;
+        const uint64_t a = a0 + offset, b = b0 + offset;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+          if (kOp == kExpertDw && s >= steps) break;
+          mma<kE4m3, kPair>(d, a + s * kStepA, b + s * kStepB, idesc, accumulate);
+          if (kFused)
+            mma<kE4m3, kPair>(d + kMaxN / 2, a + (kTileM * kRowBytes >> 4) + s * kStepA,
+                              b + s * kStepB, idesc, accumulate);
+          accumulate = 1;
         }
         mma_commit<kPair>(&sh.empty[stage]);
       }
-      __syncwarp();
-      ++used;
+      at.advance(p.stages);
     }
-    if (lane == 0) mma_commit<kPair>(&sh.acc_full[buffer]);
-    __syncwarp();
+    if (one) mma_commit<kPair>(&sh.acc_full[buffer]);
     ++tiles;
   }
 }
@@ -593,7 +621,7 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
   OutTile t;
   while (walk.next(p, sh, t)) {
     if (t.depth == 0) continue;
-    used += (t.depth + 63) / 64;
+    used += (t.depth + 63) / 64;  // stages so far
     const int have = t.depth % 64;
     if (have == 0) continue;
     const int stage = (used - 1) % p.stages;
