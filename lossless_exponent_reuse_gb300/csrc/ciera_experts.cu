@@ -114,10 +114,8 @@ __global__ void __launch_bounds__(kExpertThreads) k_expert_any(const ExpertParam
             w = load_value(p.w, expert + (c + part * p.n) * p.w_stride + dd, p.e4m3);
           else if (kOp == kExpertDx)
             w = load_value(p.w, expert + dd * p.w_stride + c, 0);
-          else {
-            const int64_t t = x_row_of(p, x.first + dd);
-            if (t >= 0) w = load_value(p.x, t * p.x_stride + c, 0);
-          }
+          else
+            w = load_value(p.x, (x.first + dd) * p.x_stride + c, 0);
         }
         b[part][db][cb] = w;
       }

@@ -33,6 +33,7 @@ constexpr int kRowBytes = 128;          // bytes of the contraction per stage an
 constexpr int kBoxRows = 64;            // rows of one B load
 constexpr int kMaxStages = 12;
 constexpr int kMaxN = 256;              // columns of one TMEM accumulator buffer
+constexpr int kMaxSmallN = 64;          // most rows of a tile with small groups
 constexpr int kSmemLimit = 227 * 1024;
 
 struct TcParams {
@@ -223,7 +224,7 @@ __device__ __forceinline__ uint32_t instruction(bool e4m3, bool a_rows, bool b_r
 struct Shared {
   uint64_t full[kMaxStages];
   uint64_t empty[kMaxStages];
-  uint64_t tail[kMaxStages];         // dw, second block of a pair: a group's last stage is full
+  uint64_t tail[kMaxStages];         // dw: a group's last stage has landed
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
   uint32_t tmem;
@@ -377,8 +378,7 @@ __device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __e
 // ------------------------------------------------------------------------
 // Warp 0: loads by TMA.  Gathered rows are left to the gathering warps.  The
 // bytes of both blocks of a pair are counted by the first one's barriers,
-// where the products are issued.  Only a group's last stage of dw, which has
-// to be cleared behind the last row, is counted where it lands.
+// where the products are issued.
 
 template <int kOp, bool kGated, bool kE4m3, int kPair>
 __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CUtensorMap* map_b,
@@ -387,8 +387,7 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
   constexpr bool kFused = kOp == kExpertForward && kGated;
   if (!one_lane()) return;
   const bool first = kPair == 1 || cluster_rank() == 0;
-  const bool gather = kPair == 1 && kOp != kExpertDx && p.e.row_tokens != nullptr;
-  const bool load_a = !(kOp == kExpertDw && gather), load_b = !(kOp == kExpertForward && gather);
+  const bool gather = kOp == kExpertForward && kPair == 1 && p.e.row_tokens != nullptr;
   Place at;
   int issued = 0;
   Walk<kOp, kPair> walk;
@@ -399,27 +398,23 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
     const int share = padded<kPair>(t.rows) / kPair;
     const int row = t.row + (first ? 0 : share);
     const int boxes = (share + kBoxRows - 1) / kBoxRows;
-    const uint32_t bytes =
-        (load_a ? p.a_bytes : 0) + (load_b ? boxes * kBoxRows * kRowBytes : 0);
+    const uint32_t bytes = p.a_bytes + (gather ? 0 : boxes * kBoxRows * kRowBytes);
     for (int c = 0; c < t.depth; c += kDepth) {
       uint64_t* full = &sh.full[at.stage];
       alive = wait(p, sh, &sh.empty[at.stage], at.parity ^ 1);
       if (!alive) break;
       const uint32_t a = ring + at.stage * p.stage_bytes, b = a + p.a_bytes;
-      uint32_t bar = smem_addr(full);
-      if (kPair == 2) {
-        const bool tail = kOp == kExpertDw && t.depth - c < kDepth;
-        bar = in_first(full);
-        if (first) {
-          mbar_arrive_expect_tx(full, tail ? bytes : 2 * bytes);
-        } else if (tail) {
-          bar = smem_addr(&sh.tail[at.stage]);
-          mbar_arrive_expect_tx(&sh.tail[at.stage], bytes);
-        } else if (kOp == kExpertDw) {
-          mbar_arrive_first(full);
-        }
-      } else {
-        mbar_arrive_expect_tx(full, bytes);
+      // dw's last stage of a group is counted where it lands, and announced
+      // by who clears it
+      const bool tail = kOp == kExpertDw && t.depth - c < kDepth;
+      uint32_t bar = kPair == 2 ? in_first(full) : smem_addr(full);
+      if (tail) {
+        bar = smem_addr(&sh.tail[at.stage]);
+        mbar_arrive_expect_tx(&sh.tail[at.stage], bytes);
+      } else if (first) {
+        mbar_arrive_expect_tx(full, kPair * bytes);
+      } else if (kOp == kExpertDw) {
+        mbar_arrive_first(full);
       }
       if (kOp == kExpertForward) {
         tma_3d<kPair>(a, map_a, c, t.feature, t.group, bar);
@@ -429,11 +424,11 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
       } else if (kOp == kExpertDx) {
         tma_3d<kPair>(a, map_a, t.feature, c, t.group, bar);
         tma_3d<kPair>(a + 64 * kRowBytes, map_a, t.feature + 64, c, t.group, bar);
-      } else if (load_a) {
+      } else {
         tma_2d<kPair>(a, map_a, t.feature, t.from + c, bar);
         tma_2d<kPair>(a + 64 * kRowBytes, map_a, t.feature + 64, t.from + c, bar);
       }
-      if (load_b)
+      if (!gather)
         for (int i = 0; i < boxes; ++i) {
           const uint32_t to = b + i * kBoxRows * kRowBytes;
           if (kOp == kExpertDw)
@@ -446,8 +441,8 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
     }
   }
   // What is still under way writes this block's shared memory: see the products'
-  // last arrivals come in, or after a wait that ran out the copies land (the
-  // second block's are the first's to see).
+  // last arrivals come in, or after a wait that ran out the copies land (those
+  // of a pair's second block are the first's to see).
   for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
     uint64_t* bar = alive ? &sh.empty[i % p.stages] : &sh.full[i % p.stages];
     if (alive || first) mbar_wait_bounded(bar, (i / p.stages) & 1, p.e.timeout_ns);
@@ -456,73 +451,50 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
 
 // ------------------------------------------------------------------------
 // Warps 10 to 13: gathered rows, 16 bytes per thread and copy, written where
-// the 128-byte swizzle has them.  (TMA's own gather of four rows delivers 128
-// bytes about every 20 cycles, a sixth of what the products take: 1222 us for
-// the gated product of 64225 rows, 2048 to 2 x 1024.)  A stage's barrier counts
-// the threads whose copies have landed; nobody waits for them but the products.
+// the 128-byte swizzle has them.  A stage's barrier counts the threads whose
+// copies have landed; nobody waits for them but the products.  Right for small
+// groups, where it saves a launch; with large ones each row is fetched again
+// for every tile of features and the products wait (gated product of 64225
+// rows, 2048 to 2 x 1024: 412 us, against 333 us from rows gathered before;
+// TMA's own gather, four rows an instruction: 1222 us).
 
-template <int kOp, bool kE4m3>
+template <bool kE4m3>
 __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
   constexpr int kDepth = kE4m3 ? 128 : 64;
   constexpr int kSize = kE4m3 ? 1 : 2;
+  constexpr int kRows = kMaxN / 16;         // rows per thread and stage
   const ExpertParams& e = p.e;
   const int tid = threadIdx.x - (kTcThreads - 32 * kGatherWarps);
   const int piece = tid & 7, row0 = tid >> 3;  // 16 rows of 8 pieces a sweep
   const unsigned char* x = static_cast<const unsigned char*>(e.x);
   const int64_t stride = e.x_stride * kSize;
   Place at;
-  Walk<kOp, 1> walk;
+  Walk<kExpertForward, 1> walk;
   OutTile t;
   bool alive = true;
   while (alive && walk.next(p, sh, t)) {
     if (t.depth == 0) continue;
-    const int share = padded<1>(t.rows);
-    const int first_row = kOp == kExpertDw ? t.from : t.row;
-    // rows per thread and stage
-    constexpr int kRows = kOp == kExpertForward ? kMaxN / 16 : 4;
-    const int32_t end = kOp == kExpertDw ? t.from + t.depth : t.row + t.rows;
+    const int rows = padded<1>(t.rows);
     int32_t token[kRows];
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
-      token[i] = token_row(e, first_row + row0 + 16 * i, end);
+    for (int i = 0; i < kRows; ++i) token[i] = token_row(e, t.row + row0 + 16 * i, t.row + t.rows);
     for (int c = 0; c < t.depth; c += kDepth) {
-      const int stage = at.stage;
-      alive = wait(p, sh, &sh.empty[stage], at.parity ^ 1);
+      alive = wait(p, sh, &sh.empty[at.stage], at.parity ^ 1);
       if (!alive) break;
-      const uint32_t to = ring + stage * p.stage_bytes + (kOp == kExpertForward ? p.a_bytes : 0);
-      if (kOp == kExpertForward) {
-        // bytes of the row from this piece on
-        const int64_t have = (static_cast<int64_t>(t.depth) - c) * kSize - piece * 16;
-        const int bytes = have <= 0 ? 0 : have < 16 ? static_cast<int>(have) : 16;
+      const uint32_t to = ring + at.stage * p.stage_bytes + p.a_bytes;
+      // bytes of the row from this piece on
+      const int64_t have = (static_cast<int64_t>(t.depth) - c) * kSize - piece * 16;
+      const int bytes = have <= 0 ? 0 : have < 16 ? static_cast<int>(have) : 16;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const int row = row0 + 16 * i;
-          if (row >= share) break;
-          const bool some = token[i] >= 0 && bytes > 0;
-          copy16(to + row * kRowBytes + ((piece ^ (row & 7)) << 4),
-                 some ? x + token[i] * stride + static_cast<int64_t>(c) * kSize + piece * 16 : x,
-                 some ? bytes : 0);
-        }
-      } else {
-#pragma unroll
-        for (int column = 0; column < 2; ++column) {
-          const int64_t first = t.feature + column * 64 + piece * 8;
-          const int64_t have = (e.k - first) * 2;
-          const int bytes = have <= 0 ? 0 : have < 16 ? static_cast<int>(have) : 16;
-#pragma unroll
-          for (int i = 0; i < kRows; ++i) {
-            const int row = row0 + 16 * i;
-            const bool some = token[i] >= 0 && bytes > 0;
-            copy16(to + column * 64 * kRowBytes + row * kRowBytes + ((piece ^ (row & 7)) << 4),
-                   some ? x + token[i] * stride + first * 2 : x, some ? bytes : 0);
-          }
-        }
-        if (c + kDepth < t.depth)
-#pragma unroll
-          for (int i = 0; i < kRows; ++i)
-            token[i] = token_row(e, t.from + c + kDepth + row0 + 16 * i, end);
+      for (int i = 0; i < kRows; ++i) {
+        const int row = row0 + 16 * i;
+        if (row >= rows) break;
+        const bool some = token[i] >= 0 && bytes > 0;
+        copy16(to + row * kRowBytes + ((piece ^ (row & 7)) << 4),
+               some ? x + token[i] * stride + static_cast<int64_t>(c) * kSize + piece * 16 : x,
+               some ? bytes : 0);
       }
-      copy_arrive(&sh.full[stage]);
+      copy_arrive(&sh.full[at.stage]);
       at.advance(p.stages);
     }
   }
@@ -532,20 +504,8 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
 // ------------------------------------------------------------------------
 // Warp 1: products.
 
-// Zeroes what a stage holds behind the group's last row, up to the next whole
-// step: rows of the next group, or stale ones.  Both operands, since 0 times
-// an infinity there would be a NaN.
-__device__ __forceinline__ void clear_tail(unsigned char* stage, int columns, int have, int to) {
-  const int words = (to - have) * (kRowBytes / 16);
-  for (int i = threadIdx.x & 31; i < columns * words; i += 32) {
-    const int column = i / words, at = i % words;
-    *reinterpret_cast<uint4*>(stage + column * 64 * kRowBytes + have * kRowBytes + at * 16) =
-        make_uint4(0, 0, 0, 0);
-  }
-}
-
 template <int kOp, bool kGated, bool kE4m3, int kPair>
-__device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned char* ring_ptr) {
+__device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring) {
   constexpr int kDepth = kE4m3 ? 128 : 64;
   constexpr int kSteps = 4;                // instructions a stage
   constexpr int kStep = kDepth / kSteps;   // contraction per instruction
@@ -554,9 +514,8 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned 
   // an operand's next step: 32 bytes along its rows, or 16 rows
   constexpr int kStepA = (kARows ? kStep * kRowBytes : 32) >> 4;
   constexpr int kStepB = (kBRows ? kStep * kRowBytes : 32) >> 4;
-  const bool one = one_lane();
-  if (kOp != kExpertDw && !one) return;    // dw: the whole warp clears tails
-  const bool gather = kPair == 1 && kOp != kExpertDx && p.e.row_tokens != nullptr;
+  if (!one_lane()) return;
+  const bool gather = kOp == kExpertForward && kPair == 1 && p.e.row_tokens != nullptr;
   const uint64_t a0 = operand(ring, 8 * kRowBytes, kARows ? 64 * kRowBytes : 0);
   const uint64_t b0 = operand(ring + p.a_bytes, 8 * kRowBytes, kBRows ? 64 * kRowBytes : 0);
   const uint32_t tmem = sh.tmem;
@@ -576,45 +535,41 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring, unsigned 
     for (int c = 0; c < t.depth; c += kDepth) {
       const int stage = at.stage;
       if (!wait(p, sh, &sh.full[stage], at.parity)) return;
-      int steps = kSteps;
-      if (kOp == kExpertDw && t.depth - c < kDepth) {
-        const int have = t.depth - c;
-        steps = (have + kStep - 1) / kStep;
-        clear_tail(ring_ptr + stage * p.stage_bytes,
-                   p.a_bytes / (64 * kRowBytes) + (n / kPair + 63) / 64, have, steps * kStep);
-        fence_proxy_async_smem();
-        __syncwarp();
-      } else if (gather) {
-        // gathered rows came by ordinary copies: order them before the
-        // tensor core's reads
-        fence_proxy_async_smem();
-      }
+      // gathered rows came by ordinary copies: order them before the tensor
+      // core's reads
+      if (gather) fence_proxy_async_smem();
       tc_fence_after();
-      if (one) {
-        const uint32_t offset = static_cast<uint32_t>(stage * p.stage_bytes) >> 4;
-        const uint64_t a = a0 + offset, b = b0 + offset;
+      const uint32_t offset = static_cast<uint32_t>(stage * p.stage_bytes) >> 4;
+      const uint64_t a = a0 + offset, b = b0 + offset;
 #pragma unroll
-        for (int s = 0; s < kSteps; ++s) {
-          if (kOp == kExpertDw && s >= steps) break;
-          mma<kE4m3, kPair>(d, a + s * kStepA, b + s * kStepB, idesc, accumulate);
-          if (kFused)
-            mma<kE4m3, kPair>(d + kMaxN / 2, a + (kTileM * kRowBytes >> 4) + s * kStepA,
-                              b + s * kStepB, idesc, accumulate);
-          accumulate = 1;
-        }
-        mma_commit<kPair>(&sh.empty[stage]);
+      for (int s = 0; s < kSteps; ++s) {
+        if (kOp == kExpertDw && c + s * kStep >= t.depth) break;
+        mma<kE4m3, kPair>(d, a + s * kStepA, b + s * kStepB, idesc, accumulate);
+        if (kFused)
+          mma<kE4m3, kPair>(d + kMaxN / 2, a + (kTileM * kRowBytes >> 4) + s * kStepA,
+                            b + s * kStepB, idesc, accumulate);
+        accumulate = 1;
       }
+      mma_commit<kPair>(&sh.empty[stage]);
       at.advance(p.stages);
     }
-    if (one) mma_commit<kPair>(&sh.acc_full[buffer]);
+    mma_commit<kPair>(&sh.acc_full[buffer]);
     ++tiles;
   }
 }
 
-// Warp 1 of a pair's second block: its part of a group's last stage of dw.  A
-// stage has a barrier of its own for this (several groups' last stages can be
-// under way), used again only when the products have read the stage.
+// ------------------------------------------------------------------------
+// Warp 10, dw: zeroes what a group's last stage holds behind the group's last
+// row, up to the next whole step: rows of the next group, or stale ones.  Both
+// operands, since 0 times an infinity there would be a NaN.  The stage lands
+// long before its products are due, so that they do not wait for this (420 us
+// for the gradient of 2 x 1024 x 2048 weights from 64225 rows when the issuing
+// lane's warp did it).  A stage has a barrier of its own for it, since several
+// groups' last stages can be under way; it is used again only when the
+// products have read the stage.
+
 __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_ptr) {
+  const int lane = threadIdx.x & 31;
   int used = 0;
   uint32_t parity = 0;  // of each stage's barrier
   Walk<kExpertDw, 2> walk;
@@ -627,13 +582,19 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
     const int stage = (used - 1) % p.stages;
     if (!wait(p, sh, &sh.tail[stage], parity >> stage & 1)) return;
     parity ^= 1u << stage;
-    clear_tail(ring_ptr + stage * p.stage_bytes,
-               p.a_bytes / (64 * kRowBytes) + (padded<2>(t.rows) / 2 + 63) / 64, have,
-               (have + 15) & ~15);
+    unsigned char* base = ring_ptr + stage * p.stage_bytes;
+    const int columns =
+        p.a_bytes / (64 * kRowBytes) + (padded<2>(t.rows) / 2 + 63) / 64;
+    const int words = (((have + 15) & ~15) - have) * (kRowBytes / 16);
+    for (int column = 0; column < columns; ++column)
+      for (int i = lane; i < words; i += 32)
+        *reinterpret_cast<uint4*>(base + column * 64 * kRowBytes + have * kRowBytes + i * 16) =
+            make_uint4(0, 0, 0, 0);
     fence_proxy_async_smem();
+    // the other block's tensor core reads this block's operands on the first's order
     asm volatile("fence.acq_rel.cluster;" ::: "memory");
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) mbar_arrive_first(&sh.full[stage]);
+    if (lane == 0) mbar_arrive_first(&sh.full[stage]);
   }
 }
 
@@ -814,11 +775,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t ring = (base + 1023) & ~1023u;
   unsigned char* ring_ptr = raw + (ring - base);
   const int warp = threadIdx.x >> 5;
-  const bool gather = kPair == 1 && kOp != kExpertDx && p.e.row_tokens != nullptr;
+  const bool gather = kOp == kExpertForward && kPair == 1 && p.e.row_tokens != nullptr;
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
       mbar_init(&sh.full[i], gather ? 1 + 32 * kGatherWarps
-                             : kPair == 2 && kOp == kExpertDw ? 2 : 1);
+                             : kOp == kExpertDw ? 2 : 1);
       mbar_init(&sh.empty[i], 1);
       mbar_init(&sh.tail[i], 1);
     }
@@ -853,13 +814,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 0)
     load_tiles<kOp, kGated, kE4m3, kPair>(p, &map_a, &map_b, sh, ring);
   else if (warp == 1 && (kPair == 1 || cluster_rank() == 0))
-    multiply<kOp, kGated, kE4m3, kPair>(p, sh, ring, ring_ptr);
-  else if (warp == 1 && kOp == kExpertDw)
-    clear_tails(p, sh, ring_ptr);
+    multiply<kOp, kGated, kE4m3, kPair>(p, sh, ring);
   else if (warp >= 2 && warp < 2 + kStoreWarps)
     store_tiles<kOp, kGated, kE4m3, kPair>(p, sh);
+  else if (warp == 2 + kStoreWarps && kOp == kExpertDw)
+    clear_tails(p, sh, ring_ptr);
   else if (warp >= 2 + kStoreWarps && gather)
-    gather_tiles<kOp, kE4m3>(p, sh, ring);
+    gather_tiles<kE4m3>(p, sh, ring);
   tc_fence_before();
   __syncthreads();
   sync_all<kPair>();
@@ -942,7 +903,7 @@ int launch_at(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int
 template <int kPair>
 int launch_with(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid,
                 cudaStream_t s) {
-  const ExpertParams& e = p.e;
+  const ExpertParams& e = p.e;  // dw always takes pairs
   if (e.op == kExpertForward) {
     if (e.e4m3)
       return e.gated ? launch_at<kExpertForward, true, true, kPair>(p, a, b, grid, s)
@@ -953,7 +914,7 @@ int launch_with(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, i
   if (e.op == kExpertDx)
     return e.gated ? launch_at<kExpertDx, true, false, kPair>(p, a, b, grid, s)
                    : launch_at<kExpertDx, false, false, kPair>(p, a, b, grid, s);
-  return launch_at<kExpertDw, false, false, kPair>(p, a, b, grid, s);
+  return launch_at<kExpertDw, false, false, 2>(p, a, b, grid, s);
 }
 
 int sm_count() {
@@ -974,13 +935,13 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   const bool fused = e.op == kExpertForward && e.gated;
   const int64_t features = e.op == kExpertForward ? e.n : e.k;
   const int64_t depth = e.op == kExpertForward ? e.k : e.n;
+  const bool small = e.op != kExpertDw && e.rows <= 32 * static_cast<int64_t>(e.experts);
   if (e.experts < 1 || e.rows < 1 || features < 1 || depth < 1 || e.x_rows < 1) return false;
   TcParams p{};
   p.e = e;
   // Rows of a tile.  With few rows per expert on average the weights' bytes
   // bound the call: small row tiles leave room for more stages in flight.
-  const bool small = e.op != kExpertDw && e.rows <= 32 * static_cast<int64_t>(e.experts);
-  p.tile_n = small ? 64 : fused ? kMaxN / 2 : kMaxN;
+  p.tile_n = small ? kMaxSmallN : fused ? kMaxN / 2 : kMaxN;
   p.a_bytes = (fused ? 2 : 1) * kTileM * kRowBytes;
   const int pair = small || e.row_tokens ? 1 : 2;
   p.stage_bytes = p.a_bytes + p.tile_n / pair * kRowBytes;

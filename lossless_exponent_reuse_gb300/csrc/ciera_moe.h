@@ -81,6 +81,19 @@ struct RouteBackwardParams {
   void* dlogits;
 };
 
+struct GatherParams {
+  const void* x;
+  int64_t x_stride;
+  int64_t x_rows;
+  int32_t size;              // bytes of an element
+  const float* x_scale;      // e4m3
+  const int32_t* row_tokens;
+  int64_t rows;
+  int64_t dim;
+  void* y;
+  float* y_scale;
+};
+
 struct CombineParams {
   const uint16_t* rows;
   int64_t stride;
@@ -112,7 +125,7 @@ struct ExpertParams {
   const void* x;             // forward: rows; dx: dy; dw: x
   int64_t x_stride;
   int64_t x_rows;
-  const int32_t* row_tokens; // may be null
+  const int32_t* row_tokens; // forward: may be null
   const void* w;             // forward, dx: weights; dw: dy
   int64_t w_stride;
   int64_t w_expert_stride;   // forward, dx
@@ -137,6 +150,7 @@ int launch_rmsnorm(const NormParams& p, void* stream);
 int launch_rmsnorm_backward(const NormBackwardParams& p, int blocks, void* stream);
 int launch_route(const RouteParams& p, void* stream);
 int launch_route_backward(const RouteBackwardParams& p, void* stream);
+int launch_gather(const GatherParams& p, void* stream);
 int launch_combine(const CombineParams& p, void* stream);
 int launch_combine_backward(const CombineParams& p, void* stream);
 int launch_expert(const ExpertParams& p, void* stream);

@@ -211,6 +211,33 @@ int ciera_route_backward(const float* dweights_dev, const float* weights_dev,
   return status_of(launch_route_backward(p, stream));
 }
 
+int ciera_gather_rows(const void* x_dev, int64_t x_stride, int64_t x_rows, int type,
+                      const float* x_scale_dev, const int32_t* row_tokens_dev, int64_t rows,
+                      int64_t dim, void* y_dev, float* y_scale_dev, void* stream) {
+  const bool e4m3 = type == CIERA_E4M3;
+  if (!e4m3 && type != CIERA_BF16) return CIERA_E_INVAL;
+  const uintptr_t size = e4m3 ? 1 : 2;
+  if (!matrix(x_dev, x_rows, dim, x_stride, size) || rows < 0 || rows > kMaxRows ||
+      !buffer(row_tokens_dev, rows, 4) || !buffer(y_dev, rows * dim, size))
+    return CIERA_E_INVAL;
+  if (e4m3 ? !buffer(x_scale_dev, x_rows, 4) || !buffer(y_scale_dev, rows, 4)
+           : x_scale_dev || y_scale_dev)
+    return CIERA_E_INVAL;
+  if (rows == 0 || dim == 0) return CIERA_OK;
+  GatherParams p{};
+  p.x = x_dev;
+  p.x_stride = x_stride;
+  p.x_rows = x_rows;
+  p.size = static_cast<int32_t>(size);
+  p.x_scale = x_scale_dev;
+  p.row_tokens = row_tokens_dev;
+  p.rows = rows;
+  p.dim = dim;
+  p.y = y_dev;
+  p.y_scale = y_scale_dev;
+  return status_of(launch_gather(p, stream));
+}
+
 int ciera_combine(const uint16_t* rows_dev, int64_t rows_stride, int64_t rows,
                   const int32_t* slots_dev, const float* weights_dev, int64_t tokens, int topk,
                   int64_t dim, uint16_t* y_dev, void* stream) {
@@ -363,16 +390,15 @@ int ciera_expert_mm_dx(const uint16_t* dy_dev, int64_t dy_stride, const uint16_t
 }
 
 int ciera_expert_mm_dw(const uint16_t* dy_dev, int64_t dy_stride, const uint16_t* x_dev,
-                       int64_t x_stride, int64_t x_rows, const int32_t* row_tokens_dev,
-                       const int32_t* offsets_dev, int64_t rows, int64_t experts, int64_t n,
-                       int64_t k, void* dw_dev, int64_t dw_stride, int64_t dw_expert_stride,
-                       int dw_type, uint32_t flags, void* workspace_dev, void* stream) {
+                       int64_t x_stride, const int32_t* offsets_dev, int64_t rows,
+                       int64_t experts, int64_t n, int64_t k, void* dw_dev, int64_t dw_stride,
+                       int64_t dw_expert_stride, int dw_type, uint32_t flags,
+                       void* workspace_dev, void* stream) {
   const bool f32 = dw_type == CIERA_F32;
   if ((!f32 && dw_type != CIERA_BF16) || (flags & ~CIERA_ACCUMULATE)) return CIERA_E_INVAL;
-  if (!grouped(rows, experts, n, k, offsets_dev, row_tokens_dev, workspace_dev))
+  if (!grouped(rows, experts, n, k, offsets_dev, nullptr, workspace_dev))
     return CIERA_E_INVAL;
-  if (!matrix(dy_dev, rows, n, dy_stride, 2) || !matrix(x_dev, x_rows, k, x_stride, 2) ||
-      (!row_tokens_dev && x_rows < rows) ||
+  if (!matrix(dy_dev, rows, n, dy_stride, 2) || !matrix(x_dev, rows, k, x_stride, 2) ||
       !stacked(dw_dev, experts, n, k, dw_stride, dw_expert_stride, f32 ? 4 : 2) ||
       (experts > 1 && dw_expert_stride < k))
     return CIERA_E_INVAL;
@@ -383,8 +409,7 @@ int ciera_expert_mm_dw(const uint16_t* dy_dev, int64_t dy_stride, const uint16_t
   p.accumulate = (flags & CIERA_ACCUMULATE) != 0;
   p.x = x_dev;
   p.x_stride = x_stride;
-  p.x_rows = x_rows;
-  p.row_tokens = row_tokens_dev;
+  p.x_rows = rows;
   p.w = dy_dev;
   p.w_stride = dy_stride;
   p.offsets = offsets_dev;

@@ -330,6 +330,37 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteBackwardParam
 }
 
 // ------------------------------------------------------------------------
+// Gather: a warp per row.  V bytes per access: 16 where rows and bases are
+// 16-byte aligned, else the element's size.
+
+template <typename V>
+__global__ void __launch_bounds__(kRowThreads) k_gather(const GatherParams p) {
+  const int lane = threadIdx.x & 31;
+  const int64_t r = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
+  if (r >= p.rows) return;
+  int64_t t = p.row_tokens[r];
+  if (t >= p.x_rows) t = -1;
+  const int64_t n = p.dim * p.size / static_cast<int64_t>(sizeof(V));
+  V* y = static_cast<V*>(p.y) + r * n;
+  if (t >= 0) {
+    const V* x = reinterpret_cast<const V*>(static_cast<const unsigned char*>(p.x) +
+                                            t * p.x_stride * p.size);
+    int64_t i = lane;
+    for (; i + 3 * 32 < n; i += 4 * 32) {
+      const V a = x[i], b = x[i + 32], c = x[i + 64], d = x[i + 96];
+      y[i] = a;
+      y[i + 32] = b;
+      y[i + 64] = c;
+      y[i + 96] = d;
+    }
+    for (; i < n; i += 32) y[i] = x[i];
+  } else {
+    for (int64_t i = lane; i < n; i += 32) y[i] = V{};
+  }
+  if (p.x_scale && lane == 0) p.y_scale[r] = t >= 0 ? p.x_scale[t] : 0.0f;
+}
+
+// ------------------------------------------------------------------------
 // Combine: a block per token.
 
 __device__ __forceinline__ int64_t slot_of(const CombineParams& p, int64_t pair) {
@@ -432,6 +463,19 @@ int launch_route_backward(const RouteBackwardParams& p, void* stream) {
     route_backward_at<8>(p, blocks, s);
   else
     route_backward_at<32>(p, blocks, s);
+  return cudaGetLastError();
+}
+
+int launch_gather(const GatherParams& p, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int blocks = static_cast<int>((p.rows + kRowThreads / 32 - 1) / (kRowThreads / 32));
+  const uintptr_t at = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.y);
+  if (at % 16 == 0 && p.dim * p.size % 16 == 0 && p.x_stride * p.size % 16 == 0)
+    k_gather<uint4><<<blocks, kRowThreads, 0, s>>>(p);
+  else if (p.size == 2)
+    k_gather<uint16_t><<<blocks, kRowThreads, 0, s>>>(p);
+  else
+    k_gather<uint8_t><<<blocks, kRowThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

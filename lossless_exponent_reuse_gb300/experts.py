@@ -8,7 +8,7 @@ fallback.
 
     norm       rmsnorm, rmsnorm_backward, quantize_rows
     route      route, route_backward
-    combine    combine, combine_backward
+    combine    gather_rows, combine, combine_backward
     products   mm, mm_gated, mm_dx, mm_dw
 
 The products take the experts' weights as strided views: ``bucket_views``
@@ -78,6 +78,9 @@ def bucket_views(bucket: torch.Tensor, experts: int, dim: int, ff: int,
 
 _workspaces = {}
 _CONTROL_BYTES = 256
+# Rows per expert above which a product's rows are gathered before it, by a
+# launch of its own, instead of inside it (see ciera_expert_mm's row_tokens).
+_GATHER_ROWS = 32
 
 
 def _on_stream(fn):
@@ -373,6 +376,31 @@ def _rows_of(x: torch.Tensor, tokens: Optional[torch.Tensor]) -> int:
     return tokens.numel()
 
 
+def _gather(x, tokens, x_scale, device):
+    rows, dim = tokens.numel(), x.shape[1]
+    y = torch.empty((rows, dim), dtype=x.dtype, device=device)
+    scale = None if x_scale is None else torch.empty(rows, dtype=_F32, device=device)
+    _call("ciera_gather_rows", device, _ptr(x), _stride(x), x.shape[0],
+          E4M3 if x.dtype == _E4M3 else BF16, _ptr(x_scale), _ptr(tokens), rows, dim, _ptr(y),
+          _ptr(scale), _current(device))
+    return y, scale
+
+
+@_on_stream
+def gather_rows(x: torch.Tensor, tokens: torch.Tensor, x_scale: Optional[torch.Tensor] = None):
+    """ciera_gather_rows: x[tokens] in expert order (bf16, or e4m3 with
+    ``x_scale``: then (rows, scales)), zeros where tokens is -1.  A training
+    step that needs the rows twice (``mm_gated``, then ``mm_dw``) gathers them
+    once."""
+    e4m3 = x_scale is not None
+    _matrix(x, "x", _E4M3 if e4m3 else _BF16)
+    _rows_of(x, tokens)
+    if e4m3:
+        _array(x_scale, "x_scale", _F32, (x.shape[0],))
+    y, scale = _gather(x, tokens, x_scale, _same_device(x, tokens, x_scale))
+    return (y, scale) if e4m3 else y
+
+
 def _forward(x, w, offsets, tokens, x_scale, w_scale, gated, keep):
     e4m3 = isinstance(x, torch.Tensor) and x.dtype == _E4M3
     dtype = _E4M3 if e4m3 else _BF16
@@ -393,6 +421,9 @@ def _forward(x, w, offsets, tokens, x_scale, w_scale, gated, keep):
     n = features // 2 if gated else features
     device = _same_device(x, w, offsets, tokens, x_scale, w_scale)
     s = _current(device)
+    if tokens is not None and rows > _GATHER_ROWS * experts:
+        x, x_scale = _gather(x, tokens, x_scale, device)
+        tokens = None
     y = torch.empty((rows, n), dtype=_BF16, device=device)
     pre = torch.empty((rows, features), dtype=_BF16, device=device) if keep else None
     _call("ciera_expert_mm", device, _ptr(x), _stride(x), x.shape[0], _ptr(tokens), _ptr(w),
@@ -472,8 +503,9 @@ def mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
         raise ValueError("out's experts overlap")
     device = _same_device(dy, x, offsets, tokens, out)
     s = _current(device)
-    _call("ciera_expert_mm_dw", device, _ptr(dy), _stride(dy), _ptr(x), _stride(x), x.shape[0],
-          _ptr(tokens), _ptr(offsets), rows, experts, n, k, _ptr(out), _stride(out),
-          out.stride(0) if experts > 1 else n * k, F32 if out.dtype == _F32 else BF16,
+    if tokens is not None:
+        x, _ = _gather(x, tokens, None, device)
+    _call("ciera_expert_mm_dw", device, _ptr(dy), _stride(dy), _ptr(x), _stride(x),
+          _ptr(offsets), rows, experts, n, k, _ptr(out), _stride(out), out.stride(0) if experts > 1 else n * k, F32 if out.dtype == _F32 else BF16,
           ACCUMULATE if accumulate else 0, _ptr(workspace(device, s)), s)
     return out

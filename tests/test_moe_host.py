@@ -139,17 +139,28 @@ def test_expert_mm_dx_refuses(bad):
 
 
 @pytest.mark.parametrize("bad", [
-    dict(dy=None), dict(ds=3), dict(x=None), dict(xs=3), dict(x_rows=99), dict(offsets=None),
+    dict(dy=None), dict(ds=3), dict(x=None), dict(xs=3), dict(offsets=None),
     dict(E=2000), dict(dw=None), dict(dws=3), dict(es=3), dict(kind=experts.E4M3),
     dict(kind=experts.F32, dw=4098), dict(flags=1), dict(work=None)])
 def test_expert_mm_dw_refuses(bad):
-    a = dict(dy=FAKE, ds=32, x=FAKE, xs=64, x_rows=100, tokens=None, offsets=FAKE, rows=100, E=4,
-             n=32, k=64, dw=FAKE, dws=64, es=64 * 32, kind=experts.BF16, flags=0, work=FAKE)
+    a = dict(dy=FAKE, ds=32, x=FAKE, xs=64, offsets=FAKE, rows=100, E=4, n=32, k=64, dw=FAKE, dws=64, es=64 * 32, kind=experts.BF16, flags=0, work=FAKE)
     a.update(bad)
     assert ciera.lib().ciera_expert_mm_dw(
-        vp(a["dy"]), a["ds"], vp(a["x"]), a["xs"], a["x_rows"], vp(a["tokens"]),
-        vp(a["offsets"]), a["rows"], a["E"], a["n"], a["k"], vp(a["dw"]), a["dws"], a["es"],
+        vp(a["dy"]), a["ds"], vp(a["x"]), a["xs"], vp(a["offsets"]), a["rows"], a["E"], a["n"], a["k"], vp(a["dw"]), a["dws"], a["es"],
         a["kind"], a["flags"], vp(a["work"]), None) == ciera.E_INVAL
+
+
+@pytest.mark.parametrize("bad", [
+    dict(x=None), dict(x=ODD), dict(xs=7), dict(kind=experts.F32), dict(scale=FAKE),
+    dict(yscale=FAKE), dict(kind=experts.E4M3), dict(kind=experts.E4M3, scale=FAKE),
+    dict(tokens=None), dict(tokens=4098), dict(rows=-1), dict(y=None), dict(y=ODD)])
+def test_gather_rows_refuses(bad):
+    a = dict(x=FAKE, xs=8, kind=experts.BF16, scale=None, tokens=FAKE, rows=4, y=FAKE,
+             yscale=None)
+    a.update(bad)
+    assert ciera.lib().ciera_gather_rows(vp(a["x"]), a["xs"], 3, a["kind"], vp(a["scale"]),
+                                         vp(a["tokens"]), a["rows"], 8, vp(a["y"]),
+                                         vp(a["yscale"]), None) == ciera.E_INVAL
 
 
 def test_calls_without_rows_need_no_device():

@@ -330,6 +330,24 @@ def test_combine_and_its_gradient(T, k, dim, E, kind):
                rounded=ref.U_F32)
 
 
+@pytest.mark.parametrize("kind", ["plain", "wide", "odd"])
+@pytest.mark.parametrize("T,R,dim", [(1, 8, 2048), (40, 0, 16), (40, 333, 1001), (7, 100, 136),
+                                     (5, 9, 1)])
+def test_gather_rows(T, R, dim, kind):
+    x = rand(T, dim, seed=29)
+    tokens = torch.randint(-1, T + 1, (R,), generator=torch.Generator().manual_seed(R),
+                           dtype=torch.int32).cuda()
+    some = (tokens >= 0) & (tokens < T)
+    at = tokens.long().clamp(0, T - 1)
+    want = torch.where(some[:, None], x[at], 0.0)
+    assert torch.equal(experts.gather_rows(strided(x, kind), tokens), want)
+    x8, scale = experts.quantize_rows(x)
+    y8, y_scale = experts.gather_rows(x8, tokens, x_scale=scale)
+    assert torch.equal(y8.view(torch.uint8), torch.where(some[:, None], x8.view(torch.uint8)[at],
+                                                         0).to(torch.uint8))
+    assert torch.equal(y_scale, torch.where(some, scale[at], 0.0))
+
+
 def test_combine_takes_indexes_outside_for_none():
     rows = rand(6, 16, seed=26)
     slots = torch.tensor([[0, 6], [-5, 2 ** 30], [5, -1]], dtype=torch.int32, device="cuda")
