@@ -640,6 +640,7 @@ __device__ __forceinline__ float row_scale(const ExpertParams& e, int64_t r) {
 template <int kOp, bool kGated, bool kE4m3, int kPair>
 __device__ void store_tiles(const TcParams& p, Shared& sh) {
   constexpr bool kFused = kOp == kExpertForward && kGated;
+  constexpr bool kReadsPre = kOp == kExpertDx && kGated;
   const ExpertParams& e = p.e;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quadrant = warp & 3;
   const int half = (warp - 2) >> 2;
@@ -654,35 +655,44 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
     const int64_t f_in = mine ? f : features - 1;  // for loads
     const int buffer = tiles & 1;
     const bool zero = t.depth == 0;
-    float scale = 1.0f, scale_up = 1.0f;
-    if (kE4m3 && !zero) {
-      const float* ws = e.w_scale + static_cast<int64_t>(t.group) * (kFused ? 2 : 1) * e.n;
-      scale = ws[f_in];
-      if (kFused) scale_up = ws[f_in + e.n];
-    }
+    // What the outputs need besides the products is fetched before them: e4m3's
+    // scales (lane i of row[q]: row 16 (2 q + half + 2 (i / 16)) + i % 16 of the
+    // tile, that is this warp's chunks 2 q and 2 q + 1), and the first chunk
+    // of the gated unit's inputs; each further chunk one chunk ahead.
+    float scale = 1.0f, scale_up = 1.0f, row[kMaxN / 64];
+    uint16_t gate_in[kChunk], up_in[kChunk];
+    const auto fetch_pre = [&](int c) {
+      const uint16_t* pre = e.pre_in + (static_cast<int64_t>(t.row) + c) * 2 * e.k + f_in;
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) {
+        const int64_t at = min(j, t.rows - c - 1) * 2 * e.k;
+        gate_in[j] = pre[at];
+        up_in[j] = pre[at + e.k];
+      }
+    };
     if (!zero) {
+      if (kE4m3) {
+        const float* ws = e.w_scale + static_cast<int64_t>(t.group) * (kFused ? 2 : 1) * e.n;
+        scale = ws[f_in];
+        if (kFused) scale_up = ws[f_in + e.n];
+#pragma unroll
+        for (int q = 0; q < kMaxN / 64; ++q) {
+          const int at = 64 * q + 32 * (lane >> 4) + 16 * half + (lane & 15);
+          row[q] = at < t.rows ? row_scale(e, static_cast<int64_t>(t.row) + at) : 0.0f;
+        }
+      }
+      if (kReadsPre && half * kChunk < t.rows) fetch_pre(half * kChunk);
       if (!wait(p, sh, &sh.acc_full[buffer], (tiles >> 1) & 1)) return;
       tc_fence_after();
       ++tiles;
     }
     const uint32_t acc =
         sh.tmem + buffer * kMaxN + (static_cast<uint32_t>(quadrant * 32) << 16);
+#pragma unroll 1
     for (int c = half * kChunk; c < t.rows; c += 2 * kChunk) {
       const int left = t.rows - c;
       const int64_t r = t.row + c;
       float v[kChunk], up[kChunk];
-      uint16_t gate_in[kChunk], up_in[kChunk];
-      float row = 0.0f;  // e4m3: lane j holds row j's scale
-      if (kOp == kExpertDx && kGated && !zero) {
-        const uint16_t* pre = e.pre_in + r * 2 * e.k + f_in;
-#pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-          const int64_t at = min(j, left - 1) * 2 * e.k;
-          gate_in[j] = pre[at];
-          up_in[j] = pre[at + e.k];
-        }
-      }
-      if (kE4m3 && !zero && lane < min(left, kChunk)) row = row_scale(e, r + lane);
       if (zero) {
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) v[j] = up[j] = 0.0f;
@@ -692,9 +702,13 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
         tmem_ld_wait();
       }
       if (kE4m3 && !zero) {
+        float mine_row = row[0];
+#pragma unroll
+        for (int q = 1; q < kMaxN / 64; ++q)
+          if (c >> 6 == q) mine_row = row[q];
 #pragma unroll
         for (int j = 0; j < kChunk; ++j) {
-          const float xs = __shfl_sync(0xffffffffu, row, j);
+          const float xs = __shfl_sync(0xffffffffu, mine_row, (c >> 1 & 16) + j);
           v[j] *= xs * scale;
           if (kFused) up[j] *= xs * scale_up;
         }
@@ -712,9 +726,16 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
         store_bf16(y + r * e.n + f, e.n, v, left, mine);
       } else if (kOp == kExpertDx && kGated) {
         if (!zero) {
+          float gate[kChunk];
 #pragma unroll
           for (int j = 0; j < kChunk; ++j) {
-            const float g = bf16_to_f32(gate_in[j]), u = bf16_to_f32(up_in[j]);
+            gate[j] = bf16_to_f32(gate_in[j]);
+            up[j] = bf16_to_f32(up_in[j]);
+          }
+          if (c + 2 * kChunk < t.rows) fetch_pre(c + 2 * kChunk);
+#pragma unroll
+          for (int j = 0; j < kChunk; ++j) {
+            const float g = gate[j], u = up[j];
             const float s = sigmoid(g);
             up[j] = v[j] * g * s;
             v[j] = v[j] * u * s * (1.0f + g * (1.0f - s));
