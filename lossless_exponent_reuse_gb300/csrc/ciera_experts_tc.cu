@@ -376,13 +376,14 @@ __device__ __forceinline__ float sigmoid(float a) {
 __device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
 
 // ------------------------------------------------------------------------
-// Warp 0: loads by TMA.  Gathered rows are left to the gathering warps.  The
-// bytes of both blocks of a pair are counted by the first one's barriers,
-// where the products are issued.
+// Warps 0 and 11: loads of A and of B by TMA (one warp for both takes nearly
+// as long to issue a stage's loads as the products take).  Gathered rows are
+// left to the gathering warps.  The bytes of both operands, and of both blocks
+// of a pair, are counted by the first block's barriers, where the products are
+// issued; the loader of A announces them.
 
-template <int kOp, bool kGated, bool kE4m3, int kPair>
-__device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CUtensorMap* map_b,
-                           Shared& sh, uint32_t ring) {
+template <int kOp, bool kGated, bool kE4m3, int kPair, bool kLoadsA>
+__device__ void load_tiles(const TcParams& p, const CUtensorMap* map, Shared& sh, uint32_t ring) {
   constexpr int kDepth = kE4m3 ? 128 : 64;  // contraction per stage
   constexpr bool kFused = kOp == kExpertForward && kGated;
   if (!one_lane()) return;
@@ -408,34 +409,35 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map_a, const CU
       // by who clears it
       const bool tail = kOp == kExpertDw && t.depth - c < kDepth;
       uint32_t bar = kPair == 2 ? in_first(full) : smem_addr(full);
-      if (tail) {
-        bar = smem_addr(&sh.tail[at.stage]);
-        mbar_arrive_expect_tx(&sh.tail[at.stage], bytes);
-      } else if (first) {
-        mbar_arrive_expect_tx(full, kPair * bytes);
-      } else if (kOp == kExpertDw) {
-        mbar_arrive_first(full);
-      }
-      if (kOp == kExpertForward) {
-        tma_3d<kPair>(a, map_a, c, t.feature, t.group, bar);
-        if (kFused)
-          tma_3d<kPair>(a + kTileM * kRowBytes, map_a, c, static_cast<int>(p.e.n) + t.feature,
-                        t.group, bar);
-      } else if (kOp == kExpertDx) {
-        tma_3d<kPair>(a, map_a, t.feature, c, t.group, bar);
-        tma_3d<kPair>(a + 64 * kRowBytes, map_a, t.feature + 64, c, t.group, bar);
+      if (tail) bar = smem_addr(&sh.tail[at.stage]);
+      if constexpr (kLoadsA) {
+        if (tail)
+          mbar_arrive_expect_tx(&sh.tail[at.stage], bytes);
+        else if (first)
+          mbar_arrive_expect_tx(full, kPair * bytes);
+        else if (kOp == kExpertDw)
+          mbar_arrive_first(full);
+        if (kOp == kExpertForward) {
+          tma_3d<kPair>(a, map, c, t.feature, t.group, bar);
+          if (kFused)
+            tma_3d<kPair>(a + kTileM * kRowBytes, map, c, static_cast<int>(p.e.n) + t.feature,
+                          t.group, bar);
+        } else if (kOp == kExpertDx) {
+          tma_3d<kPair>(a, map, t.feature, c, t.group, bar);
+          tma_3d<kPair>(a + 64 * kRowBytes, map, t.feature + 64, c, t.group, bar);
+        } else {
+          tma_2d<kPair>(a, map, t.feature, t.from + c, bar);
+          tma_2d<kPair>(a + 64 * kRowBytes, map, t.feature + 64, t.from + c, bar);
+        }
       } else {
-        tma_2d<kPair>(a, map_a, t.feature, t.from + c, bar);
-        tma_2d<kPair>(a + 64 * kRowBytes, map_a, t.feature + 64, t.from + c, bar);
-      }
-      if (!gather)
         for (int i = 0; i < boxes; ++i) {
           const uint32_t to = b + i * kBoxRows * kRowBytes;
           if (kOp == kExpertDw)
-            tma_2d<kPair>(to, map_b, row + i * kBoxRows, t.from + c, bar);
+            tma_2d<kPair>(to, map, row + i * kBoxRows, t.from + c, bar);
           else
-            tma_2d<kPair>(to, map_b, c, row + i * kBoxRows, bar);
+            tma_2d<kPair>(to, map, c, row + i * kBoxRows, bar);
         }
+      }
       at.advance(p.stages);
       ++issued;
     }
@@ -833,7 +835,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   sync_all<kPair>();
   tc_fence_after();
   if (warp == 0)
-    load_tiles<kOp, kGated, kE4m3, kPair>(p, &map_a, &map_b, sh, ring);
+    load_tiles<kOp, kGated, kE4m3, kPair, true>(p, &map_a, sh, ring);
   else if (warp == 1 && (kPair == 1 || cluster_rank() == 0))
     multiply<kOp, kGated, kE4m3, kPair>(p, sh, ring);
   else if (warp >= 2 && warp < 2 + kStoreWarps)
@@ -842,6 +844,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     clear_tails(p, sh, ring_ptr);
   else if (warp >= 2 + kStoreWarps && gather)
     gather_tiles<kE4m3>(p, sh, ring);
+  else if (warp == 3 + kStoreWarps)
+    load_tiles<kOp, kGated, kE4m3, kPair, false>(p, &map_b, sh, ring);
   tc_fence_before();
   __syncthreads();
   sync_all<kPair>();
