@@ -38,7 +38,7 @@ ROUTE_RENORMALIZE = 1
 GATED = 1
 ACCUMULATE = 2
 
-_BF16, _F32, _E4M3 = torch.bfloat16, torch.float32, torch.float8_e4m3fn
+_BF16, _F32, _E4M3, _I32 = torch.bfloat16, torch.float32, torch.float8_e4m3fn, torch.int32
 
 
 class Norm(NamedTuple):
@@ -78,6 +78,8 @@ def bucket_views(bucket: torch.Tensor, experts: int, dim: int, ff: int,
 
 _workspaces = {}
 _CONTROL_BYTES = 256
+_functions = {}
+_raw_stream = torch._C._cuda_getCurrentRawStream
 # Rows per expert above which a product's rows are gathered before it, by a
 # launch of its own, instead of inside it (see ciera_expert_mm's row_tokens).
 _GATHER_ROWS = 32
@@ -97,97 +99,114 @@ def _on_stream(fn):
     return call
 
 
-def _current(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def workspace(device, stream: int, tokens: int = 0, experts: int = 0, dim: int = 0):
-    """The workspace of a device and stream handle, for calls of these sizes."""
-    need = ciera.lib().ciera_moe_workspace_bytes(tokens, experts, dim)
-    if need == 0:
-        raise ValueError(f"no workspace for {tokens} tokens, {experts} experts, {dim} columns")
-    key = (device, stream)
-    ws = _workspaces.get(key)
+def workspace(index: int, stream: int, tokens: int = 0, experts: int = 0,
+              dim: int = 0) -> torch.Tensor:
+    """The workspace of a device index and stream handle, for calls of these sizes."""
+    ws = _workspaces.get((index, stream))
+    need = _CONTROL_BYTES
+    if tokens or ws is None:
+        need = ciera.lib().ciera_moe_workspace_bytes(tokens, experts, dim)
+        if need == 0:
+            raise ValueError(f"no workspace for {tokens} tokens, {experts} experts, {dim} columns")
     if ws is None or ws.numel() < need:
-        old, ws = ws, torch.zeros(need, dtype=torch.uint8, device=device)
+        old, ws = ws, torch.zeros(need, dtype=torch.uint8, device=f"cuda:{index}")
         if old is not None:  # a status not read yet
             ws[:_CONTROL_BYTES].copy_(old[:_CONTROL_BYTES])
-        _workspaces[key] = ws
+        _workspaces[index, stream] = ws
     return ws
 
 
 @_on_stream
 def status(device="cuda") -> int:
     """ciera_status of the stream's workspace: waits for the stream."""
-    device = torch.empty(0, device=device).device
-    s = _current(device)
-    ws = _workspaces.get((device, s))
+    index = torch.empty(0, device=device).get_device()
+    s = _raw_stream(index)
+    ws = _workspaces.get((index, s))
     return ciera.OK if ws is None else ciera.status(ws, stream=s)
 
 
-def _matrix(t: torch.Tensor, name: str, dtype, shape=None) -> torch.Tensor:
+# The checks below are on every call's path: one test where all is well, and
+# the words for what is wrong apart from it.
+
+def _index(t, name: str) -> int:
+    """Device index of the tensor that the others have to be with."""
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
+    return t.get_device()
+
+
+def _placed(t, name: str, dtype, index: int) -> None:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != index:
+        raise ValueError(f"{name} is on cuda:{t.get_device()}, other tensors on cuda:{index}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+
+
+def _matrix(t, name: str, dtype, index: int, rows: Optional[int] = None,
+            cols: Optional[int] = None) -> int:
+    """Row stride of a matrix with contiguous rows (of one row: any)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index:
+        shape = t.shape
+        if (len(shape) == 2 and (rows is None or shape[0] == rows)
+                and (cols is None or shape[1] == cols)):
+            stride, unit = t.stride()
+            if unit == 1 or shape[1] <= 1:
+                if shape[0] <= 1:
+                    return shape[1]
+                if stride >= shape[1]:
+                    return stride
+    _placed(t, name, dtype, index)
     if t.dim() != 2:
         raise ValueError(f"{name} must have two dimensions, got {t.dim()}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    if (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        want = ["any" if rows is None else rows, "any" if cols is None else cols]
+        raise ValueError(f"{name} must be {want}, got {list(t.shape)}")
     if t.shape[1] > 1 and t.stride(1) != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    if t.shape[0] > 1 and t.stride(0) < t.shape[1]:
-        raise ValueError(f"{name}'s rows overlap")
-    return t
+    raise ValueError(f"{name}'s rows overlap")
 
 
-def _stride(t: torch.Tensor) -> int:
-    """Row stride; that of a single row does not matter and may be anything."""
-    return t.stride(-2) if t.shape[-2] > 1 else t.shape[-1]
+def _array(t, name: str, dtype, index: int, *shape: int) -> int:
+    """Pointer of a contiguous tensor of this shape."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index
+            and t.shape == shape and t.is_contiguous()):
+        return t.data_ptr()
+    _placed(t, name, dtype, index)
+    raise ValueError(f"{name} must be contiguous and {list(shape)}, got {list(t.shape)}")
 
 
-def _array(t: torch.Tensor, name: str, dtype, shape) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {list(shape)}, got "
-                         f"{t.dtype} {list(t.shape)}")
-    return t
-
-
-def _stack(t: torch.Tensor, name: str, dtype) -> torch.Tensor:
-    """Experts' matrices [experts, rows, columns], contiguous rows."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+def _stack(t, name: str, dtype, index: int) -> Tuple[int, int]:
+    """Row and expert strides of [experts, rows, columns], contiguous rows."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index:
+        shape = t.shape
+        if len(shape) == 3:
+            expert, row, unit = t.stride()
+            if shape[1] <= 1:
+                row = shape[2]
+            if (unit == 1 or shape[2] <= 1) and row >= shape[2]:
+                return row, expert if shape[0] > 1 else shape[1] * row
+    _placed(t, name, dtype, index)
     if t.dim() != 3:
         raise ValueError(f"{name} must be [experts, rows, columns]")
     if t.shape[2] > 1 and t.stride(2) != 1:
         raise ValueError(f"{name}'s rows must be contiguous")
-    if t.shape[1] > 1 and t.stride(1) < t.shape[2]:
-        raise ValueError(f"{name}'s rows overlap")
-    return t
+    raise ValueError(f"{name}'s rows overlap")
 
 
-def _same_device(*tensors) -> torch.device:
-    device = tensors[0].device
-    for t in tensors[1:]:
-        if t is not None and t.device != device:
-            raise ValueError(f"tensors on {device} and {t.device}")
-    return device
+def _load(name: str):
+    fn = _functions[name] = getattr(ciera.lib(), name)
+    return fn
 
 
-def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
-    return None if t is None else t.data_ptr()
-
-
-def _call(name: str, device: torch.device, *args) -> None:
-    if device.index == torch.cuda.current_device():
-        st = getattr(ciera.lib(), name)(*args)
+def _call(name: str, index: int, *args) -> None:
+    fn = _functions.get(name) or _load(name)
+    if index == torch._C._cuda_getDevice():
+        st = fn(*args)
     else:
-        with torch.cuda.device(device):
-            st = getattr(ciera.lib(), name)(*args)
+        with torch.cuda.device(index):
+            st = fn(*args)
     if st != ciera.OK:
         raise ciera.CieraError(st, name)
 
@@ -199,44 +218,47 @@ def rmsnorm(x: torch.Tensor, weight: torch.Tensor, residual: Optional[torch.Tens
             eps: float = 1e-6, quantize: bool = False) -> Norm:
     """ciera_rmsnorm: the norm of x + residual (bf16 [rows, dim]), as bf16 or,
     with ``quantize``, as e4m3 with a scale per row."""
-    _matrix(x, "x", _BF16)
+    index = _index(x, "x")
+    x_stride = _matrix(x, "x", _BF16, index)
     rows, dim = x.shape
-    _array(weight, "weight", _BF16, (dim,))
-    if residual is not None:
-        _matrix(residual, "residual", _BF16, (rows, dim))
-    device = _same_device(x, weight, residual)
+    w = _array(weight, "weight", _BF16, index, dim)
+    device = x.device
     y = torch.empty((rows, dim), dtype=_E4M3 if quantize else _BF16, device=device)
-    scale = torch.empty(rows, dtype=_F32, device=device) if quantize else None
-    h = torch.empty((rows, dim), dtype=_BF16, device=device) if residual is not None else x
     rstd = torch.empty(rows, dtype=_F32, device=device)
-    _call("ciera_rmsnorm", device, _ptr(x), _stride(x), _ptr(residual),
-          0 if residual is None else _stride(residual), _ptr(weight), rows, dim, float(eps),
-          _ptr(y), E4M3 if quantize else BF16, _ptr(scale),
-          None if residual is None else _ptr(h), _ptr(rstd), _current(device))
+    scale = torch.empty(rows, dtype=_F32, device=device) if quantize else None
+    if residual is None:
+        h, res, res_stride, h_ptr = x, None, 0, None
+    else:
+        res_stride = _matrix(residual, "residual", _BF16, index, rows, dim)
+        h = torch.empty((rows, dim), dtype=_BF16, device=device)
+        res, h_ptr = residual.data_ptr(), h.data_ptr()
+    _call("ciera_rmsnorm", index, x.data_ptr(), x_stride, res, res_stride, w, rows, dim, eps,
+          y.data_ptr(), E4M3 if quantize else BF16, scale.data_ptr() if quantize else None,
+          h_ptr, rstd.data_ptr(), _raw_stream(index))
     return Norm(y, scale, h, rstd)
 
 
 @_on_stream
 def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
-                     weight: torch.Tensor, dh: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+                     weight: torch.Tensor,
+                     dh: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
     """ciera_rmsnorm_backward: (dx, dweight) with dx the gradient of x and of
     the residual alike; ``dh`` is the gradient that reaches h through the next
     residual."""
-    _matrix(dy, "dy", _BF16)
+    index = _index(dy, "dy")
+    dy_stride = _matrix(dy, "dy", _BF16, index)
     rows, dim = dy.shape
-    _matrix(h, "h", _BF16, (rows, dim))
-    _array(rstd, "rstd", _F32, (rows,))
-    _array(weight, "weight", _BF16, (dim,))
-    if dh is not None:
-        _matrix(dh, "dh", _BF16, (rows, dim))
-    device = _same_device(dy, h, rstd, weight, dh)
-    s = _current(device)
-    ws = workspace(device, s, tokens=rows, dim=dim)
-    dx = torch.empty((rows, dim), dtype=_BF16, device=device)
-    dweight = torch.empty(dim, dtype=_F32, device=device)
-    _call("ciera_rmsnorm_backward", device, _ptr(dy), _stride(dy), _ptr(h), _stride(h),
-          _ptr(rstd), _ptr(weight), _ptr(dh), 0 if dh is None else _stride(dh), rows, dim,
-          _ptr(dx), _ptr(dweight), _ptr(ws), ws.numel(), s)
+    h_stride = _matrix(h, "h", _BF16, index, rows, dim)
+    r = _array(rstd, "rstd", _F32, index, rows)
+    w = _array(weight, "weight", _BF16, index, dim)
+    dh_stride = 0 if dh is None else _matrix(dh, "dh", _BF16, index, rows, dim)
+    s = _raw_stream(index)
+    ws = workspace(index, s, tokens=rows, dim=dim)
+    dx = torch.empty((rows, dim), dtype=_BF16, device=dy.device)
+    dweight = torch.empty(dim, dtype=_F32, device=dy.device)
+    _call("ciera_rmsnorm_backward", index, dy.data_ptr(), dy_stride, h.data_ptr(), h_stride, r, w,
+          None if dh is None else dh.data_ptr(), dh_stride, rows, dim, dx.data_ptr(),
+          dweight.data_ptr(), ws.data_ptr(), ws.numel(), s)
     return dx, dweight
 
 
@@ -244,24 +266,24 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
 def quantize_rows(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """ciera_quantize_rows: (e4m3, scale per row) of bf16 [..., dim] whose
     leading dimensions, if several, are contiguous (weights, laid out once)."""
-    flat = x if isinstance(x, torch.Tensor) and x.dim() == 2 else x.reshape(-1, x.shape[-1])
-    _matrix(flat, "x", _BF16)
+    index = _index(x, "x")
+    shape = x.shape
+    flat = x if len(shape) == 2 else x.reshape(-1, shape[-1])
+    stride = _matrix(flat, "x", _BF16, index)
     rows, dim = flat.shape
-    device = flat.device
-    y = torch.empty(x.shape, dtype=_E4M3, device=device)
-    scale = torch.empty(x.shape[:-1], dtype=_F32, device=device)
-    _call("ciera_quantize_rows", device, _ptr(flat), _stride(flat), rows, dim, _ptr(y),
-          _ptr(scale), _current(device))
+    y = torch.empty(shape, dtype=_E4M3, device=x.device)
+    scale = torch.empty(shape[:-1], dtype=_F32, device=x.device)
+    _call("ciera_quantize_rows", index, flat.data_ptr(), stride, rows, dim, y.data_ptr(),
+          scale.data_ptr(), _raw_stream(index))
     return y, scale
 
 
 # ---- route ---------------------------------------------------------------
 
-def _logits(t: torch.Tensor) -> int:
+def _logits(t) -> int:
     if not isinstance(t, torch.Tensor) or t.dtype not in (_BF16, _F32):
         raise ValueError("logits must be float32 or bfloat16")
-    _matrix(t, "logits", t.dtype)
-    return F32 if t.dtype == _F32 else BF16
+    return F32 if t.dtype is _F32 else BF16
 
 
 @_on_stream
@@ -270,25 +292,29 @@ def route(logits: torch.Tensor, topk: int, renormalize: bool = False,
     """ciera_route: the topk experts of each token and the expert order;
     ``token_mask`` (bool or uint8 per token), where false, routes nowhere."""
     kind = _logits(logits)
+    index = _index(logits, "logits")
+    stride = _matrix(logits, "logits", logits.dtype, index)
     tokens, experts = logits.shape
-    if token_mask is not None:
-        if token_mask.dtype not in (torch.bool, torch.uint8):
-            raise ValueError("token_mask must be bool or uint8")
-        _array(token_mask, "token_mask", token_mask.dtype, (tokens,))
-    device = _same_device(logits, token_mask)
-    s = _current(device)
     topk = int(topk)
     if not 1 <= topk <= experts:
         raise ValueError(f"topk must be in 1..{experts}, got {topk}")
-    ws = workspace(device, s, tokens=tokens, experts=experts)
-    weights = torch.empty((tokens, topk), dtype=_F32, device=device)
-    chosen = torch.empty((tokens, topk), dtype=torch.int32, device=device)
-    slots = torch.empty((tokens, topk), dtype=torch.int32, device=device)
-    row_tokens = torch.empty(tokens * topk, dtype=torch.int32, device=device)
-    offsets = torch.empty(experts + 1, dtype=torch.int32, device=device)
-    _call("ciera_route", device, _ptr(logits), kind, _stride(logits), _ptr(token_mask), tokens,
-          experts, topk, ROUTE_RENORMALIZE if renormalize else 0, _ptr(weights), _ptr(chosen),
-          _ptr(slots), _ptr(row_tokens), _ptr(offsets), _ptr(ws), ws.numel(), s)
+    mask = None
+    if token_mask is not None:
+        if token_mask.dtype not in (torch.bool, torch.uint8):
+            raise ValueError("token_mask must be bool or uint8")
+        mask = _array(token_mask, "token_mask", token_mask.dtype, index, tokens)
+    s = _raw_stream(index)
+    ws = workspace(index, s, tokens=tokens, experts=experts)
+    device, pairs = logits.device, (tokens, topk)
+    weights = torch.empty(pairs, dtype=_F32, device=device)
+    chosen = torch.empty(pairs, dtype=_I32, device=device)
+    slots = torch.empty(pairs, dtype=_I32, device=device)
+    row_tokens = torch.empty(tokens * topk, dtype=_I32, device=device)
+    offsets = torch.empty(experts + 1, dtype=_I32, device=device)
+    _call("ciera_route", index, logits.data_ptr(), kind, stride, mask, tokens, experts, topk,
+          ROUTE_RENORMALIZE if renormalize else 0, weights.data_ptr(), chosen.data_ptr(),
+          slots.data_ptr(), row_tokens.data_ptr(), offsets.data_ptr(), ws.data_ptr(), ws.numel(),
+          s)
     return Routing(weights, chosen, slots, row_tokens, offsets)
 
 
@@ -298,22 +324,30 @@ def route_backward(dweights: torch.Tensor, weights: torch.Tensor, experts: torch
     """ciera_route_backward: the logits' gradient from the weights' (``weights``
     and ``experts`` as ``route`` returned them)."""
     kind = _logits(logits)
+    index = _index(logits, "logits")
+    stride = _matrix(logits, "logits", logits.dtype, index)
     tokens, n_experts = logits.shape
     if weights.dim() != 2:
         raise ValueError("weights must be [tokens, topk]")
-    shape = (tokens, weights.shape[1])
-    _array(weights, "weights", _F32, shape)
-    _array(dweights, "dweights", _F32, shape)
-    _array(experts, "experts", torch.int32, shape)
-    device = _same_device(logits, dweights, weights, experts)
-    dlogits = torch.empty((tokens, n_experts), dtype=logits.dtype, device=device)
-    _call("ciera_route_backward", device, _ptr(dweights), _ptr(weights), _ptr(experts),
-          _ptr(logits), kind, _stride(logits), tokens, n_experts, shape[1],
-          ROUTE_RENORMALIZE if renormalize else 0, _ptr(dlogits), _current(device))
+    topk = weights.shape[1]
+    w = _array(weights, "weights", _F32, index, tokens, topk)
+    dw = _array(dweights, "dweights", _F32, index, tokens, topk)
+    chosen = _array(experts, "experts", _I32, index, tokens, topk)
+    dlogits = torch.empty((tokens, n_experts), dtype=logits.dtype, device=logits.device)
+    _call("ciera_route_backward", index, dw, w, chosen, logits.data_ptr(), kind, stride, tokens,
+          n_experts, topk, ROUTE_RENORMALIZE if renormalize else 0, dlogits.data_ptr(),
+          _raw_stream(index))
     return dlogits
 
 
-# ---- combine -------------------------------------------------------------
+# ---- gather and combine ----------------------------------------------------
+
+def _slots(t, index: int) -> Tuple[int, int]:
+    if not isinstance(t, torch.Tensor) or t.dim() != 2:
+        raise ValueError("slots must be [tokens, topk]")
+    _array(t, "slots", _I32, index, *t.shape)
+    return t.shape
+
 
 @_on_stream
 def combine(rows: torch.Tensor, slots: torch.Tensor,
@@ -321,68 +355,45 @@ def combine(rows: torch.Tensor, slots: torch.Tensor,
     """ciera_combine: each token's weighted sum of its rows ([tokens, dim]
     bf16); without ``weights`` the plain sum, which is the gradient of
     gathering tokens into expert order."""
-    _matrix(rows, "rows", _BF16)
-    if slots.dim() != 2:
-        raise ValueError("slots must be [tokens, topk]")
-    _array(slots, "slots", torch.int32, slots.shape)
-    if weights is not None:
-        _array(weights, "weights", _F32, slots.shape)
-    device = _same_device(rows, slots, weights)
-    tokens, topk = slots.shape
+    index = _index(rows, "rows")
+    stride = _matrix(rows, "rows", _BF16, index)
+    tokens, topk = _slots(slots, index)
+    w = None if weights is None else _array(weights, "weights", _F32, index, tokens, topk)
     n_rows, dim = rows.shape
-    y = torch.empty((tokens, dim), dtype=_BF16, device=device)
-    _call("ciera_combine", device, _ptr(rows), _stride(rows), n_rows, _ptr(slots),
-          _ptr(weights), tokens, topk, dim, _ptr(y), _current(device))
+    y = torch.empty((tokens, dim), dtype=_BF16, device=rows.device)
+    _call("ciera_combine", index, rows.data_ptr(), stride, n_rows, slots.data_ptr(), w, tokens,
+          topk, dim, y.data_ptr(), _raw_stream(index))
     return y
 
 
 @_on_stream
 def combine_backward(dy: torch.Tensor, rows: torch.Tensor, slots: torch.Tensor,
-                     weights: torch.Tensor, offsets: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
+                     weights: torch.Tensor,
+                     offsets: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     """ciera_combine_backward: (drows, dweights)."""
-    _matrix(rows, "rows", _BF16)
+    index = _index(rows, "rows")
+    stride = _matrix(rows, "rows", _BF16, index)
     n_rows, dim = rows.shape
-    if slots.dim() != 2:
-        raise ValueError("slots must be [tokens, topk]")
-    tokens, topk = slots.shape
-    _matrix(dy, "dy", _BF16, (tokens, dim))
-    _array(slots, "slots", torch.int32, (tokens, topk))
-    _array(weights, "weights", _F32, (tokens, topk))
-    _offsets(offsets)
-    device = _same_device(rows, dy, slots, weights, offsets)
-    drows = torch.empty((n_rows, dim), dtype=_BF16, device=device)
-    dweights = torch.empty((tokens, topk), dtype=_F32, device=device)
-    _call("ciera_combine_backward", device, _ptr(dy), _stride(dy), _ptr(rows), _stride(rows),
-          n_rows, _ptr(slots), _ptr(weights), _ptr(offsets), offsets.numel() - 1, tokens, topk,
-          dim, _ptr(drows), _ptr(dweights), _current(device))
+    tokens, topk = _slots(slots, index)
+    dy_stride = _matrix(dy, "dy", _BF16, index, tokens, dim)
+    w = _array(weights, "weights", _F32, index, tokens, topk)
+    off, experts = _offsets(offsets, index)
+    drows = torch.empty((n_rows, dim), dtype=_BF16, device=rows.device)
+    dweights = torch.empty((tokens, topk), dtype=_F32, device=rows.device)
+    _call("ciera_combine_backward", index, dy.data_ptr(), dy_stride, rows.data_ptr(), stride,
+          n_rows, slots.data_ptr(), w, off, experts, tokens, topk, dim, drows.data_ptr(),
+          dweights.data_ptr(), _raw_stream(index))
     return drows, dweights
 
 
-# ---- products grouped by expert -------------------------------------------
-
-def _offsets(t: torch.Tensor, experts: Optional[int] = None) -> torch.Tensor:
-    n = t.numel() if experts is None else experts + 1
-    if t.numel() < 1:
-        raise ValueError("offsets must hold experts + 1 values")
-    return _array(t, "offsets", torch.int32, (n,))
-
-
-def _rows_of(x: torch.Tensor, tokens: Optional[torch.Tensor]) -> int:
-    if tokens is None:
-        return x.shape[0]
-    if tokens.dim() != 1:
-        raise ValueError("tokens must have one dimension")
-    _array(tokens, "tokens", torch.int32, tokens.shape)
-    return tokens.numel()
-
-
-def _gather(x, tokens, x_scale, device):
+def _gather(x, tokens, x_scale, stride, index):
     rows, dim = tokens.numel(), x.shape[1]
-    y = torch.empty((rows, dim), dtype=x.dtype, device=device)
-    scale = None if x_scale is None else torch.empty(rows, dtype=_F32, device=device)
-    _call("ciera_gather_rows", device, _ptr(x), _stride(x), x.shape[0],
-          E4M3 if x.dtype == _E4M3 else BF16, _ptr(x_scale), _ptr(tokens), rows, dim, _ptr(y),
-          _ptr(scale), _current(device))
+    y = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
+    scale = None if x_scale is None else torch.empty(rows, dtype=_F32, device=x.device)
+    _call("ciera_gather_rows", index, x.data_ptr(), stride, x.shape[0],
+          E4M3 if x.dtype is _E4M3 else BF16, None if x_scale is None else x_scale.data_ptr(),
+          tokens.data_ptr(), rows, dim, y.data_ptr(),
+          None if scale is None else scale.data_ptr(), _raw_stream(index))
     return y, scale
 
 
@@ -392,44 +403,70 @@ def gather_rows(x: torch.Tensor, tokens: torch.Tensor, x_scale: Optional[torch.T
     ``x_scale``: then (rows, scales)), zeros where tokens is -1.  A training
     step that needs the rows twice (``mm_gated``, then ``mm_dw``) gathers them
     once."""
+    index = _index(x, "x")
     e4m3 = x_scale is not None
-    _matrix(x, "x", _E4M3 if e4m3 else _BF16)
-    _rows_of(x, tokens)
+    stride = _matrix(x, "x", _E4M3 if e4m3 else _BF16, index)
+    _tokens(tokens, index)
     if e4m3:
-        _array(x_scale, "x_scale", _F32, (x.shape[0],))
-    y, scale = _gather(x, tokens, x_scale, _same_device(x, tokens, x_scale))
+        _array(x_scale, "x_scale", _F32, index, x.shape[0])
+    y, scale = _gather(x, tokens, x_scale, stride, index)
     return (y, scale) if e4m3 else y
 
 
+# ---- products grouped by expert -------------------------------------------
+
+def _offsets(t, index: int, experts: Optional[int] = None) -> Tuple[int, int]:
+    """Pointer, and the number of experts."""
+    if experts is None:
+        if not isinstance(t, torch.Tensor) or t.numel() < 1:
+            raise ValueError("offsets must hold experts + 1 values")
+        experts = t.numel() - 1
+    return _array(t, "offsets", _I32, index, experts + 1), experts
+
+
+def _tokens(t, index: int) -> int:
+    if not isinstance(t, torch.Tensor) or t.dim() != 1:
+        raise ValueError("tokens must have one dimension")
+    return _array(t, "tokens", _I32, index, t.shape[0])
+
+
 def _forward(x, w, offsets, tokens, x_scale, w_scale, gated, keep):
-    e4m3 = isinstance(x, torch.Tensor) and x.dtype == _E4M3
-    dtype = _E4M3 if e4m3 else _BF16
-    _matrix(x, "x", dtype)
-    _stack(w, "w", dtype)
+    index = _index(x, "x")
+    dtype = x.dtype
+    e4m3 = dtype is _E4M3
+    if not e4m3:
+        dtype = _BF16
+    x_stride = _matrix(x, "x", dtype, index)
+    w_stride, w_expert_stride = _stack(w, "w", dtype, index)
     experts, features, k = w.shape
+    x_rows = x.shape[0]
     if x.shape[1] != k:
         raise ValueError(f"x has {x.shape[1]} columns, w {k}")
     if gated and features % 2:
         raise ValueError("a gated product needs an even number of features (gate, then up)")
     if e4m3 != (x_scale is not None) or e4m3 != (w_scale is not None):
         raise ValueError("x_scale and w_scale go with e4m3 operands")
+    xs = ws = None
     if e4m3:
-        _array(x_scale, "x_scale", _F32, (x.shape[0],))
-        _array(w_scale, "w_scale", _F32, (experts, features))
-    _offsets(offsets, experts)
-    rows = _rows_of(x, tokens)
+        xs = _array(x_scale, "x_scale", _F32, index, x_rows)
+        ws = _array(w_scale, "w_scale", _F32, index, experts, features)
+    off, _ = _offsets(offsets, index, experts)
+    rows, row_tokens = x_rows, None
+    if tokens is not None:
+        row_tokens = _tokens(tokens, index)
+        rows = tokens.shape[0]
+        if rows > _GATHER_ROWS * experts:
+            x, x_scale = _gather(x, tokens, x_scale, x_stride, index)
+            x_stride, x_rows, row_tokens = k, rows, None
+            xs = x_scale.data_ptr() if e4m3 else None
     n = features // 2 if gated else features
-    device = _same_device(x, w, offsets, tokens, x_scale, w_scale)
-    s = _current(device)
-    if tokens is not None and rows > _GATHER_ROWS * experts:
-        x, x_scale = _gather(x, tokens, x_scale, device)
-        tokens = None
-    y = torch.empty((rows, n), dtype=_BF16, device=device)
-    pre = torch.empty((rows, features), dtype=_BF16, device=device) if keep else None
-    _call("ciera_expert_mm", device, _ptr(x), _stride(x), x.shape[0], _ptr(tokens), _ptr(w),
-          _stride(w), w.stride(0) if experts > 1 else features * k, _ptr(x_scale),
-          _ptr(w_scale), _ptr(offsets), rows, experts, n, k, E4M3 if e4m3 else BF16,
-          GATED if gated else 0, _ptr(y), _ptr(pre), _ptr(workspace(device, s)), s)
+    s = _raw_stream(index)
+    y = torch.empty((rows, n), dtype=_BF16, device=x.device)
+    pre = torch.empty((rows, features), dtype=_BF16, device=x.device) if keep else None
+    _call("ciera_expert_mm", index, x.data_ptr(), x_stride, x_rows, row_tokens, w.data_ptr(),
+          w_stride, w_expert_stride, xs, ws, off, rows, experts, n, k, E4M3 if e4m3 else BF16,
+          GATED if gated else 0, y.data_ptr(), pre.data_ptr() if keep else None,
+          workspace(index, s).data_ptr(), s)
     return y, pre
 
 
@@ -458,21 +495,20 @@ def mm_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
           gated: Optional[torch.Tensor] = None) -> torch.Tensor:
     """ciera_expert_mm_dx: gradient of the rows, [rows, k]; with ``gated`` (the
     ``pre`` that mm_gated kept) through the gated unit, [rows, 2 k]."""
-    _matrix(dy, "dy", _BF16)
-    _stack(w, "w", _BF16)
+    index = _index(dy, "dy")
+    dy_stride = _matrix(dy, "dy", _BF16, index)
+    w_stride, w_expert_stride = _stack(w, "w", _BF16, index)
     experts, n, k = w.shape
     rows = dy.shape[0]
     if dy.shape[1] != n:
         raise ValueError(f"dy has {dy.shape[1]} columns, w {n} features")
-    _offsets(offsets, experts)
-    if gated is not None:
-        _array(gated, "gated", _BF16, (rows, 2 * k))
-    device = _same_device(dy, w, offsets, gated)
-    s = _current(device)
-    dx = torch.empty((rows, k if gated is None else 2 * k), dtype=_BF16, device=device)
-    _call("ciera_expert_mm_dx", device, _ptr(dy), _stride(dy), _ptr(w), _stride(w),
-          w.stride(0) if experts > 1 else n * k, _ptr(offsets), rows, experts, n, k,
-          _ptr(gated), _ptr(dx), _ptr(workspace(device, s)), s)
+    off, _ = _offsets(offsets, index, experts)
+    pre = None if gated is None else _array(gated, "gated", _BF16, index, rows, 2 * k)
+    s = _raw_stream(index)
+    dx = torch.empty((rows, k if gated is None else 2 * k), dtype=_BF16, device=dy.device)
+    _call("ciera_expert_mm_dx", index, dy.data_ptr(), dy_stride, w.data_ptr(), w_stride,
+          w_expert_stride, off, rows, experts, n, k, pre, dx.data_ptr(),
+          workspace(index, s).data_ptr(), s)
     return dx
 
 
@@ -483,29 +519,33 @@ def mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
     """ciera_expert_mm_dw: gradient of the weights, [experts, n, k], into
     ``out`` (bf16 or float32, for instance a view of a gradient bucket; bf16
     if not given), added to what it holds with ``accumulate``."""
-    _matrix(dy, "dy", _BF16)
-    _matrix(x, "x", _BF16)
+    index = _index(dy, "dy")
+    dy_stride = _matrix(dy, "dy", _BF16, index)
+    x_stride = _matrix(x, "x", _BF16, index)
     rows, n = dy.shape
-    if _rows_of(x, tokens) != rows:
-        raise ValueError(f"dy has {rows} rows, x {_rows_of(x, tokens)}")
-    _offsets(offsets)
-    experts, k = offsets.numel() - 1, x.shape[1]
+    off, experts = _offsets(offsets, index)
+    k = x.shape[1]
+    if tokens is not None:
+        _tokens(tokens, index)
+    if (x if tokens is None else tokens).shape[0] != rows:
+        raise ValueError(f"dy has {rows} rows, x {(x if tokens is None else tokens).shape[0]}")
     if out is None:
         if accumulate:
             raise ValueError("accumulate needs out")
         out = torch.empty((experts, n, k), dtype=_BF16, device=dy.device)
     elif not isinstance(out, torch.Tensor) or out.dtype not in (_BF16, _F32):
         raise ValueError("out must be bfloat16 or float32")
-    _stack(out, "out", out.dtype)
-    if tuple(out.shape) != (experts, n, k):
+    out_stride, out_expert_stride = _stack(out, "out", out.dtype, index)
+    if out.shape != (experts, n, k):
         raise ValueError(f"out must be {[experts, n, k]}, got {list(out.shape)}")
-    if experts > 1 and n and k and out.stride(0) < (n - 1) * _stride(out) + k:
+    if experts > 1 and n and k and out_expert_stride < (n - 1) * out_stride + k:
         raise ValueError("out's experts overlap")
-    device = _same_device(dy, x, offsets, tokens, out)
-    s = _current(device)
     if tokens is not None:
-        x, _ = _gather(x, tokens, None, device)
-    _call("ciera_expert_mm_dw", device, _ptr(dy), _stride(dy), _ptr(x), _stride(x),
-          _ptr(offsets), rows, experts, n, k, _ptr(out), _stride(out), out.stride(0) if experts > 1 else n * k, F32 if out.dtype == _F32 else BF16,
-          ACCUMULATE if accumulate else 0, _ptr(workspace(device, s)), s)
+        x, _ = _gather(x, tokens, None, x_stride, index)
+        x_stride = k
+    s = _raw_stream(index)
+    _call("ciera_expert_mm_dw", index, dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, off, rows,
+          experts, n, k, out.data_ptr(), out_stride, out_expert_stride,
+          F32 if out.dtype is _F32 else BF16, ACCUMULATE if accumulate else 0,
+          workspace(index, s).data_ptr(), s)
     return out
