@@ -67,6 +67,9 @@ struct RouteParams {
   uint8_t* counts;           // per block of tokens: pairs of each expert
 };
 
+// Bytes of a block's counts: whole words.
+__host__ __device__ inline int count_stride(int experts) { return (experts + 3) & ~3; }
+
 struct RouteBackwardParams {
   const float* dweights;
   const float* weights;

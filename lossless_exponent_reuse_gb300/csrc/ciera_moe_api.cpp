@@ -45,7 +45,7 @@ int64_t ciera_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t dim) 
       dim > kMaxDim)
     return 0;
   const int64_t norm = 4 * norm_backward_blocks(tokens) * dim;
-  const int64_t route = route_blocks(tokens) * experts;
+  const int64_t route = route_blocks(tokens) * count_stride(static_cast<int>(experts));
   const int64_t most = norm > route ? norm : route;
   return kMoeScratch + (most + 255) / 256 * 256;
 }

@@ -74,6 +74,28 @@ __device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* part) {
   return __reduce_max_sync(0xffffffffu, v);
 }
 
+// Eight bf16 values of a 16-byte word.
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = bf16_lo(w[i]);
+    f[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16(f[0], f[1]), pack_bf16(f[2], f[3]), pack_bf16(f[4], f[5]),
+                    pack_bf16(f[6], f[7]));
+}
+
+// Four floats to e4m3 in one word.
+__device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d) {
+  const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(c, d), __NV_SATFINITE, __NV_E4M3);
+  return lo | hi << 16;
+}
+
 // Offset of group e, clamped to [lo, rows]; `lo` is the one before it.
 __device__ __forceinline__ int32_t clamp_offset(int32_t v, int32_t lo, int32_t rows) {
   return v < lo ? lo : v > rows ? rows : v;

@@ -8,10 +8,17 @@ namespace ciera {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kMostRowThreads = 512;  // for one row of the kernels that hold rows in registers
 
 // ------------------------------------------------------------------------
-// Norm: one block per row, the row read once for its sum of squares and
-// again (from L1 or L2) for the outputs.
+// Norm.  Bound by memory: 8 bytes a value in bf16 with a residual, 7 in e4m3.
+//
+// k_rmsnorm holds a row in registers, kVecs words of 8 values per thread, so
+// that it is read once; blockDim.x threads take a row (whole warps, one
+// reduction per statistic), blockDim.y rows share a block where rows are
+// short.  It wants rows of a multiple of 8 values on 16-byte boundaries.
+// k_rmsnorm_any takes every size and alignment, value by value, and reads a
+// row once per statistic (from L1 or L2 after the first).
 
 __device__ __forceinline__ float norm_input(const NormParams& p, int64_t r, int64_t c) {
   float s = bf16_to_f32(p.x[r * p.x_stride + c]);
@@ -61,6 +68,104 @@ __global__ void __launch_bounds__(kRowThreads) k_rmsnorm_any(const NormParams p)
   }
 }
 
+// Sum over the row's threads (blockDim.x of them), the same in each; `part`
+// has blockDim.y rows of 32.
+__device__ __forceinline__ float row_sum(float v, float (*part)[32]) {
+  v = warp_sum_f32(v);
+  if (blockDim.x == 32) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) part[threadIdx.y][threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < blockDim.x >> 5 ? part[threadIdx.y][lane] : 0.0f;
+  return warp_sum_f32(v);
+}
+
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*part)[32]) {
+  v = __reduce_max_sync(0xffffffffu, v);
+  if (blockDim.x == 32) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) part[threadIdx.y][threadIdx.x >> 5] = v;
+  __syncthreads();
+  v = lane < blockDim.x >> 5 ? part[threadIdx.y][lane] : 0u;
+  return __reduce_max_sync(0xffffffffu, v);
+}
+
+template <int kVecs, bool kE4m3>
+__global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p) {
+  __shared__ float part[8][32];
+  __shared__ uint32_t part_max[8][32];
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const bool row = r < p.rows;
+  const int words = static_cast<int>(p.dim / 8);
+  float s[kVecs][8];
+  uint4 weight[kVecs] = {};
+  float sum = 0.0f;
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    const int i = v * blockDim.x + threadIdx.x;
+    uint4 x{}, add{};
+    if (row && i < words) {
+      x = reinterpret_cast<const uint4*>(p.x + r * p.x_stride)[i];
+      if (p.residual) add = reinterpret_cast<const uint4*>(p.residual + r * p.residual_stride)[i];
+      if (p.weight) weight[v] = reinterpret_cast<const uint4*>(p.weight)[i];
+    }
+    float f[8];
+    unpack8(x, s[v]);
+    unpack8(add, f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (p.residual) s[v][j] += f[j];
+      sum += s[v][j] * s[v][j];
+    }
+  }
+  if (p.h) {
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int i = v * blockDim.x + threadIdx.x;
+      if (row && i < words) reinterpret_cast<uint4*>(p.h + r * p.dim)[i] = pack8(s[v]);
+    }
+  }
+  if (p.weight) {
+    sum = row_sum(sum, part);
+    const float rstd = rsqrtf(sum / static_cast<float>(p.dim) + p.eps);
+    if (p.rstd && row && threadIdx.x == 0) p.rstd[r] = rstd;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      float w[8];
+      unpack8(weight[v], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[v][j] = s[v][j] * rstd * w[j];
+    }
+  }
+  float inverse = 1.0f;
+  if (kE4m3) {
+    uint32_t amax = 0;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (v * blockDim.x + threadIdx.x < words)  // behind the row a NaN may stand
+          amax = max(amax, __float_as_uint(s[v][j]) & 0x7FFFFFFFu);
+    const float scale = e4m3_scale(row_max(amax, part_max));
+    inverse = 1.0f / scale;
+    if (row && threadIdx.x == 0) p.scale[r] = scale;
+  }
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    const int i = v * blockDim.x + threadIdx.x;
+    if (!row || i >= words) continue;
+    if (kE4m3) {
+      float (&f)[8] = s[v];
+      const uint2 q = make_uint2(
+          pack_e4m3(f[0] * inverse, f[1] * inverse, f[2] * inverse, f[3] * inverse),
+          pack_e4m3(f[4] * inverse, f[5] * inverse, f[6] * inverse, f[7] * inverse));
+      reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + r * p.dim)[i] = q;
+    } else {
+      reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + r * p.dim)[i] = pack8(s[v]);
+    }
+  }
+}
+
 // Gradient of the norm: each block takes rows blockIdx.x, + gridDim.x, ... in
 // that order and keeps its part of the weight's gradient in its own row of
 // `partial`, so that the result does not depend on the blocks' order.
@@ -88,13 +193,114 @@ __global__ void __launch_bounds__(kRowThreads) k_rmsnorm_backward_any(const Norm
   }
 }
 
-__global__ void __launch_bounds__(kRowThreads) k_sum_partials(const float* partial, int blocks,
-                                                              int64_t dim, float* out) {
-  const int64_t c = static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x;
-  if (c >= dim) return;
+// The same with a row in registers and the weight's gradient too, the next
+// row's words under way while this one is reduced.  Bound by memory, 8 bytes a
+// value.
+template <int kVecs>
+__global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm_backward(const NormBackwardParams p) {
+  __shared__ float part[2][8][32];
+  const int words = static_cast<int>(p.dim / 8);
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  float dw[kVecs][8] = {};
+  uint4 weight[kVecs], dy[kVecs], h[kVecs], dh[kVecs];
+  float rstd = 0.0f;
+  const auto fetch = [&](int64_t r) {
+    const bool row = r < p.rows;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int i = v * blockDim.x + threadIdx.x;
+      dy[v] = h[v] = dh[v] = make_uint4(0, 0, 0, 0);
+      if (!row || i >= words) continue;
+      dy[v] = reinterpret_cast<const uint4*>(p.dy + r * p.dy_stride)[i];
+      h[v] = reinterpret_cast<const uint4*>(p.h + r * p.h_stride)[i];
+      if (p.dh) dh[v] = reinterpret_cast<const uint4*>(p.dh + r * p.dh_stride)[i];
+    }
+    rstd = row ? p.rstd[r] : 0.0f;
+  };
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    const int i = v * blockDim.x + threadIdx.x;
+    weight[v] = i < words ? reinterpret_cast<const uint4*>(p.weight)[i] : make_uint4(0, 0, 0, 0);
+  }
+  fetch(static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y);
+  int turn = 0;  // two reductions' scratch in turn: one barrier each
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step) {
+    const int64_t r = r0 + threadIdx.y;
+    float g[kVecs][8], hv[kVecs][8];
+    uint4 more[kVecs];
+    float dot = 0.0f;
+    const float rs = rstd;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      float d[8], w[8];
+      unpack8(dy[v], d);
+      unpack8(h[v], hv[v]);
+      unpack8(weight[v], w);
+      more[v] = dh[v];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        g[v][j] = d[j] * w[j];
+        dot += g[v][j] * hv[v][j];
+        dw[v][j] += d[j] * hv[v][j] * rs;
+      }
+    }
+    fetch(r + step);
+    dot = row_sum(dot, part[turn]);
+    turn ^= 1;
+    const float pull = dot / static_cast<float>(p.dim) * rs * rs * rs;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      const int i = v * blockDim.x + threadIdx.x;
+      if (r >= p.rows || i >= words) continue;
+      float out[8];
+      unpack8(more[v], out);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float dx = rs * g[v][j] - hv[v][j] * pull;
+        out[j] = p.dh ? dx + out[j] : dx;
+      }
+      reinterpret_cast<uint4*>(p.dx + r * p.dim)[i] = pack8(out);
+    }
+  }
+  // this block's part of the weight's gradient, its rows' in order
+  extern __shared__ float column[];  // blockDim.y > 1: dim floats
+  float* mine = p.partial + static_cast<int64_t>(blockIdx.x) * p.dim;
+  for (int turn_y = 0; turn_y < blockDim.y; ++turn_y) {
+    if (threadIdx.y == turn_y) {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        const int i = v * blockDim.x + threadIdx.x;
+        if (i >= words) continue;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float before = turn_y ? column[i * 8 + j] : 0.0f;
+          if (turn_y + 1 == blockDim.y)
+            mine[i * 8 + j] = before + dw[v][j];
+          else
+            column[i * 8 + j] = before + dw[v][j];
+        }
+      }
+    }
+    if (blockDim.y > 1) __syncthreads();
+  }
+}
+
+// Sums of the blocks' parts: 32 columns a block, each by 32 threads that take
+// every 32nd part in order, then those 32 sums in order of a tree.
+__global__ void __launch_bounds__(1024) k_sum_partials(const float* partial, int blocks,
+                                                       int64_t dim, float* out) {
+  __shared__ float sums[32][33];
+  const int lane = threadIdx.x & 31, way = threadIdx.x >> 5;
+  const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float sum = 0.0f;
-  for (int b = 0; b < blocks; ++b) sum += partial[b * dim + c];
-  out[c] = sum;
+  if (c < dim)
+#pragma unroll 4
+    for (int b = way; b < blocks; b += 32) sum += partial[b * dim + c];
+  sums[way][lane] = sum;
+  __syncthreads();
+  const float total = warp_sum_f32(sums[lane][way]);
+  const int64_t to = static_cast<int64_t>(blockIdx.x) * 32 + way;
+  if (lane == 0 && to < dim) out[to] = total;
 }
 
 // ------------------------------------------------------------------------
@@ -117,9 +323,33 @@ __device__ __forceinline__ uint32_t logit_key(float l) {
 }
 constexpr uint32_t kKeyMinusInf = 0x007FFFFFu;  // logit_key(-inf)
 
+// The logit of a key (+0 for either zero, a NaN for any).
+__device__ __forceinline__ float key_logit(uint32_t k) {
+  return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k);
+}
+
 __device__ __forceinline__ float load_logit(const void* logits, int bf16, int64_t i) {
   return bf16 ? bf16_to_f32(static_cast<const uint16_t*>(logits)[i])
               : static_cast<const float*>(logits)[i];
+}
+
+// Exclusive sums of v[0 .. n) in place, the total in v[n]; one warp.
+__device__ __forceinline__ void exclusive_sums(int32_t* v, int n) {
+  const int lane = threadIdx.x & 31;
+  int32_t run = 0;
+  for (int i0 = 0; i0 < n; i0 += 32) {
+    const int i = i0 + lane;
+    const int32_t own = i < n ? v[i] : 0;
+    int32_t sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int32_t left = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += left;
+    }
+    if (i < n) v[i] = run + sum - own;
+    run += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  if (lane == 0) v[n] = run;
 }
 
 constexpr int kRouteWarps = 16;
@@ -158,101 +388,119 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteParams p)
       if (v * 32 + lane < p.experts) sum += expf(l[v] - top);
     sum = warp_sum_f32(sum);
 
-    float mine = 0.0f, total = 0.0f;  // lane j: the weight of choice j
+    uint32_t picked = 0;  // lane j: key and expert of choice j
     int choice = -1;
     for (int j = 0; j < p.topk; ++j) {
       uint32_t best = 0;
 #pragma unroll
       for (int v = 0; v < V; ++v) best = max(best, key[v]);
-      const uint32_t all = __reduce_max_sync(0xffffffffu, best);
-      if (all == 0) break;  // nothing left to choose
+      best = __reduce_max_sync(0xffffffffu, best);
+      if (best == 0) break;  // nothing left to choose
       uint32_t at = 0xFFFFFFFFu;
-      float logit = 0.0f;
 #pragma unroll
       for (int v = V - 1; v >= 0; --v)
-        if (key[v] == all) {
-          at = v * 32 + lane;
-          logit = l[v];
-        }
+        if (key[v] == best) at = v * 32 + lane;
       const uint32_t e = __reduce_min_sync(0xffffffffu, at);
-      logit = __shfl_sync(0xffffffffu, logit, e & 31);
 #pragma unroll
       for (int v = 0; v < V; ++v)
         if (e == v * 32 + lane) key[v] = 0u;
-      const float w = expf(logit - top) / sum;
-      total += w;
       if (lane == j) {
-        mine = w;
+        picked = best;
         choice = static_cast<int>(e);
       }
-      if (lane == 0) atomicOr(&bits[e], 1ull << i);
     }
-    if (p.renormalize && choice >= 0) mine /= total;
+    float mine = choice >= 0 ? expf(key_logit(picked) - top) / sum : 0.0f;
+    if (p.renormalize) {
+      const float total = warp_sum_f32(mine);
+      if (choice >= 0) mine /= total;
+    }
+    if (choice >= 0) atomicOr(&bits[choice], 1ull << i);
     if (lane < p.topk) {
       p.weights[t * p.topk + lane] = mine;
       p.chosen[t * p.topk + lane] = choice;
     }
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.experts; e += blockDim.x)
-    p.counts[static_cast<int64_t>(blockIdx.x) * p.experts + e] =
-        static_cast<uint8_t>(__popcll(bits[e]));
   const int64_t pairs = min(static_cast<int64_t>(kRouteTokens), p.tokens - first) * p.topk;
+  if (gridDim.x > 1) {
+    const int row = count_stride(p.experts);
+    for (int e = threadIdx.x; e < row; e += blockDim.x)
+      p.counts[static_cast<int64_t>(blockIdx.x) * row + e] =
+          e < p.experts ? static_cast<uint8_t>(__popcll(bits[e])) : 0;
+    for (int64_t i = threadIdx.x; i < pairs; i += blockDim.x) {
+      const int e = p.chosen[first * p.topk + i];
+      const int token = static_cast<int>(i / p.topk);
+      p.slots[first * p.topk + i] = e < 0 ? -1 : __popcll(bits[e] & ((1ull << token) - 1));
+    }
+    return;
+  }
+  // One block has all tokens: the order at once.
+  __shared__ int32_t base[kMaxExperts + 1];
+  for (int e = threadIdx.x; e < p.experts; e += blockDim.x) base[e] = __popcll(bits[e]);
+  __syncthreads();
+  if (threadIdx.x < 32) exclusive_sums(base, p.experts);
+  __syncthreads();
+  for (int e = threadIdx.x; e <= p.experts; e += blockDim.x) p.offsets[e] = base[e];
   for (int64_t i = threadIdx.x; i < pairs; i += blockDim.x) {
-    const int e = p.chosen[first * p.topk + i];
+    const int e = p.chosen[i];
     const int token = static_cast<int>(i / p.topk);
-    p.slots[first * p.topk + i] = e < 0 ? -1 : __popcll(bits[e] & ((1ull << token) - 1));
+    if (e >= 0) {
+      const int32_t slot = base[e] + __popcll(bits[e] & ((1ull << token) - 1));
+      p.slots[i] = slot;
+      p.row_tokens[slot] = token;
+    } else {
+      p.slots[i] = -1;
+    }
+    if (i >= base[p.experts]) p.row_tokens[i] = -1;
   }
 }
 
+// Adds what stands before a block to its pairs' ranks.  Every block sums the
+// counts of all blocks, four experts a word: with 16384 tokens 256 x 128 bytes
+// from L2, shared among eight warps.
 constexpr int kPlaceThreads = 256;
+constexpr int kPlaceWays = 8;
 
 __global__ void __launch_bounds__(kPlaceThreads) k_route_place(const RouteParams p) {
-  __shared__ int32_t base[kMaxExperts];    // rows before this block's, of each expert
-  __shared__ int32_t total[kMaxExperts + 1];
-  const int blocks = gridDim.x;
-  for (int e = threadIdx.x; e < p.experts; e += kPlaceThreads) {
-    int32_t before = 0, all = 0;
-    for (int b = 0; b < blocks; ++b) {
-      const int32_t n = p.counts[static_cast<int64_t>(b) * p.experts + e];
-      all += n;
-      if (b < static_cast<int>(blockIdx.x)) before += n;
-    }
-    base[e] = before;
-    total[e] = all;
-  }
+  __shared__ int32_t base[kMaxExperts + 1];     // offsets, then with the rows before this block
+  __shared__ int32_t before[kMaxExperts];
+  for (int e = threadIdx.x; e < p.experts; e += kPlaceThreads) base[e] = before[e] = 0;
   __syncthreads();
-  if (threadIdx.x < 32) {  // exclusive sum of the totals: the offsets
-    int32_t run = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += 32) {
-      const int e = e0 + threadIdx.x;
-      const int32_t n = e < p.experts ? total[e] : 0;
-      int32_t s = n;
+  const int lane = threadIdx.x & 31, way = threadIdx.x >> 5;
+  const int words = count_stride(p.experts) / 4;
+  const uint32_t* counts = reinterpret_cast<const uint32_t*>(p.counts);
+  for (int w = lane; w < words; w += 32) {
+    int32_t all[4] = {}, mine[4] = {};
+#pragma unroll 8
+    for (int b = way; b < gridDim.x; b += kPlaceWays) {
+      const uint32_t n = counts[static_cast<int64_t>(b) * words + w];
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int32_t left = __shfl_up_sync(0xffffffffu, s, o);
-        if (static_cast<int>(threadIdx.x) >= o) s += left;
+      for (int i = 0; i < 4; ++i) {
+        const int32_t c = n >> (8 * i) & 0xFF;
+        all[i] += c;
+        if (b < static_cast<int>(blockIdx.x)) mine[i] += c;
       }
-      if (e < p.experts) {
-        base[e] += run + s - n;
-        if (blockIdx.x == 0) p.offsets[e] = run + s - n;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (w * 4 + i < p.experts) {  // whole numbers: the order does not matter
+        atomicAdd(&base[w * 4 + i], all[i]);
+        atomicAdd(&before[w * 4 + i], mine[i]);
       }
-      run += __shfl_sync(0xffffffffu, s, 31);
-    }
-    if (threadIdx.x == 0) {
-      total[p.experts] = run;
-      if (blockIdx.x == 0) p.offsets[p.experts] = run;
-    }
   }
   __syncthreads();
+  if (threadIdx.x < 32) exclusive_sums(base, p.experts);
+  __syncthreads();
+  if (blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= p.experts; e += kPlaceThreads) p.offsets[e] = base[e];
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kRouteTokens;
   const int64_t pairs = min(static_cast<int64_t>(kRouteTokens), p.tokens - first) * p.topk;
-  const int32_t used = total[p.experts];
+  const int32_t used = base[p.experts];
   for (int64_t i = threadIdx.x; i < pairs; i += kPlaceThreads) {
     const int64_t pair = first * p.topk + i;
     const int e = p.chosen[pair];
     if (e >= 0) {
-      const int32_t slot = base[e] + p.slots[pair];
+      const int32_t slot = base[e] + before[e] + p.slots[pair];
       p.slots[pair] = slot;
       p.row_tokens[slot] = static_cast<int32_t>(first + i / p.topk);
     }
@@ -382,12 +630,51 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_any(const CombineParams
   }
 }
 
+// The same 16 bytes at a time, eight rows' words under way at once.
+__global__ void __launch_bounds__(kRowThreads) k_combine(const CombineParams p) {
+  const int64_t t = blockIdx.x;
+  const int words = static_cast<int>(p.dim / 8);
+  __shared__ int32_t slot[kMaxTopk];
+  __shared__ float weight[kMaxTopk];
+  if (threadIdx.x < p.topk) {
+    slot[threadIdx.x] = static_cast<int32_t>(slot_of(p, t * p.topk + threadIdx.x));
+    weight[threadIdx.x] = p.weights ? p.weights[t * p.topk + threadIdx.x] : 1.0f;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < words; i += blockDim.x) {
+    float sum[8] = {};
+    for (int j0 = 0; j0 < p.topk; j0 += 8) {
+      uint4 word[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const bool some = j0 + j < p.topk && slot[j0 + j] >= 0;
+        word[j] = make_uint4(0, 0, 0, 0);
+        if (some)
+          word[j] = reinterpret_cast<const uint4*>(
+              p.rows + static_cast<int64_t>(slot[j0 + j]) * p.stride)[i];
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if (j0 + j >= p.topk || slot[j0 + j] < 0) continue;
+        float f[8];
+        unpack8(word[j], f);
+#pragma unroll
+        for (int q = 0; q < 8; ++q) sum[q] += weight[j0 + j] * f[q];
+      }
+    }
+    reinterpret_cast<uint4*>(p.y + t * p.dim)[i] = pack8(sum);
+  }
+}
+
 // Zeros to the rows past the last group, shared among the blocks.
+template <typename V>
 __device__ __forceinline__ void zero_unused_rows(const CombineParams& p) {
+  const int64_t n = p.dim * 2 / static_cast<int64_t>(sizeof(V));
   int64_t used = p.offsets[p.experts];
   used = used < 0 ? 0 : used;
   for (int64_t r = used + blockIdx.x; r < p.n_rows; r += gridDim.x)
-    for (int64_t c = threadIdx.x; c < p.dim; c += blockDim.x) p.drows[r * p.dim + c] = 0;
+    for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
+      reinterpret_cast<V*>(p.drows)[r * n + i] = V{};
 }
 
 __global__ void __launch_bounds__(kRowThreads) k_combine_backward_any(const CombineParams p) {
@@ -407,7 +694,77 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_backward_any(const Comb
       if (threadIdx.x == 0) p.dweights[t * p.topk + j] = dot;
       __syncthreads();
     }
-  zero_unused_rows(p);
+  zero_unused_rows<uint16_t>(p);
+}
+
+// The same 16 bytes at a time: a block per token, eight rows at once.  The
+// eight dot products are reduced together: at each of three exchanges a lane
+// hands over half of its sums, so that a warp needs 9 exchanges for 8 sums.
+__global__ void __launch_bounds__(kRowThreads) k_combine_backward(const CombineParams p) {
+  __shared__ int32_t slot[kMaxTopk];
+  __shared__ float weight[kMaxTopk];
+  __shared__ float part[32][8];
+  const int words = static_cast<int>(p.dim / 8);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t t = blockIdx.x;
+  if (t < p.tokens) {
+    if (threadIdx.x < p.topk) {
+      slot[threadIdx.x] = static_cast<int32_t>(slot_of(p, t * p.topk + threadIdx.x));
+      weight[threadIdx.x] = p.weights[t * p.topk + threadIdx.x];
+    }
+    __syncthreads();
+    for (int j0 = 0; j0 < p.topk; j0 += 8) {
+      float dot[8] = {};
+      for (int i = threadIdx.x; i < words; i += blockDim.x) {
+        uint4 word[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          word[j] = make_uint4(0, 0, 0, 0);
+          if (j0 + j < p.topk && slot[j0 + j] >= 0)
+            word[j] = reinterpret_cast<const uint4*>(
+                p.rows + static_cast<int64_t>(slot[j0 + j]) * p.stride)[i];
+        }
+        float dy[8];
+        unpack8(reinterpret_cast<const uint4*>(p.dy + t * p.dy_stride)[i], dy);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j0 + j >= p.topk || slot[j0 + j] < 0) continue;
+          float f[8], out[8];
+          unpack8(word[j], f);
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            dot[j] += dy[q] * f[q];
+            out[q] = weight[j0 + j] * dy[q];
+          }
+          reinterpret_cast<uint4*>(p.drows + static_cast<int64_t>(slot[j0 + j]) * p.dim)[i] =
+              pack8(out);
+        }
+      }
+      // lane bits 4, 3, 2 choose sums 4.., 2.., 1..
+#pragma unroll
+      for (int half = 4; half > 0; half >>= 1) {
+        const int o = half * 4;
+        const bool upper = lane & o;
+#pragma unroll
+        for (int j = 0; j < half; ++j) {
+          const float give = upper ? dot[j] : dot[j + half];
+          const float keep = upper ? dot[j + half] : dot[j];
+          dot[j] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      }
+      dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 2);
+      dot[0] += __shfl_xor_sync(0xffffffffu, dot[0], 1);
+      if ((lane & 3) == 0) part[warp][lane >> 2] = dot[0];
+      __syncthreads();
+      if (threadIdx.x < 8 && j0 + threadIdx.x < p.topk) {
+        float sum = 0.0f;
+        for (int w = 0; w < blockDim.x >> 5; ++w) sum += part[w][threadIdx.x];
+        p.dweights[t * p.topk + j0 + threadIdx.x] = sum;
+      }
+      __syncthreads();
+    }
+  }
+  zero_unused_rows<uint4>(p);
 }
 
 template <int V>
@@ -424,16 +781,80 @@ int grid_of(int64_t n) { return static_cast<int>(n < (1 << 30) ? n : (1 << 30));
 
 }  // namespace
 
+namespace {
+
+bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// A row of 16-byte words: words per thread, threads per row, rows per block.
+// One word per thread as far as 512 threads reach, then two and four; short
+// rows share a block of 256 threads.
+struct RowShape {
+  int vecs;  // 0: the row does not fit
+  dim3 block;
+};
+
+RowShape row_shape(int64_t dim) {
+  const int64_t words = dim / 8;
+  RowShape s{};
+  for (int vecs = 1; vecs <= 4; vecs *= 2) {
+    const int64_t threads = (words + 32 * vecs - 1) / (32 * vecs) * 32;
+    if (threads > kMostRowThreads) continue;
+    s.vecs = vecs;
+    const unsigned rows = threads <= 128 ? 256 / static_cast<unsigned>(threads) : 1;
+    s.block = dim3(static_cast<unsigned>(threads), rows);
+    break;
+  }
+  return s;
+}
+
+template <int kVecs>
+void norm_at(const NormParams& p, dim3 block, cudaStream_t s) {
+  const int grid = grid_of((p.rows + block.y - 1) / block.y);
+  if (p.e4m3)
+    k_rmsnorm<kVecs, true><<<grid, block, 0, s>>>(p);
+  else
+    k_rmsnorm<kVecs, false><<<grid, block, 0, s>>>(p);
+}
+
+}  // namespace
+
 int launch_rmsnorm(const NormParams& p, void* stream) {
-  k_rmsnorm_any<<<grid_of(p.rows), kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const RowShape shape = row_shape(p.dim);
+  const bool words = p.dim % 8 == 0 && p.x_stride % 8 == 0 && on16(p.x) && on16(p.y) &&
+                     on16(p.weight) && on16(p.h) &&
+                     (!p.residual || (on16(p.residual) && p.residual_stride % 8 == 0));
+  if (!words || shape.vecs == 0)
+    k_rmsnorm_any<<<grid_of(p.rows), kRowThreads, 0, s>>>(p);
+  else if (shape.vecs == 1)
+    norm_at<1>(p, shape.block, s);
+  else if (shape.vecs == 2)
+    norm_at<2>(p, shape.block, s);
+  else
+    norm_at<4>(p, shape.block, s);
   return cudaGetLastError();
 }
 
 int launch_rmsnorm_backward(const NormBackwardParams& p, int blocks, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  k_rmsnorm_backward_any<<<blocks, kRowThreads, 0, s>>>(p);
-  k_sum_partials<<<grid_of((p.dim + kRowThreads - 1) / kRowThreads), kRowThreads, 0, s>>>(
-      p.partial, blocks, p.dim, p.dweight);
+  const RowShape shape = row_shape(p.dim);
+  const bool words = p.dim % 8 == 0 && p.dy_stride % 8 == 0 && p.h_stride % 8 == 0 &&
+                     on16(p.dy) && on16(p.h) && on16(p.weight) && on16(p.dx) &&
+                     (!p.dh || (on16(p.dh) && p.dh_stride % 8 == 0));
+  if (!words || shape.vecs == 0) {
+    k_rmsnorm_backward_any<<<blocks, kRowThreads, 0, s>>>(p);
+  } else {
+    const int64_t most = (p.rows + shape.block.y - 1) / shape.block.y;
+    if (most < blocks) blocks = static_cast<int>(most);
+    const size_t smem = shape.block.y > 1 ? 4 * static_cast<size_t>(p.dim) : 0;
+    if (shape.vecs == 1)
+      k_rmsnorm_backward<1><<<blocks, shape.block, smem, s>>>(p);
+    else if (shape.vecs == 2)
+      k_rmsnorm_backward<2><<<blocks, shape.block, smem, s>>>(p);
+    else
+      k_rmsnorm_backward<4><<<blocks, shape.block, smem, s>>>(p);
+  }
+  k_sum_partials<<<grid_of((p.dim + 31) / 32), 1024, 0, s>>>(p.partial, blocks, p.dim, p.dweight);
   return cudaGetLastError();
 }
 
@@ -448,7 +869,7 @@ int launch_route(const RouteParams& p, void* stream) {
     route_at<8>(p, blocks, s);
   else
     route_at<32>(p, blocks, s);
-  k_route_place<<<blocks, kPlaceThreads, 0, s>>>(p);
+  if (blocks > 1) k_route_place<<<blocks, kPlaceThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -479,15 +900,34 @@ int launch_gather(const GatherParams& p, void* stream) {
   return cudaGetLastError();
 }
 
+namespace {
+
+// Threads for a row of 16-byte words: one word each up to 256.
+int word_threads(int64_t dim) {
+  const int64_t words = dim / 8;
+  return words >= 256 ? 256 : words <= 32 ? 32 : static_cast<int>((words + 31) / 32 * 32);
+}
+
+}  // namespace
+
 int launch_combine(const CombineParams& p, void* stream) {
-  k_combine_any<<<p.tokens, kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p.dim % 8 == 0 && p.stride % 8 == 0 && on16(p.rows) && on16(p.y))
+    k_combine<<<p.tokens, word_threads(p.dim), 0, s>>>(p);
+  else
+    k_combine_any<<<p.tokens, kRowThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
 int launch_combine_backward(const CombineParams& p, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   // without tokens there may still be rows to zero
   const int blocks = p.tokens > 0 ? p.tokens : grid_of(p.n_rows);
-  k_combine_backward_any<<<blocks, kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(p);
+  if (p.dim % 8 == 0 && p.stride % 8 == 0 && p.dy_stride % 8 == 0 && on16(p.rows) && on16(p.dy) &&
+      on16(p.drows))
+    k_combine_backward<<<blocks, word_threads(p.dim), 0, s>>>(p);
+  else
+    k_combine_backward_any<<<blocks, kRowThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
