@@ -11,8 +11,8 @@ namespace ciera {
 
 constexpr int kMaxExperts = 1024;
 constexpr int kMaxTopk = 32;
-constexpr int kRouteTokens = 64;        // tokens per block of k_route
-constexpr int kNormBackwardBlocks = 608;  // most blocks of a norm's gradient: 4 per SM
+constexpr int kRouteTokens = 32;        // tokens per block of k_route
+constexpr int kNormBackwardBlocks = 760;  // most blocks of a norm's gradient: 5 per SM
 constexpr int64_t kMoeScratch = 256;    // offset of the scratch behind the control block
 
 // Limit of every bounded device-side wait (ciera_set_wait_timeout_ns).

@@ -197,10 +197,11 @@ __global__ void __launch_bounds__(kRowThreads) k_rmsnorm_backward_any(const Norm
 // row's words under way while this one is reduced.  Bound by memory, 8 bytes a
 // value.
 template <int kVecs>
-__global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm_backward(const NormBackwardParams p) {
+__global__ void __launch_bounds__(kMostRowThreads, kVecs == 1 ? 2 : 1) k_rmsnorm_backward(const NormBackwardParams p) {
   __shared__ float part[2][8][32];
   const int words = static_cast<int>(p.dim / 8);
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  const float inverse_dim = 1.0f / static_cast<float>(p.dim);
   float dw[kVecs][8] = {};
   uint4 weight[kVecs], dy[kVecs], h[kVecs], dh[kVecs];
   float rstd = 0.0f;
@@ -226,7 +227,8 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm_backward(const Norm
   int turn = 0;  // two reductions' scratch in turn: one barrier each
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step) {
     const int64_t r = r0 + threadIdx.y;
-    float g[kVecs][8], hv[kVecs][8];
+    // with n = h rstd:  dx = rstd (g - n mean(g n)) + dh,  dweight += dy n
+    float g[kVecs][8], n[kVecs][8];
     uint4 more[kVecs];
     float dot = 0.0f;
     const float rs = rstd;
@@ -234,20 +236,21 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm_backward(const Norm
     for (int v = 0; v < kVecs; ++v) {
       float d[8], w[8];
       unpack8(dy[v], d);
-      unpack8(h[v], hv[v]);
+      unpack8(h[v], n[v]);
       unpack8(weight[v], w);
       more[v] = dh[v];
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
+        n[v][j] *= rs;
         g[v][j] = d[j] * w[j];
-        dot += g[v][j] * hv[v][j];
-        dw[v][j] += d[j] * hv[v][j] * rs;
+        dot += g[v][j] * n[v][j];
+        dw[v][j] += d[j] * n[v][j];
       }
     }
     fetch(r + step);
     dot = row_sum(dot, part[turn]);
     turn ^= 1;
-    const float pull = dot / static_cast<float>(p.dim) * rs * rs * rs;
+    const float mean = dot * inverse_dim;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const int i = v * blockDim.x + threadIdx.x;
@@ -255,10 +258,7 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm_backward(const Norm
       float out[8];
       unpack8(more[v], out);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float dx = rs * g[v][j] - hv[v][j] * pull;
-        out[j] = p.dh ? dx + out[j] : dx;
-      }
+      for (int j = 0; j < 8; ++j) out[j] += rs * (g[v][j] - n[v][j] * mean);
       reinterpret_cast<uint4*>(p.dx + r * p.dim)[i] = pack8(out);
     }
   }
@@ -304,12 +304,13 @@ __global__ void __launch_bounds__(1024) k_sum_partials(const float* partial, int
 }
 
 // ------------------------------------------------------------------------
-// Route.  A warp per token: its logits in registers, the softmax's maximum
-// and sum, then topk rounds of "largest remaining, lowest index".
+// Route.  A warp per token: its logits in registers, topk rounds of "largest
+// remaining, lowest index" (the first round's is the softmax's maximum), then
+// the softmax's sum and the chosen weights.
 //
 // The order: a token chooses an expert at most once, so a pair's rank among
 // its block's pairs of the same expert is the number of earlier tokens of the
-// block that chose it.  With a bit per token and expert (64 tokens a block)
+// block that chose it.  With a bit per token and expert (32 tokens a block)
 // that is a population count, independent of the order in which warps set
 // the bits.  k_route leaves ranks and the counts per block and expert;
 // k_route_place adds what stands before the block.
@@ -354,67 +355,109 @@ __device__ __forceinline__ void exclusive_sums(int32_t* v, int n) {
 
 constexpr int kRouteWarps = 16;
 
+// Batcher's odd-even merge sort of a lane's V keys, descending; equal keys keep
+// the lower place first.
+template <int V>
+__device__ __forceinline__ void sort_lane(uint32_t (&key)[V], int (&place)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p <<= 1)
+#pragma unroll
+    for (int k = p; k >= 1; k >>= 1)
+#pragma unroll
+      for (int j = k % p; j + k < V; j += 2 * k)
+#pragma unroll
+        for (int i = 0; i < k; ++i) {
+          const int a = i + j, b = i + j + k;
+          if (b < V && a / (2 * p) == b / (2 * p)) {
+            const bool swap =
+                key[b] > key[a] || (key[b] == key[a] && place[b] < place[a]);
+            const uint32_t ka = key[a];
+            const int pa = place[a];
+            key[a] = swap ? key[b] : ka;
+            place[a] = swap ? place[b] : pa;
+            key[b] = swap ? ka : key[b];
+            place[b] = swap ? pa : place[b];
+          }
+        }
+}
+
 // V: logits per lane (experts <= 32 V).
 template <int V>
 __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteParams p) {
-  extern __shared__ unsigned long long bits[];  // per expert: tokens of this block
+  __shared__ uint32_t bits[kMaxExperts];  // per expert: a bit per token of this block
   for (int e = threadIdx.x; e < p.experts; e += blockDim.x) bits[e] = 0;
   __syncthreads();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t first = static_cast<int64_t>(blockIdx.x) * kRouteTokens;
-  for (int i = warp; i < kRouteTokens; i += kRouteWarps) {
+  // the next token's logits are under way while this one's are sorted
+  float next[V];
+  bool next_live = false;
+  const auto fetch = [&](int i) {
     const int64_t t = first + i;
-    if (t >= p.tokens) break;
-    const bool live = !p.mask || p.mask[t] != 0;
-    float l[V];
-    uint32_t key[V];
-    float top = -INFINITY;
+    const bool some = i < kRouteTokens && t < p.tokens;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int e = v * 32 + lane;
-      l[v] = e < p.experts ? load_logit(p.logits, p.bf16, t * p.stride + e) : -INFINITY;
+      next[v] = some && e < p.experts ? load_logit(p.logits, p.bf16, t * p.stride + e) : -INFINITY;
+    }
+    next_live = some && (!p.mask || p.mask[t] != 0);
+  };
+  fetch(warp);
+  for (int i = warp; i < kRouteTokens; i += kRouteWarps) {
+    const int64_t t = first + i;
+    if (t >= p.tokens) break;
+    const bool live = next_live;
+    float l[V];
+    uint32_t key[V];
+#pragma unroll
+    for (int v = 0; v < V; ++v) l[v] = next[v];
+    fetch(i + kRouteWarps);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int e = v * 32 + lane;
       key[v] = e < p.experts && live ? logit_key(l[v]) : 0u;
       if (key[v] <= kKeyMinusInf) key[v] = 0u;  // -inf is never chosen
-      top = l[v] > top || l[v] != l[v] ? l[v] : top;
     }
+    // Each lane sorts its logits, largest first, lowest index first among
+    // equals (V is a power of two: a network of compare-exchanges), and offers
+    // its first; the lane that is taken moves up.
+    int place[V];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      const float other = __shfl_xor_sync(0xffffffffu, top, o);
-      top = other > top || other != other ? other : top;
-    }
-    float sum = 0.0f;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-      if (v * 32 + lane < p.experts) sum += expf(l[v] - top);
-    sum = warp_sum_f32(sum);
-
-    uint32_t picked = 0;  // lane j: key and expert of choice j
+    for (int v = 0; v < V; ++v) place[v] = v * 32 + lane;
+    sort_lane<V>(key, place);
+    uint32_t picked = 0, largest = 0;  // lane j: key and expert of choice j
     int choice = -1;
     for (int j = 0; j < p.topk; ++j) {
-      uint32_t best = 0;
-#pragma unroll
-      for (int v = 0; v < V; ++v) best = max(best, key[v]);
-      best = __reduce_max_sync(0xffffffffu, best);
+      const uint32_t best = __reduce_max_sync(0xffffffffu, key[0]);
       if (best == 0) break;  // nothing left to choose
-      uint32_t at = 0xFFFFFFFFu;
+      if (j == 0) largest = best;
+      const uint32_t e =
+          __reduce_min_sync(0xffffffffu, key[0] == best ? static_cast<uint32_t>(place[0]) : ~0u);
+      if (e == static_cast<uint32_t>(place[0])) {
 #pragma unroll
-      for (int v = V - 1; v >= 0; --v)
-        if (key[v] == best) at = v * 32 + lane;
-      const uint32_t e = __reduce_min_sync(0xffffffffu, at);
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-        if (e == v * 32 + lane) key[v] = 0u;
+        for (int v = 0; v + 1 < V; ++v) {
+          key[v] = key[v + 1];
+          place[v] = place[v + 1];
+        }
+        key[V - 1] = 0u;
+      }
       if (lane == j) {
         picked = best;
         choice = static_cast<int>(e);
       }
     }
+    const float top = key_logit(largest);
+    float sum = 0.0f;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+      if (v * 32 + lane < p.experts) sum += expf(l[v] - top);
+    sum = warp_sum_f32(sum);
     float mine = choice >= 0 ? expf(key_logit(picked) - top) / sum : 0.0f;
     if (p.renormalize) {
       const float total = warp_sum_f32(mine);
       if (choice >= 0) mine /= total;
     }
-    if (choice >= 0) atomicOr(&bits[choice], 1ull << i);
+    if (choice >= 0) atomicOr(&bits[choice], 1u << i);
     if (lane < p.topk) {
       p.weights[t * p.topk + lane] = mine;
       p.chosen[t * p.topk + lane] = choice;
@@ -426,17 +469,17 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteParams p)
     const int row = count_stride(p.experts);
     for (int e = threadIdx.x; e < row; e += blockDim.x)
       p.counts[static_cast<int64_t>(blockIdx.x) * row + e] =
-          e < p.experts ? static_cast<uint8_t>(__popcll(bits[e])) : 0;
+          e < p.experts ? static_cast<uint8_t>(__popc(bits[e])) : 0;
     for (int64_t i = threadIdx.x; i < pairs; i += blockDim.x) {
       const int e = p.chosen[first * p.topk + i];
       const int token = static_cast<int>(i / p.topk);
-      p.slots[first * p.topk + i] = e < 0 ? -1 : __popcll(bits[e] & ((1ull << token) - 1));
+      p.slots[first * p.topk + i] = e < 0 ? -1 : __popc(bits[e] & ((1u << token) - 1));
     }
     return;
   }
   // One block has all tokens: the order at once.
   __shared__ int32_t base[kMaxExperts + 1];
-  for (int e = threadIdx.x; e < p.experts; e += blockDim.x) base[e] = __popcll(bits[e]);
+  for (int e = threadIdx.x; e < p.experts; e += blockDim.x) base[e] = __popc(bits[e]);
   __syncthreads();
   if (threadIdx.x < 32) exclusive_sums(base, p.experts);
   __syncthreads();
@@ -445,7 +488,7 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteParams p)
     const int e = p.chosen[i];
     const int token = static_cast<int>(i / p.topk);
     if (e >= 0) {
-      const int32_t slot = base[e] + __popcll(bits[e] & ((1ull << token) - 1));
+      const int32_t slot = base[e] + __popc(bits[e] & ((1u << token) - 1));
       p.slots[i] = slot;
       p.row_tokens[slot] = token;
     } else {
@@ -455,30 +498,44 @@ __global__ void __launch_bounds__(kRouteWarps * 32) k_route(const RouteParams p)
   }
 }
 
-// Adds what stands before a block to its pairs' ranks.  Every block sums the
-// counts of all blocks, four experts a word: with 16384 tokens 256 x 128 bytes
-// from L2, shared among eight warps.
-constexpr int kPlaceThreads = 256;
-constexpr int kPlaceWays = 8;
+// Adds what stands before a block of k_route to its pairs' ranks.  A block
+// here takes `group` of those in turn, at most 152 blocks in all: each of them
+// sums the counts of all (four experts a word, 16 warps), which costs 64 KB
+// from L2 with 16384 tokens and 128 experts.
+constexpr int kPlaceThreads = 512;
+constexpr int kPlaceBlocks = 152;
 
-__global__ void __launch_bounds__(kPlaceThreads) k_route_place(const RouteParams p) {
-  __shared__ int32_t base[kMaxExperts + 1];     // offsets, then with the rows before this block
-  __shared__ int32_t before[kMaxExperts];
+__global__ void __launch_bounds__(kPlaceThreads) k_route_place(const RouteParams p, int blocks,
+                                                               int group) {
+  __shared__ int32_t base[kMaxExperts + 1];  // offsets
+  __shared__ int32_t before[kMaxExperts];    // rows of earlier blocks
   for (int e = threadIdx.x; e < p.experts; e += kPlaceThreads) base[e] = before[e] = 0;
-  __syncthreads();
   const int lane = threadIdx.x & 31, way = threadIdx.x >> 5;
   const int words = count_stride(p.experts) / 4;
+  const int begin = blockIdx.x * group, end = min(begin + group, blocks);
   const uint32_t* counts = reinterpret_cast<const uint32_t*>(p.counts);
+  // this thread's first pair is under way meanwhile
+  const int64_t all_pairs = static_cast<int64_t>(p.tokens) * p.topk;
+  const int block_pairs = kRouteTokens * p.topk;
+  int expert = -1, rank = 0;
+  const auto fetch = [&](int b) {
+    const int64_t pair = static_cast<int64_t>(b) * block_pairs + threadIdx.x;
+    const bool some = b < end && static_cast<int>(threadIdx.x) < block_pairs && pair < all_pairs;
+    expert = some ? p.chosen[pair] : -1;
+    rank = some ? p.slots[pair] : 0;
+  };
+  fetch(begin);
+  __syncthreads();
   for (int w = lane; w < words; w += 32) {
     int32_t all[4] = {}, mine[4] = {};
-#pragma unroll 8
-    for (int b = way; b < gridDim.x; b += kPlaceWays) {
+#pragma unroll 16
+    for (int b = way; b < blocks; b += kPlaceThreads / 32) {
       const uint32_t n = counts[static_cast<int64_t>(b) * words + w];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const int32_t c = n >> (8 * i) & 0xFF;
         all[i] += c;
-        if (b < static_cast<int>(blockIdx.x)) mine[i] += c;
+        if (b < begin) mine[i] += c;
       }
     }
 #pragma unroll
@@ -493,18 +550,28 @@ __global__ void __launch_bounds__(kPlaceThreads) k_route_place(const RouteParams
   __syncthreads();
   if (blockIdx.x == 0)
     for (int e = threadIdx.x; e <= p.experts; e += kPlaceThreads) p.offsets[e] = base[e];
-  const int64_t first = static_cast<int64_t>(blockIdx.x) * kRouteTokens;
-  const int64_t pairs = min(static_cast<int64_t>(kRouteTokens), p.tokens - first) * p.topk;
   const int32_t used = base[p.experts];
-  for (int64_t i = threadIdx.x; i < pairs; i += kPlaceThreads) {
-    const int64_t pair = first * p.topk + i;
-    const int e = p.chosen[pair];
-    if (e >= 0) {
-      const int32_t slot = base[e] + before[e] + p.slots[pair];
-      p.slots[pair] = slot;
-      p.row_tokens[slot] = static_cast<int32_t>(first + i / p.topk);
-    }
-    if (pair >= used) p.row_tokens[pair] = -1;  // rows past the last group
+  for (int b = begin; b < end; ++b) {
+    const int64_t first = static_cast<int64_t>(b) * block_pairs;
+    const auto put = [&](int i, int e, int r) {
+      const int64_t pair = first + i;
+      if (e >= 0) {
+        const int32_t slot = base[e] + before[e] + r;
+        p.slots[pair] = slot;
+        p.row_tokens[slot] = b * kRouteTokens + i / p.topk;
+      }
+      if (pair >= used) p.row_tokens[pair] = -1;  // rows past the last group
+    };
+    const int pairs = static_cast<int>(min(static_cast<int64_t>(block_pairs), all_pairs - first));
+    if (static_cast<int>(threadIdx.x) < pairs) put(threadIdx.x, expert, rank);
+    for (int i = threadIdx.x + kPlaceThreads; i < pairs; i += kPlaceThreads)
+      put(i, p.chosen[first + i], p.slots[first + i]);
+    if (b + 1 == end) break;
+    fetch(b + 1);
+    __syncthreads();
+    for (int e = threadIdx.x; e < p.experts; e += kPlaceThreads)
+      before[e] += p.counts[static_cast<int64_t>(b) * words * 4 + e];
+    __syncthreads();
   }
 }
 
@@ -769,7 +836,7 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_backward(const CombineP
 
 template <int V>
 void route_at(const RouteParams& p, int blocks, cudaStream_t s) {
-  k_route<V><<<blocks, kRouteWarps * 32, 8 * p.experts, s>>>(p);
+  k_route<V><<<blocks, kRouteWarps * 32, 0, s>>>(p);
 }
 
 template <int V>
@@ -869,7 +936,10 @@ int launch_route(const RouteParams& p, void* stream) {
     route_at<8>(p, blocks, s);
   else
     route_at<32>(p, blocks, s);
-  if (blocks > 1) k_route_place<<<blocks, kPlaceThreads, 0, s>>>(p);
+  if (blocks > 1) {
+    const int group = (blocks + kPlaceBlocks - 1) / kPlaceBlocks;
+    k_route_place<<<(blocks + group - 1) / group, kPlaceThreads, 0, s>>>(p, blocks, group);
+  }
   return cudaGetLastError();
 }
 
