@@ -11,6 +11,9 @@
 // would waste up to 127, and the lanes of a warp hold neighbouring features of
 // one row, which they store contiguously without a transposition.
 //
+// The gated product's M are 64 gates and the 64 ups that go with them in turn,
+// so that neighbouring lanes hold the two halves of an output.
+//
 // A persistent block per SM: warp 0 moves tiles of 128 bytes by 64 or 128 rows
 // into a ring of stages with TMA (128-byte swizzle), four warps copy gathered
 // rows to the same places, one lane of warp 1 issues tcgen05.mma into one
@@ -28,7 +31,7 @@ namespace {
 constexpr int kStoreWarps = 8;
 constexpr int kGatherWarps = 4;
 constexpr int kTcThreads = 64 + 32 * kStoreWarps + 32 * kGatherWarps;
-constexpr int kTileM = 128;             // features of one accumulator
+constexpr int kTileM = 128;             // lanes of one accumulator: features, or gates and ups
 constexpr int kRowBytes = 128;          // bytes of the contraction per stage and row
 constexpr int kBoxRows = 64;            // rows of one B load
 constexpr int kMaxStages = 12;
@@ -82,6 +85,23 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
         "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+template <int kPair>
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                       int32_t z, int32_t u, uint32_t bar) {
+  if (kPair == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
         : "memory");
 }
 
@@ -314,8 +334,9 @@ struct OutTile {
 };
 
 // Walks this block's (or pair's) tiles in order.
-template <int kOp, int kPair>
+template <int kOp, int kPair, bool kFused>
 struct Walk {
+  static constexpr int kFeatures = kFused ? kTileM / 2 : kTileM;
   int index, group = 0;
   __device__ explicit Walk() : index(blockIdx.x / kPair) {}
   __device__ bool next(const TcParams& p, const Shared& sh, OutTile& t) {
@@ -325,8 +346,8 @@ struct Walk {
     const int local = index - sh.tile[group];
     const int m = sh.start[group + 1] - sh.start[group];
     t.group = group;
-    t.feature = local % p.m_tiles * (kTileM * kPair) +
-                (kPair == 2 ? static_cast<int>(cluster_rank()) * kTileM : 0);
+    t.feature = local % p.m_tiles * (kFeatures * kPair) +
+                (kPair == 2 ? static_cast<int>(cluster_rank()) * kFeatures : 0);
     const int at = local / p.m_tiles;
     if (kOp == kExpertDw) {
       t.row = at * p.tile_n;
@@ -368,12 +389,14 @@ __device__ __forceinline__ int32_t token_row(const ExpertParams& p, int32_t r, i
   return t >= 0 && t < p.x_rows ? t : -1;
 }
 
-// exp and the quotient to a few units in the last of 24 bits; the results are
-// rounded to 8.
+// exp and the reciprocal to a few units in the last of 24 bits; the results are
+// rounded to 8.  1 / inf is 0.
 __device__ __forceinline__ float sigmoid(float a) {
-  return __fdividef(1.0f, 1.0f + __expf(-a));
+  float s;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + __expf(-a)));
+  return s;
 }
-__device__ __forceinline__ float silu(float a) { return __fdividef(a, 1.0f + __expf(-a)); }
+__device__ __forceinline__ float silu(float a) { return a * sigmoid(a); }
 
 // ------------------------------------------------------------------------
 // Warps 0 and 11: loads of A and of B by TMA (one warp for both takes nearly
@@ -391,7 +414,7 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map, Shared& sh
   const bool gather = kOp == kExpertForward && kPair == 1 && p.e.row_tokens != nullptr;
   Place at;
   int issued = 0;
-  Walk<kOp, kPair> walk;
+  Walk<kOp, kPair, kFused> walk;
   OutTile t;
   bool alive = true;
   while (alive && walk.next(p, sh, t)) {
@@ -418,10 +441,10 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map, Shared& sh
         else if (kOp == kExpertDw)
           mbar_arrive_first(full);
         if (kOp == kExpertForward) {
-          tma_3d<kPair>(a, map, c, t.feature, t.group, bar);
           if (kFused)
-            tma_3d<kPair>(a + kTileM * kRowBytes, map, c, static_cast<int>(p.e.n) + t.feature,
-                          t.group, bar);
+            tma_4d<kPair>(a, map, c, 0, t.feature, t.group, bar);
+          else
+            tma_3d<kPair>(a, map, c, t.feature, t.group, bar);
         } else if (kOp == kExpertDx) {
           tma_3d<kPair>(a, map, t.feature, c, t.group, bar);
           tma_3d<kPair>(a + 64 * kRowBytes, map, t.feature + 64, c, t.group, bar);
@@ -460,7 +483,7 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map, Shared& sh
 // rows, 2048 to 2 x 1024: 412 us, against 333 us from rows gathered before;
 // TMA's own gather, four rows an instruction: 1222 us).
 
-template <bool kE4m3>
+template <bool kFused, bool kE4m3>
 __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
   constexpr int kDepth = kE4m3 ? 128 : 64;
   constexpr int kSize = kE4m3 ? 1 : 2;
@@ -471,7 +494,7 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
   const unsigned char* x = static_cast<const unsigned char*>(e.x);
   const int64_t stride = e.x_stride * kSize;
   Place at;
-  Walk<kExpertForward, 1> walk;
+  Walk<kExpertForward, 1, kFused> walk;
   OutTile t;
   bool alive = true;
   while (alive && walk.next(p, sh, t)) {
@@ -523,7 +546,7 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring) {
   const uint32_t tmem = sh.tmem;
   Place at;
   int tiles = 0;
-  Walk<kOp, kPair> walk;
+  Walk<kOp, kPair, kFused> walk;
   OutTile t;
   while (walk.next(p, sh, t)) {
     if (t.depth == 0) continue;
@@ -547,9 +570,6 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring) {
       for (int s = 0; s < kSteps; ++s) {
         if (kOp == kExpertDw && c + s * kStep >= t.depth) break;
         mma<kE4m3, kPair>(d, a + s * kStepA, b + s * kStepB, idesc, accumulate);
-        if (kFused)
-          mma<kE4m3, kPair>(d + kMaxN / 2, a + (kTileM * kRowBytes >> 4) + s * kStepA,
-                            b + s * kStepB, idesc, accumulate);
         accumulate = 1;
       }
       mma_commit<kPair>(&sh.empty[stage]);
@@ -574,7 +594,7 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
   const int lane = threadIdx.x & 31;
   int used = 0;
   uint32_t parity = 0;  // of each stage's barrier
-  Walk<kExpertDw, 2> walk;
+  Walk<kExpertDw, 2, false> walk;
   OutTile t;
   while (walk.next(p, sh, t)) {
     if (t.depth == 0) continue;
@@ -639,44 +659,84 @@ __device__ __forceinline__ float row_scale(const ExpertParams& e, int64_t r) {
   return e.x_scale[x];
 }
 
+// Eight rows of two features f and f + 1 (in one word) at p + j * stride, the
+// second feature only where `second`; words where rows start on 4-byte
+// boundaries.  Row j is row min(j, last).
+__device__ __forceinline__ void load_pairs(const uint16_t* p, int64_t stride, int last, bool wide,
+                                           bool second, uint32_t (&v)[kChunk / 2]) {
+  if (wide) {
+#pragma unroll
+    for (int j = 0; j < kChunk / 2; ++j)
+      v[j] = *reinterpret_cast<const uint32_t*>(p + min(j, last) * stride);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kChunk / 2; ++j) {
+      const uint16_t* at = p + min(j, last) * stride;
+      v[j] = at[0] | (second ? static_cast<uint32_t>(at[1]) << 16 : 0u);
+    }
+  }
+}
+
+__device__ __forceinline__ void store_pairs(uint16_t* p, int64_t stride, int rows, bool wide,
+                                            bool second, const uint32_t (&v)[kChunk / 2]) {
+  if (wide && rows >= kChunk / 2) {
+#pragma unroll
+    for (int j = 0; j < kChunk / 2; ++j) *reinterpret_cast<uint32_t*>(p + j * stride) = v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < kChunk / 2; ++j)
+      if (j < rows) {
+        p[j * stride] = static_cast<uint16_t>(v[j]);
+        if (second) p[j * stride + 1] = static_cast<uint16_t>(v[j] >> 16);
+      }
+  }
+}
+
 template <int kOp, bool kGated, bool kE4m3, int kPair>
 __device__ void store_tiles(const TcParams& p, Shared& sh) {
   constexpr bool kFused = kOp == kExpertForward && kGated;
   constexpr bool kReadsPre = kOp == kExpertDx && kGated;
+  constexpr int kHalf = kChunk / 2;
   const ExpertParams& e = p.e;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quadrant = warp & 3;
   const int half = (warp - 2) >> 2;
+  const bool odd = lane & 1;
   const int64_t features = kOp == kExpertForward ? e.n : e.k;
   uint16_t* y = static_cast<uint16_t*>(e.y);
+  const bool wide = kReadsPre && e.k % 2 == 0 &&
+                    ((reinterpret_cast<uintptr_t>(e.pre_in) | reinterpret_cast<uintptr_t>(y)) & 3) == 0;
   int tiles = 0;
-  Walk<kOp, kPair> walk;
+  Walk<kOp, kPair, kFused> walk;
   OutTile t;
   while (walk.next(p, sh, t)) {
-    const int64_t f = t.feature + quadrant * 32 + lane;
-    const bool mine = f < features;
-    const int64_t f_in = mine ? f : features - 1;  // for loads
+    // this thread's feature: of a gate (even lanes) or up (odd lanes) when they
+    // come in turn; the gated unit's gradient takes two lanes' features
+    // together, even lanes the first half of a chunk's rows, odd the second
+    const int64_t f = t.feature + (kFused     ? quadrant * 16 + (lane >> 1)
+                                   : kReadsPre ? quadrant * 32 + (lane & ~1)
+                                               : quadrant * 32 + lane);
+    const bool mine = f < features, second = f + 1 < features;
+    const int64_t f_in = mine ? f : wide ? features - 2 : features - 1;  // for loads
     const int buffer = tiles & 1;
     const bool zero = t.depth == 0;
     // What the outputs need besides the products is fetched before them: e4m3's
     // scales (lane i of row[q]: row 16 (2 q + half + 2 (i / 16)) + i % 16 of the
     // tile, that is this warp's chunks 2 q and 2 q + 1), and the first chunk
     // of the gated unit's inputs; each further chunk one chunk ahead.
-    float scale = 1.0f, scale_up = 1.0f, row[kMaxN / 64];
-    uint16_t gate_in[kChunk], up_in[kChunk];
+    float scale = 1.0f, row[kMaxN / 64];
+    uint32_t gate_in[kHalf], up_in[kHalf];
     const auto fetch_pre = [&](int c) {
-      const uint16_t* pre = e.pre_in + (static_cast<int64_t>(t.row) + c) * 2 * e.k + f_in;
-#pragma unroll
-      for (int j = 0; j < kChunk; ++j) {
-        const int64_t at = min(j, t.rows - c - 1) * 2 * e.k;
-        gate_in[j] = pre[at];
-        up_in[j] = pre[at + e.k];
-      }
+      // the last row stands in for rows behind the tile
+      const int first = min(c + (odd ? kHalf : 0), t.rows - 1);
+      const uint16_t* pre = e.pre_in + (static_cast<int64_t>(t.row) + first) * 2 * e.k + f_in;
+      const bool two = f_in + 1 < features;
+      load_pairs(pre, 2 * e.k, t.rows - 1 - first, wide, two, gate_in);
+      load_pairs(pre + e.k, 2 * e.k, t.rows - 1 - first, wide, two, up_in);
     };
     if (!zero) {
       if (kE4m3) {
         const float* ws = e.w_scale + static_cast<int64_t>(t.group) * (kFused ? 2 : 1) * e.n;
-        scale = ws[f_in];
-        if (kFused) scale_up = ws[f_in + e.n];
+        scale = ws[f_in + (kFused && odd ? e.n : 0)];
 #pragma unroll
         for (int q = 0; q < kMaxN / 64; ++q) {
           const int at = 64 * q + 32 * (lane >> 4) + 16 * half + (lane & 15);
@@ -694,13 +754,12 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
     for (int c = half * kChunk; c < t.rows; c += 2 * kChunk) {
       const int left = t.rows - c;
       const int64_t r = t.row + c;
-      float v[kChunk], up[kChunk];
+      float v[kChunk];
       if (zero) {
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) v[j] = up[j] = 0.0f;
+        for (int j = 0; j < kChunk; ++j) v[j] = 0.0f;
       } else {
         tmem_ld16(acc + c, v);
-        if (kFused) tmem_ld16(acc + kMaxN / 2 + c, up);
         tmem_ld_wait();
       }
       if (kE4m3 && !zero) {
@@ -709,42 +768,62 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
         for (int q = 1; q < kMaxN / 64; ++q)
           if (c >> 6 == q) mine_row = row[q];
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) {
-          const float xs = __shfl_sync(0xffffffffu, mine_row, (c >> 1 & 16) + j);
-          v[j] *= xs * scale;
-          if (kFused) up[j] *= xs * scale_up;
-        }
+        for (int j = 0; j < kChunk; ++j)
+          v[j] *= __shfl_sync(0xffffffffu, mine_row, (c >> 1 & 16) + j) * scale;
       }
       if (kFused) {
-        if (e.pre_out) {
-          uint16_t* pre = e.pre_out + r * 2 * e.n + f;
-          store_bf16(pre, 2 * e.n, v, left, mine);
-          store_bf16(pre + e.n, 2 * e.n, up, left, mine);
-        }
+        if (e.pre_out)
+          store_bf16(e.pre_out + r * 2 * e.n + (odd ? e.n : 0) + f, 2 * e.n, v, left, mine);
+        // even lanes get the ups of the first rows, odd lanes the gates of the last
+        float out[kHalf];
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) v[j] = silu(v[j]) * up[j];
-      }
-      if (kOp == kExpertForward) {
+        for (int j = 0; j < kHalf; ++j) {
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[kHalf + j], 1);
+          out[j] = silu(odd ? got : v[j]) * (odd ? v[kHalf + j] : got);
+        }
+        const int first = odd ? kHalf : 0;
+        uint16_t* to = y + (r + first) * e.n + f;
+        if (left >= kChunk) {
+          if (mine)
+#pragma unroll
+            for (int j = 0; j < kHalf; ++j) to[j * e.n] = f32_to_bf16(out[j]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < kHalf; ++j)
+            if (mine && first + j < left) to[j * e.n] = f32_to_bf16(out[j]);
+        }
+      } else if (kOp == kExpertForward) {
         store_bf16(y + r * e.n + f, e.n, v, left, mine);
-      } else if (kOp == kExpertDx && kGated) {
-        if (!zero) {
-          float gate[kChunk];
+      } else if (kReadsPre) {
+        uint32_t gate[kHalf], up[kHalf];
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            gate[j] = bf16_to_f32(gate_in[j]);
-            up[j] = bf16_to_f32(up_in[j]);
-          }
-          if (c + 2 * kChunk < t.rows) fetch_pre(c + 2 * kChunk);
-#pragma unroll
-          for (int j = 0; j < kChunk; ++j) {
-            const float g = gate[j], u = up[j];
-            const float s = sigmoid(g);
-            up[j] = v[j] * g * s;
-            v[j] = v[j] * u * s * (1.0f + g * (1.0f - s));
-          }
+        for (int j = 0; j < kHalf; ++j) {
+          gate[j] = gate_in[j];
+          up[j] = up_in[j];
         }
-        store_bf16(y + r * 2 * e.k + f, 2 * e.k, v, left, mine);
-        store_bf16(y + r * 2 * e.k + e.k + f, 2 * e.k, up, left, mine);
+        if (!zero && c + 2 * kChunk < t.rows) fetch_pre(c + 2 * kChunk);
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) {
+          const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[kHalf + j], 1);
+          const float d[2] = {odd ? got : v[j], odd ? v[kHalf + j] : got};
+          float dg[2], du[2];
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const float g = i ? bf16_hi(gate[j]) : bf16_lo(gate[j]);
+            const float u = i ? bf16_hi(up[j]) : bf16_lo(up[j]);
+            const float s = sigmoid(g), ds = d[i] * s;
+            du[i] = ds * g;
+            dg[i] = ds * u * (1.0f + g * (1.0f - s));
+          }
+          gate[j] = zero ? 0u : pack_bf16(dg[0], dg[1]);
+          up[j] = zero ? 0u : pack_bf16(du[0], du[1]);
+        }
+        const int first = odd ? kHalf : 0;
+        uint16_t* to = y + (r + first) * 2 * e.k + f;
+        if (mine) {
+          store_pairs(to, 2 * e.k, left - first, wide, second, gate);
+          store_pairs(to + e.k, 2 * e.k, left - first, wide, second, up);
+        }
       } else if (kOp == kExpertDx) {
         store_bf16(y + r * e.k + f, e.k, v, left, mine);
       } else {
@@ -752,11 +831,12 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
         if (e.f32_out) {
           float* out = static_cast<float*>(e.y) + at;
           if (e.accumulate) {
+            float old[kChunk];
 #pragma unroll
             for (int j = 0; j < kChunk; ++j)
-              up[j] = mine && j < left ? out[j * e.y_stride] : 0.0f;
+              old[j] = mine && j < left ? out[j * e.y_stride] : 0.0f;
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j) v[j] += up[j];
+            for (int j = 0; j < kChunk; ++j) v[j] += old[j];
           }
 #pragma unroll
           for (int j = 0; j < kChunk; ++j)
@@ -764,10 +844,11 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
         } else {
           uint16_t* out = y + at;
           if (e.accumulate) {
+            uint16_t old[kChunk];
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j) up_in[j] = mine && j < left ? out[j * e.y_stride] : 0;
+            for (int j = 0; j < kChunk; ++j) old[j] = mine && j < left ? out[j * e.y_stride] : 0;
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j) v[j] += bf16_to_f32(up_in[j]);
+            for (int j = 0; j < kChunk; ++j) v[j] += bf16_to_f32(old[j]);
           }
           store_bf16(out, e.y_stride, v, left, mine);
         }
@@ -843,7 +924,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   else if (warp == 2 + kStoreWarps && kOp == kExpertDw)
     clear_tails(p, sh, ring_ptr);
   else if (warp >= 2 + kStoreWarps && gather)
-    gather_tiles<kE4m3>(p, sh, ring);
+    gather_tiles<kGated, kE4m3>(p, sh, ring);
   else if (warp == 3 + kStoreWarps)
     load_tiles<kOp, kGated, kE4m3, kPair, false>(p, &map_b, sh, ring);
   tc_fence_before();
@@ -880,29 +961,35 @@ Encode encode() {
   return fn;
 }
 
-// A map of `planes` matrices of rows x columns; boxes of 128 bytes by box_rows.
+// A map of matrices of rows x columns, `planes` of them (0: one, without the
+// dimension); boxes of 128 bytes by box_rows.  With `parts` 2 a box's rows are
+// row i of the first part and row i of the second in turn, part_stride apart.
 bool make_map(CUtensorMap* map, const void* base, bool e4m3, int64_t columns, int64_t rows,
-              int64_t stride, int64_t planes, int64_t plane_stride, int box_rows) {
+              int64_t stride, int64_t planes, int64_t plane_stride, int box_rows, int parts = 1,
+              int64_t part_stride = 0) {
   const int64_t size = e4m3 ? 1 : 2;
   if ((reinterpret_cast<uintptr_t>(base) & 15) || stride * size % 16 ||
-      (planes > 1 && (plane_stride * size % 16 || plane_stride <= 0)) || columns < 1 || rows < 1 ||
-      planes < 1)
+      (planes > 1 && (plane_stride * size % 16 || plane_stride <= 0)) || columns < 1 || rows < 1)
     return false;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows),
-                              static_cast<cuuint64_t>(planes)};
-  const cuuint64_t strides[2] = {
-      static_cast<cuuint64_t>(stride * size),
-      static_cast<cuuint64_t>((planes > 1 ? plane_stride : stride * rows) * size)};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(kRowBytes / size),
-                             static_cast<cuuint32_t>(box_rows), 1};
-  const cuuint32_t ones[3] = {1, 1, 1};
+  cuuint64_t dims[4], strides[3];
+  cuuint32_t box[4];
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  int rank = 0;
+  const auto add = [&](int64_t n, int64_t apart, int64_t of_box) {
+    if (rank) strides[rank - 1] = static_cast<cuuint64_t>(apart * size);
+    dims[rank] = static_cast<cuuint64_t>(n);
+    box[rank++] = static_cast<cuuint32_t>(of_box);
+  };
+  add(columns, 0, kRowBytes / size);
+  if (parts == 2) add(2, part_stride, 2);
+  add(rows, stride, box_rows / parts);
+  if (planes > 0) add(planes, planes > 1 ? plane_stride : stride * rows * parts, 1);
   return encode()(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                  plane_stride < 0 ? 2 : 3, const_cast<void*>(base), dims, strides, box, ones,
+                  static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-constexpr int64_t kNoPlanes = -1;
 
 template <int kOp, bool kGated, bool kE4m3, int kPair>
 int launch_at(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid,
@@ -966,13 +1053,14 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   p.e = e;
   // Rows of a tile.  With few rows per expert on average the weights' bytes
   // bound the call: small row tiles leave room for more stages in flight.
-  p.tile_n = small ? kMaxSmallN : fused ? kMaxN / 2 : kMaxN;
-  p.a_bytes = (fused ? 2 : 1) * kTileM * kRowBytes;
+  p.tile_n = small ? kMaxSmallN : kMaxN;
+  p.a_bytes = kTileM * kRowBytes;
   const int pair = small || e.row_tokens ? 1 : 2;
   p.stage_bytes = p.a_bytes + p.tile_n / pair * kRowBytes;
   p.stages = (kSmemLimit - 14 * 1024) / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
-  const int64_t m_tiles = (features + kTileM * pair - 1) / (kTileM * pair);
+  const int64_t tile_m = (fused ? kTileM / 2 : kTileM) * pair;
+  const int64_t m_tiles = (features + tile_m - 1) / tile_m;
   const int64_t n_tiles = e.op == kExpertDw ? (e.n + p.tile_n - 1) / p.tile_n : 1;
   const int64_t row_tiles = e.op == kExpertDw ? n_tiles * e.experts
                                               : e.rows / 16 + e.experts + 1;  // at most
@@ -983,16 +1071,15 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   CUtensorMap a, b;
   bool ok;
   if (e.op == kExpertForward)
-    ok = make_map(&a, e.w, e.e4m3, e.k, fused ? 2 * e.n : e.n, e.w_stride, e.experts,
-                  e.w_expert_stride, kTileM) &&
-         make_map(&b, e.x, e.e4m3, e.k, e.x_rows, e.x_stride, 1, kNoPlanes,
-                  kBoxRows);
+    ok = make_map(&a, e.w, e.e4m3, e.k, e.n, e.w_stride, e.experts, e.w_expert_stride, kTileM,
+                  fused ? 2 : 1, e.n * e.w_stride) &&
+         make_map(&b, e.x, e.e4m3, e.k, e.x_rows, e.x_stride, 0, 0, kBoxRows);
   else if (e.op == kExpertDx)
     ok = make_map(&a, e.w, false, e.k, e.n, e.w_stride, e.experts, e.w_expert_stride, 64) &&
-         make_map(&b, e.x, false, e.n, e.x_rows, e.x_stride, 1, kNoPlanes, kBoxRows);
+         make_map(&b, e.x, false, e.n, e.x_rows, e.x_stride, 0, 0, kBoxRows);
   else
-    ok = make_map(&a, e.x, false, e.k, e.x_rows, e.x_stride, 1, kNoPlanes, 64) &&
-         make_map(&b, e.w, false, e.n, e.rows, e.w_stride, 1, kNoPlanes, 64);
+    ok = make_map(&a, e.x, false, e.k, e.x_rows, e.x_stride, 0, 0, 64) &&
+         make_map(&b, e.w, false, e.n, e.rows, e.w_stride, 0, 0, 64);
   if (!ok) return false;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
