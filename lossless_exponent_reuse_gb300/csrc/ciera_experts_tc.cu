@@ -17,7 +17,7 @@
 // A persistent block per SM: warp 0 moves tiles of 128 bytes by 64 or 128 rows
 // into a ring of stages with TMA (128-byte swizzle), four warps copy gathered
 // rows to the same places, one lane of warp 1 issues tcgen05.mma into one
-// of two accumulators in TMEM, warps 2 to 9 store the other accumulator.
+// of two accumulators in TMEM, eight or twelve store the other accumulator.
 // Tiles are dealt out round-robin over all groups; each block finds the
 // groups' tiles from the offsets by itself.
 #include <cuda.h>
@@ -28,9 +28,15 @@
 namespace ciera {
 namespace {
 
-constexpr int kStoreWarps = 8;
 constexpr int kGatherWarps = 4;
-constexpr int kTcThreads = 64 + 32 * kStoreWarps + 32 * kGatherWarps;
+// Warps: 0 loads A, 1 issues the products, then the storing warps, one that
+// loads B, and those that gather rows (single blocks) or clear (pairs).
+template <int kPair>
+struct Roles {
+  static constexpr int kStoreWarps = kPair == 2 ? 12 : 8;
+  static constexpr int kLoadB = 2 + kStoreWarps;
+  static constexpr int kThreads = 32 * (kLoadB + 1 + (kPair == 2 ? 1 : kGatherWarps));
+};
 constexpr int kTileM = 128;             // lanes of one accumulator: features, or gates and ups
 constexpr int kRowBytes = 128;          // bytes of the contraction per stage and row
 constexpr int kBoxRows = 64;            // rows of one B load
@@ -399,7 +405,7 @@ __device__ __forceinline__ float sigmoid(float a) {
 __device__ __forceinline__ float silu(float a) { return a * sigmoid(a); }
 
 // ------------------------------------------------------------------------
-// Warps 0 and 11: loads of A and of B by TMA (one warp for both takes nearly
+// Two warps: loads of A and of B by TMA (one warp for both takes nearly
 // as long to issue a stage's loads as the products take).  Gathered rows are
 // left to the gathering warps.  The bytes of both operands, and of both blocks
 // of a pair, are counted by the first block's barriers, where the products are
@@ -475,7 +481,7 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map, Shared& sh
 }
 
 // ------------------------------------------------------------------------
-// Warps 10 to 13: gathered rows, 16 bytes per thread and copy, written where
+// Four warps of a single block: gathered rows, 16 bytes per thread and copy, written where
 // the 128-byte swizzle has them.  A stage's barrier counts the threads whose
 // copies have landed; nobody waits for them but the products.  Right for small
 // groups, where it saves a launch; with large ones each row is fetched again
@@ -489,7 +495,7 @@ __device__ void gather_tiles(const TcParams& p, Shared& sh, uint32_t ring) {
   constexpr int kSize = kE4m3 ? 1 : 2;
   constexpr int kRows = kMaxN / 16;         // rows per thread and stage
   const ExpertParams& e = p.e;
-  const int tid = threadIdx.x - (kTcThreads - 32 * kGatherWarps);
+  const int tid = threadIdx.x - 32 * (Roles<1>::kLoadB + 1);
   const int piece = tid & 7, row0 = tid >> 3;  // 16 rows of 8 pieces a sweep
   const unsigned char* x = static_cast<const unsigned char*>(e.x);
   const int64_t stride = e.x_stride * kSize;
@@ -581,7 +587,7 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring) {
 }
 
 // ------------------------------------------------------------------------
-// Warp 10, dw: zeroes what a group's last stage holds behind the group's last
+// One warp, dw: zeroes what a group's last stage holds behind the group's last
 // row, up to the next whole step: rows of the next group, or stale ones.  Both
 // operands, since 0 times an infinity there would be a NaN.  The stage lands
 // long before its products are due, so that they do not wait for this (420 us
@@ -621,10 +627,10 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
 }
 
 // ------------------------------------------------------------------------
-// Warps 2 to 9: outputs.  A thread holds one feature of 16 rows at a time;
-// the 32 lanes of a warp store 32 neighbouring features of a row.  Two warps
-// share a quarter of the features (a warp can read only the TMEM lanes of its
-// number modulo 4) and take alternate chunks of rows.
+// Storing warps.  A thread holds one feature of 16 rows at a time; the 32 lanes
+// of a warp store 32 neighbouring features of a row.  Two or three warps share
+// a quarter of the features (a warp can read only the TMEM lanes of its number
+// modulo 4) and take chunks of rows in turn.
 //
 // Nothing in a chunk branches on a row: loads come from the last row where a
 // row lies behind the tile, so that sixteen independent rows hide each
@@ -645,6 +651,20 @@ __device__ __forceinline__ void store_bf16(uint16_t* out, int64_t stride, const 
   } else {
 #pragma unroll
     for (int j = 0; j < kChunk; ++j)
+      if (mine && j < left) out[j * stride] = f32_to_bf16(v[j]);
+  }
+}
+
+// The same for half a chunk, `left` of whose rows are the tile's.
+__device__ __forceinline__ void store_half(uint16_t* out, int64_t stride, const float* v, int left,
+                                           bool mine) {
+  if (left >= kChunk / 2) {
+    if (mine)
+#pragma unroll
+      for (int j = 0; j < kChunk / 2; ++j) out[j * stride] = f32_to_bf16(v[j]);
+  } else {
+#pragma unroll
+    for (int j = 0; j < kChunk / 2; ++j)
       if (mine && j < left) out[j * stride] = f32_to_bf16(v[j]);
   }
 }
@@ -699,7 +719,10 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
   constexpr int kHalf = kChunk / 2;
   const ExpertParams& e = p.e;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quadrant = warp & 3;
-  const int half = (warp - 2) >> 2;
+  constexpr int kTurns = Roles<kPair>::kStoreWarps / 4;  // warps of a quarter
+  constexpr int kStride = kTurns * kChunk;        // rows from chunk to chunk
+  constexpr int kScales = (kMaxN / kChunk + 2 * kTurns - 1) / (2 * kTurns);
+  const int first_row = ((warp - 2) >> 2) * kChunk;
   const bool odd = lane & 1;
   const int64_t features = kOp == kExpertForward ? e.n : e.k;
   uint16_t* y = static_cast<uint16_t*>(e.y);
@@ -720,10 +743,10 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
     const int buffer = tiles & 1;
     const bool zero = t.depth == 0;
     // What the outputs need besides the products is fetched before them: e4m3's
-    // scales (lane i of row[q]: row 16 (2 q + half + 2 (i / 16)) + i % 16 of the
-    // tile, that is this warp's chunks 2 q and 2 q + 1), and the first chunk
+    // scales (lanes 0 to 15 of row[q]: the rows of this warp's chunk 2 q, lanes
+    // 16 to 31 those of chunk 2 q + 1), and the first chunk
     // of the gated unit's inputs; each further chunk one chunk ahead.
-    float scale = 1.0f, row[kMaxN / 64];
+    float scale = 1.0f, scale_up = 1.0f, row[kScales];
     uint32_t gate_in[kHalf], up_in[kHalf];
     const auto fetch_pre = [&](int c) {
       // the last row stands in for rows behind the tile
@@ -736,14 +759,15 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
     if (!zero) {
       if (kE4m3) {
         const float* ws = e.w_scale + static_cast<int64_t>(t.group) * (kFused ? 2 : 1) * e.n;
-        scale = ws[f_in + (kFused && odd ? e.n : 0)];
+        scale = ws[f_in];
+        if (kFused) scale_up = ws[f_in + e.n];
 #pragma unroll
-        for (int q = 0; q < kMaxN / 64; ++q) {
-          const int at = 64 * q + 32 * (lane >> 4) + 16 * half + (lane & 15);
+        for (int q = 0; q < kScales; ++q) {
+          const int at = first_row + (2 * q + (lane >> 4)) * kStride + (lane & 15);
           row[q] = at < t.rows ? row_scale(e, static_cast<int64_t>(t.row) + at) : 0.0f;
         }
       }
-      if (kReadsPre && half * kChunk < t.rows) fetch_pre(half * kChunk);
+      if (kReadsPre && first_row < t.rows) fetch_pre(first_row);
       if (!wait(p, sh, &sh.acc_full[buffer], (tiles >> 1) & 1)) return;
       tc_fence_after();
       ++tiles;
@@ -751,7 +775,7 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
     const uint32_t acc =
         sh.tmem + buffer * kMaxN + (static_cast<uint32_t>(quadrant * 32) << 16);
 #pragma unroll 1
-    for (int c = half * kChunk; c < t.rows; c += 2 * kChunk) {
+    for (int c = first_row, chunk = 0; c < t.rows; c += kStride, ++chunk) {
       const int left = t.rows - c;
       const int64_t r = t.row + c;
       float v[kChunk];
@@ -762,36 +786,43 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
         tmem_ld16(acc + c, v);
         tmem_ld_wait();
       }
+      // e4m3: this chunk's row scales, row j's in lane from + j
+      float scales = 1.0f;
+      const int from = (chunk & 1) * kChunk;
       if (kE4m3 && !zero) {
-        float mine_row = row[0];
+        scales = row[0];
 #pragma unroll
-        for (int q = 1; q < kMaxN / 64; ++q)
-          if (c >> 6 == q) mine_row = row[q];
+        for (int q = 1; q < kScales; ++q)
+          if (chunk >> 1 == q) scales = row[q];
+      }
+      if (kE4m3 && !kFused && !zero) {
 #pragma unroll
         for (int j = 0; j < kChunk; ++j)
-          v[j] *= __shfl_sync(0xffffffffu, mine_row, (c >> 1 & 16) + j) * scale;
+          v[j] *= __shfl_sync(0xffffffffu, scales, from + j) * scale;
       }
       if (kFused) {
-        if (e.pre_out)
-          store_bf16(e.pre_out + r * 2 * e.n + (odd ? e.n : 0) + f, 2 * e.n, v, left, mine);
         // even lanes get the ups of the first rows, odd lanes the gates of the last
-        float out[kHalf];
+        const int first = odd ? kHalf : 0;
+        float gate[kHalf], up[kHalf];
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) {
           const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[kHalf + j], 1);
-          out[j] = silu(odd ? got : v[j]) * (odd ? v[kHalf + j] : got);
+          gate[j] = odd ? got : v[j];
+          up[j] = odd ? v[kHalf + j] : got;
+          if (kE4m3) {
+            const float xs = __shfl_sync(0xffffffffu, scales, from + first + j);
+            gate[j] *= xs * scale;
+            up[j] *= xs * scale_up;
+          }
         }
-        const int first = odd ? kHalf : 0;
-        uint16_t* to = y + (r + first) * e.n + f;
-        if (left >= kChunk) {
-          if (mine)
-#pragma unroll
-            for (int j = 0; j < kHalf; ++j) to[j * e.n] = f32_to_bf16(out[j]);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kHalf; ++j)
-            if (mine && first + j < left) to[j * e.n] = f32_to_bf16(out[j]);
+        if (e.pre_out) {
+          uint16_t* pre = e.pre_out + (r + first) * 2 * e.n + f;
+          store_half(pre, 2 * e.n, gate, left - first, mine);
+          store_half(pre + e.n, 2 * e.n, up, left - first, mine);
         }
+#pragma unroll
+        for (int j = 0; j < kHalf; ++j) gate[j] = silu(gate[j]) * up[j];
+        store_half(y + (r + first) * e.n + f, e.n, gate, left - first, mine);
       } else if (kOp == kExpertForward) {
         store_bf16(y + r * e.n + f, e.n, v, left, mine);
       } else if (kReadsPre) {
@@ -801,7 +832,7 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
           gate[j] = gate_in[j];
           up[j] = up_in[j];
         }
-        if (!zero && c + 2 * kChunk < t.rows) fetch_pre(c + 2 * kChunk);
+        if (!zero && c + kStride < t.rows) fetch_pre(c + kStride);
 #pragma unroll
         for (int j = 0; j < kHalf; ++j) {
           const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[kHalf + j], 1);
@@ -869,7 +900,7 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
 }
 
 template <int kOp, bool kGated, bool kE4m3, int kPair>
-__global__ void __launch_bounds__(kTcThreads, 1)
+__global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
     k_expert_tc(const TcParams p, const __grid_constant__ CUtensorMap map_a,
                 const __grid_constant__ CUtensorMap map_b) {
   extern __shared__ unsigned char raw[];
@@ -878,6 +909,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t base = smem_addr(raw);
   const uint32_t ring = (base + 1023) & ~1023u;
   unsigned char* ring_ptr = raw + (ring - base);
+  constexpr int kLoadB = Roles<kPair>::kLoadB;
   const int warp = threadIdx.x >> 5;
   const bool gather = kOp == kExpertForward && kPair == 1 && p.e.row_tokens != nullptr;
   if (threadIdx.x == 0) {
@@ -889,7 +921,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 1);
-      mbar_init(&sh.acc_empty[i], kStoreWarps * kPair);
+      mbar_init(&sh.acc_empty[i], Roles<kPair>::kStoreWarps * kPair);
     }
     sh.stop = 0;
     fence_barrier_init();
@@ -919,14 +951,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     load_tiles<kOp, kGated, kE4m3, kPair, true>(p, &map_a, sh, ring);
   else if (warp == 1 && (kPair == 1 || cluster_rank() == 0))
     multiply<kOp, kGated, kE4m3, kPair>(p, sh, ring);
-  else if (warp >= 2 && warp < 2 + kStoreWarps)
+  else if (warp >= 2 && warp < kLoadB)
     store_tiles<kOp, kGated, kE4m3, kPair>(p, sh);
-  else if (warp == 2 + kStoreWarps && kOp == kExpertDw)
-    clear_tails(p, sh, ring_ptr);
-  else if (warp >= 2 + kStoreWarps && gather)
-    gather_tiles<kGated, kE4m3>(p, sh, ring);
-  else if (warp == 3 + kStoreWarps)
+  else if (warp == kLoadB && !gather)
     load_tiles<kOp, kGated, kE4m3, kPair, false>(p, &map_b, sh, ring);
+  else if (warp > kLoadB && kOp == kExpertDw)
+    clear_tails(p, sh, ring_ptr);
+  else if (warp > kLoadB && gather)
+    gather_tiles<kGated, kE4m3>(p, sh, ring);
   tc_fence_before();
   __syncthreads();
   sync_all<kPair>();
@@ -1000,7 +1032,7 @@ int launch_at(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int
   if (ready != cudaSuccess) return ready;
   cudaLaunchConfig_t config{};
   config.gridDim = dim3(static_cast<unsigned>(grid));
-  config.blockDim = dim3(kTcThreads);
+  config.blockDim = dim3(Roles<kPair>::kThreads);
   config.dynamicSmemBytes = static_cast<size_t>(p.stages) * p.stage_bytes + 1024;
   config.stream = s;
   cudaLaunchAttribute pair{};
