@@ -618,9 +618,11 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
       for (int i = lane; i < words; i += 32)
         *reinterpret_cast<uint4*>(base + column * 64 * kRowBytes + have * kRowBytes + i * 16) =
             make_uint4(0, 0, 0, 0);
+    // each lane's zeros are in shared memory, for this block's tensor core, before
+    // the first block hears of it; nothing else is handed over (a fence over
+    // the cluster would wait for the storing warps' writes too: 427 instead of
+    // 396 us for the gradient of 2 x 1024 x 2048 weights from 64225 rows)
     fence_proxy_async_smem();
-    // the other block's tensor core reads this block's operands on the first's order
-    asm volatile("fence.acq_rel.cluster;" ::: "memory");
     __syncwarp();
     if (lane == 0) mbar_arrive_first(&sh.full[stage]);
   }
