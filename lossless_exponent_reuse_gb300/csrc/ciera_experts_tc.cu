@@ -52,6 +52,7 @@ struct TcParams {
   int32_t stage_bytes;   // A then B
   int32_t a_bytes;
   int32_t m_tiles;       // tiles of the feature dimension
+  uint32_t m_tiles_inverse;  // 2^32 / m_tiles, rounded up (of 2 and more)
   int32_t n_tiles;       // dw: tiles of its rows
 };
 
@@ -339,31 +340,40 @@ struct OutTile {
   int depth;     // length of the contraction; 0: the tile is zeros
 };
 
-// Walks this block's (or pair's) tiles in order.
+// Walks this block's (or pair's) tiles in order.  Every role does so by itself,
+// between two tiles: what belongs to a group is kept while the group lasts,
+// and the division by m_tiles is a multiplication.
 template <int kOp, int kPair, bool kFused>
 struct Walk {
   static constexpr int kFeatures = kFused ? kTileM / 2 : kTileM;
-  int index, group = 0;
+  int index, group = -1, end = 0;   // tiles before the group's end
+  int begin = 0, first = 0, rows = 0, per = 0;
   __device__ explicit Walk() : index(blockIdx.x / kPair) {}
   __device__ bool next(const TcParams& p, const Shared& sh, OutTile& t) {
     const int E = p.e.experts;
-    if (index >= sh.tile[E + 1]) return false;
-    while (index >= sh.tile[group + 1]) ++group;
-    const int local = index - sh.tile[group];
-    const int m = sh.start[group + 1] - sh.start[group];
+    if (index >= end) {
+      if (index >= sh.tile[E + 1]) return false;
+      while (index >= end) end = sh.tile[++group + 1];
+      begin = sh.tile[group];
+      first = sh.start[group];
+      rows = sh.start[group + 1] - first;
+      per = kOp == kExpertDw ? p.tile_n : rows_per_tile<kPair>(rows, p.tile_n);
+    }
+    const int local = index - begin;
+    // local / m_tiles; the product is that or one more
+    int at = p.m_tiles == 1 ? local : static_cast<int>(__umulhi(local, p.m_tiles_inverse));
+    if (at * p.m_tiles > local) --at;
     t.group = group;
-    t.feature = local % p.m_tiles * (kFeatures * kPair) +
+    t.feature = (local - at * p.m_tiles) * (kFeatures * kPair) +
                 (kPair == 2 ? static_cast<int>(cluster_rank()) * kFeatures : 0);
-    const int at = local / p.m_tiles;
     if (kOp == kExpertDw) {
-      t.row = at * p.tile_n;
-      t.rows = min(p.tile_n, static_cast<int>(p.e.n) - t.row);
-      t.from = sh.start[group];
-      t.depth = m;
+      t.row = at * per;
+      t.rows = min(per, static_cast<int>(p.e.n) - t.row);
+      t.from = first;
+      t.depth = rows;
     } else {
-      const int per = rows_per_tile<kPair>(m, p.tile_n);
-      t.row = sh.start[group] + at * per;
-      t.rows = min(per, m - at * per);
+      t.row = first + at * per;
+      t.rows = min(per, rows - at * per);
       t.from = 0;
       t.depth = group == E ? 0 : static_cast<int>(kOp == kExpertForward ? p.e.k : p.e.n);
     }
@@ -1100,6 +1110,7 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
                                               : e.rows / 16 + e.experts + 1;  // at most
   if (m_tiles * row_tiles > (int64_t(1) << 30)) return false;
   p.m_tiles = static_cast<int32_t>(m_tiles);
+  p.m_tiles_inverse = static_cast<uint32_t>(((uint64_t(1) << 32) + m_tiles - 1) / m_tiles);
   p.n_tiles = static_cast<int32_t>(n_tiles);
 
   CUtensorMap a, b;
