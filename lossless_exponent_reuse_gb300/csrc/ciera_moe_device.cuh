@@ -96,6 +96,49 @@ __device__ __forceinline__ uint32_t pack_e4m3(float a, float b, float c, float d
   return lo | hi << 16;
 }
 
+// Words of 8, 2 or 1 bf16 values, for rows that start on 16-, 4- or 2-byte
+// boundaries; a Half holds as many e4m3 values.
+template <typename W>
+struct Word;
+template <>
+struct Word<uint4> {
+  static constexpr int kValues = 8;
+  using Half = uint2;
+  static __device__ __forceinline__ void unpack(const uint4& v, float (&f)[8]) { unpack8(v, f); }
+  static __device__ __forceinline__ uint4 pack(const float (&f)[8]) { return pack8(f); }
+  static __device__ __forceinline__ uint2 pack_8bit(const float (&f)[8], float by) {
+    return make_uint2(pack_e4m3(f[0] * by, f[1] * by, f[2] * by, f[3] * by),
+                      pack_e4m3(f[4] * by, f[5] * by, f[6] * by, f[7] * by));
+  }
+};
+template <>
+struct Word<uint32_t> {
+  static constexpr int kValues = 2;
+  using Half = uint16_t;
+  static __device__ __forceinline__ void unpack(uint32_t v, float (&f)[2]) {
+    f[0] = bf16_lo(v);
+    f[1] = bf16_hi(v);
+  }
+  static __device__ __forceinline__ uint32_t pack(const float (&f)[2]) {
+    return pack_bf16(f[0], f[1]);
+  }
+  static __device__ __forceinline__ uint16_t pack_8bit(const float (&f)[2], float by) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(f[0] * by, f[1] * by), __NV_SATFINITE, __NV_E4M3);
+  }
+};
+template <>
+struct Word<uint16_t> {
+  static constexpr int kValues = 1;
+  using Half = uint8_t;
+  static __device__ __forceinline__ void unpack(uint16_t v, float (&f)[1]) {
+    f[0] = bf16_to_f32(v);
+  }
+  static __device__ __forceinline__ uint16_t pack(const float (&f)[1]) { return f32_to_bf16(f[0]); }
+  static __device__ __forceinline__ uint8_t pack_8bit(const float (&f)[1], float by) {
+    return f32_to_e4m3(f[0] * by);
+  }
+};
+
 // Offset of group e, clamped to [lo, rows]; `lo` is the one before it.
 __device__ __forceinline__ int32_t clamp_offset(int32_t v, int32_t lo, int32_t rows) {
   return v < lo ? lo : v > rows ? rows : v;

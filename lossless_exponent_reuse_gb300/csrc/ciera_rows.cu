@@ -2,23 +2,26 @@
 // the norm with the residual's addition and its gradient, rows to e4m3, the
 // router's choice with the expert order, and the combination of the experts'
 // rows.
+#include <initializer_list>
+
 #include "ciera_moe_device.cuh"
 
 namespace ciera {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int64_t kManyRows = 2048;    // enough to fill the SMs with half the threads a row
 constexpr int kMostRowThreads = 512;  // for one row of the kernels that hold rows in registers
 
 // ------------------------------------------------------------------------
 // Norm.  Bound by memory: 8 bytes a value in bf16 with a residual, 7 in e4m3.
 //
-// k_rmsnorm holds a row in registers, kVecs words of 8 values per thread, so
-// that it is read once; blockDim.x threads take a row (whole warps, one
-// reduction per statistic), blockDim.y rows share a block where rows are
-// short.  It wants rows of a multiple of 8 values on 16-byte boundaries.
-// k_rmsnorm_any takes every size and alignment, value by value, and reads a
-// row once per statistic (from L1 or L2 after the first).
+// k_rmsnorm holds a row in registers, kVecs words per thread, so that it is
+// read once; blockDim.x threads take a row (whole warps, one reduction per
+// statistic), blockDim.y rows share a block where rows are short.  Words are
+// 16 bytes where all rows start on 16-byte boundaries, else 4 or 2.
+// k_rmsnorm_any takes rows of any length, value by value, and reads a row once
+// per statistic (from L1 or L2 after the first).
 
 __device__ __forceinline__ float norm_input(const NormParams& p, int64_t r, int64_t c) {
   float s = bf16_to_f32(p.x[r * p.x_stride + c]);
@@ -90,30 +93,31 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*part)[32]) {
   return __reduce_max_sync(0xffffffffu, v);
 }
 
-template <int kVecs, bool kE4m3>
+template <typename W, int kVecs, bool kE4m3>
 __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p) {
   __shared__ float part[8][32];
   __shared__ uint32_t part_max[8][32];
   const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
   const bool row = r < p.rows;
-  const int words = static_cast<int>(p.dim / 8);
-  float s[kVecs][8];
-  uint4 weight[kVecs] = {};
+  constexpr int kN = Word<W>::kValues;
+  const int words = static_cast<int>(p.dim / kN);
+  float s[kVecs][kN];
+  W weight[kVecs] = {};
   float sum = 0.0f;
 #pragma unroll
   for (int v = 0; v < kVecs; ++v) {
     const int i = v * blockDim.x + threadIdx.x;
-    uint4 x{}, add{};
+    W x{}, add{};
     if (row && i < words) {
-      x = reinterpret_cast<const uint4*>(p.x + r * p.x_stride)[i];
-      if (p.residual) add = reinterpret_cast<const uint4*>(p.residual + r * p.residual_stride)[i];
-      if (p.weight) weight[v] = reinterpret_cast<const uint4*>(p.weight)[i];
+      x = reinterpret_cast<const W*>(p.x + r * p.x_stride)[i];
+      if (p.residual) add = reinterpret_cast<const W*>(p.residual + r * p.residual_stride)[i];
+      if (p.weight) weight[v] = reinterpret_cast<const W*>(p.weight)[i];
     }
-    float f[8];
-    unpack8(x, s[v]);
-    unpack8(add, f);
+    float f[kN];
+    Word<W>::unpack(x, s[v]);
+    Word<W>::unpack(add, f);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < kN; ++j) {
       if (p.residual) s[v][j] += f[j];
       sum += s[v][j] * s[v][j];
     }
@@ -122,7 +126,7 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p)
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const int i = v * blockDim.x + threadIdx.x;
-      if (row && i < words) reinterpret_cast<uint4*>(p.h + r * p.dim)[i] = pack8(s[v]);
+      if (row && i < words) reinterpret_cast<W*>(p.h + r * p.dim)[i] = Word<W>::pack(s[v]);
     }
   }
   if (p.weight) {
@@ -131,10 +135,10 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p)
     if (p.rstd && row && threadIdx.x == 0) p.rstd[r] = rstd;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-      float w[8];
-      unpack8(weight[v], w);
+      float w[kN];
+      Word<W>::unpack(weight[v], w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) s[v][j] = s[v][j] * rstd * w[j];
+      for (int j = 0; j < kN; ++j) s[v][j] = s[v][j] * rstd * w[j];
     }
   }
   float inverse = 1.0f;
@@ -143,7 +147,7 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p)
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
+      for (int j = 0; j < kN; ++j)
         if (v * blockDim.x + threadIdx.x < words)  // behind the row a NaN may stand
           amax = max(amax, __float_as_uint(s[v][j]) & 0x7FFFFFFFu);
     const float scale = e4m3_scale(row_max(amax, part_max));
@@ -155,13 +159,10 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p)
     const int i = v * blockDim.x + threadIdx.x;
     if (!row || i >= words) continue;
     if (kE4m3) {
-      float (&f)[8] = s[v];
-      const uint2 q = make_uint2(
-          pack_e4m3(f[0] * inverse, f[1] * inverse, f[2] * inverse, f[3] * inverse),
-          pack_e4m3(f[4] * inverse, f[5] * inverse, f[6] * inverse, f[7] * inverse));
-      reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + r * p.dim)[i] = q;
+      reinterpret_cast<typename Word<W>::Half*>(static_cast<uint8_t*>(p.y) + r * p.dim)[i] =
+          Word<W>::pack_8bit(s[v], inverse);
     } else {
-      reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.y) + r * p.dim)[i] = pack8(s[v]);
+      reinterpret_cast<W*>(static_cast<uint16_t*>(p.y) + r * p.dim)[i] = Word<W>::pack(s[v]);
     }
   }
 }
@@ -196,51 +197,53 @@ __global__ void __launch_bounds__(kRowThreads) k_rmsnorm_backward_any(const Norm
 // The same with a row in registers and the weight's gradient too, the next
 // row's words under way while this one is reduced.  Bound by memory, 8 bytes a
 // value.
-template <int kVecs>
-__global__ void __launch_bounds__(kMostRowThreads, kVecs == 1 ? 2 : 1) k_rmsnorm_backward(const NormBackwardParams p) {
+template <typename W, int kVecs>
+__global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8 ? 2 : 1)
+    k_rmsnorm_backward(const NormBackwardParams p) {
   __shared__ float part[2][8][32];
-  const int words = static_cast<int>(p.dim / 8);
+  constexpr int kN = Word<W>::kValues;
+  const int words = static_cast<int>(p.dim / kN);
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
   const float inverse_dim = 1.0f / static_cast<float>(p.dim);
-  float dw[kVecs][8] = {};
-  uint4 weight[kVecs], dy[kVecs], h[kVecs], dh[kVecs];
+  float dw[kVecs][kN] = {};
+  W weight[kVecs], dy[kVecs], h[kVecs], dh[kVecs];
   float rstd = 0.0f;
   const auto fetch = [&](int64_t r) {
     const bool row = r < p.rows;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       const int i = v * blockDim.x + threadIdx.x;
-      dy[v] = h[v] = dh[v] = make_uint4(0, 0, 0, 0);
+      dy[v] = h[v] = dh[v] = W{};
       if (!row || i >= words) continue;
-      dy[v] = reinterpret_cast<const uint4*>(p.dy + r * p.dy_stride)[i];
-      h[v] = reinterpret_cast<const uint4*>(p.h + r * p.h_stride)[i];
-      if (p.dh) dh[v] = reinterpret_cast<const uint4*>(p.dh + r * p.dh_stride)[i];
+      dy[v] = reinterpret_cast<const W*>(p.dy + r * p.dy_stride)[i];
+      h[v] = reinterpret_cast<const W*>(p.h + r * p.h_stride)[i];
+      if (p.dh) dh[v] = reinterpret_cast<const W*>(p.dh + r * p.dh_stride)[i];
     }
     rstd = row ? p.rstd[r] : 0.0f;
   };
 #pragma unroll
   for (int v = 0; v < kVecs; ++v) {
     const int i = v * blockDim.x + threadIdx.x;
-    weight[v] = i < words ? reinterpret_cast<const uint4*>(p.weight)[i] : make_uint4(0, 0, 0, 0);
+    weight[v] = i < words ? reinterpret_cast<const W*>(p.weight)[i] : W{};
   }
   fetch(static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y);
   int turn = 0;  // two reductions' scratch in turn: one barrier each
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step) {
     const int64_t r = r0 + threadIdx.y;
     // with n = h rstd:  dx = rstd (g - n mean(g n)) + dh,  dweight += dy n
-    float g[kVecs][8], n[kVecs][8];
-    uint4 more[kVecs];
+    float g[kVecs][kN], n[kVecs][kN];
+    W more[kVecs];
     float dot = 0.0f;
     const float rs = rstd;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-      float d[8], w[8];
-      unpack8(dy[v], d);
-      unpack8(h[v], n[v]);
-      unpack8(weight[v], w);
+      float d[kN], w[kN];
+      Word<W>::unpack(dy[v], d);
+      Word<W>::unpack(h[v], n[v]);
+      Word<W>::unpack(weight[v], w);
       more[v] = dh[v];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
+      for (int j = 0; j < kN; ++j) {
         n[v][j] *= rs;
         g[v][j] = d[j] * w[j];
         dot += g[v][j] * n[v][j];
@@ -255,11 +258,11 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs == 1 ? 2 : 1) k_rmsnorm
     for (int v = 0; v < kVecs; ++v) {
       const int i = v * blockDim.x + threadIdx.x;
       if (r >= p.rows || i >= words) continue;
-      float out[8];
-      unpack8(more[v], out);
+      float out[kN];
+      Word<W>::unpack(more[v], out);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) out[j] += rs * (g[v][j] - n[v][j] * mean);
-      reinterpret_cast<uint4*>(p.dx + r * p.dim)[i] = pack8(out);
+      for (int j = 0; j < kN; ++j) out[j] += rs * (g[v][j] - n[v][j] * mean);
+      reinterpret_cast<W*>(p.dx + r * p.dim)[i] = Word<W>::pack(out);
     }
   }
   // this block's part of the weight's gradient, its rows' in order
@@ -272,12 +275,12 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs == 1 ? 2 : 1) k_rmsnorm
         const int i = v * blockDim.x + threadIdx.x;
         if (i >= words) continue;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float before = turn_y ? column[i * 8 + j] : 0.0f;
+        for (int j = 0; j < kN; ++j) {
+          const float before = turn_y ? column[i * kN + j] : 0.0f;
           if (turn_y + 1 == blockDim.y)
-            mine[i * 8 + j] = before + dw[v][j];
+            mine[i * kN + j] = before + dw[v][j];
           else
-            column[i * 8 + j] = before + dw[v][j];
+            column[i * kN + j] = before + dw[v][j];
         }
       }
     }
@@ -852,21 +855,31 @@ namespace {
 
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// A row of 16-byte words: words per thread, threads per row, rows per block.
-// One word per thread as far as 512 threads reach, then two and four; short
-// rows share a block of 256 threads.
+// Widest words that a call's rows and buffers allow: 8, 2 or 1 values.
+int word_values(int64_t dim, std::initializer_list<const void*> at,
+                std::initializer_list<int64_t> strides) {
+  uintptr_t bytes = static_cast<uintptr_t>(2 * dim);
+  for (const void* p : at) bytes |= reinterpret_cast<uintptr_t>(p);  // null counts as aligned
+  for (int64_t s : strides) bytes |= static_cast<uintptr_t>(2 * s);
+  return bytes % 16 == 0 ? 8 : bytes % 4 == 0 ? 2 : 1;
+}
+
+// Words per thread, threads per row, rows per block.  Eight values per thread
+// as far as 512 threads reach (with one matrix read and many rows 16, so that
+// as many bytes are under way), then 16 and 32; rows of few threads share a
+// block of 256.
 struct RowShape {
-  int vecs;  // 0: the row does not fit
+  int values;  // of a thread; 0: the row does not fit
   dim3 block;
 };
 
-RowShape row_shape(int64_t dim) {
-  const int64_t words = dim / 8;
+RowShape row_shape(int64_t dim, int word, int at_first) {
   RowShape s{};
-  for (int vecs = 1; vecs <= 4; vecs *= 2) {
+  for (int values = at_first; values <= (word == 8 ? 32 : 16); values *= 2) {
+    const int64_t words = dim / word, vecs = values / word;
     const int64_t threads = (words + 32 * vecs - 1) / (32 * vecs) * 32;
     if (threads > kMostRowThreads) continue;
-    s.vecs = vecs;
+    s.values = values;
     const unsigned rows = threads <= 128 ? 256 / static_cast<unsigned>(threads) : 1;
     s.block = dim3(static_cast<unsigned>(threads), rows);
     break;
@@ -874,52 +887,61 @@ RowShape row_shape(int64_t dim) {
   return s;
 }
 
-template <int kVecs>
+template <typename W, int kVecs>
 void norm_at(const NormParams& p, dim3 block, cudaStream_t s) {
   const int grid = grid_of((p.rows + block.y - 1) / block.y);
   if (p.e4m3)
-    k_rmsnorm<kVecs, true><<<grid, block, 0, s>>>(p);
+    k_rmsnorm<W, kVecs, true><<<grid, block, 0, s>>>(p);
   else
-    k_rmsnorm<kVecs, false><<<grid, block, 0, s>>>(p);
+    k_rmsnorm<W, kVecs, false><<<grid, block, 0, s>>>(p);
+}
+
+template <typename W, int kVecs>
+void norm_backward_at(const NormBackwardParams& p, dim3 block, int blocks, cudaStream_t s) {
+  const size_t smem = block.y > 1 ? 4 * static_cast<size_t>(p.dim) : 0;
+  k_rmsnorm_backward<W, kVecs><<<blocks, block, smem, s>>>(p);
 }
 
 }  // namespace
 
 int launch_rmsnorm(const NormParams& p, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const RowShape shape = row_shape(p.dim);
-  const bool words = p.dim % 8 == 0 && p.x_stride % 8 == 0 && on16(p.x) && on16(p.y) &&
-                     on16(p.weight) && on16(p.h) &&
-                     (!p.residual || (on16(p.residual) && p.residual_stride % 8 == 0));
-  if (!words || shape.vecs == 0)
-    k_rmsnorm_any<<<grid_of(p.rows), kRowThreads, 0, s>>>(p);
-  else if (shape.vecs == 1)
-    norm_at<1>(p, shape.block, s);
-  else if (shape.vecs == 2)
-    norm_at<2>(p, shape.block, s);
-  else
-    norm_at<4>(p, shape.block, s);
+  const int word = word_values(p.dim, {p.x, p.residual, p.weight, p.h, p.y},
+                               {p.x_stride, p.residual ? p.residual_stride : 0});
+  const RowShape shape = row_shape(p.dim, word, !p.residual && p.rows >= kManyRows ? 16 : 8);
+  const dim3 b = shape.block;
+  switch (shape.values * 16 + word) {
+    case 8 * 16 + 8: norm_at<uint4, 1>(p, b, s); break;
+    case 16 * 16 + 8: norm_at<uint4, 2>(p, b, s); break;
+    case 32 * 16 + 8: norm_at<uint4, 4>(p, b, s); break;
+    case 8 * 16 + 2: norm_at<uint32_t, 4>(p, b, s); break;
+    case 16 * 16 + 2: norm_at<uint32_t, 8>(p, b, s); break;
+    case 8 * 16 + 1: norm_at<uint16_t, 8>(p, b, s); break;
+    case 16 * 16 + 1: norm_at<uint16_t, 16>(p, b, s); break;
+    default: k_rmsnorm_any<<<grid_of(p.rows), kRowThreads, 0, s>>>(p);
+  }
   return cudaGetLastError();
 }
 
 int launch_rmsnorm_backward(const NormBackwardParams& p, int blocks, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const RowShape shape = row_shape(p.dim);
-  const bool words = p.dim % 8 == 0 && p.dy_stride % 8 == 0 && p.h_stride % 8 == 0 &&
-                     on16(p.dy) && on16(p.h) && on16(p.weight) && on16(p.dx) &&
-                     (!p.dh || (on16(p.dh) && p.dh_stride % 8 == 0));
-  if (!words || shape.vecs == 0) {
-    k_rmsnorm_backward_any<<<blocks, kRowThreads, 0, s>>>(p);
-  } else {
-    const int64_t most = (p.rows + shape.block.y - 1) / shape.block.y;
+  const int word = word_values(p.dim, {p.dy, p.h, p.weight, p.dh, p.dx},
+                               {p.dy_stride, p.h_stride, p.dh ? p.dh_stride : 0});
+  const RowShape shape = row_shape(p.dim, word, 8);
+  const dim3 b = shape.block;
+  if (shape.values) {
+    const int64_t most = (p.rows + b.y - 1) / b.y;
     if (most < blocks) blocks = static_cast<int>(most);
-    const size_t smem = shape.block.y > 1 ? 4 * static_cast<size_t>(p.dim) : 0;
-    if (shape.vecs == 1)
-      k_rmsnorm_backward<1><<<blocks, shape.block, smem, s>>>(p);
-    else if (shape.vecs == 2)
-      k_rmsnorm_backward<2><<<blocks, shape.block, smem, s>>>(p);
-    else
-      k_rmsnorm_backward<4><<<blocks, shape.block, smem, s>>>(p);
+  }
+  switch (shape.values * 16 + word) {
+    case 8 * 16 + 8: norm_backward_at<uint4, 1>(p, b, blocks, s); break;
+    case 16 * 16 + 8: norm_backward_at<uint4, 2>(p, b, blocks, s); break;
+    case 32 * 16 + 8: norm_backward_at<uint4, 4>(p, b, blocks, s); break;
+    case 8 * 16 + 2: norm_backward_at<uint32_t, 4>(p, b, blocks, s); break;
+    case 16 * 16 + 2: norm_backward_at<uint32_t, 8>(p, b, blocks, s); break;
+    case 8 * 16 + 1: norm_backward_at<uint16_t, 8>(p, b, blocks, s); break;
+    case 16 * 16 + 1: norm_backward_at<uint16_t, 16>(p, b, blocks, s); break;
+    default: k_rmsnorm_backward_any<<<blocks, kRowThreads, 0, s>>>(p);
   }
   k_sum_partials<<<grid_of((p.dim + 31) / 32), 1024, 0, s>>>(p.partial, blocks, p.dim, p.dweight);
   return cudaGetLastError();
