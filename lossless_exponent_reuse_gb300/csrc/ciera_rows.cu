@@ -93,46 +93,55 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*part)[32]) {
   return __reduce_max_sync(0xffffffffu, v);
 }
 
-template <typename W, int kVecs, bool kE4m3>
+// kNorm false: rows to e4m3 as they are.
+template <typename W, int kVecs, bool kNorm, bool kE4m3>
 __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p) {
   __shared__ float part[8][32];
   __shared__ uint32_t part_max[8][32];
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const bool row = r < p.rows;
   constexpr int kN = Word<W>::kValues;
-  const int words = static_cast<int>(p.dim / kN);
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  // words of the row from this thread's first on; a row behind the last has none
+  const int words = r < p.rows ? static_cast<int>(p.dim / kN) - static_cast<int>(threadIdx.x) : 0;
+  const int step = blockDim.x;
+  const W* x = reinterpret_cast<const W*>(p.x + r * p.x_stride) + threadIdx.x;
+  const W* residual = reinterpret_cast<const W*>(p.residual + r * p.residual_stride) + threadIdx.x;
+  const W* weights = reinterpret_cast<const W*>(p.weight) + threadIdx.x;
   float s[kVecs][kN];
   W weight[kVecs] = {};
   float sum = 0.0f;
+  uint32_t amax = 0;
+  W in[kVecs], add[kVecs];
 #pragma unroll
   for (int v = 0; v < kVecs; ++v) {
-    const int i = v * blockDim.x + threadIdx.x;
-    W x{}, add{};
-    if (row && i < words) {
-      x = reinterpret_cast<const W*>(p.x + r * p.x_stride)[i];
-      if (p.residual) add = reinterpret_cast<const W*>(p.residual + r * p.residual_stride)[i];
-      if (p.weight) weight[v] = reinterpret_cast<const W*>(p.weight)[i];
-    }
-    float f[kN];
-    Word<W>::unpack(x, s[v]);
-    Word<W>::unpack(add, f);
-#pragma unroll
-    for (int j = 0; j < kN; ++j) {
-      if (p.residual) s[v][j] += f[j];
-      sum += s[v][j] * s[v][j];
+    in[v] = add[v] = W{};
+    if (v * step < words) {
+      in[v] = x[v * step];
+      if (kNorm && p.residual) add[v] = residual[v * step];
+      if (kNorm) weight[v] = weights[v * step];
     }
   }
-  if (p.h) {
 #pragma unroll
-    for (int v = 0; v < kVecs; ++v) {
-      const int i = v * blockDim.x + threadIdx.x;
-      if (row && i < words) reinterpret_cast<W*>(p.h + r * p.dim)[i] = Word<W>::pack(s[v]);
+  for (int v = 0; v < kVecs; ++v) {
+    Word<W>::unpack(in[v], s[v]);
+    if (kNorm && p.residual) {
+      float f[kN];
+      Word<W>::unpack(add[v], f);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) s[v][j] += f[j];
     }
+#pragma unroll
+    for (int j = 0; j < kN; ++j) sum += kNorm ? s[v][j] * s[v][j] : 0.0f;
   }
-  if (p.weight) {
+  if (kNorm) {
+    if (p.h) {
+      W* h = reinterpret_cast<W*>(p.h + r * p.dim) + threadIdx.x;
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v)
+        if (v * step < words) h[v * step] = Word<W>::pack(s[v]);
+    }
     sum = row_sum(sum, part);
     const float rstd = rsqrtf(sum / static_cast<float>(p.dim) + p.eps);
-    if (p.rstd && row && threadIdx.x == 0) p.rstd[r] = rstd;
+    if (p.rstd && r < p.rows && threadIdx.x == 0) p.rstd[r] = rstd;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
       float w[kN];
@@ -143,28 +152,28 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p)
   }
   float inverse = 1.0f;
   if (kE4m3) {
-    uint32_t amax = 0;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
 #pragma unroll
       for (int j = 0; j < kN; ++j)
-        if (v * blockDim.x + threadIdx.x < words)  // behind the row a NaN may stand
+        // behind the row stands 0 times rstd: not a number where rstd is infinite
+        if (!kNorm || v * step < words)
           amax = max(amax, __float_as_uint(s[v][j]) & 0x7FFFFFFFu);
     const float scale = e4m3_scale(row_max(amax, part_max));
     inverse = 1.0f / scale;
-    if (row && threadIdx.x == 0) p.scale[r] = scale;
+    if (r < p.rows && threadIdx.x == 0) p.scale[r] = scale;
   }
+  using Half = typename Word<W>::Half;
+  W* y = reinterpret_cast<W*>(static_cast<uint16_t*>(p.y) + r * p.dim) + threadIdx.x;
+  Half* y8 = reinterpret_cast<Half*>(static_cast<uint8_t*>(p.y) + r * p.dim) + threadIdx.x;
 #pragma unroll
-  for (int v = 0; v < kVecs; ++v) {
-    const int i = v * blockDim.x + threadIdx.x;
-    if (!row || i >= words) continue;
-    if (kE4m3) {
-      reinterpret_cast<typename Word<W>::Half*>(static_cast<uint8_t*>(p.y) + r * p.dim)[i] =
-          Word<W>::pack_8bit(s[v], inverse);
-    } else {
-      reinterpret_cast<W*>(static_cast<uint16_t*>(p.y) + r * p.dim)[i] = Word<W>::pack(s[v]);
+  for (int v = 0; v < kVecs; ++v)
+    if (v * step < words) {
+      if (kE4m3)
+        y8[v * step] = Word<W>::pack_8bit(s[v], inverse);
+      else
+        y[v * step] = Word<W>::pack(s[v]);
     }
-  }
 }
 
 // Gradient of the norm: each block takes rows blockIdx.x, + gridDim.x, ... in
@@ -890,10 +899,12 @@ RowShape row_shape(int64_t dim, int word, int at_first) {
 template <typename W, int kVecs>
 void norm_at(const NormParams& p, dim3 block, cudaStream_t s) {
   const int grid = grid_of((p.rows + block.y - 1) / block.y);
-  if (p.e4m3)
-    k_rmsnorm<W, kVecs, true><<<grid, block, 0, s>>>(p);
+  if (!p.weight)
+    k_rmsnorm<W, kVecs, false, true><<<grid, block, 0, s>>>(p);
+  else if (p.e4m3)
+    k_rmsnorm<W, kVecs, true, true><<<grid, block, 0, s>>>(p);
   else
-    k_rmsnorm<W, kVecs, false><<<grid, block, 0, s>>>(p);
+    k_rmsnorm<W, kVecs, true, false><<<grid, block, 0, s>>>(p);
 }
 
 template <typename W, int kVecs>
@@ -930,7 +941,10 @@ int launch_rmsnorm_backward(const NormBackwardParams& p, int blocks, void* strea
   const RowShape shape = row_shape(p.dim, word, 8);
   const dim3 b = shape.block;
   if (shape.values) {
+    // as many as are resident at once, with 64 registers a thread: 1024 threads an SM
+    const int64_t resident = 152 * (1024 / static_cast<int64_t>(b.x * b.y));
     const int64_t most = (p.rows + b.y - 1) / b.y;
+    if (resident < blocks) blocks = static_cast<int>(resident);
     if (most < blocks) blocks = static_cast<int>(most);
   }
   switch (shape.values * 16 + word) {
