@@ -211,34 +211,47 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8
     k_rmsnorm_backward(const NormBackwardParams p) {
   __shared__ float part[2][8][32];
   constexpr int kN = Word<W>::kValues;
-  const int words = static_cast<int>(p.dim / kN);
+  // words of a row from this thread's first on
+  const int words = static_cast<int>(p.dim / kN) - static_cast<int>(threadIdx.x);
+  const int across = blockDim.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
   const float inverse_dim = 1.0f / static_cast<float>(p.dim);
   float dw[kVecs][kN] = {};
   W weight[kVecs], dy[kVecs], h[kVecs], dh[kVecs];
   float rstd = 0.0f;
-  const auto fetch = [&](int64_t r) {
-    const bool row = r < p.rows;
+  int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const W* dy_at = reinterpret_cast<const W*>(p.dy + r * p.dy_stride) + threadIdx.x;
+  const W* h_at = reinterpret_cast<const W*>(p.h + r * p.h_stride) + threadIdx.x;
+  const W* dh_at = reinterpret_cast<const W*>(p.dh + r * p.dh_stride) + threadIdx.x;
+  W* dx_at = reinterpret_cast<W*>(p.dx + r * p.dim) + threadIdx.x;
+  const float* rstd_at = p.rstd + r;
+  const int64_t dy_step = step * p.dy_stride / kN, h_step = step * p.h_stride / kN;
+  const int64_t dh_step = step * p.dh_stride / kN, dx_step = step * p.dim / kN;
+  const auto fetch = [&](bool row) {
+    const int have = row ? words : 0;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-      const int i = v * blockDim.x + threadIdx.x;
       dy[v] = h[v] = dh[v] = W{};
-      if (!row || i >= words) continue;
-      dy[v] = reinterpret_cast<const W*>(p.dy + r * p.dy_stride)[i];
-      h[v] = reinterpret_cast<const W*>(p.h + r * p.h_stride)[i];
-      if (p.dh) dh[v] = reinterpret_cast<const W*>(p.dh + r * p.dh_stride)[i];
+      if (v * across < have) {
+        dy[v] = dy_at[v * across];
+        h[v] = h_at[v * across];
+        if (p.dh) dh[v] = dh_at[v * across];
+      }
     }
-    rstd = row ? p.rstd[r] : 0.0f;
+    rstd = row ? *rstd_at : 0.0f;
+    dy_at += dy_step;
+    h_at += h_step;
+    dh_at += dh_step;
+    rstd_at += step;
   };
 #pragma unroll
   for (int v = 0; v < kVecs; ++v) {
-    const int i = v * blockDim.x + threadIdx.x;
-    weight[v] = i < words ? reinterpret_cast<const W*>(p.weight)[i] : W{};
+    weight[v] = W{};
+    if (v * across < words) weight[v] = reinterpret_cast<const W*>(p.weight)[v * across + threadIdx.x];
   }
-  fetch(static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y);
+  fetch(r < p.rows);
   int turn = 0;  // two reductions' scratch in turn: one barrier each
   for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step) {
-    const int64_t r = r0 + threadIdx.y;
     // with n = h rstd:  dx = rstd (g - n mean(g n)) + dh,  dweight += dy n
     float g[kVecs][kN], n[kVecs][kN];
     W more[kVecs];
@@ -259,20 +272,21 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8
         dw[v][j] += d[j] * n[v][j];
       }
     }
-    fetch(r + step);
+    const int have = r < p.rows ? words : 0;
+    r += step;
+    fetch(r < p.rows);
     dot = row_sum(dot, part[turn]);
     turn ^= 1;
     const float mean = dot * inverse_dim;
 #pragma unroll
     for (int v = 0; v < kVecs; ++v) {
-      const int i = v * blockDim.x + threadIdx.x;
-      if (r >= p.rows || i >= words) continue;
       float out[kN];
       Word<W>::unpack(more[v], out);
 #pragma unroll
       for (int j = 0; j < kN; ++j) out[j] += rs * (g[v][j] - n[v][j] * mean);
-      reinterpret_cast<W*>(p.dx + r * p.dim)[i] = Word<W>::pack(out);
+      if (v * across < have) dx_at[v * across] = Word<W>::pack(out);
     }
+    dx_at += dx_step;
   }
   // this block's part of the weight's gradient, its rows' in order
   extern __shared__ float column[];  // blockDim.y > 1: dim floats
@@ -281,8 +295,8 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8
     if (threadIdx.y == turn_y) {
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
-        const int i = v * blockDim.x + threadIdx.x;
-        if (i >= words) continue;
+        const int i = v * across + threadIdx.x;
+        if (v * across >= words) continue;
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
           const float before = turn_y ? column[i * kN + j] : 0.0f;
