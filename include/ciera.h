@@ -461,6 +461,11 @@ const char *ciera_strerror(int status);
  *     zero-filled once (ciera_moe_workspace_init), and use it as above:
  *     one call at a time.  Its status is read with ciera_status().
  *   - Results do not depend on the order in which thread blocks run.
+ *   - Fast paths: the products run on the tensor cores where both operands
+ *     start on 16-byte boundaries and their row (and expert) strides are
+ *     multiples of 16 bytes; the row-wise calls move 16 bytes at a time under
+ *     the same condition (the norms also 4).  Other layouts take plain kernels
+ *     that give the same results up to the order of their 32-bit sums.
  */
 #define CIERA_BF16 0
 #define CIERA_E4M3 1
