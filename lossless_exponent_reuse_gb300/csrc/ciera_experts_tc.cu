@@ -22,8 +22,6 @@
 // groups' tiles from the offsets by itself.
 #include <cuda.h>
 
-#include <atomic>
-
 #include "ciera_device.cuh"
 #include "ciera_moe_device.cuh"
 
@@ -114,11 +112,6 @@ __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int
         : "memory");
 }
 
-// 16 bytes to shared memory, of which the first `bytes` come from `src`.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-               : "memory");
-}
 // Arrives on `bar` (an arrival it counts on) when this thread's copies so far
 // have landed.
 __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
@@ -1040,19 +1033,9 @@ bool make_map(CUtensorMap* map, const void* base, bool e4m3, int64_t columns, in
 template <int kOp, bool kGated, bool kE4m3, int kPair>
 int launch_at(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid,
               cudaStream_t s) {
-  // once per device: the stages need more shared memory than kernels get unasked
-  static std::atomic<uint64_t> asked{0};
-  int device = 0;
-  cudaError_t err = cudaGetDevice(&device);
+  const cudaError_t err =
+      allow_shared<k_expert_tc<kOp, kGated, kE4m3, kPair>>(kSmemLimit - 12 * 1024);
   if (err != cudaSuccess) return err;
-  const uint64_t bit = uint64_t(1) << (device & 63);
-  if (!(asked.load(std::memory_order_relaxed) & bit)) {
-    err = cudaFuncSetAttribute(k_expert_tc<kOp, kGated, kE4m3, kPair>,
-                               cudaFuncAttributeMaxDynamicSharedMemorySize,
-                               kSmemLimit - 12 * 1024);
-    if (err != cudaSuccess) return err;
-    asked.fetch_or(bit, std::memory_order_relaxed);
-  }
   cudaLaunchConfig_t config{};
   config.gridDim = dim3(static_cast<unsigned>(grid));
   config.blockDim = dim3(Roles<kPair>::kThreads);

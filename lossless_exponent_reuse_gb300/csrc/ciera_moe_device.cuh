@@ -6,6 +6,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cstdint>
 
 #include "ciera_moe.h"
@@ -44,6 +45,15 @@ __device__ __forceinline__ float e4m3_to_f32(uint8_t v) {
 __device__ __forceinline__ float e4m3_scale(uint32_t amax_bits) {
   if (amax_bits >= 0x7F800000u) return __uint_as_float(0x7FC00000u);
   return fmaxf(__uint_as_float(amax_bits), kTinyAmax) / kE4m3Max;
+}
+
+// 16 bytes to shared memory, of which the first `bytes` come from `src`.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+               : "memory");
+}
+__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
+  copy16(static_cast<uint32_t>(__cvta_generic_to_shared(dst)), src, bytes);
 }
 
 __device__ __forceinline__ float warp_sum_f32(float v) {
@@ -142,6 +152,21 @@ struct Word<uint16_t> {
 // Offset of group e, clamped to [lo, rows]; `lo` is the one before it.
 __device__ __forceinline__ int32_t clamp_offset(int32_t v, int32_t lo, int32_t rows) {
   return v < lo ? lo : v > rows ? rows : v;
+}
+
+// Host: lets a kernel have `bytes` of dynamic shared memory, once per device
+// (more than 48 KB want asking).
+template <auto kKernel>
+cudaError_t allow_shared(int bytes) {
+  static std::atomic<uint64_t> asked{0};
+  int device = 0;
+  cudaError_t err = cudaGetDevice(&device);
+  if (err != cudaSuccess) return err;
+  const uint64_t bit = uint64_t(1) << (device & 63);
+  if (asked.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  err = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (err == cudaSuccess) asked.fetch_or(bit, std::memory_order_relaxed);
+  return err;
 }
 
 }  // namespace

@@ -10,6 +10,7 @@ namespace ciera {
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kRingBytes = 48 * 1024;
 constexpr int64_t kManyRows = 2048;    // enough to fill the SMs with half the threads a row
 constexpr int kMostRowThreads = 512;  // for one row of the kernels that hold rows in registers
 
@@ -311,6 +312,132 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8
   }
 }
 
+// The same for rows of 16-byte words that fit: rows come into a ring in shared
+// memory by asynchronous copies, kRing - 1 of them ahead, each thread copying
+// and reading its own words, so that the bytes under way do not depend on
+// registers (10007 rows of 1536 values not in L2: 29 us with one row ahead in
+// registers).
+template <int kVecs, int kRing>
+__global__ void __launch_bounds__(kMostRowThreads)
+    k_rmsnorm_backward_ring(const NormBackwardParams p) {
+  extern __shared__ uint4 ring[];  // kRing x 3 x blockDim.y x words
+  __shared__ float part[2][8][32];
+  const int words = static_cast<int>(p.dim / 8), across = blockDim.x;
+  const int have = words - static_cast<int>(threadIdx.x);  // words from this thread's first on
+  const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
+  const float inverse_dim = 1.0f / static_cast<float>(p.dim);
+  float dw[kVecs][8] = {};
+  uint4 weight[kVecs];
+#pragma unroll
+  for (int v = 0; v < kVecs; ++v) {
+    weight[v] = make_uint4(0, 0, 0, 0);
+    if (v * across < have)
+      weight[v] = reinterpret_cast<const uint4*>(p.weight)[v * across + threadIdx.x];
+  }
+  const int plane = blockDim.y * words;  // words of one tensor's rows in a stage
+  uint4* mine = ring + threadIdx.y * words + threadIdx.x;
+  const int64_t r_first = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  // this thread's words of the next row to fetch, and of the row in hand
+  const uint16_t* dy_in = p.dy + r_first * p.dy_stride + threadIdx.x * 8;
+  const uint16_t* h_in = p.h + r_first * p.h_stride + threadIdx.x * 8;
+  const uint16_t* dh_in = p.dh + r_first * p.dh_stride + threadIdx.x * 8;
+  uint16_t* dx_out = p.dx + r_first * p.dim + threadIdx.x * 8;
+  const int64_t dy_step = step * p.dy_stride, h_step = step * p.h_stride;
+  const int64_t dh_step = step * p.dh_stride, dx_step = step * p.dim;
+  int64_t left_in = p.rows - r_first, left = left_in;  // rows from that one on
+  const auto fetch = [&](int stage) {
+    if (left_in > 0) {
+      uint4* to = mine + stage * 3 * plane;
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v)
+        if (v * across < have) {
+          copy16(to + v * across, dy_in + v * across * 8, 16);
+          copy16(to + plane + v * across, h_in + v * across * 8, 16);
+          if (p.dh) copy16(to + 2 * plane + v * across, dh_in + v * across * 8, 16);
+        }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    left_in -= step;
+    dy_in += dy_step;
+    h_in += h_step;
+    dh_in += dh_step;
+  };
+#pragma unroll
+  for (int i = 0; i + 1 < kRing; ++i) fetch(i);
+  const float* rstd_in = p.rstd + r_first;
+  float rstd = left > 0 ? *rstd_in : 0.0f;
+  int turn = 0, stage = 0;
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * blockDim.y; r0 < p.rows; r0 += step) {
+    const float rs = rstd;
+    rstd_in += step;
+    rstd = left > step ? *rstd_in : 0.0f;
+    // the stage read in the last turn is free: its reader is this thread
+    fetch(stage == 0 ? kRing - 1 : stage - 1);
+    asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 1) : "memory");
+    const uint4* from = mine + stage * 3 * plane;
+    float g[kVecs][8], n[kVecs][8];
+    float dot = 0.0f;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v) {
+      float d[8], w[8];
+      const bool some = left > 0 && v * across < have;  // else nothing was fetched
+      unpack8(some ? from[v * across] : make_uint4(0, 0, 0, 0), d);
+      unpack8(some ? from[plane + v * across] : make_uint4(0, 0, 0, 0), n[v]);
+      unpack8(weight[v], w);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        n[v][j] *= rs;
+        g[v][j] = d[j] * w[j];
+        dot += g[v][j] * n[v][j];
+        dw[v][j] += d[j] * n[v][j];
+      }
+    }
+    dot = row_sum(dot, part[turn]);
+    turn ^= 1;
+    const float mean = dot * inverse_dim;
+#pragma unroll
+    for (int v = 0; v < kVecs; ++v)
+      if (left > 0 && v * across < have) {
+        float out[8] = {};
+        if (p.dh) unpack8(from[2 * plane + v * across], out);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) out[j] += rs * (g[v][j] - n[v][j] * mean);
+        *reinterpret_cast<uint4*>(dx_out + v * across * 8) = pack8(out);
+      }
+    left -= step;
+    dx_out += dx_step;
+    stage = stage + 1 == kRing ? 0 : stage + 1;
+  }
+  // the block's rows' parts in order, through the ring's memory
+  asm volatile("cp.async.wait_all;" ::: "memory");
+  __syncthreads();
+  float4* column = reinterpret_cast<float4*>(ring) + threadIdx.x * 2;
+  float4* out = reinterpret_cast<float4*>(p.partial + static_cast<int64_t>(blockIdx.x) * p.dim) +
+                threadIdx.x * 2;
+  for (int y = 0; y < blockDim.y; ++y) {
+    if (threadIdx.y == y) {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        if (v * across >= have) continue;
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          float4 sum = make_float4(dw[v][4 * q], dw[v][4 * q + 1], dw[v][4 * q + 2],
+                                   dw[v][4 * q + 3]);
+          if (y) {
+            const float4 before = column[v * across * 2 + q];
+            sum.x += before.x;
+            sum.y += before.y;
+            sum.z += before.z;
+            sum.w += before.w;
+          }
+          (y + 1 == blockDim.y ? out : column)[v * across * 2 + q] = sum;
+        }
+      }
+    }
+    if (blockDim.y > 1) __syncthreads();
+  }
+}
+
 // Sums of the blocks' parts: 32 columns a block, each by 32 threads that take
 // every 32nd part in order, then those 32 sums in order of a tree.
 __global__ void __launch_bounds__(1024) k_sum_partials(const float* partial, int blocks,
@@ -320,7 +447,7 @@ __global__ void __launch_bounds__(1024) k_sum_partials(const float* partial, int
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float sum = 0.0f;
   if (c < dim)
-#pragma unroll 4
+#pragma unroll 8
     for (int b = way; b < blocks; b += 32) sum += partial[b * dim + c];
   sums[way][lane] = sum;
   __syncthreads();
@@ -929,6 +1056,19 @@ void norm_backward_at(const NormBackwardParams& p, dim3 block, int blocks, cudaS
 
 }  // namespace
 
+namespace {
+
+template <int kVecs, int kRing>
+int backward_ring(const NormBackwardParams& p, dim3 block, int blocks, size_t bytes,
+                  cudaStream_t s) {
+  const cudaError_t err = allow_shared<k_rmsnorm_backward_ring<kVecs, kRing>>(kRingBytes);
+  if (err != cudaSuccess) return err;
+  k_rmsnorm_backward_ring<kVecs, kRing><<<blocks, block, bytes, s>>>(p);
+  return cudaSuccess;
+}
+
+}  // namespace
+
 int launch_rmsnorm(const NormParams& p, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int word = word_values(p.dim, {p.x, p.residual, p.weight, p.h, p.y},
@@ -952,18 +1092,35 @@ int launch_rmsnorm_backward(const NormBackwardParams& p, int blocks, void* strea
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int word = word_values(p.dim, {p.dy, p.h, p.weight, p.dh, p.dx},
                                {p.dy_stride, p.h_stride, p.dh ? p.dh_stride : 0});
-  const RowShape shape = row_shape(p.dim, word, 8);
+  // 16 values per thread where that leaves a warp's worth: half the work of a
+  // row's sum and of its addresses per value
+  const RowShape shape = row_shape(p.dim, word, word == 8 && p.dim >= 512 ? 16 : 8);
   const dim3 b = shape.block;
+  // a ring of four rows as far as it takes 48 KB, else of two
+  const int64_t line = 6 * p.dim * b.y;  // bytes of the rows of all three tensors
+  const int ring = 4 * line <= kRingBytes ? 4 : 2 * line <= kRingBytes ? 2 : 0;
+  const size_t bytes = static_cast<size_t>(ring * line);
   if (shape.values) {
-    // as many as are resident at once, with 64 registers a thread: 1024 threads an SM
+    // as many as are resident at once, 64 registers a thread or shared memory
+    // allowing: 1024 threads an SM
     const int64_t resident = 152 * (1024 / static_cast<int64_t>(b.x * b.y));
     const int64_t most = (p.rows + b.y - 1) / b.y;
     if (resident < blocks) blocks = static_cast<int>(resident);
     if (most < blocks) blocks = static_cast<int>(most);
   }
+  int err = cudaSuccess;
   switch (shape.values * 16 + word) {
-    case 8 * 16 + 8: norm_backward_at<uint4, 1>(p, b, blocks, s); break;
-    case 16 * 16 + 8: norm_backward_at<uint4, 2>(p, b, blocks, s); break;
+    case 8 * 16 + 8:  // fewer than 512 values: the ring fits
+      err = backward_ring<1, 4>(p, b, blocks, bytes, s);
+      break;
+    case 16 * 16 + 8:
+      if (ring == 4)
+        err = backward_ring<2, 4>(p, b, blocks, bytes, s);
+      else if (ring == 2)
+        err = backward_ring<2, 2>(p, b, blocks, bytes, s);
+      else
+        norm_backward_at<uint4, 2>(p, b, blocks, s);
+      break;
     case 32 * 16 + 8: norm_backward_at<uint4, 4>(p, b, blocks, s); break;
     case 8 * 16 + 2: norm_backward_at<uint32_t, 4>(p, b, blocks, s); break;
     case 16 * 16 + 2: norm_backward_at<uint32_t, 8>(p, b, blocks, s); break;
@@ -971,6 +1128,7 @@ int launch_rmsnorm_backward(const NormBackwardParams& p, int blocks, void* strea
     case 16 * 16 + 1: norm_backward_at<uint16_t, 16>(p, b, blocks, s); break;
     default: k_rmsnorm_backward_any<<<blocks, kRowThreads, 0, s>>>(p);
   }
+  if (err != cudaSuccess) return err;
   k_sum_partials<<<grid_of((p.dim + 31) / 32), 1024, 0, s>>>(p.partial, blocks, p.dim, p.dweight);
   return cudaGetLastError();
 }
