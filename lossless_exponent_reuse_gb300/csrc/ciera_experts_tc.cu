@@ -253,6 +253,7 @@ struct Shared {
   uint32_t stop;                     // a wait ran out: every role leaves its loop
   int32_t start[kMaxExperts + 2];    // first row of each group; the unused rows are the last
   int32_t tile[kMaxExperts + 2];     // tiles before each group
+  uint16_t per[kMaxExperts + 1];     // rows of each group's tiles
 };
 
 // N of a tile's instructions: multiples of 16, of 32 for a pair.
@@ -269,14 +270,13 @@ __device__ __forceinline__ int rows_per_tile(int m, int tile_n) {
   return tiles <= 1 ? tile_n : padded<kPair>((m + tiles - 1) / tiles);
 }
 
-template <int kOp, int kPair>
-__device__ __forceinline__ int tiles_of_group(const TcParams& p, int m, bool unused) {
+template <int kOp>
+__device__ __forceinline__ int tiles_of_group(const TcParams& p, int m, int per, bool unused) {
   if (kOp == kExpertDw) return unused ? 0 : p.m_tiles * p.n_tiles;
-  const int per = rows_per_tile<kPair>(m, p.tile_n);
   return (m + per - 1) / per * p.m_tiles;
 }
 
-// Fills start[] and tile[]; one warp.
+// Fills start[], tile[] and per[]; one warp.
 template <int kOp, int kPair>
 __device__ void find_groups(const TcParams& p, Shared& sh) {
   const int lane = threadIdx.x & 31, E = p.e.experts;
@@ -294,7 +294,8 @@ __device__ void find_groups(const TcParams& p, Shared& sh) {
     end = max(end, highest);
     int32_t begin = __shfl_up_sync(0xffffffffu, end, 1);
     if (lane == 0) begin = highest;
-    const int32_t tiles = g <= E ? tiles_of_group<kOp, kPair>(p, end - begin, g == E) : 0;
+    const int per = kOp == kExpertDw ? p.tile_n : rows_per_tile<kPair>(end - begin, p.tile_n);
+    const int32_t tiles = g <= E ? tiles_of_group<kOp>(p, end - begin, per, g == E) : 0;
     int32_t sum = tiles;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -303,6 +304,7 @@ __device__ void find_groups(const TcParams& p, Shared& sh) {
     }
     if (g <= E) {
       sh.start[g] = begin;
+      sh.per[g] = static_cast<uint16_t>(per);
       sh.tile[g] = before + sum - tiles;
       if (g == E) {
         sh.start[E + 1] = rows;
@@ -352,7 +354,7 @@ struct Walk {
       begin = sh.tile[group];
       first = sh.start[group];
       rows = sh.start[group + 1] - first;
-      per = kOp == kExpertDw ? p.tile_n : rows_per_tile<kPair>(rows, p.tile_n);
+      per = sh.per[group];
     }
     const int local = index - begin;
     // local / m_tiles; the product is that or one more
@@ -558,9 +560,14 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring) {
   Place at;
   int tiles = 0;
   Walk<kOp, kPair, kFused> walk;
-  OutTile t;
-  while (walk.next(p, sh, t)) {
-    if (t.depth == 0) continue;
+  OutTile t, next;
+  bool have = walk.next(p, sh, next);
+  while (have) {
+    t = next;
+    if (t.depth == 0) {
+      have = walk.next(p, sh, next);
+      continue;
+    }
     const int buffer = tiles & 1;
     if (!wait(p, sh, &sh.acc_empty[buffer], ((tiles >> 1) & 1) ^ 1)) return;
     tc_fence_after();
@@ -585,6 +592,10 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring) {
       }
       mma_commit<kPair>(&sh.empty[stage]);
       at.advance(p.stages);
+      // the next tile is looked up behind the third stage, while the tensor
+      // core has products in hand
+      if (c == 2 * kDepth || (c < 2 * kDepth && c + kDepth >= t.depth))
+        have = walk.next(p, sh, next);
     }
     mma_commit<kPair>(&sh.acc_full[buffer]);
     ++tiles;
@@ -1034,7 +1045,7 @@ template <int kOp, bool kGated, bool kE4m3, int kPair>
 int launch_at(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid,
               cudaStream_t s) {
   const cudaError_t err =
-      allow_shared<k_expert_tc<kOp, kGated, kE4m3, kPair>>(kSmemLimit - 12 * 1024);
+      allow_shared<k_expert_tc<kOp, kGated, kE4m3, kPair>>(kSmemLimit - 14 * 1024);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t config{};
   config.gridDim = dim3(static_cast<unsigned>(grid));
@@ -1098,7 +1109,7 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   p.a_bytes = kTileM * kRowBytes;
   const int pair = small || e.row_tokens ? 1 : 2;
   p.stage_bytes = p.a_bytes + p.tile_n / pair * kRowBytes;
-  p.stages = (kSmemLimit - 14 * 1024) / p.stage_bytes;
+  p.stages = (kSmemLimit - 16 * 1024) / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const int64_t tile_m = (fused ? kTileM / 2 : kTileM) * pair;
   const int64_t m_tiles = (features + tile_m - 1) / tile_m;
