@@ -537,7 +537,7 @@ int ciera_quantize_rows(const uint16_t *x_dev, int64_t x_stride, int64_t rows, i
  *   row_tokens_dev  tokens * topk: each row's token, -1 for unused rows
  *   offsets_dev     experts + 1 row offsets
  * Errors: CIERA_E_INVAL (topk outside [1, min(experts, 32)], experts outside
- * [1, 1024], tokens * topk >= 2^31, short stride, NULL or misaligned pointers,
+ * [1, 1024], tokens * topk > 2^31 - 4096, short stride, NULL or misaligned pointers,
  * unknown flags, a workspace smaller than
  * ciera_moe_workspace_bytes(tokens, experts, 0)), CIERA_E_CUDA. */
 int ciera_route(const void *logits_dev, int logits_type, int64_t logits_stride,
@@ -607,7 +607,7 @@ int ciera_combine_backward(const uint16_t *dy_dev, int64_t dy_stride, const uint
  *                scales go on after the 32-bit sum
  *   y_dev        rows x n bf16, contiguous
  *   pre_dev      rows x 2n bf16, contiguous: a, kept for the gradient; or NULL
- * Errors: CIERA_E_INVAL (experts outside [0, 1024], rows or x_rows >= 2^31,
+ * Errors: CIERA_E_INVAL (experts outside [0, 1024], rows or x_rows > 2^31 - 4096,
  * sizes, strides, NULL or misaligned pointers, flags), CIERA_E_CUDA. */
 int ciera_expert_mm(const void *x_dev, int64_t x_stride, int64_t x_rows,
                     const int32_t *row_tokens_dev, const void *w_dev, int64_t w_stride,

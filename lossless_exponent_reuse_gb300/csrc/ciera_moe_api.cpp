@@ -12,7 +12,8 @@ using namespace ciera;
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t(1) << 31) - 1;
+// Rows that 32-bit indexes can count with a tile's rows to spare.
+constexpr int64_t kMaxRows = (int64_t(1) << 31) - 4096;
 constexpr int64_t kMaxDim = int64_t(1) << 30;
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }

@@ -77,6 +77,9 @@ def bucket_views(bucket: torch.Tensor, experts: int, dim: int, ff: int,
 # ---- arguments -----------------------------------------------------------
 
 _workspaces = {}
+_outgrown = []
+_needs = {}           # (tokens, experts, dim): bytes
+_NEVER = 1 << 62
 _CONTROL_BYTES = 256
 _functions = {}
 _raw_stream = torch._C._cuda_getCurrentRawStream
@@ -103,15 +106,20 @@ def workspace(index: int, stream: int, tokens: int = 0, experts: int = 0,
               dim: int = 0) -> torch.Tensor:
     """The workspace of a device index and stream handle, for calls of these sizes."""
     ws = _workspaces.get((index, stream))
-    need = _CONTROL_BYTES
-    if tokens or ws is None:
-        need = ciera.lib().ciera_moe_workspace_bytes(tokens, experts, dim)
-        if need == 0:
-            raise ValueError(f"no workspace for {tokens} tokens, {experts} experts, {dim} columns")
+    if ws is not None and (not tokens or ws.numel() >= _needs.get((tokens, experts, dim), _NEVER)):
+        return ws
+    need = ciera.lib().ciera_moe_workspace_bytes(tokens, experts, dim)
+    if need == 0:
+        raise ValueError(f"no workspace for {tokens} tokens, {experts} experts, {dim} columns")
+    if len(_needs) < 4096:
+        _needs[tokens, experts, dim] = need
     if ws is None or ws.numel() < need:
-        old, ws = ws, torch.zeros(need, dtype=torch.uint8, device=f"cuda:{index}")
-        if old is not None:  # a status not read yet
-            ws[:_CONTROL_BYTES].copy_(old[:_CONTROL_BYTES])
+        # a power of two, and the one before is kept: a captured graph may use it
+        old, ws = ws, torch.zeros(1 << (need - 1).bit_length(), dtype=torch.uint8,
+                                  device=f"cuda:{index}")
+        if old is not None:
+            ws[:_CONTROL_BYTES].copy_(old[:_CONTROL_BYTES])  # a status not read yet
+            _outgrown.append(old)
         _workspaces[index, stream] = ws
     return ws
 

@@ -371,3 +371,26 @@ def test_rows_on_another_stream():
         experts.rmsnorm(x, w, stream=side.cuda_stream)
     side.synchronize()
     assert torch.equal(got, want)
+
+
+def test_a_graph_outlives_its_workspace():
+    """A captured call keeps its scratch memory when a larger call wants more."""
+    h, dy, w = rand(64, 256, seed=30), rand(64, 256, seed=31), rand(256, seed=32)
+    rstd = torch.ones(64, device="cuda")
+    want = experts.rmsnorm_backward(dy, h, rstd, w)
+    side = torch.cuda.Stream()
+    experts.rmsnorm_backward(dy, h, rstd, w, stream=side)
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        dx, dw = experts.rmsnorm_backward(dy, h, rstd, w)
+    big = rand(3000, 2048, seed=33)
+    experts.rmsnorm_backward(big, big, torch.ones(3000, device="cuda"), rand(2048, seed=34),
+                             stream=side)
+    side.synchronize()
+    filler = [torch.full((1 << 20,), 3.0, device="cuda") for _ in range(8)]
+    dw.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
+    assert all((f == 3.0).all() for f in filler)
