@@ -15,7 +15,9 @@ constexpr int64_t kManyRows = 2048;    // enough to fill the SMs with half the t
 constexpr int kMostRowThreads = 512;  // for one row of the kernels that hold rows in registers
 
 // ------------------------------------------------------------------------
-// Norm.  Bound by memory: 8 bytes a value in bf16 with a residual, 7 in e4m3.
+// Norm.  Bound by memory: 8 bytes a value in bf16 with a residual, 7 in e4m3
+// (16384 rows of 2048 values: 39.9 us, 6.7 TB/s; in e4m3 40.4 us; rows to e4m3
+// without a norm 15.1 us).
 //
 // k_rmsnorm holds a row in registers, kVecs words per thread, so that it is
 // read once; blockDim.x threads take a row (whole warps, one reduction per
@@ -315,8 +317,8 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8
 // The same for rows of 16-byte words that fit: rows come into a ring in shared
 // memory by asynchronous copies, kRing - 1 of them ahead, each thread copying
 // and reading its own words, so that the bytes under way do not depend on
-// registers (10007 rows of 1536 values not in L2: 29 us with one row ahead in
-// registers).
+// registers.  Rows of 16384 x 2048 values not in L2: 47 us with the sum of the
+// blocks' parts (57 us with one row ahead in registers); 10007 x 1536: 25 us and 5.
 template <int kVecs, int kRing>
 __global__ void __launch_bounds__(kMostRowThreads)
     k_rmsnorm_backward_ring(const NormBackwardParams p) {
@@ -459,7 +461,9 @@ __global__ void __launch_bounds__(1024) k_sum_partials(const float* partial, int
 // ------------------------------------------------------------------------
 // Route.  A warp per token: its logits in registers, topk rounds of "largest
 // remaining, lowest index" (the first round's is the softmax's maximum), then
-// the softmax's sum and the chosen weights.
+// the softmax's sum and the chosen weights.  Bound by issue slots, about 600
+// instructions a token: 16384 tokens, 128 experts, 8 chosen: 13.4 us, and 8.6 for
+// k_route_place; one token 3.1 us.
 //
 // The order: a token chooses an expert at most once, so a pair's rank among
 // its block's pairs of the same expert is the number of earlier tokens of the
@@ -798,7 +802,8 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteBackwardParam
 }
 
 // ------------------------------------------------------------------------
-// Gather: a warp per row.  V bytes per access: 16 where rows and bases are
+// Gather: a warp per row, four words of a lane under way (65536 rows of 2048
+// bf16 values: 52 us, 5.2 TB/s of writes).  V bytes per access: 16 where rows and bases are
 // 16-byte aligned, else the element's size.
 
 template <typename V>
@@ -850,7 +855,8 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_any(const CombineParams
   }
 }
 
-// The same 16 bytes at a time, eight rows' words under way at once.
+// The same 16 bytes at a time, eight rows' words under way at once (333 tokens,
+// 8 rows of 2048 values each: 3.0 us).
 __global__ void __launch_bounds__(kRowThreads) k_combine(const CombineParams p) {
   const int64_t t = blockIdx.x;
   const int words = static_cast<int>(p.dim / 8);
@@ -920,6 +926,7 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_backward_any(const Comb
 // The same 16 bytes at a time: a block per token, eight rows at once.  The
 // eight dot products are reduced together: at each of three exchanges a lane
 // hands over half of its sums, so that a warp needs 9 exchanges for 8 sums.
+// Bound by memory: 8192 tokens, 8 rows of 2048 values, 85 us, 6.8 TB/s.
 __global__ void __launch_bounds__(kRowThreads) k_combine_backward(const CombineParams p) {
   __shared__ int32_t slot[kMaxTopk];
   __shared__ float weight[kMaxTopk];
