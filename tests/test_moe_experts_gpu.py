@@ -26,7 +26,17 @@ GROUPS = [
     ([4] * 130, 5, 128, 136),
     ([16, 31, 32, 33, 15, 1, 48, 0, 80], 0, 320, 384),
     ([1, 2, 3, 4], 6, 4096, 1000),
+    ([37 * i % 611 for i in range(24)], 50, 520, 1544),   # several tiles for every pair of blocks
+    ([29 * i % 64 for i in range(100)], 3, 264, 2056),    # and for every single block
 ]
+
+
+def test_large_cases_fill_the_device_several_times():
+    """The two cases above that are meant to: tiles of 256 x 256, and of 128 x 64."""
+    pairs = sum(-(-n // 256) for n in GROUPS[-2][0]) * -(-GROUPS[-2][3] // 256)
+    single = sum(-(-n // 64) for n in GROUPS[-1][0]) * -(-GROUPS[-1][3] // 128)
+    assert pairs > 3 * 76 and single > 3 * 152
+    assert sum(GROUPS[-2][0]) > 32 * 24 and sum(GROUPS[-1][0]) <= 32 * 100
 
 
 def make(groups, unused, seed=0, T=None):

@@ -143,10 +143,12 @@ def test_expert_mm_dx_refuses(bad):
     dict(E=2000), dict(dw=None), dict(dws=3), dict(es=3), dict(kind=experts.E4M3),
     dict(kind=experts.F32, dw=4098), dict(flags=1), dict(work=None)])
 def test_expert_mm_dw_refuses(bad):
-    a = dict(dy=FAKE, ds=32, x=FAKE, xs=64, offsets=FAKE, rows=100, E=4, n=32, k=64, dw=FAKE, dws=64, es=64 * 32, kind=experts.BF16, flags=0, work=FAKE)
+    a = dict(dy=FAKE, ds=32, x=FAKE, xs=64, offsets=FAKE, rows=100, E=4, n=32, k=64, dw=FAKE,
+             dws=64, es=64 * 32, kind=experts.BF16, flags=0, work=FAKE)
     a.update(bad)
     assert ciera.lib().ciera_expert_mm_dw(
-        vp(a["dy"]), a["ds"], vp(a["x"]), a["xs"], vp(a["offsets"]), a["rows"], a["E"], a["n"], a["k"], vp(a["dw"]), a["dws"], a["es"],
+        vp(a["dy"]), a["ds"], vp(a["x"]), a["xs"], vp(a["offsets"]), a["rows"], a["E"], a["n"],
+        a["k"], vp(a["dw"]), a["dws"], a["es"],
         a["kind"], a["flags"], vp(a["work"]), None) == ciera.E_INVAL
 
 
