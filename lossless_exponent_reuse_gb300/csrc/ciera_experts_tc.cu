@@ -11,8 +11,8 @@
 // would waste up to 127, and the lanes of a warp hold neighbouring features of
 // one row, which they store contiguously without a transposition.
 //
-// The gated product's M are 64 gates and the 64 ups that go with them in turn,
-// so that neighbouring lanes hold the two halves of an output.
+// The gated product's M are 64 gates and the 64 ups that go with them, eight of
+// each in turn, so that a thread reads both halves of an output from TMEM.
 //
 // A persistent block per SM: warp 0 moves tiles of 128 bytes by 64 or 128 rows
 // into a ring of stages with TMA (128-byte swizzle), four warps copy gathered
@@ -41,6 +41,9 @@ namespace {
 constexpr int kGatherWarps = 4;
 // Warps: 0 loads A, 1 issues the products, then the storing warps, one that
 // loads B, and those that gather rows (single blocks) or clear (pairs).
+// A storing warp has 1 KB of shared memory, two where it reads what the gated
+// unit's gradient needs (and then there are eight).
+constexpr int kStagingBytes = 16 * 1024;
 template <int kPair>
 struct Roles {
   static constexpr int kStoreWarps = kPair == 2 ? 12 : 8;
@@ -54,6 +57,7 @@ constexpr int kMaxStages = 12;
 constexpr int kMaxN = 256;              // columns of one TMEM accumulator buffer
 constexpr int kMaxSmallN = 64;          // most rows of a tile with small groups
 constexpr int kSmemLimit = 227 * 1024;
+constexpr int kStaticBytes = 11 * 1024;  // more than Shared below
 
 struct TcParams {
   ExpertParams e;
@@ -64,6 +68,7 @@ struct TcParams {
   int32_t m_tiles;       // tiles of the feature dimension
   uint32_t m_tiles_inverse;  // 2^32 / m_tiles, rounded up (of 2 and more)
   int32_t n_tiles;       // dw: tiles of its rows
+  int32_t pieces;        // gated: A comes eight rows a load (n is no multiple of 8)
 };
 
 // ------------------------------------------------------------------------
@@ -106,19 +111,19 @@ __device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, int
 }
 
 template <int kPair>
-__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
-                                       int32_t z, int32_t u, uint32_t bar) {
+__device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                       int32_t z, int32_t u, int32_t v, uint32_t bar) {
   if (kPair == 2)
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-        ".cta_group::2 [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        ".cta_group::2 [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
         : "memory");
   else
     asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(bar)
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(v), "r"(bar)
         : "memory");
 }
 
@@ -202,14 +207,15 @@ __device__ __forceinline__ void sync_all() {
     __syncthreads();
 }
 
-__device__ __forceinline__ void tmem_ld16(uint32_t addr, float* v) {
+// 16 lanes by 16 columns: lane l of the warp gets, of columns 2 (l % 4) and the
+// next, v[0] and v[1] of TMEM lane l / 4, v[2] and v[3] of lane 8 + l / 4; the
+// same of columns 8 further on in v[4] to v[7].
+__device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[8]) {
   uint32_t* r = reinterpret_cast<uint32_t*>(v);
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+      "tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
-        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
-        "=r"(r[14]), "=r"(r[15])
+        "=r"(r[7])
       : "r"(addr)
       : "memory");
 }
@@ -222,6 +228,34 @@ __device__ __forceinline__ void tc_fence_before() {
 }
 __device__ __forceinline__ void tc_fence_after() {
   asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit values, transposed on their way: lane l holds, of
+// matrix m, elements (l / 4, 2 (l % 4)) and the next in v[m]; in shared memory
+// lane 8 m + i points at what is row i there and was column i here.
+__device__ __forceinline__ void store_matrices(uint32_t addr, const uint32_t (&v)[4]) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr),
+               "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3])
+               : "memory");
+}
+__device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint4 load_shared(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ void store_shared(uint32_t addr, const uint4& v) {
+  asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
+               "r"(v.z), "r"(v.w)
+               : "memory");
 }
 
 // One lane of a warp, the same for every call; the compiler then knows that
@@ -464,8 +498,13 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map, Shared& sh
         else if (kOp == kExpertDw)
           mbar_arrive_first(full);
         if (kOp == kExpertForward) {
-          if (kFused)
-            tma_4d<kPair>(a, map, c, 0, t.feature, t.group, bar);
+          if (kFused && !p.pieces)
+            tma_5d<kPair>(a, map, c, 0, 0, t.feature / 8, t.group, bar);
+          else if (kFused)
+            for (int i = 0; i < kTileM / 8; ++i)
+              tma_3d<kPair>(a + i * 8 * kRowBytes, map, c,
+                            t.feature + i / 2 * 8 + (i & 1 ? static_cast<int>(p.e.n) : 0), t.group,
+                            bar);
           else
             tma_3d<kPair>(a, map, c, t.feature, t.group, bar);
         } else if (kOp == kExpertDx) {
@@ -655,48 +694,76 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
 }
 
 // ------------------------------------------------------------------------
-// Storing warps.  A thread holds one feature of 16 rows at a time; the 32 lanes
-// of a warp store 32 neighbouring features of a row.  Two or three warps share
-// a quarter of the features (a warp can read only the TMEM lanes of its number
-// modulo 4) and take chunks of rows in turn.
+// Storing warps.  A chunk is 16 rows of a quarter's 32 lanes; two or three warps
+// share a quarter (a warp can read only the TMEM lanes of its number modulo 4)
+// and take chunks in turn.  They come out of TMEM as fragments of 8 x 8 matrices
+// with the features along the matrices' rows; rounded, they are transposed on
+// their way into the warp's shared memory, and 16 bytes of a row at a time go on
+// to the output.  What the gated unit's gradient reads takes the same way back.
+// Sixteen 2-byte stores of a thread's feature kept the load and store units
+// busy for 800 to 1100 cycles a chunk in e4m3, where this takes xxx.
 //
-// Nothing in a chunk branches on a row: loads come from the last row where a
-// row lies behind the tile, so that sixteen independent rows hide each
-// other's latency, and only the stores are predicated.  (With a test per row
-// the exponentials, divisions and loads of a chunk ran one after another:
-// 2111 instead of 259 us for the
-// gradient through the gated unit of 64225 rows, 2048 to 1024.)
+// Outputs whose rows do not start on 16-byte boundaries, and the weights'
+// gradients in 32 bits or added to, are stored value by value.
 
-// Chunks of 16 rows: two or three warps a quarter make a tile's outputs in 3 to
-// 7 thousand cycles while the next tile's products take 8 to 16.
 constexpr int kChunk = 16;
 
-// 16 rows of one feature each to bf16, row j at out + j * stride.
-__device__ __forceinline__ void store_bf16(uint16_t* out, int64_t stride, const float* v, int left,
-                                           bool mine) {
-  if (left >= kChunk) {
-    if (mine)
+// Place of row r's 16-byte piece p in a chunk of 16 rows of 4 pieces, or of 2:
+// eight rows of one piece lie in different banks.
+__device__ __forceinline__ uint32_t piece4(int r, int p) { return r * 64 + ((p ^ (r >> 1 & 3)) << 4); }
+__device__ __forceinline__ uint32_t piece2(int r, int p) { return r * 32 + ((p ^ (r >> 2 & 1)) << 4); }
+
+// 16 rows of 32 features, v[2 fb + cb] the fragment of features 8 fb and rows
+// 8 cb; `rows` and `features` of them are the output's.
+__device__ __forceinline__ void put32(uint32_t buf, uint16_t* out, int64_t stride,
+                                      const uint32_t (&v)[8], int rows, int64_t features) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) out[j * stride] = f32_to_bf16(v[j]);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kChunk; ++j)
-      if (mine && j < left) out[j * stride] = f32_to_bf16(v[j]);
+  for (int cb = 0; cb < 2; ++cb) {
+    const uint32_t m[4] = {v[cb], v[2 + cb], v[4 + cb], v[6 + cb]};
+    store_matrices(buf + piece4(cb * 8 + (lane & 7), lane >> 3), m);
   }
+  __syncwarp();
+  const int piece = lane & 3;
+#pragma unroll
+  for (int cb = 0; cb < 2; ++cb) {
+    const int r = cb * 8 + (lane >> 2);
+    const uint4 w = load_shared(buf + piece4(r, piece));
+    if (r < rows && piece * 8 < features)
+      *reinterpret_cast<uint4*>(out + r * stride + piece * 8) = w;
+  }
+  __syncwarp();
 }
 
-// The same for half a chunk, `left` of whose rows are the tile's.
-__device__ __forceinline__ void store_half(uint16_t* out, int64_t stride, const float* v, int left,
-                                           bool mine) {
-  if (left >= kChunk / 2) {
-    if (mine)
+// 16 rows of 16 features, v[2 fb + cb].
+__device__ __forceinline__ void put16(uint32_t buf, uint16_t* out, int64_t stride,
+                                      const uint32_t (&v)[4], int rows, int64_t features) {
+  const int lane = threadIdx.x & 31;
+  // matrix 2 fb + cb
+  store_matrices(buf + piece2((lane >> 3 & 1) * 8 + (lane & 7), lane >> 4), v);
+  __syncwarp();
+  const int r = lane >> 1, piece = lane & 1;
+  const uint4 w = load_shared(buf + piece2(r, piece));
+  if (r < rows && piece * 8 < features) *reinterpret_cast<uint4*>(out + r * stride + piece * 8) = w;
+  __syncwarp();
+}
+
+// The same value by value: v[2 fb + cb]'s two values are rows 8 cb + 2 (lane % 4)
+// and the next of feature 8 fb + lane / 4.
+template <int kBlocks>
+__device__ __forceinline__ void put_values(uint16_t* out, int64_t stride,
+                                           const uint32_t (&v)[2 * kBlocks], int rows,
+                                           int64_t features) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
-      for (int j = 0; j < kChunk / 2; ++j) out[j * stride] = f32_to_bf16(v[j]);
-  } else {
+  for (int fb = 0; fb < kBlocks; ++fb)
 #pragma unroll
-    for (int j = 0; j < kChunk / 2; ++j)
-      if (mine && j < left) out[j * stride] = f32_to_bf16(v[j]);
-  }
+    for (int cb = 0; cb < 2; ++cb) {
+      const int f = fb * 8 + (lane >> 2), r = cb * 8 + 2 * (lane & 3);
+      if (f < features && r < rows) out[r * stride + f] = static_cast<uint16_t>(v[2 * fb + cb]);
+      if (f < features && r + 1 < rows)
+        out[(r + 1) * stride + f] = static_cast<uint16_t>(v[2 * fb + cb] >> 16);
+    }
 }
 
 // Scale of x's row behind grouped row r.
@@ -709,95 +776,70 @@ __device__ __forceinline__ float row_scale(const ExpertParams& e, int64_t r) {
   return e.x_scale[x];
 }
 
-// Eight rows of two features f and f + 1 (in one word) at p + j * stride, the
-// second feature only where `second`; words where rows start on 4-byte
-// boundaries.  Row j is row min(j, last).
-__device__ __forceinline__ void load_pairs(const uint16_t* p, int64_t stride, int last, bool wide,
-                                           bool second, uint32_t (&v)[kChunk / 2]) {
-  if (wide) {
-#pragma unroll
-    for (int j = 0; j < kChunk / 2; ++j)
-      v[j] = *reinterpret_cast<const uint32_t*>(p + min(j, last) * stride);
-  } else {
-#pragma unroll
-    for (int j = 0; j < kChunk / 2; ++j) {
-      const uint16_t* at = p + min(j, last) * stride;
-      v[j] = at[0] | (second ? static_cast<uint32_t>(at[1]) << 16 : 0u);
-    }
-  }
-}
-
-__device__ __forceinline__ void store_pairs(uint16_t* p, int64_t stride, int rows, bool wide,
-                                            bool second, const uint32_t (&v)[kChunk / 2]) {
-  if (wide && rows >= kChunk / 2) {
-#pragma unroll
-    for (int j = 0; j < kChunk / 2; ++j) *reinterpret_cast<uint32_t*>(p + j * stride) = v[j];
-  } else {
-#pragma unroll
-    for (int j = 0; j < kChunk / 2; ++j)
-      if (j < rows) {
-        p[j * stride] = static_cast<uint16_t>(v[j]);
-        if (second) p[j * stride + 1] = static_cast<uint16_t>(v[j] >> 16);
-      }
-  }
+__device__ __forceinline__ bool on_words(const void* p, int64_t stride) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) == 0 && (stride & 7) == 0;
 }
 
 template <int kOp, bool kGated, bool kE4m3, int kPair>
-__device__ void store_tiles(const TcParams& p, Shared& sh) {
+__device__ void store_tiles(const TcParams& p, Shared& sh, uint32_t staging) {
   constexpr bool kFused = kOp == kExpertForward && kGated;
   constexpr bool kReadsPre = kOp == kExpertDx && kGated;
-  constexpr int kHalf = kChunk / 2;
   const ExpertParams& e = p.e;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quadrant = warp & 3;
-  constexpr int kTurns = Roles<kPair>::kStoreWarps / 4;  // warps of a quarter
+  using R = Roles<kPair>;
+  constexpr int kStores = kReadsPre ? 8 : R::kStoreWarps;
+  constexpr int kTurns = kStores / 4;             // warps of a quarter
   constexpr int kStride = kTurns * kChunk;        // rows from chunk to chunk
   constexpr int kScales = (kMaxN / kChunk + 2 * kTurns - 1) / (2 * kTurns);
   const int first_row = ((warp - 2) >> 2) * kChunk;
-  const bool odd = lane & 1;
+  const uint32_t buf = staging + (warp - 2) * (kReadsPre ? 2048 : 1024), buf_up = buf + 1024;
   const int64_t features = kOp == kExpertForward ? e.n : e.k;
   uint16_t* y = static_cast<uint16_t*>(e.y);
-  const bool wide = kReadsPre && e.k % 2 == 0 &&
-                    ((reinterpret_cast<uintptr_t>(e.pre_in) | reinterpret_cast<uintptr_t>(y)) & 3) == 0;
+  const bool wide =
+      (features & 7) == 0 && on_words(y, kOp == kExpertDw ? e.y_stride | e.y_expert_stride : 0) &&
+      on_words(e.pre_out, 0) && on_words(e.pre_in, 0);
   int tiles = 0;
   Walk<kOp, kPair, kFused> walk;
   OutTile t;
   while (walk.next(p, sh, t)) {
-    // this thread's feature: of a gate (even lanes) or up (odd lanes) when they
-    // come in turn; the gated unit's gradient takes two lanes' features
-    // together, even lanes the first half of a chunk's rows, odd the second
-    const int64_t f = t.feature + (kFused     ? quadrant * 16 + (lane >> 1)
-                                   : kReadsPre ? quadrant * 32 + (lane & ~1)
-                                               : quadrant * 32 + lane);
-    const bool mine = f < features, second = f + 1 < features;
-    const int64_t f_in = mine ? f : wide ? features - 2 : features - 1;  // for loads
+    const int64_t f0 = t.feature + quadrant * (kFused ? 16 : 32);  // the warp's first feature
+    const int64_t left_f = features - f0;
     const int buffer = tiles & 1;
     const bool zero = t.depth == 0;
     // What the outputs need besides the products is fetched before them: e4m3's
     // scales (lanes 0 to 15 of row[q]: the rows of this warp's chunk 2 q, lanes
-    // 16 to 31 those of chunk 2 q + 1), and the first chunk
-    // of the gated unit's inputs; each further chunk one chunk ahead.
-    float scale = 1.0f, scale_up = 1.0f, row[kScales];
-    uint32_t gate_in[kHalf], up_in[kHalf];
+    // 16 to 31 those of chunk 2 q + 1), and the first chunk of the gated unit's
+    // inputs (rows lane / 4 and 8 more, features 8 (lane % 4) on); each further
+    // chunk one chunk ahead.
+    float row[kScales], scale[4];
+    uint4 gate_in[2], up_in[2];
     const auto fetch_pre = [&](int c) {
-      // the last row stands in for rows behind the tile
-      const int first = min(c + (odd ? kHalf : 0), t.rows - 1);
-      const uint16_t* pre = e.pre_in + (static_cast<int64_t>(t.row) + first) * 2 * e.k + f_in;
-      const bool two = f_in + 1 < features;
-      load_pairs(pre, 2 * e.k, t.rows - 1 - first, wide, two, gate_in);
-      load_pairs(pre + e.k, 2 * e.k, t.rows - 1 - first, wide, two, up_in);
+      const int64_t f = min(f0 + (lane & 3) * 8, features - 8);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        // the last row stands in for rows behind the tile
+        const int64_t r = t.row + min(c + i * 8 + (lane >> 2), t.rows - 1);
+        const uint16_t* pre = e.pre_in + r * 2 * e.k + f;
+        gate_in[i] = *reinterpret_cast<const uint4*>(pre);
+        up_in[i] = *reinterpret_cast<const uint4*>(pre + e.k);
+      }
     };
     if (!zero) {
       if (kE4m3) {
         const float* ws = e.w_scale + static_cast<int64_t>(t.group) * (kFused ? 2 : 1) * e.n;
-        scale = ws[f_in];
-        if (kFused) scale_up = ws[f_in + e.n];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          // fragment rows: features 8 i, or gates and ups of 8 (i / 2) in turn
+          const int64_t f = min(f0 + (kFused ? i / 2 : i) * 8 + (lane >> 2), features - 1);
+          scale[i] = ws[f + (kFused && (i & 1) ? e.n : 0)];
+        }
 #pragma unroll
         for (int q = 0; q < kScales; ++q) {
           const int at = first_row + (2 * q + (lane >> 4)) * kStride + (lane & 15);
           row[q] = at < t.rows ? row_scale(e, static_cast<int64_t>(t.row) + at) : 0.0f;
         }
       }
-      if (kReadsPre && first_row < t.rows) fetch_pre(first_row);
+      if (kReadsPre && wide && first_row < t.rows) fetch_pre(first_row);
       if (!wait(p, sh, &sh.acc_full[buffer], (tiles >> 1) & 1)) return;
       tc_fence_after();
       ++tiles;
@@ -808,113 +850,159 @@ __device__ void store_tiles(const TcParams& p, Shared& sh) {
     for (int c = first_row, chunk = 0; c < t.rows; c += kStride, ++chunk) {
       const int left = t.rows - c;
       const int64_t r = t.row + c;
-      float v[kChunk];
+      // v[h][4 cb + i]: lanes 16 h + 8 (i / 2) + lane / 4, rows 8 cb + 2 (lane % 4) + i % 2
+      float v[2][8];
       if (zero) {
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j) v[j] = 0.0f;
+        for (int i = 0; i < 16; ++i) v[i / 8][i % 8] = 0.0f;
       } else {
-        tmem_ld16(acc + c, v);
+        tmem_ld(acc + c, v[0]);
+        tmem_ld(acc + (16u << 16) + c, v[1]);
         tmem_ld_wait();
-      }
-      // e4m3: this chunk's row scales, row j's in lane from + j
-      float scales = 1.0f;
-      const int from = (chunk & 1) * kChunk;
-      if (kE4m3 && !zero) {
-        scales = row[0];
+        if (kE4m3) {
+          float scales = row[0];
 #pragma unroll
-        for (int q = 1; q < kScales; ++q)
-          if (chunk >> 1 == q) scales = row[q];
-      }
-      if (kE4m3 && !kFused && !zero) {
+          for (int q = 1; q < kScales; ++q)
+            if (chunk >> 1 == q) scales = row[q];
+          const int from = (chunk & 1) * kChunk + 2 * (lane & 3);
 #pragma unroll
-        for (int j = 0; j < kChunk; ++j)
-          v[j] *= __shfl_sync(0xffffffffu, scales, from + j) * scale;
-      }
-      if (kFused) {
-        // even lanes get the ups of the first rows, odd lanes the gates of the last
-        const int first = odd ? kHalf : 0;
-        float gate[kHalf], up[kHalf];
+          for (int i = 0; i < 4; ++i) {  // row 8 (i / 2) + i % 2 further on
+            const float xs = __shfl_sync(0xffffffffu, scales, from + (i >> 1) * 8 + (i & 1));
+            const int at = (i >> 1) * 4 + (i & 1);
 #pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-          const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[kHalf + j], 1);
-          gate[j] = odd ? got : v[j];
-          up[j] = odd ? v[kHalf + j] : got;
-          if (kE4m3) {
-            const float xs = __shfl_sync(0xffffffffu, scales, from + first + j);
-            gate[j] *= xs * scale;
-            up[j] *= xs * scale_up;
+            for (int h = 0; h < 2; ++h) {
+              v[h][at] *= xs * scale[2 * h];
+              v[h][at + 2] *= xs * scale[2 * h + 1];
+            }
           }
         }
-        if (e.pre_out) {
-          uint16_t* pre = e.pre_out + (r + first) * 2 * e.n + f;
-          store_half(pre, 2 * e.n, gate, left - first, mine);
-          store_half(pre + e.n, 2 * e.n, up, left - first, mine);
+      }
+      if constexpr (kFused) {
+        uint32_t gate[4], up[4], out[4];  // of features 8 h and rows 8 cb at 2 h + cb
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float* w = v[i >> 1] + (i & 1) * 4;
+          gate[i] = pack_bf16(w[0], w[1]);
+          up[i] = pack_bf16(w[2], w[3]);
+          out[i] = pack_bf16(silu(w[0]) * w[2], silu(w[1]) * w[3]);
         }
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) gate[j] = silu(gate[j]) * up[j];
-        store_half(y + (r + first) * e.n + f, e.n, gate, left - first, mine);
-      } else if (kOp == kExpertForward) {
-        store_bf16(y + r * e.n + f, e.n, v, left, mine);
-      } else if (kReadsPre) {
-        uint32_t gate[kHalf], up[kHalf];
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-          gate[j] = gate_in[j];
-          up[j] = up_in[j];
+        uint16_t* pre = e.pre_out + r * 2 * e.n + f0;
+        uint16_t* to = y + r * e.n + f0;
+        if (wide) {
+          if (e.pre_out) {
+            put16(buf, pre, 2 * e.n, gate, left, left_f);
+            put16(buf, pre + e.n, 2 * e.n, up, left, left_f);
+          }
+          put16(buf, to, e.n, out, left, left_f);
+        } else {
+          if (e.pre_out) {
+            put_values<2>(pre, 2 * e.n, gate, left, left_f);
+            put_values<2>(pre + e.n, 2 * e.n, up, left, left_f);
+          }
+          put_values<2>(to, e.n, out, left, left_f);
         }
-        if (!zero && c + kStride < t.rows) fetch_pre(c + kStride);
-#pragma unroll
-        for (int j = 0; j < kHalf; ++j) {
-          const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[kHalf + j], 1);
-          const float d[2] = {odd ? got : v[j], odd ? v[kHalf + j] : got};
-          float dg[2], du[2];
+        continue;
+      }
+      uint32_t out[8];  // of features 8 fb and rows 8 cb at 2 fb + cb
+      if constexpr (kReadsPre) {
+        uint32_t gate[8] = {}, up[8] = {};
+        if (!zero && wide) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
-            const float g = i ? bf16_hi(gate[j]) : bf16_lo(gate[j]);
-            const float u = i ? bf16_hi(up[j]) : bf16_lo(up[j]);
-            const float s = sigmoid(g), ds = d[i] * s;
-            du[i] = ds * g;
-            dg[i] = ds * u * (1.0f + g * (1.0f - s));
+            const uint32_t at = piece4(i * 8 + (lane >> 2), lane & 3);
+            store_shared(buf + at, gate_in[i]);
+            store_shared(buf_up + at, up_in[i]);
           }
-          gate[j] = zero ? 0u : pack_bf16(dg[0], dg[1]);
-          up[j] = zero ? 0u : pack_bf16(du[0], du[1]);
-        }
-        const int first = odd ? kHalf : 0;
-        uint16_t* to = y + (r + first) * 2 * e.k + f;
-        if (mine) {
-          store_pairs(to, 2 * e.k, left - first, wide, second, gate);
-          store_pairs(to + e.k, 2 * e.k, left - first, wide, second, up);
-        }
-      } else if (kOp == kExpertDx) {
-        store_bf16(y + r * e.k + f, e.k, v, left, mine);
-      } else {
-        const int64_t at = t.group * e.y_expert_stride + r * e.y_stride + f;
-        if (e.f32_out) {
-          float* out = static_cast<float*>(e.y) + at;
-          if (e.accumulate) {
-            float old[kChunk];
+          if (c + kStride < t.rows) fetch_pre(c + kStride);
+          __syncwarp();
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j)
-              old[j] = mine && j < left ? out[j * e.y_stride] : 0.0f;
+          for (int cb = 0; cb < 2; ++cb) {
+            const uint32_t at = piece4(cb * 8 + (lane & 7), lane >> 3);
+            uint32_t m[4];
+            load_matrices(buf + at, m);
 #pragma unroll
-            for (int j = 0; j < kChunk; ++j) v[j] += old[j];
+            for (int fb = 0; fb < 4; ++fb) gate[2 * fb + cb] = m[fb];
+            load_matrices(buf_up + at, m);
+#pragma unroll
+            for (int fb = 0; fb < 4; ++fb) up[2 * fb + cb] = m[fb];
           }
+          __syncwarp();
+        } else if (!zero) {
 #pragma unroll
-          for (int j = 0; j < kChunk; ++j)
-            if (mine && j < left) out[j * e.y_stride] = v[j];
+          for (int i = 0; i < 16; ++i) {
+            const int64_t f = min(f0 + (i >> 2) * 8 + (lane >> 2), features - 1);
+            const int64_t at = t.row + min(c + (i >> 1 & 1) * 8 + 2 * (lane & 3) + (i & 1),
+                                           t.rows - 1);
+            const uint16_t* pre = e.pre_in + at * 2 * e.k + f;
+            gate[i >> 1] |= static_cast<uint32_t>(pre[0]) << (16 * (i & 1));
+            up[i >> 1] |= static_cast<uint32_t>(pre[e.k]) << (16 * (i & 1));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float* d = v[i >> 2] + (i & 1) * 4 + (i >> 1 & 1) * 2;
+          float dg[2], du[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float g = j ? bf16_hi(gate[i]) : bf16_lo(gate[i]);
+            const float u = j ? bf16_hi(up[i]) : bf16_lo(up[i]);
+            const float s = sigmoid(g), ds = d[j] * s;
+            du[j] = ds * g;
+            dg[j] = ds * u * (1.0f + g * (1.0f - s));
+          }
+          out[i] = zero ? 0u : pack_bf16(dg[0], dg[1]);
+          up[i] = zero ? 0u : pack_bf16(du[0], du[1]);
+        }
+        uint16_t* to = y + r * 2 * e.k + f0;
+        if (wide) {
+          put32(buf, to, 2 * e.k, out, left, left_f);
+          put32(buf_up, to + e.k, 2 * e.k, up, left, left_f);
         } else {
-          uint16_t* out = y + at;
-          if (e.accumulate) {
-            uint16_t old[kChunk];
-#pragma unroll
-            for (int j = 0; j < kChunk; ++j) old[j] = mine && j < left ? out[j * e.y_stride] : 0;
-#pragma unroll
-            for (int j = 0; j < kChunk; ++j) v[j] += bf16_to_f32(old[j]);
-          }
-          store_bf16(out, e.y_stride, v, left, mine);
+          put_values<4>(to, 2 * e.k, out, left, left_f);
+          put_values<4>(to + e.k, 2 * e.k, up, left, left_f);
         }
+        continue;
       }
-      __syncwarp();
+      if (kOp == kExpertDw && (e.f32_out || e.accumulate)) {
+        const int64_t base = t.group * e.y_expert_stride + r * e.y_stride + f0;
+        // one row of eight features at a time: i counts (h, cb, second lanes, second row)
+        float old[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int f = (i >> 3) * 16 + (i >> 1 & 1) * 8 + (lane >> 2);
+          const int rr = (i >> 2 & 1) * 8 + 2 * (lane & 3) + (i & 1);
+          const int64_t at = base + rr * e.y_stride + f;
+          old[i] = 0.0f;
+          if (e.accumulate && rr < left && f < left_f)
+            old[i] = e.f32_out ? static_cast<const float*>(e.y)[at] : bf16_to_f32(y[at]);
+        }
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int f = (i >> 3) * 16 + (i >> 1 & 1) * 8 + (lane >> 2);
+          const int rr = (i >> 2 & 1) * 8 + 2 * (lane & 3) + (i & 1);
+          const int64_t at = base + rr * e.y_stride + f;
+          const float sum = old[i] + v[i >> 3][i & 7];
+          if (rr < left && f < left_f) {
+            if (e.f32_out)
+              static_cast<float*>(e.y)[at] = sum;
+            else
+              y[at] = f32_to_bf16(sum);
+          }
+        }
+        continue;
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float* w = v[i >> 2] + (i & 1) * 4 + (i >> 1 & 1) * 2;
+        out[i] = pack_bf16(w[0], w[1]);
+      }
+      const int64_t stride = kOp == kExpertDw ? e.y_stride : features;
+      uint16_t* to =
+          y + (kOp == kExpertDw ? t.group * e.y_expert_stride : 0) + r * stride + f0;
+      if (wide)
+        put32(buf, to, stride, out, left, left_f);
+      else
+        put_values<4>(to, stride, out, left, left_f);
     }
     if (!zero) {
       tc_fence_before();
@@ -935,10 +1023,13 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
                 const __grid_constant__ CUtensorMap map_b) {
   extern __shared__ unsigned char raw[];
   __shared__ Shared sh;
-  // stages on 1024-byte boundaries: the swizzle's period
+  // stages on 1024-byte boundaries: the swizzle's period; then the storing warps' memory
   const uint32_t base = smem_addr(raw);
   const uint32_t ring = (base + 1023) & ~1023u;
+  const uint32_t staging = ring + p.stages * p.stage_bytes;
   unsigned char* ring_ptr = raw + (ring - base);
+  // storing warps at work (see kStagingBytes)
+  constexpr int kStores = kOp == kExpertDx && kGated ? 8 : Roles<kPair>::kStoreWarps;
   constexpr int kLoadB = Roles<kPair>::kLoadB;
   const int warp = threadIdx.x >> 5;
   const bool gather = kOp == kExpertForward && kPair == 1 && p.e.row_tokens != nullptr;
@@ -951,7 +1042,7 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.acc_full[i], 1);
-      mbar_init(&sh.acc_empty[i], Roles<kPair>::kStoreWarps * kPair);
+      mbar_init(&sh.acc_empty[i], kStores * kPair);
     }
     sh.stop = 0;
     fence_barrier_init();
@@ -981,8 +1072,8 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
     load_tiles<kOp, kGated, kE4m3, kPair, true>(p, &map_a, sh, ring);
   else if (warp == 1 && (kPair == 1 || cluster_rank() == 0))
     multiply<kOp, kGated, kE4m3, kPair>(p, sh, ring);
-  else if (warp >= 2 && warp < kLoadB)
-    store_tiles<kOp, kGated, kE4m3, kPair>(p, sh);
+  else if (warp >= 2 && warp < 2 + kStores)
+    store_tiles<kOp, kGated, kE4m3, kPair>(p, sh, staging);
   else if (warp == kLoadB && !gather)
     load_tiles<kOp, kGated, kE4m3, kPair, false>(p, &map_b, sh, ring);
   else if (warp > kLoadB && kOp == kExpertDw)
@@ -1024,18 +1115,19 @@ Encode encode() {
 }
 
 // A map of matrices of rows x columns, `planes` of them (0: one, without the
-// dimension); boxes of 128 bytes by box_rows.  With `parts` 2 a box's rows are
-// row i of the first part and row i of the second in turn, part_stride apart.
+// dimension); boxes of 128 bytes by box_rows.  With part_stride a box is eight
+// rows of the first part and the same eight of the second, part_stride further
+// on, in turn (rows a multiple of 8).
 bool make_map(CUtensorMap* map, const void* base, bool e4m3, int64_t columns, int64_t rows,
-              int64_t stride, int64_t planes, int64_t plane_stride, int box_rows, int parts = 1,
+              int64_t stride, int64_t planes, int64_t plane_stride, int box_rows,
               int64_t part_stride = 0) {
   const int64_t size = e4m3 ? 1 : 2;
   if ((reinterpret_cast<uintptr_t>(base) & 15) || stride * size % 16 ||
       (planes > 1 && (plane_stride * size % 16 || plane_stride <= 0)) || columns < 1 || rows < 1)
     return false;
-  cuuint64_t dims[4], strides[3];
-  cuuint32_t box[4];
-  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  cuuint64_t dims[5], strides[4];
+  cuuint32_t box[5];
+  const cuuint32_t ones[5] = {1, 1, 1, 1, 1};
   int rank = 0;
   const auto add = [&](int64_t n, int64_t apart, int64_t of_box) {
     if (rank) strides[rank - 1] = static_cast<cuuint64_t>(apart * size);
@@ -1043,9 +1135,14 @@ bool make_map(CUtensorMap* map, const void* base, bool e4m3, int64_t columns, in
     box[rank++] = static_cast<cuuint32_t>(of_box);
   };
   add(columns, 0, kRowBytes / size);
-  if (parts == 2) add(2, part_stride, 2);
-  add(rows, stride, box_rows / parts);
-  if (planes > 0) add(planes, planes > 1 ? plane_stride : stride * rows * parts, 1);
+  if (part_stride) {
+    add(8, stride, 8);
+    add(2, part_stride, 2);
+    add(rows / 8, 8 * stride, box_rows / 16);
+  } else {
+    add(rows, stride, box_rows);
+  }
+  if (planes > 0) add(planes, planes > 1 ? plane_stride : stride * rows * 2, 1);
   return encode()(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                   static_cast<cuuint32_t>(rank), const_cast<void*>(base), dims, strides, box, ones,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -1057,12 +1154,12 @@ template <int kOp, bool kGated, bool kE4m3, int kPair>
 int launch_at(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid,
               cudaStream_t s) {
   const cudaError_t err =
-      allow_shared<k_expert_tc<kOp, kGated, kE4m3, kPair>>(kSmemLimit - 14 * 1024);
+      allow_shared<k_expert_tc<kOp, kGated, kE4m3, kPair>>(kSmemLimit - kStaticBytes);
   if (err != cudaSuccess) return err;
   cudaLaunchConfig_t config{};
   config.gridDim = dim3(static_cast<unsigned>(grid));
   config.blockDim = dim3(Roles<kPair>::kThreads);
-  config.dynamicSmemBytes = static_cast<size_t>(p.stages) * p.stage_bytes + 1024;
+  config.dynamicSmemBytes = static_cast<size_t>(p.stages) * p.stage_bytes + 1024 + kStagingBytes;
   config.stream = s;
   cudaLaunchAttribute pair{};
   pair.id = cudaLaunchAttributeClusterDimension;
@@ -1121,7 +1218,7 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   p.a_bytes = kTileM * kRowBytes;
   const int pair = small || e.row_tokens ? 1 : 2;
   p.stage_bytes = p.a_bytes + p.tile_n / pair * kRowBytes;
-  p.stages = (kSmemLimit - 16 * 1024) / p.stage_bytes;
+  p.stages = (kSmemLimit - kStaticBytes - kStagingBytes - 1024) / p.stage_bytes;
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   const int64_t tile_m = (fused ? kTileM / 2 : kTileM) * pair;
   const int64_t m_tiles = (features + tile_m - 1) / tile_m;
@@ -1132,12 +1229,20 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   p.m_tiles = static_cast<int32_t>(m_tiles);
   p.m_tiles_inverse = static_cast<uint32_t>(((uint64_t(1) << 32) + m_tiles - 1) / m_tiles);
   p.n_tiles = static_cast<int32_t>(n_tiles);
+  p.pieces = fused && e.n % 8 != 0;
 
   CUtensorMap a, b;
   bool ok;
   if (e.op == kExpertForward)
-    ok = make_map(&a, e.w, e.e4m3, e.k, e.n, e.w_stride, e.experts, e.w_expert_stride, kTileM,
-                  fused ? 2 : 1, e.n * e.w_stride) &&
+    // gates and ups in turn: one load, or where n is no multiple of 8 sixteen
+    // of eight rows each, which may read past the gates (into the ups: not
+    // stored) but not past an expert's last row
+    ok = (!fused     ? make_map(&a, e.w, e.e4m3, e.k, e.n, e.w_stride, e.experts,
+                                e.w_expert_stride, kTileM)
+          : p.pieces ? make_map(&a, e.w, e.e4m3, e.k, 2 * e.n, e.w_stride, e.experts,
+                                e.w_expert_stride, 8)
+                     : make_map(&a, e.w, e.e4m3, e.k, e.n, e.w_stride, e.experts,
+                                e.w_expert_stride, kTileM, e.n * e.w_stride)) &&
          make_map(&b, e.x, e.e4m3, e.k, e.x_rows, e.x_stride, 0, 0, kBoxRows);
   else if (e.op == kExpertDx)
     ok = make_map(&a, e.w, false, e.k, e.n, e.w_stride, e.experts, e.w_expert_stride, 64) &&
