@@ -42,8 +42,10 @@ constexpr int kGatherWarps = 4;
 // Warps: 0 loads A, 1 issues the products, then the storing warps, one that
 // loads B, and those that gather rows (single blocks) or clear (pairs).
 // A storing warp has 1 KB of shared memory, two where it reads what the gated
-// unit's gradient needs (and then there are eight).
-constexpr int kStagingBytes = 16 * 1024;
+// unit's gradient needs (and then there are eight); all of them 6 KB of scales.
+constexpr int kOutputBytes = 16 * 1024;
+constexpr int kScaleBytes = 6 * 1024;
+constexpr int kStagingBytes = kOutputBytes + kScaleBytes;
 template <int kPair>
 struct Roles {
   static constexpr int kStoreWarps = kPair == 2 ? 12 : 8;
@@ -68,6 +70,7 @@ struct TcParams {
   int32_t m_tiles;       // tiles of the feature dimension
   uint32_t m_tiles_inverse;  // 2^32 / m_tiles, rounded up (of 2 and more)
   int32_t n_tiles;       // dw: tiles of its rows
+  int32_t bulk;          // outputs leave by TMA
   int32_t pieces;        // gated: A comes eight rows a load (n is no multiple of 8)
 };
 
@@ -127,10 +130,32 @@ __device__ __forceinline__ void tma_5d(uint32_t dst, const CUtensorMap* map, int
         : "memory");
 }
 
+// A box from shared memory to a matrix; what lies outside the matrix is left out.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, uint32_t src, int32_t x,
+                                             int32_t y) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::
+                   "l"(map),
+               "r"(x), "r"(y), "r"(src)
+               : "memory");
+}
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int32_t x,
+                                             int32_t y, int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(
+          map),
+      "r"(x), "r"(y), "r"(z), "r"(src)
+      : "memory");
+}
+
 // Arrives on `bar` (an arrival it counts on) when this thread's copies so far
 // have landed.
 __device__ __forceinline__ void copy_arrive(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar))
+               : "memory");
+}
+// Four bytes to shared memory, of which the first `bytes` come from `src`.
+__device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                : "memory");
 }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
@@ -243,6 +268,11 @@ __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&v)[4]) {
                : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                : "r"(addr)
                : "memory");
+}
+__device__ __forceinline__ float load_float(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
 }
 __device__ __forceinline__ uint4 load_shared(uint32_t addr) {
   uint4 v;
@@ -700,8 +730,11 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
 // with the features along the matrices' rows; rounded, they are transposed on
 // their way into the warp's shared memory, and 16 bytes of a row at a time go on
 // to the output.  What the gated unit's gradient reads takes the same way back.
-// Sixteen 2-byte stores of a thread's feature kept the load and store units
-// busy for 800 to 1100 cycles a chunk in e4m3, where this takes xxx.
+// (Sixteen 2-byte stores of a thread's feature: 147 instead of 137 us for the
+// e4m3 product of 64225 rows, 1024 to 2048.)  Large groups' plain outputs leave
+// by TMA, whose 64-byte swizzle is the order in which they lie there, where a
+// chunk's 16 rows are all the group's: the load and store units, which the
+// matrices and the scales' shuffles need, see no global store.
 //
 // Outputs whose rows do not start on 16-byte boundaries, and the weights'
 // gradients in 32 bits or added to, are stored value by value.
@@ -714,15 +747,21 @@ __device__ __forceinline__ uint32_t piece4(int r, int p) { return r * 64 + ((p ^
 __device__ __forceinline__ uint32_t piece2(int r, int p) { return r * 32 + ((p ^ (r >> 2 & 1)) << 4); }
 
 // 16 rows of 32 features, v[2 fb + cb] the fragment of features 8 fb and rows
-// 8 cb; `rows` and `features` of them are the output's.
-__device__ __forceinline__ void put32(uint32_t buf, uint16_t* out, int64_t stride,
-                                      const uint32_t (&v)[8], int rows, int64_t features) {
+// 8 cb, to shared memory.
+__device__ __forceinline__ void stage32(uint32_t buf, const uint32_t (&v)[8]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int cb = 0; cb < 2; ++cb) {
     const uint32_t m[4] = {v[cb], v[2 + cb], v[4 + cb], v[6 + cb]};
     store_matrices(buf + piece4(cb * 8 + (lane & 7), lane >> 3), m);
   }
+}
+
+// And on to the output, of which `rows` and `features` are.
+__device__ __forceinline__ void put32(uint32_t buf, uint16_t* out, int64_t stride,
+                                      const uint32_t (&v)[8], int rows, int64_t features) {
+  const int lane = threadIdx.x & 31;
+  stage32(buf, v);
   __syncwarp();
   const int piece = lane & 3;
 #pragma unroll
@@ -766,14 +805,10 @@ __device__ __forceinline__ void put_values(uint16_t* out, int64_t stride,
     }
 }
 
-// Scale of x's row behind grouped row r.
-__device__ __forceinline__ float row_scale(const ExpertParams& e, int64_t r) {
-  int64_t x = r;
-  if (e.row_tokens) {
-    x = e.row_tokens[r];
-    if (x < 0 || x >= e.x_rows) return 0.0f;
-  }
-  return e.x_scale[x];
+// Row of x behind grouped row r; -1: none.
+__device__ __forceinline__ int64_t scale_row(const ExpertParams& e, int64_t r) {
+  const int64_t x = e.row_tokens ? e.row_tokens[r] : r;
+  return x < e.x_rows ? x : -1;
 }
 
 __device__ __forceinline__ bool on_words(const void* p, int64_t stride) {
@@ -781,7 +816,8 @@ __device__ __forceinline__ bool on_words(const void* p, int64_t stride) {
 }
 
 template <int kOp, bool kGated, bool kE4m3, int kPair>
-__device__ void store_tiles(const TcParams& p, Shared& sh, uint32_t staging) {
+__device__ void store_tiles(const TcParams& p, const CUtensorMap* map_y, Shared& sh,
+                            uint32_t staging) {
   constexpr bool kFused = kOp == kExpertForward && kGated;
   constexpr bool kReadsPre = kOp == kExpertDx && kGated;
   const ExpertParams& e = p.e;
@@ -798,51 +834,69 @@ __device__ void store_tiles(const TcParams& p, Shared& sh, uint32_t staging) {
   const bool wide =
       (features & 7) == 0 && on_words(y, kOp == kExpertDw ? e.y_stride | e.y_expert_stride : 0) &&
       on_words(e.pre_out, 0) && on_words(e.pre_in, 0);
+  // What the outputs need besides the products is fetched ahead: e4m3's scales
+  // for the next tile while this one is stored, into shared memory (32 features'
+  // or 16 gates' and 16 ups', then rows: word 32 + 32 q + l is that of row l % 16
+  // of this warp's chunk 2 q + l / 16), and the gated unit's inputs for the first
+  // chunk before the products, then one chunk ahead (rows lane / 4 and 8 more,
+  // features 8 (lane % 4) on).  Loads of scales into registers were waited for in
+  // every first chunk, 2000 cycles a tile.
+  constexpr int kOwnScales = 128 * (1 + kScales);
+  static_assert(kStores * kOwnScales <= kScaleBytes, "the scales' memory");
+  const uint32_t scales_at = staging + kOutputBytes + (warp - 2) * kOwnScales;
+  const auto fetch_scales = [&](const OutTile& t) {
+    const int64_t f0 = t.feature + quadrant * (kFused ? 16 : 32) + (kFused ? lane & 15 : lane);
+    const float* ws = e.w_scale + static_cast<int64_t>(t.group) * (kFused ? 2 : 1) * e.n;
+    copy4(scales_at + lane * 4, ws + min(f0, features - 1) + (kFused && lane >= 16 ? e.n : 0), 4);
+#pragma unroll
+    for (int q = 0; q < kScales; ++q) {
+      const int at = first_row + (2 * q + (lane >> 4)) * kStride + (lane & 15);
+      const int64_t x = at < t.rows ? scale_row(e, static_cast<int64_t>(t.row) + at) : -1;
+      copy4(scales_at + 128 + q * 128 + lane * 4, e.x_scale + (x < 0 ? 0 : x), x < 0 ? 0 : 4);
+    }
+  };
+  uint4 gate_in[2], up_in[2];
+  const auto fetch_pre = [&](const OutTile& t, int c) {
+    const int64_t f0 = t.feature + quadrant * 32 + (lane & 3) * 8, f = min(f0, features - 8);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      // the last row stands in for rows behind the tile
+      const int64_t r = t.row + min(c + i * 8 + (lane >> 2), t.rows - 1);
+      const uint16_t* pre = e.pre_in + r * 2 * e.k + f;
+      gate_in[i] = *reinterpret_cast<const uint4*>(pre);
+      up_in[i] = *reinterpret_cast<const uint4*>(pre + e.k);
+    }
+  };
   int tiles = 0;
   Walk<kOp, kPair, kFused> walk;
-  OutTile t;
-  while (walk.next(p, sh, t)) {
+  OutTile t, next;
+  bool have = walk.next(p, sh, next);
+  if (kE4m3 && have && next.depth > 0) fetch_scales(next);
+  while (have) {
+    t = next;
     const int64_t f0 = t.feature + quadrant * (kFused ? 16 : 32);  // the warp's first feature
     const int64_t left_f = features - f0;
     const int buffer = tiles & 1;
     const bool zero = t.depth == 0;
-    // What the outputs need besides the products is fetched before them: e4m3's
-    // scales (lanes 0 to 15 of row[q]: the rows of this warp's chunk 2 q, lanes
-    // 16 to 31 those of chunk 2 q + 1), and the first chunk of the gated unit's
-    // inputs (rows lane / 4 and 8 more, features 8 (lane % 4) on); each further
-    // chunk one chunk ahead.
-    float row[kScales], scale[4];
-    uint4 gate_in[2], up_in[2];
-    const auto fetch_pre = [&](int c) {
-      const int64_t f = min(f0 + (lane & 3) * 8, features - 8);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        // the last row stands in for rows behind the tile
-        const int64_t r = t.row + min(c + i * 8 + (lane >> 2), t.rows - 1);
-        const uint16_t* pre = e.pre_in + r * 2 * e.k + f;
-        gate_in[i] = *reinterpret_cast<const uint4*>(pre);
-        up_in[i] = *reinterpret_cast<const uint4*>(pre + e.k);
-      }
-    };
+    have = walk.next(p, sh, next);
     if (!zero) {
-      if (kE4m3) {
-        const float* ws = e.w_scale + static_cast<int64_t>(t.group) * (kFused ? 2 : 1) * e.n;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          // fragment rows: features 8 i, or gates and ups of 8 (i / 2) in turn
-          const int64_t f = min(f0 + (kFused ? i / 2 : i) * 8 + (lane >> 2), features - 1);
-          scale[i] = ws[f + (kFused && (i & 1) ? e.n : 0)];
-        }
-#pragma unroll
-        for (int q = 0; q < kScales; ++q) {
-          const int at = first_row + (2 * q + (lane >> 4)) * kStride + (lane & 15);
-          row[q] = at < t.rows ? row_scale(e, static_cast<int64_t>(t.row) + at) : 0.0f;
-        }
-      }
-      if (kReadsPre && wide && first_row < t.rows) fetch_pre(first_row);
-      if (!wait(p, sh, &sh.acc_full[buffer], (tiles >> 1) & 1)) return;
+      if (kReadsPre && wide && first_row < t.rows) fetch_pre(t, first_row);
+      if (!wait(p, sh, &sh.acc_full[buffer], (tiles >> 1) & 1)) break;
       tc_fence_after();
       ++tiles;
+    }
+    float row[kScales], scale[4];
+    if (kE4m3) {
+      copy_wait_all();
+      __syncwarp();
+#pragma unroll
+      for (int q = 0; q < kScales; ++q) row[q] = load_float(scales_at + 128 + q * 128 + lane * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // of the fragments' features: 8 i on, or gate and up of 8 (i / 2) on
+        scale[i] = load_float(scales_at + 4 * ((kFused ? (i & 1) * 16 + i / 2 * 8 : i * 8) +
+                                               (lane >> 2)));
+      __syncwarp();
+      if (have && next.depth > 0) fetch_scales(next);
     }
     const uint32_t acc =
         sh.tmem + buffer * kMaxN + (static_cast<uint32_t>(quadrant * 32) << 16);
@@ -913,7 +967,7 @@ __device__ void store_tiles(const TcParams& p, Shared& sh, uint32_t staging) {
             store_shared(buf + at, gate_in[i]);
             store_shared(buf_up + at, up_in[i]);
           }
-          if (c + kStride < t.rows) fetch_pre(c + kStride);
+          if (c + kStride < t.rows) fetch_pre(t, c + kStride);
           __syncwarp();
 #pragma unroll
           for (int cb = 0; cb < 2; ++cb) {
@@ -996,6 +1050,23 @@ __device__ void store_tiles(const TcParams& p, Shared& sh, uint32_t staging) {
         const float* w = v[i >> 2] + (i & 1) * 4 + (i >> 1 & 1) * 2;
         out[i] = pack_bf16(w[0], w[1]);
       }
+      if (p.bulk) {  // the copies of the chunk before have read the buffer
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+      }
+      if (p.bulk && (kOp == kExpertDw || left >= kChunk)) {
+        stage32(buf, out);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0 && left_f > 0) {
+          if (kOp == kExpertDw)
+            tma_store_3d(map_y, buf, static_cast<int>(f0), static_cast<int>(r), t.group);
+          else
+            tma_store_2d(map_y, buf, static_cast<int>(f0), static_cast<int>(r));
+          bulk_commit();
+        }
+        continue;
+      }
       const int64_t stride = kOp == kExpertDw ? e.y_stride : features;
       uint16_t* to =
           y + (kOp == kExpertDw ? t.group * e.y_expert_stride : 0) + r * stride + f0;
@@ -1015,12 +1086,15 @@ __device__ void store_tiles(const TcParams& p, Shared& sh, uint32_t staging) {
       }
     }
   }
+  // nothing of this warp's is under way when its block's memory goes
+  if (p.bulk && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 template <int kOp, bool kGated, bool kE4m3, int kPair>
 __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
     k_expert_tc(const TcParams p, const __grid_constant__ CUtensorMap map_a,
-                const __grid_constant__ CUtensorMap map_b) {
+                const __grid_constant__ CUtensorMap map_b,
+                const __grid_constant__ CUtensorMap map_y) {
   extern __shared__ unsigned char raw[];
   __shared__ Shared sh;
   // stages on 1024-byte boundaries: the swizzle's period; then the storing warps' memory
@@ -1073,7 +1147,7 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
   else if (warp == 1 && (kPair == 1 || cluster_rank() == 0))
     multiply<kOp, kGated, kE4m3, kPair>(p, sh, ring);
   else if (warp >= 2 && warp < 2 + kStores)
-    store_tiles<kOp, kGated, kE4m3, kPair>(p, sh, staging);
+    store_tiles<kOp, kGated, kE4m3, kPair>(p, &map_y, sh, staging);
   else if (warp == kLoadB && !gather)
     load_tiles<kOp, kGated, kE4m3, kPair, false>(p, &map_b, sh, ring);
   else if (warp > kLoadB && kOp == kExpertDw)
@@ -1150,9 +1224,28 @@ bool make_map(CUtensorMap* map, const void* base, bool e4m3, int64_t columns, in
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// A map of bf16 outputs, boxes of 16 rows of 32 features.
+bool make_out_map(CUtensorMap* map, void* base, int64_t columns, int64_t rows, int64_t stride,
+                  int64_t planes, int64_t plane_stride) {
+  if (planes > 1 && plane_stride <= 0) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(planes)};
+  const cuuint64_t strides[2] = {
+      static_cast<cuuint64_t>(2 * stride),
+      static_cast<cuuint64_t>(2 * (planes > 1 ? plane_stride : stride * rows))};
+  const cuuint32_t box[3] = {32, 16, 1}, ones[3] = {1, 1, 1};
+  return encode()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, base, dims, strides, box,
+                  ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+struct Maps {
+  CUtensorMap a, b, y;
+};
+
 template <int kOp, bool kGated, bool kE4m3, int kPair>
-int launch_at(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid,
-              cudaStream_t s) {
+int launch_at(const TcParams& p, const Maps& m, int grid, cudaStream_t s) {
   const cudaError_t err =
       allow_shared<k_expert_tc<kOp, kGated, kE4m3, kPair>>(kSmemLimit - kStaticBytes);
   if (err != cudaSuccess) return err;
@@ -1167,24 +1260,23 @@ int launch_at(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int
   pair.val.clusterDim.y = pair.val.clusterDim.z = 1;
   config.attrs = &pair;
   config.numAttrs = kPair == 2 ? 1 : 0;
-  return cudaLaunchKernelEx(&config, k_expert_tc<kOp, kGated, kE4m3, kPair>, p, a, b);
+  return cudaLaunchKernelEx(&config, k_expert_tc<kOp, kGated, kE4m3, kPair>, p, m.a, m.b, m.y);
 }
 
 template <int kPair>
-int launch_with(const TcParams& p, const CUtensorMap& a, const CUtensorMap& b, int grid,
-                cudaStream_t s) {
+int launch_with(const TcParams& p, const Maps& m, int grid, cudaStream_t s) {
   const ExpertParams& e = p.e;  // dw always takes pairs
   if (e.op == kExpertForward) {
     if (e.e4m3)
-      return e.gated ? launch_at<kExpertForward, true, true, kPair>(p, a, b, grid, s)
-                     : launch_at<kExpertForward, false, true, kPair>(p, a, b, grid, s);
-    return e.gated ? launch_at<kExpertForward, true, false, kPair>(p, a, b, grid, s)
-                   : launch_at<kExpertForward, false, false, kPair>(p, a, b, grid, s);
+      return e.gated ? launch_at<kExpertForward, true, true, kPair>(p, m, grid, s)
+                     : launch_at<kExpertForward, false, true, kPair>(p, m, grid, s);
+    return e.gated ? launch_at<kExpertForward, true, false, kPair>(p, m, grid, s)
+                   : launch_at<kExpertForward, false, false, kPair>(p, m, grid, s);
   }
   if (e.op == kExpertDx)
-    return e.gated ? launch_at<kExpertDx, true, false, kPair>(p, a, b, grid, s)
-                   : launch_at<kExpertDx, false, false, kPair>(p, a, b, grid, s);
-  return launch_at<kExpertDw, false, false, 2>(p, a, b, grid, s);
+    return e.gated ? launch_at<kExpertDx, true, false, kPair>(p, m, grid, s)
+                   : launch_at<kExpertDx, false, false, kPair>(p, m, grid, s);
+  return launch_at<kExpertDw, false, false, 2>(p, m, grid, s);
 }
 
 int sm_count() {
@@ -1231,7 +1323,8 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   p.n_tiles = static_cast<int32_t>(n_tiles);
   p.pieces = fused && e.n % 8 != 0;
 
-  CUtensorMap a, b;
+  Maps m;
+  CUtensorMap &a = m.a, &b = m.b;
   bool ok;
   if (e.op == kExpertForward)
     // gates and ups in turn: one load, or where n is no multiple of 8 sixteen
@@ -1251,11 +1344,20 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
     ok = make_map(&a, e.x, false, e.k, e.x_rows, e.x_stride, 0, 0, 64) &&
          make_map(&b, e.w, false, e.n, e.rows, e.w_stride, 0, 0, 64);
   if (!ok) return false;
+  // plain bf16 outputs of large groups leave by TMA where their rows are words
+  if (pair == 2 && !e.gated && !e.f32_out && !e.accumulate && features % 8 == 0 &&
+      (reinterpret_cast<uintptr_t>(e.y) & 15) == 0) {
+    if (e.op != kExpertDw)
+      p.bulk = make_out_map(&m.y, e.y, features, e.rows, features, 0, 0);
+    else if (e.y_stride % 8 == 0 && e.y_expert_stride % 8 == 0)
+      p.bulk = make_out_map(&m.y, e.y, e.k, e.n, e.y_stride, e.experts, e.y_expert_stride);
+  }
+  if (!p.bulk) m.y = m.b;  // not used
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t most = m_tiles * row_tiles, slots = sm_count() / pair;
   const int grid = static_cast<int>(most < slots ? most : slots) * pair;
-  *status = pair == 2 ? launch_with<2>(p, a, b, grid, s) : launch_with<1>(p, a, b, grid, s);
+  *status = pair == 2 ? launch_with<2>(p, m, grid, s) : launch_with<1>(p, m, grid, s);
   return true;
 }
 
