@@ -58,6 +58,7 @@ constexpr int kBoxRows = 64;            // rows of one B load
 constexpr int kMaxStages = 12;
 constexpr int kMaxN = 256;              // columns of one TMEM accumulator buffer
 constexpr int kMaxSmallN = 64;          // most rows of a tile with small groups
+constexpr uint64_t kLandNs = 100000000;  // limit for what is under way when a wait ran out
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kStaticBytes = 11 * 1024;  // more than Shared below
 
@@ -323,6 +324,7 @@ struct Shared {
   uint64_t tail[kMaxStages];         // dw: a group's last stage has landed
   uint64_t acc_full[2];
   uint64_t acc_empty[2];
+  uint64_t drain;                    // after a wait that ran out: the products issued are done
   uint32_t tmem;
   uint32_t stop;                     // a wait ran out: every role leaves its loop
   int32_t start[kMaxExperts + 2];    // first row of each group; the unused rows are the last
@@ -562,7 +564,7 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map, Shared& sh
   // of a pair's second block are the first's to see).
   for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
     uint64_t* bar = alive ? &sh.empty[i % p.stages] : &sh.full[i % p.stages];
-    if (alive || first) mbar_wait_bounded(bar, (i / p.stages) & 1, p.e.timeout_ns);
+    if (alive || first) mbar_wait_bounded(bar, (i / p.stages) & 1, kLandNs);
   }
 }
 
@@ -648,15 +650,16 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring) {
       continue;
     }
     const int buffer = tiles & 1;
-    if (!wait(p, sh, &sh.acc_empty[buffer], ((tiles >> 1) & 1) ^ 1)) return;
+    bool alive = wait(p, sh, &sh.acc_empty[buffer], ((tiles >> 1) & 1) ^ 1);
     tc_fence_after();
     const uint32_t d = tmem + buffer * kMaxN;
     const int n = padded<kPair>(t.rows);
     const uint32_t idesc = instruction(kE4m3, kARows, kBRows, kTileM * kPair, n);
     uint32_t accumulate = 0;
-    for (int c = 0; c < t.depth; c += kDepth) {
+    for (int c = 0; alive && c < t.depth; c += kDepth) {
       const int stage = at.stage;
-      if (!wait(p, sh, &sh.full[stage], at.parity)) return;
+      alive = wait(p, sh, &sh.full[stage], at.parity);
+      if (!alive) break;
       // gathered rows came by ordinary copies: order them before the tensor
       // core's reads
       if (gather) fence_proxy_async_smem();
@@ -675,6 +678,12 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring) {
       // core has products in hand
       if (c == 2 * kDepth || (c < 2 * kDepth && c + kDepth >= t.depth))
         have = walk.next(p, sh, next);
+    }
+    if (!alive) {
+      // the tensor core is done with shared memory and TMEM before they go
+      mma_commit<kPair>(&sh.drain);
+      mbar_wait_bounded(&sh.drain, 0, kLandNs);
+      return;
     }
     mma_commit<kPair>(&sh.acc_full[buffer]);
     ++tiles;
@@ -1118,6 +1127,7 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
       mbar_init(&sh.acc_full[i], 1);
       mbar_init(&sh.acc_empty[i], kStores * kPair);
     }
+    mbar_init(&sh.drain, 1);
     sh.stop = 0;
     fence_barrier_init();
   }
