@@ -24,11 +24,11 @@
 // With large groups two blocks of a cluster share a product of 256 features by
 // 256 rows (cta_group::2), each holding half of either operand: 32 KB of loads
 // per block and 512 cycles of products, which L2 can just deliver.  Bound by
-// the tensor cores: 2 x 1024 features of 64225 rows of 64 experts, 2048 deep, 322
-// us, 1706 TFLOP/s, 16.7 thousand cycles a tile of which 16.4 are the products';
-// gated 318 us; gradient of the rows 323 us; of the weights 366 us (ragged ends
-// and 537 MB of results); e4m3 238 us with the gather.  With small groups bound
-// by the weights' bytes: 24 tokens of the fine-grained layer in e4m3, 142 and 80
+// the tensor cores: 2 x 1024 features of 64225 rows of 64 experts, 2048 deep, 327
+// us, 1680 TFLOP/s, 16.6 thousand cycles a tile of which 16.4 are the products';
+// gated 317 us; gradient of the rows 311 to 342 us; of the weights 380 us (ragged
+// ends and 537 MB of results); e4m3 235 us with the gather.  With small groups bound
+// by the weights' bytes: 24 tokens of the fine-grained layer in e4m3, 141 and 80
 // us for gate and up and for down, 6.7 TB/s.
 #include <cuda.h>
 
