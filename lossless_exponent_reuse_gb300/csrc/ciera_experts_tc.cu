@@ -41,11 +41,12 @@ namespace {
 constexpr int kGatherWarps = 4;
 // Warps: 0 loads A, 1 issues the products, then the storing warps, one that
 // loads B, and those that gather rows (single blocks) or clear (pairs).
-// A storing warp has 1 KB of shared memory, two where it reads what the gated
-// unit's gradient needs (and then there are eight); all of them 6 KB of scales.
-constexpr int kOutputBytes = 16 * 1024;
+// A storing warp has 2 KB of shared memory, half of which takes what the gated
+// unit's gradient reads (and then there are eight); in e4m3 1 KB, and 512 bytes
+// of scales.
+constexpr int kStagingBytes = 24 * 1024;
 constexpr int kScaleBytes = 6 * 1024;
-constexpr int kStagingBytes = kOutputBytes + kScaleBytes;
+constexpr int kOutputBytes = 16 * 1024;  // before the scales
 template <int kPair>
 struct Roles {
   static constexpr int kStoreWarps = kPair == 2 ? 12 : 8;
@@ -60,7 +61,7 @@ constexpr int kMaxN = 256;              // columns of one TMEM accumulator buffe
 constexpr int kMaxSmallN = 64;          // most rows of a tile with small groups
 constexpr uint64_t kLandNs = 100000000;  // limit for what is under way when a wait ran out
 constexpr int kSmemLimit = 227 * 1024;
-constexpr int kStaticBytes = 11 * 1024;  // more than Shared below
+constexpr int kStaticBytes = 10 * 1024;  // Shared below
 
 struct TcParams {
   ExpertParams e;
@@ -329,8 +330,9 @@ struct Shared {
   uint32_t stop;                     // a wait ran out: every role leaves its loop
   int32_t start[kMaxExperts + 2];    // first row of each group; the unused rows are the last
   int32_t tile[kMaxExperts + 2];     // tiles before each group
-  uint16_t per[kMaxExperts + 1];     // rows of each group's tiles
+  uint8_t per[kMaxExperts + 1];      // rows of each group's tiles, in sixteens less one
 };
+static_assert(sizeof(Shared) <= kStaticBytes, "stages and staging take the rest");
 
 // N of a tile's instructions: multiples of 16, of 32 for a pair.
 template <int kPair>
@@ -380,7 +382,7 @@ __device__ void find_groups(const TcParams& p, Shared& sh) {
     }
     if (g <= E) {
       sh.start[g] = begin;
-      sh.per[g] = static_cast<uint16_t>(per);
+      sh.per[g] = static_cast<uint8_t>(per / 16 - 1);
       sh.tile[g] = before + sum - tiles;
       if (g == E) {
         sh.start[E + 1] = rows;
@@ -430,7 +432,7 @@ struct Walk {
       begin = sh.tile[group];
       first = sh.start[group];
       rows = sh.start[group + 1] - first;
-      per = sh.per[group];
+      per = (sh.per[group] + 1) * 16;
     }
     const int local = index - begin;
     // local / m_tiles; the product is that or one more
@@ -741,9 +743,16 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
 // to the output.  What the gated unit's gradient reads takes the same way back.
 // (Sixteen 2-byte stores of a thread's feature: 147 instead of 137 us for the
 // e4m3 product of 64225 rows, 1024 to 2048.)  Large groups' plain outputs leave
-// by TMA, whose 64-byte swizzle is the order in which they lie there, where a
-// chunk's 16 rows are all the group's: the load and store units, which the
-// matrices and the scales' shuffles need, see no global store.
+// by TMA, whose 64-byte swizzle is the order in which they lie there, where the
+// chunk's rows are all the group's: the load and store units, which the
+// matrices and the scales' shuffles need, see no global store.  In bf16 two
+// chunks leave at a time: the wait for TMEM, the fence and the copy's issue take
+// 590 cycles in turn whether 16 rows or 32 go, and short contractions, or a last
+// tile of few features, wait for them (gradient of 128 experts' weights, 37 rows
+// each: 4528 x 272, 135 -> 96 us; 512 x 2272, 74 -> 64; 60 experts' 1752 x 2976
+// from 5 rows each, 139 -> 102.  Where rows of results start inside a 32-byte
+// sector, n % 16 == 8, results of 200 MB and more gain less, and 512 x 2264 lost:
+// 78 -> 84).
 //
 // Outputs whose rows do not start on 16-byte boundaries, and the weights'
 // gradients in 32 bits or added to, are stored value by value.
@@ -837,7 +846,11 @@ __device__ void store_tiles(const TcParams& p, const CUtensorMap* map_y, Shared&
   constexpr int kStride = kTurns * kChunk;        // rows from chunk to chunk
   constexpr int kScales = (kMaxN / kChunk + 2 * kTurns - 1) / (2 * kTurns);
   const int first_row = ((warp - 2) >> 2) * kChunk;
-  const uint32_t buf = staging + (warp - 2) * (kReadsPre ? 2048 : 1024), buf_up = buf + 1024;
+  // plain outputs leave two chunks at a time
+  constexpr bool kDouble = kPair == 2 && !kFused && !kReadsPre && !kE4m3;
+  constexpr int kOwn = kE4m3 ? 1024 : 2048;
+  static_assert(kStores * kOwn <= (kE4m3 ? kOutputBytes : kStagingBytes), "the warps' memory");
+  const uint32_t buf = staging + (warp - 2) * kOwn, buf_up = buf + 1024;
   const int64_t features = kOp == kExpertForward ? e.n : e.k;
   uint16_t* y = static_cast<uint16_t*>(e.y);
   const bool wide =
@@ -909,8 +922,50 @@ __device__ void store_tiles(const TcParams& p, const CUtensorMap* map_y, Shared&
     }
     const uint32_t acc =
         sh.tmem + buffer * kMaxN + (static_cast<uint32_t>(quadrant * 32) << 16);
+    int rows = left_f > 0 ? t.rows : 0;  // a warp behind the last feature stores none
+    if constexpr (kDouble)
+      if (p.bulk) {
 #pragma unroll 1
-    for (int c = first_row, chunk = 0; c < t.rows; c += kStride, ++chunk) {
+        for (int c = 2 * first_row; c < rows; c += 2 * kStride) {
+          const int left = t.rows - c;
+          const int64_t r = t.row + c;
+          float v[4][8] = {};
+          if (!zero) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              tmem_ld(acc + (static_cast<uint32_t>(16 * (i & 1)) << 16) + c + (i >> 1) * kChunk, v[i]);
+            tmem_ld_wait();
+          }
+          uint32_t out[2][8];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float* w = v[i >> 3 << 1 | (i >> 2 & 1)] + (i & 1) * 4 + (i >> 1 & 1) * 2;
+            out[i >> 3][i & 7] = pack_bf16(w[0], w[1]);
+          }
+          if (lane == 0) bulk_wait_read_all();  // the copy before has read the buffer
+          __syncwarp();
+          if (kOp == kExpertDw || left >= 2 * kChunk) {
+            stage32(buf, out[0]);
+            stage32(buf_up, out[1]);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (kOp == kExpertDw)
+                tma_store_3d(map_y, buf, static_cast<int>(f0), static_cast<int>(r), t.group);
+              else
+                tma_store_2d(map_y, buf, static_cast<int>(f0), static_cast<int>(r));
+              bulk_commit();
+            }
+          } else {
+            uint16_t* to = y + r * features + f0;
+            put32(buf, to, features, out[0], left, left_f);
+            put32(buf_up, to + kChunk * features, features, out[1], left - kChunk, left_f);
+          }
+        }
+        rows = 0;  // all stored
+      }
+#pragma unroll 1
+    for (int c = first_row, chunk = 0; c < rows; c += kStride, ++chunk) {
       const int left = t.rows - c;
       const int64_t r = t.row + c;
       // v[h][4 cb + i]: lanes 16 h + 8 (i / 2) + lane / 4, rows 8 cb + 2 (lane % 4) + i % 2
@@ -1059,23 +1114,21 @@ __device__ void store_tiles(const TcParams& p, const CUtensorMap* map_y, Shared&
         const float* w = v[i >> 2] + (i & 1) * 4 + (i >> 1 & 1) * 2;
         out[i] = pack_bf16(w[0], w[1]);
       }
-      if (p.bulk) {  // the copies of the chunk before have read the buffer
-        if (lane == 0) bulk_wait_read_all();
-        __syncwarp();
-      }
-      if (p.bulk && (kOp == kExpertDw || left >= kChunk)) {
-        stage32(buf, out);
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0 && left_f > 0) {
-          if (kOp == kExpertDw)
-            tma_store_3d(map_y, buf, static_cast<int>(f0), static_cast<int>(r), t.group);
-          else
-            tma_store_2d(map_y, buf, static_cast<int>(f0), static_cast<int>(r));
-          bulk_commit();
+      if constexpr (kE4m3)
+        if (p.bulk) {
+          if (lane == 0) bulk_wait_read_all();  // the copy before has read the buffer
+          __syncwarp();
+          if (left >= kChunk) {
+            stage32(buf, out);
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              tma_store_2d(map_y, buf, static_cast<int>(f0), static_cast<int>(r));
+              bulk_commit();
+            }
+            continue;
+          }
         }
-        continue;
-      }
       const int64_t stride = kOp == kExpertDw ? e.y_stride : features;
       uint16_t* to =
           y + (kOp == kExpertDw ? t.group * e.y_expert_stride : 0) + r * stride + f0;
@@ -1234,16 +1287,16 @@ bool make_map(CUtensorMap* map, const void* base, bool e4m3, int64_t columns, in
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// A map of bf16 outputs, boxes of 16 rows of 32 features.
+// A map of bf16 outputs, boxes of box_rows rows of 32 features.
 bool make_out_map(CUtensorMap* map, void* base, int64_t columns, int64_t rows, int64_t stride,
-                  int64_t planes, int64_t plane_stride) {
+                  int64_t planes, int64_t plane_stride, int box_rows) {
   if (planes > 1 && plane_stride <= 0) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(columns), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(planes)};
   const cuuint64_t strides[2] = {
       static_cast<cuuint64_t>(2 * stride),
       static_cast<cuuint64_t>(2 * (planes > 1 ? plane_stride : stride * rows))};
-  const cuuint32_t box[3] = {32, 16, 1}, ones[3] = {1, 1, 1};
+  const cuuint32_t box[3] = {32, static_cast<cuuint32_t>(box_rows), 1}, ones[3] = {1, 1, 1};
   return encode()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, planes ? 3 : 2, base, dims, strides, box,
                   ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_NONE,
@@ -1358,9 +1411,10 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
   if (pair == 2 && !e.gated && !e.f32_out && !e.accumulate && features % 8 == 0 &&
       (reinterpret_cast<uintptr_t>(e.y) & 15) == 0) {
     if (e.op != kExpertDw)
-      p.bulk = make_out_map(&m.y, e.y, features, e.rows, features, 0, 0);
+      p.bulk = make_out_map(&m.y, e.y, features, e.rows, features, 0, 0, e.e4m3 ? kChunk : 2 * kChunk);
     else if (e.y_stride % 8 == 0 && e.y_expert_stride % 8 == 0)
-      p.bulk = make_out_map(&m.y, e.y, e.k, e.n, e.y_stride, e.experts, e.y_expert_stride);
+      p.bulk = make_out_map(&m.y, e.y, e.k, e.n, e.y_stride, e.experts, e.y_expert_stride,
+                            2 * kChunk);
   }
   if (!p.bulk) m.y = m.b;  // not used
 
