@@ -12,6 +12,7 @@ namespace {
 constexpr int kRowThreads = 256;
 constexpr int kRingBytes = 48 * 1024;
 constexpr int64_t kManyRows = 2048;    // enough to fill the SMs with half the threads a row
+constexpr int64_t kShiftDim = 768;     // values of an odd row from which on it goes by words
 constexpr int kMostRowThreads = 512;  // for one row of the kernels that hold rows in registers
 
 // ------------------------------------------------------------------------
@@ -22,7 +23,11 @@ constexpr int kMostRowThreads = 512;  // for one row of the kernels that hold ro
 // k_rmsnorm holds a row in registers, kVecs words per thread, so that it is
 // read once; blockDim.x threads take a row (whole warps, one reduction per
 // statistic), blockDim.y rows share a block where rows are short.  Words are
-// 16 bytes where all rows start on 16-byte boundaries, else 4 or 2.
+// 16 bytes where all rows start on 16-byte boundaries, else 4 or 2.  Rows of odd
+// length of matrices laid out alike go by 16-byte words too, but for their ends
+// (see Part; 16384 x 2047: 51 us, 74 value by value; in e4m3 66 and 80; of 511
+// values 22.5 and 22.5, and 28.7 and 24.6, the ends' words are then most of a
+// row's warps).
 // k_rmsnorm_any takes rows of any length, value by value, and reads a row once
 // per statistic (from L1 or L2 after the first).
 
@@ -96,18 +101,119 @@ __device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t (*part)[32]) {
   return __reduce_max_sync(0xffffffffu, v);
 }
 
+// Rows that do not start on 16-byte boundaries, but all of a call's at the same
+// place `shift` behind one, are read and written by the 16-byte words that they
+// touch.  Of the row's first and last word some values belong to it, `lo` to
+// `hi` (never neither end: rows have 16 values and more); those go in up to
+// three pieces of 2, 4 and 8 bytes, so that nothing outside the row is touched.
+struct Part {
+  int lo, hi;
+  __device__ __forceinline__ Part(int column, int dim)
+      : lo(column < 0 ? -column : 0), hi(dim - column < 8 ? dim - column : 8) {}
+  __device__ __forceinline__ bool whole() const { return lo == 0 && hi == 8; }
+};
+
+// Pieces of a word as they are loaded, all before the first is needed.
+struct Pieces {
+  uint32_t one = 0, two = 0;
+  uint2 four = {0, 0};
+  __device__ __forceinline__ Pieces(const uint4* at, const Part& part) {
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(at);
+    const int e = part.lo ? (part.lo + 1) & ~1 : part.hi & 4;  // of the two
+    if ((part.lo | part.hi) & 1) one = v[part.lo ? part.lo : part.hi - 1];
+    if (part.lo ? e & 2 : part.hi & 2) two = *reinterpret_cast<const uint32_t*>(v + e);
+    if (part.lo ? part.lo <= 4 : part.hi >= 4)
+      four = *reinterpret_cast<const uint2*>(v + (part.lo ? 4 : 0));
+  }
+  __device__ __forceinline__ uint4 word(const Part& part) const {
+    if (part.lo) {
+      const uint32_t high = one << 16;
+      if (part.lo <= 4)
+        return make_uint4(part.lo == 1 ? high : 0u, part.lo == 3 ? high : two, four.x, four.y);
+      return make_uint4(0, 0, part.lo == 5 ? high : 0u, part.lo == 7 ? high : two);
+    }
+    const uint32_t first = part.hi & 2 ? two : one, second = part.hi & 2 ? one : 0u;
+    return part.hi & 4 ? make_uint4(four.x, four.y, first, second)
+                       : make_uint4(first, second, 0, 0);
+  }
+};
+
+__device__ __forceinline__ void store_part(uint4* at, const uint4& w, const Part& part) {
+  uint16_t* v = reinterpret_cast<uint16_t*>(at);
+  if (part.whole()) {
+    *at = w;
+  } else if (part.lo) {
+    const int odd = part.lo & 1, e = part.lo + odd;
+    if (odd)
+      v[part.lo] = static_cast<uint16_t>(
+          (part.lo < 4 ? part.lo < 2 ? w.x : w.y : part.lo < 6 ? w.z : w.w) >> 16);
+    if (e & 2) *reinterpret_cast<uint32_t*>(v + e) = e == 2 ? w.y : w.w;
+    if (e <= 4) *reinterpret_cast<uint2*>(v + 4) = make_uint2(w.z, w.w);
+  } else {
+    if (part.hi & 4) *reinterpret_cast<uint2*>(v) = make_uint2(w.x, w.y);
+    if (part.hi & 2) *reinterpret_cast<uint32_t*>(v + (part.hi & 4)) = part.hi & 4 ? w.z : w.x;
+    if (part.hi & 1)
+      v[part.hi - 1] = static_cast<uint16_t>(
+          part.hi < 4 ? part.hi < 2 ? w.x : w.y : part.hi < 6 ? w.z : w.w);
+  }
+}
+
+// The same of eight e4m3 values.
+__device__ __forceinline__ void store_part(uint2* at, const uint2& w, const Part& part) {
+  uint8_t* v = reinterpret_cast<uint8_t*>(at);
+  if (part.whole()) {
+    *at = w;
+  } else if (part.lo) {
+    const int odd = part.lo & 1, e = part.lo + odd;
+    if (odd) v[part.lo] = static_cast<uint8_t>((part.lo < 4 ? w.x : w.y) >> (part.lo & 3) * 8);
+    if (e & 2)
+      *reinterpret_cast<uint16_t*>(v + e) = static_cast<uint16_t>((e == 2 ? w.x : w.y) >> 16);
+    if (e <= 4) *reinterpret_cast<uint32_t*>(v + 4) = w.y;
+  } else {
+    const uint32_t rest = part.hi & 4 ? w.y : w.x;
+    if (part.hi & 4) *reinterpret_cast<uint32_t*>(v) = w.x;
+    if (part.hi & 2) *reinterpret_cast<uint16_t*>(v + (part.hi & 4)) = static_cast<uint16_t>(rest);
+    if (part.hi & 1) v[part.hi - 1] = static_cast<uint8_t>(rest >> (part.hi & 2) * 8);
+  }
+}
+
+// The weights of a word's columns, from 4-byte words, put together where the
+// columns start inside one; `part` of them value by value.
+__device__ __forceinline__ uint4 load_weights(const uint16_t* weight, int column) {
+  const int odd = column & 1;
+  const uint32_t* at = reinterpret_cast<const uint32_t*>(weight + (column - odd));
+  uint32_t w[5] = {at[0], at[1], at[2], at[3], odd ? weight[column + 7] : 0u};
+  if (odd)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ uint4 load_weights(const uint16_t* weight, int column,
+                                              const Part& part) {
+  uint32_t f[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = j >= part.lo && j < part.hi ? weight[column + j] : 0u;
+  return make_uint4(f[0] | f[1] << 16, f[2] | f[3] << 16, f[4] | f[5] << 16, f[6] | f[7] << 16);
+}
+
 // kNorm false: rows to e4m3 as they are.
-template <typename W, int kVecs, bool kNorm, bool kE4m3>
+template <typename W, int kVecs, bool kNorm, bool kE4m3, bool kShift = false>
 __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p) {
   __shared__ float part[8][32];
   __shared__ uint32_t part_max[8][32];
   constexpr int kN = Word<W>::kValues;
   const int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
+  const int dim = static_cast<int>(p.dim), step = blockDim.x;
+  const int shift =
+      kShift ? static_cast<int>(reinterpret_cast<uintptr_t>(p.x + r * p.x_stride) >> 1 & 7) : 0;
   // words of the row from this thread's first on; a row behind the last has none
-  const int words = r < p.rows ? static_cast<int>(p.dim / kN) - static_cast<int>(threadIdx.x) : 0;
-  const int step = blockDim.x;
-  const W* x = reinterpret_cast<const W*>(p.x + r * p.x_stride) + threadIdx.x;
-  const W* residual = reinterpret_cast<const W*>(p.residual + r * p.residual_stride) + threadIdx.x;
+  const int words =
+      r < p.rows ? (kShift ? (shift + dim + 7) / 8 : dim / kN) - static_cast<int>(threadIdx.x) : 0;
+  const auto column = [&](int v) { return static_cast<int>(threadIdx.x + v * step) * 8 - shift; };
+  const W* x = reinterpret_cast<const W*>(p.x + r * p.x_stride - shift) + threadIdx.x;
+  const W* residual =
+      reinterpret_cast<const W*>(p.residual + r * p.residual_stride - shift) + threadIdx.x;
   const W* weights = reinterpret_cast<const W*>(p.weight) + threadIdx.x;
   float s[kVecs][kN];
   W weight[kVecs] = {};
@@ -118,6 +224,21 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p)
   for (int v = 0; v < kVecs; ++v) {
     in[v] = add[v] = W{};
     if (v * step < words) {
+      if constexpr (kShift) {
+        const Part part(column(v), dim);
+        if (part.whole()) {
+          in[v] = x[v * step];
+          if (kNorm && p.residual) add[v] = residual[v * step];
+          if (kNorm) weight[v] = load_weights(p.weight, column(v));
+        } else {
+          const Pieces of_x(x + v * step, part);
+          const Pieces of_residual(kNorm && p.residual ? residual + v * step : x + v * step, part);
+          if (kNorm) weight[v] = load_weights(p.weight, column(v), part);
+          in[v] = of_x.word(part);
+          if (kNorm && p.residual) add[v] = of_residual.word(part);
+        }
+        continue;
+      }
       in[v] = x[v * step];
       if (kNorm && p.residual) add[v] = residual[v * step];
       if (kNorm) weight[v] = weights[v * step];
@@ -137,10 +258,15 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p)
   }
   if (kNorm) {
     if (p.h) {
-      W* h = reinterpret_cast<W*>(p.h + r * p.dim) + threadIdx.x;
+      W* h = reinterpret_cast<W*>(p.h + r * p.dim - shift) + threadIdx.x;
 #pragma unroll
       for (int v = 0; v < kVecs; ++v)
-        if (v * step < words) h[v * step] = Word<W>::pack(s[v]);
+        if (v * step < words) {
+          if constexpr (kShift)
+            store_part(h + v * step, Word<W>::pack(s[v]), Part(column(v), dim));
+          else
+            h[v * step] = Word<W>::pack(s[v]);
+        }
     }
     sum = row_sum(sum, part);
     const float rstd = rsqrtf(sum / static_cast<float>(p.dim) + p.eps);
@@ -155,6 +281,16 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p)
   }
   float inverse = 1.0f;
   if (kE4m3) {
+    if constexpr (kShift && kNorm) {
+#pragma unroll
+      for (int v = 0; v < kVecs; ++v) {
+        const Part part(column(v), dim);
+        if (!part.whole())
+#pragma unroll
+          for (int j = 0; j < kN; ++j)
+            if (j < part.lo || j >= part.hi) s[v][j] = 0.0f;
+      }
+    }
 #pragma unroll
     for (int v = 0; v < kVecs; ++v)
 #pragma unroll
@@ -167,11 +303,19 @@ __global__ void __launch_bounds__(kMostRowThreads) k_rmsnorm(const NormParams p)
     if (r < p.rows && threadIdx.x == 0) p.scale[r] = scale;
   }
   using Half = typename Word<W>::Half;
-  W* y = reinterpret_cast<W*>(static_cast<uint16_t*>(p.y) + r * p.dim) + threadIdx.x;
-  Half* y8 = reinterpret_cast<Half*>(static_cast<uint8_t*>(p.y) + r * p.dim) + threadIdx.x;
+  W* y = reinterpret_cast<W*>(static_cast<uint16_t*>(p.y) + r * p.dim - shift) + threadIdx.x;
+  Half* y8 = reinterpret_cast<Half*>(static_cast<uint8_t*>(p.y) + r * p.dim - shift) + threadIdx.x;
 #pragma unroll
   for (int v = 0; v < kVecs; ++v)
     if (v * step < words) {
+      if constexpr (kShift) {
+        const Part part(column(v), dim);
+        if (kE4m3)
+          store_part(y8 + v * step, Word<W>::pack_8bit(s[v], inverse), part);
+        else
+          store_part(y + v * step, Word<W>::pack(s[v]), part);
+        continue;
+      }
       if (kE4m3)
         y8[v * step] = Word<W>::pack_8bit(s[v], inverse);
       else
@@ -1044,15 +1188,25 @@ RowShape row_shape(int64_t dim, int word, int at_first) {
   return s;
 }
 
-template <typename W, int kVecs>
+template <typename W, int kVecs, bool kShift = false>
 void norm_at(const NormParams& p, dim3 block, cudaStream_t s) {
   const int grid = grid_of((p.rows + block.y - 1) / block.y);
   if (!p.weight)
-    k_rmsnorm<W, kVecs, false, true><<<grid, block, 0, s>>>(p);
+    k_rmsnorm<W, kVecs, false, true, kShift><<<grid, block, 0, s>>>(p);
   else if (p.e4m3)
-    k_rmsnorm<W, kVecs, true, true><<<grid, block, 0, s>>>(p);
+    k_rmsnorm<W, kVecs, true, true, kShift><<<grid, block, 0, s>>>(p);
   else
-    k_rmsnorm<W, kVecs, true, false><<<grid, block, 0, s>>>(p);
+    k_rmsnorm<W, kVecs, true, false, kShift><<<grid, block, 0, s>>>(p);
+}
+
+// Whether all rows of all buffers start at the same place in a 16-byte word.
+bool same_shift(int64_t dim, const void* first, std::initializer_list<const void*> at,
+                std::initializer_list<int64_t> strides) {
+  for (const void* p : at)
+    if (p && ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(first)) & 15)) return false;
+  for (int64_t s : strides)
+    if ((s - dim) % 8) return false;
+  return true;
 }
 
 template <typename W, int kVecs>
@@ -1080,7 +1234,20 @@ int launch_rmsnorm(const NormParams& p, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int word = word_values(p.dim, {p.x, p.residual, p.weight, p.h, p.y},
                                {p.x_stride, p.residual ? p.residual_stride : 0});
-  const RowShape shape = row_shape(p.dim, word, !p.residual && p.rows >= kManyRows ? 16 : 8);
+  const int at_first = !p.residual && p.rows >= kManyRows ? 16 : 8;
+  const uintptr_t y_place = reinterpret_cast<uintptr_t>(p.y) * (p.e4m3 ? 2 : 1);
+  if (word == 1 && p.dim >= kShiftDim && same_shift(p.dim, p.x, {p.residual, p.h, reinterpret_cast<const void*>(y_place)},
+                              {p.x_stride, p.residual ? p.residual_stride : p.dim}) &&
+      (reinterpret_cast<uintptr_t>(p.weight) & 3) == 0) {
+    // a row touches at most this many words' values
+    const RowShape shape = row_shape((p.dim + 14) / 8 * 8, 8, at_first);
+    switch (shape.values) {
+      case 8: norm_at<uint4, 1, true>(p, shape.block, s); return cudaGetLastError();
+      case 16: norm_at<uint4, 2, true>(p, shape.block, s); return cudaGetLastError();
+      case 32: norm_at<uint4, 4, true>(p, shape.block, s); return cudaGetLastError();
+    }
+  }
+  const RowShape shape = row_shape(p.dim, word, at_first);
   const dim3 b = shape.block;
   switch (shape.values * 16 + word) {
     case 8 * 16 + 8: norm_at<uint4, 1>(p, b, s); break;

@@ -68,6 +68,73 @@ def test_norm(rows, dim, with_residual, kind):
     torch.testing.assert_close(q.h, r.h, rtol=0, atol=0)
 
 
+def guarded(t, at):
+    """The values at element ``at`` of a flat buffer, others around them; (view, buffer)."""
+    flat = torch.full((t.numel() + at + 24,), 7.0, device="cuda").to(t.dtype)
+    flat[at:at + t.numel()] = t.reshape(-1)
+    return flat[at:at + t.numel()].view(t.shape), flat
+
+
+def untouched(flat, at, n):
+    return (flat[:at].float() == 7).all() and (flat[at + n:].float() == 7).all()
+
+
+@pytest.mark.parametrize("at", range(8))
+@pytest.mark.parametrize("dim", [769, 1001, 2047, 4099, 9001])
+def test_norm_of_odd_rows_that_start_anywhere(dim, at):
+    """All matrices at the same place behind a 16-byte boundary; nothing is
+    written outside the rows."""
+    rows = 5
+    x, w = rand(rows, dim), rand(dim, seed=1) + 1
+    res = rand(rows, dim, seed=2, scale=3.0)
+    s, rstd, y = ref.norm(x, w, res, 1e-6)
+    e_rstd = (dim + 8) * ref.U_F32
+    sized = x.double().abs() + res.double().abs()
+    e_y = y.abs() * (e_rstd + 4 * ref.U_F32) + (sized * rstd[:, None] * w.double().abs()
+                                                * ref.U_F32)
+    (xs, _), (rs, _) = guarded(x, at), guarded(res, at)
+    for kind, dtype in ((experts.BF16, BF16), (experts.E4M3, torch.float8_e4m3fn)):
+        ys, y_flat = guarded(torch.zeros(rows, dim, dtype=BF16, device="cuda").to(dtype), at)
+        hs, h_flat = guarded(torch.zeros_like(x), at)
+        scale, r = torch.zeros(rows, device="cuda"), torch.zeros(rows, device="cuda")
+        st = ciera.lib().ciera_rmsnorm(
+            xs.data_ptr(), dim, rs.data_ptr(), dim, w.data_ptr(), rows, dim, 1e-6, ys.data_ptr(),
+            kind, scale.data_ptr() if kind == experts.E4M3 else None, hs.data_ptr(), r.data_ptr(),
+            torch.cuda.current_stream().cuda_stream)
+        assert st == ciera.OK
+        assert untouched(y_flat, at, rows * dim) and untouched(h_flat, at, rows * dim)
+        ref.within(r, rstd, 0.0, "rstd", rounded=e_rstd)
+        ref.within(hs, s, sized * ref.U_F32, "h")
+        if kind == experts.BF16:
+            ref.within(ys, y, e_y, "y")
+        else:
+            want, code = ref.quantize(y)
+            ref.within(scale, want, e_y.amax(1) / ref.E4M3_MAX, "scale", rounded=4 * ref.U_F32)
+            slack = e_y / want[:, None] + code.abs() * (e_y.amax(1) / ref.E4M3_MAX / want)[:, None] \
+                + code.abs() * 8 * ref.U_F32 + 2.0 ** -10
+            ref.within(ys.float(), code, slack, "e4m3", rounded=2.0 ** -4)
+    # rows to e4m3 as they are
+    ys, y_flat = guarded(torch.zeros(rows, dim, device="cuda").to(torch.float8_e4m3fn), at)
+    st = ciera.lib().ciera_quantize_rows(xs.data_ptr(), dim, rows, dim, ys.data_ptr(),
+                                         scale.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert st == ciera.OK and untouched(y_flat, at, rows * dim)
+    want, code = ref.quantize(x.double())
+    ref.within(scale, want, 0.0, "scale", rounded=2 * ref.U_F32)
+    ref.within(ys.float(), code, code.abs() * 8 * ref.U_F32 + 2.0 ** -10, "e4m3",
+               rounded=2.0 ** -4)
+
+
+def test_norm_of_odd_zero_rows():
+    """Nothing behind a row's end counts, even where zeros give no number."""
+    x = torch.zeros(9, 1001, dtype=BF16, device="cuda")
+    w = torch.ones(1001, dtype=BF16, device="cuda")
+    r = experts.rmsnorm(x, w, eps=1e-6, quantize=True)
+    assert (r.y.float() == 0).all() and torch.isfinite(r.scale).all()
+    x[:, 1000] = 1.0
+    r = experts.rmsnorm(x, w, eps=0.0, quantize=True)
+    assert (r.y[:, 1000].float() == 448).all() and (r.y[:, :1000].float() == 0).all()
+
+
 def test_norm_of_zeros_infinities_and_nan():
     w = torch.ones(64, dtype=BF16, device="cuda")
     x = torch.zeros(4, 64, dtype=BF16, device="cuda")
