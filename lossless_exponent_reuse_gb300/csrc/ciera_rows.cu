@@ -13,6 +13,7 @@ constexpr int kRowThreads = 256;
 constexpr int kRingBytes = 48 * 1024;
 constexpr int64_t kManyRows = 2048;    // enough to fill the SMs with half the threads a row
 constexpr int64_t kShiftDim = 768;     // values of an odd row from which on it goes by words
+constexpr int64_t kShiftGradientDim = 128;  // the same of the gradient
 constexpr int kMostRowThreads = 512;  // for one row of the kernels that hold rows in registers
 
 // ------------------------------------------------------------------------
@@ -352,25 +353,33 @@ __global__ void __launch_bounds__(kRowThreads) k_rmsnorm_backward_any(const Norm
 
 // The same with a row in registers and the weight's gradient too, the next
 // row's words under way while this one is reduced.  Bound by memory, 8 bytes a
-// value.
-template <typename W, int kVecs>
+// value.  kShift: rows of odd length by the 16-byte words they touch; a block's
+// rows are a multiple of eight apart, so that all of a thread's start alike
+// (16384 x 2047: 82 us, 115 value by value, 109 with 16 values a thread, which
+// every row's ends wait for; x 511 37 and 45).
+template <typename W, int kVecs, bool kShift = false>
 __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8 ? 2 : 1)
     k_rmsnorm_backward(const NormBackwardParams p) {
   __shared__ float part[2][8][32];
   constexpr int kN = Word<W>::kValues;
-  // words of a row from this thread's first on
-  const int words = static_cast<int>(p.dim / kN) - static_cast<int>(threadIdx.x);
-  const int across = blockDim.x;
+  const int dim = static_cast<int>(p.dim), across = blockDim.x;
   const int64_t step = static_cast<int64_t>(gridDim.x) * blockDim.y;
   const float inverse_dim = 1.0f / static_cast<float>(p.dim);
   float dw[kVecs][kN] = {};
   W weight[kVecs], dy[kVecs], h[kVecs], dh[kVecs];
   float rstd = 0.0f;
   int64_t r = static_cast<int64_t>(blockIdx.x) * blockDim.y + threadIdx.y;
-  const W* dy_at = reinterpret_cast<const W*>(p.dy + r * p.dy_stride) + threadIdx.x;
-  const W* h_at = reinterpret_cast<const W*>(p.h + r * p.h_stride) + threadIdx.x;
-  const W* dh_at = reinterpret_cast<const W*>(p.dh + r * p.dh_stride) + threadIdx.x;
-  W* dx_at = reinterpret_cast<W*>(p.dx + r * p.dim) + threadIdx.x;
+  const int shift =
+      kShift ? static_cast<int>(reinterpret_cast<uintptr_t>(p.dy + r * p.dy_stride) >> 1 & 7) : 0;
+  // words of a row from this thread's first on
+  const int words = (kShift ? (shift + dim + 7) / 8 : dim / kN) - static_cast<int>(threadIdx.x);
+  const auto column_of = [&](int v) {
+    return static_cast<int>(threadIdx.x + v * across) * kN - shift;
+  };
+  const W* dy_at = reinterpret_cast<const W*>(p.dy + r * p.dy_stride - shift) + threadIdx.x;
+  const W* h_at = reinterpret_cast<const W*>(p.h + r * p.h_stride - shift) + threadIdx.x;
+  const W* dh_at = reinterpret_cast<const W*>(p.dh + r * p.dh_stride - shift) + threadIdx.x;
+  W* dx_at = reinterpret_cast<W*>(p.dx + r * p.dim - shift) + threadIdx.x;
   const float* rstd_at = p.rstd + r;
   const int64_t dy_step = step * p.dy_stride / kN, h_step = step * p.h_stride / kN;
   const int64_t dh_step = step * p.dh_stride / kN, dx_step = step * p.dim / kN;
@@ -380,6 +389,17 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8
     for (int v = 0; v < kVecs; ++v) {
       dy[v] = h[v] = dh[v] = W{};
       if (v * across < have) {
+        if constexpr (kShift) {
+          const Part part(column_of(v), dim);
+          if (!part.whole()) {
+            const Pieces of_dy(dy_at + v * across, part), of_h(h_at + v * across, part);
+            const Pieces of_dh((p.dh ? dh_at : dy_at) + v * across, part);
+            dy[v] = of_dy.word(part);
+            h[v] = of_h.word(part);
+            if (p.dh) dh[v] = of_dh.word(part);
+            continue;
+          }
+        }
         dy[v] = dy_at[v * across];
         h[v] = h_at[v * across];
         if (p.dh) dh[v] = dh_at[v * across];
@@ -394,7 +414,15 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8
 #pragma unroll
   for (int v = 0; v < kVecs; ++v) {
     weight[v] = W{};
-    if (v * across < words) weight[v] = reinterpret_cast<const W*>(p.weight)[v * across + threadIdx.x];
+    if (v * across < words) {
+      if constexpr (kShift) {
+        const Part part(column_of(v), dim);
+        weight[v] = part.whole() ? load_weights(p.weight, column_of(v))
+                                 : load_weights(p.weight, column_of(v), part);
+      } else {
+        weight[v] = reinterpret_cast<const W*>(p.weight)[v * across + threadIdx.x];
+      }
+    }
   }
   fetch(r < p.rows);
   int turn = 0;  // two reductions' scratch in turn: one barrier each
@@ -431,7 +459,12 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8
       Word<W>::unpack(more[v], out);
 #pragma unroll
       for (int j = 0; j < kN; ++j) out[j] += rs * (g[v][j] - n[v][j] * mean);
-      if (v * across < have) dx_at[v * across] = Word<W>::pack(out);
+      if (v * across < have) {
+        if constexpr (kShift)
+          store_part(dx_at + v * across, Word<W>::pack(out), Part(column_of(v), dim));
+        else
+          dx_at[v * across] = Word<W>::pack(out);
+      }
     }
     dx_at += dx_step;
   }
@@ -442,15 +475,16 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8
     if (threadIdx.y == turn_y) {
 #pragma unroll
       for (int v = 0; v < kVecs; ++v) {
-        const int i = v * across + threadIdx.x;
+        const int i = column_of(v);
         if (v * across >= words) continue;
 #pragma unroll
         for (int j = 0; j < kN; ++j) {
-          const float before = turn_y ? column[i * kN + j] : 0.0f;
+          if (kShift && (i + j < 0 || i + j >= dim)) continue;
+          const float before = turn_y ? column[i + j] : 0.0f;
           if (turn_y + 1 == blockDim.y)
-            mine[i * kN + j] = before + dw[v][j];
+            mine[i + j] = before + dw[v][j];
           else
-            column[i * kN + j] = before + dw[v][j];
+            column[i + j] = before + dw[v][j];
         }
       }
     }
@@ -1209,10 +1243,10 @@ bool same_shift(int64_t dim, const void* first, std::initializer_list<const void
   return true;
 }
 
-template <typename W, int kVecs>
+template <typename W, int kVecs, bool kShift = false>
 void norm_backward_at(const NormBackwardParams& p, dim3 block, int blocks, cudaStream_t s) {
   const size_t smem = block.y > 1 ? 4 * static_cast<size_t>(p.dim) : 0;
-  k_rmsnorm_backward<W, kVecs><<<blocks, block, smem, s>>>(p);
+  k_rmsnorm_backward<W, kVecs, kShift><<<blocks, block, smem, s>>>(p);
 }
 
 }  // namespace
@@ -1266,9 +1300,16 @@ int launch_rmsnorm_backward(const NormBackwardParams& p, int blocks, void* strea
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int word = word_values(p.dim, {p.dy, p.h, p.weight, p.dh, p.dx},
                                {p.dy_stride, p.h_stride, p.dh ? p.dh_stride : 0});
+  const bool shifted = word == 1 && p.dim >= kShiftGradientDim &&
+                       same_shift(p.dim, p.dy, {p.h, p.dh, p.dx},
+                                  {p.dy_stride, p.h_stride, p.dh ? p.dh_stride : p.dim}) &&
+                       (reinterpret_cast<uintptr_t>(p.weight) & 3) == 0;
   // 16 values per thread where that leaves a warp's worth: half the work of a
   // row's sum and of its addresses per value
-  const RowShape shape = row_shape(p.dim, word, word == 8 && p.dim >= 512 ? 16 : 8);
+  RowShape shape = shifted ? row_shape((p.dim + 14) / 8 * 8, 8, 8)
+                           : row_shape(p.dim, word, word == 8 && p.dim >= 512 ? 16 : 8);
+  const bool by_words = shifted && shape.values;
+  if (shifted && !by_words) shape = row_shape(p.dim, word, 8);
   const dim3 b = shape.block;
   // a ring of four rows as far as it takes 48 KB, else of two
   const int64_t line = 6 * p.dim * b.y;  // bytes of the rows of all three tensors
@@ -1281,8 +1322,21 @@ int launch_rmsnorm_backward(const NormBackwardParams& p, int blocks, void* strea
     const int64_t most = (p.rows + b.y - 1) / b.y;
     if (resident < blocks) blocks = static_cast<int>(resident);
     if (most < blocks) blocks = static_cast<int>(most);
+    if (by_words && blocks < most) {  // (blocks > 8 then)
+      const int apart = b.y % 8 == 0 ? 1 : b.y % 4 == 0 ? 2 : b.y % 2 == 0 ? 4 : 8;
+      blocks = blocks / apart * apart;
+    }
   }
   int err = cudaSuccess;
+  if (by_words) {
+    switch (shape.values) {
+      case 8: norm_backward_at<uint4, 1, true>(p, b, blocks, s); break;
+      case 16: norm_backward_at<uint4, 2, true>(p, b, blocks, s); break;
+      default: norm_backward_at<uint4, 4, true>(p, b, blocks, s);
+    }
+    k_sum_partials<<<grid_of((p.dim + 31) / 32), 1024, 0, s>>>(p.partial, blocks, p.dim, p.dweight);
+    return cudaGetLastError();
+  }
   switch (shape.values * 16 + word) {
     case 8 * 16 + 8:  // fewer than 512 values: the ring fits
       err = backward_ring<1, 4>(p, b, blocks, bytes, s);

@@ -212,6 +212,36 @@ def test_norm_gradient(rows, dim, with_dh, kind):
     assert torch.equal(dx, again[0]) and torch.equal(dw, again[1])
 
 
+@pytest.mark.parametrize("at", range(8))
+@pytest.mark.parametrize("rows,dim", [(3, 129), (5000, 129), (3000, 511), (2500, 1001),
+                                      (1500, 2047), (700, 5001), (400, 9001)])
+def test_norm_gradient_of_odd_rows_that_start_anywhere(rows, dim, at):
+    """All matrices at the same place behind a 16-byte boundary, more rows than
+    blocks at once; nothing is written outside the rows."""
+    h, w = rand(rows, dim, seed=5, scale=2.0), rand(dim, seed=6) + 1
+    dy, dh = rand(rows, dim, seed=7), rand(rows, dim, seed=8)
+    hd, wd, dyd = h.double(), w.double(), dy.double()
+    rd = ((hd * hd).mean(1, keepdim=True) + 1e-6) ** -0.5
+    rstd = rd[:, 0].float()
+    g = dyd * wd
+    want = rd * g - hd * rd ** 3 * (g * hd).mean(1, keepdim=True) + dh.double()
+    size = rd * g.abs() + hd.abs() * rd ** 3 * (g * hd).abs().mean(1, keepdim=True) \
+        + dh.double().abs()
+    (dys, _), (hs, _), (dhs, _) = (guarded(t, at) for t in (dy, h, dh))
+    dxs, dx_flat = guarded(torch.zeros_like(dy), at)
+    dw = torch.zeros(dim, device="cuda")
+    s = torch.cuda.current_stream().cuda_stream
+    ws = experts.workspace(0, s, tokens=rows, dim=dim)
+    st = ciera.lib().ciera_rmsnorm_backward(
+        dys.data_ptr(), dim, hs.data_ptr(), dim, rstd.data_ptr(), w.data_ptr(), dhs.data_ptr(),
+        dim, rows, dim, dxs.data_ptr(), dw.data_ptr(), ws.data_ptr(), ws.numel(), s)
+    assert st == ciera.OK and untouched(dx_flat, at, rows * dim)
+    ref.within(dxs, want, size * (dim + 16) * ref.U_F32, "dx")
+    terms = (dyd.abs() * hd.abs() * rd).sum(0)
+    ref.within(dw, (dyd * hd * rd).sum(0), terms * (rows + 8) * ref.U_F32, "dweight",
+               rounded=ref.U_F32)
+
+
 def test_norm_gradient_against_differences():
     rows, dim = 6, 96
     x, w, dy = rand(rows, dim, seed=9), rand(dim, seed=10) + 1, rand(rows, dim, seed=11)
