@@ -59,6 +59,7 @@ constexpr int kBoxRows = 64;            // rows of one B load
 constexpr int kMaxStages = 12;
 constexpr int kMaxN = 256;              // columns of one TMEM accumulator buffer
 constexpr int kMaxSmallN = 64;          // most rows of a tile with small groups
+constexpr int kShallowRows = 256;       // dw: rows per expert up to which two chunks leave at once
 constexpr uint64_t kLandNs = 100000000;  // limit for what is under way when a wait ran out
 constexpr int kSmemLimit = 227 * 1024;
 constexpr int kStaticBytes = 10 * 1024;  // Shared below
@@ -72,7 +73,7 @@ struct TcParams {
   int32_t m_tiles;       // tiles of the feature dimension
   uint32_t m_tiles_inverse;  // 2^32 / m_tiles, rounded up (of 2 and more)
   int32_t n_tiles;       // dw: tiles of its rows
-  int32_t bulk;          // outputs leave by TMA
+  int32_t bulk;          // outputs leave by TMA: a chunk at a time, or two
   int32_t pieces;        // gated: A comes eight rows a load (n is no multiple of 8)
 };
 
@@ -745,14 +746,17 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
 // e4m3 product of 64225 rows, 1024 to 2048.)  Large groups' plain outputs leave
 // by TMA, whose 64-byte swizzle is the order in which they lie there, where the
 // chunk's rows are all the group's: the load and store units, which the
-// matrices and the scales' shuffles need, see no global store.  In bf16 two
-// chunks leave at a time: the wait for TMEM, the fence and the copy's issue take
-// 590 cycles in turn whether 16 rows or 32 go, and short contractions, or a last
-// tile of few features, wait for them (gradient of 128 experts' weights, 37 rows
-// each: 4528 x 272, 135 -> 96 us; 512 x 2272, 74 -> 64; 60 experts' 1752 x 2976
-// from 5 rows each, 139 -> 102.  Where rows of results start inside a 32-byte
-// sector, n % 16 == 8, results of 200 MB and more gain less, and 512 x 2264 lost:
-// 78 -> 84).
+// matrices and the scales' shuffles need, see no global store.
+//
+// Gradients of weights from few rows an expert leave two chunks at a time: the
+// wait for TMEM, the fence and the copy's issue take 590 cycles in turn whether
+// 16 rows or 32 go, and short contractions, or a last tile of few features, wait
+// for them.  64 experts' 2048 x 2048, one chunk and two, in us: 16 rows an expert
+// 112.6, 92.2; 128 rows 118.8, 98.3; 256 rows 131.1, 124.9; 384 rows 155.7, 155.6;
+// 512 rows 188.4, 198.7; 1003 rows 309, 318.  128 experts' 4528 x 272 from 37 rows
+// 133, 96; but 512 x 2264, whose rows start inside 32-byte sectors, 78, 84.  The
+// other products, whose contractions are long, lose by it (2 x 1024 features of
+// 64225 rows 329, 351).
 //
 // Outputs whose rows do not start on 16-byte boundaries, and the weights'
 // gradients in 32 bits or added to, are stored value by value.
@@ -846,8 +850,6 @@ __device__ void store_tiles(const TcParams& p, const CUtensorMap* map_y, Shared&
   constexpr int kStride = kTurns * kChunk;        // rows from chunk to chunk
   constexpr int kScales = (kMaxN / kChunk + 2 * kTurns - 1) / (2 * kTurns);
   const int first_row = ((warp - 2) >> 2) * kChunk;
-  // plain outputs leave two chunks at a time
-  constexpr bool kDouble = kPair == 2 && !kFused && !kReadsPre && !kE4m3;
   constexpr int kOwn = kE4m3 ? 1024 : 2048;
   static_assert(kStores * kOwn <= (kE4m3 ? kOutputBytes : kStagingBytes), "the warps' memory");
   const uint32_t buf = staging + (warp - 2) * kOwn, buf_up = buf + 1024;
@@ -923,12 +925,10 @@ __device__ void store_tiles(const TcParams& p, const CUtensorMap* map_y, Shared&
     const uint32_t acc =
         sh.tmem + buffer * kMaxN + (static_cast<uint32_t>(quadrant * 32) << 16);
     int rows = left_f > 0 ? t.rows : 0;  // a warp behind the last feature stores none
-    if constexpr (kDouble)
-      if (p.bulk) {
+    if constexpr (kOp == kExpertDw)
+      if (p.bulk == 2) {
 #pragma unroll 1
         for (int c = 2 * first_row; c < rows; c += 2 * kStride) {
-          const int left = t.rows - c;
-          const int64_t r = t.row + c;
           float v[4][8] = {};
           if (!zero) {
 #pragma unroll
@@ -944,22 +944,13 @@ __device__ void store_tiles(const TcParams& p, const CUtensorMap* map_y, Shared&
           }
           if (lane == 0) bulk_wait_read_all();  // the copy before has read the buffer
           __syncwarp();
-          if (kOp == kExpertDw || left >= 2 * kChunk) {
-            stage32(buf, out[0]);
-            stage32(buf_up, out[1]);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              if (kOp == kExpertDw)
-                tma_store_3d(map_y, buf, static_cast<int>(f0), static_cast<int>(r), t.group);
-              else
-                tma_store_2d(map_y, buf, static_cast<int>(f0), static_cast<int>(r));
-              bulk_commit();
-            }
-          } else {
-            uint16_t* to = y + r * features + f0;
-            put32(buf, to, features, out[0], left, left_f);
-            put32(buf_up, to + kChunk * features, features, out[1], left - kChunk, left_f);
+          stage32(buf, out[0]);
+          stage32(buf_up, out[1]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(map_y, buf, static_cast<int>(f0), t.row + c, t.group);
+            bulk_commit();
           }
         }
         rows = 0;  // all stored
@@ -1114,21 +1105,23 @@ __device__ void store_tiles(const TcParams& p, const CUtensorMap* map_y, Shared&
         const float* w = v[i >> 2] + (i & 1) * 4 + (i >> 1 & 1) * 2;
         out[i] = pack_bf16(w[0], w[1]);
       }
-      if constexpr (kE4m3)
-        if (p.bulk) {
-          if (lane == 0) bulk_wait_read_all();  // the copy before has read the buffer
-          __syncwarp();
-          if (left >= kChunk) {
-            stage32(buf, out);
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-              tma_store_2d(map_y, buf, static_cast<int>(f0), static_cast<int>(r));
-              bulk_commit();
-            }
-            continue;
-          }
+      if (p.bulk) {  // the copy before has read the buffer
+        if (lane == 0) bulk_wait_read_all();
+        __syncwarp();
+      }
+      if (p.bulk && (kOp == kExpertDw || left >= kChunk)) {
+        stage32(buf, out);
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (kOp == kExpertDw)
+            tma_store_3d(map_y, buf, static_cast<int>(f0), static_cast<int>(r), t.group);
+          else
+            tma_store_2d(map_y, buf, static_cast<int>(f0), static_cast<int>(r));
+          bulk_commit();
         }
+        continue;
+      }
       const int64_t stride = kOp == kExpertDw ? e.y_stride : features;
       uint16_t* to =
           y + (kOp == kExpertDw ? t.group * e.y_expert_stride : 0) + r * stride + f0;
@@ -1407,14 +1400,16 @@ bool launch_expert_tc(const ExpertParams& e, void* stream, int* status) {
     ok = make_map(&a, e.x, false, e.k, e.x_rows, e.x_stride, 0, 0, 64) &&
          make_map(&b, e.w, false, e.n, e.rows, e.w_stride, 0, 0, 64);
   if (!ok) return false;
+  const bool shallow = e.rows <= kShallowRows * static_cast<int64_t>(e.experts);
   // plain bf16 outputs of large groups leave by TMA where their rows are words
   if (pair == 2 && !e.gated && !e.f32_out && !e.accumulate && features % 8 == 0 &&
       (reinterpret_cast<uintptr_t>(e.y) & 15) == 0) {
     if (e.op != kExpertDw)
-      p.bulk = make_out_map(&m.y, e.y, features, e.rows, features, 0, 0, e.e4m3 ? kChunk : 2 * kChunk);
-    else if (e.y_stride % 8 == 0 && e.y_expert_stride % 8 == 0)
-      p.bulk = make_out_map(&m.y, e.y, e.k, e.n, e.y_stride, e.experts, e.y_expert_stride,
-                            2 * kChunk);
+      p.bulk = make_out_map(&m.y, e.y, features, e.rows, features, 0, 0, kChunk);
+    else if (e.y_stride % 8 == 0 && e.y_expert_stride % 8 == 0 &&
+             make_out_map(&m.y, e.y, e.k, e.n, e.y_stride, e.experts, e.y_expert_stride,
+                          shallow ? 2 * kChunk : kChunk))
+      p.bulk = shallow ? 2 : 1;
   }
   if (!p.bulk) m.y = m.b;  // not used
 

@@ -190,6 +190,23 @@ def test_gradient_of_weights(groups, unused, K, N, gather, kind):
     assert experts.status() == ciera.OK
 
 
+@pytest.mark.parametrize("groups", [[1, 0, 40], [250, 270, 248], [255, 256, 257],
+                                    [260, 300, 209], [700, 0, 130]])
+@pytest.mark.parametrize("K,N", [(272, 40), (264, 272), (8, 8), (520, 304)])
+def test_gradient_of_weights_from_few_and_from_many_rows(groups, K, N):
+    """On both sides of 256 rows an expert, with last tiles of few features and
+    few rows, into a strided buffer whose gaps stay."""
+    offsets, R, _ = make(groups, 0)
+    dy, x = rand(R, N, seed=21), rand(R, K, seed=22)
+    want, size = ref.product_dw(dy.double(), x.double(), offsets, N, K)
+    flat = torch.full((3, N + 2, K + 8), 7.0, dtype=BF16, device="cuda")
+    out = flat[:, 1:N + 1, :K]
+    experts.mm_dw(dy, x, offsets, out=out)
+    ref.within(out, want, sums(size, max(groups)), "dw")
+    assert (flat[:, 0] == 7).all() and (flat[:, N + 1] == 7).all() and (flat[:, :, K:] == 7).all()
+    assert experts.status() == ciera.OK
+
+
 def test_a_group_with_infinities_does_not_touch_its_neighbours():
     groups, K, N = [20, 1, 50, 7], 192, 136
     offsets, R, _ = make(groups, 3)
