@@ -457,9 +457,12 @@ const char *ciera_strerror(int status);
  *     outside its buffer is taken for "none" (a zero row), an offset outside
  *     [previous offset, rows] for the nearest end of that range; offsets[0]
  *     is taken for 0.
- *   - Calls that take a workspace want ciera_moe_workspace_bytes() bytes,
- *     zero-filled once (ciera_moe_workspace_init), and use it as above:
- *     one call at a time.  Its status is read with ciera_status().
+ *   - ciera_rmsnorm_backward and ciera_route want ciera_moe_workspace_bytes()
+ *     bytes for themselves until they have run; what these hold before does
+ *     not matter.  The products keep nothing there but a status word in the
+ *     first 256 bytes: zero-filled once (ciera_moe_workspace_init), that block
+ *     may be shared by calls that run at the same time.  ciera_moe_control()
+ *     gives one.  The status is read with ciera_status().
  *   - Results do not depend on the order in which thread blocks run.
  *   - Fast paths: the products run on the tensor cores where both operands
  *     start on 16-byte boundaries and their row (and expert) strides are
@@ -478,6 +481,11 @@ int64_t ciera_moe_workspace_bytes(int64_t tokens, int64_t experts, int64_t dim);
 
 /* Zero-fill the status and control words of such a workspace on `stream`. */
 int ciera_moe_workspace_init(void *workspace_dev, void *stream);
+
+/* The library's own status block of the current device, for any number of
+ * products at once: zero when the library is loaded, there as long as the
+ * process.  Errors: CIERA_E_INVAL (NULL), CIERA_E_CUDA. */
+int ciera_moe_control(void **control_dev);
 
 /* Root-mean-square norm of s = x + residual (s = x without a residual):
  *   rstd = (mean_i s_i^2 + eps)^(-1/2),  y_i = s_i rstd weight_i

@@ -107,6 +107,7 @@ SIGNATURES = {
     "ciera_strerror": (ctypes.c_char_p, [_i32]),
     "ciera_moe_workspace_bytes": (_i64, [_i64, _i64, _i64]),
     "ciera_moe_workspace_init": (_i32, [_vp, _vp]),
+    "ciera_moe_control": (_i32, [ctypes.POINTER(_vp)]),
     "ciera_rmsnorm": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _f32, _vp, _i32, _vp, _vp,
                              _vp, _vp]),
     "ciera_rmsnorm_backward": (_i32, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _i64, _i64, _i64, _vp,

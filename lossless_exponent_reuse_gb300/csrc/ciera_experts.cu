@@ -14,6 +14,10 @@
 namespace ciera {
 namespace {
 
+// Products keep a status there and nothing else, so that calls on different
+// streams and in replayed graphs share it.
+__device__ Control g_control;
+
 constexpr int kTile = 64;
 constexpr int kDepth = 16;
 constexpr int kExpertThreads = 256;
@@ -195,6 +199,8 @@ __global__ void __launch_bounds__(kExpertThreads) k_expert_any(const ExpertParam
 int64_t tiles_of(int64_t n) { return (n + kTile - 1) / kTile; }
 
 }  // namespace
+
+int control_block(void** control) { return cudaGetSymbolAddress(control, g_control); }
 
 int launch_expert(const ExpertParams& p, void* stream) {
   int status = cudaSuccess;

@@ -157,6 +157,8 @@ int launch_gather(const GatherParams& p, void* stream);
 int launch_combine(const CombineParams& p, void* stream);
 int launch_combine_backward(const CombineParams& p, void* stream);
 int launch_expert(const ExpertParams& p, void* stream);
+// Address of the current device's control block.
+int control_block(void** control);
 // The tensor-core form; false when it cannot take these sizes and strides.
 bool launch_expert_tc(const ExpertParams& p, void* stream, int* status);
 

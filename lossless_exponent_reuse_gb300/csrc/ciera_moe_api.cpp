@@ -57,6 +57,11 @@ int ciera_moe_workspace_init(void* workspace_dev, void* stream) {
                                    static_cast<cudaStream_t>(stream)));
 }
 
+int ciera_moe_control(void** control_dev) {
+  if (!control_dev) return CIERA_E_INVAL;
+  return status_of(control_block(control_dev));
+}
+
 int ciera_rmsnorm(const uint16_t* x_dev, int64_t x_stride, const uint16_t* residual_dev,
                   int64_t residual_stride, const uint16_t* weight_dev, int64_t rows, int64_t dim,
                   float eps, void* y_dev, int y_type, float* scale_dev, uint16_t* h_dev,

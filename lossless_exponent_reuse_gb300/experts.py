@@ -17,13 +17,14 @@ that no weight is copied between the Allgather and the layer.  Matrices may
 have any row stride; their last dimension must be contiguous.
 
 Every call takes ``stream`` (a torch stream or a handle) as a keyword and runs
-on the current one without it; what it allocates belongs to that stream.
-Calls that need scratch memory share one workspace per device and stream
-(``workspace``), created on first use and grown as needed; ``status`` reads
-the error word the kernels leave there.
+on the current one without it; what it allocates, outputs and scratch memory,
+belongs to that stream or to the graph it is captured in, so that calls of
+several threads, streams and replayed graphs may overlap.  ``status`` reads the
+device's error word.
 """
 from __future__ import annotations
 
+import ctypes
 import functools
 from typing import NamedTuple, Optional, Tuple
 
@@ -76,11 +77,8 @@ def bucket_views(bucket: torch.Tensor, experts: int, dim: int, ff: int,
 
 # ---- arguments -----------------------------------------------------------
 
-_workspaces = {}
-_outgrown = []
 _needs = {}           # (tokens, experts, dim): bytes
-_NEVER = 1 << 62
-_CONTROL_BYTES = 256
+_controls = {}        # device index: its control block's address
 _functions = {}
 _raw_stream = torch._C._cuda_getCurrentRawStream
 # Rows per expert above which a product's rows are gathered before it, by a
@@ -102,35 +100,46 @@ def _on_stream(fn):
     return call
 
 
+def _scratch(index: int, tokens: int, experts: int, dim: int) -> torch.Tensor:
+    """Memory of the current stream for one call of these sizes."""
+    need = _needs.get((tokens, experts, dim))
+    if need is None:
+        need = ciera.lib().ciera_moe_workspace_bytes(tokens, experts, dim)
+        if need == 0:
+            raise ValueError(f"no workspace for {tokens} tokens, {experts} experts, {dim} columns")
+        if len(_needs) < 4096:
+            _needs[tokens, experts, dim] = need
+    return torch.empty(need, dtype=torch.uint8, device=index)
+
+
 def workspace(index: int, stream: int, tokens: int = 0, experts: int = 0,
               dim: int = 0) -> torch.Tensor:
-    """The workspace of a device index and stream handle, for calls of these sizes."""
-    ws = _workspaces.get((index, stream))
-    if ws is not None and (not tokens or ws.numel() >= _needs.get((tokens, experts, dim), _NEVER)):
-        return ws
-    need = ciera.lib().ciera_moe_workspace_bytes(tokens, experts, dim)
-    if need == 0:
-        raise ValueError(f"no workspace for {tokens} tokens, {experts} experts, {dim} columns")
-    if len(_needs) < 4096:
-        _needs[tokens, experts, dim] = need
-    if ws is None or ws.numel() < need:
-        # a power of two, and the one before is kept: a captured graph may use it
-        old, ws = ws, torch.zeros(1 << (need - 1).bit_length(), dtype=torch.uint8,
-                                  device=f"cuda:{index}")
-        if old is not None:
-            ws[:_CONTROL_BYTES].copy_(old[:_CONTROL_BYTES])  # a status not read yet
-            _outgrown.append(old)
-        _workspaces[index, stream] = ws
-    return ws
+    """A workspace for the C entry points' calls of these sizes on a stream
+    handle of a device: the caller's own, zero-filled."""
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index)):
+        return _scratch(index, tokens, experts, dim).zero_()
+
+
+def _control(index: int) -> int:
+    """The device's control block, which all products share."""
+    at = _controls.get(index)
+    if at is None:
+        got = ctypes.c_void_p()
+        _call("ciera_moe_control", index, ctypes.byref(got))
+        at = _controls[index] = got.value
+    return at
 
 
 @_on_stream
 def status(device="cuda") -> int:
-    """ciera_status of the stream's workspace: waits for the stream."""
+    """ciera_status of the device's products: waits for the stream; what other
+    streams' calls and replayed graphs have reported by then counts too."""
     index = torch.empty(0, device=device).get_device()
-    s = _raw_stream(index)
-    ws = _workspaces.get((index, s))
-    return ciera.OK if ws is None else ciera.status(ws, stream=s)
+    with torch.cuda.device(index):
+        st = ciera.lib().ciera_status(_control(index), _raw_stream(index))
+    if st == ciera.E_CUDA:
+        raise ciera.CieraError(st, "ciera_status")
+    return st
 
 
 # The checks below are on every call's path: one test where all is well, and
@@ -261,7 +270,7 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     w = _array(weight, "weight", _BF16, index, dim)
     dh_stride = 0 if dh is None else _matrix(dh, "dh", _BF16, index, rows, dim)
     s = _raw_stream(index)
-    ws = workspace(index, s, tokens=rows, dim=dim)
+    ws = _scratch(index, rows, 0, dim)
     dx = torch.empty((rows, dim), dtype=_BF16, device=dy.device)
     dweight = torch.empty(dim, dtype=_F32, device=dy.device)
     _call("ciera_rmsnorm_backward", index, dy.data_ptr(), dy_stride, h.data_ptr(), h_stride, r, w,
@@ -312,7 +321,7 @@ def route(logits: torch.Tensor, topk: int, renormalize: bool = False,
             raise ValueError("token_mask must be bool or uint8")
         mask = _array(token_mask, "token_mask", token_mask.dtype, index, tokens)
     s = _raw_stream(index)
-    ws = workspace(index, s, tokens=tokens, experts=experts)
+    ws = _scratch(index, tokens, experts, 0)
     device, pairs = logits.device, (tokens, topk)
     weights = torch.empty(pairs, dtype=_F32, device=device)
     chosen = torch.empty(pairs, dtype=_I32, device=device)
@@ -474,7 +483,7 @@ def _forward(x, w, offsets, tokens, x_scale, w_scale, gated, keep):
     _call("ciera_expert_mm", index, x.data_ptr(), x_stride, x_rows, row_tokens, w.data_ptr(),
           w_stride, w_expert_stride, xs, ws, off, rows, experts, n, k, E4M3 if e4m3 else BF16,
           GATED if gated else 0, y.data_ptr(), pre.data_ptr() if keep else None,
-          workspace(index, s).data_ptr(), s)
+          _control(index), s)
     return y, pre
 
 
@@ -516,7 +525,7 @@ def mm_dx(dy: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor,
     dx = torch.empty((rows, k if gated is None else 2 * k), dtype=_BF16, device=dy.device)
     _call("ciera_expert_mm_dx", index, dy.data_ptr(), dy_stride, w.data_ptr(), w_stride,
           w_expert_stride, off, rows, experts, n, k, pre, dx.data_ptr(),
-          workspace(index, s).data_ptr(), s)
+          _control(index), s)
     return dx
 
 
@@ -555,5 +564,5 @@ def mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
     _call("ciera_expert_mm_dw", index, dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, off, rows,
           experts, n, k, out.data_ptr(), out_stride, out_expert_stride,
           F32 if out.dtype is _F32 else BF16, ACCUMULATE if accumulate else 0,
-          workspace(index, s).data_ptr(), s)
+          _control(index), s)
     return out

@@ -219,3 +219,7 @@ def test_bucket_views_are_the_workloads_tensors():
         experts.bucket_views(bits, 3, 2048, 1024)
     with pytest.raises(ValueError):
         experts.bucket_views(bits.view(2, -1), 2, 2048, 1024)
+
+
+def test_control_block_wants_a_place():
+    assert ciera.lib().ciera_moe_control(None) == ciera.E_INVAL
