@@ -893,7 +893,9 @@ __global__ void __launch_bounds__(kPlaceThreads) k_route_place(const RouteParams
       if (e >= 0) {
         const int32_t slot = base[e] + before[e] + r;
         p.slots[pair] = slot;
-        p.row_tokens[slot] = b * kRouteTokens + i / p.topk;
+        // (counts that someone else wrote to would lead outside)
+        if (static_cast<uint32_t>(slot) < static_cast<uint32_t>(all_pairs))
+          p.row_tokens[slot] = b * kRouteTokens + i / p.topk;
       }
       if (pair >= used) p.row_tokens[pair] = -1;  // rows past the last group
     };
