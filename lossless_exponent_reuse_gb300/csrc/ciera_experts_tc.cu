@@ -214,6 +214,15 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   return r;
 }
 
+// Stores to the same place in the pair's other block.
+__device__ __forceinline__ void store_peer(const void* at, uint32_t v) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;"
+               : "=r"(a)
+               : "r"(smem_addr(at)), "r"(cluster_rank() ^ 1));
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
+}
+
 // Address of the barrier at the same place in the pair's first block.
 __device__ __forceinline__ uint32_t in_first(const uint64_t* bar) {
   uint32_t a;
@@ -329,6 +338,10 @@ struct Shared {
   uint64_t drain;                    // after a wait that ran out: the products issued are done
   uint32_t tmem;
   uint32_t stop;                     // a wait ran out: every role leaves its loop
+  // the same of the pair's other block, told when its roles have left; stages
+  // whose loads a loader that left early had issued at most, here and there
+  uint32_t peer_stop;
+  int32_t issued, peer_issued;
   int32_t start[kMaxExperts + 2];    // first row of each group; the unused rows are the last
   int32_t tile[kMaxExperts + 2];     // tiles before each group
   uint8_t per[kMaxExperts + 1];      // rows of each group's tiles, in sixteens less one
@@ -506,6 +519,8 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map, Shared& sh
   const bool gather = kOp == kExpertForward && kPair == 1 && p.e.row_tokens != nullptr;
   Place at;
   int issued = 0;
+  // a bit per stage: dw's tail[] phase to come, and whether the last load counts on it
+  uint32_t tail_parity = 0, tails = 0;
   Walk<kOp, kPair, kFused> walk;
   OutTile t;
   bool alive = true;
@@ -524,6 +539,11 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map, Shared& sh
       // by who clears it
       const bool tail = kOp == kExpertDw && t.depth - c < kDepth;
       uint32_t bar = kPair == 2 ? in_first(full) : smem_addr(full);
+      if (kOp == kExpertDw) {
+        const uint32_t bit = 1u << at.stage;
+        tails = tail ? tails | bit : tails & ~bit;
+        if (tail) tail_parity ^= bit;
+      }
       if (tail) bar = smem_addr(&sh.tail[at.stage]);
       if constexpr (kLoadsA) {
         if (tail)
@@ -562,12 +582,38 @@ __device__ void load_tiles(const TcParams& p, const CUtensorMap* map, Shared& sh
       ++issued;
     }
   }
-  // What is still under way writes this block's shared memory: see the products'
-  // last arrivals come in, or after a wait that ran out the copies land (those
-  // of a pair's second block are the first's to see).
-  for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i) {
-    uint64_t* bar = alive ? &sh.empty[i % p.stages] : &sh.full[i % p.stages];
-    if (alive || first) mbar_wait_bounded(bar, (i / p.stages) & 1, kLandNs);
+  // What is under way writes this block's shared memory: the products of the
+  // last stages have read it, or after a wait that ran out it is seen to land,
+  // tails here and the rest in settle().
+  for (int i = issued > p.stages ? issued - p.stages : 0; alive && i < issued; ++i)
+    alive = wait(p, sh, &sh.empty[i % p.stages], (i / p.stages) & 1);
+  if (alive) return;
+  atomicMax(&sh.issued, issued);
+  for (int i = 0; i < p.stages; ++i)
+    if ((tails >> i & 1) &&
+        !mbar_wait_bounded(&sh.tail[i], (tail_parity >> i & 1) ^ 1, kLandNs))
+      break;
+}
+
+// After a wait that ran out in either block of a pair, when the roles of both
+// have left: nothing of theirs may still be under way when shared memory and
+// TMEM go.  The products issued are seen to end by both blocks.  The loads count on
+// the first block's barriers: it waits for every stage that a loader of either
+// block has issued and the products have not taken.  Where another loader left
+// before its part of a stage the wait runs out, which leaves the others' loads
+// kLandNs to land, a thousand times what they take.
+template <int kPair>
+__device__ void settle(const TcParams& p, Shared& sh) {
+  const int warp = threadIdx.x >> 5;
+  const bool first = kPair == 1 || cluster_rank() == 0;
+  if (warp > 1 || !one_lane()) return;
+  if (warp == 1) {  // the lane that issued the products
+    if (first) mma_commit<kPair>(&sh.drain);
+    mbar_wait_bounded(&sh.drain, 0, kLandNs);
+  } else if (first) {
+    const int issued = max(sh.issued, sh.peer_issued);
+    for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+      if (!mbar_wait_bounded(&sh.full[i % p.stages], (i / p.stages) & 1, kLandNs)) break;
   }
 }
 
@@ -682,12 +728,7 @@ __device__ void multiply(const TcParams& p, Shared& sh, uint32_t ring) {
       if (c == 2 * kDepth || (c < 2 * kDepth && c + kDepth >= t.depth))
         have = walk.next(p, sh, next);
     }
-    if (!alive) {
-      // the tensor core is done with shared memory and TMEM before they go
-      mma_commit<kPair>(&sh.drain);
-      mbar_wait_bounded(&sh.drain, 0, kLandNs);
-      return;
-    }
+    if (!alive) return;
     mma_commit<kPair>(&sh.acc_full[buffer]);
     ++tiles;
   }
@@ -1142,6 +1183,7 @@ __device__ void store_tiles(const TcParams& p, const CUtensorMap* map_y, Shared&
     }
   }
   // nothing of this warp's is under way when its block's memory goes
+  if (kE4m3) copy_wait_all();
   if (p.bulk && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
@@ -1174,7 +1216,8 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
       mbar_init(&sh.acc_empty[i], kStores * kPair);
     }
     mbar_init(&sh.drain, 1);
-    sh.stop = 0;
+    sh.stop = sh.peer_stop = 0;
+    sh.issued = sh.peer_issued = 0;
     fence_barrier_init();
   }
   if (warp == 1) {
@@ -1212,7 +1255,16 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
     gather_tiles<kGated, kE4m3>(p, sh, ring);
   tc_fence_before();
   __syncthreads();
+  if (kPair == 2 && threadIdx.x == 0 && sh.stop) {
+    store_peer(&sh.peer_issued, static_cast<uint32_t>(sh.issued));
+    store_peer(&sh.peer_stop, 1);
+  }
   sync_all<kPair>();
+  if (*const_cast<volatile uint32_t*>(&sh.stop) | *const_cast<volatile uint32_t*>(&sh.peer_stop)) {
+    settle<kPair>(p, sh);
+    __syncthreads();
+    sync_all<kPair>();
+  }
   tc_fence_after();
   if (warp == 1) {
     if (kPair == 2)
