@@ -575,6 +575,14 @@ int ciera_gather_rows(const void *x_dev, int64_t x_stride, int64_t x_rows, int t
                       const float *x_scale_dev, const int32_t *row_tokens_dev, int64_t rows,
                       int64_t dim, void *y_dev, float *y_scale_dev, void *stream);
 
+/* The same to rows y_stride >= dim elements apart (what lies between them
+ * stays): a stride of whole 16-byte words keeps the products that read y on
+ * the tensor cores whatever dim is. */
+int ciera_gather_rows_strided(const void *x_dev, int64_t x_stride, int64_t x_rows, int type,
+                              const float *x_scale_dev, const int32_t *row_tokens_dev,
+                              int64_t rows, int64_t dim, void *y_dev, int64_t y_stride,
+                              float *y_scale_dev, void *stream);
+
 /* Rows in expert order back to their tokens:
  *   y_t = sum_j weights[t, j] row(slots[t, j]),  nothing for slots of -1
  *   weights_dev  tokens x topk floats, or NULL: 1 (the gradient of a product

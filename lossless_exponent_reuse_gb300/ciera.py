@@ -127,6 +127,8 @@ SIGNATURES = {
     "ciera_expert_mm_dw": (_i32, [_vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _vp, _i64,
                                   _i64, _i32, _u32, _vp, _vp]),
     "ciera_gather_rows": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _vp]),
+    "ciera_gather_rows_strided": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _i64, _vp, _i64,
+                                         _vp, _vp]),
 }
 
 _lock = threading.Lock()

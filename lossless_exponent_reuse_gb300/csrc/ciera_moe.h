@@ -94,6 +94,7 @@ struct GatherParams {
   int64_t rows;
   int64_t dim;
   void* y;
+  int64_t y_stride;
   float* y_scale;
 };
 

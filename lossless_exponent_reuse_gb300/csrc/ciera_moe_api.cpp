@@ -220,11 +220,19 @@ int ciera_route_backward(const float* dweights_dev, const float* weights_dev,
 int ciera_gather_rows(const void* x_dev, int64_t x_stride, int64_t x_rows, int type,
                       const float* x_scale_dev, const int32_t* row_tokens_dev, int64_t rows,
                       int64_t dim, void* y_dev, float* y_scale_dev, void* stream) {
+  return ciera_gather_rows_strided(x_dev, x_stride, x_rows, type, x_scale_dev, row_tokens_dev,
+                                   rows, dim, y_dev, dim, y_scale_dev, stream);
+}
+
+int ciera_gather_rows_strided(const void* x_dev, int64_t x_stride, int64_t x_rows, int type,
+                              const float* x_scale_dev, const int32_t* row_tokens_dev,
+                              int64_t rows, int64_t dim, void* y_dev, int64_t y_stride,
+                              float* y_scale_dev, void* stream) {
   const bool e4m3 = type == CIERA_E4M3;
   if (!e4m3 && type != CIERA_BF16) return CIERA_E_INVAL;
   const uintptr_t size = e4m3 ? 1 : 2;
-  if (!matrix(x_dev, x_rows, dim, x_stride, size) || rows < 0 || rows > kMaxRows ||
-      !buffer(row_tokens_dev, rows, 4) || !buffer(y_dev, rows * dim, size))
+  if (!matrix(x_dev, x_rows, dim, x_stride, size) ||
+      !matrix(y_dev, rows, dim, y_stride, size) || !buffer(row_tokens_dev, rows, 4))
     return CIERA_E_INVAL;
   if (e4m3 ? !buffer(x_scale_dev, x_rows, 4) || !buffer(y_scale_dev, rows, 4)
            : x_scale_dev || y_scale_dev)
@@ -240,6 +248,7 @@ int ciera_gather_rows(const void* x_dev, int64_t x_stride, int64_t x_rows, int t
   p.rows = rows;
   p.dim = dim;
   p.y = y_dev;
+  p.y_stride = y_stride;
   p.y_scale = y_scale_dev;
   return status_of(launch_gather(p, stream));
 }

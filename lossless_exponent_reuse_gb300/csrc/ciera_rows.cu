@@ -983,21 +983,24 @@ __global__ void __launch_bounds__(256) k_route_backward(const RouteBackwardParam
 
 // ------------------------------------------------------------------------
 // Gather: a warp per row, four words of a lane under way (65536 rows of 2048
-// bf16 values: 52 us, 5.2 TB/s of writes).  V bytes per access: 16 where rows and bases are
-// 16-byte aligned, else the element's size.
+// bf16 values: 52 us, 5.2 TB/s of writes).  Words V where bases and strides are
+// whole 16-byte words, and what a row has behind its last word element by
+// element; else all elements, of type E.
 
-template <typename V>
+template <typename V, typename E>
 __global__ void __launch_bounds__(kRowThreads) k_gather(const GatherParams p) {
   const int lane = threadIdx.x & 31;
   const int64_t r = (static_cast<int64_t>(blockIdx.x) * kRowThreads + threadIdx.x) >> 5;
   if (r >= p.rows) return;
   int64_t t = p.row_tokens[r];
   if (t >= p.x_rows) t = -1;
-  const int64_t n = p.dim * p.size / static_cast<int64_t>(sizeof(V));
-  V* y = static_cast<V*>(p.y) + r * n;
+  constexpr int kOf = sizeof(V) / sizeof(E);
+  const int64_t n = p.dim / kOf;
+  E* to = static_cast<E*>(p.y) + r * p.y_stride;
+  const E* from = static_cast<const E*>(p.x) + (t >= 0 ? t * p.x_stride : 0);
+  V* y = reinterpret_cast<V*>(to);
   if (t >= 0) {
-    const V* x = reinterpret_cast<const V*>(static_cast<const unsigned char*>(p.x) +
-                                            t * p.x_stride * p.size);
+    const V* x = reinterpret_cast<const V*>(from);
     int64_t i = lane;
     for (; i + 3 * 32 < n; i += 4 * 32) {
       const V a = x[i], b = x[i + 32], c = x[i + 64], d = x[i + 96];
@@ -1010,6 +1013,7 @@ __global__ void __launch_bounds__(kRowThreads) k_gather(const GatherParams p) {
   } else {
     for (int64_t i = lane; i < n; i += 32) y[i] = V{};
   }
+  if (n * kOf + lane < p.dim) to[n * kOf + lane] = t >= 0 ? from[n * kOf + lane] : E{};
   if (p.x_scale && lane == 0) p.y_scale[r] = t >= 0 ? p.x_scale[t] : 0.0f;
 }
 
@@ -1399,12 +1403,17 @@ int launch_gather(const GatherParams& p, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int blocks = static_cast<int>((p.rows + kRowThreads / 32 - 1) / (kRowThreads / 32));
   const uintptr_t at = reinterpret_cast<uintptr_t>(p.x) | reinterpret_cast<uintptr_t>(p.y);
-  if (at % 16 == 0 && p.dim * p.size % 16 == 0 && p.x_stride * p.size % 16 == 0)
-    k_gather<uint4><<<blocks, kRowThreads, 0, s>>>(p);
-  else if (p.size == 2)
-    k_gather<uint16_t><<<blocks, kRowThreads, 0, s>>>(p);
-  else
-    k_gather<uint8_t><<<blocks, kRowThreads, 0, s>>>(p);
+  const bool words = at % 16 == 0 && p.x_stride * p.size % 16 == 0 && p.y_stride * p.size % 16 == 0;
+  if (p.size == 2) {
+    if (words)
+      k_gather<uint4, uint16_t><<<blocks, kRowThreads, 0, s>>>(p);
+    else
+      k_gather<uint16_t, uint16_t><<<blocks, kRowThreads, 0, s>>>(p);
+  } else if (words) {
+    k_gather<uint4, uint8_t><<<blocks, kRowThreads, 0, s>>>(p);
+  } else {
+    k_gather<uint8_t, uint8_t><<<blocks, kRowThreads, 0, s>>>(p);
+  }
   return cudaGetLastError();
 }
 

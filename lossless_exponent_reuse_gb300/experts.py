@@ -403,13 +403,15 @@ def combine_backward(dy: torch.Tensor, rows: torch.Tensor, slots: torch.Tensor,
     return drows, dweights
 
 
-def _gather(x, tokens, x_scale, stride, index):
+def _gather(x, tokens, x_scale, stride, index, grain=1):
+    """x[tokens], rows a multiple of ``grain`` elements apart, and their scales."""
     rows, dim = tokens.numel(), x.shape[1]
-    y = torch.empty((rows, dim), dtype=x.dtype, device=x.device)
+    y_stride = -(-dim // grain) * grain
+    y = torch.empty((rows, y_stride), dtype=x.dtype, device=x.device)
     scale = None if x_scale is None else torch.empty(rows, dtype=_F32, device=x.device)
-    _call("ciera_gather_rows", index, x.data_ptr(), stride, x.shape[0],
+    _call("ciera_gather_rows_strided", index, x.data_ptr(), stride, x.shape[0],
           E4M3 if x.dtype is _E4M3 else BF16, None if x_scale is None else x_scale.data_ptr(),
-          tokens.data_ptr(), rows, dim, y.data_ptr(),
+          tokens.data_ptr(), rows, dim, y.data_ptr(), y_stride,
           None if scale is None else scale.data_ptr(), _raw_stream(index))
     return y, scale
 
@@ -473,8 +475,8 @@ def _forward(x, w, offsets, tokens, x_scale, w_scale, gated, keep):
         row_tokens = _tokens(tokens, index)
         rows = tokens.shape[0]
         if rows > _GATHER_ROWS * experts:
-            x, x_scale = _gather(x, tokens, x_scale, x_stride, index)
-            x_stride, x_rows, row_tokens = k, rows, None
+            x, x_scale = _gather(x, tokens, x_scale, x_stride, index, 16 if e4m3 else 8)
+            x_stride, x_rows, row_tokens = x.shape[1], rows, None
             xs = x_scale.data_ptr() if e4m3 else None
     n = features // 2 if gated else features
     s = _raw_stream(index)
@@ -558,8 +560,8 @@ def mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
     if experts > 1 and n and k and out_expert_stride < (n - 1) * out_stride + k:
         raise ValueError("out's experts overlap")
     if tokens is not None:
-        x, _ = _gather(x, tokens, None, x_stride, index)
-        x_stride = k
+        x, _ = _gather(x, tokens, None, x_stride, index, 8)
+        x_stride = x.shape[1]
     s = _raw_stream(index)
     _call("ciera_expert_mm_dw", index, dy.data_ptr(), dy_stride, x.data_ptr(), x_stride, off, rows,
           experts, n, k, out.data_ptr(), out_stride, out_expert_stride,

@@ -54,3 +54,67 @@ def test_rows_gathered_inside_products_of_any_size(groups, unused, K, N, kind, m
     y = experts.mm(x8, w8, offsets, tokens=tokens, x_scale=xs, w_scale=ws)
     ref.within(y, a, e, "y, 8 bits")
     assert experts.status() == ciera.OK
+
+
+def padded(t, grain):
+    """The same rows, a multiple of `grain` elements apart."""
+    wide = torch.zeros(*t.shape[:-1], -(-t.shape[-1] // grain) * grain, dtype=t.dtype,
+                       device=t.device)
+    wide[..., :t.shape[-1]] = t
+    return wide[..., :t.shape[-1]]
+
+
+@pytest.mark.parametrize("K,N", [(1001, 520), (76, 72), (9, 264)])
+def test_gathered_rows_of_odd_length_keep_the_fast_products(K, N):
+    """Rows that are no whole 16-byte words, padded to them: gathering gives what
+    the same rows, picked before, give bit for bit, so the same kernel ran."""
+    T = 700
+    offsets, R, tokens = make([300, 0, 900, 801], 9, T=T)
+    x, w = rand(T, K, seed=31), rand(4, N, K, seed=32, scale=1.0 / K ** 0.5)
+    rows = ref.gather(x, tokens, R).to(BF16)
+    want, size = ref.product(rows.double(), w, offsets)
+    y = experts.mm(padded(x, 8), padded(w, 8), offsets, tokens=tokens)
+    ref.within(y, want, sums(size, K), "y")
+    assert torch.equal(y, experts.mm(padded(rows, 8), padded(w, 8), offsets))
+
+    x8, xs = experts.quantize_rows(x)
+    w8, ws = experts.quantize_rows(w)
+    r8, rs = experts.gather_rows(x8, tokens, x_scale=xs)
+    scales = dict(w_scale=ws)
+    y = experts.mm(padded(x8, 16), padded(w8, 16), offsets, tokens=tokens, x_scale=xs, **scales)
+    assert torch.equal(y, experts.mm(padded(r8, 16), padded(w8, 16), offsets, x_scale=rs, **scales))
+
+    dy = rand(R, N, seed=33)
+    out = [torch.empty(4, N, K, device="cuda") for _ in range(2)]
+    experts.mm_dw(dy, padded(x, 8), offsets, tokens=tokens, out=out[0])
+    experts.mm_dw(dy, padded(rows, 8), offsets, out=out[1])
+    want, size = ref.product_dw(dy.double(), rows.double(), offsets, N, K)
+    ref.within(out[0], want, sums(size, 901), "dw", rounded=ref.U_F32)
+    assert torch.equal(*out)
+
+
+@pytest.mark.parametrize("dtype", [BF16, torch.uint8])
+@pytest.mark.parametrize("at,stride", [(0, 16), (0, 48), (0, 19), (3, 32), (16, 64)])
+@pytest.mark.parametrize("dim", [1, 7, 16])
+def test_gather_rows_strided(dim, at, stride, dtype):
+    """What lies between the rows stays."""
+    e4m3 = dtype is torch.uint8
+    x = torch.randint(0, 100, (11, 16), dtype=torch.uint8, device="cuda").to(dtype)[:, :dim]
+    tokens = torch.tensor([3, -1, 10, 11, 0], dtype=torch.int32, device="cuda")
+    scale = torch.rand(11, device="cuda")
+    got_scale = torch.empty(5, device="cuda")
+    flat = torch.full((at + 5 * stride,), 77, dtype=dtype, device="cuda")
+    want = flat.clone()
+    for r, t in enumerate([3, None, 10, None, 0]):
+        row = torch.zeros(dim, dtype=dtype, device="cuda") if t is None else x[t]
+        want[at + r * stride:at + r * stride + dim] = row
+    size = flat.element_size()
+    st = ciera.lib().ciera_gather_rows_strided(
+        x.data_ptr(), 16, 11, experts.E4M3 if e4m3 else experts.BF16,
+        scale.data_ptr() if e4m3 else None, tokens.data_ptr(), 5, dim,
+        flat.data_ptr() + at * size, stride, got_scale.data_ptr() if e4m3 else None,
+        torch.cuda.current_stream().cuda_stream)
+    assert st == ciera.OK and torch.equal(flat, want)
+    if e4m3:
+        assert torch.equal(got_scale, torch.stack([scale[3], scale[0] * 0, scale[10],
+                                                   scale[0] * 0, scale[0]]))

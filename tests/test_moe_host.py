@@ -223,3 +223,12 @@ def test_bucket_views_are_the_workloads_tensors():
 
 def test_control_block_wants_a_place():
     assert ciera.lib().ciera_moe_control(None) == ciera.E_INVAL
+
+
+@pytest.mark.parametrize("bad", [dict(ys=7), dict(ys=-8), dict(y=None), dict(y=ODD)])
+def test_gather_rows_strided_refuses(bad):
+    a = dict(y=FAKE, ys=8)
+    a.update(bad)
+    assert ciera.lib().ciera_gather_rows_strided(
+        vp(FAKE), 8, 3, experts.BF16, None, vp(FAKE), 4, 8, vp(a["y"]), a["ys"], None,
+        None) == ciera.E_INVAL
