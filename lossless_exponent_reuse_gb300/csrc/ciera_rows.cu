@@ -1076,12 +1076,19 @@ __global__ void __launch_bounds__(kRowThreads) k_combine(const CombineParams p) 
   }
 }
 
-// Zeros to the rows past the last group, shared among the blocks.
+// Zeros to the rows past the last group, shared among the blocks.  As the
+// products read the offsets, each is at least the one before: the last group ends
+// at the highest.
 template <typename V>
 __device__ __forceinline__ void zero_unused_rows(const CombineParams& p) {
+  __shared__ uint32_t part_max[32];
   const int64_t n = p.dim * 2 / static_cast<int64_t>(sizeof(V));
-  int64_t used = p.offsets[p.experts];
-  used = used < 0 ? 0 : used;
+  const int64_t last = p.experts > 0 ? max(p.offsets[p.experts], 0) : 0;
+  if (last + blockIdx.x >= p.n_rows) return;  // no row for this block, whatever stands before
+  uint32_t highest = 0;
+  for (int e = threadIdx.x + 1; e <= p.experts; e += blockDim.x)
+    highest = max(highest, static_cast<uint32_t>(max(p.offsets[e], 0)));
+  const int64_t used = block_max(highest, part_max);
   for (int64_t r = used + blockIdx.x; r < p.n_rows; r += gridDim.x)
     for (int64_t i = threadIdx.x; i < n; i += blockDim.x)
       reinterpret_cast<V*>(p.drows)[r * n + i] = V{};

@@ -491,3 +491,19 @@ def test_a_graph_outlives_its_workspace():
     torch.cuda.synchronize()
     assert torch.equal(dx, want[0]) and torch.equal(dw, want[1])
     assert all((f == 3.0).all() for f in filler)
+
+
+@pytest.mark.parametrize("dim", [16, 17])
+@pytest.mark.parametrize("ends,used", [([4, 2], 4), ([], 0), ([99, 3], 8), ([-3, -1], 0),
+                                       ([6, 6], 6), ([1] * 1023 + [5], 5)])
+def test_combine_gradient_reads_offsets_as_the_products_do(ends, used, dim):
+    """Rows from the highest offset on are zeroed, and no row that has a slot;
+    offsets[0] is not read."""
+    rows, dy = rand(8, dim, seed=40), rand(8, dim, seed=41)
+    slots = torch.arange(8, dtype=torch.int32, device="cuda")[:, None].clone()
+    slots[used:] = -1
+    offsets = torch.tensor([2 ** 30, *ends], dtype=torch.int32, device="cuda")
+    w = torch.full((8, 1), 0.5, device="cuda")
+    drows, dweights = experts.combine_backward(dy, rows, slots, w, offsets)
+    assert torch.equal(drows[:used], (dy[:used].float() * 0.5).to(BF16))
+    assert (drows[used:] == 0).all() and (dweights[used:] == 0).all()
