@@ -446,8 +446,9 @@ const char *ciera_strerror(int status);
  *     length) and contiguous rows; bf16 values are uint16_t bit patterns,
  *     e4m3 values uint8_t.  Sums, norms, softmax statistics and gradients'
  *     partial sums are held in 32-bit floats; each output is rounded once.
- *   - Rows, tokens or experts may be zero in number.  Any size, stride and
- *     alignment of the element type is accepted.
+ *   - Rows, tokens, columns or experts may be zero in number (a norm over no
+ *     columns has rstd 0 / 0, its e4m3 rows the scale of zeros).  Any size, stride
+ *     and alignment of the element type is accepted.
  *   - "Expert order": the (token, expert) pairs grouped by expert and, in a
  *     group, by token.  Expert e owns the rows [offsets[e], offsets[e+1]) of
  *     `rows` = tokens * topk rows; the pairs of tokens that chose fewer than

@@ -76,13 +76,14 @@ int ciera_rmsnorm(const uint16_t* x_dev, int64_t x_stride, const uint16_t* resid
   if (e4m3 ? !buffer(scale_dev, rows, 4) : scale_dev != nullptr) return CIERA_E_INVAL;
   // s may replace the residual in place, but only row for row
   if (h_dev && h_dev == residual_dev && residual_stride != dim) return CIERA_E_INVAL;
-  if (rows == 0 || dim == 0) return CIERA_OK;
+  if (rows == 0) return CIERA_OK;
   NormParams p{};
   p.x = x_dev;
   p.x_stride = x_stride;
   p.residual = residual_dev;
   p.residual_stride = residual_stride;
-  p.weight = weight_dev;
+  // of no columns: not read, but not null, which stands for "no norm"
+  p.weight = weight_dev ? weight_dev : reinterpret_cast<const uint16_t*>(rstd_dev);
   p.rows = rows;
   p.dim = dim;
   p.eps = eps;
@@ -99,7 +100,7 @@ int ciera_quantize_rows(const uint16_t* x_dev, int64_t x_stride, int64_t rows, i
   if (!matrix(x_dev, rows, dim, x_stride, 2) || !buffer(y_dev, rows * dim, 1) ||
       !buffer(scale_dev, rows, 4))
     return CIERA_E_INVAL;
-  if (rows == 0 || dim == 0) return CIERA_OK;
+  if (rows == 0) return CIERA_OK;
   NormParams p{};
   p.x = x_dev;
   p.x_stride = x_stride;
@@ -237,7 +238,7 @@ int ciera_gather_rows_strided(const void* x_dev, int64_t x_stride, int64_t x_row
   if (e4m3 ? !buffer(x_scale_dev, x_rows, 4) || !buffer(y_scale_dev, rows, 4)
            : x_scale_dev || y_scale_dev)
     return CIERA_E_INVAL;
-  if (rows == 0 || dim == 0) return CIERA_OK;
+  if (rows == 0 || (dim == 0 && !e4m3)) return CIERA_OK;
   GatherParams p{};
   p.x = x_dev;
   p.x_stride = x_stride;

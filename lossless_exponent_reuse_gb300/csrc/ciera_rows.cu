@@ -29,7 +29,8 @@ constexpr int kMostRowThreads = 512;  // for one row of the kernels that hold ro
 // (see Part; 16384 x 2047: 51 us, 74 value by value; in e4m3 66 and 80; of 511
 // values 22.5 and 22.5, and 28.7 and 24.6, the ends' words are then most of a
 // row's warps).
-// k_rmsnorm_any takes rows of any length, value by value, and reads a row once
+// k_rmsnorm_any takes rows of any length, none too (whose mean is 0 / 0, and whose
+// e4m3 scale that of zeros), value by value, and reads a row once
 // per statistic (from L1 or L2 after the first).
 
 __device__ __forceinline__ float norm_input(const NormParams& p, int64_t r, int64_t c) {
@@ -1223,6 +1224,7 @@ struct RowShape {
 
 RowShape row_shape(int64_t dim, int word, int at_first) {
   RowShape s{};
+  if (dim == 0) return s;
   for (int values = at_first; values <= (word == 8 ? 32 : 16); values *= 2) {
     const int64_t words = dim / word, vecs = values / word;
     const int64_t threads = (words + 32 * vecs - 1) / (32 * vecs) * 32;

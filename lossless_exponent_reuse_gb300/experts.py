@@ -26,6 +26,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 from typing import NamedTuple, Optional, Tuple
 
 import torch
@@ -285,7 +286,7 @@ def quantize_rows(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
     leading dimensions, if several, are contiguous (weights, laid out once)."""
     index = _index(x, "x")
     shape = x.shape
-    flat = x if len(shape) == 2 else x.reshape(-1, shape[-1])
+    flat = x if len(shape) == 2 else x.reshape(math.prod(shape[:-1]), *shape[-1:])
     stride = _matrix(flat, "x", _BF16, index)
     rows, dim = flat.shape
     y = torch.empty(shape, dtype=_E4M3, device=x.device)

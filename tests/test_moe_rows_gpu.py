@@ -507,3 +507,30 @@ def test_combine_gradient_reads_offsets_as_the_products_do(ends, used, dim):
     drows, dweights = experts.combine_backward(dy, rows, slots, w, offsets)
     assert torch.equal(drows[:used], (dy[:used].float() * 0.5).to(BF16))
     assert (drows[used:] == 0).all() and (dweights[used:] == 0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 5, 3000])
+def test_rows_of_no_columns(rows):
+    """Their scales are those of zeros and are written; memory that held something
+    else before is behind them."""
+    x, w = rand(rows, 0, seed=50), rand(0, seed=51)
+    tiny = torch.full((rows,), ref.TINY, device="cuda") / ref.E4M3_MAX
+    for res in (None, x):
+        dirty = [torch.full((rows,), 7.0, device="cuda") for _ in range(4)]
+        del dirty
+        q = experts.rmsnorm(x, w, residual=res, quantize=True)
+        assert torch.equal(q.scale, tiny) and q.rstd.isnan().all()
+        dirty = [torch.full((rows,), 7.0, device="cuda") for _ in range(4)]
+        del dirty
+        assert experts.rmsnorm(x, w, residual=res).rstd.isnan().all()
+    dirty = [torch.full((rows,), 7.0, device="cuda") for _ in range(4)]
+    del dirty
+    y, scale = experts.quantize_rows(x)
+    assert y.shape == (rows, 0) and torch.equal(scale, tiny)
+    y, scale = experts.quantize_rows(x.view(1, rows, 0))
+    assert y.shape == (1, rows, 0) and torch.equal(scale, tiny[None])
+    tokens = torch.tensor([0, -1, rows - 1], dtype=torch.int32, device="cuda")
+    dirty = [torch.full((3,), 7.0, device="cuda") for _ in range(4)]
+    del dirty
+    _, got = experts.gather_rows(y[0], tokens, x_scale=scale[0])
+    assert torch.equal(got, torch.stack([tiny[0], tiny[0] * 0, tiny[0]]))
