@@ -118,3 +118,18 @@ def test_gather_rows_strided(dim, at, stride, dtype):
     if e4m3:
         assert torch.equal(got_scale, torch.stack([scale[3], scale[0] * 0, scale[10],
                                                    scale[0] * 0, scale[0]]))
+
+
+def test_more_columns_than_a_grid_has_blocks_for():
+    """Layouts that the tensor cores' loads refuse, with over 65535 * 64 columns."""
+    wide, R = 65535 * 64 + 65, 3
+    offsets, _, _ = make([2, 1], 0)
+    x, w = rand(R, 1, seed=34), rand(2, wide, 1, seed=35)
+    want, size = ref.product(x.double(), w, offsets)
+    ref.within(experts.mm(x, w, offsets), want, sums(size, 1), "y")
+    dy, w = rand(R, 2, seed=36), rand(2, 2, wide, seed=37)
+    want, size = ref.product(dy.double(), w.transpose(1, 2), offsets)
+    ref.within(experts.mm_dx(dy, w, offsets), want, sums(size, 2), "dx")
+    x = rand(R, wide, seed=38)
+    want, size = ref.product_dw(dy, x.double(), offsets, 2, wide)
+    ref.within(experts.mm_dw(dy, x, offsets), want, sums(size, R), "dw")
