@@ -558,7 +558,9 @@ def mm_dw(dy: torch.Tensor, x: torch.Tensor, offsets: torch.Tensor,
     out_stride, out_expert_stride = _stack(out, "out", out.dtype, index)
     if out.shape != (experts, n, k):
         raise ValueError(f"out must be {[experts, n, k]}, got {list(out.shape)}")
-    if experts > 1 and n and k and out_expert_stride < (n - 1) * out_stride + k:
+    # an expert behind the other, or each row's experts side by side
+    if (experts > 1 and n and k and out_expert_stride < (n - 1) * out_stride + k
+            and (out_expert_stride < k or out_stride < (experts - 1) * out_expert_stride + k)):
         raise ValueError("out's experts overlap")
     if tokens is not None:
         x, _ = _gather(x, tokens, None, x_stride, index, 8)

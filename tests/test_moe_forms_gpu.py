@@ -133,3 +133,34 @@ def test_more_columns_than_a_grid_has_blocks_for():
     x = rand(R, wide, seed=38)
     want, size = ref.product_dw(dy, x.double(), offsets, 2, wide)
     ref.within(experts.mm_dw(dy, x, offsets), want, sums(size, R), "dw")
+
+
+@pytest.mark.parametrize("K,N", [(264, 136), (37, 19)])
+@pytest.mark.parametrize("dtype,accumulate", [(BF16, False), (BF16, True), (F32, False),
+                                              (F32, True)])
+@pytest.mark.parametrize("rows", [[40, 0, 130], [400, 300, 500]])
+def test_gradients_of_weights_with_experts_side_by_side(rows, K, N, dtype, accumulate):
+    """Each row of the result holds that row of all experts: experts closer than
+    an expert is long, and nothing overlaps."""
+    offsets, R, _ = make(rows, 0)
+    dy, x = rand(R, N, seed=39), rand(R, K, seed=40)
+    flat = torch.full((N, 3, K + 8), 3.0, dtype=dtype, device="cuda")
+    out = flat[:, :, :K].transpose(0, 1)
+    want, size = ref.product_dw(dy.double(), x.double(), offsets, N, K)
+    slack = sums(size, max(rows))
+    if accumulate:
+        want, slack = want + 3.0, slack + (3.0 + size) * ref.U_F32
+    experts.mm_dw(dy, x, offsets, out=out, accumulate=accumulate)
+    ref.within(out, want, slack, "dw", rounded=ref.U_F32 if dtype is F32 else ref.U_BF16)
+    assert (flat[:, :, K:] == 3).all()
+    assert experts.status() == ciera.OK
+
+
+def test_gradients_of_weights_refuse_experts_that_overlap():
+    offsets, R, _ = make([4, 3], 0)
+    dy, x, flat = rand(R, 5), rand(R, 6), torch.zeros(200, dtype=BF16, device="cuda")
+    for strides in ((1, 12, 1), (6, 6, 1), (5, 12, 1), (29, 6, 1), (24, 12, 1), (0, 6, 1)):
+        with pytest.raises(ValueError, match="overlap"):
+            experts.mm_dw(dy, x, offsets, out=flat.as_strided((2, 5, 6), strides))
+    for strides in ((30, 6, 1), (6, 12, 1), (54, 12, 1)):
+        experts.mm_dw(dy, x, offsets, out=flat.as_strided((2, 5, 6), strides))
