@@ -469,7 +469,9 @@ const char *ciera_strerror(int status);
  *     start on 16-byte boundaries and their row (and expert) strides are
  *     multiples of 16 bytes; the row-wise calls move 16 bytes at a time under
  *     the same condition (the norms also 4).  Other layouts take plain kernels
- *     that give the same results up to the order of their 32-bit sums.
+ *     that give the same results up to the order of their 32-bit sums and, in
+ *     the gated unit, the exponential: within 2^-16 of its value on the tensor
+ *     cores' path, where a sigmoid below 2^-126 is 0.
  */
 #define CIERA_BF16 0
 #define CIERA_E4M3 1

@@ -494,8 +494,9 @@ __device__ __forceinline__ int32_t token_row(const ExpertParams& p, int32_t r, i
   return t >= 0 && t < p.x_rows ? t : -1;
 }
 
-// exp and the reciprocal to a few units in the last of 24 bits; the results are
-// rounded to 8.  1 / inf is 0.
+// The results are rounded to 8 bits: exp within 2 + 1.173 |a| units in the last
+// of 24 (105 where it overflows, 2^-16), the reciprocal within one, below 2^-126 (a
+// under -87.3) 0.  1 / inf is 0.
 __device__ __forceinline__ float sigmoid(float a) {
   float s;
   asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(s) : "f"(1.0f + __expf(-a)));

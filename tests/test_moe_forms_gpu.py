@@ -164,3 +164,56 @@ def test_gradients_of_weights_refuse_experts_that_overlap():
             experts.mm_dw(dy, x, offsets, out=flat.as_strided((2, 5, 6), strides))
     for strides in ((30, 6, 1), (6, 12, 1), (54, 12, 1)):
         experts.mm_dw(dy, x, offsets, out=flat.as_strided((2, 5, 6), strides))
+
+
+def gates(rows, n, seed):
+    """Gates from -120 to 120, with ups and gradients of ordinary size."""
+    edge = torch.tensor([-120, -100, -90, -88.5, -88, -87.5, -87, -86, -80, -50, -20, -10, -5, -2,
+                         -1.28, -1, -0.1, 0, 0.1, 1, 2, 5, 10, 20, 50, 87, 88, 89, 100, 120.0])
+    some = torch.randint(0, len(edge), (rows, n), generator=torch.Generator().manual_seed(seed))
+    spread = (rand(rows, n, seed=seed, dtype=F32).cpu() * 0.01 + 1) * edge[some]
+    return spread.to(BF16).cuda(), rand(rows, n, seed=seed + 1, scale=30.0)
+
+
+# exp is within 2 + 1.173 |g| units in the last place of 2^-23 (CUDA's bound for
+# __expf), the sum, the reciprocal and the products behind it within 8 together;
+# a sigmoid below the smallest normal number, 2^-126, may be 0.
+def exp_slack(g):
+    return (1.173 * g.abs() + 16) * ref.U_F32
+
+
+@pytest.mark.parametrize("R", [24, 90])
+@pytest.mark.parametrize("kind", ["plain", "odd"])
+def test_gated_unit_of_large_gates(R, kind):
+    """Rows of one 1, so that the products are the weights themselves."""
+    K = n = 64
+    g, u = gates(n, K, 41)                       # as weights: feature by column
+    w = torch.cat([g, u])[None]
+    if kind == "odd":
+        w = strided(w[0], "odd")[None]
+    at = torch.arange(R, device="cuda") % K
+    x = torch.nn.functional.one_hot(at, K).to(BF16)
+    offsets = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    h, pre = experts.mm_gated(x, w, offsets, keep=True)
+    gd, ud = g.double().T[at], u.double().T[at]
+    assert torch.equal(pre.double(), torch.cat([gd, ud], 1))
+    want = ref.silu(gd) * ud
+    ref.within(h, want, want.abs() * exp_slack(gd) + (gd * ud).abs() * 2.0 ** -126, "h")
+
+
+@pytest.mark.parametrize("R", [24, 90])
+@pytest.mark.parametrize("kind", ["plain", "odd"])
+def test_gradient_through_large_gates(R, kind):
+    n, k = 64, 72
+    g, u = gates(R, k, 43)
+    w = rand(1, n, k, seed=45)
+    at = torch.arange(R, device="cuda") % n
+    dy = torch.nn.functional.one_hot(at, n).to(BF16)
+    offsets = torch.tensor([0, R], dtype=torch.int32, device="cuda")
+    got = experts.mm_dx(strided(dy, kind), w, offsets, gated=torch.cat([g, u], 1))
+    d, gd, ud = w[0].double()[at], g.double(), u.double()
+    want = ref.gated_gradient(d, torch.cat([gd, ud], 1))
+    s = 1 / (1 + torch.exp(-gd))
+    size = torch.cat([(d * ud).abs() * (1 + gd.abs()), (d * gd).abs()], 1)
+    both = torch.cat([s, s], 1) * torch.cat([exp_slack(gd)] * 2, 1)
+    ref.within(got, want, size * both + size * 2.0 ** -126, "dpre")
