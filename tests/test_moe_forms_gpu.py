@@ -217,3 +217,37 @@ def test_gradient_through_large_gates(R, kind):
     size = torch.cat([(d * ud).abs() * (1 + gd.abs()), (d * gd).abs()], 1)
     both = torch.cat([s, s], 1) * torch.cat([exp_slack(gd)] * 2, 1)
     ref.within(got, want, size * both + size * 2.0 ** -126, "dpre")
+
+
+def e4m3_in(t, pad, at):
+    """e4m3 matrices inside a larger buffer of NaNs: rows `pad` bytes further apart, from
+    byte `at` on."""
+    *stack, rows, dim = t.shape
+    ld = dim + pad
+    each = rows * ld + pad
+    n = stack[0] if stack else 1
+    buf = torch.full((at + n * each,), 0x7F, dtype=torch.uint8, device="cuda")
+    strides = (each, ld, 1) if stack else (ld, 1)
+    v = buf.as_strided(tuple(t.shape), strides, at)
+    v.copy_(t.view(torch.uint8))
+    return v.view(torch.float8_e4m3fn)
+
+
+@pytest.mark.parametrize("pad,at", [(16, 32), (16, 1), (3, 0), (5, 7)])
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("groups,unused,K,N", [GROUPS[i] for i in (2, 3, 4, 8, 9, 13)])
+def test_e4m3_operands_anywhere_in_memory(groups, unused, K, N, gather, pad, at):
+    T = 60
+    offsets, R, tokens = make(groups, unused, T=T if gather else None)
+    x8, xs = experts.quantize_rows(rand(T if gather else R, K, seed=46))
+    w8, ws = experts.quantize_rows(rand(len(groups), 2 * N, K, seed=47, scale=1.0 / K ** 0.5))
+    rows = ref.gather(x8.double() * xs.double()[:, None], tokens, R)
+    a, size = ref.product(rows, w8.double() * ws.double()[..., None], offsets)
+    e = sums(size, K + 4)
+    scales = dict(tokens=tokens, x_scale=xs, w_scale=ws)
+    x, w = e4m3_in(x8, pad, at), e4m3_in(w8, pad, at)
+    ref.within(experts.mm(x, w, offsets, **scales), a, e, "y")
+    h, pre = experts.mm_gated(x, w, offsets, keep=True, **scales)
+    ref.within(pre, a, e, "pre")
+    ref.within(h, ref.gated(a), gated_slack(a, e), "h")
+    assert experts.status() == ciera.OK

@@ -534,3 +534,23 @@ def test_rows_of_no_columns(rows):
     del dirty
     _, got = experts.gather_rows(y[0], tokens, x_scale=scale[0])
     assert torch.equal(got, torch.stack([tiny[0], tiny[0] * 0, tiny[0]]))
+
+
+@pytest.mark.parametrize("kind", ["plain", "wide", "odd"])
+@pytest.mark.parametrize("rows,dim", [(500, 5120), (500, 7168), (400, 8200), (320, 16384),
+                                      (900, 12290), (800, 17000)])
+def test_norm_gradient_of_wide_rows_with_several_a_block(rows, dim, kind):
+    h, w = rand(rows, dim, seed=52, scale=2.0), rand(dim, seed=53) + 1
+    dy, dh = rand(rows, dim, seed=54), rand(rows, dim, seed=55)
+    hd, dyd = h.double(), dy.double()
+    rd = ((hd * hd).mean(1, keepdim=True) + 1e-6) ** -0.5
+    g = dyd * w.double()
+    want = rd * g - hd * rd ** 3 * (g * hd).mean(1, keepdim=True) + dh.double()
+    size = rd * g.abs() + hd.abs() * rd ** 3 * (g * hd).abs().mean(1, keepdim=True) \
+        + dh.double().abs()
+    dx, dw = experts.rmsnorm_backward(strided(dy, kind), strided(h, kind), rd[:, 0].float(), w,
+                                      dh=strided(dh, kind))
+    ref.within(dx, want, size * (dim + 16) * ref.U_F32, "dx")
+    terms = (dyd.abs() * hd.abs() * rd).sum(0)
+    ref.within(dw, (dyd * hd * rd).sum(0), terms * (rows + 8) * ref.U_F32, "dweight",
+               rounded=ref.U_F32)
