@@ -460,10 +460,12 @@ const char *ciera_strerror(int status);
  *     is taken for 0.
  *   - ciera_rmsnorm_backward and ciera_route want ciera_moe_workspace_bytes()
  *     bytes for themselves until they have run; what these hold before does
- *     not matter.  The products keep nothing there but a status word in the
- *     first 256 bytes: zero-filled once (ciera_moe_workspace_init), that block
- *     may be shared by calls that run at the same time.  ciera_moe_control()
- *     gives one.  The status is read with ciera_status().
+ *     not matter.  Calls on one stream may share them, from several host
+ *     threads too: a call's launches are enqueued together.  The products
+ *     keep nothing but a status word in the first 256 bytes: zero-filled once
+ *     (ciera_moe_workspace_init), that block may be shared by calls that run at
+ *     the same time.  ciera_moe_control() gives one.  The status is read with
+ *     ciera_status().
  *   - Results do not depend on the order in which thread blocks run.
  *   - Fast paths: the products run on the tensor cores where both operands
  *     start on 16-byte boundaries and their row (and expert) strides are

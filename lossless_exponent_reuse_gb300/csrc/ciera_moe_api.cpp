@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstdint>
+#include <mutex>
 
 #include "ciera.h"
 #include "ciera_moe.h"
@@ -34,6 +35,11 @@ int status_of(int cuda) { return cuda == cudaSuccess ? CIERA_OK : CIERA_E_CUDA; 
 int64_t norm_backward_blocks(int64_t rows) {
   return rows < kNormBackwardBlocks ? rows : kNormBackwardBlocks;
 }
+
+// Held while a call enqueues two launches that hand scratch memory on: of calls
+// on one stream with the same scratch, from several host threads, each one's
+// launches follow one another.
+std::mutex g_launches;
 
 int64_t route_blocks(int64_t tokens) { return (tokens + kRouteTokens - 1) / kRouteTokens; }
 
@@ -143,6 +149,7 @@ int ciera_rmsnorm_backward(const uint16_t* dy_dev, int64_t dy_stride, const uint
   p.dx = dx_dev;
   p.dweight = dweight_dev;
   p.partial = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace_dev) + kMoeScratch);
+  std::lock_guard<std::mutex> together(g_launches);
   return status_of(
       launch_rmsnorm_backward(p, static_cast<int>(norm_backward_blocks(rows)), stream));
 }
@@ -184,6 +191,7 @@ int ciera_route(const void* logits_dev, int logits_type, int64_t logits_stride,
   p.row_tokens = row_tokens_dev;
   p.offsets = offsets_dev;
   p.counts = static_cast<uint8_t*>(workspace_dev) + kMoeScratch;
+  std::lock_guard<std::mutex> together(g_launches);
   return status_of(launch_route(p, stream));
 }
 

@@ -79,9 +79,11 @@ def bucket_views(bucket: torch.Tensor, experts: int, dim: int, ff: int,
 # ---- arguments -----------------------------------------------------------
 
 _needs = {}           # (tokens, experts, dim): bytes
+_workspaces = {}      # (device index, stream handle): scratch memory of its calls
 _controls = {}        # device index: its control block's address
 _functions = {}
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 # Rows per expert above which a product's rows are gathered before it, by a
 # launch of its own, instead of inside it (see ciera_expert_mm's row_tokens).
 _GATHER_ROWS = 32
@@ -101,16 +103,27 @@ def _on_stream(fn):
     return call
 
 
-def _scratch(index: int, tokens: int, experts: int, dim: int) -> torch.Tensor:
-    """Memory of the current stream for one call of these sizes."""
-    need = _needs.get((tokens, experts, dim))
-    if need is None:
-        need = ciera.lib().ciera_moe_workspace_bytes(tokens, experts, dim)
-        if need == 0:
-            raise ValueError(f"no workspace for {tokens} tokens, {experts} experts, {dim} columns")
-        if len(_needs) < 4096:
-            _needs[tokens, experts, dim] = need
-    return torch.empty(need, dtype=torch.uint8, device=index)
+def _scratch(index: int, stream: int, tokens: int, experts: int, dim: int) -> torch.Tensor:
+    """Memory for one call of these sizes on the current stream, whose handle is
+    ``stream``: calls on a stream follow one another and share it (the library
+    keeps a call's launches together), a captured call has its graph's own."""
+    need = _needs.get((tokens, experts, dim)) or _need(tokens, experts, dim)
+    if _capturing():
+        return torch.empty(need, dtype=torch.uint8, device=index)
+    ws = _workspaces.get((index, stream))
+    if ws is None or ws.numel() < need:
+        ws = _workspaces[index, stream] = torch.empty(1 << (need - 1).bit_length(),
+                                                      dtype=torch.uint8, device=index)
+    return ws
+
+
+def _need(tokens: int, experts: int, dim: int) -> int:
+    need = ciera.lib().ciera_moe_workspace_bytes(tokens, experts, dim)
+    if need == 0:
+        raise ValueError(f"no workspace for {tokens} tokens, {experts} experts, {dim} columns")
+    if len(_needs) < 4096:
+        _needs[tokens, experts, dim] = need
+    return need
 
 
 def workspace(index: int, stream: int, tokens: int = 0, experts: int = 0,
@@ -118,7 +131,7 @@ def workspace(index: int, stream: int, tokens: int = 0, experts: int = 0,
     """A workspace for the C entry points' calls of these sizes on a stream
     handle of a device: the caller's own, zero-filled."""
     with torch.cuda.stream(torch.cuda.ExternalStream(stream, device=index)):
-        return _scratch(index, tokens, experts, dim).zero_()
+        return torch.zeros(_need(tokens, experts, dim), dtype=torch.uint8, device=index)
 
 
 def _control(index: int) -> int:
@@ -271,7 +284,7 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
     w = _array(weight, "weight", _BF16, index, dim)
     dh_stride = 0 if dh is None else _matrix(dh, "dh", _BF16, index, rows, dim)
     s = _raw_stream(index)
-    ws = _scratch(index, rows, 0, dim)
+    ws = _scratch(index, s, rows, 0, dim)
     dx = torch.empty((rows, dim), dtype=_BF16, device=dy.device)
     dweight = torch.empty(dim, dtype=_F32, device=dy.device)
     _call("ciera_rmsnorm_backward", index, dy.data_ptr(), dy_stride, h.data_ptr(), h_stride, r, w,
@@ -322,7 +335,7 @@ def route(logits: torch.Tensor, topk: int, renormalize: bool = False,
             raise ValueError("token_mask must be bool or uint8")
         mask = _array(token_mask, "token_mask", token_mask.dtype, index, tokens)
     s = _raw_stream(index)
-    ws = _scratch(index, tokens, experts, 0)
+    ws = _scratch(index, s, tokens, experts, 0)
     device, pairs = logits.device, (tokens, topk)
     weights = torch.empty(pairs, dtype=_F32, device=device)
     chosen = torch.empty(pairs, dtype=_I32, device=device)
