@@ -20,7 +20,8 @@ Every call takes ``stream`` (a torch stream or a handle) as a keyword and runs
 on the current one without it; what it allocates, outputs and scratch memory,
 belongs to that stream or to the graph it is captured in, so that calls of
 several threads, streams and replayed graphs may overlap.  ``status`` reads the
-device's error word.
+device's error word.  Nothing is registered with autograd: outputs carry no
+history, and a training step makes the gradients' calls itself.
 """
 from __future__ import annotations
 
@@ -82,6 +83,7 @@ _needs = {}           # (tokens, experts, dim): bytes
 _workspaces = {}      # (device index, stream handle): scratch memory of its calls
 _controls = {}        # device index: its control block's address
 _functions = {}
+_MAX_TOPK = 32        # the router's limit
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _capturing = torch._C._cuda_isCurrentStreamCapturing
 # Rows per expert above which a product's rows are gathered before it, by a
@@ -295,8 +297,9 @@ def rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, rstd: torch.Tensor,
 
 @_on_stream
 def quantize_rows(x: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor]:
-    """ciera_quantize_rows: (e4m3, scale per row) of bf16 [..., dim] whose
-    leading dimensions, if several, are contiguous (weights, laid out once)."""
+    """ciera_quantize_rows: (e4m3, scale per row) of bf16 [..., dim] (weights,
+    laid out once; several leading dimensions that no one row stride covers, as
+    a bucket's views have them, are copied first)."""
     index = _index(x, "x")
     shape = x.shape
     flat = x if len(shape) == 2 else x.reshape(math.prod(shape[:-1]), *shape[-1:])
@@ -327,8 +330,8 @@ def route(logits: torch.Tensor, topk: int, renormalize: bool = False,
     stride = _matrix(logits, "logits", logits.dtype, index)
     tokens, experts = logits.shape
     topk = int(topk)
-    if not 1 <= topk <= experts:
-        raise ValueError(f"topk must be in 1..{experts}, got {topk}")
+    if not 1 <= topk <= min(experts, _MAX_TOPK):
+        raise ValueError(f"topk must be in 1..{min(experts, _MAX_TOPK)}, got {topk}")
     mask = None
     if token_mask is not None:
         if token_mask.dtype not in (torch.bool, torch.uint8):

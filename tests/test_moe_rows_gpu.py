@@ -554,3 +554,13 @@ def test_norm_gradient_of_wide_rows_with_several_a_block(rows, dim, kind):
     terms = (dyd.abs() * hd.abs() * rd).sum(0)
     ref.within(dw, (dyd * hd * rd).sum(0), terms * (rows + 8) * ref.U_F32, "dweight",
                rounded=ref.U_F32)
+
+
+def test_route_refuses_more_choices_than_it_makes():
+    logits = rand(3, 64, seed=60, dtype=F32)
+    for topk, most in ((0, 32), (33, 32), (64, 32), (-1, 32)):
+        with pytest.raises(ValueError, match=f"1..{most}"):
+            experts.route(logits, topk)
+    with pytest.raises(ValueError, match="1..8"):
+        experts.route(logits[:, :8], 9)
+    assert experts.route(logits, 32).weights.shape == (3, 32)
