@@ -7,8 +7,8 @@
 //   dw       A = x transposed (k contiguous)       B = dy transposed; c: the
 //                                                  group's rows
 // so that a group's rows are the N of the instruction, which may be any
-// multiple of 16: a ragged group wastes at most 15 columns where rows in M
-// would waste up to 127, and the lanes of a warp hold neighbouring features of
+// multiple of 16, for pairs of blocks of 32: a ragged group wastes at most 15
+// columns, or 31, where rows in M would waste up to 127 or 255, and the lanes of a warp hold neighbouring features of
 // one row, which they store contiguously without a transposition.
 //
 // The gated product's M are 64 gates and the 64 ups that go with them, eight of
@@ -785,7 +785,8 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
 // their way into the warp's shared memory, and 16 bytes of a row at a time go on
 // to the output.  What the gated unit's gradient reads takes the same way back.
 // (Sixteen 2-byte stores of a thread's feature: 147 instead of 137 us for the
-// e4m3 product of 64225 rows, 1024 to 2048.)  Large groups' plain outputs leave
+// e4m3 product of 64225 rows, 1024 to 2048.  That product is bound by this chain
+// of steps: 6.0 thousand cycles a tile, of which the products take 4.1.)  Large groups' plain outputs leave
 // by TMA, whose 64-byte swizzle is the order in which they lie there, where the
 // chunk's rows are all the group's: the load and store units, which the
 // matrices and the scales' shuffles need, see no global store.
@@ -801,7 +802,9 @@ __device__ void clear_tails(const TcParams& p, Shared& sh, unsigned char* ring_p
 // 64225 rows 329, 351).
 //
 // Outputs whose rows do not start on 16-byte boundaries, and the weights'
-// gradients in 32 bits or added to, are stored value by value.
+// gradients in 32 bits or added to, are stored value by value: 64 experts' 2048 x
+// 2048 from 65536 rows 322 us in bf16, 406 in 32 bits, 616 added to 32 bits, and
+// 1440 added to bf16, whose 2-byte words are read and written one by one.
 
 constexpr int kChunk = 16;
 

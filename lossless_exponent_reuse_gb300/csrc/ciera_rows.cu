@@ -498,6 +498,10 @@ __global__ void __launch_bounds__(kMostRowThreads, kVecs * Word<W>::kValues <= 8
 // and reading its own words, so that the bytes under way do not depend on
 // registers.  Rows of 16384 x 2048 values not in L2: 47 us with the sum of the
 // blocks' parts (57 us with one row ahead in registers); 10007 x 1536: 25 us and 5.
+// Wider rows, with all launches and nothing in L2: 16384 x 4096 94 us, 5.7 TB/s; x
+// 5120 148, 4.6, and x 7168 170, 5.5, by the form above, of whose rows two do not
+// fit the ring; 4096 x 12288 174, 2.3, whose 32 values a thread leave the
+// registers; 2048 x 20000 297, 1.1, value by value.
 template <int kVecs, int kRing>
 __global__ void __launch_bounds__(kMostRowThreads)
     k_rmsnorm_backward_ring(const NormBackwardParams p) {
@@ -642,7 +646,9 @@ __global__ void __launch_bounds__(1024) k_sum_partials(const float* partial, int
 // remaining, lowest index" (the first round's is the softmax's maximum), then
 // the softmax's sum and the chosen weights.  Bound by issue slots, about 600
 // instructions a token: 16384 tokens, 128 experts, 8 chosen: 13.4 us, and 8.6 for
-// k_route_place; one token 3.1 us.
+// k_route_place; one token 3.1 us.  From 257 experts on a lane holds 32 logits, which
+// leave the registers, and sorts as many whatever their number: both launches 43 us
+// with 256 experts, 365 with 384, 530 with 1024 (the gradient 18, 84, 121).
 //
 // The order: a token chooses an expert at most once, so a pair's rank among
 // its block's pairs of the same expert is the number of earlier tokens of the
@@ -1118,7 +1124,8 @@ __global__ void __launch_bounds__(kRowThreads) k_combine_backward_any(const Comb
 // The same 16 bytes at a time: a block per token, eight rows at once.  The
 // eight dot products are reduced together: at each of three exchanges a lane
 // hands over half of its sums, so that a warp needs 9 exchanges for 8 sums.
-// Bound by memory: 8192 tokens, 8 rows of 2048 values, 85 us, 6.8 TB/s.
+// Bound by memory: 8192 tokens, 8 rows of 2048 values, one in twenty unused, 85 us,
+// 6.6 TB/s.
 __global__ void __launch_bounds__(kRowThreads) k_combine_backward(const CombineParams p) {
   __shared__ int32_t slot[kMaxTopk];
   __shared__ float weight[kMaxTopk];
@@ -1198,10 +1205,6 @@ void route_backward_at(const RouteBackwardParams& p, int blocks, cudaStream_t s)
 
 int grid_of(int64_t n) { return static_cast<int>(n < (1 << 30) ? n : (1 << 30)); }
 
-}  // namespace
-
-namespace {
-
 bool on16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 // Widest words that a call's rows and buffers allow: 8, 2 or 1 values.
@@ -1263,10 +1266,6 @@ void norm_backward_at(const NormBackwardParams& p, dim3 block, int blocks, cudaS
   const size_t smem = block.y > 1 ? 4 * static_cast<size_t>(p.dim) : 0;
   k_rmsnorm_backward<W, kVecs, kShift><<<blocks, block, smem, s>>>(p);
 }
-
-}  // namespace
-
-namespace {
 
 template <int kVecs, int kRing>
 int backward_ring(const NormBackwardParams& p, dim3 block, int blocks, size_t bytes,
