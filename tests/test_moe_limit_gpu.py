@@ -53,3 +53,22 @@ def test_a_limit_shorter_than_the_contraction(kind):
         ciera.set_wait_timeout_ns(1_000_000_000)
     assert torch.equal(call(), want)
     assert experts.status() == ciera.OK
+
+
+def test_a_replayed_graph_reports_to_the_device_s_status():
+    """The limit is the one at the time of the capture; whoever asks next hears."""
+    call = deep("weights")
+    want = call()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    try:
+        ciera.set_wait_timeout_ns(1000)
+        torch.cuda.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            call()
+    finally:
+        ciera.set_wait_timeout_ns(1_000_000_000)
+    assert experts.status() == ciera.OK
+    graph.replay()
+    assert experts.status() == ciera.E_TIMEOUT
+    assert torch.equal(call(), want)
+    assert experts.status() == ciera.OK
