@@ -666,6 +666,158 @@ int ciera_expert_mm_dw(const uint16_t *dy_dev, int64_t dy_stride, const uint16_t
                        int64_t dw_expert_stride, int dw_type, uint32_t flags,
                        void *workspace_dev, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators of the attention half of a layer whose weights the path above
+ * rebuilds: rotary positions and their gradient, the pages of a serving
+ * step's requests, keys and values into those pages, and attention over them.
+ *
+ * The conventions of the mixture-of-experts operators hold (bf16 bit patterns,
+ * 32-bit sums and statistics, one rounding per output, counts of zero, any
+ * stride and alignment of the element type, results that do not depend on the
+ * order in which thread blocks run), and
+ *   - A head's values are contiguous; tokens and heads have strides of their
+ *     own, in elements: a view of a product that made q, k and v at once is
+ *     taken in place.
+ *   - Tokens of several requests lie one request behind the other: request r
+ *     owns the tokens [offsets[r], offsets[r+1]).  offsets[0] is taken for 0,
+ *     an offset outside [0, tokens] for the nearest end; a request whose end is
+ *     not behind its begin has no tokens.  Offsets that fall give rows that
+ *     belong to two requests, which hold either's result, or to none.
+ *   - A slot is page * page_size + place.  A page outside [0, pages) holds
+ *     zeros where it is read, and a slot outside the cache is not written.
+ */
+#define CIERA_INTERLEAVED 1u   /* pairs (2i, 2i + 1); else (i, i + pairs) */
+#define CIERA_INVERSE 2u       /* the gradient: turned back */
+
+/* Rotary positions.  The first 2 * pairs values of each head are rotated,
+ * pair by pair, and the others copied:
+ *   y_a = s (x_a cos t - x_b sin t),  y_b = s (x_a sin t + x_b cos t)
+ * s the amplitude, t = 2 pi frac(position * turns[i] / 2^64): frequencies are
+ * given in 2^-64 of a turn per position, modulo 2^64, and multiplied as such,
+ * so that no position is too far.  CIERA_INVERSE: with -t, which is the
+ * gradient (of x, from that of y).
+ *   x_dev, y_dev   tokens x heads x head_dim bf16; y may be x itself (the same
+ *                  pointer and strides), else must not overlap it
+ *   positions_dev  tokens
+ *   turns_dev      pairs
+ * Errors: CIERA_E_INVAL (a negative size, 2 * pairs > head_dim, head_dim >
+ * 1024, tokens * heads > 2^31 - 4096, overlapping rows of y, NULL or misaligned
+ * pointers, unknown flags, an amplitude that is not finite), CIERA_E_CUDA. */
+int ciera_rotary(const uint16_t *x_dev, int64_t x_token_stride, int64_t x_head_stride,
+                 const int32_t *positions_dev, const int64_t *turns_dev, int64_t pairs,
+                 float amplitude, int64_t tokens, int64_t heads, int64_t head_dim,
+                 uint16_t *y_dev, int64_t y_token_stride, int64_t y_head_stride, uint32_t flags,
+                 void *stream);
+
+/* Pages of keys and values.  Row (page, place, head) of head_dim contiguous
+ * values starts at page * stride[0] + place * stride[1] + head * stride[2]
+ * (elements).  CIERA_BF16, or CIERA_E4M3 with an exponent per row at
+ * page * stride[0] + place * stride[1] + head * stride[2] of its own: the row
+ * stands for e4m3 * 2^(exponent - 127), NaN where the exponent is 255. */
+typedef struct {
+    void *key_dev;
+    void *value_dev;
+    uint8_t *key_exponent_dev;    /* CIERA_E4M3, else NULL */
+    uint8_t *value_exponent_dev;
+    int64_t key_stride[3];
+    int64_t value_stride[3];
+    int64_t key_exponent_stride[3];
+    int64_t value_exponent_stride[3];
+    int64_t pages;
+    int64_t page_size;
+    int64_t heads;
+    int64_t head_dim;
+    int64_t type;
+} ciera_cache;
+
+/* Rotated queries, and keys and values into their slots, in one call:
+ *   q_out = rotary(q);  key[slot] = rotary(k);  value[slot] = v
+ * e4m3 rows are rounded from the unrounded values with the exponent
+ *   127 + min(119, max(-100, least e with m <= 448 * 2^e)),
+ * m the largest |a| + |b| of the row's pairs times |amplitude| (no rotation
+ * exceeds it) or |x| behind them and in v; 27 for a row of zeros, 255 where m is
+ * infinite or NaN.
+ *   q_dev, q_out_dev  tokens x q_heads x head_dim bf16; q_out may be q itself
+ *   k_dev, v_dev      tokens x cache->heads x head_dim bf16
+ *   slots_dev         tokens; two tokens of one slot: either's rows stay
+ * Errors: as ciera_rotary (CIERA_INVERSE is refused), and CIERA_E_INVAL for
+ * pages * page_size > 2^31 - 1 or another cache that does not fit the above. */
+int ciera_append(const uint16_t *q_dev, int64_t q_token_stride, int64_t q_head_stride,
+                 const uint16_t *k_dev, int64_t k_token_stride, int64_t k_head_stride,
+                 const uint16_t *v_dev, int64_t v_token_stride, int64_t v_head_stride,
+                 const int32_t *positions_dev, const int32_t *slots_dev, const int64_t *turns_dev,
+                 int64_t pairs, float amplitude, int64_t tokens, int64_t q_heads,
+                 uint16_t *q_out_dev, int64_t out_token_stride, int64_t out_head_stride,
+                 const ciera_cache *cache, uint32_t flags, void *stream);
+
+/* The pages of a step.  Request r holds cached[r] tokens in the pages that its
+ * row of the table names, and gets new[r] more (negative: 0).  In order of the
+ * requests the pages that it lacks are taken from the top of the stack of
+ * free pages; the first request whose pages are not there, or do not fit its
+ * row, or whose new tokens pass `tokens`, gets none, nor does any behind it
+ * that wants pages.
+ *   table_dev      requests x width page numbers (rows table_stride apart);
+ *                  the places of new pages are written
+ *   free_dev       the stack: capacity page numbers, of which the first
+ *                  count_dev[0] are free
+ *   count_out_dev  what is left of count (may be count_dev)
+ *   offsets_dev    requests + 1: running sum of new, tokens at most
+ *   context_dev    requests: cached + new, 0 for a request that got no pages
+ *                  (attention then gives its rows zeros)
+ *   lengths_dev    requests: cached + new, or cached; the next step's cached
+ *                  (may be cached_dev)
+ *   positions_dev  tokens: cached + place among the new, 0 behind the last
+ *   slots_dev      tokens: -1 behind the last and without pages
+ * Errors: CIERA_E_INVAL (a negative size, requests > 2^20, page_size < 1, a
+ * short stride, NULL or misaligned pointers), CIERA_E_CUDA. */
+int ciera_assign_pages(const int32_t *cached_dev, const int32_t *new_dev, int64_t requests,
+                       int64_t tokens, int64_t page_size, int32_t *table_dev,
+                       int64_t table_stride, int64_t width, const int32_t *free_dev,
+                       int64_t capacity, const int32_t *count_dev, int32_t *count_out_dev,
+                       int32_t *offsets_dev, int32_t *context_dev, int32_t *lengths_dev,
+                       int32_t *positions_dev, int32_t *slots_dev, void *stream);
+
+/* The pages of requests that are done, back on the stack: for each r with
+ * done[r] != 0, in order, its row's first ceil(lengths[r] / page_size) pages are
+ * pushed, their places become -1 and lengths[r] 0.  Pages outside
+ * [0, capacity) are not pushed, nor what would pass capacity.
+ * Errors: as ciera_assign_pages. */
+int ciera_release_pages(const uint8_t *done_dev, int32_t *lengths_dev, int64_t requests,
+                        int64_t page_size, int32_t *table_dev, int64_t table_stride,
+                        int64_t width, int32_t *free_dev, int64_t capacity,
+                        const int32_t *count_dev, int32_t *count_out_dev, void *stream);
+
+/* Bytes of workspace of ciera_attend for these heads on the current device. 0
+ * for a negative argument, or no such heads. */
+int64_t ciera_attend_workspace_bytes(int64_t q_heads, int64_t heads, int64_t head_dim);
+
+/* Attention of each request's new tokens over its pages.  With n new tokens
+ * and L = context[r], token i sees the first L - n + i + 1 keys (the new ones
+ * are the last of L, appended before):
+ *   o = sum_j p_j v_j,  p_j = exp(scale q . k_j - max) / sum of them
+ * over the keys it sees; zeros where it sees none, and in the rows behind the
+ * last request.  Keys that a token does not see have no part in its row, be
+ * they infinite or NaN.  q's head h reads the cache's head
+ * h / (q_heads / heads).  Weights are rounded to 16 bits (8 significant) on
+ * their way to the tensor cores, sums and maxima held in 32.
+ *   q_dev        tokens x q_heads x head_dim bf16
+ *   table_dev    requests x width pages, rows table_stride apart
+ *   offsets_dev  requests + 1
+ *   context_dev  requests, at most width * page_size each
+ *   longest      most new tokens of a request, as far as the caller knows: fewer
+ *                launches, never other rows; tokens if unknown
+ *   o_dev        tokens x q_heads x head_dim bf16, contiguous
+ * The workspace belongs to the call until it has run; what it holds before does
+ * not matter.  control_dev: a status block (ciera_moe_control).
+ * Errors: CIERA_E_INVAL (heads that do not divide q_heads, head_dim outside
+ * [1, 256], tokens * q_heads > 2^31 - 4096, scale not finite, ...), CIERA_E_CUDA. */
+int ciera_attend(const uint16_t *q_dev, int64_t q_token_stride, int64_t q_head_stride,
+                 int64_t tokens, int64_t q_heads, const ciera_cache *cache,
+                 const int32_t *table_dev, int64_t table_stride, int64_t width,
+                 const int32_t *offsets_dev, const int32_t *context_dev, int64_t requests,
+                 int64_t longest, float scale, uint16_t *o_dev, void *workspace_dev,
+                 int64_t workspace_bytes, void *control_dev, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

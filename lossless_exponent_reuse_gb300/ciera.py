@@ -129,6 +129,17 @@ SIGNATURES = {
     "ciera_gather_rows": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _i64, _vp, _vp, _vp]),
     "ciera_gather_rows_strided": (_i32, [_vp, _i64, _i64, _i32, _vp, _vp, _i64, _i64, _vp, _i64,
                                          _vp, _vp]),
+    "ciera_rotary": (_i32, [_vp, _i64, _i64, _vp, _vp, _i64, _f32, _i64, _i64, _i64, _vp, _i64,
+                            _i64, _u32, _vp]),
+    "ciera_append": (_i32, [_vp, _i64, _i64] * 3 + [_vp, _vp, _vp, _i64, _f32, _i64, _i64, _vp, _i64,
+                                                    _i64, _vp, _u32, _vp]),
+    "ciera_assign_pages": (_i32, [_vp, _vp, _i64, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp,
+                                  _vp, _vp, _vp, _vp, _vp, _vp]),
+    "ciera_release_pages": (_i32, [_vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _vp,
+                                   _vp]),
+    "ciera_attend_workspace_bytes": (_i64, [_i64, _i64, _i64]),
+    "ciera_attend": (_i32, [_vp, _i64, _i64, _i64, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _i64, _i64,
+                            _f32, _vp, _vp, _i64, _vp, _vp]),
 }
 
 _lock = threading.Lock()

@@ -1,0 +1,44 @@
+// ciera_attend.cu -- attention over pages of keys and values: which form a call
+// takes, and the form that takes any size, stride and alignment.
+#include "ciera_attend_device.cuh"
+
+namespace ciera {
+namespace {
+
+constexpr int kAnyWarps = 4;
+
+// A warp per row (token and query head), a key at a time.  Bound by its
+// instructions: right for every layout, not fast.
+__global__ void __launch_bounds__(32 * kAnyWarps) k_attend_any(const AttendParams p) {
+  const int64_t row = static_cast<int64_t>(blockIdx.x) * kAnyWarps + (threadIdx.x >> 5);
+  const int heads = p.heads * p.group;
+  const int64_t t = row / heads;
+  if (t >= p.tokens) return;
+  const int head = static_cast<int>(row - t * heads), lane = threadIdx.x & 31;
+  int32_t request, place;
+  Slice own{};
+  find_row(p, static_cast<int32_t>(t), &request, &place);
+  if (request >= 0) {
+    const Request r = request_of(p, request);
+    warp_attend(p, p.q + t * p.q_token + head * p.q_head, request, head / p.group, 0,
+                seen_keys(r, place), &own);
+  }
+  const float by = inverse_sum(own.sum);
+  uint16_t* o = p.o + row * p.head_dim;
+#pragma unroll
+  for (int i = 0; i < kSliceValues; ++i)
+    if (lane + 32 * i < p.head_dim) o[lane + 32 * i] = f32_to_bf16(own.o[i] * by);
+}
+
+}  // namespace
+
+int64_t attend_workspace_bytes(int64_t, int64_t, int64_t) { return 256; }
+
+int launch_attend(const AttendParams& p, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int64_t rows = static_cast<int64_t>(p.tokens) * p.heads * p.group;
+  k_attend_any<<<static_cast<unsigned>((rows + kAnyWarps - 1) / kAnyWarps), 32 * kAnyWarps, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace ciera

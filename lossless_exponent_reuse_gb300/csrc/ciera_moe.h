@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <mutex>
 
 #include "ciera.h"
 #include "ciera_internal.h"
@@ -17,6 +18,11 @@ constexpr int64_t kMoeScratch = 256;    // offset of the scratch behind the cont
 
 // Limit of every bounded device-side wait (ciera_set_wait_timeout_ns).
 uint64_t wait_timeout_ns();
+
+// Held while a call enqueues launches that hand scratch memory on: of calls on
+// one stream with the same scratch, from several host threads, each one's
+// launches follow one another.
+std::mutex& launches();
 
 struct NormParams {
   const uint16_t* x;

@@ -107,9 +107,14 @@ def _on_stream(fn):
 
 def _scratch(index: int, stream: int, tokens: int, experts: int, dim: int) -> torch.Tensor:
     """Memory for one call of these sizes on the current stream, whose handle is
-    ``stream``: calls on a stream follow one another and share it (the library
+    ``stream``."""
+    return _scratch_bytes(index, stream,
+                          _needs.get((tokens, experts, dim)) or _need(tokens, experts, dim))
+
+
+def _scratch_bytes(index: int, stream: int, need: int) -> torch.Tensor:
+    """Calls on a stream follow one another and share its memory (the library
     keeps a call's launches together), a captured call has its graph's own."""
-    need = _needs.get((tokens, experts, dim)) or _need(tokens, experts, dim)
     if _capturing():
         return torch.empty(need, dtype=torch.uint8, device=index)
     ws = _workspaces.get((index, stream))
