@@ -32,9 +32,27 @@ __global__ void __launch_bounds__(32 * kAnyWarps) k_attend_any(const AttendParam
 
 }  // namespace
 
-int64_t attend_workspace_bytes(int64_t, int64_t, int64_t) { return 256; }
+namespace {
 
-int launch_attend(const AttendParams& p, void* stream) {
+int sm_count() {
+  int device = 0, n = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+    return 1;
+  return n;
+}
+
+}  // namespace
+
+int64_t attend_workspace_bytes(int64_t, int64_t, int64_t) {
+  return (split_workspace_bytes(sm_count()) + 255) / 256 * 256;
+}
+
+int launch_attend(const AttendParams& given, void* stream) {
+  AttendParams p = given;
+  p.wide_rows = 0x7FFFFFFF;
+  p.split_blocks = 2 * sm_count();
+  if (split_takes(p)) return launch_attend_split(p, stream);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = static_cast<int64_t>(p.tokens) * p.heads * p.group;
   k_attend_any<<<static_cast<unsigned>((rows + kAnyWarps - 1) / kAnyWarps), 32 * kAnyWarps, 0, s>>>(p);

@@ -142,5 +142,233 @@ __device__ __noinline__ void warp_attend(const AttendParams& p, const uint16_t* 
   for (int i = 0; i < kSliceValues; ++i) own->o[i] = o[i];
 }
 
+// ------------------------------------------------------------------------
+// How a call's work is dealt out.  A tile is up to kRows rows (new tokens by
+// query heads of one head of keys, token by token); a unit is kKeys keys of a
+// tile, as many units as its last row sees, one if that sees none.  All units of
+// all tiles, in order of request, head and tile, are cut into as many even
+// ranges as there are blocks, whatever the lengths are: ragged batches, one long
+// context and whole prompts fill the blocks alike.  A block that has a part of
+// a tile leaves its sums in the workspace, in a slot of its own: slot 0 if the tile
+// began before it, slot 1 if it goes on behind it.  The parts of a tile are joined
+// by a launch of their own, in the order of the blocks.
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// Requests of up to p.wide_rows rows a head, or those of more.
+template <bool kWide>
+__device__ __forceinline__ bool is_own(const AttendParams& p, const Request& r) {
+  const int32_t rows = r.tokens * p.group;
+  return r.tokens > 0 && (rows > p.wide_rows) == kWide;
+}
+
+template <int kRows, int kKeys>
+struct Tiles {
+  static __device__ __forceinline__ int32_t count(const AttendParams& p, const Request& r) {
+    return (r.tokens * p.group + kRows - 1) / kRows;
+  }
+  // Keys that a tile's last row sees.
+  static __device__ __forceinline__ int32_t keys(const AttendParams& p, const Request& r,
+                                                 int32_t tile) {
+    const int32_t left = r.tokens * p.group - tile * kRows;
+    const int32_t last = tile * kRows + (left < kRows ? left : kRows) - 1;
+    return seen_keys(r, p.group == 1 ? last : last / p.group);
+  }
+  static __device__ __forceinline__ int32_t units(const AttendParams& p, const Request& r,
+                                                  int32_t tile) {
+    const int32_t n = (keys(p, r, tile) + p.unit_keys - 1) / p.unit_keys;
+    return n > 0 ? n : 1;
+  }
+  static __device__ int64_t of_head(const AttendParams& p, const Request& r) {
+    const int32_t n = count(p, r);
+    int64_t sum = 0;
+    for (int32_t t = 0; t < n; ++t) sum += units(p, r, t);
+    return sum;
+  }
+};
+
+// A block's range and where it begins.
+struct Share {
+  int64_t total, begin, end;
+  int64_t into;      // units of the first request before it
+  int32_t request;
+  int32_t blocks;    // that have units: each one at least
+};
+
+// Sums over the block, inclusive; `part` holds a value per warp and one more.
+template <int kThreads>
+__device__ __forceinline__ int64_t scan_block(int64_t v, int64_t* part, int64_t* all) {
+  constexpr int kWarps = kThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t left = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += left;
+  }
+  __syncthreads();
+  if (lane == 31) part[warp] = v;
+  __syncthreads();
+  int64_t sum = 0;
+#pragma unroll
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) v += part[w];
+    sum += part[w];
+  }
+  *all = sum;
+  return v;
+}
+
+// Fills `share` for block `block` of `blocks`; all kThreads threads.
+template <bool kWide, int kRows, int kKeys, int kThreads>
+__device__ void find_share(const AttendParams& p, int block, int blocks, int64_t* part,
+                           Share* share) {
+  using T = Tiles<kRows, kKeys>;
+  const auto units = [&](int32_t r) -> int64_t {
+    if (r >= p.requests) return 0;
+    const Request q = request_of(p, r);
+    return is_own<kWide>(p, q) ? T::of_head(p, q) * p.heads : 0;
+  };
+  int64_t own = 0, total;
+  for (int32_t base = 0; base < p.requests; base += kThreads) own += units(base + threadIdx.x);
+  const int64_t first = own;
+  scan_block<kThreads>(own, part, &total);
+  if (total < blocks) blocks = static_cast<int>(total);
+  const int64_t begin = block < blocks ? block * total / blocks : total;
+  const int64_t end = block < blocks ? (block + 1) * total / blocks : total;
+  if (threadIdx.x == 0) {
+    share->blocks = blocks;
+    share->total = total;
+    share->begin = begin;
+    share->end = end;
+    share->request = p.requests;
+    share->into = 0;
+  }
+  int64_t before = 0;
+  for (int32_t base = 0; begin < end && base < p.requests && before <= begin; base += kThreads) {
+    const int32_t r = base + threadIdx.x;
+    const int64_t n = p.requests <= kThreads ? first : units(r);
+    int64_t all;
+    const int64_t to = before + scan_block<kThreads>(n, part, &all);
+    if (begin < to && begin >= to - n) {
+      share->request = r;
+      share->into = begin - (to - n);
+    }
+    before += all;
+  }
+  __syncthreads();
+}
+
+// Units [from, to) of one tile, of `all`.
+struct Segment {
+  Request request;
+  int32_t index;     // of the request
+  int32_t head, tile;
+  int32_t from, to, all;
+  int32_t keys;      // that the tile's last row sees
+  int32_t rows;      // of the tile
+  int64_t end;       // of the tile, in units of all
+};
+
+template <bool kWide, int kRows, int kKeys>
+struct Walk {
+  using T = Tiles<kRows, kKeys>;
+  Request request;
+  int32_t index, head = 0, tile = 0, unit = 0, tiles = 0;
+  int64_t at, end;
+
+  __device__ Walk(const AttendParams& p, const Share& s)
+      : index(s.request), at(s.begin), end(s.end) {
+    if (at >= end) return;
+    request = request_of(p, index);
+    tiles = T::count(p, request);
+    int64_t into = s.into;
+    const int64_t of_head = T::of_head(p, request);
+    head = static_cast<int32_t>(into / of_head);
+    into -= head * of_head;
+    for (int32_t n = T::units(p, request, 0); into >= n; n = T::units(p, request, tile)) {
+      into -= n;
+      ++tile;
+    }
+    unit = static_cast<int32_t>(into);
+  }
+  __device__ bool next(const AttendParams& p, Segment* s) {
+    if (at >= end) return false;
+    s->request = request;
+    s->index = index;
+    s->head = head;
+    s->tile = tile;
+    s->keys = T::keys(p, request, tile);
+    s->all = T::units(p, request, tile);
+    const int32_t left = request.tokens * p.group - tile * kRows;
+    s->rows = left < kRows ? left : kRows;
+    s->from = unit;
+    s->to = end - at < s->all - unit ? unit + static_cast<int32_t>(end - at) : s->all;
+    s->end = at - unit + s->all;
+    at += s->to - unit;
+    unit = s->to;
+    if (unit == s->all) {
+      unit = 0;
+      if (++tile == tiles) {
+        tile = 0;
+        if (++head == p.heads) {
+          head = 0;
+          while (at < end && ++index < p.requests) {
+            request = request_of(p, index);
+            if (is_own<kWide>(p, request)) break;
+          }
+          if (index >= p.requests) end = at;
+          tiles = T::count(p, request);
+        }
+      }
+    }
+    return true;
+  }
+};
+
+// What a block says of the tile that begins in it and ends in another: the
+// parts to join, its own slot 1 and the next blocks' slots 0.
+struct Joint {
+  int32_t parts;   // 0: none
+  int32_t first;   // the request's first token
+  int32_t row;     // the tile's first row
+  int32_t rows;
+  int32_t head;
+  int32_t pad[3];
+};
+
+__device__ __forceinline__ void leave_joint(Joint* joint, const Segment* s, const Share& share,
+                                            int32_t row, int block) {
+  Joint j{};
+  if (s) {
+    // the last block that begins before the tile's end
+    const int64_t last = (s->end * share.blocks + share.total - 1) / share.total - 1;
+    j.parts = static_cast<int32_t>(last) - block + 1;
+    j.first = s->request.first;
+    j.row = row;
+    j.rows = s->rows;
+    j.head = s->head;
+  }
+  *joint = j;
+}
+
+// Query and output of a row: row `row` of a head's rows of a request.
+__device__ __forceinline__ const uint16_t* query_row(const AttendParams& p, int32_t first,
+                                                     int32_t head, int32_t row) {
+  const int32_t i = p.group == 1 ? row : row / p.group;
+  return p.q + (static_cast<int64_t>(first) + i) * p.q_token +
+         (head * p.group + row - i * p.group) * p.q_head;
+}
+__device__ __forceinline__ uint16_t* output_row(const AttendParams& p, int32_t first, int32_t head,
+                                                int32_t row) {
+  const int32_t i = p.group == 1 ? row : row / p.group;
+  return p.o + ((static_cast<int64_t>(first) + i) * (p.heads * p.group) + head * p.group + row -
+                i * p.group) *
+                   p.head_dim;
+}
+
 }  // namespace
 }  // namespace ciera

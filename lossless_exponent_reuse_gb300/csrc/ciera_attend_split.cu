@@ -1,0 +1,594 @@
+// ciera_attend_split.cu -- attention of few rows a head over pages.
+//
+// Bound by memory: every key and value is read once, for all query heads that
+// share it.  Four warps of a block take 16 keys each of a unit of 64, on their
+// own: each has a ring of stages in shared memory that its lanes fill by
+// asynchronous copies, a row of a page at a time, some 24 KB ahead, and joins the
+// others at the end of a tile alone.
+//
+// The products have the keys as rows and the queries as columns, S^T = K Q^T of
+// 16 x 8, so that eight rows (8 query heads, say) cost one instruction per 16
+// values of the heads; the weights' fragments are transposed in registers
+// (movmatrix) for O^T = V^T P^T, whose values come transposed from shared memory
+// (ldmatrix).  mma.sync does: at the rate of memory it is idle.
+//
+// e4m3 rows are widened to fp16, which holds them exactly, on their way into
+// the fragments; queries are fp16 too, scaled by a power of two per row (an error of
+// 2^-25 of a row's largest value at most).  A key's exponent goes on its scores; a
+// value's goes into its weight's exponent before the maximum is taken, so that weights
+// stay in range however the rows' exponents lie, and is taken out of the sum again.
+//
+// The running maximum moves only where a score passes it by 2^8 (weights are at
+// most 256, which 8 bits of mantissa hold as well as 1): most units then need
+// neither the maximum over the lanes nor the sums' scaling.
+#include "ciera_attend_device.cuh"
+#include "ciera_device.cuh"
+
+namespace ciera {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kUnitKeys = 64;
+constexpr int kWarpKeys = kUnitKeys / kWarps;
+constexpr int kRingBytes = 24 * 1024;   // of a warp
+constexpr float kSlack = 8.0f;
+constexpr int kMostPartValues = 4096 + 64;  // floats of a part: rows by values, maxima, sums
+
+__device__ __forceinline__ void ldsm(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void ldsm_t(uint32_t addr, uint32_t (&v)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ uint32_t transpose(uint32_t v) {
+  uint32_t t;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(t) : "r"(v));
+  return t;
+}
+template <bool kHalf>
+__device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if (kHalf)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two e4m3 values of the low (0) or high (1) half of a word, as fp16.
+template <int kHigh>
+__device__ __forceinline__ uint32_t widen(uint32_t v) {
+  uint32_t h;
+  if (kHigh)
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}"
+        : "=r"(h)
+        : "r"(v));
+  else
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}"
+        : "=r"(h)
+        : "r"(v));
+  return h;
+}
+__device__ __forceinline__ uint32_t pack_half(float lo, float hi) {
+  uint32_t v;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(v) : "f"(hi), "f"(lo));
+  return v;
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int kLeft>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(kLeft) : "memory");
+}
+
+// kDim: values of a row in shared memory, those past the head's own zeros.
+// kBlocks: of 8 rows of a tile.
+template <int kDim, int kBlocks, bool kE4m3>
+struct Form {
+  static constexpr int kRows = 8 * kBlocks;
+  static constexpr int kRowBytes = kDim * (kE4m3 ? 1 : 2);
+  static constexpr int kPieces = kRowBytes / 16;
+  static constexpr int kSideBytes = kWarpKeys * kRowBytes;
+  static constexpr int kStageBytes = 2 * kSideBytes;
+  static constexpr int kStages = kStageBytes > kRingBytes / 2 ? 3 : kRingBytes / kStageBytes;
+  static constexpr int kQueryStride = kDim + 8;      // 16-bit values; eight rows in different banks
+  static constexpr int kSumStride = kDim + 4;        // floats, likewise
+  static constexpr int kQueryBytes = kRows * kQueryStride * 2;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kSumBytes = kWarps * kRows * kSumStride * 4;
+  static constexpr int kSmem =
+      kQueryBytes + (kWarps * kWarpBytes > kSumBytes ? kWarps * kWarpBytes : kSumBytes);
+  static constexpr int kPartValues = kRows * (kDim + 2);
+  static constexpr int kSteps = kDim / 16;
+  static constexpr bool kKeep = kSteps * kBlocks <= 16;  // queries' fragments in registers
+  static_assert(kPartValues <= kMostPartValues, "a part's place in the workspace");
+};
+
+// Bytes from a row's start at which its 16-byte piece lies: eight rows' pieces
+// of one place are in different banks.
+template <int kPieces>
+__device__ __forceinline__ int piece_at(int row, int piece) {
+  return kPieces >= 8 ? ((piece ^ (row & 7)) << 4) : ((piece ^ ((row >> 1) & (kPieces - 1))) << 4);
+}
+
+struct Shared {
+  Share share;
+  int64_t part[kWarps + 1];
+  float query_scale[32];
+  int32_t seen[32];              // keys that a row sees
+  float most[kWarps][32], sum[kWarps][32];
+  uint32_t again;                // rows to be computed again
+};
+
+template <int kDim, int kBlocks, bool kE4m3>
+__global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p) {
+  using F = Form<kDim, kBlocks, kE4m3>;
+  extern __shared__ __align__(16) unsigned char raw[];
+  __shared__ Shared sh;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int blocks = gridDim.x, block = blockIdx.x;
+  const int column = lane & 3, line = lane >> 2;   // of a fragment
+  uint16_t* queries = reinterpret_cast<uint16_t*>(raw);
+  unsigned char* ring = raw + F::kQueryBytes;
+  const uint32_t own_ring = smem_addr(ring) + warp * F::kWarpBytes;
+  float* sums = reinterpret_cast<float*>(ring);
+  Joint* joint = reinterpret_cast<Joint*>(p.workspace) + block;
+  float* parts = reinterpret_cast<float*>(reinterpret_cast<Joint*>(p.workspace) + blocks);
+
+  find_share<false, F::kRows, kUnitKeys, kThreads>(p, block, blocks, sh.part, &sh.share);
+  Walk<false, F::kRows, kUnitKeys> walk(p, sh.share);
+  Segment seg;
+  bool left_joint = false;
+  const int size = kE4m3 ? 1 : 2;
+  const int pieces = p.head_dim * size / 16;       // that a row has
+
+  while (walk.next(p, &seg)) {
+    const int32_t row0 = seg.tile * F::kRows;
+    // ---- queries: a warp a row
+    if (threadIdx.x == 0) sh.again = 0;
+    for (int r = warp; r < F::kRows; r += kWarps) {
+      const bool live = r < seg.rows;
+      const uint16_t* q = query_row(p, seg.request.first, seg.head, row0 + (live ? r : 0));
+      uint16_t v[kDim / 32];
+      uint32_t most = 0;
+#pragma unroll
+      for (int i = 0; i < kDim / 32; ++i) {
+        const int d = lane + 32 * i;
+        v[i] = live && d < p.head_dim ? q[d] : 0;
+        most = max(most, static_cast<uint32_t>(v[i] & 0x7FFF));
+      }
+      float by = 1.0f, scale = p.scale * kLog2e;
+      if (kE4m3) {
+        // the largest value to 2^13 .. 2^14
+        most = __reduce_max_sync(0xffffffffu, most);
+        int e = static_cast<int>(most >> 7) - 127 - 13;
+        e = most >= 0x7F80u ? 0 : e < -100 ? -100 : e;
+        by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
+        scale *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+      }
+#pragma unroll
+      for (int i = 0; i < kDim / 32; ++i) {
+        uint16_t w = v[i];
+        if (kE4m3) w = static_cast<uint16_t>(pack_half(bf16_to_f32(v[i]) * by, 0.0f));
+        queries[r * F::kQueryStride + lane + 32 * i] = w;
+      }
+      if (lane == 0) {
+        sh.query_scale[r] = scale;
+        sh.seen[r] = live ? seen_keys(seg.request, (row0 + r) / p.group) : 0;
+      }
+    }
+    __syncthreads();
+    float scale[kBlocks][2], top[kBlocks][2], sum[kBlocks][2];
+    int32_t seen[kBlocks][2];
+    int32_t least = 0x7FFFFFFF;
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = b * 8 + 2 * column + j;
+        scale[b][j] = sh.query_scale[r];
+        seen[b][j] = sh.seen[r];
+        if (r < seg.rows) least = min(least, seen[b][j]);
+        top[b][j] = minus_infinity();
+        sum[b][j] = 0.0f;
+      }
+    least = __reduce_min_sync(0xffffffffu, least);  // all rows see the keys before
+    // queries' fragments of one step: bf16 in the heads' order; of e4m3 a lane has four
+    // neighbouring values of a row, which a word of keys has too
+    const auto query = [&](int step, int b, uint32_t& b0, uint32_t& b1) {
+      const uint16_t* row = queries + (b * 8 + line) * F::kQueryStride + step * 16;
+      if (kE4m3) {
+        const uint2 w = *reinterpret_cast<const uint2*>(row + 4 * column);
+        b0 = w.x;
+        b1 = w.y;
+      } else {
+        b0 = *reinterpret_cast<const uint32_t*>(row + 2 * column);
+        b1 = *reinterpret_cast<const uint32_t*>(row + 2 * column + 8);
+      }
+    };
+    uint32_t qf[F::kKeep ? F::kSteps : 1][F::kKeep ? kBlocks : 1][2];
+    if (F::kKeep)
+#pragma unroll
+      for (int s = 0; s < F::kSteps; ++s)
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+          query(s, b, qf[F::kKeep ? s : 0][F::kKeep ? b : 0][0],
+                qf[F::kKeep ? s : 0][F::kKeep ? b : 0][1]);
+    float o[F::kSteps][kBlocks][4] = {};
+
+    // ---- this warp's units
+    const int units = seg.to - seg.from;
+    const int32_t key0 = seg.from * kUnitKeys + warp * kWarpKeys;
+    const int64_t head_k = seg.head * p.key.stride[2], head_v = seg.head * p.value.stride[2];
+    // Lanes 0 to 15 know where the keys of a unit begin, 16 to 31 where its values; -1:
+    // zeros.
+    const auto locate = [&](int unit) -> int64_t {
+      const int32_t key = key0 + unit * kUnitKeys + (lane & 15);
+      if (unit >= units || key >= seg.keys) return -1;
+      const int32_t at = key / p.page_size, page = page_at(p, seg.index, at);
+      if (page < 0) return -1;
+      const int32_t place = key - at * p.page_size;
+      return lane < 16 ? page * p.key.stride[0] + place * p.key.stride[1] + head_k
+                       : page * p.value.stride[0] + place * p.value.stride[1] + head_v;
+    };
+    const auto exponent_of = [&](int unit) -> uint32_t {
+      const int32_t key = key0 + unit * kUnitKeys + (lane & 15);
+      if (unit >= units || key >= seg.keys) return kExponentBias;
+      const int32_t at = key / p.page_size, page = page_at(p, seg.index, at);
+      if (page < 0) return kExponentBias;
+      const int32_t place = key - at * p.page_size;
+      const Side& s = lane < 16 ? p.key : p.value;
+      return s.exponent[page * s.exponent_stride[0] + place * s.exponent_stride[1] +
+                        seg.head * s.exponent_stride[2]];
+    };
+    const auto issue = [&](int unit, int64_t where) {
+      if (unit < units) {
+        const uint32_t to = own_ring + (unit % F::kStages) * F::kStageBytes;
+#pragma unroll
+        for (int side = 0; side < 2; ++side)
+#pragma unroll
+          for (int i = 0; i < kWarpKeys * F::kPieces / 32; ++i) {
+            const int at = i * 32 + lane, row = at / F::kPieces, piece = at % F::kPieces;
+            const int64_t from = __shfl_sync(0xffffffffu, where, side * 16 + row);
+            const unsigned char* base =
+                static_cast<const unsigned char*>(side ? p.value.data : p.key.data);
+            const bool some = from >= 0 && piece < pieces;
+            copy16(to + side * F::kSideBytes + row * F::kRowBytes + piece_at<F::kPieces>(row, piece),
+                   some ? base + from * size + piece * 16 : base, some ? 16 : 0);
+          }
+      }
+      copy_commit();
+    };
+#pragma unroll 1
+    for (int u = 0; u < F::kStages; ++u) issue(u, locate(u));
+    int64_t where = locate(F::kStages);
+    uint32_t exponent = kE4m3 ? exponent_of(0) : 0;
+
+#pragma unroll 1
+    for (int u = 0; u < units; ++u) {
+      copy_wait<F::kStages - 1>();
+      __syncwarp();
+      const uint32_t keys_at = own_ring + (u % F::kStages) * F::kStageBytes;
+      const uint32_t values_at = keys_at + F::kSideBytes;
+      // ---- scores: 16 keys by 8 rows a block
+      float s[kBlocks][4] = {};
+      if (kE4m3) {
+#pragma unroll
+        for (int step = 0; step < F::kSteps; step += 2) {
+          uint32_t w[4];
+          const int row = lane & 15;
+          ldsm(keys_at + row * F::kRowBytes + piece_at<F::kPieces>(row, step + (lane >> 4)), w);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t a[4] = {widen<0>(w[2 * h]), widen<0>(w[2 * h + 1]), widen<1>(w[2 * h]),
+                                   widen<1>(w[2 * h + 1])};
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b) {
+              uint32_t b0, b1;
+              if (F::kKeep) {
+                b0 = qf[F::kKeep ? step + h : 0][F::kKeep ? b : 0][0];
+                b1 = qf[F::kKeep ? step + h : 0][F::kKeep ? b : 0][1];
+              } else {
+                query(step + h, b, b0, b1);
+              }
+              mma<true>(s[b], a, b0, b1);
+            }
+          }
+        }
+      } else {
+#pragma unroll
+        for (int step = 0; step < F::kSteps; ++step) {
+          uint32_t a[4];
+          const int row = lane & 15;
+          ldsm(keys_at + row * F::kRowBytes + piece_at<F::kPieces>(row, 2 * step + (lane >> 4)), a);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) {
+            uint32_t b0, b1;
+            if (F::kKeep) {
+              b0 = qf[F::kKeep ? step : 0][F::kKeep ? b : 0][0];
+              b1 = qf[F::kKeep ? step : 0][F::kKeep ? b : 0][1];
+            } else {
+              query(step, b, b0, b1);
+            }
+            mma<false>(s[b], a, b0, b1);
+          }
+        }
+      }
+      // ---- weights: a lane has keys `line` and `line` + 8 of rows 2 column and the next
+      const int32_t key = key0 + u * kUnitKeys + line;
+      float back[2] = {1.0f, 1.0f};   // 2^-e of the values
+      float shift[2] = {0.0f, 0.0f}, key_scale[2] = {1.0f, 1.0f};
+      if (kE4m3) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t ke = __shfl_sync(0xffffffffu, exponent, line + 8 * j);
+          const uint32_t ve = __shfl_sync(0xffffffffu, exponent, 16 + line + 8 * j);
+          key_scale[j] = scale_of(ke);
+          shift[j] = ve == 255 ? __uint_as_float(0x7FC00000u)
+                               : static_cast<float>(static_cast<int>(ve) - kExponentBias);
+          back[j] = __uint_as_float((254 - min(ve, 254u)) << 23);
+        }
+        exponent = exponent_of(u + 1);
+      }
+      const bool masked = key0 + u * kUnitKeys + kWarpKeys > least;
+      bool rises = false;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = i & 1, k = i >> 1;
+          float t = s[b][i] * scale[b][j];
+          if (kE4m3) t = t * key_scale[k] + shift[k];
+          if (masked && key + 8 * k >= seen[b][j]) t = minus_infinity();
+          s[b][i] = t;
+          rises |= t > top[b][j] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, rises)) {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float m = fmaxf(s[b][j], s[b][2 + j]);
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            m = fmaxf(m, top[b][j]);
+            const float by = m == minus_infinity() ? 1.0f : exp2_fast(top[b][j] - m);
+            top[b][j] = m;
+            sum[b][j] *= by;
+#pragma unroll
+            for (int t = 0; t < F::kSteps; ++t) {
+              o[t][b][j] *= by;
+              o[t][b][2 + j] *= by;
+            }
+          }
+      }
+      uint32_t weights[kBlocks][2];
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float base = top[b][i & 1] == minus_infinity() ? 0.0f : top[b][i & 1];
+          const float w = exp2_fast(s[b][i] - base);
+          s[b][i] = w;
+          sum[b][i & 1] += kE4m3 ? w * back[i >> 1] : w;
+        }
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+          weights[b][k] = transpose(kE4m3 ? pack_half(s[b][2 * k], s[b][2 * k + 1])
+                                          : pack_bf16(s[b][2 * k], s[b][2 * k + 1]));
+      }
+      // ---- sums: 16 values of the heads by 8 rows a block
+      if (kE4m3) {
+        // a 16-bit element is two values: fragments of even and odd ones
+#pragma unroll
+        for (int step = 0; step < F::kSteps; step += 2) {
+          uint32_t w[4];
+          const int row = lane & 15;
+          ldsm_t(values_at + row * F::kRowBytes + piece_at<F::kPieces>(row, step + (lane >> 4)), w);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t lo = __byte_perm(w[2 * h], 0, 0x3120);
+            const uint32_t hi = __byte_perm(w[2 * h + 1], 0, 0x3120);
+            const uint32_t a[4] = {widen<0>(lo), widen<1>(lo), widen<0>(hi), widen<1>(hi)};
+#pragma unroll
+            for (int b = 0; b < kBlocks; ++b)
+              mma<true>(o[step + h][b], a, weights[b][0], weights[b][1]);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int step = 0; step < F::kSteps; ++step) {
+          uint32_t w[4];
+          const int row = (lane & 7) + ((lane >> 4) << 3);
+          ldsm_t(values_at + row * F::kRowBytes +
+                     piece_at<F::kPieces>(row, 2 * step + (lane >> 3 & 1)),
+                 w);
+#pragma unroll
+          for (int b = 0; b < kBlocks; ++b) mma<false>(o[step][b], w, weights[b][0], weights[b][1]);
+        }
+      }
+      __syncwarp();
+      issue(u + F::kStages, where);
+      where = locate(u + F::kStages + 1);
+    }
+    copy_wait<0>();
+
+    // ---- the warps' sums, through the ring's memory
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float l = sum[b][j];
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+        const int r = b * 8 + 2 * column + j;
+        if (line == 0) {
+          sh.most[warp][r] = top[b][j];
+          sh.sum[warp][r] = l;
+        }
+        float* to = sums + (warp * F::kRows + r) * F::kSumStride;
+#pragma unroll
+        for (int t = 0; t < F::kSteps; ++t) {
+          to[t * 16 + (kE4m3 ? 2 * line : line)] = o[t][b][j];
+          to[t * 16 + (kE4m3 ? 2 * line + 1 : line + 8)] = o[t][b][2 + j];
+        }
+      }
+    __syncthreads();
+    const bool whole = seg.from == 0 && seg.to == seg.all;
+    float* part = parts + (2 * block + (seg.from == 0)) * static_cast<int64_t>(F::kPartValues);
+    // rows of different sight: what one does not see may have spoilt its products
+    const bool differ = seg.rows > p.group;
+    for (int at = threadIdx.x; at < seg.rows * kDim; at += kThreads) {
+      const int r = at / kDim, d = at % kDim;
+      float m = sh.most[0][r];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.most[w][r]);
+      const float base = m == minus_infinity() ? 0.0f : m;
+      float l = 0.0f, v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float by = exp2_fast(sh.most[w][r] - base);
+        l += sh.sum[w][r] * by;
+        v += sums[(w * F::kRows + r) * F::kSumStride + d] * by;
+      }
+      if (differ && !(fabsf(v) + fabsf(l) < __uint_as_float(0x7F800000u)))
+        atomicOr(&sh.again, 1u << r);
+      if (whole) {
+        if (d < p.head_dim)
+          output_row(p, seg.request.first, seg.head, row0 + r)[d] = f32_to_bf16(v * inverse_sum(l));
+      } else {
+        part[2 * F::kRows + at] = v;
+        if (d == 0) {
+          part[r] = m;
+          part[F::kRows + r] = l;
+        }
+      }
+    }
+    __syncthreads();
+    for (uint32_t again = sh.again; again; again &= again - 1) {
+      const int r = __ffs(again) - 1;
+      if (r % kWarps != warp) continue;
+      Slice own;
+      const int32_t to = min(seg.to * kUnitKeys, sh.seen[r]);
+      warp_attend(p, query_row(p, seg.request.first, seg.head, row0 + r), seg.index, seg.head,
+                  seg.from * kUnitKeys, to, &own);
+      uint16_t* out = output_row(p, seg.request.first, seg.head, row0 + r);
+#pragma unroll
+      for (int i = 0; i < kSliceValues; ++i) {
+        const int d = lane + 32 * i;
+        if (d >= p.head_dim) continue;
+        if (whole)
+          out[d] = f32_to_bf16(own.o[i] * inverse_sum(own.sum));
+        else
+          part[2 * F::kRows + r * kDim + d] = own.o[i];
+      }
+      if (!whole && lane == 0) {
+        part[r] = own.most;
+        part[F::kRows + r] = own.sum;
+      }
+    }
+    if (!whole && seg.from == 0) {
+      if (threadIdx.x == 0) leave_joint(joint, &seg, sh.share, row0, block);
+      left_joint = true;
+    }
+    __syncthreads();
+  }
+  if (!left_joint && threadIdx.x == 0) leave_joint(joint, nullptr, sh.share, 0, block);
+}
+
+// Joins a tile's parts, a block for each of k_attend_split's; rows behind the
+// last request become zeros.
+template <int kDim, int kBlocks>
+__global__ void __launch_bounds__(kThreads) k_attend_join(const AttendParams p) {
+  using F = Form<kDim, kBlocks, false>;
+  const int blocks = p.split_blocks, block = blockIdx.x;
+  const Joint j = reinterpret_cast<const Joint*>(p.workspace)[block];
+  const float* parts =
+      reinterpret_cast<const float*>(reinterpret_cast<const Joint*>(p.workspace) + blocks);
+  const auto part = [&](int i) {
+    return parts + (2 * (block + i) + (i == 0)) * static_cast<int64_t>(F::kPartValues);
+  };
+  if (j.parts > 0) {
+    for (int at = threadIdx.x; at < j.rows * kDim; at += kThreads) {
+      const int r = at / kDim, d = at % kDim;
+      float m = minus_infinity(), l = 0.0f, v = 0.0f;
+      for (int i = 0; i < j.parts; ++i) {
+        const float* from = part(i);
+        const float top = from[r];
+        const float most = fmaxf(m, top);
+        const float base = most == minus_infinity() ? 0.0f : most;
+        const float old = exp2_fast(m - base), by = exp2_fast(top - base);
+        l = l * old + from[F::kRows + r] * by;
+        v = v * old + from[2 * F::kRows + at] * by;
+        m = most;
+      }
+      if (d < p.head_dim)
+        output_row(p, j.first, j.head, j.row + r)[d] = f32_to_bf16(v * inverse_sum(l));
+    }
+  }
+  const int64_t width = static_cast<int64_t>(p.heads) * p.group * p.head_dim;
+  const int64_t behind = p.requests ? clamp_to(p.offsets[p.requests], p.tokens) : 0;
+  for (int64_t at = behind * width + block * kThreads + threadIdx.x; at < p.tokens * width;
+       at += static_cast<int64_t>(blocks) * kThreads)
+    p.o[at] = 0;
+}
+
+template <int kDim, int kBlocks, bool kE4m3>
+int launch_at(const AttendParams& p, cudaStream_t s) {
+  using F = Form<kDim, kBlocks, kE4m3>;
+  const cudaError_t err = allow_shared<k_attend_split<kDim, kBlocks, kE4m3>>(F::kSmem);
+  if (err != cudaSuccess) return err;
+  k_attend_split<kDim, kBlocks, kE4m3><<<p.split_blocks, kThreads, F::kSmem, s>>>(p);
+  k_attend_join<kDim, kBlocks><<<p.split_blocks, kThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+template <int kDim, int kBlocks>
+int launch_with(const AttendParams& p, cudaStream_t s) {
+  return p.e4m3 ? launch_at<kDim, kBlocks, true>(p, s) : launch_at<kDim, kBlocks, false>(p, s);
+}
+
+bool on_words(const Side& s, int size) {
+  return (reinterpret_cast<uintptr_t>(s.data) & 15) == 0 && s.stride[0] * size % 16 == 0 &&
+         s.stride[1] * size % 16 == 0 && s.stride[2] * size % 16 == 0;
+}
+
+}  // namespace
+
+// Rows of whole 16-byte pieces.
+bool split_takes(const AttendParams& p) {
+  const int size = p.e4m3 ? 1 : 2;
+  return p.head_dim * size % 16 == 0 && on_words(p.key, size) && on_words(p.value, size);
+}
+
+int64_t split_workspace_bytes(int sms) {
+  return 2 * static_cast<int64_t>(sms) * (sizeof(Joint) + 2 * 4 * kMostPartValues);
+}
+
+int launch_attend_split(const AttendParams& given, void* stream) {
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  AttendParams p = given;
+  p.unit_keys = kUnitKeys;
+  // rows of a tile: as many as a request has at most, by eights
+  const int64_t rows = p.longest * p.group < p.wide_rows ? p.longest * p.group : p.wide_rows;
+  if (p.head_dim <= 64)
+    return rows <= 8 ? launch_with<64, 1>(p, s)
+                     : rows <= 16 ? launch_with<64, 2>(p, s) : launch_with<64, 4>(p, s);
+  if (p.head_dim <= 128)
+    return rows <= 8 ? launch_with<128, 1>(p, s)
+                     : rows <= 16 ? launch_with<128, 2>(p, s) : launch_with<128, 4>(p, s);
+  p.split_blocks /= 2;  // one to an SM
+  return rows <= 8 ? launch_with<256, 1>(p, s) : launch_with<256, 2>(p, s);
+}
+
+}  // namespace ciera
