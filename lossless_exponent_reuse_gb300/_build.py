@@ -14,11 +14,13 @@ LIB_CHECKED = os.path.join(OUT_DIR, "libciera_checked.so")
 SOURCES = ["ciera_kernels.cu", "ciera_rans.cu", "ciera_api.cpp", "ciera_noalloc.cu",
            "ciera_moe_api.cpp", "ciera_rows.cu", "ciera_experts.cu",
            "ciera_experts_tc.cu", "ciera_attention_api.cpp", "ciera_rotary.cu",
-           "ciera_attend.cu", "ciera_attend_split.cu"]
+           "ciera_attend.cu", "ciera_attend_split.cu",
+           "ciera_attend_wide.cu"]
 HEADERS = [os.path.join(ROOT, "include", "ciera.h"), os.path.join(CSRC, "ciera_internal.h"),
            os.path.join(CSRC, "ciera_device.cuh"), os.path.join(CSRC, "ciera_rans.h"),
            os.path.join(CSRC, "ciera_moe.h"), os.path.join(CSRC, "ciera_moe_device.cuh"),
-           os.path.join(CSRC, "ciera_attention.h"), os.path.join(CSRC, "ciera_attend_device.cuh")]
+           os.path.join(CSRC, "ciera_attention.h"), os.path.join(CSRC, "ciera_attend_device.cuh"),
+           os.path.join(CSRC, "ciera_tc_device.cuh")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -6,6 +6,8 @@ namespace ciera {
 namespace {
 
 constexpr int kAnyWarps = 4;
+// Rows a head up to which a call takes the form for few rows.
+constexpr int kFewRows = 16;
 
 // A warp per row (token and query head), a key at a time.  Bound by its
 // instructions: right for every layout, not fast.
@@ -44,15 +46,20 @@ int sm_count() {
 
 }  // namespace
 
-int64_t attend_workspace_bytes(int64_t, int64_t, int64_t) {
-  return (split_workspace_bytes(sm_count()) + 255) / 256 * 256;
+int64_t attend_workspace_bytes(int64_t, int64_t, int64_t head_dim) {
+  const int sms = sm_count();
+  int64_t most = split_workspace_bytes(sms);
+  if (head_dim <= 128 && wide_workspace_bytes(sms) > most) most = wide_workspace_bytes(sms);
+  return (most + 255) / 256 * 256;
 }
 
 int launch_attend(const AttendParams& given, void* stream) {
   AttendParams p = given;
-  p.wide_rows = 0x7FFFFFFF;
-  p.split_blocks = 2 * sm_count();
-  if (split_takes(p)) return launch_attend_split(p, stream);
+  int status = cudaSuccess;
+  p.blocks = sm_count();
+  if (p.longest * p.group > kFewRows && launch_attend_wide(p, stream, &status)) return status;
+  p.blocks *= 2;
+  if (launch_attend_split(p, stream, &status)) return status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = static_cast<int64_t>(p.tokens) * p.heads * p.group;
   k_attend_any<<<static_cast<unsigned>((rows + kAnyWarps - 1) / kAnyWarps), 32 * kAnyWarps, 0, s>>>(p);

@@ -144,8 +144,8 @@ __device__ __noinline__ void warp_attend(const AttendParams& p, const uint16_t* 
 
 // ------------------------------------------------------------------------
 // How a call's work is dealt out.  A tile is up to kRows rows (new tokens by
-// query heads of one head of keys, token by token); a unit is kKeys keys of a
-// tile, as many units as its last row sees, one if that sees none.  All units of
+// query heads of one head of keys, token by token); a unit is p.unit_keys
+// keys of a tile, as many units as its last row sees, one if that sees none.  All units of
 // all tiles, in order of request, head and tile, are cut into as many even
 // ranges as there are blocks, whatever the lengths are: ragged batches, one long
 // context and whole prompts fill the blocks alike.  A block that has a part of
@@ -159,14 +159,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
-// Requests of up to p.wide_rows rows a head, or those of more.
-template <bool kWide>
-__device__ __forceinline__ bool is_own(const AttendParams& p, const Request& r) {
-  const int32_t rows = r.tokens * p.group;
-  return r.tokens > 0 && (rows > p.wide_rows) == kWide;
-}
-
-template <int kRows, int kKeys>
+template <int kRows>
 struct Tiles {
   static __device__ __forceinline__ int32_t count(const AttendParams& p, const Request& r) {
     return (r.tokens * p.group + kRows - 1) / kRows;
@@ -223,14 +216,13 @@ __device__ __forceinline__ int64_t scan_block(int64_t v, int64_t* part, int64_t*
 }
 
 // Fills `share` for block `block` of `blocks`; all kThreads threads.
-template <bool kWide, int kRows, int kKeys, int kThreads>
+template <int kRows, int kThreads>
 __device__ void find_share(const AttendParams& p, int block, int blocks, int64_t* part,
                            Share* share) {
-  using T = Tiles<kRows, kKeys>;
+  using T = Tiles<kRows>;
   const auto units = [&](int32_t r) -> int64_t {
     if (r >= p.requests) return 0;
-    const Request q = request_of(p, r);
-    return is_own<kWide>(p, q) ? T::of_head(p, q) * p.heads : 0;
+    return T::of_head(p, request_of(p, r)) * p.heads;
   };
   int64_t own = 0, total;
   for (int32_t base = 0; base < p.requests; base += kThreads) own += units(base + threadIdx.x);
@@ -273,9 +265,9 @@ struct Segment {
   int64_t end;       // of the tile, in units of all
 };
 
-template <bool kWide, int kRows, int kKeys>
+template <int kRows>
 struct Walk {
-  using T = Tiles<kRows, kKeys>;
+  using T = Tiles<kRows>;
   Request request;
   int32_t index, head = 0, tile = 0, unit = 0, tiles = 0;
   int64_t at, end;
@@ -318,7 +310,7 @@ struct Walk {
           head = 0;
           while (at < end && ++index < p.requests) {
             request = request_of(p, index);
-            if (is_own<kWide>(p, request)) break;
+            if (request.tokens > 0) break;
           }
           if (index >= p.requests) end = at;
           tiles = T::count(p, request);

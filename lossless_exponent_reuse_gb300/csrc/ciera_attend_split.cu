@@ -144,8 +144,8 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
   Joint* joint = reinterpret_cast<Joint*>(p.workspace) + block;
   float* parts = reinterpret_cast<float*>(reinterpret_cast<Joint*>(p.workspace) + blocks);
 
-  find_share<false, F::kRows, kUnitKeys, kThreads>(p, block, blocks, sh.part, &sh.share);
-  Walk<false, F::kRows, kUnitKeys> walk(p, sh.share);
+  find_share<F::kRows, kThreads>(p, block, blocks, sh.part, &sh.share);
+  Walk<F::kRows> walk(p, sh.share);
   Segment seg;
   bool left_joint = false;
   const int size = kE4m3 ? 1 : 2;
@@ -511,7 +511,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
 template <int kDim, int kBlocks>
 __global__ void __launch_bounds__(kThreads) k_attend_join(const AttendParams p) {
   using F = Form<kDim, kBlocks, false>;
-  const int blocks = p.split_blocks, block = blockIdx.x;
+  const int blocks = p.blocks, block = blockIdx.x;
   const Joint j = reinterpret_cast<const Joint*>(p.workspace)[block];
   const float* parts =
       reinterpret_cast<const float*>(reinterpret_cast<const Joint*>(p.workspace) + blocks);
@@ -548,8 +548,8 @@ int launch_at(const AttendParams& p, cudaStream_t s) {
   using F = Form<kDim, kBlocks, kE4m3>;
   const cudaError_t err = allow_shared<k_attend_split<kDim, kBlocks, kE4m3>>(F::kSmem);
   if (err != cudaSuccess) return err;
-  k_attend_split<kDim, kBlocks, kE4m3><<<p.split_blocks, kThreads, F::kSmem, s>>>(p);
-  k_attend_join<kDim, kBlocks><<<p.split_blocks, kThreads, 0, s>>>(p);
+  k_attend_split<kDim, kBlocks, kE4m3><<<p.blocks, kThreads, F::kSmem, s>>>(p);
+  k_attend_join<kDim, kBlocks><<<p.blocks, kThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 
@@ -563,32 +563,36 @@ bool on_words(const Side& s, int size) {
          s.stride[1] * size % 16 == 0 && s.stride[2] * size % 16 == 0;
 }
 
-}  // namespace
-
 // Rows of whole 16-byte pieces.
 bool split_takes(const AttendParams& p) {
   const int size = p.e4m3 ? 1 : 2;
   return p.head_dim * size % 16 == 0 && on_words(p.key, size) && on_words(p.value, size);
 }
 
+}  // namespace
+
 int64_t split_workspace_bytes(int sms) {
   return 2 * static_cast<int64_t>(sms) * (sizeof(Joint) + 2 * 4 * kMostPartValues);
 }
 
-int launch_attend_split(const AttendParams& given, void* stream) {
+bool launch_attend_split(const AttendParams& given, void* stream, int* status) {
+  if (!split_takes(given)) return false;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   AttendParams p = given;
   p.unit_keys = kUnitKeys;
   // rows of a tile: as many as a request has at most, by eights
-  const int64_t rows = p.longest * p.group < p.wide_rows ? p.longest * p.group : p.wide_rows;
+  const int64_t rows = p.longest * p.group;
   if (p.head_dim <= 64)
-    return rows <= 8 ? launch_with<64, 1>(p, s)
-                     : rows <= 16 ? launch_with<64, 2>(p, s) : launch_with<64, 4>(p, s);
-  if (p.head_dim <= 128)
-    return rows <= 8 ? launch_with<128, 1>(p, s)
-                     : rows <= 16 ? launch_with<128, 2>(p, s) : launch_with<128, 4>(p, s);
-  p.split_blocks /= 2;  // one to an SM
-  return rows <= 8 ? launch_with<256, 1>(p, s) : launch_with<256, 2>(p, s);
+    *status = rows <= 8 ? launch_with<64, 1>(p, s)
+                        : rows <= 16 ? launch_with<64, 2>(p, s) : launch_with<64, 4>(p, s);
+  else if (p.head_dim <= 128)
+    *status = rows <= 8 ? launch_with<128, 1>(p, s)
+                        : rows <= 16 ? launch_with<128, 2>(p, s) : launch_with<128, 4>(p, s);
+  else {
+    p.blocks /= 2;  // one to an SM
+    *status = rows <= 8 ? launch_with<256, 1>(p, s) : launch_with<256, 2>(p, s);
+  }
+  return true;
 }
 
 }  // namespace ciera

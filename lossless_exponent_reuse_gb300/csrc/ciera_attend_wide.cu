@@ -1,0 +1,741 @@
+// ciera_attend_wide.cu -- attention of many rows a head over pages, on the
+// tensor cores (tcgen05).
+//
+// A persistent block per SM takes 256 rows, in two halves of 128, over units of up
+// to 128 keys.  One warp brings pages' keys and values into a ring of stages by TMA
+// (128-byte swizzle; a box is a page, or the largest part of it that a tile holds
+// in whole), one lane of another issues S = Q K^T and O += P V, and two groups of
+// four warps, one to a half, a thread to a row, turn scores into weights: S from
+// TMEM to registers, the running maximum and sum, and the weights in bf16 back to
+// TMEM, over the scores, from where the products take them as their A operand, so
+// that only keys, values and queries are read from shared memory.  O stays in TMEM;
+// it is scaled only where a row's maximum has passed the one in use by 2^8, and
+// then by the row's own thread.  While one half's weights are made, the other
+// half's products run: S0 S1 | O0 S0' O1 S1' | ...
+//
+// A tile's last keys may lie in a page with others behind them, which hold
+// anything: those values are cleared in shared memory before the products.  What a row
+// does not see inside a unit has weight 0; where it is infinite or NaN the row is
+// computed again, value by value.
+#include "ciera_attend_device.cuh"
+#include "ciera_tc_device.cuh"
+
+namespace ciera {
+namespace {
+
+constexpr int kHalf = 128;              // rows of a half: lanes of TMEM
+constexpr int kTileRows = 2 * kHalf;
+constexpr int kKeys = 128;              // most keys of a unit
+constexpr int kRowBytes = 128;          // of a stage's row: 64 values
+constexpr int kSoftmaxWarps = 8;
+constexpr int kMultiplyWarp = kSoftmaxWarps;
+constexpr int kLoadWarp = kSoftmaxWarps + 1;
+constexpr int kJointWarp = kSoftmaxWarps + 2;
+// Three groups of four warps, of 168 registers a thread at launch, 64512: 208 for
+// the two that hold a row's scores, 80 for the third, 63488.
+constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+constexpr float kSlack = 8.0f;
+constexpr uint64_t kLandNs = 100000000;  // limit for what is under way when a wait ran out
+constexpr int kMostStages = 8;
+constexpr int kTmemColumns = 512;       // S0 S1 O0 O1, 128 each
+constexpr int kJoinColumns = 16;        // of a block of the launch that joins
+
+template <int kDim>
+struct Form {
+  static constexpr int kHalves = kDim / 64;                       // columns of 64 values
+  static constexpr int kTileBytes = kHalves * kKeys * kRowBytes;  // a stage; half the queries
+  static constexpr int kStages = kDim == 128 ? 4 : 8;
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
+  static constexpr int kPartValues = kTileRows * (kDim + 2);
+};
+
+struct Shared {
+  uint64_t full[kMostStages];
+  uint64_t empty[kMostStages];
+  uint64_t queries[2];     // a half's queries are in shared memory
+  uint64_t scores[2];      // its scores are in TMEM
+  uint64_t weights[2];     // its weights are in TMEM, and its output as scaled
+  uint64_t output[2];      // its weights have gone into its output
+  uint64_t drain;          // after a wait that ran out: the products issued are done
+  uint32_t tmem;
+  uint32_t stop;           // a wait ran out: every role leaves
+  uint32_t busy;           // warps that compute rows again: nobody's wait runs out meanwhile
+  int32_t issued;          // loads
+  Share share;
+  int64_t part[kThreads / 32 + 1];
+};
+
+// Bounded wait of a whole warp; false, for all its lanes, when it ran out here
+// or anywhere in the block.
+__device__ __forceinline__ bool wait_on(const AttendParams& p, Shared& sh, uint64_t* bar,
+                                        uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  uint64_t t0 = globaltimer();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*reinterpret_cast<volatile uint32_t*>(&sh.stop)) return false;
+    const uint64_t now = globaltimer();
+    if (*reinterpret_cast<volatile uint32_t*>(&sh.busy)) t0 = now;
+    if (now - t0 > p.timeout_ns) {
+      *reinterpret_cast<volatile uint32_t*>(&sh.stop) = 1;
+      record_status(p.ctl, kStatusTimeout);
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait(const AttendParams& p, Shared& sh, uint64_t* bar,
+                                     uint32_t parity) {
+  return __all_sync(0xffffffffu, wait_on(p, sh, bar, parity));
+}
+
+__device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
+                                       int32_t z, int32_t u, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+      "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(u), "r"(smem_addr(bar))
+      : "memory");
+}
+
+// Both operands in shared memory.
+__device__ __forceinline__ void mma_shared(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                           uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// A in TMEM.
+__device__ __forceinline__ void mma_tmem(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+          smem_addr(bar))
+      : "memory");
+}
+
+// 32 columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_load32(uint32_t addr, float* f) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(f);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store32(uint32_t addr, const float* f) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(f);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+      "%29, %30, %31, %32};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+      "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]),
+      "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]),
+      "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+      "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Two sums or products at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)),
+        "l"(reinterpret_cast<uint64_t&>(c)));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(reinterpret_cast<uint64_t&>(d))
+      : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+  return d;
+}
+
+// What every role works out alike of a segment: each half's rows and units.
+struct Halves {
+  int32_t rows[2];
+  int32_t units[2];
+  int32_t most;
+  __device__ Halves(const AttendParams& p, const Segment& s) {
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const int32_t left = s.rows - t * kHalf;
+      rows[t] = left < 0 ? 0 : left < kHalf ? left : kHalf;
+      units[t] = 0;
+      if (rows[t] == 0) continue;
+      const int32_t last = s.tile * kTileRows + t * kHalf + rows[t] - 1;
+      const int32_t keys = seen_keys(s.request, p.group == 1 ? last : last / p.group);
+      const int32_t all = (keys + p.unit_keys - 1) / p.unit_keys;
+      const int32_t n = (all < s.to ? all : s.to) - s.from;
+      units[t] = n > 0 ? n : 0;
+    }
+    most = units[0] > units[1] ? units[0] : units[1];
+  }
+};
+
+struct Maps {
+  CUtensorMap key, value;
+  int32_t box;       // keys of a box, which divide a page's
+};
+
+// ------------------------------------------------------------------------
+// One warp: keys and values by TMA.  A lane per box: it looks up the page, a unit
+// ahead, and issues the box's loads.
+template <int kDim>
+__device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32_t ring) {
+  using F = Form<kDim>;
+  const int lane = threadIdx.x & 31;
+  const int columns = (p.head_dim + 63) / 64;
+  Walk<kTileRows> walk(p, sh.share);
+  Segment s;
+  int issued = 0;
+  bool alive = true;
+  while (alive && walk.next(p, &s)) {
+    const Halves halves(p, s);
+    const auto look = [&](int unit, int32_t* page, int32_t* place) {
+      const int32_t key = (s.from + unit) * p.unit_keys + lane * maps.box;
+      *page = p.pages;     // none: zeros
+      *place = 0;
+      if (unit >= halves.most || lane * maps.box >= p.unit_keys || key >= s.keys) return;
+      const int32_t at = key / p.page_size, found = page_at(p, s.index, at);
+      *place = key - at * p.page_size;
+      if (found >= 0) *page = found;
+    };
+    int32_t page, place;
+    look(0, &page, &place);
+    for (int u = 0; alive && u < halves.most; ++u) {
+      const int32_t left = s.keys - (s.from + u) * p.unit_keys;
+      const int32_t keys = left < p.unit_keys ? left : p.unit_keys;
+      const int boxes = (keys + maps.box - 1) / maps.box;
+      for (int side = 0; side < 2; ++side) {
+        const int stage = issued % F::kStages;
+        uint64_t* full = &sh.full[stage];
+        alive = wait(p, sh, &sh.empty[stage], ((issued / F::kStages) & 1) ^ 1);
+        if (!alive) break;
+        if (lane == 0)
+          mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * columns * maps.box * kRowBytes));
+        __syncwarp();
+        if (lane < boxes) {
+          const uint32_t to = ring + stage * F::kTileBytes + lane * maps.box * kRowBytes;
+          const CUtensorMap* map = side ? &maps.value : &maps.key;
+          for (int c = 0; c < columns; ++c)
+            tma_4d(to + c * kKeys * kRowBytes, map, c * 64, place, s.head, page, full);
+        }
+        ++issued;
+      }
+      look(u + 1, &page, &place);
+    }
+  }
+  // What is under way writes this block's shared memory: the products have read
+  // it, or after a wait that ran out it is seen to land (settle).
+  for (int i = issued > F::kStages ? issued - F::kStages : 0; alive && i < issued; ++i)
+    alive = wait(p, sh, &sh.empty[i % F::kStages], (i / F::kStages) & 1);
+  if (lane == 0) sh.issued = issued;
+}
+
+// ------------------------------------------------------------------------
+// One warp, of which a lane issues the products.
+template <int kDim>
+__device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, uint32_t ring,
+                         unsigned char* ring_ptr) {
+  using F = Form<kDim>;
+  const int lane = threadIdx.x & 31;
+  const bool leader = one_lane();
+  const int steps = (p.head_dim + 15) / 16;               // of S
+  const int key_steps = (p.unit_keys + 15) / 16;          // of O
+  const uint32_t scores = instruction(false, false, false, kHalf, kKeys);
+  const uint32_t output = instruction(false, false, true, kHalf, steps * 16);
+  const uint64_t a0 = operand(queries, 8 * kRowBytes, 0);
+  const uint64_t k0 = operand(ring, 8 * kRowBytes, 0);
+  const uint64_t v0 = operand(ring, 8 * kRowBytes, kKeys * kRowBytes);
+  constexpr uint32_t kTile = F::kTileBytes >> 4, kColumn = (kKeys * kRowBytes) >> 4;
+  const uint32_t tmem = sh.tmem;
+  Walk<kTileRows> walk(p, sh.share);
+  Segment s;
+  int taken = 0;                      // stages
+  uint32_t query_parity = 0, weight_parity = 0;   // a bit per half
+  while (walk.next(p, &s)) {
+    const Halves h(p, s);
+    const auto full = [&](int i) {
+      return wait(p, sh, &sh.full[i % F::kStages], (i / F::kStages) & 1);
+    };
+    const auto multiply_scores = [&](int t, int stage) {
+      const uint64_t a = a0 + t * kTile, b = k0 + stage * kTile;
+      if (leader) {
+        for (int i = 0; i < steps; ++i) {
+          const uint32_t at = (i >> 2) * kColumn + (i & 3) * 2;
+          mma_shared(tmem + t * kHalf, a + at, b + at, scores, i > 0);
+        }
+        commit(&sh.scores[t]);
+      }
+    };
+    if (h.most == 0) continue;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (h.units[t] > 0) {
+        if (!wait(p, sh, &sh.queries[t], query_parity >> t & 1)) return;
+        query_parity ^= 1u << t;
+      }
+    if (!full(taken)) return;
+    tc_fence_after();
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (h.units[t] > 0) multiply_scores(t, taken % F::kStages);
+    if (leader) commit(&sh.empty[taken % F::kStages]);
+    __syncwarp();
+    ++taken;
+    for (int u = 0; u < h.most; ++u) {
+      const int value = taken, next = taken + 1;       // this unit's values, the next one's keys
+      if (!full(value)) return;
+      const int32_t left = s.keys - (s.from + u) * p.unit_keys;
+      if (left < p.unit_keys) {
+        // what lies behind the last key, up to the unit's end
+        unsigned char* base = ring_ptr + (value % F::kStages) * F::kTileBytes;
+        const int words = (p.unit_keys - left) * (kRowBytes / 16);
+        for (int c = 0; c < F::kHalves; ++c)
+          for (int i = lane; i < words; i += 32)
+            *reinterpret_cast<uint4*>(base + (c * kKeys + left) * kRowBytes + i * 16) =
+                make_uint4(0, 0, 0, 0);
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      bool have = false;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        if (u < h.units[t]) {
+          if (!wait(p, sh, &sh.weights[t], weight_parity >> t & 1)) return;
+          weight_parity ^= 1u << t;
+          tc_fence_after();
+          if (leader) {
+            const uint64_t b = v0 + (value % F::kStages) * kTile;
+            for (int i = 0; i < key_steps; ++i)
+              mma_tmem(tmem + 2 * kHalf + t * kHalf, tmem + t * kHalf + i * 8,
+                       b + i * ((16 * kRowBytes) >> 4), output, u > 0 || i > 0);
+            commit(&sh.output[t]);
+          }
+        }
+        if (u + 1 < h.units[t]) {
+          if (!have && !full(next)) return;
+          have = true;
+          tc_fence_after();
+          multiply_scores(t, next % F::kStages);
+        }
+      }
+      if (leader) {
+        commit(&sh.empty[value % F::kStages]);
+        if (have) commit(&sh.empty[next % F::kStages]);
+      }
+      __syncwarp();
+      taken += have ? 2 : 1;
+    }
+  }
+}
+
+// ------------------------------------------------------------------------
+// Four warps, a thread a row.
+template <int kDim>
+__device__ void soften(const AttendParams& p, Shared& sh, unsigned char* queries_ptr, int t) {
+  using F = Form<kDim>;
+  const int lane = threadIdx.x & 31, tid = threadIdx.x & (kHalf - 1), warp = tid >> 5;
+  const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
+  const uint32_t score_at = sh.tmem + lanes + t * kHalf, out_at = score_at + 2 * kHalf;
+  const int block = blockIdx.x;
+  float* parts = reinterpret_cast<float*>(reinterpret_cast<Joint*>(p.workspace) + gridDim.x);
+  unsigned char* queries = queries_ptr + t * F::kTileBytes;
+  // a negative scale: of the queries' opposites
+  const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
+  const float scale = fabsf(p.scale) * kLog2e;
+  const int words = p.head_dim / 8;
+  Walk<kTileRows> walk(p, sh.share);
+  Segment s;
+  uint32_t done = 0;        // units of this half so far
+  while (walk.next(p, &s)) {
+    const Halves h(p, s);
+    const int32_t row0 = s.tile * kTileRows + t * kHalf, rows = t ? h.rows[1] : h.rows[0];
+    const int32_t units = t ? h.units[1] : h.units[0];
+    float top = minus_infinity(), sum = 0.0f;
+    int32_t seen = 0;
+    if (tid < rows) seen = seen_keys(s.request, p.group == 1 ? row0 + tid : (row0 + tid) / p.group);
+    if (units > 0) {
+      // ---- queries, eight lanes a row of 64 values
+      constexpr int kPieces = kDim / 8;
+#pragma unroll 4
+      for (int i = 0; i < kPieces; ++i) {
+        const int at = i * kHalf + tid, r = at / kPieces, piece = at % kPieces;
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (r < rows && piece < words)
+          w = *reinterpret_cast<const uint4*>(query_row(p, s.request.first, s.head, row0 + r) +
+                                              piece * 8);
+        w.x ^= flip;
+        w.y ^= flip;
+        w.z ^= flip;
+        w.w ^= flip;
+        *reinterpret_cast<uint4*>(queries + (piece / 8) * kKeys * kRowBytes + r * kRowBytes +
+                                  (((piece & 7) ^ (r & 7)) << 4)) = w;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&sh.queries[t]);
+    }
+    for (int u = 0; u < units; ++u) {
+      if (!wait(p, sh, &sh.scores[t], done & 1)) return;
+      tc_fence_after();
+      float v[kKeys];
+#pragma unroll
+      for (int c = 0; c < kKeys; c += 32) tmem_load32(score_at + c, v + c);
+      tmem_ld_wait();
+      const int32_t key0 = (s.from + u) * p.unit_keys;
+      int32_t valid = seen - key0;
+      valid = valid < p.unit_keys ? valid : p.unit_keys;
+      if (valid < kKeys) {
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c)
+          if (c >= valid) v[c] = minus_infinity();
+      }
+      float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+      for (int c = 4; c < kKeys; c += 8)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          m[i] = c + 4 + i < kKeys ? fmaxf(m[i], fmaxf(v[c + i], v[c + 4 + i])) : fmaxf(m[i], v[c + i]);
+      const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * scale;
+      if (__any_sync(0xffffffffu, most > top + kSlack)) {
+        const float now = fmaxf(top, most);
+        const float by = now == minus_infinity() ? 1.0f : exp2_fast(top - now);
+        top = now;
+        sum *= by;
+        if (u > 0) {
+          if (!wait(p, sh, &sh.output[t], (done - 1) & 1)) return;
+          tc_fence_after();
+#pragma unroll 1
+          for (int c = 0; c < p.head_dim; c += 32) {
+            float o[32];
+            tmem_load32(out_at + c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] *= by;
+            tmem_store32(out_at + c, o);
+          }
+        }
+      }
+      const float base = top == minus_infinity() ? 0.0f : -top;
+      const float2 scale2 = make_float2(scale, scale), base2 = make_float2(base, base);
+      float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+      for (int c = 0; c < kKeys; c += 32) {
+        uint32_t w[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          float2 x = fma2(make_float2(v[c + 2 * i], v[c + 2 * i + 1]), scale2, base2);
+          x.x = exp2_fast(x.x);
+          x.y = exp2_fast(x.y);
+          sums[i & 1] = add2(sums[i & 1], x);
+          w[i] = pack_bf16(x.x, x.y);
+        }
+        tmem_store16(score_at + c / 2, w);
+      }
+      sum += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+      tmem_store_wait();
+      tc_fence_before();
+      mbar_arrive(&sh.weights[t]);
+      ++done;
+    }
+    if (units > 0) {
+      if (!wait(p, sh, &sh.output[t], (done - 1) & 1)) return;
+      tc_fence_after();
+    }
+    // ---- output, or this block's part of it
+    const bool whole = s.from == 0 && s.to == s.all;
+    float* part = parts + (2 * block + (s.from == 0)) * static_cast<int64_t>(F::kPartValues) +
+                  t * kHalf + tid;
+    const bool live = tid < rows;
+    uint16_t* out = live ? output_row(p, s.request.first, s.head, row0 + tid) : nullptr;
+    const float by = inverse_sum(sum);
+    bool odd = !(fabsf(sum) < __uint_as_float(0x7F800000u));
+    if (!whole && live) {
+      part[0] = top;
+      part[kTileRows] = sum;
+    }
+#pragma unroll 1
+    for (int c = 0; c < p.head_dim; c += 32) {
+      float o[32];
+      if (units > 0) {
+        tmem_load32(out_at + c, o);
+        tmem_ld_wait();
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
+      }
+      float size = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (c + i < p.head_dim) size += fabsf(o[i]);
+      odd |= !(size < __uint_as_float(0x7F800000u));
+      if (!live) continue;
+      if (whole) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 8)
+          if (c + i < p.head_dim) {
+            const float f[8] = {o[i] * by,     o[i + 1] * by, o[i + 2] * by, o[i + 3] * by,
+                                o[i + 4] * by, o[i + 5] * by, o[i + 6] * by, o[i + 7] * by};
+            *reinterpret_cast<uint4*>(out + c + i) = pack8(f);
+          }
+      } else if (units > 0) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+          if (c + i < p.head_dim) part[(2 + c + i) * kTileRows] = o[i];
+      }
+    }
+    tc_fence_before();
+    // ---- rows that something out of sight may have spoilt, a warp a row
+    const uint32_t spoilt = __ballot_sync(0xffffffffu, odd && live && units > 0);
+    if (spoilt && lane == 0) atomicAdd(&sh.busy, 1u);
+    for (uint32_t again = spoilt; again; again &= again - 1) {
+      const int who = __ffs(again) - 1;
+      const int32_t row = row0 + warp * 32 + who;
+      const int32_t to = min(__shfl_sync(0xffffffffu, seen, who), s.to * p.unit_keys);
+      Slice own;
+      warp_attend(p, query_row(p, s.request.first, s.head, row), s.index, s.head,
+                  s.from * p.unit_keys, to, &own);
+      float* its = part - lane + who;
+      uint16_t* there = output_row(p, s.request.first, s.head, row);
+      for (int i = 0; i < kDim / 32; ++i) {
+        const int d = lane + 32 * i;
+        if (d >= p.head_dim) continue;
+        if (whole)
+          there[d] = f32_to_bf16(own.o[i] * inverse_sum(own.sum));
+        else
+          its[(2 + d) * kTileRows] = own.o[i];
+      }
+      if (!whole && lane == 0) {
+        its[0] = own.most;
+        its[kTileRows] = own.sum;
+      }
+      __syncwarp();
+    }
+    if (spoilt && lane == 0) atomicSub(&sh.busy, 1u);
+  }
+}
+
+// One lane: what the launch that joins has to know of the block's last tile.
+__device__ void announce(const AttendParams& p, const Shared& sh) {
+  Walk<kTileRows> walk(p, sh.share);
+  Segment s{};
+  bool goes_on = false;
+  while (walk.next(p, &s)) goes_on = s.from == 0 && s.to < s.all;
+  leave_joint(reinterpret_cast<Joint*>(p.workspace) + blockIdx.x, goes_on ? &s : nullptr, sh.share,
+              s.tile * kTileRows, blockIdx.x);
+}
+
+template <int kDim>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attend_wide(const AttendParams p, const __grid_constant__ Maps maps) {
+  using F = Form<kDim>;
+  extern __shared__ unsigned char raw[];
+  __shared__ Shared sh;
+  const uint32_t base = smem_addr(raw);
+  const uint32_t queries = (base + 1023) & ~1023u, ring = queries + 2 * F::kTileBytes;
+  unsigned char* queries_ptr = raw + (queries - base);
+  unsigned char* ring_ptr = queries_ptr + 2 * F::kTileBytes;
+  const int warp = threadIdx.x >> 5, blocks = gridDim.x, block = blockIdx.x;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < F::kStages; ++i) {
+      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.queries[t], kHalf);
+      mbar_init(&sh.scores[t], 1);
+      mbar_init(&sh.weights[t], kHalf);
+      mbar_init(&sh.output[t], 1);
+    }
+    mbar_init(&sh.drain, 1);
+    sh.stop = sh.busy = 0;
+    sh.issued = 0;
+    fence_barrier_init();
+  }
+  if (warp == kMultiplyWarp) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_addr(&sh.tmem)),
+                 "r"(kTmemColumns)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  // rows of a stage that no load fills
+  for (int i = threadIdx.x; i < F::kStages * F::kTileBytes / 16; i += kThreads)
+    reinterpret_cast<uint4*>(ring_ptr)[i] = make_uint4(0, 0, 0, 0);
+  fence_proxy_async_smem();
+  find_share<kTileRows, kThreads>(p, block, blocks, sh.part, &sh.share);
+  __syncthreads();
+  tc_fence_after();
+  if (warp < kSoftmaxWarps) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    soften<kDim>(p, sh, queries_ptr, warp / 4);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == kLoadWarp)
+      load<kDim>(p, maps, sh, ring);
+    else if (warp == kMultiplyWarp)
+      multiply<kDim>(p, sh, queries, ring, ring_ptr);
+    else if (warp == kJointWarp && one_lane())
+      announce(p, sh);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (sh.stop) {
+    // a wait ran out: the products issued are seen to end, the loads to land
+    if (warp == kMultiplyWarp && one_lane()) {
+      commit(&sh.drain);
+      mbar_wait_bounded(&sh.drain, 0, kLandNs);
+    } else if (warp == kLoadWarp) {
+      for (int i = sh.issued > F::kStages ? sh.issued - F::kStages : 0; i < sh.issued; ++i)
+        if (!mbar_wait_bounded(&sh.full[i % F::kStages], (i / F::kStages) & 1, kLandNs)) break;
+    }
+    __syncthreads();
+  }
+  tc_fence_after();
+  if (warp == kMultiplyWarp)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(sh.tmem),
+                 "r"(kTmemColumns)
+                 : "memory");
+}
+
+// Joins a tile's parts, a thread a row, kJoinColumns of its values; rows behind
+// the last request become zeros.
+template <int kDim>
+__global__ void __launch_bounds__(kTileRows) k_attend_wide_join(const AttendParams p) {
+  using F = Form<kDim>;
+  const int blocks = gridDim.x, block = blockIdx.x, row = threadIdx.x;
+  const int c0 = blockIdx.y * kJoinColumns;
+  const Joint j = reinterpret_cast<const Joint*>(p.workspace)[block];
+  const float* parts =
+      reinterpret_cast<const float*>(reinterpret_cast<const Joint*>(p.workspace) + blocks);
+  if (row < j.rows && j.parts > 0) {
+    float m = minus_infinity(), l = 0.0f, v[kJoinColumns] = {};
+    for (int i = 0; i < j.parts; ++i) {
+      const float* from =
+          parts + (2 * (block + i) + (i == 0)) * static_cast<int64_t>(F::kPartValues) + row;
+      const float top = from[0];
+      if (top == minus_infinity()) continue;   // none of its keys seen, and no sums left
+      const float most = fmaxf(m, top);
+      const float old = exp2_fast(m - most), by = exp2_fast(top - most);
+      l = l * old + from[kTileRows] * by;
+#pragma unroll
+      for (int c = 0; c < kJoinColumns; ++c)
+        if (c0 + c < p.head_dim) v[c] = v[c] * old + from[(2 + c0 + c) * kTileRows] * by;
+      m = most;
+    }
+    const float by = inverse_sum(l);
+    uint16_t* out = output_row(p, j.first, j.head, j.row + row) + c0;
+#pragma unroll
+    for (int c = 0; c < kJoinColumns; c += 8)
+      if (c0 + c < p.head_dim) {
+        const float f[8] = {v[c] * by,     v[c + 1] * by, v[c + 2] * by, v[c + 3] * by,
+                            v[c + 4] * by, v[c + 5] * by, v[c + 6] * by, v[c + 7] * by};
+        *reinterpret_cast<uint4*>(out + c) = pack8(f);
+      }
+  }
+  if (blockIdx.y) return;
+  const int64_t width = static_cast<int64_t>(p.heads) * p.group * p.head_dim;
+  const int64_t behind = p.requests ? clamp_to(p.offsets[p.requests], p.tokens) : 0;
+  for (int64_t at = behind * width + block * kTileRows + row; at < p.tokens * width;
+       at += static_cast<int64_t>(blocks) * kTileRows)
+    p.o[at] = 0;
+}
+
+// ------------------------------------------------------------------------
+// Host
+
+bool make_map(CUtensorMap* map, const Side& s, const AttendParams& p, int box) {
+  const int64_t n[3] = {p.page_size, p.heads, p.pages};
+  const int64_t at[3] = {s.stride[1], s.stride[2], s.stride[0]};
+  cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.head_dim)}, strides[3];
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = static_cast<cuuint64_t>(n[i]);
+    // (of one: any)
+    strides[i] = static_cast<cuuint64_t>(n[i] > 1 && at[i] > 0 ? 2 * at[i] : 16);
+    if (n[i] > 1 && at[i] <= 0) return false;
+  }
+  const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, ones[4] = {1, 1, 1, 1};
+  return encode()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, s.data, dims, strides, boxes, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool on_words(const Side& s) {
+  return (reinterpret_cast<uintptr_t>(s.data) & 15) == 0 && s.stride[0] % 8 == 0 &&
+         s.stride[1] % 8 == 0 && s.stride[2] % 8 == 0;
+}
+
+template <int kDim>
+int launch_at(const AttendParams& p, const Maps& maps, cudaStream_t s) {
+  using F = Form<kDim>;
+  const cudaError_t err = allow_shared<k_attend_wide<kDim>>(F::kSmem);
+  if (err != cudaSuccess) return err;
+  k_attend_wide<kDim><<<p.blocks, kThreads, F::kSmem, s>>>(p, maps);
+  const dim3 grid(static_cast<unsigned>(p.blocks),
+                  static_cast<unsigned>((p.head_dim + kJoinColumns - 1) / kJoinColumns));
+  k_attend_wide_join<kDim><<<grid, kTileRows, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+// bf16 pages of whole eights of keys, whose rows are 16-byte words, as queries
+// and outputs are.
+bool wide_takes(const AttendParams& p) {
+  return !p.e4m3 && p.head_dim <= 128 && p.head_dim % 8 == 0 && p.page_size % 8 == 0 &&
+         p.pages > 0 && p.scale != 0.0f && on_words(p.key) && on_words(p.value) &&
+         (reinterpret_cast<uintptr_t>(p.q) & 15) == 0 && p.q_token % 8 == 0 && p.q_head % 8 == 0 &&
+         (reinterpret_cast<uintptr_t>(p.o) & 15) == 0 && encode();
+}
+
+}  // namespace
+
+int64_t wide_workspace_bytes(int sms) {
+  return static_cast<int64_t>(sms) * (sizeof(Joint) + 2 * 4 * Form<128>::kPartValues);
+}
+
+bool launch_attend_wide(const AttendParams& given, void* stream, int* status) {
+  if (!wide_takes(given)) return false;
+  AttendParams p = given;
+  Maps maps;
+  // keys of a box: the most, by eights, that divide a page and fit a unit
+  maps.box = kKeys;
+  while (p.page_size % maps.box) maps.box -= 8;
+  p.unit_keys = kKeys / maps.box * maps.box;
+  if (!make_map(&maps.key, p.key, p, maps.box) || !make_map(&maps.value, p.value, p, maps.box))
+    return false;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  *status = p.head_dim <= 64 ? launch_at<64>(p, maps, s) : launch_at<128>(p, maps, s);
+  return true;
+}
+
+}  // namespace ciera

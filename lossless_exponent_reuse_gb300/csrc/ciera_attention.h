@@ -91,9 +91,8 @@ struct AttendParams {
   int32_t e4m3;
   float scale;
   int64_t longest;
-  int32_t wide_rows;              // most rows a head of the form for few rows
   int32_t unit_keys;              // keys of a unit of work
-  int32_t split_blocks, wide_blocks;  // of the two forms; 0: not launched
+  int32_t blocks;                 // that share the work
   void* workspace;
   Control* ctl;
   uint64_t timeout_ns;
@@ -105,10 +104,12 @@ int launch_assign_pages(const PagesParams& p, void* stream);
 int launch_release_pages(const PagesParams& p, void* stream);
 int launch_attend(const AttendParams& p, void* stream);
 int64_t attend_workspace_bytes(int64_t q_heads, int64_t heads, int64_t head_dim);
-// Attention in units of a few rows by few keys (mma.sync): its launch, the bytes
-// of workspace of its blocks, and the launch that joins parted tiles.
-bool split_takes(const AttendParams& p);
-int launch_attend_split(const AttendParams& p, void* stream);
+// Attention in tiles of few rows (mma.sync), and of up to 256 (tcgen05), with
+// p.blocks twice, or once, the SMs; false where a call's layout is not one that
+// they take.  And the bytes of workspace of so many blocks.
+bool launch_attend_split(const AttendParams& p, void* stream, int* status);
 int64_t split_workspace_bytes(int sms);
+bool launch_attend_wide(const AttendParams& p, void* stream, int* status);
+int64_t wide_workspace_bytes(int sms);
 
 }  // namespace ciera

@@ -30,10 +30,9 @@
 // ends and 537 MB of results); e4m3 235 us with the gather.  With small groups bound
 // by the weights' bytes: 24 tokens of the fine-grained layer in e4m3, 141 and 80
 // us for gate and up and for down, 6.7 TB/s.
-#include <cuda.h>
-
 #include "ciera_device.cuh"
 #include "ciera_moe_device.cuh"
+#include "ciera_tc_device.cuh"
 
 namespace ciera {
 namespace {
@@ -163,10 +162,6 @@ __device__ __forceinline__ void copy4(uint32_t dst, const void* src, int bytes) 
 }
 __device__ __forceinline__ void copy_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
 // kPair: blocks of one product (1, or 2 neighbours of a cluster, whose tensor
 // cores take the two halves of its features and share its rows).
 template <bool kE4m3, int kPair>
@@ -257,16 +252,6 @@ __device__ __forceinline__ void tmem_ld(uint32_t addr, float (&v)[8]) {
       : "memory");
 }
 
-__device__ __forceinline__ void tmem_ld_wait() {
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_before() {
-  asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
-}
-__device__ __forceinline__ void tc_fence_after() {
-  asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-}
-
 // Four 8 x 8 matrices of 16-bit values, transposed on their way: lane l holds, of
 // matrix m, elements (l / 4, 2 (l % 4)) and the next in v[m]; in shared memory
 // lane 8 m + i points at what is row i there and was column i here.
@@ -298,32 +283,6 @@ __device__ __forceinline__ void store_shared(uint32_t addr, const uint4& v) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y),
                "r"(v.z), "r"(v.w)
                : "memory");
-}
-
-// One lane of a warp, the same for every call; the compiler then knows that
-// what it issues is issued once.
-__device__ __forceinline__ bool one_lane() {
-  uint32_t one;
-  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}"
-               : "=r"(one));
-  return one != 0;
-}
-
-// Shared-memory operand: 128-byte swizzle; `stride` bytes between groups of
-// eight rows, `lead` between 128-byte columns (operands with the contraction
-// along the rows only).
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t stride, uint32_t lead) {
-  return static_cast<uint64_t>((addr & 0x3FFFF) >> 4) | static_cast<uint64_t>(lead >> 4) << 16 |
-         static_cast<uint64_t>(stride >> 4) << 32 | uint64_t(1) << 46 | uint64_t(2) << 61;
-}
-
-// Instruction descriptor: 32-bit float sums, operand types, which operands
-// have the contraction along their rows, N and M.
-__device__ __forceinline__ uint32_t instruction(bool e4m3, bool a_rows, bool b_rows, int m,
-                                                int n) {
-  const uint32_t type = e4m3 ? 0u : 1u;
-  return 1u << 4 | type << 7 | type << 10 | (a_rows ? 1u << 15 : 0u) | (b_rows ? 1u << 16 : 0u) |
-         static_cast<uint32_t>(n >> 3) << 17 | static_cast<uint32_t>(m >> 4) << 24;
 }
 
 // ------------------------------------------------------------------------
@@ -1284,21 +1243,6 @@ __global__ void __launch_bounds__(Roles<kPair>::kThreads, 1)
 
 // ------------------------------------------------------------------------
 // Host
-
-using Encode = decltype(&cuTensorMapEncodeTiled);
-
-Encode encode() {
-  static const Encode fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult found;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault,
-                                         &found) != cudaSuccess ||
-        found != cudaDriverEntryPointSuccess)
-      f = nullptr;
-    return reinterpret_cast<Encode>(f);
-  }();
-  return fn;
-}
 
 // A map of matrices of rows x columns, `planes` of them (0: one, without the
 // dimension); boxes of 128 bytes by box_rows.  With part_stride a box is eight
