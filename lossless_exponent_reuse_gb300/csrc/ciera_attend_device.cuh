@@ -91,7 +91,7 @@ __device__ __noinline__ void warp_attend(const AttendParams& p, const uint16_t* 
   const float scale = p.scale * kLog2e;
   int32_t page = -1, index = -1;
   for (int32_t key = from; key < to; ++key) {
-    const int32_t at = key / p.page_size;
+    const int32_t at = p.by_page(key);
     if (at != index) {
       index = at;
       page = page_at(p, request, at);
@@ -169,12 +169,12 @@ struct Tiles {
                                                  int32_t tile) {
     const int32_t left = r.tokens * p.group - tile * kRows;
     const int32_t last = tile * kRows + (left < kRows ? left : kRows) - 1;
-    return seen_keys(r, p.group == 1 ? last : last / p.group);
+    return seen_keys(r, p.by_group(last));
   }
   static __device__ __forceinline__ int32_t units(const AttendParams& p, const Request& r,
                                                   int32_t tile) {
-    const int32_t n = (keys(p, r, tile) + p.unit_keys - 1) / p.unit_keys;
-    return n > 0 ? n : 1;
+    const int32_t n = keys(p, r, tile);
+    return n > 0 ? p.by_unit.up(n) : 1;
   }
   static __device__ int64_t of_head(const AttendParams& p, const Request& r) {
     const int32_t n = count(p, r);
@@ -350,13 +350,13 @@ __device__ __forceinline__ void leave_joint(Joint* joint, const Segment* s, cons
 // Query and output of a row: row `row` of a head's rows of a request.
 __device__ __forceinline__ const uint16_t* query_row(const AttendParams& p, int32_t first,
                                                      int32_t head, int32_t row) {
-  const int32_t i = p.group == 1 ? row : row / p.group;
+  const int32_t i = p.by_group(row);
   return p.q + (static_cast<int64_t>(first) + i) * p.q_token +
          (head * p.group + row - i * p.group) * p.q_head;
 }
 __device__ __forceinline__ uint16_t* output_row(const AttendParams& p, int32_t first, int32_t head,
                                                 int32_t row) {
-  const int32_t i = p.group == 1 ? row : row / p.group;
+  const int32_t i = p.by_group(row);
   return p.o + ((static_cast<int64_t>(first) + i) * (p.heads * p.group) + head * p.group + row -
                 i * p.group) *
                    p.head_dim;

@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
       }
       if (lane == 0) {
         sh.query_scale[r] = scale;
-        sh.seen[r] = live ? seen_keys(seg.request, (row0 + r) / p.group) : 0;
+        sh.seen[r] = live ? seen_keys(seg.request, p.by_group(row0 + r)) : 0;
       }
     }
     __syncthreads();
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
     const auto locate = [&](int unit) -> int64_t {
       const int32_t key = key0 + unit * kUnitKeys + (lane & 15);
       if (unit >= units || key >= seg.keys) return -1;
-      const int32_t at = key / p.page_size, page = page_at(p, seg.index, at);
+      const int32_t at = p.by_page(key), page = page_at(p, seg.index, at);
       if (page < 0) return -1;
       const int32_t place = key - at * p.page_size;
       return lane < 16 ? page * p.key.stride[0] + place * p.key.stride[1] + head_k
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
     const auto exponent_of = [&](int unit) -> uint32_t {
       const int32_t key = key0 + unit * kUnitKeys + (lane & 15);
       if (unit >= units || key >= seg.keys) return kExponentBias;
-      const int32_t at = key / p.page_size, page = page_at(p, seg.index, at);
+      const int32_t at = p.by_page(key), page = page_at(p, seg.index, at);
       if (page < 0) return kExponentBias;
       const int32_t place = key - at * p.page_size;
       const Side& s = lane < 16 ? p.key : p.value;
@@ -580,6 +580,7 @@ bool launch_attend_split(const AttendParams& given, void* stream, int* status) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   AttendParams p = given;
   p.unit_keys = kUnitKeys;
+  p.by_unit = Divide(kUnitKeys);
   // rows of a tile: as many as a request has at most, by eights
   const int64_t rows = p.longest * p.group;
   if (p.head_dim <= 64)

@@ -26,13 +26,14 @@ namespace {
 constexpr int kHalf = 128;              // rows of a half: lanes of TMEM
 constexpr int kTileRows = 2 * kHalf;
 constexpr int kKeys = 128;              // most keys of a unit
+constexpr int kStep = 64;               // keys whose weights are handed on at once
 constexpr int kRowBytes = 128;          // of a stage's row: 64 values
 constexpr int kSoftmaxWarps = 8;
 constexpr int kMultiplyWarp = kSoftmaxWarps;
 constexpr int kLoadWarp = kSoftmaxWarps + 1;
-constexpr int kJointWarp = kSoftmaxWarps + 2;
-// Three groups of four warps, of 168 registers a thread at launch, 64512: 208 for
-// the two that hold a row's scores, 80 for the third, 63488.
+constexpr int kQueryWarp = kSoftmaxWarps + 2;   // and the next, one to a half
+// Three groups of four warps, of 168 registers a thread at launch, 64512: 200 for
+// the two that hold a row's scores, 104 for the third, 64512.
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
 constexpr float kSlack = 8.0f;
 constexpr uint64_t kLandNs = 100000000;  // limit for what is under way when a wait ran out
@@ -44,7 +45,7 @@ template <int kDim>
 struct Form {
   static constexpr int kHalves = kDim / 64;                       // columns of 64 values
   static constexpr int kTileBytes = kHalves * kKeys * kRowBytes;  // a stage; half the queries
-  static constexpr int kStages = kDim == 128 ? 4 : 8;
+  static constexpr int kStages = kDim == 128 ? 5 : 8;
   static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
   static constexpr int kPartValues = kTileRows * (kDim + 2);
 };
@@ -53,9 +54,11 @@ struct Shared {
   uint64_t full[kMostStages];
   uint64_t empty[kMostStages];
   uint64_t queries[2];     // a half's queries are in shared memory
+  uint64_t asked[2];       // and have been read for the last time
   uint64_t scores[2];      // its scores are in TMEM
-  uint64_t weights[2];     // its weights are in TMEM, and its output as scaled
-  uint64_t output[2];      // its weights have gone into its output
+  uint64_t weights[2][2];  // a step's weights are in TMEM, and the output as scaled
+  uint64_t output[2][2];   // a step's weights have gone into the output
+  uint64_t cleared;        // a tile's last values have zeros behind the last key
   uint64_t drain;          // after a wait that ran out: the products issued are done
   uint32_t tmem;
   uint32_t stop;           // a wait ran out: every role leaves
@@ -66,12 +69,17 @@ struct Shared {
 };
 
 // Bounded wait of a whole warp; false, for all its lanes, when it ran out here
-// or anywhere in the block.
+// or anywhere in the block.  The clock is looked at between rounds of tries alone
+// (each try, and the others' polling, took from the softmax: 2.0 us a unit).
 __device__ __forceinline__ bool wait_on(const AttendParams& p, Shared& sh, uint64_t* bar,
                                         uint32_t parity) {
-  if (mbar_try_wait(bar, parity)) return true;
+  constexpr int kTries = 64;
+  for (int i = 0; i < kTries; ++i)
+    if (mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = globaltimer();
-  while (!mbar_try_wait(bar, parity)) {
+  for (;;) {
+    for (int i = 0; i < kTries; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
     if (*reinterpret_cast<volatile uint32_t*>(&sh.stop)) return false;
     const uint64_t now = globaltimer();
     if (*reinterpret_cast<volatile uint32_t*>(&sh.busy)) t0 = now;
@@ -81,7 +89,6 @@ __device__ __forceinline__ bool wait_on(const AttendParams& p, Shared& sh, uint6
       return false;
     }
   }
-  return true;
 }
 __device__ __forceinline__ bool wait(const AttendParams& p, Shared& sh, uint64_t* bar,
                                      uint32_t parity) {
@@ -150,16 +157,40 @@ __device__ __forceinline__ void tmem_store32(uint32_t addr, const float* f) {
       "r"(r[30]), "r"(r[31])
       : "memory");
 }
-__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-      "%11, %12, %13, %14, %15, %16};" ::"r"(addr),
-      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
-      : "memory");
-}
 __device__ __forceinline__ void tmem_store_wait() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// Waits for the loads from TMEM; what they brought is not looked at before.
+template <int kCount>
+__device__ __forceinline__ void tmem_arrived(float* f) {
+  tmem_ld_wait();
+#pragma unroll
+  for (int i = 0; i < kCount; i += 8)
+    asm volatile(""
+                 : "+f"(f[i]), "+f"(f[i + 1]), "+f"(f[i + 2]), "+f"(f[i + 3]), "+f"(f[i + 4]),
+                   "+f"(f[i + 5]), "+f"(f[i + 6]), "+f"(f[i + 7]));
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// 16 values as bf16, 32 bytes at once or twice 16.
+__device__ __forceinline__ void store16(uint16_t* to, const float* f, float by, bool at_once) {
+  uint32_t w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = pack_bf16(f[2 * i] * by, f[2 * i + 1] * by);
+  if (at_once) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(to), "r"(w[0]),
+                 "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4*>(to + 8) = make_uint4(w[4], w[5], w[6], w[7]);
+  }
 }
 
 // Two sums or products at once.
@@ -192,8 +223,7 @@ struct Halves {
       units[t] = 0;
       if (rows[t] == 0) continue;
       const int32_t last = s.tile * kTileRows + t * kHalf + rows[t] - 1;
-      const int32_t keys = seen_keys(s.request, p.group == 1 ? last : last / p.group);
-      const int32_t all = (keys + p.unit_keys - 1) / p.unit_keys;
+      const int32_t all = p.by_unit.up(seen_keys(s.request, p.by_group(last)));
       const int32_t n = (all < s.to ? all : s.to) - s.from;
       units[t] = n > 0 ? n : 0;
     }
@@ -204,6 +234,7 @@ struct Halves {
 struct Maps {
   CUtensorMap key, value;
   int32_t box;       // keys of a box, which divide a page's
+  Divide by_box;
 };
 
 // ------------------------------------------------------------------------
@@ -225,7 +256,7 @@ __device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32
       *page = p.pages;     // none: zeros
       *place = 0;
       if (unit >= halves.most || lane * maps.box >= p.unit_keys || key >= s.keys) return;
-      const int32_t at = key / p.page_size, found = page_at(p, s.index, at);
+      const int32_t at = p.by_page(key), found = page_at(p, s.index, at);
       *place = key - at * p.page_size;
       if (found >= 0) *page = found;
     };
@@ -234,7 +265,7 @@ __device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32
     for (int u = 0; alive && u < halves.most; ++u) {
       const int32_t left = s.keys - (s.from + u) * p.unit_keys;
       const int32_t keys = left < p.unit_keys ? left : p.unit_keys;
-      const int boxes = (keys + maps.box - 1) / maps.box;
+      const int boxes = maps.by_box.up(keys);
       for (int side = 0; side < 2; ++side) {
         const int stage = issued % F::kStages;
         uint64_t* full = &sh.full[stage];
@@ -262,13 +293,15 @@ __device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32
 }
 
 // ------------------------------------------------------------------------
-// One warp, of which a lane issues the products.
+// One lane issues the products.  Everything that it does between two of them
+// counts (65 cycles a product): the loops are unrolled, the operands' addresses
+// differ by constants, and what has long been there is waited for ahead.
+// (Loops with the whole warp: 85 to 120 cycles a product, 230 a wait.)
 template <int kDim>
-__device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, uint32_t ring,
-                         unsigned char* ring_ptr) {
+__device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, uint32_t ring) {
   using F = Form<kDim>;
-  const int lane = threadIdx.x & 31;
-  const bool leader = one_lane();
+  if (!one_lane()) return;
+  constexpr int kSteps = kDim / 16;
   const int steps = (p.head_dim + 15) / 16;               // of S
   const int key_steps = (p.unit_keys + 15) / 16;          // of O
   const uint32_t scores = instruction(false, false, false, kHalf, kKeys);
@@ -281,99 +314,165 @@ __device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, ui
   Walk<kTileRows> walk(p, sh.share);
   Segment s;
   int taken = 0;                      // stages
-  uint32_t query_parity = 0, weight_parity = 0;   // a bit per half
+  uint32_t query_parity = 0, weight_parity = 0, clear_parity = 0;   // (a bit per half)
+  const auto full = [&](int i) {
+    return wait_on(p, sh, &sh.full[i % F::kStages], (i / F::kStages) & 1);
+  };
+  const auto multiply_scores = [&](int t, int stage, bool last) {
+    const uint64_t a = a0 + t * kTile, b = k0 + stage * kTile;
+#pragma unroll
+    for (int i = 0; i < kSteps; ++i) {
+      const uint32_t at = (i >> 2) * kColumn + (i & 3) * 2;
+      if (i < steps) mma_shared(tmem + t * kHalf, a + at, b + at, scores, i > 0);
+    }
+    commit(&sh.scores[t]);
+    if (last) commit(&sh.asked[t]);
+  };
   while (walk.next(p, &s)) {
     const Halves h(p, s);
-    const auto full = [&](int i) {
-      return wait(p, sh, &sh.full[i % F::kStages], (i / F::kStages) & 1);
-    };
-    const auto multiply_scores = [&](int t, int stage) {
-      const uint64_t a = a0 + t * kTile, b = k0 + stage * kTile;
-      if (leader) {
-        for (int i = 0; i < steps; ++i) {
-          const uint32_t at = (i >> 2) * kColumn + (i & 3) * 2;
-          mma_shared(tmem + t * kHalf, a + at, b + at, scores, i > 0);
-        }
-        commit(&sh.scores[t]);
-      }
-    };
     if (h.most == 0) continue;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
       if (h.units[t] > 0) {
-        if (!wait(p, sh, &sh.queries[t], query_parity >> t & 1)) return;
+        if (!wait_on(p, sh, &sh.queries[t], query_parity >> t & 1)) return;
         query_parity ^= 1u << t;
       }
     if (!full(taken)) return;
+    // queries came by ordinary copies: order them before the tensor core's reads
+    fence_proxy_async_smem();
     tc_fence_after();
 #pragma unroll
     for (int t = 0; t < 2; ++t)
-      if (h.units[t] > 0) multiply_scores(t, taken % F::kStages);
-    if (leader) commit(&sh.empty[taken % F::kStages]);
-    __syncwarp();
+      if (h.units[t] > 0) multiply_scores(t, taken % F::kStages, h.units[t] == 1);
+    commit(&sh.empty[taken % F::kStages]);
     ++taken;
     for (int u = 0; u < h.most; ++u) {
-      const int value = taken, next = taken + 1;       // this unit's values, the next one's keys
-      if (!full(value)) return;
-      const int32_t left = s.keys - (s.from + u) * p.unit_keys;
-      if (left < p.unit_keys) {
-        // what lies behind the last key, up to the unit's end
-        unsigned char* base = ring_ptr + (value % F::kStages) * F::kTileBytes;
-        const int words = (p.unit_keys - left) * (kRowBytes / 16);
-        for (int c = 0; c < F::kHalves; ++c)
-          for (int i = lane; i < words; i += 32)
-            *reinterpret_cast<uint4*>(base + (c * kKeys + left) * kRowBytes + i * 16) =
-                make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
-        __syncwarp();
+      const int value = taken % F::kStages;                  // this unit's values
+      const int next = (taken + 1) % F::kStages;             // the next one's keys
+      const bool goes_on = u + 1 < h.most;
+      if (s.keys - (s.from + u) * p.unit_keys < p.unit_keys) {
+        if (!wait_on(p, sh, &sh.cleared, clear_parity)) return;
+        clear_parity ^= 1;
+      } else if (!full(taken)) {
+        return;
       }
-      bool have = false;
+      if (goes_on && !full(taken + 1)) return;
+      const uint64_t b = v0 + value * kTile;
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         if (u < h.units[t]) {
-          if (!wait(p, sh, &sh.weights[t], weight_parity >> t & 1)) return;
-          weight_parity ^= 1u << t;
-          tc_fence_after();
-          if (leader) {
-            const uint64_t b = v0 + (value % F::kStages) * kTile;
-            for (int i = 0; i < key_steps; ++i)
-              mma_tmem(tmem + 2 * kHalf + t * kHalf, tmem + t * kHalf + i * 8,
-                       b + i * ((16 * kRowBytes) >> 4), output, u > 0 || i > 0);
-            commit(&sh.output[t]);
+          const uint32_t from = tmem + t * kHalf, to = from + 2 * kHalf;
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (!wait_on(p, sh, &sh.weights[t][half], weight_parity >> t & 1)) return;
+            tc_fence_after();
+#pragma unroll
+            for (int i = half * kStep / 16; i < (half + 1) * kStep / 16; ++i)
+              if (i < key_steps)
+                mma_tmem(to, from + i * 8, b + i * ((16 * kRowBytes) >> 4), output, u > 0 || i > 0);
+            commit(&sh.output[t][half]);
           }
+          weight_parity ^= 1u << t;
         }
-        if (u + 1 < h.units[t]) {
-          if (!have && !full(next)) return;
-          have = true;
-          tc_fence_after();
-          multiply_scores(t, next % F::kStages);
-        }
+        if (u + 1 < h.units[t]) multiply_scores(t, next, u + 2 == h.units[t]);
       }
-      if (leader) {
-        commit(&sh.empty[value % F::kStages]);
-        if (have) commit(&sh.empty[next % F::kStages]);
-      }
-      __syncwarp();
-      taken += have ? 2 : 1;
+      commit(&sh.empty[value]);
+      if (goes_on) commit(&sh.empty[next]);
+      taken += goes_on ? 2 : 1;
     }
   }
 }
 
 // ------------------------------------------------------------------------
-// Four warps, a thread a row.
+// One warp to a half: its queries, 16 bytes a copy, written where the 128-byte
+// swizzle has them, while the last tile's weights and output are still made.
+// (Loaded by the softmax threads before a tile's first products: 10 us a tile.)
+// The first of them also clears what lies behind a tile's last key in its values.
 template <int kDim>
-__device__ void soften(const AttendParams& p, Shared& sh, unsigned char* queries_ptr, int t) {
+__device__ void ask(const AttendParams& p, Shared& sh, uint32_t queries, unsigned char* ring_ptr,
+                    int t) {
+  using F = Form<kDim>;
+  constexpr int kPieces = kDim / 8, kStride = 32 / kPieces;   // rows at once
+  const int lane = threadIdx.x & 31, words = p.head_dim / 8;
+  const int piece = lane % kPieces;
+  const uint32_t to = queries + t * F::kTileBytes + (piece / 8) * kKeys * kRowBytes;
+  Walk<kTileRows> walk(p, sh.share);
+  Segment s;
+  int tiles[2] = {0, 0}, loaded = 0;
+  while (walk.next(p, &s)) {
+    const Halves h(p, s);
+    const int32_t rows = t ? h.rows[1] : h.rows[0], row0 = s.tile * kTileRows + t * kHalf;
+    if ((t ? h.units[1] : h.units[0]) > 0) {
+      if (!wait(p, sh, &sh.asked[t], ((t ? tiles[1] : tiles[0]) & 1) ^ 1)) break;
+      // (token and head of a row are counted, not divided for: 15 us a half)
+      int r = lane / kPieces;
+      int32_t token = p.by_group(row0 + r), head = row0 + r - token * p.group;
+      const int32_t tokens = p.by_group(kStride), heads = kStride - tokens * p.group;
+      const uint16_t* from = query_row(p, s.request.first, s.head, row0 + r) + piece * 8;
+      const int64_t step = tokens * p.q_token + heads * p.q_head;
+      const int64_t carry = p.q_token - p.group * p.q_head;
+#pragma unroll 8
+      for (int i = 0; i < kHalf / kStride; ++i) {
+        const bool some = r < rows && piece < words;
+        copy16(to + r * kRowBytes + (((piece & 7) ^ (r & 7)) << 4), some ? from : p.q, some ? 16 : 0);
+        r += kStride;
+        head += heads;
+        from += step;
+        if (head >= p.group) {
+          head -= p.group;
+          from += carry;
+        }
+      }
+      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                       smem_addr(&sh.queries[t]))
+                   : "memory");
+    }
+    loaded += 2 * h.most;
+    // A barrier is looked at in each of its phases, lest one be taken for the next.
+    bool asked = true;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (h.units[i] == 0) continue;
+      if (t == 0) asked = asked && wait(p, sh, &sh.asked[i], tiles[i] & 1);
+      ++tiles[i];
+    }
+    if (!asked) break;
+    const int32_t left = s.keys - (s.from + h.most - 1) * p.unit_keys;
+    if (t == 0 && h.most > 0 && left < p.unit_keys) {
+      // the last scores are there: the last values' stage is in its last phase
+      const int stage = (loaded - 1) % F::kStages;
+      if (!wait(p, sh, &sh.full[stage], ((loaded - 1) / F::kStages) & 1)) break;
+      unsigned char* base = ring_ptr + stage * F::kTileBytes;
+      const int n = (p.unit_keys - left) * (kRowBytes / 16);
+      for (int c = 0; c < F::kHalves; ++c)
+        for (int i = lane; i < n; i += 32)
+          *reinterpret_cast<uint4*>(base + (c * kKeys + left) * kRowBytes + i * 16) =
+              make_uint4(0, 0, 0, 0);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.cleared);
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// ------------------------------------------------------------------------
+// Four warps, a thread a row.  A unit's weights go in two steps of 64 keys, each
+// with its own look at the maximum, so that the first step's products run while
+// the second's weights are made: the chain from scores to weights and back is what
+// bounds a unit (scores 130 cycles out of TMEM, 64 weights some 330, 130 to
+// TMEM and the products' start; products of a half 1024).
+template <int kDim>
+__device__ void soften(const AttendParams& p, Shared& sh, int t) {
   using F = Form<kDim>;
   const int lane = threadIdx.x & 31, tid = threadIdx.x & (kHalf - 1), warp = tid >> 5;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   const uint32_t score_at = sh.tmem + lanes + t * kHalf, out_at = score_at + 2 * kHalf;
   const int block = blockIdx.x;
   float* parts = reinterpret_cast<float*>(reinterpret_cast<Joint*>(p.workspace) + gridDim.x);
-  unsigned char* queries = queries_ptr + t * F::kTileBytes;
-  // a negative scale: of the queries' opposites
-  const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0u;
-  const float scale = fabsf(p.scale) * kLog2e;
-  const int words = p.head_dim / 8;
+  const float scale = p.scale * kLog2e;
+  const bool at_once =
+      (reinterpret_cast<uintptr_t>(p.o) & 31) == 0 && p.head_dim % 16 == 0;
   Walk<kTileRows> walk(p, sh.share);
   Segment s;
   uint32_t done = 0;        // units of this half so far
@@ -383,93 +482,74 @@ __device__ void soften(const AttendParams& p, Shared& sh, unsigned char* queries
     const int32_t units = t ? h.units[1] : h.units[0];
     float top = minus_infinity(), sum = 0.0f;
     int32_t seen = 0;
-    if (tid < rows) seen = seen_keys(s.request, p.group == 1 ? row0 + tid : (row0 + tid) / p.group);
-    if (units > 0) {
-      // ---- queries, eight lanes a row of 64 values
-      constexpr int kPieces = kDim / 8;
-#pragma unroll 4
-      for (int i = 0; i < kPieces; ++i) {
-        const int at = i * kHalf + tid, r = at / kPieces, piece = at % kPieces;
-        uint4 w = make_uint4(0, 0, 0, 0);
-        if (r < rows && piece < words)
-          w = *reinterpret_cast<const uint4*>(query_row(p, s.request.first, s.head, row0 + r) +
-                                              piece * 8);
-        w.x ^= flip;
-        w.y ^= flip;
-        w.z ^= flip;
-        w.w ^= flip;
-        *reinterpret_cast<uint4*>(queries + (piece / 8) * kKeys * kRowBytes + r * kRowBytes +
-                                  (((piece & 7) ^ (r & 7)) << 4)) = w;
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&sh.queries[t]);
-    }
+    if (tid < rows) seen = seen_keys(s.request, p.by_group(row0 + tid));
     for (int u = 0; u < units; ++u) {
       if (!wait(p, sh, &sh.scores[t], done & 1)) return;
       tc_fence_after();
       float v[kKeys];
-#pragma unroll
-      for (int c = 0; c < kKeys; c += 32) tmem_load32(score_at + c, v + c);
-      tmem_ld_wait();
+      tmem_load32(score_at, v);
+      tmem_load32(score_at + 32, v + 32);
+      tmem_arrived<kStep>(v);
+      tmem_load32(score_at + 64, v + 64);
+      tmem_load32(score_at + 96, v + 96);
       const int32_t key0 = (s.from + u) * p.unit_keys;
       int32_t valid = seen - key0;
       valid = valid < p.unit_keys ? valid : p.unit_keys;
-      if (valid < kKeys) {
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c)
-          if (c >= valid) v[c] = minus_infinity();
-      }
-      float m[4] = {v[0], v[1], v[2], v[3]};
+      for (int half = 0; half < 2; ++half) {
+        float* x = v + half * kStep;
+        if (half == 1) tmem_arrived<kStep>(x);
+        if (valid < (half + 1) * kStep) {
 #pragma unroll
-      for (int c = 4; c < kKeys; c += 8)
+          for (int c = 0; c < kStep; ++c)
+            if (half * kStep + c >= valid) x[c] = minus_infinity();
+        }
+        float m[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          m[i] = c + 4 + i < kKeys ? fmaxf(m[i], fmaxf(v[c + i], v[c + 4 + i])) : fmaxf(m[i], v[c + i]);
-      const float most = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])) * scale;
-      if (__any_sync(0xffffffffu, most > top + kSlack)) {
-        const float now = fmaxf(top, most);
-        const float by = now == minus_infinity() ? 1.0f : exp2_fast(top - now);
-        top = now;
-        sum *= by;
-        if (u > 0) {
-          if (!wait(p, sh, &sh.output[t], (done - 1) & 1)) return;
-          tc_fence_after();
+        for (int c = 4; c < kStep; c += 8)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            m[i] = c + 4 + i < kStep ? max3(m[i], x[c + i], x[c + 4 + i]) : fmaxf(m[i], x[c + i]);
+        const float most = fmaxf(max3(m[0], m[1], m[2]), m[3]) * scale;
+        if (__any_sync(0xffffffffu, most > top + kSlack)) {
+          const float now = fmaxf(top, most);
+          const float by = now == minus_infinity() ? 1.0f : exp2_fast(top - now);
+          top = now;
+          sum *= by;
+          if (u > 0 || half == 1) {
+            // the step before has gone into the output
+            if (!wait(p, sh, &sh.output[t][half ^ 1], half == 1 ? done & 1 : (done - 1) & 1)) return;
+            tc_fence_after();
 #pragma unroll 1
-          for (int c = 0; c < p.head_dim; c += 32) {
-            float o[32];
-            tmem_load32(out_at + c, o);
-            tmem_ld_wait();
+            for (int c = 0; c < p.head_dim; c += 32) {
+              float o[32];
+              tmem_load32(out_at + c, o);
+              tmem_arrived<32>(o);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] *= by;
-            tmem_store32(out_at + c, o);
+              for (int i = 0; i < 32; ++i) o[i] *= by;
+              tmem_store32(out_at + c, o);
+            }
           }
         }
-      }
-      const float base = top == minus_infinity() ? 0.0f : -top;
-      const float2 scale2 = make_float2(scale, scale), base2 = make_float2(base, base);
-      float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        const float base = top == minus_infinity() ? 0.0f : -top;
+        const float2 scale2 = make_float2(scale, scale), base2 = make_float2(base, base);
+        float2 sums[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+        uint32_t w[kStep / 2];
 #pragma unroll
-      for (int c = 0; c < kKeys; c += 32) {
-        uint32_t w[16];
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          float2 x = fma2(make_float2(v[c + 2 * i], v[c + 2 * i + 1]), scale2, base2);
-          x.x = exp2_fast(x.x);
-          x.y = exp2_fast(x.y);
-          sums[i & 1] = add2(sums[i & 1], x);
-          w[i] = pack_bf16(x.x, x.y);
+        for (int i = 0; i < kStep / 2; ++i) {
+          float2 y = fma2(make_float2(x[2 * i], x[2 * i + 1]), scale2, base2);
+          y.x = exp2_fast(y.x);
+          y.y = exp2_fast(y.y);
+          sums[i & 1] = add2(sums[i & 1], y);
+          w[i] = pack_bf16(y.x, y.y);
         }
-        tmem_store16(score_at + c / 2, w);
+        sum += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
+        tmem_store32(score_at + half * (kStep / 2), reinterpret_cast<const float*>(w));
+        tmem_store_wait();
+        tc_fence_before();
+        mbar_arrive(&sh.weights[t][half]);
       }
-      sum += (sums[0].x + sums[0].y) + (sums[1].x + sums[1].y);
-      tmem_store_wait();
-      tc_fence_before();
-      mbar_arrive(&sh.weights[t]);
       ++done;
-    }
-    if (units > 0) {
-      if (!wait(p, sh, &sh.output[t], (done - 1) & 1)) return;
-      tc_fence_after();
     }
     // ---- output, or this block's part of it
     const bool whole = s.from == 0 && s.to == s.all;
@@ -477,70 +557,70 @@ __device__ void soften(const AttendParams& p, Shared& sh, unsigned char* queries
                   t * kHalf + tid;
     const bool live = tid < rows;
     uint16_t* out = live ? output_row(p, s.request.first, s.head, row0 + tid) : nullptr;
-    const float by = inverse_sum(sum);
-    bool odd = !(fabsf(sum) < __uint_as_float(0x7F800000u));
-    if (!whole && live) {
-      part[0] = top;
-      part[kTileRows] = sum;
-    }
-#pragma unroll 1
-    for (int c = 0; c < p.head_dim; c += 32) {
-      float o[32];
-      if (units > 0) {
-        tmem_load32(out_at + c, o);
-        tmem_ld_wait();
-      } else {
+    if (units > 0) {
+      float o[kDim];
+      if (!wait(p, sh, &sh.output[t][1], (done - 1) & 1)) return;
+      tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < 32; ++i) o[i] = 0.0f;
-      }
-      float size = 0.0f;
+      for (int c = 0; c < kDim; c += 32) tmem_load32(out_at + c, o + c);
+      tmem_arrived<kDim>(o);
+      float size = fabsf(sum);
 #pragma unroll
-      for (int i = 0; i < 32; ++i)
-        if (c + i < p.head_dim) size += fabsf(o[i]);
-      odd |= !(size < __uint_as_float(0x7F800000u));
-      if (!live) continue;
-      if (whole) {
+      for (int c = 0; c < kDim; ++c)
+        if (c < p.head_dim) size += fabsf(o[c]);
+      if (live && whole) {
+        const float by = inverse_sum(sum);
 #pragma unroll
-        for (int i = 0; i < 32; i += 8)
-          if (c + i < p.head_dim) {
-            const float f[8] = {o[i] * by,     o[i + 1] * by, o[i + 2] * by, o[i + 3] * by,
-                                o[i + 4] * by, o[i + 5] * by, o[i + 6] * by, o[i + 7] * by};
-            *reinterpret_cast<uint4*>(out + c + i) = pack8(f);
+        for (int c = 0; c < kDim; c += 16)
+          if (c + 16 <= p.head_dim) {
+            store16(out + c, o + c, by, at_once);
+          } else if (c < p.head_dim) {  // eight
+            const float f[8] = {o[c] * by,     o[c + 1] * by, o[c + 2] * by, o[c + 3] * by,
+                                o[c + 4] * by, o[c + 5] * by, o[c + 6] * by, o[c + 7] * by};
+            *reinterpret_cast<uint4*>(out + c) = pack8(f);
           }
-      } else if (units > 0) {
+      } else if (live) {
+        part[0] = top;
+        part[kTileRows] = sum;
 #pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c + i < p.head_dim) part[(2 + c + i) * kTileRows] = o[i];
+        for (int c = 0; c < kDim; ++c)
+          if (c < p.head_dim) part[(2 + c) * kTileRows] = o[c];
       }
+      tc_fence_before();
+      // ---- rows that something out of sight may have spoilt, a warp a row
+      const uint32_t spoilt =
+          __ballot_sync(0xffffffffu, live && !(size < __uint_as_float(0x7F800000u)));
+      if (spoilt && lane == 0) atomicAdd(&sh.busy, 1u);
+      for (uint32_t again = spoilt; again; again &= again - 1) {
+        const int who = __ffs(again) - 1;
+        const int32_t row = row0 + warp * 32 + who;
+        const int32_t to = min(__shfl_sync(0xffffffffu, seen, who), s.to * p.unit_keys);
+        Slice own;
+        warp_attend(p, query_row(p, s.request.first, s.head, row), s.index, s.head,
+                    s.from * p.unit_keys, to, &own);
+        float* its = part - lane + who;
+        uint16_t* there = output_row(p, s.request.first, s.head, row);
+        for (int i = 0; i < kDim / 32; ++i) {
+          const int d = lane + 32 * i;
+          if (d >= p.head_dim) continue;
+          if (whole)
+            there[d] = f32_to_bf16(own.o[i] * inverse_sum(own.sum));
+          else
+            its[(2 + d) * kTileRows] = own.o[i];
+        }
+        if (!whole && lane == 0) {
+          its[0] = own.most;
+          its[kTileRows] = own.sum;
+        }
+        __syncwarp();
+      }
+      if (spoilt && lane == 0) atomicSub(&sh.busy, 1u);
+    } else if (live && whole) {
+      for (int c = 0; c < p.head_dim; c += 8)
+        *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
+    } else if (live) {
+      part[0] = minus_infinity();   // the join looks no further
     }
-    tc_fence_before();
-    // ---- rows that something out of sight may have spoilt, a warp a row
-    const uint32_t spoilt = __ballot_sync(0xffffffffu, odd && live && units > 0);
-    if (spoilt && lane == 0) atomicAdd(&sh.busy, 1u);
-    for (uint32_t again = spoilt; again; again &= again - 1) {
-      const int who = __ffs(again) - 1;
-      const int32_t row = row0 + warp * 32 + who;
-      const int32_t to = min(__shfl_sync(0xffffffffu, seen, who), s.to * p.unit_keys);
-      Slice own;
-      warp_attend(p, query_row(p, s.request.first, s.head, row), s.index, s.head,
-                  s.from * p.unit_keys, to, &own);
-      float* its = part - lane + who;
-      uint16_t* there = output_row(p, s.request.first, s.head, row);
-      for (int i = 0; i < kDim / 32; ++i) {
-        const int d = lane + 32 * i;
-        if (d >= p.head_dim) continue;
-        if (whole)
-          there[d] = f32_to_bf16(own.o[i] * inverse_sum(own.sum));
-        else
-          its[(2 + d) * kTileRows] = own.o[i];
-      }
-      if (!whole && lane == 0) {
-        its[0] = own.most;
-        its[kTileRows] = own.sum;
-      }
-      __syncwarp();
-    }
-    if (spoilt && lane == 0) atomicSub(&sh.busy, 1u);
   }
 }
 
@@ -562,8 +642,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ Shared sh;
   const uint32_t base = smem_addr(raw);
   const uint32_t queries = (base + 1023) & ~1023u, ring = queries + 2 * F::kTileBytes;
-  unsigned char* queries_ptr = raw + (queries - base);
-  unsigned char* ring_ptr = queries_ptr + 2 * F::kTileBytes;
+  unsigned char* ring_ptr = raw + (ring - base);
   const int warp = threadIdx.x >> 5, blocks = gridDim.x, block = blockIdx.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < F::kStages; ++i) {
@@ -571,11 +650,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sh.queries[t], kHalf);
+      mbar_init(&sh.queries[t], 32);
+      mbar_init(&sh.asked[t], 1);
       mbar_init(&sh.scores[t], 1);
-      mbar_init(&sh.weights[t], kHalf);
-      mbar_init(&sh.output[t], 1);
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.weights[t][i], kHalf);
+        mbar_init(&sh.output[t][i], 1);
+      }
     }
+    mbar_init(&sh.cleared, 1);
     mbar_init(&sh.drain, 1);
     sh.stop = sh.busy = 0;
     sh.issued = 0;
@@ -597,16 +680,17 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   if (warp < kSoftmaxWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-    soften<kDim>(p, sh, queries_ptr, warp / 4);
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    soften<kDim>(p, sh, warp / 4);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kLoadWarp)
       load<kDim>(p, maps, sh, ring);
     else if (warp == kMultiplyWarp)
-      multiply<kDim>(p, sh, queries, ring, ring_ptr);
-    else if (warp == kJointWarp && one_lane())
-      announce(p, sh);
+      multiply<kDim>(p, sh, queries, ring);
+    else
+      ask<kDim>(p, sh, queries, ring_ptr, warp - kQueryWarp);
+    if (warp == kQueryWarp && one_lane()) announce(p, sh);
   }
   tc_fence_before();
   __syncthreads();
@@ -712,7 +796,7 @@ int launch_at(const AttendParams& p, const Maps& maps, cudaStream_t s) {
 // and outputs are.
 bool wide_takes(const AttendParams& p) {
   return !p.e4m3 && p.head_dim <= 128 && p.head_dim % 8 == 0 && p.page_size % 8 == 0 &&
-         p.pages > 0 && p.scale != 0.0f && on_words(p.key) && on_words(p.value) &&
+         p.pages > 0 && p.scale > 0.0f && on_words(p.key) && on_words(p.value) &&
          (reinterpret_cast<uintptr_t>(p.q) & 15) == 0 && p.q_token % 8 == 0 && p.q_head % 8 == 0 &&
          (reinterpret_cast<uintptr_t>(p.o) & 15) == 0 && encode();
 }
@@ -731,6 +815,8 @@ bool launch_attend_wide(const AttendParams& given, void* stream, int* status) {
   maps.box = kKeys;
   while (p.page_size % maps.box) maps.box -= 8;
   p.unit_keys = kKeys / maps.box * maps.box;
+  maps.by_box = Divide(maps.box);
+  p.by_unit = Divide(p.unit_keys);
   if (!make_map(&maps.key, p.key, p, maps.box) || !make_map(&maps.value, p.value, p, maps.box))
     return false;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -71,6 +71,28 @@ struct PagesParams {
   int32_t* slots;
 };
 
+// Division of a number below 2^31 by d: with 2^(l-1) < d <= 2^l and
+// m = ceil(2^(31+l) / d) the product n m exceeds n 2^(31+l) / d by less than
+// 2^(31+l) / d, so that its quotient is exact.
+struct Divide {
+  uint32_t by, multiplier;
+  int32_t shift;
+  Divide() = default;
+  explicit Divide(uint32_t d) : by(d), shift(31) {
+    while ((uint64_t(1) << (shift - 31)) < d) ++shift;
+    multiplier = static_cast<uint32_t>(((uint64_t(1) << shift) + d - 1) / d);
+  }
+#ifdef __CUDACC__
+  __device__ __forceinline__ int32_t operator()(int32_t n) const {
+    return static_cast<int32_t>((static_cast<uint64_t>(static_cast<uint32_t>(n)) * multiplier) >>
+                                shift);
+  }
+  __device__ __forceinline__ int32_t up(int32_t n) const {  // rounded up
+    return (*this)(n + static_cast<int32_t>(by) - 1);
+  }
+#endif
+};
+
 struct AttendParams {
   const uint16_t* q;
   int64_t q_token, q_head;
@@ -92,6 +114,7 @@ struct AttendParams {
   float scale;
   int64_t longest;
   int32_t unit_keys;              // keys of a unit of work
+  Divide by_group, by_page, by_unit;
   int32_t blocks;                 // that share the work
   void* workspace;
   Control* ctl;

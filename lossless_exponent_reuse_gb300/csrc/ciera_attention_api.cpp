@@ -285,6 +285,8 @@ int ciera_attend(const uint16_t *q_dev, int64_t q_token_stride, int64_t q_head_s
   p.head_dim = static_cast<int32_t>(dim);
   p.pages = static_cast<int32_t>(cache->pages);
   p.page_size = static_cast<int32_t>(cache->page_size);
+  p.by_group = Divide(static_cast<uint32_t>(p.group));
+  p.by_page = Divide(static_cast<uint32_t>(p.page_size));
   p.e4m3 = cache->type == CIERA_E4M3;
   p.scale = scale;
   p.longest = longest < tokens ? longest : tokens;
