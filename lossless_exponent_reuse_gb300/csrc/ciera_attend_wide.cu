@@ -30,8 +30,8 @@ constexpr int kStep = 64;               // keys whose weights are handed on at o
 constexpr int kRowBytes = 128;          // of a stage's row: 64 values
 constexpr int kSoftmaxWarps = 8;
 constexpr int kMultiplyWarp = kSoftmaxWarps;
-constexpr int kLoadWarp = kSoftmaxWarps + 1;
-constexpr int kQueryWarp = kSoftmaxWarps + 2;   // and the next, one to a half
+constexpr int kLoadWarp = kSoftmaxWarps + 1;    // keys, and the next warp values
+constexpr int kQueryWarp = kSoftmaxWarps + 3;
 // Three groups of four warps, of 168 registers a thread at launch, 64512: 200 for
 // the two that hold a row's scores, 104 for the third, 64512.
 constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
@@ -232,22 +232,25 @@ struct Halves {
 };
 
 struct Maps {
-  CUtensorMap key, value;
+  CUtensorMap key, value, query;
+  int32_t query_box;  // tokens of a half's queries; 0: they come by ordinary copies
   int32_t box;       // keys of a box, which divide a page's
   Divide by_box;
 };
 
 // ------------------------------------------------------------------------
-// One warp: keys and values by TMA.  A lane per box: it looks up the page, a unit
-// ahead, and issues the box's loads.
+// Two warps: keys and values by TMA, stages in turn.  A lane per box: it looks up
+// the page, a unit ahead, and issues the box's loads.  (One warp for both: with
+// pages of 16 its 32 loads a unit took as long as the products.)
 template <int kDim>
-__device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32_t ring) {
+__device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32_t ring, int side) {
   using F = Form<kDim>;
   const int lane = threadIdx.x & 31;
   const int columns = (p.head_dim + 63) / 64;
+  const CUtensorMap* map = side ? &maps.value : &maps.key;
   Walk<kTileRows> walk(p, sh.share);
   Segment s;
-  int issued = 0;
+  int at = side;      // of all loads
   bool alive = true;
   while (alive && walk.next(p, &s)) {
     const Halves halves(p, s);
@@ -256,40 +259,36 @@ __device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32
       *page = p.pages;     // none: zeros
       *place = 0;
       if (unit >= halves.most || lane * maps.box >= p.unit_keys || key >= s.keys) return;
-      const int32_t at = p.by_page(key), found = page_at(p, s.index, at);
-      *place = key - at * p.page_size;
+      const int32_t index = p.by_page(key), found = page_at(p, s.index, index);
+      *place = key - index * p.page_size;
       if (found >= 0) *page = found;
     };
     int32_t page, place;
     look(0, &page, &place);
-    for (int u = 0; alive && u < halves.most; ++u) {
+    for (int u = 0; u < halves.most; ++u, at += 2) {
       const int32_t left = s.keys - (s.from + u) * p.unit_keys;
-      const int32_t keys = left < p.unit_keys ? left : p.unit_keys;
-      const int boxes = maps.by_box.up(keys);
-      for (int side = 0; side < 2; ++side) {
-        const int stage = issued % F::kStages;
-        uint64_t* full = &sh.full[stage];
-        alive = wait(p, sh, &sh.empty[stage], ((issued / F::kStages) & 1) ^ 1);
-        if (!alive) break;
-        if (lane == 0)
-          mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * columns * maps.box * kRowBytes));
-        __syncwarp();
-        if (lane < boxes) {
-          const uint32_t to = ring + stage * F::kTileBytes + lane * maps.box * kRowBytes;
-          const CUtensorMap* map = side ? &maps.value : &maps.key;
-          for (int c = 0; c < columns; ++c)
-            tma_4d(to + c * kKeys * kRowBytes, map, c * 64, place, s.head, page, full);
-        }
-        ++issued;
+      const int boxes = maps.by_box.up(left < p.unit_keys ? left : p.unit_keys);
+      const int stage = at % F::kStages;
+      uint64_t* full = &sh.full[stage];
+      alive = wait(p, sh, &sh.empty[stage], ((at / F::kStages) & 1) ^ 1);
+      if (!alive) break;
+      if (lane == 0)
+        mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * columns * maps.box * kRowBytes));
+      __syncwarp();
+      if (lane < boxes) {
+        const uint32_t to = ring + stage * F::kTileBytes + lane * maps.box * kRowBytes;
+        for (int c = 0; c < columns; ++c)
+          tma_4d(to + c * kKeys * kRowBytes, map, c * 64, place, s.head, page, full);
       }
       look(u + 1, &page, &place);
     }
   }
   // What is under way writes this block's shared memory: the products have read
   // it, or after a wait that ran out it is seen to land (settle).
-  for (int i = issued > F::kStages ? issued - F::kStages : 0; alive && i < issued; ++i)
-    alive = wait(p, sh, &sh.empty[i % F::kStages], (i / F::kStages) & 1);
-  if (lane == 0) sh.issued = issued;
+  const int first = at - 2 * F::kStages;
+  for (int i = first < side ? side : first; alive && i < at; i += 2)
+    if (i >= at - F::kStages) alive = wait(p, sh, &sh.empty[i % F::kStages], (i / F::kStages) & 1);
+  if (lane == 0) atomicMax(&sh.issued, at - 1);
 }
 
 // ------------------------------------------------------------------------
@@ -384,64 +383,83 @@ __device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, ui
 }
 
 // ------------------------------------------------------------------------
-// One warp to a half: its queries, 16 bytes a copy, written where the 128-byte
-// swizzle has them, while the last tile's weights and output are still made.
-// (Loaded by the softmax threads before a tile's first products: 10 us a tile.)
-// The first of them also clears what lies behind a tile's last key in its values.
+// One warp: queries, while the last tile's weights and output are still made.
+// By TMA, a box of whole tokens, where a half is a number of them; else 16
+// bytes a copy, written where the 128-byte swizzle has them (6 us a half).  And it
+// clears what lies behind a tile's last key in its values.
 template <int kDim>
-__device__ void ask(const AttendParams& p, Shared& sh, uint32_t queries, unsigned char* ring_ptr,
-                    int t) {
+__device__ __forceinline__ void copy_queries(const AttendParams& p, const Segment& s, Shared& sh,
+                                             uint32_t queries, int t, int32_t rows) {
   using F = Form<kDim>;
   constexpr int kPieces = kDim / 8, kStride = 32 / kPieces;   // rows at once
-  const int lane = threadIdx.x & 31, words = p.head_dim / 8;
-  const int piece = lane % kPieces;
+  const int lane = threadIdx.x & 31, words = p.head_dim / 8, piece = lane % kPieces;
+  const int32_t row0 = s.tile * kTileRows + t * kHalf;
   const uint32_t to = queries + t * F::kTileBytes + (piece / 8) * kKeys * kRowBytes;
+  // token and head of a row are counted, not divided for
+  int r = lane / kPieces;
+  int32_t head = row0 + r - p.by_group(row0 + r) * p.group;
+  const int32_t tokens = p.by_group(kStride), heads = kStride - tokens * p.group;
+  const uint16_t* from = query_row(p, s.request.first, s.head, row0 + r) + piece * 8;
+  const int64_t step = tokens * p.q_token + heads * p.q_head;
+  const int64_t carry = p.q_token - p.group * p.q_head;
+#pragma unroll 8
+  for (int i = 0; i < kHalf / kStride; ++i) {
+    const bool some = r < rows && piece < words;
+    copy16(to + r * kRowBytes + (((piece & 7) ^ (r & 7)) << 4), some ? from : p.q, some ? 16 : 0);
+    r += kStride;
+    head += heads;
+    from += step;
+    if (head >= p.group) {
+      head -= p.group;
+      from += carry;
+    }
+  }
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
+                   smem_addr(&sh.queries[t]))
+               : "memory");
+}
+
+template <int kDim>
+__device__ void ask(const AttendParams& p, const Maps& maps, Shared& sh, uint32_t queries,
+                    unsigned char* ring_ptr) {
+  using F = Form<kDim>;
+  const int lane = threadIdx.x & 31;
+  const int columns = (p.head_dim + 63) / 64;
   Walk<kTileRows> walk(p, sh.share);
   Segment s;
   int tiles[2] = {0, 0}, loaded = 0;
-  while (walk.next(p, &s)) {
+  bool alive = true;
+  while (alive && walk.next(p, &s)) {
     const Halves h(p, s);
-    const int32_t rows = t ? h.rows[1] : h.rows[0], row0 = s.tile * kTileRows + t * kHalf;
-    if ((t ? h.units[1] : h.units[0]) > 0) {
-      if (!wait(p, sh, &sh.asked[t], ((t ? tiles[1] : tiles[0]) & 1) ^ 1)) break;
-      // (token and head of a row are counted, not divided for: 15 us a half)
-      int r = lane / kPieces;
-      int32_t token = p.by_group(row0 + r), head = row0 + r - token * p.group;
-      const int32_t tokens = p.by_group(kStride), heads = kStride - tokens * p.group;
-      const uint16_t* from = query_row(p, s.request.first, s.head, row0 + r) + piece * 8;
-      const int64_t step = tokens * p.q_token + heads * p.q_head;
-      const int64_t carry = p.q_token - p.group * p.q_head;
-#pragma unroll 8
-      for (int i = 0; i < kHalf / kStride; ++i) {
-        const bool some = r < rows && piece < words;
-        copy16(to + r * kRowBytes + (((piece & 7) ^ (r & 7)) << 4), some ? from : p.q, some ? 16 : 0);
-        r += kStride;
-        head += heads;
-        from += step;
-        if (head >= p.group) {
-          head -= p.group;
-          from += carry;
-        }
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      if (h.units[t] == 0) continue;
+      // (the last scores of the tile before are waited for below)
+      if (!maps.query_box) {
+        copy_queries<kDim>(p, s, sh, queries, t, h.rows[t]);
+      } else if (lane == 0) {
+        const int32_t token = s.request.first + p.by_group(s.tile * kTileRows + t * kHalf);
+        mbar_arrive_expect_tx(&sh.queries[t], static_cast<uint32_t>(columns * kHalf * kRowBytes));
+        for (int c = 0; c < columns; ++c)
+          tma_4d(queries + t * F::kTileBytes + c * kKeys * kRowBytes, &maps.query, c * 64, 0, s.head,
+                 token, &sh.queries[t]);
       }
-      asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(
-                       smem_addr(&sh.queries[t]))
-                   : "memory");
     }
     loaded += 2 * h.most;
-    // A barrier is looked at in each of its phases, lest one be taken for the next.
-    bool asked = true;
+    // the tile's last scores: its queries have been read (a barrier is looked at
+    // in each of its phases, lest one be taken for the next)
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (h.units[i] == 0) continue;
-      if (t == 0) asked = asked && wait(p, sh, &sh.asked[i], tiles[i] & 1);
-      ++tiles[i];
+    for (int t = 0; t < 2; ++t) {
+      if (h.units[t] == 0) continue;
+      alive = alive && wait(p, sh, &sh.asked[t], tiles[t] & 1);
+      ++tiles[t];
     }
-    if (!asked) break;
     const int32_t left = s.keys - (s.from + h.most - 1) * p.unit_keys;
-    if (t == 0 && h.most > 0 && left < p.unit_keys) {
-      // the last scores are there: the last values' stage is in its last phase
+    if (alive && h.most > 0 && left < p.unit_keys) {
+      // its last values' stage is in its last phase
       const int stage = (loaded - 1) % F::kStages;
-      if (!wait(p, sh, &sh.full[stage], ((loaded - 1) / F::kStages) & 1)) break;
+      alive = wait(p, sh, &sh.full[stage], ((loaded - 1) / F::kStages) & 1);
+      if (!alive) break;
       unsigned char* base = ring_ptr + stage * F::kTileBytes;
       const int n = (p.unit_keys - left) * (kRowBytes / 16);
       for (int c = 0; c < F::kHalves; ++c)
@@ -454,6 +472,12 @@ __device__ void ask(const AttendParams& p, Shared& sh, uint32_t queries, unsigne
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
+  if (!alive && maps.query_box) {
+    // queries asked for and never read are seen to land
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+      if (tiles[t]) mbar_wait_bounded(&sh.queries[t], (tiles[t] - 1) & 1, kLandNs);
+  }
 }
 
 // ------------------------------------------------------------------------
@@ -650,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&sh.empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
-      mbar_init(&sh.queries[t], 32);
+      mbar_init(&sh.queries[t], maps.query_box ? 1 : 32);
       mbar_init(&sh.asked[t], 1);
       mbar_init(&sh.scores[t], 1);
       for (int i = 0; i < 2; ++i) {
@@ -684,12 +708,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     soften<kDim>(p, sh, warp / 4);
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == kLoadWarp)
-      load<kDim>(p, maps, sh, ring);
-    else if (warp == kMultiplyWarp)
+    if (warp == kMultiplyWarp)
       multiply<kDim>(p, sh, queries, ring);
+    else if (warp < kQueryWarp)
+      load<kDim>(p, maps, sh, ring, warp - kLoadWarp);
     else
-      ask<kDim>(p, sh, queries, ring_ptr, warp - kQueryWarp);
+      ask<kDim>(p, maps, sh, queries, ring_ptr);
     if (warp == kQueryWarp && one_lane()) announce(p, sh);
   }
   tc_fence_before();
@@ -758,9 +782,9 @@ __global__ void __launch_bounds__(kTileRows) k_attend_wide_join(const AttendPara
 // ------------------------------------------------------------------------
 // Host
 
-bool make_map(CUtensorMap* map, const Side& s, const AttendParams& p, int box) {
-  const int64_t n[3] = {p.page_size, p.heads, p.pages};
-  const int64_t at[3] = {s.stride[1], s.stride[2], s.stride[0]};
+// Of rows of head_dim values, n[i] of them at[i] elements apart; boxes of 64 values.
+bool make_map(CUtensorMap* map, const void* data, const AttendParams& p, const int64_t (&n)[3],
+              const int64_t (&at)[3], const int (&box)[3]) {
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.head_dim)}, strides[3];
   for (int i = 0; i < 3; ++i) {
     dims[i + 1] = static_cast<cuuint64_t>(n[i]);
@@ -768,11 +792,18 @@ bool make_map(CUtensorMap* map, const Side& s, const AttendParams& p, int box) {
     strides[i] = static_cast<cuuint64_t>(n[i] > 1 && at[i] > 0 ? 2 * at[i] : 16);
     if (n[i] > 1 && at[i] <= 0) return false;
   }
-  const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box), 1, 1}, ones[4] = {1, 1, 1, 1};
-  return encode()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, s.data, dims, strides, boxes, ones,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box[0]),
+                               static_cast<cuuint32_t>(box[1]), static_cast<cuuint32_t>(box[2])};
+  const cuuint32_t ones[4] = {1, 1, 1, 1};
+  return encode()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(data), dims, strides,
+                  boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool make_side_map(CUtensorMap* map, const Side& s, const AttendParams& p, int box) {
+  return make_map(map, s.data, p, {p.page_size, p.heads, p.pages},
+                  {s.stride[1], s.stride[2], s.stride[0]}, {box, 1, 1});
 }
 
 bool on_words(const Side& s) {
@@ -817,8 +848,16 @@ bool launch_attend_wide(const AttendParams& given, void* stream, int* status) {
   p.unit_keys = kKeys / maps.box * maps.box;
   maps.by_box = Divide(maps.box);
   p.by_unit = Divide(p.unit_keys);
-  if (!make_map(&maps.key, p.key, p, maps.box) || !make_map(&maps.value, p.value, p, maps.box))
+  if (!make_side_map(&maps.key, p.key, p, maps.box) ||
+      !make_side_map(&maps.value, p.value, p, maps.box))
     return false;
+  maps.query_box = kHalf % p.group ? 0 : kHalf / p.group;
+  if (!maps.query_box ||
+      !make_map(&maps.query, p.q, p, {p.group, p.heads, p.tokens},
+                {p.q_head, p.q_head * p.group, p.q_token}, {p.group, 1, maps.query_box})) {
+    maps.query_box = 0;
+    maps.query = maps.key;  // not used
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   *status = p.head_dim <= 64 ? launch_at<64>(p, maps, s) : launch_at<128>(p, maps, s);
   return true;
