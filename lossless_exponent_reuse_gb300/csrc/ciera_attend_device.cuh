@@ -64,8 +64,9 @@ __device__ __forceinline__ int32_t page_at(const AttendParams& p, int32_t reques
   return page >= 0 && page < p.pages ? page : -1;
 }
 
+// 2^(exponent - 127)
 __device__ __forceinline__ float scale_of(uint32_t exponent) {
-  return exponent == 255 ? __uint_as_float(0x7FC00000u) : __uint_as_float(exponent << 23);
+  return __uint_as_float(exponent == 255 ? 0x7FC00000u : exponent ? exponent << 23 : 0x00400000u);
 }
 
 // A warp's share of one row: values lane, lane + 32, ... of the head.
@@ -145,13 +146,14 @@ __device__ __noinline__ void warp_attend(const AttendParams& p, const uint16_t* 
 // ------------------------------------------------------------------------
 // How a call's work is dealt out.  A tile is up to kRows rows (new tokens by
 // query heads of one head of keys, token by token); a unit is p.unit_keys
-// keys of a tile, as many units as its last row sees, one if that sees none.  All units of
-// all tiles, in order of request, head and tile, are cut into as many even
-// ranges as there are blocks, whatever the lengths are: ragged batches, one long
-// context and whole prompts fill the blocks alike.  A block that has a part of
-// a tile leaves its sums in the workspace, in a slot of its own: slot 0 if the tile
-// began before it, slot 1 if it goes on behind it.  The parts of a tile are joined
-// by a launch of their own, in the order of the blocks.
+// keys of a tile, as many units as its last row sees, one if that sees none.
+// A unit weighs 1, and a tile has a weight of its own besides (its queries and output).
+// All tiles, in order of request, head and tile, are cut into ranges of even
+// weight, as many as there are blocks, whatever the lengths are: ragged batches,
+// one long context and whole prompts fill the blocks alike.  A block that has a
+// part of a tile leaves its sums in the workspace, in a slot of its own: slot 0
+// if the tile began before it, slot 1 if it goes on behind it.  The parts of a tile
+// are joined by a launch of their own, in the order of the blocks.
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -176,10 +178,35 @@ struct Tiles {
     const int32_t n = keys(p, r, tile);
     return n > 0 ? p.by_unit.up(n) : 1;
   }
+  // A tile weighs as much as two of its units besides (8192-token prompt of 16
+  // heads, 24 chunks, in us: without 234, 172; one 232, 137; two 236, 128; three 240, 124).
+  static constexpr int32_t kTileWeight = 2;
+  static __device__ __forceinline__ int32_t weight(const AttendParams& p, const Request& r,
+                                                   int32_t tile) {
+    return kTileWeight + units(p, r, tile);
+  }
+  // Of all tiles of a head of each lane's request; a whole warp.  Its lanes share the
+  // tiles of a request that has many (a prompt of 8192 tokens of 16 heads to one: 35 us
+  // to find the last block's place by one lane).
   static __device__ int64_t of_head(const AttendParams& p, const Request& r) {
+    constexpr int32_t kFew = 8;
+    const int lane = threadIdx.x & 31;
     const int32_t n = count(p, r);
     int64_t sum = 0;
-    for (int32_t t = 0; t < n; ++t) sum += units(p, r, t);
+    if (n <= kFew)
+      for (int32_t t = 0; t < n; ++t) sum += weight(p, r, t);
+    for (uint32_t many = __ballot_sync(0xffffffffu, n > kFew); many; many &= many - 1) {
+      const int who = __ffs(many) - 1;
+      const Request its = {__shfl_sync(0xffffffffu, r.first, who),
+                           __shfl_sync(0xffffffffu, r.tokens, who),
+                           __shfl_sync(0xffffffffu, r.keys, who)};
+      const int32_t tiles = count(p, its);
+      int64_t part = 0;
+      for (int32_t t = lane; t < tiles; t += 32) part += weight(p, its, t);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(0xffffffffu, part, o);
+      if (lane == who) sum = part;
+    }
     return sum;
   }
 };
@@ -187,9 +214,10 @@ struct Tiles {
 // A block's range and where it begins.
 struct Share {
   int64_t total, begin, end;
-  int64_t into;      // units of the first request before it
-  int32_t request;
-  int32_t blocks;    // that have units: each one at least
+  int64_t into;      // weight of the first request, then of the first tile, before it
+  int64_t of_head;   // of the first request
+  int32_t request, head, tile;
+  int32_t blocks;    // that have a range: of 1 at least
 };
 
 // Sums over the block, inclusive; `part` holds a value per warp and one more.
@@ -215,17 +243,25 @@ __device__ __forceinline__ int64_t scan_block(int64_t v, int64_t* part, int64_t*
   return v;
 }
 
+// The range that a block of `blocks` takes.  Neighbouring blocks are on the two dies in
+// turn: the even ones take the first half of the work, the odd ones the second, so
+// that keys and values that several blocks read stay in one die's L2 (8192-token
+// prompt of 16 heads 259 -> 222 us, of 64 heads of 4096 304 -> 260; 24 chunks 134).
+__device__ __forceinline__ int range_of(int block, int blocks) {
+  return (block & 1) * ((blocks + 1) / 2) + block / 2;
+}
+
 // Fills `share` for block `block` of `blocks`; all kThreads threads.
 template <int kRows, int kThreads>
 __device__ void find_share(const AttendParams& p, int block, int blocks, int64_t* part,
                            Share* share) {
   using T = Tiles<kRows>;
-  const auto units = [&](int32_t r) -> int64_t {
-    if (r >= p.requests) return 0;
-    return T::of_head(p, request_of(p, r)) * p.heads;
+  const auto weight = [&](int32_t r) -> int64_t {
+    const Request none{};
+    return T::of_head(p, r < p.requests ? request_of(p, r) : none) * p.heads;
   };
   int64_t own = 0, total;
-  for (int32_t base = 0; base < p.requests; base += kThreads) own += units(base + threadIdx.x);
+  for (int32_t base = 0; base < p.requests; base += kThreads) own += weight(base + threadIdx.x);
   const int64_t first = own;
   scan_block<kThreads>(own, part, &total);
   if (total < blocks) blocks = static_cast<int>(total);
@@ -236,18 +272,37 @@ __device__ void find_share(const AttendParams& p, int block, int blocks, int64_t
     share->total = total;
     share->begin = begin;
     share->end = end;
-    share->request = p.requests;
-    share->into = 0;
   }
-  int64_t before = 0;
-  for (int32_t base = 0; begin < end && base < p.requests && before <= begin; base += kThreads) {
+  if (begin >= end) {
+    __syncthreads();
+    return;
+  }
+  int64_t before = 0, all;
+  for (int32_t base = 0; base < p.requests && before <= begin; base += kThreads) {
     const int32_t r = base + threadIdx.x;
-    const int64_t n = p.requests <= kThreads ? first : units(r);
-    int64_t all;
+    const int64_t n = p.requests <= kThreads ? first : weight(r);
     const int64_t to = before + scan_block<kThreads>(n, part, &all);
     if (begin < to && begin >= to - n) {
       share->request = r;
       share->into = begin - (to - n);
+      share->of_head = n / p.heads;
+    }
+    before += all;
+  }
+  __syncthreads();
+  const Request r = request_of(p, share->request);
+  const int32_t tiles = T::count(p, r);
+  const int32_t head = static_cast<int32_t>(share->into / share->of_head);
+  const int64_t into = share->into - head * share->of_head;
+  before = 0;
+  for (int32_t base = 0; base < tiles && before <= into; base += kThreads) {
+    const int32_t t = base + threadIdx.x;
+    const int64_t n = t < tiles ? T::weight(p, r, t) : 0;
+    const int64_t to = before + scan_block<kThreads>(n, part, &all);  // (all have read `share`)
+    if (into < to && into >= to - n) {
+      share->head = head;
+      share->tile = t;
+      share->into = into - (to - n);
     }
     before += all;
   }
@@ -262,62 +317,64 @@ struct Segment {
   int32_t from, to, all;
   int32_t keys;      // that the tile's last row sees
   int32_t rows;      // of the tile
-  int64_t end;       // of the tile, in units of all
+  int64_t end;       // of the tile, in the weight of all
 };
 
 template <int kRows>
 struct Walk {
   using T = Tiles<kRows>;
   Request request;
-  int32_t index, head = 0, tile = 0, unit = 0, tiles = 0;
+  int32_t index, head, tile, tiles;
+  int32_t into;      // weight of the tile before `at`
   int64_t at, end;
 
-  __device__ Walk(const AttendParams& p, const Share& s)
-      : index(s.request), at(s.begin), end(s.end) {
+  __device__ Walk(const AttendParams& p, const Share& s) : at(s.begin), end(s.end) {
     if (at >= end) return;
+    index = s.request;
+    head = s.head;
+    tile = s.tile;
+    into = static_cast<int32_t>(s.into);
     request = request_of(p, index);
     tiles = T::count(p, request);
-    int64_t into = s.into;
-    const int64_t of_head = T::of_head(p, request);
-    head = static_cast<int32_t>(into / of_head);
-    into -= head * of_head;
-    for (int32_t n = T::units(p, request, 0); into >= n; n = T::units(p, request, tile)) {
-      into -= n;
-      ++tile;
-    }
-    unit = static_cast<int32_t>(into);
   }
   __device__ bool next(const AttendParams& p, Segment* s) {
-    if (at >= end) return false;
-    s->request = request;
-    s->index = index;
-    s->head = head;
-    s->tile = tile;
-    s->keys = T::keys(p, request, tile);
-    s->all = T::units(p, request, tile);
-    const int32_t left = request.tokens * p.group - tile * kRows;
-    s->rows = left < kRows ? left : kRows;
-    s->from = unit;
-    s->to = end - at < s->all - unit ? unit + static_cast<int32_t>(end - at) : s->all;
-    s->end = at - unit + s->all;
-    at += s->to - unit;
-    unit = s->to;
-    if (unit == s->all) {
-      unit = 0;
-      if (++tile == tiles) {
-        tile = 0;
-        if (++head == p.heads) {
-          head = 0;
-          while (at < end && ++index < p.requests) {
-            request = request_of(p, index);
-            if (request.tokens > 0) break;
+    while (at < end) {
+      const int32_t all = T::units(p, request, tile), of_tile = T::kTileWeight + all;
+      const int32_t upto = end - at < of_tile - into ? into + static_cast<int32_t>(end - at) : of_tile;
+      // (the tile's own weight comes before its units)
+      const int32_t from = into > T::kTileWeight ? into - T::kTileWeight : 0;
+      const int32_t to = upto > T::kTileWeight ? upto - T::kTileWeight : 0;
+      s->request = request;
+      s->index = index;
+      s->head = head;
+      s->tile = tile;
+      s->keys = T::keys(p, request, tile);
+      s->all = all;
+      const int32_t left = request.tokens * p.group - tile * kRows;
+      s->rows = left < kRows ? left : kRows;
+      s->from = from;
+      s->to = to;
+      s->end = at - into + of_tile;
+      at += upto - into;
+      into = upto;
+      if (into == of_tile) {
+        into = 0;
+        if (++tile == tiles) {
+          tile = 0;
+          if (++head == p.heads) {
+            head = 0;
+            while (at < end && ++index < p.requests) {
+              request = request_of(p, index);
+              if (request.tokens > 0) break;
+            }
+            if (index >= p.requests) end = at;
+            tiles = T::count(p, request);
           }
-          if (index >= p.requests) end = at;
-          tiles = T::count(p, request);
         }
       }
+      if (from < to) return true;
     }
-    return true;
+    return false;
   }
 };
 
@@ -345,6 +402,22 @@ __device__ __forceinline__ void leave_joint(Joint* joint, const Segment* s, cons
     j.head = s->head;
   }
   *joint = j;
+}
+
+// Host: a launch that may begin, and waits, before the one before it has ended.
+inline int launch_after(void (*kernel)(AttendParams), dim3 grid, int threads, cudaStream_t s,
+                        const AttendParams& p) {
+  cudaLaunchConfig_t config{};
+  config.gridDim = grid;
+  config.blockDim = dim3(static_cast<unsigned>(threads));
+  config.stream = s;
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  config.attrs = &early;
+  config.numAttrs = 1;
+  const cudaError_t before = cudaGetLastError();  // of the launch before
+  return before != cudaSuccess ? before : cudaLaunchKernelEx(&config, kernel, p);
 }
 
 // Query and output of a row: row `row` of a head's rows of a request.

@@ -12,11 +12,14 @@
 // (movmatrix) for O^T = V^T P^T, whose values come transposed from shared memory
 // (ldmatrix).  mma.sync does: at the rate of memory it is idle.
 //
-// e4m3 rows are widened to fp16, which holds them exactly, on their way into
-// the fragments; queries are fp16 too, scaled by a power of two per row (an error of
-// 2^-25 of a row's largest value at most).  A key's exponent goes on its scores; a
-// value's goes into its weight's exponent before the maximum is taken, so that weights
-// stay in range however the rows' exponents lie, and is taken out of the sum again.
+// e4m3 keys are widened to fp16, which holds them exactly, on their way into the
+// fragments; queries are fp16 too, scaled by a power of two per row (an error of
+// 2^-25 of a row's largest value at most).  A key's exponent goes on its scores.
+// Values go to bf16, whose weights have the range that rows of any exponents
+// want: a value's exponent goes on its weight's before a maximum of their own is
+// taken (the sum has the scores' maximum), and its bits, moved to where bf16 has
+// them, are it times 2^-120, which the weights' 2^100 and a product at the end make
+// good.
 //
 // The running maximum moves only where a score passes it by 2^8 (weights are at
 // most 256, which 8 bits of mantissa hold as well as 1): most units then need
@@ -31,9 +34,9 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnitKeys = 64;
 constexpr int kWarpKeys = kUnitKeys / kWarps;
-constexpr int kRingBytes = 24 * 1024;   // of a warp
+constexpr float kLift = 0x1p100f, kDrop = 0x1p20f;   // e4m3: of weights, of sums
 constexpr float kSlack = 8.0f;
-constexpr int kMostPartValues = 4096 + 64;  // floats of a part: rows by values, maxima, sums
+constexpr int kMostPartValues = 4096 + 96;  // floats of a part: rows by values, sums, maxima
 
 __device__ __forceinline__ void ldsm(uint32_t addr, uint32_t (&v)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -99,6 +102,7 @@ struct Form {
   static constexpr int kPieces = kRowBytes / 16;
   static constexpr int kSideBytes = kWarpKeys * kRowBytes;
   static constexpr int kStageBytes = 2 * kSideBytes;
+  static constexpr int kRingBytes = (kE4m3 ? 16 : 24) * 1024;   // of a warp
   static constexpr int kStages = kStageBytes > kRingBytes / 2 ? 3 : kRingBytes / kStageBytes;
   static constexpr int kQueryStride = kDim + 8;      // 16-bit values; eight rows in different banks
   static constexpr int kSumStride = kDim + 4;        // floats, likewise
@@ -107,11 +111,16 @@ struct Form {
   static constexpr int kSumBytes = kWarps * kRows * kSumStride * 4;
   static constexpr int kSmem =
       kQueryBytes + (kWarps * kWarpBytes > kSumBytes ? kWarps * kWarpBytes : kSumBytes);
-  static constexpr int kPartValues = kRows * (kDim + 2);
+  static constexpr int kPartValues = kRows * (kDim + 3);
   static constexpr int kSteps = kDim / 16;
   static constexpr bool kKeep = kSteps * kBlocks <= 16;  // queries' fragments in registers
   static_assert(kPartValues <= kMostPartValues, "a part's place in the workspace");
 };
+
+// 2^(m - most), of maxima; 1 of none.
+__device__ __forceinline__ float since(float m, float most) {
+  return most == minus_infinity() ? 1.0f : exp2_fast(m - most);
+}
 
 // Bytes from a row's start at which its 16-byte piece lies: eight rows' pieces
 // of one place are in different banks.
@@ -125,7 +134,8 @@ struct Shared {
   int64_t part[kWarps + 1];
   float query_scale[32];
   int32_t seen[32];              // keys that a row sees
-  float most[kWarps][32], sum[kWarps][32];
+  // maxima of the values' weights and of the scores (bf16: the same), sums
+  float most[kWarps][32], score[kWarps][32], sum[kWarps][32];
   uint32_t again;                // rows to be computed again
 };
 
@@ -187,7 +197,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
       }
     }
     __syncthreads();
-    float scale[kBlocks][2], top[kBlocks][2], sum[kBlocks][2];
+    float scale[kBlocks][2], top[kBlocks][2], high[kBlocks][2], sum[kBlocks][2];
     int32_t seen[kBlocks][2];
     int32_t least = 0x7FFFFFFF;
 #pragma unroll
@@ -198,7 +208,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
         scale[b][j] = sh.query_scale[r];
         seen[b][j] = sh.seen[r];
         if (r < seg.rows) least = min(least, seen[b][j]);
-        top[b][j] = minus_infinity();
+        top[b][j] = high[b][j] = minus_infinity();
         sum[b][j] = 0.0f;
       }
     least = __reduce_min_sync(0xffffffffu, least);  // all rows see the keys before
@@ -224,6 +234,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
           query(s, b, qf[F::kKeep ? s : 0][F::kKeep ? b : 0][0],
                 qf[F::kKeep ? s : 0][F::kKeep ? b : 0][1]);
     float o[F::kSteps][kBlocks][4] = {};
+    uint32_t odd = 0;        // e4m3: a NaN among the values
 
     // ---- this warp's units
     const int units = seg.to - seg.from;
@@ -325,7 +336,6 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
       }
       // ---- weights: a lane has keys `line` and `line` + 8 of rows 2 column and the next
       const int32_t key = key0 + u * kUnitKeys + line;
-      float back[2] = {1.0f, 1.0f};   // 2^-e of the values
       float shift[2] = {0.0f, 0.0f}, key_scale[2] = {1.0f, 1.0f};
       if (kE4m3) {
 #pragma unroll
@@ -335,7 +345,6 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
           key_scale[j] = scale_of(ke);
           shift[j] = ve == 255 ? __uint_as_float(0x7FC00000u)
                                : static_cast<float>(static_cast<int>(ve) - kExponentBias);
-          back[j] = __uint_as_float((254 - min(ve, 254u)) << 23);
         }
         exponent = exponent_of(u + 1);
       }
@@ -347,23 +356,35 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
         for (int i = 0; i < 4; ++i) {
           const int j = i & 1, k = i >> 1;
           float t = s[b][i] * scale[b][j];
-          if (kE4m3) t = t * key_scale[k] + shift[k];
+          if (kE4m3) t *= key_scale[k];
           if (masked && key + 8 * k >= seen[b][j]) t = minus_infinity();
           s[b][i] = t;
-          rises |= t > top[b][j] + kSlack;
+          rises |= t > high[b][j] + kSlack;
+          if (kE4m3) rises |= t + shift[k] > top[b][j] + kSlack;
         }
       if (__any_sync(0xffffffffu, rises)) {
+        const auto over_keys = [](float m) {
+#pragma unroll
+          for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+          return m;
+        };
 #pragma unroll
         for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            float m = fmaxf(s[b][j], s[b][2 + j]);
-#pragma unroll
-            for (int d = 4; d < 32; d <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            m = fmaxf(m, top[b][j]);
-            const float by = m == minus_infinity() ? 1.0f : exp2_fast(top[b][j] - m);
-            top[b][j] = m;
-            sum[b][j] *= by;
+            const float m = fmaxf(over_keys(fmaxf(s[b][j], s[b][2 + j])), high[b][j]);
+            const float less = m == minus_infinity() ? 1.0f : exp2_fast(high[b][j] - m);
+            high[b][j] = m;
+            sum[b][j] *= less;
+            float by = less;
+            if (kE4m3) {
+              const float n =
+                  fmaxf(over_keys(fmaxf(s[b][j] + shift[0], s[b][2 + j] + shift[1])), top[b][j]);
+              by = n == minus_infinity() ? 1.0f : exp2_fast(top[b][j] - n);
+              top[b][j] = n;
+            } else {
+              top[b][j] = m;
+            }
 #pragma unroll
             for (int t = 0; t < F::kSteps; ++t) {
               o[t][b][j] *= by;
@@ -376,15 +397,16 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
       for (int b = 0; b < kBlocks; ++b) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const float base = top[b][i & 1] == minus_infinity() ? 0.0f : top[b][i & 1];
-          const float w = exp2_fast(s[b][i] - base);
-          s[b][i] = w;
-          sum[b][i & 1] += kE4m3 ? w * back[i >> 1] : w;
+          const int j = i & 1;
+          const float w = exp2_fast(s[b][i] - (high[b][j] == minus_infinity() ? 0.0f : high[b][j]));
+          sum[b][j] += w;
+          s[b][i] = kE4m3 ? kLift * exp2_fast(s[b][i] + shift[i >> 1] -
+                                              (top[b][j] == minus_infinity() ? 0.0f : top[b][j]))
+                          : w;
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k)
-          weights[b][k] = transpose(kE4m3 ? pack_half(s[b][2 * k], s[b][2 * k + 1])
-                                          : pack_bf16(s[b][2 * k], s[b][2 * k + 1]));
+          weights[b][k] = transpose(pack_bf16(s[b][2 * k], s[b][2 * k + 1]));
       }
       // ---- sums: 16 values of the heads by 8 rows a block
       if (kE4m3) {
@@ -396,12 +418,17 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
           ldsm_t(values_at + row * F::kRowBytes + piece_at<F::kPieces>(row, step + (lane >> 4)), w);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t lo = __byte_perm(w[2 * h], 0, 0x3120);
-            const uint32_t hi = __byte_perm(w[2 * h + 1], 0, 0x3120);
-            const uint32_t a[4] = {widen<0>(lo), widen<1>(lo), widen<0>(hi), widen<1>(hi)};
+            uint32_t a[4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+              const uint32_t v = w[2 * h + k];
+              odd |= (v & 0x7F7F7F7Fu) + 0x01010101u;
+              a[2 * k] = ((v << 4) & 0x07F007F0u) | ((v << 8) & 0x80008000u);
+              a[2 * k + 1] = ((v >> 4) & 0x07F007F0u) | (v & 0x80008000u);
+            }
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
-              mma<true>(o[step + h][b], a, weights[b][0], weights[b][1]);
+              mma<false>(o[step + h][b], a, weights[b][0], weights[b][1]);
           }
         }
       } else {
@@ -434,13 +461,15 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
         const int r = b * 8 + 2 * column + j;
         if (line == 0) {
           sh.most[warp][r] = top[b][j];
+          sh.score[warp][r] = high[b][j];
           sh.sum[warp][r] = l;
         }
         float* to = sums + (warp * F::kRows + r) * F::kSumStride;
 #pragma unroll
         for (int t = 0; t < F::kSteps; ++t) {
-          to[t * 16 + (kE4m3 ? 2 * line : line)] = o[t][b][j];
-          to[t * 16 + (kE4m3 ? 2 * line + 1 : line + 8)] = o[t][b][2 + j];
+          to[t * 16 + (kE4m3 ? 2 * line : line)] = kE4m3 ? o[t][b][j] * kDrop : o[t][b][j];
+          to[t * 16 + (kE4m3 ? 2 * line + 1 : line + 8)] =
+              kE4m3 ? o[t][b][2 + j] * kDrop : o[t][b][2 + j];
         }
       }
     __syncthreads();
@@ -448,29 +477,33 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
     float* part = parts + (2 * block + (seg.from == 0)) * static_cast<int64_t>(F::kPartValues);
     // rows of different sight: what one does not see may have spoilt its products
     const bool differ = seg.rows > p.group;
+    if (kE4m3 && (odd & 0x80808080u)) atomicOr(&sh.again, 0xFFFFFFFFu >> (32 - seg.rows));
     for (int at = threadIdx.x; at < seg.rows * kDim; at += kThreads) {
       const int r = at / kDim, d = at % kDim;
-      float m = sh.most[0][r];
+      float m = sh.most[0][r], n = sh.score[0][r];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) m = fmaxf(m, sh.most[w][r]);
-      const float base = m == minus_infinity() ? 0.0f : m;
+      for (int w = 1; w < kWarps; ++w) {
+        m = fmaxf(m, sh.most[w][r]);
+        n = fmaxf(n, sh.score[w][r]);
+      }
       float l = 0.0f, v = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float by = exp2_fast(sh.most[w][r] - base);
-        l += sh.sum[w][r] * by;
-        v += sums[(w * F::kRows + r) * F::kSumStride + d] * by;
+        l += sh.sum[w][r] * since(sh.score[w][r], n);
+        v += sums[(w * F::kRows + r) * F::kSumStride + d] * since(sh.most[w][r], m);
       }
       if (differ && !(fabsf(v) + fabsf(l) < __uint_as_float(0x7F800000u)))
         atomicOr(&sh.again, 1u << r);
       if (whole) {
         if (d < p.head_dim)
-          output_row(p, seg.request.first, seg.head, row0 + r)[d] = f32_to_bf16(v * inverse_sum(l));
+          output_row(p, seg.request.first, seg.head, row0 + r)[d] =
+              f32_to_bf16(v * inverse_sum(l) * (kE4m3 ? since(m, n) : 1.0f));
       } else {
-        part[2 * F::kRows + at] = v;
+        part[3 * F::kRows + at] = v;
         if (d == 0) {
           part[r] = m;
           part[F::kRows + r] = l;
+          part[2 * F::kRows + r] = n;
         }
       }
     }
@@ -490,10 +523,10 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
         if (whole)
           out[d] = f32_to_bf16(own.o[i] * inverse_sum(own.sum));
         else
-          part[2 * F::kRows + r * kDim + d] = own.o[i];
+          part[3 * F::kRows + r * kDim + d] = own.o[i];
       }
       if (!whole && lane == 0) {
-        part[r] = own.most;
+        part[r] = part[2 * F::kRows + r] = own.most;
         part[F::kRows + r] = own.sum;
       }
     }
@@ -512,6 +545,7 @@ template <int kDim, int kBlocks>
 __global__ void __launch_bounds__(kThreads) k_attend_join(const AttendParams p) {
   using F = Form<kDim, kBlocks, false>;
   const int blocks = p.blocks, block = blockIdx.x;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Joint j = reinterpret_cast<const Joint*>(p.workspace)[block];
   const float* parts =
       reinterpret_cast<const float*>(reinterpret_cast<const Joint*>(p.workspace) + blocks);
@@ -521,19 +555,20 @@ __global__ void __launch_bounds__(kThreads) k_attend_join(const AttendParams p) 
   if (j.parts > 0) {
     for (int at = threadIdx.x; at < j.rows * kDim; at += kThreads) {
       const int r = at / kDim, d = at % kDim;
-      float m = minus_infinity(), l = 0.0f, v = 0.0f;
+      float m = minus_infinity(), n = m, l = 0.0f, v = 0.0f;
+#pragma unroll 4
+      for (int i = 0; i < j.parts; ++i) {
+        m = fmaxf(m, part(i)[r]);
+        n = fmaxf(n, part(i)[2 * F::kRows + r]);
+      }
+#pragma unroll 4
       for (int i = 0; i < j.parts; ++i) {
         const float* from = part(i);
-        const float top = from[r];
-        const float most = fmaxf(m, top);
-        const float base = most == minus_infinity() ? 0.0f : most;
-        const float old = exp2_fast(m - base), by = exp2_fast(top - base);
-        l = l * old + from[F::kRows + r] * by;
-        v = v * old + from[2 * F::kRows + at] * by;
-        m = most;
+        l += from[F::kRows + r] * since(from[2 * F::kRows + r], n);
+        v += from[3 * F::kRows + at] * since(from[r], m);
       }
       if (d < p.head_dim)
-        output_row(p, j.first, j.head, j.row + r)[d] = f32_to_bf16(v * inverse_sum(l));
+        output_row(p, j.first, j.head, j.row + r)[d] = f32_to_bf16(v * inverse_sum(l) * since(m, n));
     }
   }
   const int64_t width = static_cast<int64_t>(p.heads) * p.group * p.head_dim;
@@ -549,8 +584,8 @@ int launch_at(const AttendParams& p, cudaStream_t s) {
   const cudaError_t err = allow_shared<k_attend_split<kDim, kBlocks, kE4m3>>(F::kSmem);
   if (err != cudaSuccess) return err;
   k_attend_split<kDim, kBlocks, kE4m3><<<p.blocks, kThreads, F::kSmem, s>>>(p);
-  k_attend_join<kDim, kBlocks><<<p.blocks, kThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(k_attend_join<kDim, kBlocks>, dim3(static_cast<unsigned>(p.blocks)), kThreads,
+                      s, p);
 }
 
 template <int kDim, int kBlocks>

@@ -13,6 +13,9 @@
 // then by the row's own thread.  While one half's weights are made, the other
 // half's products run: S0 S1 | O0 S0' O1 S1' | ...
 //
+// e4m3 pages come by TMA as they are; four warps more widen them to bf16, which
+// holds every row times its power of two exactly, into the ring's stages.
+//
 // A tile's last keys may lie in a page with others behind them, which hold
 // anything: those values are cleared in shared memory before the products.  What a row
 // does not see inside a unit has weight 0; where it is infinite or NaN the row is
@@ -32,27 +35,35 @@ constexpr int kSoftmaxWarps = 8;
 constexpr int kMultiplyWarp = kSoftmaxWarps;
 constexpr int kLoadWarp = kSoftmaxWarps + 1;    // keys, and the next warp values
 constexpr int kQueryWarp = kSoftmaxWarps + 3;
-// Three groups of four warps, of 168 registers a thread at launch, 64512: 200 for
-// the two that hold a row's scores, 104 for the third, 64512.
-constexpr int kThreads = 32 * (kSoftmaxWarps + 4);
+constexpr int kWidenWarp = kSoftmaxWarps + 4;   // e4m3: four
 constexpr float kSlack = 8.0f;
 constexpr uint64_t kLandNs = 100000000;  // limit for what is under way when a wait ran out
 constexpr int kMostStages = 8;
 constexpr int kTmemColumns = 512;       // S0 S1 O0 O1, 128 each
 constexpr int kJoinColumns = 16;        // of a block of the launch that joins
 
-template <int kDim>
+// Registers a thread: bf16 has three groups of four warps, 168 at launch, 64512 in
+// all: 200 for the two that hold a row's scores, 104 for the third, 64512.  e4m3
+// has four groups, 128 at launch, 65536: 176, 176, 80 and 80, 65536.
+template <int kDim, bool kE4m3 = false>
 struct Form {
+  static constexpr int kThreads = 32 * (kSoftmaxWarps + (kE4m3 ? 8 : 4));
   static constexpr int kHalves = kDim / 64;                       // columns of 64 values
   static constexpr int kTileBytes = kHalves * kKeys * kRowBytes;  // a stage; half the queries
-  static constexpr int kStages = kDim == 128 ? 5 : 8;
-  static constexpr int kSmem = (2 + kStages) * kTileBytes + 1024;
-  static constexpr int kPartValues = kTileRows * (kDim + 2);
+  static constexpr int kStages = kDim == 128 ? kE4m3 ? 4 : 5 : 8;
+  static constexpr int kRawBytes = kKeys * kDim;                  // e4m3: as loaded
+  static constexpr int kRaw = kE4m3 ? 2 : 0;
+  static constexpr int kSlots = kE4m3 ? kRaw : kStages;           // that TMA fills
+  static constexpr int kSmem = (2 + kStages) * kTileBytes + kRaw * kRawBytes + 1024;
 };
+template <int kDim>
+constexpr int64_t kPartValues = kTileRows * (kDim + 2);
 
 struct Shared {
   uint64_t full[kMostStages];
   uint64_t empty[kMostStages];
+  uint64_t raw_full[2];    // e4m3
+  uint64_t raw_empty[2];
   uint64_t queries[2];     // a half's queries are in shared memory
   uint64_t asked[2];       // and have been read for the last time
   uint64_t scores[2];      // its scores are in TMEM
@@ -65,7 +76,7 @@ struct Shared {
   uint32_t busy;           // warps that compute rows again: nobody's wait runs out meanwhile
   int32_t issued;          // loads
   Share share;
-  int64_t part[kThreads / 32 + 1];
+  int64_t part[kSoftmaxWarps + 9];
 };
 
 // Bounded wait of a whole warp; false, for all its lanes, when it ran out here
@@ -242,11 +253,15 @@ struct Maps {
 // Two warps: keys and values by TMA, stages in turn.  A lane per box: it looks up
 // the page, a unit ahead, and issues the box's loads.  (One warp for both: with
 // pages of 16 its 32 loads a unit took as long as the products.)
-template <int kDim>
+template <int kDim, bool kE4m3>
 __device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32_t ring, int side) {
-  using F = Form<kDim>;
+  using F = Form<kDim, kE4m3>;
+  constexpr int kSlots = F::kSlots, kBytes = kE4m3 ? F::kRawBytes : F::kTileBytes;
+  constexpr int kLine = kE4m3 ? kDim : kRowBytes;    // of a box
+  uint64_t* const full = kE4m3 ? sh.raw_full : sh.full;
+  uint64_t* const empty = kE4m3 ? sh.raw_empty : sh.empty;
   const int lane = threadIdx.x & 31;
-  const int columns = (p.head_dim + 63) / 64;
+  const int columns = kE4m3 ? 1 : (p.head_dim + 63) / 64;
   const CUtensorMap* map = side ? &maps.value : &maps.key;
   Walk<kTileRows> walk(p, sh.share);
   Segment s;
@@ -268,27 +283,115 @@ __device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32
     for (int u = 0; u < halves.most; ++u, at += 2) {
       const int32_t left = s.keys - (s.from + u) * p.unit_keys;
       const int boxes = maps.by_box.up(left < p.unit_keys ? left : p.unit_keys);
-      const int stage = at % F::kStages;
-      uint64_t* full = &sh.full[stage];
-      alive = wait(p, sh, &sh.empty[stage], ((at / F::kStages) & 1) ^ 1);
+      const int slot = at % kSlots;
+      alive = wait(p, sh, &empty[slot], ((at / kSlots) & 1) ^ 1);
       if (!alive) break;
       if (lane == 0)
-        mbar_arrive_expect_tx(full, static_cast<uint32_t>(boxes * columns * maps.box * kRowBytes));
+        mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(boxes * columns * maps.box * kLine));
       __syncwarp();
       if (lane < boxes) {
-        const uint32_t to = ring + stage * F::kTileBytes + lane * maps.box * kRowBytes;
+        const uint32_t to = ring + slot * kBytes + lane * maps.box * kLine;
         for (int c = 0; c < columns; ++c)
-          tma_4d(to + c * kKeys * kRowBytes, map, c * 64, place, s.head, page, full);
+          tma_4d(to + c * kKeys * kRowBytes, map, c * 64, place, s.head, page, &full[slot]);
       }
       look(u + 1, &page, &place);
     }
   }
-  // What is under way writes this block's shared memory: the products have read
-  // it, or after a wait that ran out it is seen to land (settle).
-  const int first = at - 2 * F::kStages;
+  // What is under way writes this block's shared memory: it has been read, or after
+  // a wait that ran out it is seen to land (settle).
+  const int first = at - 2 * kSlots;
   for (int i = first < side ? side : first; alive && i < at; i += 2)
-    if (i >= at - F::kStages) alive = wait(p, sh, &sh.empty[i % F::kStages], (i / F::kStages) & 1);
+    if (i >= at - kSlots) alive = wait(p, sh, &empty[i % kSlots], (i / kSlots) & 1);
   if (lane == 0) atomicMax(&sh.issued, at - 1);
+}
+
+// ------------------------------------------------------------------------
+// Four warps, e4m3: rows as loaded to bf16, times their powers of two, where the
+// 128-byte swizzle has them; zeros behind the tile's last key.  A warp takes 32
+// rows of a tile, a lane 16 values of four rows in turn and the exponent of one row,
+// fetched a stage ahead.  A value's bits, moved to where bf16 has them, are it
+// times 2^-120, subnormal ones too; a product with 2^120 times the row's power
+// (or with either, where that is out of range) sets it right, exactly.
+__device__ __forceinline__ uint32_t times_bf16(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+template <int kDim>
+__device__ void widen(const AttendParams& p, Shared& sh, unsigned char* ring, unsigned char* raw,
+                      int warp) {
+  using F = Form<kDim, true>;
+  constexpr int kPieces = kDim / 16, kAtOnce = 32 / kPieces;   // of a row; rows
+  constexpr uint32_t kRange = 134;         // highest exponent whose power times 2^120 bf16 holds
+  const int lane = threadIdx.x & 31, piece = lane % kPieces;
+  Walk<kTileRows> walk(p, sh.share);
+  Segment s;
+  int at = 0;
+  while (walk.next(p, &s)) {
+    const Halves h(p, s);
+    // of this lane's row; 256: none, zeros
+    const auto exponent = [&](int load) -> uint32_t {
+      const int unit = load >> 1;
+      const int32_t row = warp * 32 + lane, key = (s.from + unit) * p.unit_keys + row;
+      if (unit >= h.most || row >= p.unit_keys || key >= s.keys) return 256;
+      const int32_t index = p.by_page(key), page = page_at(p, s.index, index);
+      if (page < 0) return 256;
+      const int32_t place = key - index * p.page_size;
+      const Side& side = load & 1 ? p.value : p.key;
+      return side.exponent[page * side.exponent_stride[0] + place * side.exponent_stride[1] +
+                           s.head * side.exponent_stride[2]];
+    };
+    uint32_t next = exponent(0);
+    for (int load = 0; load < 2 * h.most; ++load, ++at) {
+      const uint32_t own = next;
+      next = exponent(load + 1);
+      const bool in_range = __all_sync(0xffffffffu, own <= kRange || own >= 255);
+      const int slot = at % F::kRaw, stage = at % F::kStages;
+      if (!wait(p, sh, &sh.raw_full[slot], (at / F::kRaw) & 1)) return;
+      if (!wait(p, sh, &sh.empty[stage], ((at / F::kStages) & 1) ^ 1)) return;
+      const unsigned char* from = raw + slot * F::kRawBytes + warp * 32 * kDim;
+      unsigned char* to = ring + stage * F::kTileBytes;
+#pragma unroll 4
+      for (int i = 0; i < 32 / kAtOnce; ++i) {
+        const int r = i * kAtOnce + lane / kPieces, row = warp * 32 + r;
+        const uint32_t e = __shfl_sync(0xffffffffu, own, r);
+        const uint4 w = *reinterpret_cast<const uint4*>(from + r * kDim + piece * 16);
+        const uint32_t words[4] = {w.x, w.y, w.z, w.w};
+        // 2^120 times the row's power, or 2^120 and the row's power
+        uint32_t by = e >= 255 ? 0x7FC0u : in_range ? (e + 120) << 7 : 247u << 7;
+        by |= by << 16;
+        uint32_t again = e >= 255 ? 0x7FC0u : e ? e << 7 : 0x40u;
+        again |= again << 16;
+        uint32_t out[8], odd = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) odd |= (words[j] & 0x7F7F7F7Fu) + 0x01010101u;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t x = __byte_perm(words[j / 2], 0, j & 1 ? 0x3424 : 0x1404);
+          uint32_t v = times_bf16((x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), by);
+          if (!in_range) v = times_bf16(v, again);
+          if (odd & 0x80808080u) {  // 0x7F and 0xFF are NaN
+            if ((x & 0x7F00u) == 0x7F00u) v |= 0x7FC0u;
+            if ((x & 0x7F000000u) == 0x7F000000u) v |= 0x7FC00000u;
+          }
+          out[j] = e == 256 ? 0u : v;
+        }
+        unsigned char* line = to + (piece / 4) * kKeys * kRowBytes + row * kRowBytes;
+        const int first = 2 * (piece & 3);
+        *reinterpret_cast<uint4*>(line + ((first ^ (row & 7)) << 4)) =
+            make_uint4(out[0], out[1], out[2], out[3]);
+        *reinterpret_cast<uint4*>(line + (((first + 1) ^ (row & 7)) << 4)) =
+            make_uint4(out[4], out[5], out[6], out[7]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sh.raw_empty[slot]);
+        mbar_arrive(&sh.full[stage]);
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------------------
@@ -296,9 +399,9 @@ __device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32
 // counts (65 cycles a product): the loops are unrolled, the operands' addresses
 // differ by constants, and what has long been there is waited for ahead.
 // (Loops with the whole warp: 85 to 120 cycles a product, 230 a wait.)
-template <int kDim>
+template <int kDim, bool kE4m3>
 __device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, uint32_t ring) {
-  using F = Form<kDim>;
+  using F = Form<kDim, kE4m3>;
   if (!one_lane()) return;
   constexpr int kSteps = kDim / 16;
   const int steps = (p.head_dim + 15) / 16;               // of S
@@ -349,7 +452,7 @@ __device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, ui
       const int value = taken % F::kStages;                  // this unit's values
       const int next = (taken + 1) % F::kStages;             // the next one's keys
       const bool goes_on = u + 1 < h.most;
-      if (s.keys - (s.from + u) * p.unit_keys < p.unit_keys) {
+      if (!kE4m3 && s.keys - (s.from + u) * p.unit_keys < p.unit_keys) {
         if (!wait_on(p, sh, &sh.cleared, clear_parity)) return;
         clear_parity ^= 1;
       } else if (!full(taken)) {
@@ -419,10 +522,10 @@ __device__ __forceinline__ void copy_queries(const AttendParams& p, const Segmen
                : "memory");
 }
 
-template <int kDim>
+template <int kDim, bool kE4m3>
 __device__ void ask(const AttendParams& p, const Maps& maps, Shared& sh, uint32_t queries,
                     unsigned char* ring_ptr) {
-  using F = Form<kDim>;
+  using F = Form<kDim, kE4m3>;
   const int lane = threadIdx.x & 31;
   const int columns = (p.head_dim + 63) / 64;
   Walk<kTileRows> walk(p, sh.share);
@@ -455,7 +558,7 @@ __device__ void ask(const AttendParams& p, const Maps& maps, Shared& sh, uint32_
       ++tiles[t];
     }
     const int32_t left = s.keys - (s.from + h.most - 1) * p.unit_keys;
-    if (alive && h.most > 0 && left < p.unit_keys) {
+    if (!kE4m3 && alive && h.most > 0 && left < p.unit_keys) {
       // its last values' stage is in its last phase
       const int stage = (loaded - 1) % F::kStages;
       alive = wait(p, sh, &sh.full[stage], ((loaded - 1) / F::kStages) & 1);
@@ -492,7 +595,7 @@ __device__ void soften(const AttendParams& p, Shared& sh, int t) {
   const int lane = threadIdx.x & 31, tid = threadIdx.x & (kHalf - 1), warp = tid >> 5;
   const uint32_t lanes = static_cast<uint32_t>(warp * 32) << 16;
   const uint32_t score_at = sh.tmem + lanes + t * kHalf, out_at = score_at + 2 * kHalf;
-  const int block = blockIdx.x;
+  const int block = range_of(blockIdx.x, gridDim.x);
   float* parts = reinterpret_cast<float*>(reinterpret_cast<Joint*>(p.workspace) + gridDim.x);
   const float scale = p.scale * kLog2e;
   const bool at_once =
@@ -577,7 +680,7 @@ __device__ void soften(const AttendParams& p, Shared& sh, int t) {
     }
     // ---- output, or this block's part of it
     const bool whole = s.from == 0 && s.to == s.all;
-    float* part = parts + (2 * block + (s.from == 0)) * static_cast<int64_t>(F::kPartValues) +
+    float* part = parts + (2 * block + (s.from == 0)) * kPartValues<kDim> +
                   t * kHalf + tid;
     const bool live = tid < rows;
     uint16_t* out = live ? output_row(p, s.request.first, s.head, row0 + tid) : nullptr;
@@ -654,26 +757,30 @@ __device__ void announce(const AttendParams& p, const Shared& sh) {
   Segment s{};
   bool goes_on = false;
   while (walk.next(p, &s)) goes_on = s.from == 0 && s.to < s.all;
-  leave_joint(reinterpret_cast<Joint*>(p.workspace) + blockIdx.x, goes_on ? &s : nullptr, sh.share,
-              s.tile * kTileRows, blockIdx.x);
+  const int block = range_of(blockIdx.x, gridDim.x);
+  leave_joint(reinterpret_cast<Joint*>(p.workspace) + block, goes_on ? &s : nullptr, sh.share,
+              s.tile * kTileRows, block);
 }
 
-template <int kDim>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int kDim, bool kE4m3>
+__global__ void __launch_bounds__(Form<kDim, kE4m3>::kThreads, 1)
     k_attend_wide(const AttendParams p, const __grid_constant__ Maps maps) {
-  using F = Form<kDim>;
+  using F = Form<kDim, kE4m3>;
+  constexpr int kThreads = F::kThreads;
   extern __shared__ unsigned char raw[];
   __shared__ Shared sh;
   const uint32_t base = smem_addr(raw);
   const uint32_t queries = (base + 1023) & ~1023u, ring = queries + 2 * F::kTileBytes;
   unsigned char* ring_ptr = raw + (ring - base);
-  const int warp = threadIdx.x >> 5, blocks = gridDim.x, block = blockIdx.x;
+  const int warp = threadIdx.x >> 5, blocks = gridDim.x;
   if (threadIdx.x == 0) {
     for (int i = 0; i < F::kStages; ++i) {
-      mbar_init(&sh.full[i], 1);
+      mbar_init(&sh.full[i], kE4m3 ? 4 : 1);
       mbar_init(&sh.empty[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh.raw_full[t], 1);
+      mbar_init(&sh.raw_empty[t], 4);
       mbar_init(&sh.queries[t], maps.query_box ? 1 : 32);
       mbar_init(&sh.asked[t], 1);
       mbar_init(&sh.scores[t], 1);
@@ -700,20 +807,29 @@ __global__ void __launch_bounds__(kThreads, 1)
   for (int i = threadIdx.x; i < F::kStages * F::kTileBytes / 16; i += kThreads)
     reinterpret_cast<uint4*>(ring_ptr)[i] = make_uint4(0, 0, 0, 0);
   fence_proxy_async_smem();
-  find_share<kTileRows, kThreads>(p, block, blocks, sh.part, &sh.share);
+  find_share<kTileRows, kThreads>(p, range_of(blockIdx.x, blocks), blocks, sh.part, &sh.share);
   __syncthreads();
   tc_fence_after();
+  const uint32_t raw_at = ring + F::kStages * F::kTileBytes;
   if (warp < kSoftmaxWarps) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if (kE4m3)
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     soften<kDim>(p, sh, warp / 4);
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-    if (warp == kMultiplyWarp)
-      multiply<kDim>(p, sh, queries, ring);
-    else if (warp < kQueryWarp)
-      load<kDim>(p, maps, sh, ring, warp - kLoadWarp);
+    if (kE4m3)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
     else
-      ask<kDim>(p, maps, sh, queries, ring_ptr);
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+    if (warp == kMultiplyWarp)
+      multiply<kDim, kE4m3>(p, sh, queries, ring);
+    else if (warp < kQueryWarp)
+      load<kDim, kE4m3>(p, maps, sh, kE4m3 ? raw_at : ring, warp - kLoadWarp);
+    else if (warp == kQueryWarp)
+      ask<kDim, kE4m3>(p, maps, sh, queries, ring_ptr);
+    else if constexpr (kE4m3)
+      widen<kDim>(p, sh, ring_ptr, ring_ptr + F::kStages * F::kTileBytes, warp - kWidenWarp);
     if (warp == kQueryWarp && one_lane()) announce(p, sh);
   }
   tc_fence_before();
@@ -724,8 +840,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       commit(&sh.drain);
       mbar_wait_bounded(&sh.drain, 0, kLandNs);
     } else if (warp == kLoadWarp) {
-      for (int i = sh.issued > F::kStages ? sh.issued - F::kStages : 0; i < sh.issued; ++i)
-        if (!mbar_wait_bounded(&sh.full[i % F::kStages], (i / F::kStages) & 1, kLandNs)) break;
+      uint64_t* const full = kE4m3 ? sh.raw_full : sh.full;
+      for (int i = sh.issued > F::kSlots ? sh.issued - F::kSlots : 0; i < sh.issued; ++i)
+        if (!mbar_wait_bounded(&full[i % F::kSlots], (i / F::kSlots) & 1, kLandNs)) break;
     }
     __syncthreads();
   }
@@ -737,29 +854,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // Joins a tile's parts, a thread a row, kJoinColumns of its values; rows behind
-// the last request become zeros.
+// the last request become zeros.  The parts' weights come first, so that what they
+// weigh is read without waiting (one after the other: 21 us for 152 parted tiles).
 template <int kDim>
 __global__ void __launch_bounds__(kTileRows) k_attend_wide_join(const AttendParams p) {
-  using F = Form<kDim>;
   const int blocks = gridDim.x, block = blockIdx.x, row = threadIdx.x;
   const int c0 = blockIdx.y * kJoinColumns;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Joint j = reinterpret_cast<const Joint*>(p.workspace)[block];
   const float* parts =
       reinterpret_cast<const float*>(reinterpret_cast<const Joint*>(p.workspace) + blocks);
   if (row < j.rows && j.parts > 0) {
-    float m = minus_infinity(), l = 0.0f, v[kJoinColumns] = {};
+    const float* from = parts + (2 * block + 1) * kPartValues<kDim> + row;
+    const auto part = [&](int i) {  // the block's own slot 1, then the others' slots 0
+      return from + (2 * i - (i > 0)) * kPartValues<kDim>;
+    };
+    float m = minus_infinity();
+#pragma unroll 4
+    for (int i = 0; i < j.parts; ++i) m = fmaxf(m, part(i)[0]);
+    const float base = m == minus_infinity() ? 0.0f : m;
+    float l = 0.0f, v[kJoinColumns] = {};
+#pragma unroll 2
     for (int i = 0; i < j.parts; ++i) {
-      const float* from =
-          parts + (2 * (block + i) + (i == 0)) * static_cast<int64_t>(F::kPartValues) + row;
-      const float top = from[0];
-      if (top == minus_infinity()) continue;   // none of its keys seen, and no sums left
-      const float most = fmaxf(m, top);
-      const float old = exp2_fast(m - most), by = exp2_fast(top - most);
-      l = l * old + from[kTileRows] * by;
+      const float* at = part(i);
+      const float top = at[0];
+      // of none of its keys seen: no sums were left
+      if (top == minus_infinity()) continue;
+      const float by = exp2_fast(top - base);
+      l += at[kTileRows] * by;
 #pragma unroll
       for (int c = 0; c < kJoinColumns; ++c)
-        if (c0 + c < p.head_dim) v[c] = v[c] * old + from[(2 + c0 + c) * kTileRows] * by;
-      m = most;
+        if (c0 + c < p.head_dim) v[c] += at[(2 + c0 + c) * kTileRows] * by;
     }
     const float by = inverse_sum(l);
     uint16_t* out = output_row(p, j.first, j.head, j.row + row) + c0;
@@ -782,52 +907,56 @@ __global__ void __launch_bounds__(kTileRows) k_attend_wide_join(const AttendPara
 // ------------------------------------------------------------------------
 // Host
 
-// Of rows of head_dim values, n[i] of them at[i] elements apart; boxes of 64 values.
-bool make_map(CUtensorMap* map, const void* data, const AttendParams& p, const int64_t (&n)[3],
-              const int64_t (&at)[3], const int (&box)[3]) {
+// Of rows of head_dim values, n[i] of them at[i] elements apart; boxes of `wide`
+// values (bf16: 64, swizzled).
+bool make_map(CUtensorMap* map, const void* data, const AttendParams& p, bool e4m3, int wide,
+              const int64_t (&n)[3], const int64_t (&at)[3], const int (&box)[3]) {
+  const int size = e4m3 ? 1 : 2;
   cuuint64_t dims[4] = {static_cast<cuuint64_t>(p.head_dim)}, strides[3];
   for (int i = 0; i < 3; ++i) {
     dims[i + 1] = static_cast<cuuint64_t>(n[i]);
     // (of one: any)
-    strides[i] = static_cast<cuuint64_t>(n[i] > 1 && at[i] > 0 ? 2 * at[i] : 16);
+    strides[i] = static_cast<cuuint64_t>(n[i] > 1 ? size * at[i] : 16);
     if (n[i] > 1 && at[i] <= 0) return false;
   }
-  const cuuint32_t boxes[4] = {64, static_cast<cuuint32_t>(box[0]),
+  const cuuint32_t boxes[4] = {static_cast<cuuint32_t>(wide), static_cast<cuuint32_t>(box[0]),
                                static_cast<cuuint32_t>(box[1]), static_cast<cuuint32_t>(box[2])};
   const cuuint32_t ones[4] = {1, 1, 1, 1};
-  return encode()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(data), dims, strides,
-                  boxes, ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  return encode()(map, e4m3 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                  const_cast<void*>(data), dims, strides, boxes, ones,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  e4m3 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool make_side_map(CUtensorMap* map, const Side& s, const AttendParams& p, int box) {
-  return make_map(map, s.data, p, {p.page_size, p.heads, p.pages},
+bool make_side_map(CUtensorMap* map, const Side& s, const AttendParams& p, int wide, int box) {
+  return make_map(map, s.data, p, p.e4m3, wide, {p.page_size, p.heads, p.pages},
                   {s.stride[1], s.stride[2], s.stride[0]}, {box, 1, 1});
 }
 
-bool on_words(const Side& s) {
-  return (reinterpret_cast<uintptr_t>(s.data) & 15) == 0 && s.stride[0] % 8 == 0 &&
-         s.stride[1] % 8 == 0 && s.stride[2] % 8 == 0;
+bool on_words(const Side& s, int values) {
+  return (reinterpret_cast<uintptr_t>(s.data) & 15) == 0 && s.stride[0] % values == 0 &&
+         s.stride[1] % values == 0 && s.stride[2] % values == 0;
 }
 
-template <int kDim>
+template <int kDim, bool kE4m3>
 int launch_at(const AttendParams& p, const Maps& maps, cudaStream_t s) {
-  using F = Form<kDim>;
-  const cudaError_t err = allow_shared<k_attend_wide<kDim>>(F::kSmem);
+  using F = Form<kDim, kE4m3>;
+  const cudaError_t err = allow_shared<k_attend_wide<kDim, kE4m3>>(F::kSmem);
   if (err != cudaSuccess) return err;
-  k_attend_wide<kDim><<<p.blocks, kThreads, F::kSmem, s>>>(p, maps);
+  k_attend_wide<kDim, kE4m3><<<p.blocks, F::kThreads, F::kSmem, s>>>(p, maps);
   const dim3 grid(static_cast<unsigned>(p.blocks),
                   static_cast<unsigned>((p.head_dim + kJoinColumns - 1) / kJoinColumns));
-  k_attend_wide_join<kDim><<<grid, kTileRows, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(k_attend_wide_join<kDim>, grid, kTileRows, s, p);
 }
 
-// bf16 pages of whole eights of keys, whose rows are 16-byte words, as queries
-// and outputs are.
+// Pages of whole eights of keys, whose rows are 16-byte words, as queries and
+// outputs are.
 bool wide_takes(const AttendParams& p) {
-  return !p.e4m3 && p.head_dim <= 128 && p.head_dim % 8 == 0 && p.page_size % 8 == 0 &&
-         p.pages > 0 && p.scale > 0.0f && on_words(p.key) && on_words(p.value) &&
+  const int values = p.e4m3 ? 16 : 8;
+  return p.head_dim <= 128 && p.head_dim % values == 0 && p.page_size % 8 == 0 && p.pages > 0 &&
+         p.scale > 0.0f && on_words(p.key, values) && on_words(p.value, values) &&
          (reinterpret_cast<uintptr_t>(p.q) & 15) == 0 && p.q_token % 8 == 0 && p.q_head % 8 == 0 &&
          (reinterpret_cast<uintptr_t>(p.o) & 15) == 0 && encode();
 }
@@ -835,7 +964,7 @@ bool wide_takes(const AttendParams& p) {
 }  // namespace
 
 int64_t wide_workspace_bytes(int sms) {
-  return static_cast<int64_t>(sms) * (sizeof(Joint) + 2 * 4 * Form<128>::kPartValues);
+  return static_cast<int64_t>(sms) * (sizeof(Joint) + 2 * 4 * kPartValues<128>);
 }
 
 bool launch_attend_wide(const AttendParams& given, void* stream, int* status) {
@@ -848,18 +977,22 @@ bool launch_attend_wide(const AttendParams& given, void* stream, int* status) {
   p.unit_keys = kKeys / maps.box * maps.box;
   maps.by_box = Divide(maps.box);
   p.by_unit = Divide(p.unit_keys);
-  if (!make_side_map(&maps.key, p.key, p, maps.box) ||
-      !make_side_map(&maps.value, p.value, p, maps.box))
+  const int wide = !p.e4m3 ? 64 : p.head_dim <= 64 ? 64 : 128;
+  if (!make_side_map(&maps.key, p.key, p, wide, maps.box) ||
+      !make_side_map(&maps.value, p.value, p, wide, maps.box))
     return false;
   maps.query_box = kHalf % p.group ? 0 : kHalf / p.group;
   if (!maps.query_box ||
-      !make_map(&maps.query, p.q, p, {p.group, p.heads, p.tokens},
+      !make_map(&maps.query, p.q, p, false, 64, {p.group, p.heads, p.tokens},
                 {p.q_head, p.q_head * p.group, p.q_token}, {p.group, 1, maps.query_box})) {
     maps.query_box = 0;
     maps.query = maps.key;  // not used
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  *status = p.head_dim <= 64 ? launch_at<64>(p, maps, s) : launch_at<128>(p, maps, s);
+  if (p.e4m3)
+    *status = p.head_dim <= 64 ? launch_at<64, true>(p, maps, s) : launch_at<128, true>(p, maps, s);
+  else
+    *status = p.head_dim <= 64 ? launch_at<64, false>(p, maps, s) : launch_at<128, false>(p, maps, s);
   return true;
 }
 

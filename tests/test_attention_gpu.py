@@ -160,6 +160,35 @@ def test_values_out_of_sight_have_no_part(new, page, dim, q_heads, bad):
     assert torch.isfinite(got[:, :q_heads // 2]).all() and torch.isfinite(got[new:]).all()
 
 
+@pytest.mark.parametrize("new,page,dim", [(1, 16, 128), (3, 20, 64), (200, 16, 128), (200, 24, 64)])
+def test_rows_of_any_exponent(new, page, dim):
+    """Powers of two from the lowest to the highest, zeros, and NaN by exponent and by
+    value, on keys and on values."""
+    L, heads = new + 260, 2
+    cache, table = ref.paged([L], page, heads, dim, e4m3=True)
+    at = torch.arange(L, device="cuda")
+    slot = table[0].long()[at // page], at % page
+    e = torch.randint(27, 135, (L, heads), generator=torch.Generator().manual_seed(1)).cuda()
+    e[::5] = torch.randint(120, 130, (len(e[::5]), heads)).cuda()
+    e[7], e[11] = 0, 245                     # of which only the values are small
+    small = cache.value.view(torch.uint8)
+    small[slot[0][11], slot[1][11]] = 0
+    cache.value_exponent[slot] = e.to(torch.uint8)
+    k = torch.full((L, heads), 121, dtype=torch.uint8, device="cuda")
+    k[::9], k[3] = 27, 0
+    cache.key_exponent[slot] = k
+    q = rand(new, 4, dim, seed=4)
+    off, context = ints([0, new]), ints([L])
+    got = attention.attend(q, cache, table, off, context)
+    ref.check_attend(got, q, cache, table, off, context)
+    cache.value_exponent[slot[0][L - 1], slot[1][L - 1], 0] = 255      # the last row alone sees it
+    small[slot[0][L - 1], slot[1][L - 1], 1, 5] = 0xFF
+    got = attention.attend(q, cache, table, off, context)
+    ref.check_attend(got, q, cache, table, off, context)
+    assert torch.isnan(got[-1, :2]).all() and torch.isnan(got[-1, 2:, 5]).all()
+    assert torch.isfinite(got[:-1]).all()
+
+
 @pytest.mark.parametrize("e4m3", [False, True])
 def test_scores_that_rise_and_fall(e4m3):
     """Maxima that grow from tile to tile, by much and by little, and fall."""
