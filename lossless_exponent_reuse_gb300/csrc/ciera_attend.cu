@@ -58,7 +58,6 @@ int launch_attend(const AttendParams& given, void* stream) {
   int status = cudaSuccess;
   p.blocks = sm_count();
   if (p.longest * p.group > kFewRows && launch_attend_wide(p, stream, &status)) return status;
-  p.blocks *= 2;
   if (launch_attend_split(p, stream, &status)) return status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = static_cast<int64_t>(p.tokens) * p.heads * p.group;

@@ -17,9 +17,7 @@
 // 2^-25 of a row's largest value at most).  A key's exponent goes on its scores.
 // Values go to bf16, whose weights have the range that rows of any exponents
 // want: a value's exponent goes on its weight's before a maximum of their own is
-// taken (the sum has the scores' maximum), and its bits, moved to where bf16 has
-// them, are it times 2^-120, which the weights' 2^100 and a product at the end make
-// good.
+// taken (the sum has the scores' maximum).
 //
 // The running maximum moves only where a score passes it by 2^8 (weights are at
 // most 256, which 8 bits of mantissa hold as well as 1): most units then need
@@ -34,8 +32,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kUnitKeys = 64;
 constexpr int kWarpKeys = kUnitKeys / kWarps;
-constexpr float kLift = 0x1p100f, kDrop = 0x1p20f;   // e4m3: of weights, of sums
 constexpr float kSlack = 8.0f;
+constexpr int kMostPerSm = 3;
 constexpr int kMostPartValues = 4096 + 96;  // floats of a part: rows by values, sums, maxima
 
 __device__ __forceinline__ void ldsm(uint32_t addr, uint32_t (&v)[4]) {
@@ -111,6 +109,9 @@ struct Form {
   static constexpr int kSumBytes = kWarps * kRows * kSumStride * 4;
   static constexpr int kSmem =
       kQueryBytes + (kWarps * kWarpBytes > kSumBytes ? kWarps * kWarpBytes : kSumBytes);
+  // blocks of an SM: what shared memory and registers hold (64 requests of 8-bit pages
+  // in two blocks 268 us, in three 224)
+  static constexpr int kPerSm = kDim > 128 ? 1 : kE4m3 && kBlocks == 1 ? kMostPerSm : 2;
   static constexpr int kPartValues = kRows * (kDim + 3);
   static constexpr int kSteps = kDim / 16;
   static constexpr bool kKeep = kSteps * kBlocks <= 16;  // queries' fragments in registers
@@ -234,7 +235,6 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
           query(s, b, qf[F::kKeep ? s : 0][F::kKeep ? b : 0][0],
                 qf[F::kKeep ? s : 0][F::kKeep ? b : 0][1]);
     float o[F::kSteps][kBlocks][4] = {};
-    uint32_t odd = 0;        // e4m3: a NaN among the values
 
     // ---- this warp's units
     const int units = seg.to - seg.from;
@@ -400,8 +400,8 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
           const int j = i & 1;
           const float w = exp2_fast(s[b][i] - (high[b][j] == minus_infinity() ? 0.0f : high[b][j]));
           sum[b][j] += w;
-          s[b][i] = kE4m3 ? kLift * exp2_fast(s[b][i] + shift[i >> 1] -
-                                              (top[b][j] == minus_infinity() ? 0.0f : top[b][j]))
+          s[b][i] = kE4m3 ? exp2_fast(s[b][i] + shift[i >> 1] -
+                                      (top[b][j] == minus_infinity() ? 0.0f : top[b][j]))
                           : w;
         }
 #pragma unroll
@@ -421,10 +421,9 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
             uint32_t a[4];
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-              const uint32_t v = w[2 * h + k];
-              odd |= (v & 0x7F7F7F7Fu) + 0x01010101u;
-              a[2 * k] = ((v << 4) & 0x07F007F0u) | ((v << 8) & 0x80008000u);
-              a[2 * k + 1] = ((v >> 4) & 0x07F007F0u) | (v & 0x80008000u);
+              const uint32_t v = __byte_perm(w[2 * h + k], 0, 0x3120);
+              a[2 * k] = e4m3_to_bf16<0>(v);
+              a[2 * k + 1] = e4m3_to_bf16<1>(v);
             }
 #pragma unroll
             for (int b = 0; b < kBlocks; ++b)
@@ -467,9 +466,8 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
         float* to = sums + (warp * F::kRows + r) * F::kSumStride;
 #pragma unroll
         for (int t = 0; t < F::kSteps; ++t) {
-          to[t * 16 + (kE4m3 ? 2 * line : line)] = kE4m3 ? o[t][b][j] * kDrop : o[t][b][j];
-          to[t * 16 + (kE4m3 ? 2 * line + 1 : line + 8)] =
-              kE4m3 ? o[t][b][2 + j] * kDrop : o[t][b][2 + j];
+          to[t * 16 + (kE4m3 ? 2 * line : line)] = o[t][b][j];
+          to[t * 16 + (kE4m3 ? 2 * line + 1 : line + 8)] = o[t][b][2 + j];
         }
       }
     __syncthreads();
@@ -477,7 +475,6 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
     float* part = parts + (2 * block + (seg.from == 0)) * static_cast<int64_t>(F::kPartValues);
     // rows of different sight: what one does not see may have spoilt its products
     const bool differ = seg.rows > p.group;
-    if (kE4m3 && (odd & 0x80808080u)) atomicOr(&sh.again, 0xFFFFFFFFu >> (32 - seg.rows));
     for (int at = threadIdx.x; at < seg.rows * kDim; at += kThreads) {
       const int r = at / kDim, d = at % kDim;
       float m = sh.most[0][r], n = sh.score[0][r];
@@ -579,10 +576,11 @@ __global__ void __launch_bounds__(kThreads) k_attend_join(const AttendParams p) 
 }
 
 template <int kDim, int kBlocks, bool kE4m3>
-int launch_at(const AttendParams& p, cudaStream_t s) {
+int launch_at(AttendParams p, cudaStream_t s) {
   using F = Form<kDim, kBlocks, kE4m3>;
   const cudaError_t err = allow_shared<k_attend_split<kDim, kBlocks, kE4m3>>(F::kSmem);
   if (err != cudaSuccess) return err;
+  p.blocks *= F::kPerSm;
   k_attend_split<kDim, kBlocks, kE4m3><<<p.blocks, kThreads, F::kSmem, s>>>(p);
   return launch_after(k_attend_join<kDim, kBlocks>, dim3(static_cast<unsigned>(p.blocks)), kThreads,
                       s, p);
@@ -607,7 +605,7 @@ bool split_takes(const AttendParams& p) {
 }  // namespace
 
 int64_t split_workspace_bytes(int sms) {
-  return 2 * static_cast<int64_t>(sms) * (sizeof(Joint) + 2 * 4 * kMostPartValues);
+  return kMostPerSm * static_cast<int64_t>(sms) * (sizeof(Joint) + 2 * 4 * kMostPartValues);
 }
 
 bool launch_attend_split(const AttendParams& given, void* stream, int* status) {
@@ -624,10 +622,8 @@ bool launch_attend_split(const AttendParams& given, void* stream, int* status) {
   else if (p.head_dim <= 128)
     *status = rows <= 8 ? launch_with<128, 1>(p, s)
                         : rows <= 16 ? launch_with<128, 2>(p, s) : launch_with<128, 4>(p, s);
-  else {
-    p.blocks /= 2;  // one to an SM
+  else
     *status = rows <= 8 ? launch_with<256, 1>(p, s) : launch_with<256, 2>(p, s);
-  }
   return true;
 }
 

@@ -44,7 +44,7 @@ constexpr int kJoinColumns = 16;        // of a block of the launch that joins
 
 // Registers a thread: bf16 has three groups of four warps, 168 at launch, 64512 in
 // all: 200 for the two that hold a row's scores, 104 for the third, 64512.  e4m3
-// has four groups, 128 at launch, 65536: 176, 176, 80 and 80, 65536.
+// has four groups, 128 at launch, 65536: 184, 184, 72 and 72, 65536.
 template <int kDim, bool kE4m3 = false>
 struct Form {
   static constexpr int kThreads = 32 * (kSoftmaxWarps + (kE4m3 ? 8 : 4));
@@ -309,9 +309,10 @@ __device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32
 // Four warps, e4m3: rows as loaded to bf16, times their powers of two, where the
 // 128-byte swizzle has them; zeros behind the tile's last key.  A warp takes 32
 // rows of a tile, a lane 16 values of four rows in turn and the exponent of one row,
-// fetched a stage ahead.  A value's bits, moved to where bf16 has them, are it
-// times 2^-120, subnormal ones too; a product with 2^120 times the row's power
-// (or with either, where that is out of range) sets it right, exactly.
+// fetched a stage ahead.  A value goes by way of fp16 and fp32, all of which hold
+// it, so that most of the work is the multipliers'; the integer units, which the
+// softmax needs, put two together (a prompt of 8192 tokens of 16 heads: 351 us, by
+// moving bits 437; two or four rows at once, 380 and 373, spill).
 __device__ __forceinline__ uint32_t times_bf16(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -323,7 +324,6 @@ __device__ void widen(const AttendParams& p, Shared& sh, unsigned char* ring, un
                       int warp) {
   using F = Form<kDim, true>;
   constexpr int kPieces = kDim / 16, kAtOnce = 32 / kPieces;   // of a row; rows
-  constexpr uint32_t kRange = 134;         // highest exponent whose power times 2^120 bf16 holds
   const int lane = threadIdx.x & 31, piece = lane % kPieces;
   Walk<kTileRows> walk(p, sh.share);
   Segment s;
@@ -346,36 +346,25 @@ __device__ void widen(const AttendParams& p, Shared& sh, unsigned char* ring, un
     for (int load = 0; load < 2 * h.most; ++load, ++at) {
       const uint32_t own = next;
       next = exponent(load + 1);
-      const bool in_range = __all_sync(0xffffffffu, own <= kRange || own >= 255);
       const int slot = at % F::kRaw, stage = at % F::kStages;
       if (!wait(p, sh, &sh.raw_full[slot], (at / F::kRaw) & 1)) return;
       if (!wait(p, sh, &sh.empty[stage], ((at / F::kStages) & 1) ^ 1)) return;
       const unsigned char* from = raw + slot * F::kRawBytes + warp * 32 * kDim;
       unsigned char* to = ring + stage * F::kTileBytes;
-#pragma unroll 4
+#pragma unroll 1
       for (int i = 0; i < 32 / kAtOnce; ++i) {
         const int r = i * kAtOnce + lane / kPieces, row = warp * 32 + r;
         const uint32_t e = __shfl_sync(0xffffffffu, own, r);
         const uint4 w = *reinterpret_cast<const uint4*>(from + r * kDim + piece * 16);
         const uint32_t words[4] = {w.x, w.y, w.z, w.w};
-        // 2^120 times the row's power, or 2^120 and the row's power
-        uint32_t by = e >= 255 ? 0x7FC0u : in_range ? (e + 120) << 7 : 247u << 7;
+        uint32_t by = e == 255 ? 0x7FC0u : e ? e << 7 : 0x40u;   // the row's power
         by |= by << 16;
-        uint32_t again = e >= 255 ? 0x7FC0u : e ? e << 7 : 0x40u;
-        again |= again << 16;
-        uint32_t out[8], odd = 0;
+        uint32_t out[8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) odd |= (words[j] & 0x7F7F7F7Fu) + 0x01010101u;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const uint32_t x = __byte_perm(words[j / 2], 0, j & 1 ? 0x3424 : 0x1404);
-          uint32_t v = times_bf16((x & 0x80008000u) | ((x >> 4) & 0x07F007F0u), by);
-          if (!in_range) v = times_bf16(v, again);
-          if (odd & 0x80808080u) {  // 0x7F and 0xFF are NaN
-            if ((x & 0x7F00u) == 0x7F00u) v |= 0x7FC0u;
-            if ((x & 0x7F000000u) == 0x7F000000u) v |= 0x7FC00000u;
-          }
-          out[j] = e == 256 ? 0u : v;
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t v = e == 256 ? 0u : words[j];
+          out[2 * j] = times_bf16(e4m3_to_bf16<0>(v), by);
+          out[2 * j + 1] = times_bf16(e4m3_to_bf16<1>(v), by);
         }
         unsigned char* line = to + (piece / 4) * kKeys * kRowBytes + row * kRowBytes;
         const int first = 2 * (piece & 3);
@@ -813,13 +802,13 @@ __global__ void __launch_bounds__(Form<kDim, kE4m3>::kThreads, 1)
   const uint32_t raw_at = ring + F::kStages * F::kTileBytes;
   if (warp < kSoftmaxWarps) {
     if (kE4m3)
-      asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     soften<kDim>(p, sh, warp / 4);
   } else {
     if (kE4m3)
-      asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     else
       asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp == kMultiplyWarp)

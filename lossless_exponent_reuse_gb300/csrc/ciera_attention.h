@@ -128,8 +128,8 @@ int launch_release_pages(const PagesParams& p, void* stream);
 int launch_attend(const AttendParams& p, void* stream);
 int64_t attend_workspace_bytes(int64_t q_heads, int64_t heads, int64_t head_dim);
 // Attention in tiles of few rows (mma.sync), and of up to 256 (tcgen05), with
-// p.blocks twice, or once, the SMs; false where a call's layout is not one that
-// they take.  And the bytes of workspace of so many blocks.
+// p.blocks the SMs; false where a call's layout is not one that they take.  And the
+// bytes of workspace that they want.
 bool launch_attend_split(const AttendParams& p, void* stream, int* status);
 int64_t split_workspace_bytes(int sms);
 bool launch_attend_wide(const AttendParams& p, void* stream, int* status);

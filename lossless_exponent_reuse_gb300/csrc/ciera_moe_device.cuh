@@ -149,6 +149,26 @@ struct Word<uint16_t> {
   }
 };
 
+// Two e4m3 values, of a word's low or high half, as bf16, by way of fp16 and fp32,
+// all of which hold them.
+template <int kHigh>
+__device__ __forceinline__ uint32_t e4m3_to_bf16(uint32_t v) {
+  float lo, hi;
+  if (kHigh)
+    asm("{\n\t.reg .b16 a, b, x, y;\n\t.reg .b32 h;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h, b;\n\tmov.b32 {x, y}, h;\n\tcvt.f32.f16 %0, x;\n\t"
+        "cvt.f32.f16 %1, y;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(v));
+  else
+    asm("{\n\t.reg .b16 a, b, x, y;\n\t.reg .b32 h;\n\tmov.b32 {a, b}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 h, a;\n\tmov.b32 {x, y}, h;\n\tcvt.f32.f16 %0, x;\n\t"
+        "cvt.f32.f16 %1, y;\n\t}"
+        : "=f"(lo), "=f"(hi)
+        : "r"(v));
+  return __byte_perm(__float_as_uint(lo), __float_as_uint(hi), 0x7632);
+}
+
 // Offset of group e, clamped to [lo, rows]; `lo` is the one before it.
 __device__ __forceinline__ int32_t clamp_offset(int32_t v, int32_t lo, int32_t rows) {
   return v < lo ? lo : v > rows ? rows : v;
