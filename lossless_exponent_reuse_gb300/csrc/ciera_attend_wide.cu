@@ -79,18 +79,12 @@ struct Shared {
   int64_t part[kSoftmaxWarps + 9];
 };
 
-// Bounded wait of a whole warp; false, for all its lanes, when it ran out here
-// or anywhere in the block.  The clock is looked at between rounds of tries alone
-// (each try, and the others' polling, took from the softmax: 2.0 us a unit).
+// Bounded wait; false when it ran out here or anywhere in the block.
 __device__ __forceinline__ bool wait_on(const AttendParams& p, Shared& sh, uint64_t* bar,
                                         uint32_t parity) {
-  constexpr int kTries = 64;
-  for (int i = 0; i < kTries; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = globaltimer();
-  for (;;) {
-    for (int i = 0; i < kTries; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+  while (!mbar_try_wait(bar, parity)) {
     if (*reinterpret_cast<volatile uint32_t*>(&sh.stop)) return false;
     const uint64_t now = globaltimer();
     if (*reinterpret_cast<volatile uint32_t*>(&sh.busy)) t0 = now;
@@ -100,7 +94,9 @@ __device__ __forceinline__ bool wait_on(const AttendParams& p, Shared& sh, uint6
       return false;
     }
   }
+  return true;
 }
+// The same for a whole warp, all of whose lanes go on or leave.
 __device__ __forceinline__ bool wait(const AttendParams& p, Shared& sh, uint64_t* bar,
                                      uint32_t parity) {
   return __all_sync(0xffffffffu, wait_on(p, sh, bar, parity));

@@ -164,6 +164,16 @@ def test_binding_refuses_what_is_not_on_a_gpu():
             call()
 
 
+def test_cache_layout_matches_the_header():
+    from test_lib_host import _c_layout
+    fields = ["key_dev", "value_dev", "key_exponent_dev", "value_exponent_dev", "key_stride",
+              "value_stride", "key_exponent_stride", "value_exponent_stride", "pages", "page_size",
+              "heads", "head_dim", "type"]
+    size, offsets = _c_layout("ciera_cache", fields)
+    words = [0, 1, 2, 3, 4, 7, 10, 13, 16, 17, 18, 19, 20]
+    assert size == len(cache()) == 168 and offsets == [8 * w for w in words]
+
+
 def test_caches_and_pools_as_made():
     c = attention.page_cache(3, 4, 2, 16, device="cpu")
     assert c.key.shape == (3, 4, 2, 16) and c.key.stride() == (128, 16, 64, 1)
