@@ -181,6 +181,10 @@ struct Tiles {
   // A tile weighs as much as two of its units besides (8192-token prompt of 16
   // heads, 24 chunks, in us: without 234, 172; one 232, 137; two 236, 128; three 240, 124).
   static constexpr int32_t kTileWeight = 2;
+  // The least weight of a block: what one more of the wide form's takes to begin and
+  // to be joined is as long as some units (24 rows of 9003 keys, 256 of 2256, in us: least 1
+  // 45, 21.9; 2 33, 21.4; 3 28, 21.5; 6 28, 24.4).
+  static constexpr int32_t kLeast = kRows == 256 ? 3 : 1;
   static __device__ __forceinline__ int32_t weight(const AttendParams& p, const Request& r,
                                                    int32_t tile) {
     return kTileWeight + units(p, r, tile);
@@ -264,7 +268,8 @@ __device__ void find_share(const AttendParams& p, int block, int blocks, int64_t
   for (int32_t base = 0; base < p.requests; base += kThreads) own += weight(base + threadIdx.x);
   const int64_t first = own;
   scan_block<kThreads>(own, part, &total);
-  if (total < blocks) blocks = static_cast<int>(total);
+  if (total < static_cast<int64_t>(blocks) * T::kLeast)
+    blocks = total > T::kLeast ? static_cast<int>(total / T::kLeast) : total > 0;
   const int64_t begin = block < blocks ? block * total / blocks : total;
   const int64_t end = block < blocks ? (block + 1) * total / blocks : total;
   if (threadIdx.x == 0) {

@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
 // the last request become zeros.  A row's parts are shared by the warps of a block
 // (one token of 4096 keys, 16 tiles of 20 parts: part by part in every thread 12.3 us).
 constexpr int kJoinWarps = 8;
-constexpr int kJoinRows = 4;
+constexpr int kJoinRows = 8;
 
 template <int kDim, int kBlocks>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_attend_join(const AttendParams p) {
