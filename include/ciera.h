@@ -799,16 +799,22 @@ int64_t ciera_attend_workspace_bytes(int64_t q_heads, int64_t heads, int64_t hea
  * last request.  Keys that a token does not see have no part in its row, be
  * they infinite or NaN.  q's head h reads the cache's head
  * h / (q_heads / heads).  Weights are rounded to 16 bits (8 significant) on
- * their way to the tensor cores, sums and maxima held in 32.
+ * their way to the tensor cores, sums and maxima held in 32.  A row in whose
+ * products something infinite or NaN came up is computed again value by value.
  *   q_dev        tokens x q_heads x head_dim bf16
  *   table_dev    requests x width pages, rows table_stride apart
  *   offsets_dev  requests + 1
- *   context_dev  requests, at most width * page_size each
+ *   context_dev  requests, at most width * page_size, and 2^31 - 4096, each
  *   longest      most new tokens of a request, as far as the caller knows: fewer
  *                launches, never other rows; tokens if unknown
  *   o_dev        tokens x q_heads x head_dim bf16, contiguous
  * The workspace belongs to the call until it has run; what it holds before does
- * not matter.  control_dev: a status block (ciera_moe_control).
+ * not matter.  control_dev: a status block (ciera_moe_control), where a wait that
+ * ran out is reported.
+ * Forms: many rows a head of up to 128 values run on the tensor cores of tcgen05
+ * where a page is a multiple of 8 keys, scale is positive and q, o and the cache's
+ * rows start on 16-byte boundaries; other rows of whole 16-byte words, up to 256
+ * values, on mma.sync; what is left on a plain kernel.
  * Errors: CIERA_E_INVAL (heads that do not divide q_heads, head_dim outside
  * [1, 256], tokens * q_heads > 2^31 - 4096, scale not finite, ...), CIERA_E_CUDA. */
 int ciera_attend(const uint16_t *q_dev, int64_t q_token_stride, int64_t q_head_stride,

@@ -14,8 +14,8 @@ request their places, ``append`` rotates queries and keys and writes keys and
 values there, ``attend`` reads them; the first serves all layers of a step.
 Tensors of heads, [tokens, heads, head_dim], and pages may have any strides; a
 head's values must be contiguous.  Every call takes ``stream`` as ``experts``'
-calls do.  Nothing is registered with autograd: ``rotary_backward`` is the
-gradient's call.
+calls do; ``experts.status`` reads the error word that ``attend`` reports to.
+Nothing is registered with autograd: ``rotary_backward`` is the gradient's call.
 """
 from __future__ import annotations
 
@@ -372,7 +372,8 @@ def attend(q: torch.Tensor, cache: Cache, table: torch.Tensor, offsets: torch.Te
     request r's from offsets[r] on) over its pages, of which ``context`` [requests]
     keys are there, the new ones last; each token sees the keys up to its own.
     ``scale``: head_dim^-0.5 if not given.  ``longest``: the most new tokens of a
-    request, if the caller knows (1 for a step of single tokens)."""
+    request, if the caller knows (1 for a step of single tokens): it chooses the
+    faster kernel, no result; guessed 1 where tokens are no more than requests."""
     index = _index(q, "q")
     (tokens, heads, dim), q_token, q_head = _heads(q, "q", index)
     shape, words = _cache(cache, index)
@@ -382,11 +383,13 @@ def attend(q: torch.Tensor, cache: Cache, table: torch.Tensor, offsets: torch.Te
     off = _array(offsets, "offsets", _I32, index, requests + 1)
     keys = _array(context, "context", _I32, index, requests)
     need = _needs.get((index, heads, shape[2], dim)) or _need(index, heads, shape[2], dim)
+    if longest is None:
+        longest = tokens if tokens > requests else 1
     s = _raw_stream(index)
     ws = experts._scratch_bytes(index, s, need)
     o = torch.empty((tokens, heads, dim), dtype=_BF16, device=q.device)
     _call("ciera_attend", index, q.data_ptr(), q_token, q_head, tokens, heads, words, table_at,
-          stride, width, off, keys, requests, tokens if longest is None else int(longest),
+          stride, width, off, keys, requests, int(longest),
           dim ** -0.5 if scale is None else float(scale), o.data_ptr(), ws.data_ptr(), ws.numel(),
           _control(index), s)
     return o

@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
                 static_cast<const unsigned char*>(side ? p.value.data : p.key.data);
             const bool some = from >= 0 && piece < pieces;
             copy16(to + side * F::kSideBytes + row * F::kRowBytes + piece_at<F::kPieces>(row, piece),
-                   some ? base + from * size + piece * 16 : base, some ? 16 : 0);
+                   some ? base + from * size + piece * 16 : p.workspace, some ? 16 : 0);
           }
       }
       copy_commit();

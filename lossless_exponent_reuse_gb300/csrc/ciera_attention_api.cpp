@@ -268,7 +268,7 @@ int ciera_attend(const uint16_t *q_dev, int64_t q_token_stride, int64_t q_head_s
       workspace_bytes < attend_workspace_bytes(q_heads, heads, dim))
     return CIERA_E_INVAL;
   if (tokens == 0) return CIERA_OK;
-  const int64_t most = width > kMaxSlots / cache->page_size ? kMaxSlots : width * cache->page_size;
+  const int64_t most = width > kMaxRows / cache->page_size ? kMaxRows : width * cache->page_size;
   p.q = q_dev;
   p.q_token = q_token_stride;
   p.q_head = q_head_stride;

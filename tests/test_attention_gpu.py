@@ -84,6 +84,16 @@ def test_many_requests():
     run(new, cached[:300], 4, 1, 64, 16)
 
 
+def test_an_order_of_requests_changes_no_row():
+    """A batch's rows are those that each request has alone."""
+    new, cached = [3, 200, 1, 40, 1, 1], [500, 0, 3000, 77, 15, 16]
+    q, cache, table, off, context = batch(new, cached, 8, 2, 128, 16)
+    got = attention.attend(q, cache, table, off, context)
+    for r, (a, b) in enumerate(zip(off.tolist(), off.tolist()[1:])):
+        one = attention.attend(q[a:b], cache, table[r:r + 1], ints([0, b - a]), context[r:r + 1])
+        assert (got[a:b].float() - one.float()).norm() <= 2.0 ** -7 * one.float().norm()
+
+
 def test_nothing():
     q, cache, table, offsets, context = batch([3, 2], [0, 1], 4, 2, 64, 16)
     none = attention.attend(q[:0], cache, table, ints([0, 0, 0]), context)
@@ -257,6 +267,51 @@ def test_heads_of_any_size():
         run([3, 20], [10, 40], 4, 2, dim, 16)
     for dim in (16, 24, 48, 240):
         run([3, 20], [10, 40], 4, 2, dim, 16, e4m3=True)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("q_heads,heads", [(128, 1), (200, 1), (256, 1), (130, 2), (64, 2)])
+def test_many_query_heads_to_one(q_heads, heads, e4m3):
+    run([1, 5, 2], [300, 40, 0], q_heads, heads, 128, 16, e4m3=e4m3)
+    run([1], [700], q_heads, heads, 64, 24, e4m3=e4m3)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-30, 3.0])
+def test_scales(scale, e4m3):
+    for new in (1, 150):
+        q, cache, table, off, context = batch([new, 3], [200, 31], 4, 2, 128, 16, e4m3=e4m3)
+        got = attention.attend(q, cache, table, off, context, scale=scale)
+        ref.check_attend(got, q, cache, table, off, context, scale=scale)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_cache_of_no_pages_holds_zeros(e4m3):
+    cache = attention.page_cache(0, 16, 2, 128, e4m3=e4m3)
+    for new in (1, 200):
+        q, table = rand(new, 4, 128), torch.zeros(1, 20, dtype=torch.int32, device="cuda")
+        got = attention.attend(q, cache, table, ints([0, new]), ints([new + 5]))
+        assert (got == 0).all()
+    assert experts.status() == ciera.OK
+
+
+def test_rows_of_nan_are_nan_alone():
+    """Queries and keys of NaN, in rows that everyone computes together."""
+    for new in (9, 300):
+        q, cache, table, off, context = batch([new, 40], [100, 60], 4, 2, 128, 16)
+        q[3, 1] = math.nan
+        q[new + 2, 0, 5] = math.inf
+        cache.key[table[1, 1].long(), 3, 1, 7] = math.nan       # all of request 1's head 1 see it
+        got = attention.attend(q, cache, table, off, context)
+        odd = torch.isnan(got).all(2)
+        want = torch.zeros_like(odd)
+        want[3, 1] = want[new + 2, 0] = True
+        want[new:, 2:] = True
+        assert torch.equal(odd, want) and torch.isfinite(got[~want]).all()
+        q[3, 1], q[new + 2, 0, 5] = 1.0, 1.0
+        cache.key[table[1, 1].long(), 3, 1, 7] = 1.0
+        clean = attention.attend(q, cache, table, off, context)
+        assert torch.equal(got[~want], clean[~want])
 
 
 def test_places_behind_32_bits():
