@@ -476,7 +476,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
     const bool whole = seg.from == 0 && seg.to == seg.all;
     float* part = parts + (2 * block + (seg.from == 0)) * static_cast<int64_t>(F::kPartValues);
     // rows of different sight: what one does not see may have spoilt its products
-    const bool differ = seg.rows > p.group;
+    const bool differ = p.by_group(row0) != p.by_group(row0 + seg.rows - 1);
     for (int at = threadIdx.x; at < seg.rows * kDim; at += kThreads) {
       const int r = at / kDim, d = at % kDim;
       float m = sh.most[0][r], n = sh.score[0][r];

@@ -170,6 +170,21 @@ def test_values_out_of_sight_have_no_part(new, page, dim, q_heads, bad):
     assert torch.isfinite(got[:, :q_heads // 2]).all() and torch.isfinite(got[new:]).all()
 
 
+@pytest.mark.parametrize("q_heads,new,page,dim,longest", [
+    (48, 2, 20, 128, None), (40, 3, 20, 64, None), (24, 2, 16, 256, None), (12, 2, 16, 128, 1),
+    (9, 3, 20, 64, 1)])
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_tiles_that_begin_and_end_inside_a_token(q_heads, new, page, dim, longest, bad):
+    """Of fewer rows than a token has, but of two tokens, the first of which does
+    not see the second's key."""
+    q, cache, table, offsets, context = batch([new], [50], q_heads, 1, dim, page)
+    L = 50 + new
+    cache.value[table[0, (L - 1) // page].long(), (L - 1) % page, 0, 3] = bad
+    got = attention.attend(q, cache, table, offsets, context, longest=longest)
+    ref.check_attend(got, q, cache, table, offsets, context)
+    assert torch.isfinite(got[:new - 1]).all()
+
+
 @pytest.mark.parametrize("new,page,dim", [(1, 16, 128), (3, 20, 64), (200, 16, 128), (200, 24, 64)])
 def test_rows_of_any_exponent(new, page, dim):
     """Powers of two from the lowest to the highest, zeros, and NaN by exponent and by
