@@ -739,7 +739,8 @@ typedef struct {
  * infinite or NaN.
  *   q_dev, q_out_dev  tokens x q_heads x head_dim bf16; q_out may be q itself
  *   k_dev, v_dev      tokens x cache->heads x head_dim bf16
- *   slots_dev         tokens; two tokens of one slot: either's rows stay
+ *   slots_dev         tokens; two tokens of one slot leave rows that may hold values
+ *                     of both, and either's exponent
  * Errors: as ciera_rotary (CIERA_INVERSE is refused), and CIERA_E_INVAL for
  * pages * page_size > 2^31 - 1 or another cache that does not fit the above. */
 int ciera_append(const uint16_t *q_dev, int64_t q_token_stride, int64_t q_head_stride,
@@ -795,12 +796,15 @@ int64_t ciera_attend_workspace_bytes(int64_t q_heads, int64_t heads, int64_t hea
  * and L = context[r], token i sees the first L - n + i + 1 keys (the new ones
  * are the last of L, appended before):
  *   o = sum_j p_j v_j,  p_j = exp(scale q . k_j - max) / sum of them
- * over the keys it sees; zeros where it sees none, and in the rows behind the
- * last request.  Keys that a token does not see have no part in its row, be
+ * over the keys it sees; zeros where it sees none, or every score is minus
+ * infinity, and in the rows behind the last request.  Keys that a token does not see have no part in its row, be
  * they infinite or NaN.  q's head h reads the cache's head
  * h / (q_heads / heads).  Weights are rounded to 16 bits (8 significant) on
- * their way to the tensor cores, sums and maxima held in 32.  A row in whose
- * products something infinite or NaN came up is computed again value by value.
+ * their way to the tensor cores, sums and maxima held in 32; weights up to 2^8 times
+ * values are summed before they are divided by the weights' sum, which values above
+ * 2^119 / L may overflow.  Where rows that see different keys are computed together, a
+ * row in whose products something infinite or NaN came up is computed again, value
+ * by value.
  *   q_dev        tokens x q_heads x head_dim bf16
  *   table_dev    requests x width pages, rows table_stride apart
  *   offsets_dev  requests + 1

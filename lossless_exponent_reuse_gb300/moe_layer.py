@@ -132,7 +132,7 @@ class AttentionLayer:
         each with pages of its own); keys and values go to ``cache``.  ``longest``:
         most new tokens of a request."""
         norm = experts.rmsnorm(x, self.norm, residual=residual, eps=self.eps)
-        qkv = (norm.y @ self.qkv.T).view(x.shape[0], -1, self.head_dim)
+        qkv = (norm.y @ self.qkv.T).view(x.shape[0], sum(self.heads), self.head_dim)
         q, k, v = qkv.split(self.heads, 1)
         q = attention.append(q, k, v, step.positions, step.slots, self.rotary, cache, out=q)
         o = attention.attend(q, cache, step.pool.table, step.offsets, step.context,

@@ -66,6 +66,19 @@ def test_half_over_a_rebuilt_bucket(q_heads, heads, dim, page, e4m3):
         assert off(y, want) < (8 ** 0.5 * 2.0 ** -9 + 2.0 ** -9 if not e4m3 else 3 * 2.0 ** -5)
 
 
+def test_half_of_no_tokens():
+    wl = moe_layer.layer_workload(2, 128, 64, ranks=1, block=64, name="half_of_none",
+                                  attention_rows=(256, 128))
+    half = moe_layer.AttentionLayer(rand(wl.numel), wl, 64, attention.rotary_table(64))
+    cache = attention.page_cache(4, 16, 2, 64)
+    pool = attention.page_pool(4, 2, 2)
+    step = attention.assign_pages(pool, ints([0, 0]), ints([0, 0]), 0, 16, count=pool.count)
+    y, h = half.serve(rand(0, 128), step, cache)
+    assert list(y.shape) == [0, 128] and list(h.shape) == [0, 128]
+    assert pool.count.tolist() == [4] and step.offsets.tolist() == [0, 0, 0]
+    assert experts.status() == ciera.OK
+
+
 def small_batch(seed, new, e4m3=False):
     heads, dim, page = 2, 128, 16
     cached = [300, 17, 90]
