@@ -9,7 +9,9 @@ namespace ciera {
 namespace {
 
 // ------------------------------------------------------------------------
-// Rotary positions.  Bound by memory: 4 bytes a value.  A turn is a whole number
+// Rotary positions.  Bound by memory: 4 bytes a value (16384 tokens of 32 heads of 128
+// 42.5 us, 6.3 TB/s; 8192 tokens of 32, 8 and 8 heads into 8-bit pages 41.1, 4.5 TB/s: a
+// row's exponent has to wait for all of it).  A turn is a whole number
 // of 2^-64 turns per position, so that position * turns wraps as the angle does
 // and the angle's 24 bits for sin and cos are exact for every position.
 //
@@ -137,12 +139,17 @@ __device__ __forceinline__ void put_e4m3(void* to, const float* f, float by) {
 // kVec pairs a lane.  lanes: of a row (a power of two); span: rows of a warp,
 // spans: warps of a token.
 template <int kVec, bool kAppend, bool kInterleaved>
-__global__ void __launch_bounds__(32 * kRotaryWarps, kAppend ? 5 : 6)
+__global__ void __launch_bounds__(32 * kRotaryWarps, kAppend ? 5 : 7)
     k_rotary(const RotaryParams p, int lanes, int span, int spans) {
   using Word = typename RotaryWord<kVec>::Word;
-  // rows that a lane loads before it uses the first (16384 tokens of 32 heads, in us, one
-  // 50, two 45.6, four 46.7; 8192 tokens into 8-bit pages 55, two 46.6, three 44.2)
-  constexpr int kBatch = kAppend ? 3 : 2;
+  // Rows that a lane loads before it uses the first, the first ones before it works out
+  // the token's turns; into pages, whose rows take longer, the next ones before it
+  // stores these.  In us, blocks an SM in brackets: 16384 tokens of 32 heads, two behind
+  // the turns 45.8 (6), before them 43.9 (6), 42.5 (7), 43.2 (8), three 45 (5), two and
+  // the next 44.4 (5); 8192 tokens into 8-bit pages, three behind the turns 44.5 (5), before
+  // them 44.2 (5), two and the next 41.1 (5), 45.5 (4), one and the next 42.8 (6).
+  constexpr int kBatch = 2;
+  constexpr bool kAhead = kAppend;
   __shared__ float2 turns[kRotaryWarps][kMostPairs];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t item = static_cast<int64_t>(blockIdx.x) * kRotaryWarps + warp;
@@ -152,20 +159,35 @@ __global__ void __launch_bounds__(32 * kRotaryWarps, kAppend ? 5 : 6)
   const int64_t first = (item - t * spans) * span;
   const int64_t end = first + span < rows ? first + span : rows;
 
+  const int unit = lane & (lanes - 1), turned = p.pairs / kVec, step = 32 / lanes;
+  const bool rotates = unit < turned;
+  // the lane's two words of a row
+  int a = 2 * p.pairs + 2 * (unit - turned) * kVec, b = a + kVec;
+  if (rotates) {
+    a = kInterleaved ? 2 * unit * kVec : unit * kVec;
+    b = kInterleaved ? a + kVec : a + p.pairs;
+  }
+  const bool has_a = a < p.head_dim, has_b = b < p.head_dim;
+  const auto fetch = [&](int64_t j0, Word (&w)[kBatch][2]) {
+#pragma unroll
+    for (int q = 0; q < kBatch; ++q) {
+      const int64_t j = j0 + q * step + lane / lanes;
+      w[q][0] = w[q][1] = Word{};
+      if (j >= end) continue;
+      const uint16_t* from = rotary_row(p, t, j, -1, 0).from;
+      if (has_a) w[q][0] = *reinterpret_cast<const Word*>(from + a);
+      if (has_b) w[q][1] = *reinterpret_cast<const Word*>(from + b);
+    }
+  };
+  Word w[kBatch][2];
+  fetch(first, w);
   const int32_t position = p.positions[t];
   for (int i = lane; i < p.pairs; i += 32) turns[warp][i] = turn(p, position, i);
   int32_t page = -1, place = 0;
   if (kAppend) find_slot(p, t, &page, &place);
   __syncwarp();
-
-  const int unit = lane & (lanes - 1), turned = p.pairs / kVec;
-  const bool rotates = unit < turned;
-  // the lane's two words of a row
-  int a = 2 * p.pairs + 2 * (unit - turned) * kVec, b = a + kVec;
   float c[kVec], s[kVec];
   if (rotates) {
-    a = kInterleaved ? 2 * unit * kVec : unit * kVec;
-    b = kInterleaved ? a + kVec : a + p.pairs;
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const float2 v = turns[warp][unit * kVec + i];
@@ -173,29 +195,22 @@ __global__ void __launch_bounds__(32 * kRotaryWarps, kAppend ? 5 : 6)
       s[i] = v.y;
     }
   }
-  const bool has_a = a < p.head_dim, has_b = b < p.head_dim;
-  const int step = 32 / lanes;
   for (int64_t j0 = first; j0 < end; j0 += kBatch * step) {
-    RotaryRow row[kBatch];
-    Word w[kBatch][2];
-#pragma unroll
-    for (int q = 0; q < kBatch; ++q) {
-      const int64_t j = j0 + q * step + lane / lanes;
-      row[q].to = nullptr;
-      row[q].kind = 2;
-      w[q][0] = w[q][1] = Word{};
-      if (j >= end) continue;
-      row[q] = rotary_row(p, t, j, page, place);
-      if (has_a) w[q][0] = *reinterpret_cast<const Word*>(row[q].from + a);
-      if (has_b) w[q][1] = *reinterpret_cast<const Word*>(row[q].from + b);
-    }
+    // (rows of their own: also where the output is x itself)
+    Word next[kBatch][2];
+    if (kAhead) fetch(j0 + kBatch * step, next);
 #pragma unroll
     for (int q = 0; q < kBatch; ++q) {
       if (j0 + q * step >= end) break;
+      const int64_t j = j0 + q * step + lane / lanes;
+      RotaryRow row;
+      row.to = nullptr;
+      row.kind = 2;
+      if (j < end) row = rotary_row(p, t, j, page, place);
       float x[2 * kVec];
       widen<kVec>(w[q][0], x);
       widen<kVec>(w[q][1], x + kVec);
-      const bool rotate = rotates && row[q].kind < 2;
+      const bool rotate = rotates && row.kind < 2;
       uint32_t most = 0;
       if (kAppend && p.e4m3) {
 #pragma unroll
@@ -220,19 +235,28 @@ __global__ void __launch_bounds__(32 * kRotaryWarps, kAppend ? 5 : 6)
           u = y;
         }
       }
-      if (!row[q].to) continue;
-      if (kAppend && p.e4m3 && row[q].kind) {
+      if (!row.to) continue;
+      if (kAppend && p.e4m3 && row.kind) {
         const uint32_t e = row_exponent(most);
         const float by = inverse_scale(e);
-        uint8_t* to = static_cast<uint8_t*>(row[q].to);
+        uint8_t* to = static_cast<uint8_t*>(row.to);
         if (has_a) put_e4m3<kVec>(to + a, x, by);
         if (has_b) put_e4m3<kVec>(to + b, x + kVec, by);
-        if (unit == 0) *row[q].exponent = static_cast<uint8_t>(e);
+        if (unit == 0) *row.exponent = static_cast<uint8_t>(e);
       } else {
-        uint16_t* to = static_cast<uint16_t*>(row[q].to);
+        uint16_t* to = static_cast<uint16_t*>(row.to);
         if (has_a) put_bf16<kVec>(to + a, x);
         if (has_b) put_bf16<kVec>(to + b, x + kVec);
       }
+    }
+    if (kAhead) {
+#pragma unroll
+      for (int q = 0; q < kBatch; ++q) {
+        w[q][0] = next[q][0];
+        w[q][1] = next[q][1];
+      }
+    } else {
+      fetch(j0 + kBatch * step, w);
     }
   }
 }
