@@ -315,8 +315,9 @@ __global__ void __launch_bounds__(32 * kRotaryWarps) k_rotary_any(const RotaryPa
 
 // ------------------------------------------------------------------------
 // Pages of a step.  A few KB in and out: bound by its launch and the chain of
-// loads.  The first block of a cluster scans the requests and gives out the free
-// pages; then every token of the cluster finds its request by bisection.
+// loads (8 requests 6.1 us, 200 of up to 80 new tokens 11.7).  The first block of a
+// cluster scans the requests and gives out the free pages; then every token of the
+// cluster finds its request by bisection.
 
 constexpr int kPagesThreads = 1024;
 constexpr int kPagesCluster = 8;
