@@ -816,8 +816,9 @@ int64_t ciera_attend_workspace_bytes(int64_t q_heads, int64_t heads, int64_t hea
  * not matter.  control_dev: a status block (ciera_moe_control), where a wait that
  * ran out is reported.
  * Forms: many rows a head of up to 128 values run on the tensor cores of tcgen05
- * where a page is a multiple of 8 keys, scale is positive and q, o and the cache's
- * rows start on 16-byte boundaries; other rows of whole 16-byte words, up to 256
+ * where a page has a divisor from 2 to 128 (8-bit heads of up to 64 values: an even
+ * one; large ones are faster), scale is positive and q, o and the cache's rows start
+ * on 16-byte boundaries; other rows of whole 16-byte words, up to 256
  * values, on mma.sync; what is left on a plain kernel.
  * Errors: CIERA_E_INVAL (heads that do not divide q_heads, head_dim outside
  * [1, 256], tokens * q_heads > 2^31 - 4096, scale not finite, ...), CIERA_E_CUDA. */

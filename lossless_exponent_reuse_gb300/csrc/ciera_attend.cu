@@ -6,12 +6,6 @@ namespace ciera {
 namespace {
 
 constexpr int kAnyWarps = 4;
-// Rows a head (most of any request, as far as the caller knows) up to which a call
-// takes the form for few rows.  64 requests of 5000 keys on average, 4 heads, rows,
-// form for few and for many, in us: bf16 8 110, 120; 16 112, 121; 24 142, 121; 32 154,
-// 121; 64 223, 119.  e4m3 16 99, 201; 32 165, 201; 64 241, 198.
-constexpr int kFewRows = 16, kFewRowsE4m3 = 32;
-
 // A warp per row (token and query head), a key at a time.  Bound by its
 // instructions: right for every layout, not fast (one token of 4096 keys, 16 heads, 6.8
 // ms; the form for few rows takes 15 us).
@@ -61,9 +55,7 @@ int launch_attend(const AttendParams& given, void* stream) {
   AttendParams p = given;
   int status = cudaSuccess;
   p.blocks = sm_count();
-  if (p.longest * p.group > (p.e4m3 ? kFewRowsE4m3 : kFewRows) &&
-      launch_attend_wide(p, stream, &status))
-    return status;
+  if (launch_attend_wide(p, stream, &status)) return status;
   if (launch_attend_split(p, stream, &status)) return status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int64_t rows = static_cast<int64_t>(p.tokens) * p.heads * p.group;

@@ -974,11 +974,23 @@ int launch_at(const AttendParams& p, const Maps& maps, cudaStream_t s) {
   return launch_after(k_attend_wide_join<kDim>, grid, kJoinGroups * kTileRows, s, p);
 }
 
-// Pages of whole eights of keys, whose rows are 16-byte words, as queries and
-// outputs are.
+// Rows a head (most of any request, as far as the caller knows) up to which a call
+// is left to the form for few rows.  64 requests of 5000 keys on average, 4 heads, rows,
+// form for few and for many, in us: bf16 8 110, 120; 16 112, 121; 24 142, 121; 32 154,
+// 121; 64 223, 119.  e4m3 16 99, 201; 32 165, 201; 64 241, 198.
+constexpr int kFewRows = 16, kFewRowsE4m3 = 32;
+// Of boxes of fewer than eight keys, whose loads take longer, by rows times keys of a box:
+// bf16 pages of two and 40 rows 136, 230, 70 rows 199, 231, 100 rows (12 heads) 164, 166;
+// of three 44 rows 141, 163; of four 40 rows 133, 135, 70 rows 195, 132; of five 28 rows
+// 115, 115, 56 rows 154, 117.  e4m3 of two 100 rows 178, 179; of four 70 rows 211, 139; of
+// five 56 rows 168, 135.
+constexpr int kSmallBox = 8;
+constexpr int kFewSmall = 192, kFewSmallE4m3 = 256;
+
+// Rows of 16-byte words, as queries and outputs are.
 bool wide_takes(const AttendParams& p) {
   const int values = p.e4m3 ? 16 : 8;
-  return p.head_dim <= 128 && p.head_dim % values == 0 && p.page_size % 8 == 0 && p.pages > 0 &&
+  return p.head_dim <= 128 && p.head_dim % values == 0 && p.pages > 0 &&
          p.scale > 0.0f && on_words(p.key, values) && on_words(p.value, values) &&
          (reinterpret_cast<uintptr_t>(p.q) & 15) == 0 && p.q_token % 8 == 0 && p.q_head % 8 == 0 &&
          (reinterpret_cast<uintptr_t>(p.o) & 15) == 0 && encode();
@@ -994,10 +1006,18 @@ bool launch_attend_wide(const AttendParams& given, void* stream, int* status) {
   if (!wide_takes(given)) return false;
   AttendParams p = given;
   Maps maps;
-  // keys of a box: the most, by eights, that divide a page and fit a unit
+  // Keys of a box: the most that divide a page and fit a unit, by eights of pages of
+  // eights.  It may begin at any row of a stage: the swizzle goes by the address in
+  // shared memory.  Where a row as loaded has 64 bytes, by twos, as boxes begin on 128
+  // bytes.  A unit has 32 boxes at most, a lane each.
+  const int by = p.page_size % 8 == 0 ? 8 : p.e4m3 && p.head_dim <= 64 ? 2 : 1;
   maps.box = kKeys;
-  while (p.page_size % maps.box) maps.box -= 8;
-  p.unit_keys = kKeys / maps.box * maps.box;
+  while (maps.box > by && p.page_size % maps.box) maps.box -= by;
+  if (maps.box < 2 || p.page_size % maps.box) return false;
+  const int64_t rows = p.longest * p.group;
+  if (rows <= (p.e4m3 ? kFewRowsE4m3 : kFewRows)) return false;
+  if (maps.box < kSmallBox && rows * maps.box <= (p.e4m3 ? kFewSmallE4m3 : kFewSmall)) return false;
+  p.unit_keys = (kKeys / maps.box < 32 ? kKeys / maps.box : 32) * maps.box;
   maps.by_box = Divide(maps.box);
   p.by_unit = Divide(p.unit_keys);
   const int wide = !p.e4m3 ? 64 : p.head_dim <= 64 ? 64 : 128;

@@ -48,6 +48,26 @@ def test_page_sizes(page, e4m3):
     run([130, 1, 270], [0, 500, 129], 4, 2, 64, page, e4m3=e4m3, by_head=True)
 
 
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("page", [1, 2, 3, 4, 5, 6, 7, 10, 17, 20, 34, 50, 63, 65, 100, 127, 129,
+                                  131, 250])
+def test_many_rows_of_odd_pages(page, e4m3):
+    """Pages whose parts begin at any row of a stage, or that none of a size divide."""
+    run([150, 1, 290], [77, 200, 0], 4, 2, 128, page, e4m3=e4m3)
+    run([40, 129], [300, 1], 6, 1, 64, page, e4m3=e4m3, by_head=True)
+    run([60], [400], 2, 1, 80, page, e4m3=e4m3)
+    # keys and values behind the last one
+    q, cache, table, offsets, context = batch([140], [71], 4, 2, 128, page)
+    L = 211
+    at = table[0, (L - 1) // page].long()
+    cache.value[at, (L - 1) % page + 1:] = math.nan
+    cache.key[at, (L - 1) % page + 1:] = math.inf
+    cache.value[at, (L - 1) % page, 1, 3] = math.inf      # the last token alone sees it
+    got = attention.attend(q, cache, table, offsets, context)
+    ref.check_attend(got, q, cache, table, offsets, context)
+    assert torch.isfinite(got[:139]).all()
+
+
 @pytest.mark.parametrize("dim", [64, 72, 80, 96, 112, 128, 256])
 @pytest.mark.parametrize("q_heads,heads", HEADS)
 def test_chunks(q_heads, heads, dim):
@@ -172,7 +192,7 @@ def test_values_out_of_sight_have_no_part(new, page, dim, q_heads, bad):
 
 @pytest.mark.parametrize("q_heads,new,page,dim,longest", [
     (48, 2, 20, 128, None), (40, 3, 20, 64, None), (24, 2, 16, 256, None), (12, 2, 16, 128, 1),
-    (9, 3, 20, 64, 1)])
+    (9, 3, 20, 64, 1), (48, 2, 1, 128, None), (40, 3, 1, 64, None)])
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_tiles_that_begin_and_end_inside_a_token(q_heads, new, page, dim, longest, bad):
     """Of fewer rows than a token has, but of two tokens, the first of which does
