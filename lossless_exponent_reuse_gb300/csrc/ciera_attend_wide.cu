@@ -2,7 +2,7 @@
 // tensor cores (tcgen05).
 //
 // A persistent block per SM takes 256 rows, in two halves of 128, over units of up
-// to 128 keys.  One warp brings pages' keys and values into a ring of stages by TMA
+// to 128 keys.  Two warps bring pages' keys and values into a ring of stages by TMA
 // (128-byte swizzle; a box is a page, or the largest part of it that a tile holds
 // in whole), one lane of another issues S = Q K^T and O += P V, and two groups of
 // four warps, one to a half, a thread to a row, turn scores into weights: S from
@@ -18,7 +18,7 @@
 // 128, 1759 TFLOP/s; a block's start (9 us), a tile's begin and end (4) and the join
 // (5 to 9) come on top.  16 heads of 128: a prompt of 8192 tokens 211 to 224 us (1230 to
 // 1310 TFLOP/s, with the clock that power leaves), 512 tokens behind 32256 with 32 heads
-// to 4 191 to 197 (1400); 24 requests of 3 to 3000 cached keys and up to 300 new tokens
+// to 4 191 to 197 (1400); 24 requests of 100 to 3000 cached keys and up to 300 new tokens
 // 119 to 135, where some ten units a tile do not hide its begin.
 //
 // e4m3 pages come by TMA as they are; four warps more widen them to bf16, which
