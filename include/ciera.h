@@ -803,8 +803,9 @@ int64_t ciera_attend_workspace_bytes(int64_t q_heads, int64_t heads, int64_t hea
  * their way to the tensor cores, sums and maxima held in 32; weights up to 2^8 times
  * values are summed before they are divided by the weights' sum, which values above
  * 2^119 / L may overflow.  Where rows that see different keys are computed together, a
- * row in whose products something infinite or NaN came up is computed again, value
- * by value.
+ * row that is infinite or NaN, and has a value that is infinite or NaN among the keys behind its
+ * own, is computed again, value by value (not where it sees a NaN in the same place
+ * of the head).
  *   q_dev        tokens x q_heads x head_dim bf16
  *   table_dev    requests x width pages, rows table_stride apart
  *   offsets_dev  requests + 1

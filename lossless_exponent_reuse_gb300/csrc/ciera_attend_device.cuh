@@ -143,6 +143,99 @@ __device__ __noinline__ void warp_attend(const AttendParams& p, const uint16_t* 
   for (int i = 0; i < kSliceValues; ++i) own->o[i] = o[i];
 }
 
+// Where a request's value starts; -1: nowhere, zeros.  *exponent: of 8 bits.
+__device__ __forceinline__ int64_t value_at(const AttendParams& p, int32_t request, int32_t head,
+                                            int32_t key, uint32_t* exponent) {
+  const int32_t index = p.by_page(key), page = page_at(p, request, index);
+  *exponent = kExponentBias;
+  if (page < 0) return -1;
+  const int32_t place = key - index * p.page_size;
+  const Side& s = p.value;
+  if (p.e4m3)
+    *exponent = s.exponent[page * s.exponent_stride[0] + place * s.exponent_stride[1] +
+                           head * s.exponent_stride[2]];
+  return page * s.stride[0] + place * s.stride[1] + head * s.stride[2];
+}
+
+// Whether some value of a request's keys [from, to), in rows of whole 16-byte words, may be
+// infinite or NaN; a lane a key.
+__device__ __forceinline__ bool some_odd(const AttendParams& p, int32_t request, int32_t head,
+                                         int32_t from, int32_t to) {
+  const int words = p.head_dim * (p.e4m3 ? 1 : 2) / 16;
+  uint32_t odd = 0;
+  for (int32_t key = from + (threadIdx.x & 31); key < to; key += 32) {
+    uint32_t exponent;
+    const int64_t at = value_at(p, request, head, key, &exponent);
+    if (at < 0) continue;
+    odd |= exponent > 246;   // (a product with 2^120 may be infinite)
+    const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.value.data) +
+                                                      at * (p.e4m3 ? 1 : 2));
+#pragma unroll 8
+    for (int i = 0; i < words; ++i) {
+      const uint4 v = row[i];
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+      // every exponent (and in 8 bits mantissa) bit set: one more carries
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        odd |= p.e4m3 ? ((w[j] & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u
+                      : ((w[j] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+    }
+  }
+  return __any_sync(0xffffffffu, odd != 0);
+}
+
+// Of `rows` of a warp (bit i: lane i's row, which sees `seen` keys), whose products took
+// in a request's keys up to `to`, those that a value out of their sight has spoilt: one
+// that is infinite or NaN, which a weight of 0 makes NaN.  A row that sees a NaN in the
+// same place of the head is NaN there by right; rows whose weights' sum is NaN are so in all
+// places, and not asked about.  Values' rows are whole 16-byte words.  (A prompt of 8192
+// tokens of 16 heads, whose first value is NaN: 298 us, without one 214; every row of
+// it computed again was some thousand times as long.)
+__device__ __noinline__ uint32_t spoilt_rows(const AttendParams& p, int32_t request, int32_t head,
+                                             uint32_t rows, int32_t seen, int32_t to) {
+  const int lane = threadIdx.x & 31;
+  const int32_t least = __reduce_min_sync(0xffffffffu, rows >> lane & 1 ? seen : to);
+  if (!some_odd(p, request, head, least, to)) return 0;
+  int32_t last[kSliceValues], nan[kSliceValues];  // key of the last such value, of the first NaN
+#pragma unroll
+  for (int i = 0; i < kSliceValues; ++i) {
+    last[i] = -1;
+    nan[i] = 0x7FFFFFFF;
+  }
+  // from the first row's own key on
+  for (int32_t base = least > 0 ? least - 1 : 0; base < to; base += 32) {
+    uint32_t exponent = kExponentBias;
+    const int64_t at =
+        base + lane < to ? value_at(p, request, head, base + lane, &exponent) : -1;
+#pragma unroll 4
+    for (int j = 0; j < 32; ++j) {
+      const int64_t from = __shfl_sync(0xffffffffu, at, j);
+      const float by = scale_of(__shfl_sync(0xffffffffu, exponent, j));
+#pragma unroll
+      for (int i = 0; i < kSliceValues; ++i) {
+        const int d = lane + 32 * i;
+        float v = 0.0f;
+        if (from >= 0 && d < p.head_dim)
+          v = p.e4m3 ? e4m3_to_f32(static_cast<const uint8_t*>(p.value.data)[from + d]) * by
+                     : bf16_to_f32(static_cast<const uint16_t*>(p.value.data)[from + d]);
+        const uint32_t size = __float_as_uint(v) & 0x7FFFFFFFu;
+        if (size >= 0x7F800000u) last[i] = base + j;
+        if (size > 0x7F800000u) nan[i] = min(nan[i], base + j);
+      }
+    }
+  }
+  uint32_t spoilt = 0;
+  for (uint32_t left = rows; left; left &= left - 1) {
+    const int who = __ffs(left) - 1;
+    const int32_t sees = __shfl_sync(0xffffffffu, seen, who);
+    bool some = false;
+#pragma unroll
+    for (int i = 0; i < kSliceValues; ++i) some |= last[i] >= sees && nan[i] >= sees;
+    if (__any_sync(0xffffffffu, some)) spoilt |= 1u << who;
+  }
+  return spoilt;
+}
+
 // ------------------------------------------------------------------------
 // How a call's work is dealt out.  A tile is up to kRows rows (new tokens by
 // query heads of one head of keys, token by token); a unit is p.unit_keys

@@ -139,7 +139,7 @@ struct Shared {
   int32_t seen[32];              // keys that a row sees
   // maxima of the values' weights and of the scores (bf16: the same), sums
   float most[kWarps][32], score[kWarps][32], sum[kWarps][32];
-  uint32_t again;                // rows to be computed again
+  uint32_t again;                // rows that something out of their sight may have spoilt
 };
 
 template <int kDim, int kBlocks, bool kE4m3>
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
         l += sh.sum[w][r] * since(sh.score[w][r], n);
         v += sums[(w * F::kRows + r) * F::kSumStride + d] * since(sh.most[w][r], m);
       }
-      if (differ && !(fabsf(v) + fabsf(l) < __uint_as_float(0x7F800000u)))
+      if (differ && l == l && !(fabsf(v) + fabsf(l) < __uint_as_float(0x7F800000u)))
         atomicOr(&sh.again, 1u << r);
       if (whole) {
         if (d < p.head_dim)
@@ -507,9 +507,12 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
       }
     }
     __syncthreads();
-    for (uint32_t again = sh.again; again; again &= again - 1) {
+    uint32_t again = sh.again & (0x11111111u << warp);   // this warp's
+    if (again)
+      again = spoilt_rows(p, seg.index, seg.head, again, sh.seen[lane],
+                          min(seg.to * kUnitKeys, seg.keys));
+    for (; again; again &= again - 1) {
       const int r = __ffs(again) - 1;
-      if (r % kWarps != warp) continue;
       Slice own;
       const int32_t to = min(seg.to * kUnitKeys, sh.seen[r]);
       warp_attend(p, query_row(p, seg.request.first, seg.head, row0 + r), seg.index, seg.head,

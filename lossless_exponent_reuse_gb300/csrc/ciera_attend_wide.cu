@@ -26,8 +26,9 @@
 //
 // A tile's last keys may lie in a page with others behind them, which hold
 // anything: those values are cleared in shared memory before the products.  What a row
-// does not see inside a unit has weight 0; where it is infinite or NaN the row is
-// computed again, value by value.
+// does not see inside a unit has weight 0; where a row came out infinite or NaN the
+// values between its last key and the half's are looked at, and where one of them is infinite
+// or NaN the row is computed again, value by value.
 #include "ciera_attend_device.cuh"
 #include "ciera_tc_device.cuh"
 
@@ -578,6 +579,40 @@ __device__ void ask(const AttendParams& p, const Maps& maps, Shared& sh, uint32_
 }
 
 // ------------------------------------------------------------------------
+// Of a warp's rows from `row` on, of which those of `odd` came out infinite or NaN: those
+// that something out of their sight has spoilt, over the keys [from, to), a warp a row.
+// `part`: where the first one's part of the sums lies; null: whole rows.
+__device__ __noinline__ void compute_again(const AttendParams& p, uint32_t* busy, int32_t request,
+                                           int32_t head, int32_t first, int32_t row, uint32_t odd,
+                                           int32_t seen, int32_t from, int32_t to, float* part) {
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) atomicAdd(busy, 1u);
+  __syncwarp();  // what each lane wrote of its own row is overwritten below
+  for (uint32_t again = spoilt_rows(p, request, head, odd, seen, to); again; again &= again - 1) {
+    const int who = __ffs(again) - 1;
+    Slice own;
+    warp_attend(p, query_row(p, first, head, row + who), request, head, from,
+                min(__shfl_sync(0xffffffffu, seen, who), to), &own);
+    uint16_t* out = output_row(p, first, head, row + who);
+#pragma unroll
+    for (int i = 0; i < kSliceValues; ++i) {
+      const int d = lane + 32 * i;
+      if (d >= p.head_dim) continue;
+      if (part)
+        part[who + (2 + d) * kTileRows] = own.o[i];
+      else
+        out[d] = f32_to_bf16(own.o[i] * inverse_sum(own.sum));
+    }
+    if (part && lane == 0) {
+      part[who] = own.most;
+      part[who + kTileRows] = own.sum;
+    }
+    __syncwarp();
+  }
+  if (lane == 0) atomicSub(busy, 1u);
+}
+
+// ------------------------------------------------------------------------
 // Four warps, a thread a row.  A unit's weights go in two steps of 64 keys, each
 // with its own look at the maximum, so that the first step's products run while
 // the second's weights are made: the chain from scores to weights and back is what
@@ -701,41 +736,19 @@ __device__ void soften(const AttendParams& p, Shared& sh, int t) {
             *reinterpret_cast<uint4*>(out + c) = pack8(f);
           }
       } else if (live) {
-        part[0] = top;
+        part[0] = sum == sum ? top : sum;   // (of NaN alone no maximum has come up)
         part[kTileRows] = sum;
 #pragma unroll
         for (int c = 0; c < kDim; ++c)
           if (c < p.head_dim) part[(2 + c) * kTileRows] = o[c];
       }
       tc_fence_before();
-      // ---- rows that something out of sight may have spoilt, a warp a row
-      const uint32_t spoilt =
-          __ballot_sync(0xffffffffu, live && !(size < __uint_as_float(0x7F800000u)));
-      if (spoilt && lane == 0) atomicAdd(&sh.busy, 1u);
-      for (uint32_t again = spoilt; again; again &= again - 1) {
-        const int who = __ffs(again) - 1;
-        const int32_t row = row0 + warp * 32 + who;
-        const int32_t to = min(__shfl_sync(0xffffffffu, seen, who), s.to * p.unit_keys);
-        Slice own;
-        warp_attend(p, query_row(p, s.request.first, s.head, row), s.index, s.head,
-                    s.from * p.unit_keys, to, &own);
-        float* its = part - lane + who;
-        uint16_t* there = output_row(p, s.request.first, s.head, row);
-        for (int i = 0; i < kDim / 32; ++i) {
-          const int d = lane + 32 * i;
-          if (d >= p.head_dim) continue;
-          if (whole)
-            there[d] = f32_to_bf16(own.o[i] * inverse_sum(own.sum));
-          else
-            its[(2 + d) * kTileRows] = own.o[i];
-        }
-        if (!whole && lane == 0) {
-          its[0] = own.most;
-          its[kTileRows] = own.sum;
-        }
-        __syncwarp();
-      }
-      if (spoilt && lane == 0) atomicSub(&sh.busy, 1u);
+      const uint32_t odd = __ballot_sync(
+          0xffffffffu, live && sum == sum && !(size < __uint_as_float(0x7F800000u)));
+      if (odd)
+        compute_again(p, &sh.busy, s.index, s.head, s.request.first, row0 + warp * 32, odd, seen,
+                      s.from * p.unit_keys, min((s.from + units) * p.unit_keys, s.keys),
+                      whole ? nullptr : part - lane);
     } else if (live && whole) {
       for (int c = 0; c < p.head_dim; c += 8)
         *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);

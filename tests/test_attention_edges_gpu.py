@@ -1,0 +1,103 @@
+"""Attention over pages at its edges: values out of a row's sight and what looking at
+them costs, rows and powers of two of any magnitude, tiles longer than a wait's limit,
+8-bit pages behind 32 bits."""
+import math
+
+import pytest
+import torch
+
+import attention_reference as ref
+from attention_reference import BF16, ints, rand
+from lossless_exponent_reuse_gb300 import attention, ciera, experts
+from test_attention_gpu import batch
+
+pytestmark = pytest.mark.gpu
+
+
+def places(table, page, keys):
+    keys = torch.as_tensor(keys, device="cuda")
+    return table[0].long()[keys // page], keys % page
+
+
+def put(cache, slot, head, d, bad):
+    """``bad`` in the values of some keys; of 8 bits NaN by value, or by exponent where d
+    is None."""
+    if cache.value_exponent is None:
+        cache.value[(*slot, head, slice(None) if d is None else d)] = bad
+    elif d is None:
+        cache.value_exponent[(*slot, head)] = 255
+    else:
+        cache.value.view(torch.uint8)[(*slot, head, d)] = 0xFF
+
+
+# tokens, page, size of a head, query heads to two: rows by tcgen05, by few rows, one by one
+FORMS = [(300, 16, 128, 2), (140, 24, 64, 6), (300, 20, 80, 4), (7, 16, 128, 4), (9, 20, 256, 2),
+         (12, 1, 64, 4), (12, 16, 66, 2)]
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("new,page,dim,q_heads", FORMS)
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+def test_values_in_sight_and_out_of_it(new, page, dim, q_heads, bad, e4m3):
+    """The same place of the head and another one, NaN or infinite for all rows, for the
+    last ones, for every key: each row has what it sees, no more and no less."""
+    if e4m3 and bad == math.inf:
+        pytest.skip("e4m3 has no infinity")
+    cached = 190
+    L = cached + new
+    last = [L - 1, L - 2, L - 5]
+    cases = [
+        [([0], 3, bad)],                                     # all see it
+        [([0], 3, bad), (last, 3, bad)],                     # and more of it out of sight
+        [([0], 3, bad), (last, 5, bad)],                     # another place out of sight
+        [([L - new // 2], dim - 1, bad), ([0], 0, bad)],
+        [(range(L), 7, bad)],                                # in every key
+        [(range(L), 7, bad), (last, 8, bad)],
+        [(range(cached, L, 3), 2, bad)],
+        [([L - 1], None, bad)],                              # a whole row
+    ]
+    for marks in cases:
+        q, cache, table, offsets, context = batch([new], [cached], q_heads, 2, dim, page, e4m3=e4m3)
+        for keys, d, value in marks:
+            put(cache, places(table, page, list(keys)), 1, d, value)
+        got = attention.attend(q, cache, table, offsets, context)
+        ref.check_attend(got, q, cache, table, offsets, context, what=marks)
+        assert torch.isfinite(got[:, :q_heads // 2]).all()
+    assert experts.status() == ciera.OK
+
+
+def microseconds(fn, n=5):
+    fn()
+    best = math.inf
+    for _ in range(3):
+        a, b = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        a.record()
+        for _ in range(n):
+            fn()
+        b.record()
+        torch.cuda.synchronize()
+        best = min(best, a.elapsed_time(b) / n * 1000)
+    return best
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("new,cached", [(4096, 0), (512, 8192), (4, 8192)])
+def test_a_nan_in_sight_costs_little(new, cached, e4m3):
+    """One NaN that every row sees, or one in the same place of every key: no row is
+    computed again, which would take some thousand times as long."""
+    heads, dim, page = 16, 128, 16
+    L = cached + new
+    cache, table = ref.paged([L], page, heads, dim, e4m3=e4m3)
+    q, off, context = rand(new, heads, dim, seed=3), ints([0, new]), ints([L])
+    call = lambda: attention.attend(q, cache, table, off, context)
+    clean = microseconds(call)
+    put(cache, places(table, page, [0]), slice(None), 0, math.nan)
+    assert microseconds(call) < 20 * clean
+    got = call()
+    assert torch.isnan(got[:, :, 0]).all() and torch.isfinite(got[:, :, 1:]).all()
+    put(cache, tuple(x[:, None] for x in places(table, page, range(L))),
+        torch.arange(heads, device="cuda"), 1, math.nan)
+    assert microseconds(call) < 20 * clean
+    got = call()
+    assert torch.isnan(got[:, :, :2]).all() and torch.isfinite(got[:, :, 2:]).all()
+    assert experts.status() == ciera.OK
