@@ -805,7 +805,7 @@ int64_t ciera_attend_workspace_bytes(int64_t q_heads, int64_t heads, int64_t hea
  * 2^119 / L may overflow.  Where rows that see different keys are computed together, a
  * row that is infinite or NaN, and has a value that is infinite or NaN among the keys behind its
  * own, is computed again, value by value (not where it sees a NaN in the same place
- * of the head).
+ * of the head): 0.2 us a key that it sees, up to 32 rows one after the other.
  *   q_dev        tokens x q_heads x head_dim bf16
  *   table_dev    requests x width pages, rows table_stride apart
  *   offsets_dev  requests + 1

@@ -6,9 +6,9 @@ namespace ciera {
 namespace {
 
 constexpr int kAnyWarps = 4;
-// A warp per row (token and query head), a key at a time.  Bound by its
-// instructions: right for every layout, not fast (one token of 4096 keys, 16 heads, 6.8
-// ms; the form for few rows takes 15 us).
+// A warp per row (token and query head).  Bound by the latency of its loads: right for
+// every layout, not fast (one token of 4096 keys, 16 heads of 127 values, 1.15 ms, of 72 of
+// 8 bits 1.7; the form for few rows takes 15 us of heads of 128).
 __global__ void __launch_bounds__(32 * kAnyWarps) k_attend_any(const AttendParams p) {
   const int64_t row = static_cast<int64_t>(blockIdx.x) * kAnyWarps + (threadIdx.x >> 5);
   const int heads = p.heads * p.group;
@@ -20,8 +20,11 @@ __global__ void __launch_bounds__(32 * kAnyWarps) k_attend_any(const AttendParam
   find_row(p, static_cast<int32_t>(t), &request, &place);
   if (request >= 0) {
     const Request r = request_of(p, request);
-    warp_attend(p, p.q + t * p.q_token + head * p.q_head, request, head / p.group, 0,
-                seen_keys(r, place), &own);
+    const uint16_t* q = p.q + t * p.q_token + head * p.q_head;
+    if (p.e4m3)
+      warp_attend<kSliceValues, true>(p, q, request, head / p.group, 0, seen_keys(r, place), &own);
+    else
+      warp_attend<kSliceValues, false>(p, q, request, head / p.group, 0, seen_keys(r, place), &own);
   }
   const float by = inverse_sum(own.sum);
   uint16_t* o = p.o + row * p.head_dim;

@@ -69,6 +69,62 @@ __device__ __forceinline__ float scale_of(uint32_t exponent) {
   return __uint_as_float(exponent == 255 ? 0x7FC00000u : exponent ? exponent << 23 : 0x00400000u);
 }
 
+// Where a request's key or value starts; -1: nowhere, zeros.  *exponent: of 8 bits.
+__device__ __forceinline__ int64_t place_of(const AttendParams& p, const Side& s, int32_t request,
+                                            int32_t head, int32_t key, uint32_t* exponent) {
+  const int32_t index = p.by_page(key), page = page_at(p, request, index);
+  *exponent = kExponentBias;
+  if (page < 0) return -1;
+  const int32_t place = key - index * p.page_size;
+  if (p.e4m3)
+    *exponent = s.exponent[page * s.exponent_stride[0] + place * s.exponent_stride[1] +
+                           head * s.exponent_stride[2]];
+  return page * s.stride[0] + place * s.stride[1] + head * s.stride[2];
+}
+
+__device__ __forceinline__ bool whole_words(const AttendParams& p, const Side& s) {
+  const int64_t size = p.e4m3 ? 1 : 2;
+  return ((reinterpret_cast<uintptr_t>(s.data) | s.stride[0] * size | s.stride[1] * size |
+           s.stride[2] * size | p.head_dim * size) & 15) == 0;
+}
+
+// Values d .. d + 31 of a row of 16-byte words, or of any; zeros behind the head's last, and
+// of no row.  `some`: a row of queries, which is read in place of what is not there: loads that
+// nothing depends on go out together.
+template <bool kE4m3>
+__device__ __forceinline__ void values32(const AttendParams& p, const Side& s, int64_t at,
+                                         const uint16_t* some, int d, bool words, float (&f)[32]) {
+  constexpr int kSize = kE4m3 ? 1 : 2, kEach = 16 / kSize;
+  const uint8_t* own = reinterpret_cast<const uint8_t*>(some);
+  const uint8_t* row = at >= 0 ? static_cast<const uint8_t*>(s.data) + at * kSize : own;
+  if (words) {
+    uint32_t v[32 / kEach * 4];
+#pragma unroll
+    for (int i = 0; i < 32 / kEach; ++i) {
+      uint4 w = make_uint4(0, 0, 0, 0);
+      if (at >= 0 && d + i * kEach < p.head_dim)
+        w = *reinterpret_cast<const uint4*>(row + (d + i * kEach) * kSize);
+      v[4 * i] = w.x;
+      v[4 * i + 1] = w.y;
+      v[4 * i + 2] = w.z;
+      v[4 * i + 3] = w.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      f[i] = kE4m3 ? e4m3_to_f32(static_cast<uint8_t>(v[i / 4] >> (i % 4 * 8)))
+                   : i % 2 ? bf16_hi(v[i / 2]) : bf16_lo(v[i / 2]);
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i) {
+    const int c = min(d + i, p.head_dim - 1);
+    f[i] = kE4m3 ? e4m3_to_f32(row[c]) : bf16_to_f32(reinterpret_cast<const uint16_t*>(row)[c]);
+  }
+#pragma unroll
+  for (int i = 0; i < 32; ++i)
+    if (at < 0 || d + i >= p.head_dim) f[i] = 0.0f;
+}
+
 // A warp's share of one row: values lane, lane + 32, ... of the head.
 struct Slice {
   float most;      // of the scores so far, in powers of two
@@ -76,85 +132,84 @@ struct Slice {
   float o[kSliceValues];
 };
 
-// Row `q` over the keys [from, to) of a request, value by value in 32 bits.
-// Keys outside have no part in it.  own->sum 0: no keys.
+// Row `q` over the keys [from, to) of a request, value by value in 32 bits, of heads
+// of up to 32 kValues values.  Keys outside have no part in it.  own->sum 0: no keys.
+// 32 keys at a time: a lane a key for the scores, then a key after the other, a lane
+// some of its values, eight keys' loads at once: 0.2 us a key (a key at a time 1.2 to 1.7; a
+// prompt of 8192 tokens of 16 heads, whose last value is NaN, 325 and 56 ms).
+template <int kValues, bool kE4m3>
 __device__ __noinline__ void warp_attend(const AttendParams& p, const uint16_t* q, int32_t request,
                                          int32_t head, int32_t from, int32_t to, Slice* own) {
+  constexpr int kSize = kE4m3 ? 1 : 2, kAtOnce = 8;
   const int lane = threadIdx.x & 31;
-  float qv[kSliceValues], o[kSliceValues];
-  float top = minus_infinity(), sum = 0.0f;
-#pragma unroll
-  for (int i = 0; i < kSliceValues; ++i) {
-    const int d = lane + 32 * i;
-    qv[i] = d < p.head_dim ? bf16_to_f32(q[d]) : 0.0f;
-    o[i] = 0.0f;
-  }
+  const bool words = whole_words(p, p.key);
   const float scale = p.scale * kLog2e;
-  int32_t page = -1, index = -1;
-  for (int32_t key = from; key < to; ++key) {
-    const int32_t at = p.by_page(key);
-    if (at != index) {
-      index = at;
-      page = page_at(p, request, at);
+  const uint8_t* values = static_cast<const uint8_t*>(p.value.data);
+  const uint8_t* some = reinterpret_cast<const uint8_t*>(q);
+  float o[kValues] = {};
+  float top = minus_infinity(), sum = 0.0f;   // sum: of this lane's keys
+  for (int32_t base = from; base < to; base += 32) {
+    const int32_t key = base + lane, n = to - base < 32 ? to - base : 32;
+    uint32_t ke = kExponentBias, ve = kExponentBias;
+    int64_t kat = -1, vat = -1;
+    if (key < to) {
+      kat = place_of(p, p.key, request, head, key, &ke);
+      vat = place_of(p, p.value, request, head, key, &ve);
     }
-    const int32_t place = key - at * p.page_size;
-    float k[kSliceValues] = {}, v[kSliceValues] = {}, dot = 0.0f;
-    if (page >= 0) {
-      const Side &ks = p.key, &vs = p.value;
-      const int64_t kat = page * ks.stride[0] + place * ks.stride[1] + head * ks.stride[2];
-      const int64_t vat = page * vs.stride[0] + place * vs.stride[1] + head * vs.stride[2];
-      float k_scale = 1.0f, v_scale = 1.0f;
-      if (p.e4m3) {
-        k_scale = scale_of(ks.exponent[page * ks.exponent_stride[0] +
-                                       place * ks.exponent_stride[1] +
-                                       head * ks.exponent_stride[2]]);
-        v_scale = scale_of(vs.exponent[page * vs.exponent_stride[0] +
-                                       place * vs.exponent_stride[1] +
-                                       head * vs.exponent_stride[2]]);
-      }
+    float dot = 0.0f;
+    const float by = scale_of(ke);
+#pragma unroll 1
+    for (int d = 0; d < p.head_dim; d += 32) {
+      float k[32], x[32];
+      values32<kE4m3>(p, p.key, kat, q, d, words, k);
 #pragma unroll
-      for (int i = 0; i < kSliceValues; ++i) {
-        const int d = lane + 32 * i;
-        if (d < p.head_dim) {
-          if (p.e4m3) {
-            k[i] = e4m3_to_f32(static_cast<const uint8_t*>(ks.data)[kat + d]) * k_scale;
-            v[i] = e4m3_to_f32(static_cast<const uint8_t*>(vs.data)[vat + d]) * v_scale;
-          } else {
-            k[i] = bf16_to_f32(static_cast<const uint16_t*>(ks.data)[kat + d]);
-            v[i] = bf16_to_f32(static_cast<const uint16_t*>(vs.data)[vat + d]);
-          }
-          dot += qv[i] * k[i];
-        }
-      }
+      for (int i = 0; i < 32; ++i) x[i] = bf16_to_f32(q[min(d + i, p.head_dim - 1)]);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) dot += d + i < p.head_dim ? x[i] * (k[i] * by) : 0.0f;
     }
-    const float score = warp_sum_f32(dot) * scale;
-    const float most = score > top || score != score ? score : top;
+    const float score = key < to ? dot * scale : minus_infinity();
+    float most = fmaxf(score, top);   // (of NaN and a number: the number)
+#pragma unroll
+    for (int i = 16; i > 0; i >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, i));
+    if (__any_sync(0xffffffffu, score != score || top != top)) most = __uint_as_float(0x7FC00000u);
     // (of scores of minus infinity alone no weight is 0 / 0)
-    const float base = most == minus_infinity() ? 0.0f : most;
-    const float old = exp2f(top - base), w = exp2f(score - base);
+    const float zero = most == minus_infinity() ? 0.0f : most;
+    const float old = exp2f(top - zero), w = exp2f(score - zero);
     top = most;
     sum = sum * old + w;
 #pragma unroll
-    for (int i = 0; i < kSliceValues; ++i) o[i] = o[i] * old + w * v[i];
+    for (int i = 0; i < kValues; ++i) o[i] *= old;
+#pragma unroll 1
+    for (int j0 = 0; j0 < n; j0 += kAtOnce) {   // (keys behind the last weigh 0)
+      uint32_t raw[kAtOnce][kValues];
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const int64_t at = __shfl_sync(0xffffffffu, vat, j0 + j);
+        const uint8_t* row = at >= 0 ? values + at * kSize : some;
+#pragma unroll
+        for (int i = 0; i < kValues; ++i) {
+          const int d = min(lane + 32 * i, p.head_dim - 1);
+          raw[j][i] = kE4m3 ? row[d] : reinterpret_cast<const uint16_t*>(row)[d];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < kAtOnce; ++j) {
+        const bool there = __shfl_sync(0xffffffffu, vat, j0 + j) >= 0;
+        const float weight = __shfl_sync(0xffffffffu, w, j0 + j);
+        const float its = scale_of(__shfl_sync(0xffffffffu, ve, j0 + j));
+#pragma unroll
+        for (int i = 0; i < kValues; ++i) {
+          const float v = kE4m3 ? e4m3_to_f32(static_cast<uint8_t>(raw[j][i])) * its
+                                : bf16_to_f32(raw[j][i]);
+          o[i] += weight * (there ? v : 0.0f);
+        }
+      }
+    }
   }
   own->most = top;
-  own->sum = sum;
+  own->sum = warp_sum_f32(sum);
 #pragma unroll
-  for (int i = 0; i < kSliceValues; ++i) own->o[i] = o[i];
-}
-
-// Where a request's value starts; -1: nowhere, zeros.  *exponent: of 8 bits.
-__device__ __forceinline__ int64_t value_at(const AttendParams& p, int32_t request, int32_t head,
-                                            int32_t key, uint32_t* exponent) {
-  const int32_t index = p.by_page(key), page = page_at(p, request, index);
-  *exponent = kExponentBias;
-  if (page < 0) return -1;
-  const int32_t place = key - index * p.page_size;
-  const Side& s = p.value;
-  if (p.e4m3)
-    *exponent = s.exponent[page * s.exponent_stride[0] + place * s.exponent_stride[1] +
-                           head * s.exponent_stride[2]];
-  return page * s.stride[0] + place * s.stride[1] + head * s.stride[2];
+  for (int i = 0; i < kValues; ++i) own->o[i] = o[i];
 }
 
 // Whether some value of a request's keys [from, to), in rows of whole 16-byte words, may be
@@ -165,7 +220,7 @@ __device__ __forceinline__ bool some_odd(const AttendParams& p, int32_t request,
   uint32_t odd = 0;
   for (int32_t key = from + (threadIdx.x & 31); key < to; key += 32) {
     uint32_t exponent;
-    const int64_t at = value_at(p, request, head, key, &exponent);
+    const int64_t at = place_of(p, p.value, request, head, key, &exponent);
     if (at < 0) continue;
     odd |= exponent > 246;   // (a product with 2^120 may be infinite)
     const uint4* row = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(p.value.data) +
@@ -206,7 +261,7 @@ __device__ __noinline__ uint32_t spoilt_rows(const AttendParams& p, int32_t requ
   for (int32_t base = least > 0 ? least - 1 : 0; base < to; base += 32) {
     uint32_t exponent = kExponentBias;
     const int64_t at =
-        base + lane < to ? value_at(p, request, head, base + lane, &exponent) : -1;
+        base + lane < to ? place_of(p, p.value, request, head, base + lane, &exponent) : -1;
 #pragma unroll 4
     for (int j = 0; j < 32; ++j) {
       const int64_t from = __shfl_sync(0xffffffffu, at, j);

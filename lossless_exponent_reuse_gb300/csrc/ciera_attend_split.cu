@@ -143,7 +143,8 @@ struct Shared {
 };
 
 template <int kDim, int kBlocks, bool kE4m3>
-__global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p) {
+__global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm))
+    k_attend_split(const AttendParams p) {
   using F = Form<kDim, kBlocks, kE4m3>;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ Shared sh;
@@ -515,11 +516,11 @@ __global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p)
       const int r = __ffs(again) - 1;
       Slice own;
       const int32_t to = min(seg.to * kUnitKeys, sh.seen[r]);
-      warp_attend(p, query_row(p, seg.request.first, seg.head, row0 + r), seg.index, seg.head,
-                  seg.from * kUnitKeys, to, &own);
+      warp_attend<kDim / 32, kE4m3>(p, query_row(p, seg.request.first, seg.head, row0 + r),
+                                    seg.index, seg.head, seg.from * kUnitKeys, to, &own);
       uint16_t* out = output_row(p, seg.request.first, seg.head, row0 + r);
 #pragma unroll
-      for (int i = 0; i < kSliceValues; ++i) {
+      for (int i = 0; i < kDim / 32; ++i) {
         const int d = lane + 32 * i;
         if (d >= p.head_dim) continue;
         if (whole)

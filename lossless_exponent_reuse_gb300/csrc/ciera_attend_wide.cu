@@ -582,6 +582,7 @@ __device__ void ask(const AttendParams& p, const Maps& maps, Shared& sh, uint32_
 // Of a warp's rows from `row` on, of which those of `odd` came out infinite or NaN: those
 // that something out of their sight has spoilt, over the keys [from, to), a warp a row.
 // `part`: where the first one's part of the sums lies; null: whole rows.
+template <int kDim, bool kE4m3>
 __device__ __noinline__ void compute_again(const AttendParams& p, uint32_t* busy, int32_t request,
                                            int32_t head, int32_t first, int32_t row, uint32_t odd,
                                            int32_t seen, int32_t from, int32_t to, float* part) {
@@ -591,11 +592,11 @@ __device__ __noinline__ void compute_again(const AttendParams& p, uint32_t* busy
   for (uint32_t again = spoilt_rows(p, request, head, odd, seen, to); again; again &= again - 1) {
     const int who = __ffs(again) - 1;
     Slice own;
-    warp_attend(p, query_row(p, first, head, row + who), request, head, from,
-                min(__shfl_sync(0xffffffffu, seen, who), to), &own);
+    warp_attend<kDim / 32, kE4m3>(p, query_row(p, first, head, row + who), request, head, from,
+                                  min(__shfl_sync(0xffffffffu, seen, who), to), &own);
     uint16_t* out = output_row(p, first, head, row + who);
 #pragma unroll
-    for (int i = 0; i < kSliceValues; ++i) {
+    for (int i = 0; i < kDim / 32; ++i) {
       const int d = lane + 32 * i;
       if (d >= p.head_dim) continue;
       if (part)
@@ -618,7 +619,7 @@ __device__ __noinline__ void compute_again(const AttendParams& p, uint32_t* busy
 // the second's weights are made: the chain from scores to weights and back is what
 // bounds a unit (scores 130 cycles out of TMEM, 64 weights some 330, 130 to
 // TMEM and the products' start; products of a half 1024).
-template <int kDim>
+template <int kDim, bool kE4m3>
 __device__ void soften(const AttendParams& p, Shared& sh, int t) {
   using F = Form<kDim>;
   const int lane = threadIdx.x & 31, tid = threadIdx.x & (kHalf - 1), warp = tid >> 5;
@@ -746,9 +747,10 @@ __device__ void soften(const AttendParams& p, Shared& sh, int t) {
       const uint32_t odd = __ballot_sync(
           0xffffffffu, live && sum == sum && !(size < __uint_as_float(0x7F800000u)));
       if (odd)
-        compute_again(p, &sh.busy, s.index, s.head, s.request.first, row0 + warp * 32, odd, seen,
-                      s.from * p.unit_keys, min((s.from + units) * p.unit_keys, s.keys),
-                      whole ? nullptr : part - lane);
+        compute_again<kDim, kE4m3>(p, &sh.busy, s.index, s.head, s.request.first, row0 + warp * 32,
+                                   odd, seen, s.from * p.unit_keys,
+                                   min((s.from + units) * p.unit_keys, s.keys),
+                                   whole ? nullptr : part - lane);
     } else if (live && whole) {
       for (int c = 0; c < p.head_dim; c += 8)
         *reinterpret_cast<uint4*>(out + c) = make_uint4(0, 0, 0, 0);
@@ -823,7 +825,7 @@ __global__ void __launch_bounds__(Form<kDim, kE4m3>::kThreads, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
     else
       asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-    soften<kDim>(p, sh, warp / 4);
+    soften<kDim, kE4m3>(p, sh, warp / 4);
   } else {
     if (kE4m3)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");

@@ -101,3 +101,33 @@ def test_a_nan_in_sight_costs_little(new, cached, e4m3):
     got = call()
     assert torch.isnan(got[:, :, :2]).all() and torch.isfinite(got[:, :, 2:]).all()
     assert experts.status() == ciera.OK
+
+
+@pytest.mark.parametrize("dim,e4m3,page", [(66, False, 16), (129, False, 5), (7, False, 1), (72, True, 16),
+                                           (250, True, 20), (33, True, 3)])
+def test_rows_one_by_one(dim, e4m3, page):
+    """Heads that no other form takes: lengths around the keys of a step, pages that are
+    not there, queries and keys that are infinite or NaN."""
+    lengths = [1, 31, 32, 33, 63, 64, 65, 100]
+    new = [1, 3, 1, 33, 1, 2, 1, 40]
+    args = [new, [n - k for n, k in zip(lengths, new)], 4, 2, dim, page]
+    q, cache, table, off, context = batch(*args, e4m3=e4m3)
+    got = attention.attend(q, cache, table, off, context)
+    ref.check_attend(got, q, cache, table, off, context, what=(dim, e4m3, page))
+    table[7, 1], table[3, 0] = -1, cache.key.shape[0]
+    got = attention.attend(q, cache, table, off, context)
+    ref.check_attend(got, q, cache, table, off, context, what=(dim, e4m3, page))
+    clean = got.clone()
+    # scores of plus and minus infinity, and of NaN, in rows of their own
+    last, first = int(off[-1]) - 1, int(off[3])
+    q[last, 0, -1], q[last - 1, 3, 0], q[first, 2] = math.inf, -math.inf, math.nan
+    if e4m3:
+        cache.key_exponent[table[6, 0].long(), 0, 1] = 255
+    else:
+        cache.key[table[6, 0].long(), 0, 1, 0] = math.nan
+    got = attention.attend(q, cache, table, off, context)
+    row = int(off[6])
+    odd = torch.zeros_like(got, dtype=torch.bool)
+    odd[last, 0] = odd[last - 1, 3] = odd[first, 2] = odd[row, 2] = odd[row, 3] = True
+    assert torch.isnan(got[odd]).all() and torch.equal(got[~odd], clean[~odd])
+    assert experts.status() == ciera.OK
