@@ -802,7 +802,8 @@ int64_t ciera_attend_workspace_bytes(int64_t q_heads, int64_t heads, int64_t hea
  * h / (q_heads / heads).  Weights are rounded to 16 bits (8 significant) on
  * their way to the tensor cores, sums and maxima held in 32; weights up to 2^8 times
  * values are summed before they are divided by the weights' sum, which values above
- * 2^119 / L may overflow.  Where rows that see different keys are computed together, a
+ * 2^119 / L may overflow.  Of 8-bit rows a weight times its value's power of two counts where
+ * it is 2^-126 of the largest such or more.  Where rows that see different keys are computed together, a
  * row that is infinite or NaN, and has a value that is infinite or NaN among the keys behind its
  * own, is computed again, value by value (not where it sees a NaN in the same place
  * of the head): 0.2 us a key that it sees, up to 32 rows one after the other.

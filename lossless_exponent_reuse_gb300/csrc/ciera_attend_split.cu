@@ -15,8 +15,12 @@
 // (ldmatrix).  mma.sync does: at the rate of memory it is idle.
 //
 // e4m3 keys are widened to fp16, which holds them exactly, on their way into the
-// fragments; queries are fp16 too, scaled by a power of two per row (an error of
-// 2^-25 of a row's largest value at most).  A key's exponent goes on its scores.
+// fragments; queries are fp16 too, scaled by a power of two per row that brings its
+// largest finite value to 2^13 or more, so that they lose 2^-38 of it at most (of a row
+// whose largest is below 2^-113, which the power's range stops short, 2^-25 of it, and of
+// one of bf16's subnormals 2^-18).  A key's exponent goes on its scores; where a row's power
+// is beyond 2^+-60, between two halves of that, so that nothing on the way is larger,
+// or smaller, than both the product and the score.
 // Values go to bf16, whose weights have the range that rows of any exponents
 // want: a value's exponent goes on its weight's before a maximum of their own is
 // taken (the sum has the scores' maximum).
@@ -135,7 +139,9 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
 struct Shared {
   Share share;
   int64_t part[kWarps + 1];
-  float query_scale[32];
+  float query_scale[32];         // of a score, the row's power of two, or half of it, included
+  float query_power[32];         // the other half
+  uint32_t halves;               // some row has halves
   int32_t seen[32];              // keys that a row sees
   // maxima of the values' weights and of the scores (bf16: the same), sums
   float most[kWarps][32], score[kWarps][32], sum[kWarps][32];
@@ -158,6 +164,7 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
   Joint* joint = reinterpret_cast<Joint*>(p.workspace) + block;
   float* parts = reinterpret_cast<float*>(reinterpret_cast<Joint*>(p.workspace) + blocks);
 
+  if (threadIdx.x == 0) sh.halves = 0;
   find_share<F::kRows, kThreads>(p, block, blocks, sh.part, &sh.share);
   Walk<F::kRows> walk(p, sh.share);
   Segment seg;
@@ -173,21 +180,25 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
       const bool live = r < seg.rows;
       const uint16_t* q = query_row(p, seg.request.first, seg.head, row0 + (live ? r : 0));
       uint16_t v[kDim / 32];
-      uint32_t most = 0;
+      uint32_t most = 0;         // of the finite values
 #pragma unroll
       for (int i = 0; i < kDim / 32; ++i) {
         const int d = lane + 32 * i;
         v[i] = live && d < p.head_dim ? q[d] : 0;
-        most = max(most, static_cast<uint32_t>(v[i] & 0x7FFF));
+        const uint32_t size = v[i] & 0x7FFFu;
+        most = max(most, size < 0x7F80u ? size : 0);
       }
-      float by = 1.0f, scale = p.scale * kLog2e;
+      float by = 1.0f, scale = p.scale * kLog2e, power = 1.0f;
       if (kE4m3) {
         // the largest value to 2^13 .. 2^14
         most = __reduce_max_sync(0xffffffffu, most);
         int e = static_cast<int>(most >> 7) - 127 - 13;
-        e = most >= 0x7F80u ? 0 : e < -100 ? -100 : e;
+        e = most == 0 ? 0 : e < -126 ? -126 : e;
         by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        scale *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        const int rest = e < -60 || e > 60 ? e / 2 : 0;
+        scale *= __uint_as_float(static_cast<uint32_t>(127 + e - rest) << 23);
+        power = __uint_as_float(static_cast<uint32_t>(127 + rest) << 23);
+        if (rest && lane == 0) sh.halves = 1;
       }
 #pragma unroll
       for (int i = 0; i < kDim / 32; ++i) {
@@ -197,6 +208,7 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
       }
       if (lane == 0) {
         sh.query_scale[r] = scale;
+        sh.query_power[r] = power;
         sh.seen[r] = live ? seen_keys(seg.request, p.by_group(row0 + r)) : 0;
       }
     }
@@ -238,6 +250,7 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
           query(s, b, qf[F::kKeep ? s : 0][F::kKeep ? b : 0][0],
                 qf[F::kKeep ? s : 0][F::kKeep ? b : 0][1]);
     float o[F::kSteps][kBlocks][4] = {};
+    const bool halves = kE4m3 && sh.halves;
 
     // ---- this warp's units
     const int units = seg.to - seg.from;
@@ -352,14 +365,26 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
         exponent = exponent_of(u + 1);
       }
       const bool masked = key0 + u * kUnitKeys + kWarpKeys > least;
+#pragma unroll
+      for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s[b][i] *= scale[b][i & 1];
+          if (kE4m3) s[b][i] *= key_scale[i >> 1];
+        }
+      if (halves) {
+#pragma unroll
+        for (int b = 0; b < kBlocks; ++b)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[b][i] *= sh.query_power[b * 8 + 2 * column + (i & 1)];
+      }
       bool rises = false;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int j = i & 1, k = i >> 1;
-          float t = s[b][i] * scale[b][j];
-          if (kE4m3) t *= key_scale[k];
+          float t = s[b][i];
           if (masked && key + 8 * k >= seen[b][j]) t = minus_infinity();
           s[b][i] = t;
           rises |= t > high[b][j] + kSlack;
@@ -453,6 +478,7 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
 
     // ---- the warps' sums, through the ring's memory
     __syncthreads();
+    if (threadIdx.x == 0) sh.halves = 0;   // (all have read it)
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll

@@ -131,3 +131,31 @@ def test_rows_one_by_one(dim, e4m3, page):
     odd[last, 0] = odd[last - 1, 3] = odd[first, 2] = odd[row, 2] = odd[row, 3] = True
     assert torch.isnan(got[odd]).all() and torch.equal(got[~odd], clean[~odd])
     assert experts.status() == ciera.OK
+
+
+@pytest.mark.parametrize("new,page,dim,q_heads", [(1, 16, 128, 4), (3, 20, 64, 4), (5, 16, 256, 2),
+                                                  (16, 16, 128, 2), (150, 16, 128, 4), (4, 16, 72, 2)])
+@pytest.mark.parametrize("q_power,k_power", [(124, -124), (100, -100), (40, -40), (-60, 60), (-100, 100),
+                                             (-113, 113), (-119, 119), (-124, 119)])
+def test_queries_of_any_magnitude(new, page, dim, q_heads, q_power, k_power):
+    """8-bit keys whose powers of two make up for the queries': every form has the same
+    scores, and rows of other magnitudes beside them their own."""
+    L, heads = new + 150, 2
+    rows = lambda kind, r, n: rand(n, heads, dim, seed=70 + kind, dtype=torch.float32) / 64
+    cache, table = ref.paged([L], page, heads, dim, e4m3=True, value=rows)
+    slot = places(table, page, range(L))
+    cache.key_exponent[slot] = 127 + k_power
+    q = (rand(new, q_heads, dim, seed=5, dtype=torch.float64).clamp(-3, 3) * 2.0 ** q_power).to(BF16)
+    q[0, 0, :3] *= 2.0 ** -7               # within a row too
+    q[0, 1] = 0
+    off, context = ints([0, new]), ints([L])
+    for scale in (None, 4.0):
+        got = attention.attend(q, cache, table, off, context, scale=scale)
+        ref.check_attend(got, q, cache, table, off, context, scale, what=(new, dim, q_power))
+    # a value that is infinite, among large and small ones: every score minus infinity
+    key = cache.key.view(torch.uint8)
+    key[(*slot, 0, 0)] = 0x38
+    q[0, 0, 0] = -math.inf
+    got = attention.attend(q, cache, table, off, context)
+    assert (got[0, 0] == 0).all() and torch.isfinite(got).all()
+    assert experts.status() == ciera.OK
