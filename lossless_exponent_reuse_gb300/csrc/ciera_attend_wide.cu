@@ -387,6 +387,10 @@ __device__ void widen(const AttendParams& p, Shared& sh, unsigned char* ring, un
       }
     }
   }
+  // the products' last word on each stage comes by itself: it has come before this
+  // block's shared memory is another's
+  for (int i = at > F::kStages ? at - F::kStages : 0; warp == 0 && i < at; ++i)
+    if (!wait(p, sh, &sh.empty[i % F::kStages], (i / F::kStages) & 1)) return;
 }
 
 // ------------------------------------------------------------------------
@@ -758,6 +762,8 @@ __device__ void soften(const AttendParams& p, Shared& sh, int t) {
       part[0] = minus_infinity();   // the join looks no further
     }
   }
+  // (the second step's is waited for above; the first step's has come too)
+  if (done > 0) wait(p, sh, &sh.output[t][0], (done - 1) & 1);
 }
 
 // One lane: what the launch that joins has to know of the block's last tile.
