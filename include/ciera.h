@@ -430,7 +430,8 @@ int ciera_get_cost_model(ciera_cost_model *model);
 
 /* Limit of every bounded device-side wait, in nanoseconds (default 1 s).
  * A grouped product waits for a tile's whole contraction at once: 1 s is some
- * 2 * 10^8 rows of one expert's weights' gradient.
+ * 2 * 10^8 rows of one expert's weights' gradient.  Attention's tiles may take longer: there
+ * it is counted from when the keys' and values' loads last went on.
  * Errors: CIERA_E_INVAL for 0. */
 int ciera_set_wait_timeout_ns(uint64_t ns);
 

@@ -85,19 +85,30 @@ struct Shared {
   uint32_t stop;           // a wait ran out: every role leaves
   uint32_t busy;           // warps that compute rows again: nobody's wait runs out meanwhile
   int32_t issued;          // loads
+  int32_t moved[2];        // loads of keys, of values so far
   Share share;
   int64_t part[kSoftmaxWarps + 9];
 };
 
-// Bounded wait; false when it ran out here or anywhere in the block.
+// Bounded wait; false when it ran out here or anywhere in the block.  kTile: for what comes
+// when a tile ends, all of whose units go on meanwhile (some 700 000 of them, 90 million
+// keys, take a second): the limit is that of a block whose loads do not go on.
+template <bool kTile>
 __device__ __forceinline__ bool wait_on(const AttendParams& p, Shared& sh, uint64_t* bar,
                                         uint32_t parity) {
   if (mbar_try_wait(bar, parity)) return true;
   uint64_t t0 = globaltimer();
+  int32_t moved = 0;
   while (!mbar_try_wait(bar, parity)) {
     if (*reinterpret_cast<volatile uint32_t*>(&sh.stop)) return false;
     const uint64_t now = globaltimer();
     if (*reinterpret_cast<volatile uint32_t*>(&sh.busy)) t0 = now;
+    if (kTile) {
+      const volatile int32_t* loads = sh.moved;
+      const int32_t so_far = loads[0] + loads[1];
+      if (so_far != moved) t0 = now;
+      moved = so_far;
+    }
     if (now - t0 > p.timeout_ns) {
       *reinterpret_cast<volatile uint32_t*>(&sh.stop) = 1;
       record_status(p.ctl, kStatusTimeout);
@@ -107,9 +118,10 @@ __device__ __forceinline__ bool wait_on(const AttendParams& p, Shared& sh, uint6
   return true;
 }
 // The same for a whole warp, all of whose lanes go on or leave.
+template <bool kTile = false>
 __device__ __forceinline__ bool wait(const AttendParams& p, Shared& sh, uint64_t* bar,
                                      uint32_t parity) {
-  return __all_sync(0xffffffffu, wait_on(p, sh, bar, parity));
+  return __all_sync(0xffffffffu, wait_on<kTile>(p, sh, bar, parity));
 }
 
 __device__ __forceinline__ void tma_4d(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t y,
@@ -294,6 +306,7 @@ __device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32
       if (!alive) break;
       if (lane == 0)
         mbar_arrive_expect_tx(&full[slot], static_cast<uint32_t>(boxes * columns * maps.box * kLine));
+      if (lane == 0) *reinterpret_cast<volatile int32_t*>(&sh.moved[side]) = at;
       __syncwarp();
       if (lane < boxes) {
         const uint32_t to = ring + slot * kBytes + lane * maps.box * kLine;
@@ -417,7 +430,7 @@ __device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, ui
   int taken = 0;                      // stages
   uint32_t query_parity = 0, weight_parity = 0, clear_parity = 0;   // (a bit per half)
   const auto full = [&](int i) {
-    return wait_on(p, sh, &sh.full[i % F::kStages], (i / F::kStages) & 1);
+    return wait_on<false>(p, sh, &sh.full[i % F::kStages], (i / F::kStages) & 1);
   };
   const auto multiply_scores = [&](int t, int stage, bool last) {
     const uint64_t a = a0 + t * kTile, b = k0 + stage * kTile;
@@ -435,7 +448,7 @@ __device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, ui
 #pragma unroll
     for (int t = 0; t < 2; ++t)
       if (h.units[t] > 0) {
-        if (!wait_on(p, sh, &sh.queries[t], query_parity >> t & 1)) return;
+        if (!wait_on<false>(p, sh, &sh.queries[t], query_parity >> t & 1)) return;
         query_parity ^= 1u << t;
       }
     if (!full(taken)) return;
@@ -452,7 +465,7 @@ __device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, ui
       const int next = (taken + 1) % F::kStages;             // the next one's keys
       const bool goes_on = u + 1 < h.most;
       if (!kE4m3 && s.keys - (s.from + u) * p.unit_keys < p.unit_keys) {
-        if (!wait_on(p, sh, &sh.cleared, clear_parity)) return;
+        if (!wait_on<false>(p, sh, &sh.cleared, clear_parity)) return;
         clear_parity ^= 1;
       } else if (!full(taken)) {
         return;
@@ -465,7 +478,7 @@ __device__ void multiply(const AttendParams& p, Shared& sh, uint32_t queries, ui
           const uint32_t from = tmem + t * kHalf, to = from + 2 * kHalf;
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
-            if (!wait_on(p, sh, &sh.weights[t][half], weight_parity >> t & 1)) return;
+            if (!wait_on<false>(p, sh, &sh.weights[t][half], weight_parity >> t & 1)) return;
             tc_fence_after();
 #pragma unroll
             for (int i = half * kStep / 16; i < (half + 1) * kStep / 16; ++i)
@@ -553,7 +566,7 @@ __device__ void ask(const AttendParams& p, const Maps& maps, Shared& sh, uint32_
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       if (h.units[t] == 0) continue;
-      alive = alive && wait(p, sh, &sh.asked[t], tiles[t] & 1);
+      alive = alive && wait<true>(p, sh, &sh.asked[t], tiles[t] & 1);
       ++tiles[t];
     }
     const int32_t left = s.keys - (s.from + h.most - 1) * p.unit_keys;
@@ -645,7 +658,7 @@ __device__ void soften(const AttendParams& p, Shared& sh, int t) {
     int32_t seen = 0;
     if (tid < rows) seen = seen_keys(s.request, p.by_group(row0 + tid));
     for (int u = 0; u < units; ++u) {
-      if (!wait(p, sh, &sh.scores[t], done & 1)) return;
+      if (!wait<true>(p, sh, &sh.scores[t], done & 1)) return;
       tc_fence_after();
       float v[kKeys];
       tmem_load32(score_at, v);
@@ -763,7 +776,7 @@ __device__ void soften(const AttendParams& p, Shared& sh, int t) {
     }
   }
   // (the second step's is waited for above; the first step's has come too)
-  if (done > 0) wait(p, sh, &sh.output[t][0], (done - 1) & 1);
+  if (done > 0) mbar_wait_bounded(&sh.output[t][0], (done - 1) & 1, p.timeout_ns);
 }
 
 // One lane: what the launch that joins has to know of the block's last tile.
@@ -808,6 +821,7 @@ __global__ void __launch_bounds__(Form<kDim, kE4m3>::kThreads, 1)
     mbar_init(&sh.drain, 1);
     sh.stop = sh.busy = 0;
     sh.issued = 0;
+    sh.moved[0] = sh.moved[1] = 0;
     fence_barrier_init();
   }
   if (warp == kMultiplyWarp) {

@@ -159,3 +159,27 @@ def test_queries_of_any_magnitude(new, page, dim, q_heads, q_power, k_power):
     got = attention.attend(q, cache, table, off, context)
     assert (got[0, 0] == 0).all() and torch.isfinite(got).all()
     assert experts.status() == ciera.OK
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_tile_longer_than_the_limit(e4m3):
+    """Tiles of a million keys take a block some 12 ms each: with a limit of 2 ms no wait runs
+    out, as every unit's loads and products go on."""
+    page, dim, L = 128, 128, 1 << 20
+    cache = attention.page_cache(1, page, 1, dim, e4m3=e4m3)
+    v = rand(dim, seed=1).to(torch.float8_e4m3fn).to(BF16)
+    cache.value.view(torch.uint8 if e4m3 else BF16)[:] = (
+        v.to(torch.float8_e4m3fn).view(torch.uint8) if e4m3 else v)
+    if e4m3:
+        cache.key_exponent.fill_(127), cache.value_exponent.fill_(127)
+    table = torch.zeros(2, L // page, dtype=torch.int32, device="cuda")
+    new = [320 * 256, 100]
+    q, off = rand(sum(new), 1, dim, seed=2), ints([0, new[0], sum(new)])
+    try:
+        ciera.set_wait_timeout_ns(2 * 10 ** 6)
+        got = attention.attend(q, cache, table, off, ints([L, L]))
+        assert experts.status() == ciera.OK
+    finally:
+        ciera.set_wait_timeout_ns(10 ** 9)
+    # keys of zeros: the mean of values that are all the same
+    assert torch.equal(got, v.expand_as(got))
