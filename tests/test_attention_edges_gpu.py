@@ -183,3 +183,70 @@ def test_a_tile_longer_than_the_limit(e4m3):
         ciera.set_wait_timeout_ns(10 ** 9)
     # keys of zeros: the mean of values that are all the same
     assert torch.equal(got, v.expand_as(got))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("by_head", [False, True])
+def test_append_and_attend_behind_32_bits(e4m3, by_head):
+    """The last pages of a cache of more than 2^32 values a side, written and read: 8-bit
+    rows' bytes and exponents too, and by every form."""
+    page, heads, dim = 512, 32, 128
+    pages = 2 ** 32 // (page * heads * dim) + 200
+    shape = (pages, heads, page, dim) if by_head else (pages, page, heads, dim)
+    order = (lambda t: t.transpose(1, 2)) if by_head else (lambda t: t)
+    kind = torch.float8_e4m3fn if e4m3 else BF16
+    sides = [order(torch.empty(shape, dtype=kind, device="cuda")) for _ in range(2)]
+    if e4m3:
+        # exponents with gaps: places behind 2^31 too
+        sides += [order(torch.empty(*shape[:3], 32, dtype=torch.uint8, device="cuda"))[..., 7]
+                  for _ in range(2)]
+    cache = attention.Cache(*sides)
+    assert cache.key.numel() > 2 ** 32
+    used = [pages - 1, 5, pages - 2]
+    L = 2 * page + 300
+    at = torch.arange(L, device="cuda")
+    slots = torch.tensor(used, device="cuda")[at // page] * page + at % page
+    assert int(slots.max()) * heads * dim > 2 ** 32
+    r = attention.rotary_table(dim)
+    q, k, v = (rand(L, heads, dim, seed=s, scale=1.5) for s in (1, 2, 3))
+    turned = attention.append(q, k, v, at.int(), slots.int(), r, cache)
+    small = attention.page_cache(3, page, heads, dim, e4m3=e4m3)
+    assert torch.equal(turned, attention.append(q, k, v, at.int(), at.int(), r, small))
+    for side, want in zip(cache, small):
+        if side is None:
+            continue
+        got = side.view(torch.uint8) if e4m3 else side
+        want = want.view(torch.uint8) if e4m3 else want
+        for i, p in enumerate(used):
+            n = min(page, L - i * page)
+            assert torch.equal(got[p, :n], want[i, :n])
+    for new in (1, 3, 130):
+        o = attention.attend(turned[L - new:], cache, ints([used]), ints([0, new]), ints([L]))
+        assert torch.equal(o, attention.attend(turned[L - new:], small, ints([[0, 1, 2]]),
+                                               ints([0, new]), ints([L])))
+        if new == 130:
+            ref.check_attend(o, turned[L - new:], small, ints([[0, 1, 2]]), ints([0, new]), ints([L]))
+    assert experts.status() == ciera.OK
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_heads_of_odd_size_behind_32_bits(e4m3):
+    """The same of the forms for any layout: rows of 72 8-bit values, of 127 of 16 bits."""
+    page, heads, dim = 512, 8, 72 if e4m3 else 127
+    pages = 2 ** 32 // (page * heads * dim) + 100
+    kind = torch.float8_e4m3fn if e4m3 else BF16
+    sides = [torch.empty(pages, page, heads, dim, dtype=kind, device="cuda") for _ in range(2)]
+    if e4m3:
+        sides += [torch.empty(pages, page, heads, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    cache, used, L = attention.Cache(*sides), [pages - 1, pages - 2], page + 40
+    at = torch.arange(L, device="cuda")
+    slots = torch.tensor(used, device="cuda")[at // page] * page + at % page
+    r = attention.rotary_table(dim - dim % 2)
+    q, k, v = (rand(L, heads, dim, seed=s) for s in (1, 2, 3))
+    small = attention.page_cache(2, page, heads, dim, e4m3=e4m3)
+    turned = attention.append(q, k, v, at.int(), slots.int(), r, cache)
+    assert torch.equal(turned, attention.append(q, k, v, at.int(), at.int(), r, small))
+    for new in (1, 40):
+        o = attention.attend(turned[L - new:], cache, ints([used]), ints([0, new]), ints([L]))
+        assert torch.equal(o, attention.attend(turned[L - new:], small, ints([[0, 1]]),
+                                               ints([0, new]), ints([L])))
