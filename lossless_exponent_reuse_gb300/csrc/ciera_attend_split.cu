@@ -18,9 +18,9 @@
 // fragments; queries are fp16 too, scaled by a power of two per row that brings its
 // largest finite value to 2^13 or more, so that they lose 2^-38 of it at most (of a row
 // whose largest is below 2^-113, which the power's range stops short, 2^-25 of it, and of
-// one of bf16's subnormals 2^-18).  A key's exponent goes on its scores; where a row's power
-// is beyond 2^+-60, between two halves of that, so that nothing on the way is larger,
-// or smaller, than both the product and the score.
+// one of bf16's subnormals 2^-18).  The row's power goes on its scores first, then the
+// key's; a row of 2^97 and more, whose scores may pass 32 bits between the two, is computed
+// value by value.
 // Values go to bf16, whose weights have the range that rows of any exponents
 // want: a value's exponent goes on its weight's before a maximum of their own is
 // taken (the sum has the scores' maximum).
@@ -139,9 +139,8 @@ __device__ __forceinline__ int piece_at(int row, int piece) {
 struct Shared {
   Share share;
   int64_t part[kWarps + 1];
-  float query_scale[32];         // of a score, the row's power of two, or half of it, included
-  float query_power[32];         // the other half
-  uint32_t halves;               // some row has halves
+  float query_scale[32];         // of a score, with the row's power of two
+  uint32_t large[kWarps];        // a warp's own rows that are computed value by value
   int32_t seen[32];              // keys that a row sees
   // maxima of the values' weights and of the scores (bf16: the same), sums
   float most[kWarps][32], score[kWarps][32], sum[kWarps][32];
@@ -149,8 +148,7 @@ struct Shared {
 };
 
 template <int kDim, int kBlocks, bool kE4m3>
-__global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm))
-    k_attend_split(const AttendParams p) {
+__global__ void __launch_bounds__(kThreads) k_attend_split(const AttendParams p) {
   using F = Form<kDim, kBlocks, kE4m3>;
   extern __shared__ __align__(16) unsigned char raw[];
   __shared__ Shared sh;
@@ -164,7 +162,6 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
   Joint* joint = reinterpret_cast<Joint*>(p.workspace) + block;
   float* parts = reinterpret_cast<float*>(reinterpret_cast<Joint*>(p.workspace) + blocks);
 
-  if (threadIdx.x == 0) sh.halves = 0;
   find_share<F::kRows, kThreads>(p, block, blocks, sh.part, &sh.share);
   Walk<F::kRows> walk(p, sh.share);
   Segment seg;
@@ -176,6 +173,7 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
     const int32_t row0 = seg.tile * F::kRows;
     // ---- queries: a warp a row
     if (threadIdx.x == 0) sh.again = 0;
+    uint32_t large = 0;
     for (int r = warp; r < F::kRows; r += kWarps) {
       const bool live = r < seg.rows;
       const uint16_t* q = query_row(p, seg.request.first, seg.head, row0 + (live ? r : 0));
@@ -188,17 +186,16 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
         const uint32_t size = v[i] & 0x7FFFu;
         most = max(most, size < 0x7F80u ? size : 0);
       }
-      float by = 1.0f, scale = p.scale * kLog2e, power = 1.0f;
+      float by = 1.0f, scale = p.scale * kLog2e;
       if (kE4m3) {
         // the largest value to 2^13 .. 2^14
         most = __reduce_max_sync(0xffffffffu, most);
         int e = static_cast<int>(most >> 7) - 127 - 13;
         e = most == 0 ? 0 : e < -126 ? -126 : e;
         by = __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
-        const int rest = e < -60 || e > 60 ? e / 2 : 0;
-        scale *= __uint_as_float(static_cast<uint32_t>(127 + e - rest) << 23);
-        power = __uint_as_float(static_cast<uint32_t>(127 + rest) << 23);
-        if (rest && lane == 0) sh.halves = 1;
+        scale *= __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        // (a product is below 2^14 448 256 < 2^31)
+        if (live && fabsf(scale) > 0x1p96f) large |= 1u << r;
       }
 #pragma unroll
       for (int i = 0; i < kDim / 32; ++i) {
@@ -208,10 +205,10 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
       }
       if (lane == 0) {
         sh.query_scale[r] = scale;
-        sh.query_power[r] = power;
         sh.seen[r] = live ? seen_keys(seg.request, p.by_group(row0 + r)) : 0;
       }
     }
+    if (kE4m3 && lane == 0) sh.large[warp] = large;
     __syncthreads();
     float scale[kBlocks][2], top[kBlocks][2], high[kBlocks][2], sum[kBlocks][2];
     int32_t seen[kBlocks][2];
@@ -250,7 +247,6 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
           query(s, b, qf[F::kKeep ? s : 0][F::kKeep ? b : 0][0],
                 qf[F::kKeep ? s : 0][F::kKeep ? b : 0][1]);
     float o[F::kSteps][kBlocks][4] = {};
-    const bool halves = kE4m3 && sh.halves;
 
     // ---- this warp's units
     const int units = seg.to - seg.from;
@@ -365,26 +361,14 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
         exponent = exponent_of(u + 1);
       }
       const bool masked = key0 + u * kUnitKeys + kWarpKeys > least;
-#pragma unroll
-      for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          s[b][i] *= scale[b][i & 1];
-          if (kE4m3) s[b][i] *= key_scale[i >> 1];
-        }
-      if (halves) {
-#pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) s[b][i] *= sh.query_power[b * 8 + 2 * column + (i & 1)];
-      }
       bool rises = false;
 #pragma unroll
       for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int j = i & 1, k = i >> 1;
-          float t = s[b][i];
+          float t = s[b][i] * scale[b][j];
+          if (kE4m3) t *= key_scale[k];
           if (masked && key + 8 * k >= seen[b][j]) t = minus_infinity();
           s[b][i] = t;
           rises |= t > high[b][j] + kSlack;
@@ -478,7 +462,6 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
 
     // ---- the warps' sums, through the ring's memory
     __syncthreads();
-    if (threadIdx.x == 0) sh.halves = 0;   // (all have read it)
 #pragma unroll
     for (int b = 0; b < kBlocks; ++b)
 #pragma unroll
@@ -538,6 +521,7 @@ __global__ void __launch_bounds__(kThreads, (Form<kDim, kBlocks, kE4m3>::kPerSm)
     if (again)
       again = spoilt_rows(p, seg.index, seg.head, again, sh.seen[lane],
                           min(seg.to * kUnitKeys, seg.keys));
+    if (kE4m3) again |= sh.large[warp];
     for (; again; again &= again - 1) {
       const int r = __ffs(again) - 1;
       Slice own;

@@ -149,7 +149,7 @@ def test_queries_of_any_magnitude(new, page, dim, q_heads, q_power, k_power):
     q[0, 0, :3] *= 2.0 ** -7               # within a row too
     q[0, 1] = 0
     off, context = ints([0, new]), ints([L])
-    for scale in (None, 4.0):
+    for scale in (None, 4.0, -4.0):
         got = attention.attend(q, cache, table, off, context, scale=scale)
         ref.check_attend(got, q, cache, table, off, context, scale, what=(new, dim, q_power))
     # a value that is infinite, among large and small ones: every score minus infinity
