@@ -117,6 +117,9 @@ class AttentionLayer:
         if (at["attn.k"] != at["attn.q"] + rows[0] * dim
                 or at["attn.v"] != at["attn.k"] + rows[1] * dim or rows[1] != rows[2]):
             raise ValueError("attn.q, attn.k and attn.v must lie one behind the other")
+        if head_dim < 1 or any(r % head_dim for r in rows) or tuple(shape["attn.o"]) != (dim, rows[0]):
+            raise ValueError(f"weights of {rows} rows, attn.o {list(shape['attn.o'])}: no heads of "
+                             f"{head_dim}")
         self.heads = [r // head_dim for r in rows]
         self.head_dim, self.rotary, self.eps = head_dim, rotary, eps
         n = sum(rows)

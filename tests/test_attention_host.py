@@ -225,3 +225,18 @@ def test_scaled_frequencies():
 def test_rotary_table_refuses(bad):
     with pytest.raises(ValueError):
         attention.rotary_table(**{"dim": 8, "device": "cpu", **bad})
+
+
+@pytest.mark.parametrize("head_dim,rows,o", [(96, (256, 128), None), (0, (256, 128), None),
+                                             (64, (256, 100), None), (64, (256, 128), (256, 64))])
+def test_layer_refuses_heads_that_its_weights_do_not_have(head_dim, rows, o):
+    import dataclasses
+
+    from lossless_exponent_reuse_gb300 import moe_layer, workloads
+    wl = moe_layer.layer_workload(2, 64, 32, ranks=1, block=64, attention_rows=rows)
+    if o:
+        wl = dataclasses.replace(wl, tensors=tuple(
+            workloads.Tensor(t.name, o) if t.name == "attn.o" else t for t in wl.tensors))
+    bucket, turn = torch.zeros(wl.numel, dtype=torch.bfloat16), attention.rotary_table(8, device="cpu")
+    with pytest.raises(ValueError):
+        moe_layer.AttentionLayer(bucket, wl, head_dim, turn)
