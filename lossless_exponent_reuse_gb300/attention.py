@@ -160,7 +160,9 @@ def rotary_table(dim: int, base: float = 10000.0, interleaved: bool = False,
                 by factor, the fastest as it was
       "parts"   those that make fewer than bounds[0] turns in the original
                 context divided by factor, those of bounds[1] and more as they
-                were, and between the two linearly in the turns.
+                were, and between the two linearly in the turns (a model that was
+                tuned with a ramp in the pairs' index, between two rounded ends, wants
+                its ``frequencies`` given).
 
     ``amplitude``: of the rotated values; 1, and for "parts" 1 + 0.1 ln factor,
     unless given.  Laid out once for many calls."""
@@ -373,7 +375,8 @@ def attend(q: torch.Tensor, cache: Cache, table: torch.Tensor, offsets: torch.Te
     keys are there, the new ones last; each token sees the keys up to its own.
     ``scale``: head_dim^-0.5 if not given.  ``longest``: the most new tokens of a
     request, if the caller knows (1 for a step of single tokens): it chooses the
-    faster kernel, no result; guessed 1 where tokens are no more than requests."""
+    faster kernel for the whole call, no result; guessed 1 where tokens are no more than
+    requests."""
     index = _index(q, "q")
     (tokens, heads, dim), q_token, q_head = _heads(q, "q", index)
     shape, words = _cache(cache, index)

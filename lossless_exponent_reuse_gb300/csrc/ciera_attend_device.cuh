@@ -557,7 +557,8 @@ __device__ __forceinline__ void leave_joint(Joint* joint, const Segment* s, cons
   *joint = j;
 }
 
-// Host: a launch that may begin, and waits, before the one before it has ended.
+// Host: a launch that may begin, and waits, while the last blocks of the one before it
+// leave (that one says nothing earlier).
 inline int launch_after(void (*kernel)(AttendParams), dim3 grid, int threads, cudaStream_t s,
                         const AttendParams& p) {
   cudaLaunchConfig_t config{};

@@ -5,8 +5,8 @@
 // own: each has a ring of stages in shared memory that its lanes fill by
 // asynchronous copies, a row of a page at a time, some 16 KB ahead, and joins the
 // others at the end of a tile alone.  64 requests of some 4200 keys on average, 16
-// heads: 360 us, 6.1 TB/s; in e4m3 214 us, 5.2 TB/s, where issue slots are 59 % used
-// (widening takes as many as the products); 4 heads with 8 query heads each 105 us.
+// heads: 322 us, 6.9 TB/s; in e4m3 213 us, 5.2 TB/s, where issue slots are 60 % used
+// (widening takes as many as the products); 4 heads with 8 query heads each 97 us.
 //
 // The products have the keys as rows and the queries as columns, S^T = K Q^T of
 // 16 x 8, so that eight rows (8 query heads, say) cost one instruction per 16
@@ -27,7 +27,9 @@
 //
 // The running maximum moves only where a score passes it by 2^8 (weights are at
 // most 256, which 8 bits of mantissa hold as well as 1): most units then need
-// neither the maximum over the lanes nor the sums' scaling.
+// neither the maximum over the lanes nor the sums' scaling.  Weights are rounded to
+// bf16 (2^-9 of each at most, as often up as down), the values' own type, whose range
+// they need; their sum is of the 32-bit ones.
 #include "ciera_attend_device.cuh"
 #include "ciera_device.cuh"
 
@@ -116,7 +118,8 @@ struct Form {
   static constexpr int kSmem =
       kQueryBytes + (kWarps * kWarpBytes > kSumBytes ? kWarps * kWarpBytes : kSumBytes);
   // blocks of an SM: what shared memory and registers hold (64 requests in two blocks
-  // of 24 KB rings and three of 16: bf16 366, 360 us, 4 heads 109, 105; e4m3 268, 224)
+  // of 24 KB rings and three of 16, when either took longer: bf16 366, 360 us, 4 heads 109,
+  // 105; e4m3 268, 224)
   static constexpr int kPerSm = kDim > 128 ? 1 : kBlocks == 1 ? kMostPerSm : 2;
   static constexpr int kPartValues = kRows * (kDim + 3);
   static constexpr int kSteps = kDim / 16;

@@ -14,15 +14,21 @@
 // half's products run: S0 S1 | O0 S0' O1 S1' | ...  The products run in the order in
 // which the one lane issues them: S0' overwrites the weights that O0 reads.
 //
+// Weights are rounded to bf16, 2^-9 of each at most and as often up as down: A and B of a
+// product are of one type, and values have bf16's range, which fp16 with three bits more
+// does not hold.  Their sum is of the 32-bit ones.
+//
 // Bound by the tensor cores while both halves have units: 1.45 us a unit of 256 x 128 x
 // 128, 1759 TFLOP/s; a block's start (9 us), a tile's begin and end (4) and the join
-// (5 to 9) come on top.  16 heads of 128: a prompt of 8192 tokens 211 to 224 us (1230 to
-// 1310 TFLOP/s, with the clock that power leaves), 512 tokens behind 32256 with 32 heads
-// to 4 191 to 197 (1400); 24 requests of 100 to 3000 cached keys and up to 300 new tokens
-// 119 to 135, where some ten units a tile do not hide its begin.
+// (5 to 9) come on top.  16 heads of 128: a prompt of 8192 tokens 207 to 214 us (1290 to
+// 1330 TFLOP/s, with the clock that power leaves), 512 tokens behind 32256 with 32 heads
+// to 4 190 to 193 (1420); 24 requests of 100 to 3000 cached keys and up to 300 new tokens,
+// 24 heads to 8, 118 to 119, where some ten units a tile do not hide its begin, and
+// queries of three heads to one come by ordinary copies.
 //
 // e4m3 pages come by TMA as they are; four warps more widen them to bf16, which
-// holds every row times its power of two exactly, into the ring's stages.
+// holds every row times its power of two exactly (of an exponent of 3 and more, biased), into
+// the ring's stages.
 //
 // A tile's last keys may lie in a page with others behind them, which hold
 // anything: those values are cleared in shared memory before the products.  What a row
@@ -331,7 +337,7 @@ __device__ void load(const AttendParams& p, const Maps& maps, Shared& sh, uint32
 // fetched a stage ahead.  A value goes by way of fp16 and fp32, all of which hold
 // it, so that most of the work is the multipliers'; the integer units, which the
 // softmax needs, put two together (a prompt of 8192 tokens of 16 heads: 351 us, by
-// moving bits 437; two or four rows at once, 380 and 373, spill).
+// moving bits 437; two or four rows at once, 380 and 373, spill; now 359).
 __device__ __forceinline__ uint32_t times_bf16(uint32_t a, uint32_t b) {
   uint32_t d;
   asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
@@ -1011,8 +1017,8 @@ int launch_at(const AttendParams& p, const Maps& maps, cudaStream_t s) {
 
 // Rows a head (most of any request, as far as the caller knows) up to which a call
 // is left to the form for few rows.  64 requests of 5000 keys on average, 4 heads, rows,
-// form for few and for many, in us: bf16 8 110, 120; 16 112, 121; 24 142, 121; 32 154,
-// 121; 64 223, 119.  e4m3 16 99, 201; 32 165, 201; 64 241, 198.
+// form for few and for many, in us: bf16 8 117, 137; 16 118, 137; 24 159, 137; 32 167,
+// 137; 64 235, 138.  e4m3 8 90, 241; 16 110, 241; 32 184, 241; 64 258, 240.
 constexpr int kFewRows = 16, kFewRowsE4m3 = 32;
 // Of boxes of fewer than eight keys, whose loads take longer, by rows times keys of a box:
 // bf16 pages of two and 40 rows 136, 230, 70 rows 199, 231, 100 rows (12 heads) 164, 166;

@@ -105,7 +105,9 @@ class MoELayer:
 class AttentionLayer:
     """Views of a flat bucket (bf16 or uint16 bits) with the tensors of
     ``workload``: ``attn.q`` [q_heads head_dim, dim], ``attn.k``, ``attn.v``
-    [heads head_dim, dim], one behind the other, ``attn.o`` and ``input_norm``."""
+    [heads head_dim, dim], one behind the other, ``attn.o`` and ``input_norm``.
+    Queries and keys have no norms of their own before the rotary positions, as some
+    models' have: the workloads' buckets carry none."""
 
     def __init__(self, bucket: torch.Tensor, workload: workloads.Workload, head_dim: int,
                  rotary: attention.Rotary, eps: float = 1e-6):
