@@ -250,3 +250,41 @@ def test_heads_of_odd_size_behind_32_bits(e4m3):
         o = attention.attend(turned[L - new:], cache, ints([used]), ints([0, new]), ints([L]))
         assert torch.equal(o, attention.attend(turned[L - new:], small, ints([[0, 1]]),
                                                ints([0, new]), ints([L])))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("new,page,dim,q_heads", [(300, 16, 128, 4), (290, 20, 64, 6), (14, 16, 128, 2),
+                                                  (20, 1, 64, 4), (40, 16, 66, 2)])
+def test_rows_that_see_nothing_of_bad_values(new, page, dim, q_heads, e4m3):
+    """More new tokens than keys, and values that are NaN among the keys: the first rows see
+    none and are zeros, the last ones what they see."""
+    L = new // 3
+    cache, table = ref.paged([L, 50], page, 2, dim, e4m3=e4m3)
+    for key in (L // 2, L - 1):
+        put(cache, places(table, page, [key]), 1, 3, math.nan)
+    q, off = rand(new + 5, q_heads, dim, seed=6), ints([0, new, new + 5])
+    context = ints([L, 50])
+    got = attention.attend(q, cache, table, off, context)
+    ref.check_attend(got, q, cache, table, off, context)
+    assert (got[:new - L] == 0).all() and torch.isnan(got[new - 1, q_heads // 2:, 3]).all()
+    assert experts.status() == ciera.OK
+
+
+@pytest.mark.parametrize("new", [1, 3])
+def test_large_queries_over_many_blocks(new):
+    """Rows that are computed value by value in parts that several blocks leave, beside rows
+    that are not."""
+    page, dim, heads, L = 16, 128, 2, 9000
+    rows = lambda kind, r, n: rand(n, heads, dim, seed=80 + kind, dtype=torch.float32) / 64
+    cache, table = ref.paged([L], page, heads, dim, e4m3=True, value=rows)
+    cache.key_exponent[places(table, page, range(L))] = 127 - 120
+    q = (rand(new, 4, dim, seed=8, dtype=torch.float64).clamp(-3, 3) * 2.0 ** 120).to(BF16)
+    q[:, 1::2] *= 2.0 ** -40
+    off, context = ints([0, new]), ints([L])
+    got = attention.attend(q, cache, table, off, context, scale=0.25)
+    ref.check_attend(got, q, cache, table, off, context, 0.25)
+    # a scale that makes every row large, of tiles that rows do not fill
+    got = attention.attend((q.double() * 2.0 ** -120).to(BF16), cache, table, off, context,
+                           scale=2.0 ** 118)
+    ref.check_attend(got, (q.double() * 2.0 ** -120).to(BF16), cache, table, off, context, 2.0 ** 118)
+    assert experts.status() == ciera.OK
