@@ -798,16 +798,17 @@ int64_t ciera_attend_workspace_bytes(int64_t q_heads, int64_t heads, int64_t hea
  * are the last of L, appended before):
  *   o = sum_j p_j v_j,  p_j = exp(scale q . k_j - max) / sum of them
  * over the keys it sees; zeros where it sees none, or every score is minus
- * infinity, and in the rows behind the last request.  Keys that a token does not see have no part in its row, be
- * they infinite or NaN.  q's head h reads the cache's head
+ * infinity, and in the rows behind the last request.  Keys that a token does not see
+ * have no part in its row, be they infinite or NaN.  q's head h reads the cache's head
  * h / (q_heads / heads).  Weights are rounded to 16 bits (8 significant) on
  * their way to the tensor cores, sums and maxima held in 32; weights up to 2^8 times
  * values are summed before they are divided by the weights' sum, which values above
- * 2^119 / L may overflow.  Of 8-bit rows a weight times its value's power of two counts where
- * it is 2^-126 of the largest such or more.  Where rows that see different keys are computed together, a
- * row that is infinite or NaN, and has a value that is infinite or NaN among the keys behind its
- * own, is computed again, value by value (not where it sees a NaN in the same place
- * of the head): 0.2 us a key that it sees, up to 32 rows one after the other.
+ * 2^119 / L may overflow.  Of 8-bit rows a weight times its value's power of two counts
+ * where it is 2^-126 of the largest such or more.  Where rows that see different keys are
+ * computed together, a row that is infinite or NaN, and has a value that is infinite or
+ * NaN among the keys behind its own, is computed again, value by value (not where it sees
+ * a NaN in the same place of the head): 0.2 us a key that it sees, up to 32 rows one
+ * after the other.
  *   q_dev        tokens x q_heads x head_dim bf16
  *   table_dev    requests x width pages, rows table_stride apart
  *   offsets_dev  requests + 1

@@ -18,8 +18,9 @@
 // fragments; queries are fp16 too, scaled by a power of two per row that brings its
 // largest finite value to 2^13 or more, so that they lose 2^-38 of it at most (of a row
 // whose largest is below 2^-113, which the power's range stops short, 2^-25 of it, and of
-// one of bf16's subnormals 2^-18).  The row's power goes on its scores first, then the
-// key's; a row of 2^97 and more, whose scores may pass 32 bits between the two, is computed
+// one of bf16's subnormals 2^-18).  The row's power and the scale go on its scores first,
+// then the key's power; where the first are beyond 2^96, and a score might pass 32 bits
+// between the two (with a scale of 1 / 11, rows of 2^112 and more), the row is computed
 // value by value.
 // Values go to bf16, whose weights have the range that rows of any exponents
 // want: a value's exponent goes on its weight's before a maximum of their own is
@@ -28,7 +29,7 @@
 // The running maximum moves only where a score passes it by 2^8 (weights are at
 // most 256, which 8 bits of mantissa hold as well as 1): most units then need
 // neither the maximum over the lanes nor the sums' scaling.  Weights are rounded to
-// bf16 (2^-9 of each at most, as often up as down), the values' own type, whose range
+// bf16 (2^-8 of each at most, as often up as down), the values' own type, whose range
 // they need; their sum is of the 32-bit ones.
 #include "ciera_attend_device.cuh"
 #include "ciera_device.cuh"

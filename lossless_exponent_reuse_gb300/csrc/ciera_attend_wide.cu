@@ -14,7 +14,7 @@
 // half's products run: S0 S1 | O0 S0' O1 S1' | ...  The products run in the order in
 // which the one lane issues them: S0' overwrites the weights that O0 reads.
 //
-// Weights are rounded to bf16, 2^-9 of each at most and as often up as down: A and B of a
+// Weights are rounded to bf16, 2^-8 of each at most and as often up as down: A and B of a
 // product are of one type, and values have bf16's range, which fp16 with three bits more
 // does not hold.  Their sum is of the 32-bit ones.
 //
